@@ -20,6 +20,7 @@ FMT_AFFINE2 = 1
 FMT_Q4_0 = 2
 F16 = 0
 BF16 = 1
+F32 = 2
 PLAN_MEASURE = 0x1
 PLAN_FORCE_FEWROW = 0x2
 PLAN_FORCE_GEMV = 0x4
@@ -33,6 +34,11 @@ KERNEL_FEWROW_TC = 3
 KERNEL_FEWROW_TC8 = 4
 FUSED_ROTATE = 0x1
 FUSED_ARGMAX = 0x2
+ROPE_HALF = 0
+ROPE_INTERLEAVED = 1
+ROPE_NONE = 0
+ROPE_LINEAR = 1
+ROPE_BY_PARTS = 2
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_WORKSPACE, ERR_TIMEOUT, ERR_BOUNDS = range(7)
 
@@ -51,6 +57,28 @@ class Problem(ctypes.Structure):
     """One problem of a grouped call (lbv_problem)."""
     _fields_ = [("X", ctypes.c_void_p), ("M", ctypes.c_int), ("ldx", ctypes.c_int),
                 ("Wp", ctypes.c_void_p), ("Y", ctypes.c_void_p), ("ldy", ctypes.c_int)]
+
+
+class _BatchArg(ctypes.Structure):
+    """lbv_batch."""
+    _fields_ = [("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("requests", ctypes.c_int),
+                ("tokens", ctypes.c_int), ("table_stride", ctypes.c_int),
+                ("table_pages", ctypes.c_int)]
+
+
+class _RowsArg(ctypes.Structure):
+    """lbv_rows."""
+    _fields_ = [("data", ctypes.c_void_p), ("heads", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class _RulesArg(ctypes.Structure):
+    """lbv_sample_rules."""
+    _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p),
+                ("top_p", ctypes.c_void_p), ("min_p", ctypes.c_void_p),
+                ("mask", ctypes.c_void_p), ("mask_ld", ctypes.c_int64),
+                ("temperature_last", ctypes.c_int)]
 
 
 class LbvError(RuntimeError):
@@ -74,6 +102,7 @@ def lib():
                                "few_row_packed_gb300.build() (nvcc, sm_103a)")
         L = ctypes.CDLL(LIB_PATH)
         P, I, U, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint, ctypes.c_size_t
+        D, F, L64 = ctypes.c_double, ctypes.c_float, ctypes.c_int64
         st = ctypes.c_int
         sig = {
             "lbv_packed_bytes": (S, [I, I, I, I]),
@@ -111,6 +140,13 @@ def lib():
             "lbv_verify_fused_noalloc": (st, [P, P, I, I, P, U, P, P, I, P, P, P]),
             "lbv_verify_fused": (st, [P, P, I, I, P, U, P, P, I, P, P, P, S, P]),
             "lbv_dequant_fp16": (st, [P, P, P, P]),
+            "lbv_kv_cache_create": (st, [P, P, I, I, I, I, L64, L64, L64, I, ctypes.POINTER(P)]),
+            "lbv_kv_cache_destroy": (st, [P]),
+            "lbv_rope_frequencies": (st, [I, D, I, D, D, D, D, P]),
+            "lbv_rope_create": (st, [P, I, I, F, ctypes.POINTER(P)]),
+            "lbv_rope_destroy": (st, [P]),
+            "lbv_rope_append": (st, [P] * 9),
+            "lbv_sample": (st, [P, I, I, L64, I, P, P, P, P, P]),
             "lbv_last_error": (ctypes.c_char_p, []),
             "lbv_version": (ctypes.c_char_p, []),
             "lbv_checked_build": (I, []),
@@ -415,6 +451,165 @@ def fwht128(X, Xr, M: int, K: int, dtype: int = F16, signs=None, stream=None):
 def dequant_fp16(plan: Plan, Wp, W, stream=None):
     """Test export: dense fp16 W[K][N] (device) from the packed device layout."""
     _check(lib().lbv_dequant_fp16(plan.handle, _ptr(Wp), _ptr(W), _stream(stream)))
+
+
+# --- the verify step around the matmul ------------------------------------------------
+
+def _dtype_id(t) -> int:
+    import torch
+    try:
+        return {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}[t.dtype]
+    except KeyError:
+        raise LbvError(ERR_INVALID_ARG, f"tensor of {t.dtype}: float16, bfloat16 or float32 "
+                                        "is wanted") from None
+
+
+def _words(t, dtype, n: int, what: str):
+    """Address of a contiguous device tensor of at least n elements, or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() < n or not t.is_contiguous() or not t.is_cuda:
+        raise LbvError(ERR_INVALID_ARG, f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}; a "
+                                        f"contiguous {dtype} device tensor of {n} is wanted")
+    return t.data_ptr()
+
+
+class KVCache:
+    """A caller's paged cache: k, v of shape [pages, page_size, heads, head_dim]
+    (fp16 or bf16 device tensors, any order of the first three dimensions in
+    memory, the same strides for both).  The handle keeps the tensors alive."""
+
+    def __init__(self, k, v):
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+            raise LbvError(ERR_INVALID_ARG, "k and v have the same 4-d shape, strides and dtype")
+        if k.stride(3) != 1 or not (k.is_cuda and v.is_cuda):
+            raise LbvError(ERR_INVALID_ARG, "k and v are device tensors with a contiguous last "
+                                            "dimension")
+        h = ctypes.c_void_p()
+        _check(lib().lbv_kv_cache_create(k.data_ptr(), v.data_ptr(), *k.shape, *k.stride()[:3],
+                                         _dtype_id(k), ctypes.byref(h)))
+        self.handle = h
+        self.k, self.v, self.dtype = k, v, k.dtype
+        self.pages, self.page_size, self.heads, self.head_dim = k.shape
+
+    def close(self):
+        if getattr(self, "handle", None) and _lib is not None:
+            _lib.lbv_kv_cache_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class Batch:
+    """The new tokens of one step (lbv_batch): q_start int32 [requests + 1],
+    kv_len int32 [requests] (new tokens included), block_table int32
+    [requests, table_pages], all on the device and kept alive here; `tokens` is
+    the number of rows of the token-major tensors."""
+
+    def __init__(self, q_start, kv_len, block_table, tokens: int):
+        import torch
+        n = kv_len.numel()
+        if block_table.dim() != 2 or block_table.shape[0] != n or block_table.stride(1) != 1 \
+                or block_table.dtype != torch.int32 or not block_table.is_cuda:
+            raise LbvError(ERR_INVALID_ARG, "block_table: an int32 device tensor [requests, pages] "
+                                            "is wanted")
+        self.arg = _BatchArg(_words(q_start, torch.int32, n + 1, "q_start"),
+                             _words(kv_len, torch.int32, n, "kv_len"), block_table.data_ptr(), n,
+                             int(tokens), max(block_table.stride(0), block_table.shape[1]),
+                             block_table.shape[1])
+        self.ref = ctypes.byref(self.arg)
+        self.q_start, self.kv_len, self.block_table = q_start, kv_len, block_table
+        self.requests, self.tokens = n, int(tokens)
+
+
+def _rows_arg(t, tokens: int, head_dim: int, what: str):
+    """lbv_rows of a [tokens, heads, head_dim] device tensor."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] < tokens or shape[2] != head_dim or stride[2] != 1 \
+            or not t.is_cuda:
+        raise LbvError(ERR_INVALID_ARG, f"{what}: {tuple(shape)} with strides {stride} on "
+                                        f"{t.device}; [{tokens}, heads, {head_dim}] is wanted")
+    return _RowsArg(t.data_ptr(), shape[1], _dtype_id(t), stride[0], stride[1])
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = ROPE_NONE,
+                     factor: float = 1.0, trained: float = 0.0, low: float = 1.0,
+                     high: float = 32.0) -> np.ndarray:
+    """Radians per position of the rot_dim / 2 pairs (lbv_rope_frequencies)."""
+    out = np.zeros(max(rot_dim // 2, 1), np.float64)
+    _check(lib().lbv_rope_frequencies(rot_dim, base, scaling, factor, trained, low, high,
+                                      out.ctypes.data))
+    return out
+
+
+class Rope:
+    """A rotation of the first 2 * len(freqs) elements of a head."""
+
+    def __init__(self, freqs, layout: int = ROPE_HALF, factor: float = 1.0):
+        f = np.ascontiguousarray(freqs, np.float64)
+        h = ctypes.c_void_p()
+        _check(lib().lbv_rope_create(f.ctypes.data, 2 * f.size, layout, factor, ctypes.byref(h)))
+        self.handle = h
+        self.rot_dim, self.layout, self.factor = 2 * f.size, layout, factor
+
+    def close(self):
+        if getattr(self, "handle", None) and _lib is not None:
+            _lib.lbv_rope_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def rope_append(rope: Rope, batch: Batch, cache: KVCache, q, k, v, q_out, positions=None,
+                stream=None):
+    """Rotates the new tokens' queries into q_out and their keys into the cache,
+    and copies their values into the cache.  q, k, v: [tokens, heads, head_dim]
+    of one dtype (fp32, fp16, bf16), q_out of the cache's dtype; q and q_out may
+    be None.  positions: int32 [tokens] rotary positions (default: the cache
+    positions)."""
+    n, d = batch.tokens, cache.head_dim
+    k_arg, v_arg = _rows_arg(k, n, d, "k"), _rows_arg(v, n, d, "v")
+    q_arg = None if q is None else ctypes.byref(_rows_arg(q, n, d, "q"))
+    o_arg = None if q_out is None else ctypes.byref(_rows_arg(q_out, n, d, "q_out"))
+    if positions is not None:
+        import torch
+        positions = _words(positions, torch.int32, n, "positions")
+    _check(lib().lbv_rope_append(rope.handle, batch.ref, cache.handle, q_arg, ctypes.byref(k_arg),
+                                 ctypes.byref(v_arg), o_arg, positions, _stream(stream)))
+
+
+def sample(logits, u, token, prob=None, temperature=None, top_k=None, top_p=None, min_p=None,
+           mask=None, temperature_last: bool = False, stream=None):
+    """token[m] (int32) is drawn from row m of logits [M, N] (fp32, fp16, bf16) by
+    the uniform number u[m] (fp32); prob[m] (fp32, optional) is its probability
+    among the kept tokens.  temperature, top_p, min_p: fp32 [M]; top_k: int32
+    [M]; mask: int32 [M, ceil(N / 32)] bits of the allowed tokens; each may be
+    None.  See lbv_sample."""
+    import torch
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1) or not logits.is_cuda:
+        raise LbvError(ERR_INVALID_ARG, "logits: a device tensor [M, N] with contiguous rows is "
+                                        "wanted")
+    m, n = logits.shape
+    f32, i32 = torch.float32, torch.int32
+    if mask is not None and (mask.dim() != 2 or mask.shape[0] < m or mask.shape[1] * 32 < n
+                             or mask.stride(1) != 1 or mask.dtype != i32 or not mask.is_cuda):
+        raise LbvError(ERR_INVALID_ARG, "mask: an int32 device tensor [M, ceil(N / 32)] is wanted")
+    rules = _RulesArg(_words(temperature, f32, m, "temperature"), _words(top_k, i32, m, "top_k"),
+                      _words(top_p, f32, m, "top_p"), _words(min_p, f32, m, "min_p"),
+                      None if mask is None else mask.data_ptr(),
+                      0 if mask is None else mask.stride(0), int(temperature_last))
+    _check(lib().lbv_sample(logits.data_ptr(), m, n, logits.stride(0), _dtype_id(logits),
+                            ctypes.byref(rules), _words(u, f32, m, "u"),
+                            _words(token, i32, m, "token"), _words(prob, f32, m, "prob"),
+                            _stream(stream)))
 
 
 def version() -> str:

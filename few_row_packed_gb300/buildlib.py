@@ -27,6 +27,7 @@ LIB_CHECKED = os.path.join(HERE, "liblbv_checked.so")
 
 SOURCES = [
     "api.cpp",
+    "step_api.cpp",
     "tc_api.cpp",
     "t8_api.cpp",
     "aux_kernels.cu",
@@ -36,6 +37,8 @@ SOURCES = [
     "verify_affine2_g128.cu",
     "verify_q4_0.cu",
     "fused_aux.cu",
+    "rope_append.cu",
+    "sample.cu",
     "tc_aux.cu",
     "tc_sign1.cu",
     "tc_affine2_g32.cu",

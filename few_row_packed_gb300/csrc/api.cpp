@@ -38,6 +38,21 @@ lbv_status cuda_fail(cudaError_t e, const char* what)
     return fail(LBV_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
+}  // namespace
+
+// For the other host files of the library (step_internal.h).
+namespace lbv {
+
+lbv_status set_error(lbv_status st, const char* message)
+{
+    g_err = message ? message : "";
+    return st;
+}
+
+}  // namespace lbv
+
+namespace {
+
 // Rows-per-call counts of the whole process ([m - 1]: calls or active grouped
 // problems with M = m), and the report at exit that LBV_VERIFY_STATS=1 asks
 // for ("dflash-mlx-bonsai2" README, Commands: a rows-per-call histogram of the

@@ -1,0 +1,353 @@
+// step_api.cpp -- the C ABI of the operators around the verify matmul:
+// argument checks, host handles and dispatch of the rotary append, the paged
+// attention and the sampler.  Nothing here aborts or allocates device memory.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <new>
+
+#include "step_internal.h"
+
+namespace {
+
+lbv_status fail(lbv_status st, const char* fmt, ...)
+{
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return lbv::set_error(st, buf);
+}
+
+lbv_status cuda_fail(cudaError_t e, const char* what)
+{
+    return fail(LBV_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
+}
+
+bool aligned(const void* p, size_t n)
+{
+    return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
+}
+
+bool is16(int dtype)
+{
+    return dtype == LBV_F16 || dtype == LBV_BF16;
+}
+
+size_t elem_size(int dtype)
+{
+    return dtype == LBV_F32 ? 4 : 2;
+}
+
+lbv_status check_batch(const char* fn, const lbv_batch* b)
+{
+    if (!b)
+        return fail(LBV_ERR_INVALID_ARG, "%s: batch is NULL", fn);
+    if (b->requests < 1 || b->requests > 4096 || b->tokens < 0)
+        return fail(LBV_ERR_INVALID_ARG, "%s: requests=%d (1..4096) tokens=%d", fn, b->requests,
+                    b->tokens);
+    if (!b->q_start || !b->kv_len || !b->block_table || !aligned(b->q_start, 4) ||
+        !aligned(b->kv_len, 4) || !aligned(b->block_table, 4))
+        return fail(LBV_ERR_INVALID_ARG, "%s: null or misaligned batch array", fn);
+    if (b->table_pages < 1 || b->table_stride < b->table_pages)
+        return fail(LBV_ERR_INVALID_ARG, "%s: table_pages=%d table_stride=%d", fn, b->table_pages,
+                    b->table_stride);
+    return LBV_OK;
+}
+
+lbv_status check_rows(const char* fn, const char* what, const lbv_rows* r, int tokens)
+{
+    if (!r)
+        return fail(LBV_ERR_INVALID_ARG, "%s: %s is NULL", fn, what);
+    if (r->dtype != LBV_F16 && r->dtype != LBV_BF16 && r->dtype != LBV_F32)
+        return fail(LBV_ERR_INVALID_ARG, "%s: %s has unknown dtype %d", fn, what, r->dtype);
+    if (r->heads < 1 || r->heads > 65535)
+        return fail(LBV_ERR_INVALID_ARG, "%s: %s has %d heads", fn, what, r->heads);
+    if (tokens > 0 && (!r->data || !aligned(r->data, elem_size(r->dtype))))
+        return fail(LBV_ERR_INVALID_ARG, "%s: %s is null or misaligned for its element type", fn,
+                    what);
+    return LBV_OK;
+}
+
+lbv_status check_cache(const char* fn, const lbv_kv_cache* c)
+{
+    if (!c)
+        return fail(LBV_ERR_INVALID_ARG, "%s: cache is NULL", fn);
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev != c->device)
+        return fail(LBV_ERR_INVALID_ARG, "%s: current device %d is not the cache's %d", fn, dev,
+                    c->device);
+    return LBV_OK;
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// The paged cache
+
+lbv_status lbv_kv_cache_create(void* k, void* v, int pages, int page_size, int heads, int head_dim,
+                               int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                               lbv_dtype dtype, lbv_kv_cache** out)
+{
+    const char* fn = "lbv_kv_cache_create";
+    lbv::set_error(LBV_OK, "");
+    if (!out)
+        return fail(LBV_ERR_INVALID_ARG, "%s: out is NULL", fn);
+    *out = nullptr;
+    if (!k || !v || !aligned(k, 16) || !aligned(v, 16))
+        return fail(LBV_ERR_INVALID_ARG, "%s: k or v is null or not 16-byte aligned", fn);
+    if (!is16(dtype))
+        return fail(LBV_ERR_INVALID_ARG, "%s: unknown cache dtype %d", fn, (int)dtype);
+    if (pages < 1 || heads < 1 || heads > 65535)
+        return fail(LBV_ERR_INVALID_ARG, "%s: pages=%d heads=%d", fn, pages, heads);
+    if (page_size < 8 || page_size > 1024 || (page_size & (page_size - 1)) != 0)
+        return fail(LBV_ERR_UNSUPPORTED, "%s: page_size %d (a power of two, 8..1024)", fn,
+                    page_size);
+    if (head_dim != 64 && head_dim != 128)
+        return fail(LBV_ERR_UNSUPPORTED, "%s: head_dim %d (64 or 128)", fn, head_dim);
+    // the dimensions may come in any order but do not overlap: sorted by
+    // stride, each holds the extent of the ones inside it
+    int64_t st[3] = {page_stride, token_stride, head_stride};
+    int64_t ext[3] = {pages, page_size, heads};
+    for (int i = 0; i < 3; ++i) {
+        if (st[i] < head_dim || st[i] % 8 != 0 || st[i] >= (int64_t)1 << 38)
+            return fail(LBV_ERR_INVALID_ARG,
+                        "%s: strides (%lld, %lld, %lld) are multiples of 8, at least head_dim", fn,
+                        (long long)page_stride, (long long)token_stride, (long long)head_stride);
+        for (int j = i; j > 0 && st[j] < st[j - 1]; --j) {
+            const int64_t a = st[j], e = ext[j];
+            st[j] = st[j - 1], ext[j] = ext[j - 1];
+            st[j - 1] = a, ext[j - 1] = e;
+        }
+    }
+    int64_t inner = head_dim;
+    for (int i = 0; i < 3; ++i) {
+        if (ext[i] > 1 && st[i] < inner)
+            return fail(LBV_ERR_INVALID_ARG, "%s: strides (%lld, %lld, %lld) overlap", fn,
+                        (long long)page_stride, (long long)token_stride, (long long)head_stride);
+        inner = st[i] * (ext[i] - 1) + inner;
+    }
+    lbv_kv_cache* c = new (std::nothrow) lbv_kv_cache();
+    if (!c)
+        return fail(LBV_ERR_INVALID_ARG, "%s: out of host memory", fn);
+    int shift = 0;
+    while ((1 << shift) < page_size)
+        ++shift;
+    c->view = {static_cast<uint16_t*>(k), static_cast<uint16_t*>(v), page_stride, token_stride,
+               head_stride, pages, shift, heads, head_dim};
+    c->dtype = dtype;
+    if (cudaGetDevice(&c->device) != cudaSuccess) {
+        cudaGetLastError();
+        c->device = -1;
+    }
+    *out = c;
+    return LBV_OK;
+}
+
+lbv_status lbv_kv_cache_destroy(lbv_kv_cache* cache)
+{
+    delete cache;
+    return LBV_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Rotary positions
+
+lbv_status lbv_rope_frequencies(int rot_dim, double base, lbv_rope_scaling scaling, double factor,
+                                double trained, double low, double high, double* freqs)
+{
+    const char* fn = "lbv_rope_frequencies";
+    lbv::set_error(LBV_OK, "");
+    if (!freqs || rot_dim < 2 || rot_dim % 2 != 0 || !(base > 0) || !std::isfinite(base))
+        return fail(LBV_ERR_INVALID_ARG, "%s: freqs NULL, rot_dim=%d or base=%g", fn, rot_dim,
+                    base);
+    if (scaling != LBV_ROPE_NONE && scaling != LBV_ROPE_LINEAR && scaling != LBV_ROPE_BY_PARTS)
+        return fail(LBV_ERR_INVALID_ARG, "%s: unknown scaling %d", fn, (int)scaling);
+    if (scaling != LBV_ROPE_NONE && !(factor > 0 && std::isfinite(factor)))
+        return fail(LBV_ERR_INVALID_ARG, "%s: factor=%g", fn, factor);
+    if (scaling == LBV_ROPE_BY_PARTS && !(trained > 0 && low < high))
+        return fail(LBV_ERR_INVALID_ARG, "%s: trained=%g low=%g high=%g", fn, trained, low, high);
+    const double two_pi = 6.283185307179586476925;
+    for (int j = 0; j < rot_dim / 2; ++j) {
+        double f = std::pow(base, -2.0 * j / rot_dim);
+        if (scaling == LBV_ROPE_LINEAR) {
+            f /= factor;
+        } else if (scaling == LBV_ROPE_BY_PARTS) {
+            const double g = std::fmin(std::fmax((trained * f / two_pi - low) / (high - low), 0.0), 1.0);
+            f *= (1.0 - g) / factor + g;
+        }
+        freqs[j] = f;
+    }
+    return LBV_OK;
+}
+
+lbv_status lbv_rope_create(const double* freqs, int rot_dim, lbv_rope_layout layout, float factor,
+                           lbv_rope** out)
+{
+    const char* fn = "lbv_rope_create";
+    lbv::set_error(LBV_OK, "");
+    if (!out)
+        return fail(LBV_ERR_INVALID_ARG, "%s: out is NULL", fn);
+    *out = nullptr;
+    if (!freqs || rot_dim < 8 || rot_dim > lbv::kMaxRot || rot_dim % 8 != 0)
+        return fail(LBV_ERR_INVALID_ARG, "%s: freqs NULL or rot_dim=%d (a multiple of 8, 8..%d)",
+                    fn, rot_dim, lbv::kMaxRot);
+    if (layout != LBV_ROPE_HALF && layout != LBV_ROPE_INTERLEAVED)
+        return fail(LBV_ERR_INVALID_ARG, "%s: unknown layout %d", fn, (int)layout);
+    if (!std::isfinite(factor))
+        return fail(LBV_ERR_INVALID_ARG, "%s: factor=%g", fn, (double)factor);
+    for (int j = 0; j < rot_dim / 2; ++j)
+        if (!std::isfinite(freqs[j]))
+            return fail(LBV_ERR_INVALID_ARG, "%s: frequency %d is not finite", fn, j);
+    lbv_rope* r = new (std::nothrow) lbv_rope();
+    if (!r)
+        return fail(LBV_ERR_INVALID_ARG, "%s: out of host memory", fn);
+    const double two_pi = 6.283185307179586476925;
+    for (int j = 0; j < rot_dim / 2; ++j) {
+        // fraction of a turn per position in [0, 1), then in 2^-64 turns
+        double t = freqs[j] / two_pi;
+        t -= std::floor(t);
+        const double s = std::ldexp(t, 64);
+        r->turns[j] = s >= 18446744073709551616.0 ? 0 : (uint64_t)s;
+    }
+    r->rot = rot_dim;
+    r->layout = layout;
+    r->factor = factor;
+    *out = r;
+    return LBV_OK;
+}
+
+lbv_status lbv_rope_destroy(lbv_rope* rope)
+{
+    delete rope;
+    return LBV_OK;
+}
+
+lbv_status lbv_rope_append(const lbv_rope* rope, const lbv_batch* batch, const lbv_kv_cache* cache,
+                           const lbv_rows* q, const lbv_rows* k, const lbv_rows* v,
+                           const lbv_rows* q_out, const int32_t* positions, lbv_stream stream)
+{
+    const char* fn = "lbv_rope_append";
+    lbv::set_error(LBV_OK, "");
+    if (!rope)
+        return fail(LBV_ERR_INVALID_ARG, "%s: rope is NULL", fn);
+    lbv_status st = check_batch(fn, batch);
+    if (st == LBV_OK)
+        st = check_rows(fn, "k", k, batch->tokens);
+    if (st == LBV_OK)
+        st = check_rows(fn, "v", v, batch->tokens);
+    if (st == LBV_OK && (q || q_out)) {
+        st = check_rows(fn, "q", q, batch->tokens);
+        if (st == LBV_OK)
+            st = check_rows(fn, "q_out", q_out, batch->tokens);
+    }
+    if (st == LBV_OK)
+        st = check_cache(fn, cache);
+    if (st != LBV_OK)
+        return st;
+    if (k->dtype != v->dtype || (q && q->dtype != k->dtype))
+        return fail(LBV_ERR_INVALID_ARG, "%s: q, k and v have different dtypes", fn);
+    if (q && (q_out->dtype != cache->dtype || q_out->heads != q->heads))
+        return fail(LBV_ERR_INVALID_ARG, "%s: q_out is not of the cache's dtype with q's heads", fn);
+    if (k->heads != cache->view.heads || v->heads != cache->view.heads)
+        return fail(LBV_ERR_INVALID_ARG, "%s: k has %d and v %d heads, the cache %d", fn, k->heads,
+                    v->heads, cache->view.heads);
+    if (rope->rot > cache->view.dim)
+        return fail(LBV_ERR_UNSUPPORTED, "%s: rot_dim %d exceeds head_dim %d", fn, rope->rot,
+                    cache->view.dim);
+    if (!aligned(positions, 4))
+        return fail(LBV_ERR_INVALID_ARG, "%s: positions misaligned", fn);
+    if (batch->tokens == 0)
+        return LBV_OK;
+    lbv::RopeParams p;
+    const lbv_rows* rows[3] = {q, k, v};
+    bool vec = true;        // 4-element loads of every row, 4-element stores of q_out
+    for (int i = 0; i < 3; ++i) {
+        const lbv_rows* r = rows[i];
+        p.src[i] = r ? r->data : nullptr;
+        p.src_token[i] = r ? r->token_stride : 0;
+        p.src_head[i] = r ? r->head_stride : 0;
+        vec = vec && (!r || (aligned(r->data, 4 * elem_size(r->dtype)) &&
+                             r->token_stride % 4 == 0 && r->head_stride % 4 == 0));
+    }
+    p.q_out = q_out ? static_cast<uint16_t*>(q_out->data) : nullptr;
+    p.out_token = q_out ? q_out->token_stride : 0;
+    p.out_head = q_out ? q_out->head_stride : 0;
+    vec = vec && (!q_out || (aligned(q_out->data, 8) && p.out_token % 4 == 0 && p.out_head % 4 == 0));
+    for (int j = 0; j < rope->rot / 2; ++j)
+        p.turns[j] = rope->turns[j];
+    p.batch = *batch;
+    p.kv = cache->view;
+    p.positions = positions;
+    p.q_heads = q ? q->heads : 0;
+    p.rot = rope->rot;
+    p.factor = rope->factor;
+    const cudaError_t e = lbv::launch_rope_append(p, (lbv_dtype)k->dtype, cache->dtype,
+                                                  rope->layout, vec, (cudaStream_t)stream);
+    if (e != cudaSuccess)
+        return cuda_fail(e, "lbv_rope_append: launch");
+    return LBV_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Sampling
+
+lbv_status lbv_sample(const void* logits, int M, int N, int64_t ld, lbv_dtype dtype,
+                      const lbv_sample_rules* rules, const float* u, int32_t* token, float* prob,
+                      lbv_stream stream)
+{
+    const char* fn = "lbv_sample";
+    lbv::set_error(LBV_OK, "");
+    if (dtype != LBV_F32 && dtype != LBV_F16 && dtype != LBV_BF16)
+        return fail(LBV_ERR_INVALID_ARG, "%s: unknown dtype %d", fn, (int)dtype);
+    if (M < 0 || M > (1 << 24) || N < 1 || (M > 1 && ld < N))
+        return fail(LBV_ERR_INVALID_ARG, "%s: M=%d N=%d ld=%lld", fn, M, N, (long long)ld);
+    if (!rules)
+        return fail(LBV_ERR_INVALID_ARG, "%s: rules is NULL", fn);
+    if (rules->temperature_last != 0 && rules->temperature_last != 1)
+        return fail(LBV_ERR_INVALID_ARG, "%s: temperature_last=%d", fn, rules->temperature_last);
+    const void* words[] = {u, token, prob, rules->temperature, rules->top_k, rules->top_p,
+                           rules->min_p, rules->mask};
+    for (const void* w : words)
+        if (!aligned(w, 4))
+            return fail(LBV_ERR_INVALID_ARG, "%s: a per-row array is misaligned", fn);
+    if (rules->mask && M > 1 && rules->mask_ld < (N + 31) / 32)
+        return fail(LBV_ERR_INVALID_ARG, "%s: mask_ld=%lld < %d words", fn,
+                    (long long)rules->mask_ld, (N + 31) / 32);
+    // rows as many as can be in flight at once take more CTAs each
+    const int most = lbv::sample_max_slice();
+    int ctas = M <= 16 ? 8 : 4;
+    while (ctas < 16 && (int64_t)ctas * most < N)
+        ctas *= 2;
+    while (ctas > 1 && N <= ctas * 2048)
+        ctas /= 2;
+    if ((int64_t)ctas * most < N)
+        return fail(LBV_ERR_UNSUPPORTED, "%s: N=%d exceeds %d logits a row", fn, N, 16 * most);
+    if (M == 0)
+        return LBV_OK;
+    if (!logits || !aligned(logits, elem_size(dtype)) || !u || !token)
+        return fail(LBV_ERR_INVALID_ARG, "%s: null or misaligned logits, u or token", fn);
+    lbv::SampleParams p;
+    p.logits = logits;
+    p.mask = rules->mask;
+    p.u = u;
+    p.temperature = rules->temperature;
+    p.top_k = rules->top_k;
+    p.top_p = rules->top_p;
+    p.min_p = rules->min_p;
+    p.token = token;
+    p.prob = prob;
+    p.ld = ld;
+    p.mask_ld = rules->mask_ld;
+    p.N = N;
+    p.ctas = ctas;
+    p.slice = ((N + ctas - 1) / ctas + 31) / 32 * 32;
+    p.temperature_last = rules->temperature_last;
+    const cudaError_t e = lbv::launch_sample(p, M, dtype, (cudaStream_t)stream);
+    if (e != cudaSuccess)
+        return cuda_fail(e, "lbv_sample: launch");
+    return LBV_OK;
+}

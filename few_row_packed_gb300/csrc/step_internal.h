@@ -1,0 +1,77 @@
+// step_internal.h -- the operators around the verify matmul (rotary append,
+// paged attention, sampling): host objects, launch parameters and launchers
+// shared by step_api.cpp and the kernels' files.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/lbv.h"
+
+namespace lbv {
+
+// Records `message` ("" clears it) as the thread's last error; returns st.
+lbv_status set_error(lbv_status st, const char* message);
+
+// A paged cache as the kernels see it (strides in elements).
+struct KvView {
+    uint16_t* k;
+    uint16_t* v;
+    int64_t page_stride, token_stride, head_stride;
+    int pages, page_shift, heads, dim;
+};
+
+// Frequencies of a rotation in 2^-64 turns per position.
+constexpr int kMaxRot = 128;
+
+struct RopeParams {
+    uint64_t turns[kMaxRot / 2];
+    const void* src[3];              // q, k, v rows
+    int64_t src_token[3], src_head[3];
+    uint16_t* q_out;                 // NULL: no queries
+    int64_t out_token, out_head;
+    lbv_batch batch;
+    KvView kv;
+    const int32_t* positions;        // NULL: cache positions
+    int q_heads;                     // 0 without queries
+    int rot;
+    float factor;
+};
+
+cudaError_t launch_rope_append(const RopeParams& p, lbv_dtype src, lbv_dtype dst,
+                               lbv_rope_layout layout, bool vec, cudaStream_t st);
+
+struct SampleParams {
+    const void* logits;              // [rows][ld]
+    const uint32_t* mask;            // [rows][mask_ld] allowed-token bits, or NULL
+    const float* u;                  // [rows]; the rest may be NULL
+    const float* temperature;
+    const int32_t* top_k;
+    const float* top_p;
+    const float* min_p;
+    int32_t* token;                  // [rows]
+    float* prob;                     // [rows] or NULL
+    int64_t ld, mask_ld;
+    int N;
+    int ctas, slice;                 // cluster size, logits per CTA (a multiple of 32)
+    int temperature_last;
+};
+
+constexpr int kMaxSampleSmem = 224 * 1024;
+int sample_max_slice();
+cudaError_t launch_sample(const SampleParams& p, int rows, lbv_dtype dt, cudaStream_t st);
+
+}  // namespace lbv
+
+struct lbv_kv_cache {
+    lbv::KvView view;
+    lbv_dtype dtype;
+    int device;                      // -1: created without a device
+};
+
+struct lbv_rope {
+    uint64_t turns[lbv::kMaxRot / 2];
+    int rot;
+    lbv_rope_layout layout;
+    float factor;
+};

@@ -71,7 +71,9 @@ typedef enum {
     LBV_FMT_Q4_0 = 2
 } lbv_format;
 
-typedef enum { LBV_F16 = 0, LBV_BF16 = 1 } lbv_dtype;
+/* LBV_F32: only where an entry point says so (rows of lbv_rope_append, logits of
+ * lbv_sample); plans, groups and caches take the two 16-bit types. */
+typedef enum { LBV_F16 = 0, LBV_BF16 = 1, LBV_F32 = 2 } lbv_dtype;
 
 /* Plan flags. */
 #define LBV_PLAN_MEASURE     0x1u  /* time the candidate launch shapes (as
@@ -448,6 +450,144 @@ LBV_API lbv_status lbv_group_rows_reset(lbv_group* group);
  * (calls C, mean rows R)".
  */
 LBV_API lbv_status lbv_rows_histogram(uint64_t* counts);
+
+/* ------------------------------------------------------------------------ */
+/* The verify step around the matmul: the new tokens' keys and values enter a */
+/* paged cache with their positions rotated in, the new tokens attend over    */
+/* that cache, and tokens are drawn from the head's logits.                   */
+
+/* The new tokens of one step.  Request r has the rows q_start[r] ..
+ * q_start[r + 1] - 1 of the token-major tensors (n_r >= 0 of them) and a
+ * context of kv_len[r] tokens, the new ones included: its new token i has the
+ * cache position kv_len[r] - n_r + i.  Position p of request r lives in slot
+ * p % page_size of page block_table[r][p / page_size].  All arrays are dev
+ * int32, read by the kernels when they run.  Rows at or past
+ * q_start[requests] belong to no request: they are neither read nor written. */
+typedef struct lbv_batch {
+    const int32_t* q_start;      /* [requests + 1], ascending, q_start[0] >= 0    */
+    const int32_t* kv_len;       /* [requests]                                    */
+    const int32_t* block_table;  /* [requests][table_stride]                      */
+    int requests;                /* 1..4096                                       */
+    int tokens;                  /* rows of the token-major tensors, >= 0         */
+    int table_stride;            /* >= table_pages                                */
+    int table_pages;             /* entries per request                           */
+} lbv_batch;
+
+/* A token-major tensor [tokens][heads][head_dim]; strides in elements, the
+ * last dimension contiguous. */
+typedef struct lbv_rows {
+    void* data;                  /* dev                                           */
+    int heads;
+    int dtype;                   /* lbv_dtype                                     */
+    int64_t token_stride;
+    int64_t head_stride;
+} lbv_rows;
+
+typedef struct lbv_kv_cache lbv_kv_cache;   /* opaque, library-owned, host memory only */
+
+/* Describes a caller-owned paged cache: k and v (dev, 16-byte aligned, dtype
+ * fp16 or bf16) hold pages x page_size x heads x head_dim elements at
+ * page * page_stride + slot * token_stride + head * head_stride (elements,
+ * any order of the dimensions, each a multiple of 8; one set of strides for
+ * both).  page_size: a power of two, 8..1024; head_dim: 64 or 128.  Offsets
+ * are 64-bit throughout.  Allocates host memory only; the handle is immutable.
+ * LBV_ERR_UNSUPPORTED for other head dims and page sizes. */
+LBV_API lbv_status lbv_kv_cache_create(void* k, void* v, int pages, int page_size, int heads,
+                                       int head_dim, int64_t page_stride, int64_t token_stride,
+                                       int64_t head_stride, lbv_dtype dtype, lbv_kv_cache** out);
+LBV_API lbv_status lbv_kv_cache_destroy(lbv_kv_cache* cache);
+
+typedef enum {
+    LBV_ROPE_HALF = 0,         /* pair j of a head: elements j and j + rot_dim/2   */
+    LBV_ROPE_INTERLEAVED = 1   /* pair j of a head: elements 2j and 2j + 1          */
+} lbv_rope_layout;
+
+typedef enum {
+    LBV_ROPE_NONE = 0,         /* f_j = base^(-2j/rot_dim)                          */
+    LBV_ROPE_LINEAR = 1,       /* f_j / factor                                      */
+    LBV_ROPE_BY_PARTS = 2      /* f_j * ((1 - g) / factor + g), g = clamp((r - low) /
+                                  (high - low), 0, 1) with r = trained * f_j / 2 pi the
+                                  turns of pair j in the trained length (Peng et al.
+                                  2023, "YaRN", section 3.2)                        */
+} lbv_rope_scaling;
+
+/* Host helper: radians per position of the rot_dim/2 pairs.  rot_dim even,
+ * base > 0; factor > 0 unless LBV_ROPE_NONE; trained > 0 and low < high for
+ * LBV_ROPE_BY_PARTS. */
+LBV_API lbv_status lbv_rope_frequencies(int rot_dim, double base, lbv_rope_scaling scaling,
+                                        double factor, double trained, double low, double high,
+                                        double* freqs);
+
+typedef struct lbv_rope lbv_rope;           /* opaque, library-owned, host memory only */
+
+/* A rotation of the first rot_dim elements of a head (a multiple of 8, 8..128)
+ * by position * freqs[j] radians (host [rot_dim/2], finite; copied), cos and
+ * sin multiplied by `factor` (1 for plain rotary positions).  The angle is
+ * reduced exactly: frequencies are kept as 64-bit fractions of a turn and the
+ * product with the position wraps by itself. */
+LBV_API lbv_status lbv_rope_create(const double* freqs, int rot_dim, lbv_rope_layout layout,
+                                   float factor, lbv_rope** out);
+LBV_API lbv_status lbv_rope_destroy(lbv_rope* rope);
+
+/*
+ * For every new token: rotates its query heads into q_out and its key heads
+ * into the cache, and copies its value heads into the cache.
+ *   q, k, v: rows of one dtype (fp32 as the verify matmul writes them, fp16 or
+ *     bf16); k and v have the cache's heads.  q_out: the cache's dtype, the
+ *     heads of q; may be q itself when the dtypes agree.  q and q_out may both be
+ *     NULL (keys and values only).
+ *   positions: dev int32 [tokens] rotary positions, or NULL for the cache
+ *     positions (a tree of drafted tokens has siblings at one position).
+ * Sums are fp32, rounded once.  A token whose slot does not exist (a negative
+ * position, one past the block table, a page outside the cache) has its key
+ * and value left out; its query is rotated all the same.
+ * Errors: LBV_ERR_INVALID_ARG for null or misaligned pointers, sizes that do
+ * not agree and dtypes that cannot be; LBV_ERR_UNSUPPORTED if rot_dim exceeds
+ * the head.  The library allocates nothing.
+ */
+LBV_API lbv_status lbv_rope_append(const lbv_rope* rope, const lbv_batch* batch,
+                                   const lbv_kv_cache* cache, const lbv_rows* q,
+                                   const lbv_rows* k, const lbv_rows* v, const lbv_rows* q_out,
+                                   const int32_t* positions, lbv_stream stream);
+
+/* How lbv_sample draws: dev arrays with one entry per row, each may be NULL. */
+typedef struct lbv_sample_rules {
+    const float* temperature;    /* NULL: 1; a row with T <= 0 (or NaN) takes its
+                                    largest logit                                */
+    const int32_t* top_k;        /* keep the k largest; <= 0: off                */
+    const float* top_p;          /* keep the largest tokens until their weights
+                                    reach this share (of what top-k kept); >= 1:
+                                    off                                          */
+    const float* min_p;          /* keep tokens of at least this share of the
+                                    largest token's weight; <= 0: off            */
+    const uint32_t* mask;        /* [M][mask_ld]: token i is allowed if bit i % 32
+                                    of word i / 32 is set; NULL: all             */
+    int64_t mask_ld;             /* words per row                                */
+    int temperature_last;        /* 0: the filters see the weights after the
+                                    temperature; 1: before it (Ishizuki README,
+                                    sampler chain: top-k, top-p, min-p,
+                                    temperature)                                 */
+} lbv_sample_rules;
+
+/*
+ * token[m] = a token of row m < M drawn by u[m] (dev fp32, in [0, 1), taken to
+ * 24 bits), prob[m] (or NULL) = its probability among the kept tokens.
+ * logits: dev [M][ld], fp32 as the verify matmul writes them, fp16 or bf16.
+ *   Weights are whole numbers, W = floor(2^40 exp((l - max) / T)) with fp32
+ * arithmetic inside the exponential, so their sums do not depend on an order
+ * and equal inputs give equal tokens at any batch.  Rank is by logit, the
+ * lower index first among equals (-0 equals +0).  top-p keeps a token while the
+ * weights ranked before it are less than floor(floor(top_p 2^24) total / 2^24);
+ * the first token is always kept.  The token is the lowest index at which the
+ * running sum of kept weights in index order exceeds floor(floor(u 2^24) kept
+ * / 2^24).  NaN and -inf logits are never drawn; +inf ones share all weight.  A
+ * row with nothing left to draw gives token -1 and prob 0.
+ *   N at most about 740 thousand (LBV_ERR_UNSUPPORTED).  The library allocates
+ * nothing.
+ */
+LBV_API lbv_status lbv_sample(const void* logits, int M, int N, int64_t ld, lbv_dtype dtype,
+                              const lbv_sample_rules* rules, const float* u, int32_t* token,
+                              float* prob, lbv_stream stream);
 
 /*
  * Test export: X' exactly as lbv_verify_fused with LBV_FUSED_ROTATE computes
