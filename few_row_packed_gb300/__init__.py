@@ -146,6 +146,9 @@ def lib():
             "lbv_rope_create": (st, [P, I, I, F, ctypes.POINTER(P)]),
             "lbv_rope_destroy": (st, [P]),
             "lbv_rope_append": (st, [P] * 9),
+            "lbv_attend_workspace_bytes": (S, [P, P, I]),
+            "lbv_attend": (st, [P, P, P, P, F, I, P, P, P, S, P]),
+            "lbv_attend_status": (st, [P]),
             "lbv_sample": (st, [P, I, I, L64, I, P, P, P, P, P]),
             "lbv_last_error": (ctypes.c_char_p, []),
             "lbv_version": (ctypes.c_char_p, []),
@@ -584,6 +587,37 @@ def rope_append(rope: Rope, batch: Batch, cache: KVCache, q, k, v, q_out, positi
         positions = _words(positions, torch.int32, n, "positions")
     _check(lib().lbv_rope_append(rope.handle, batch.ref, cache.handle, q_arg, ctypes.byref(k_arg),
                                  ctypes.byref(v_arg), o_arg, positions, _stream(stream)))
+
+
+def attend_workspace_bytes(cache: KVCache, batch: Batch, heads: int) -> int:
+    """Bytes of device workspace (zeroed once by the caller) that attend needs
+    for batches of this many requests and tokens and `heads` query heads."""
+    return int(lib().lbv_attend_workspace_bytes(cache.handle, batch.ref, heads))
+
+
+def attend(cache: KVCache, batch: Batch, q, out, scale: float, window: int = 0, tree=None,
+           lse=None, workspace=None, stream=None):
+    """out[t, h] = attention of new token t's query head h over its request's
+    context in the cache; q, out: [tokens, heads, head_dim] of the cache's
+    dtype.  window > 0: only the last `window` positions; tree: int64 [tokens]
+    words of the request's new tokens each one sees (default: causal); lse: fp32
+    [tokens, heads]; workspace: attend_workspace_bytes, zeroed once.  See
+    lbv_attend."""
+    n, d = batch.tokens, cache.head_dim
+    q_arg, o_arg = _rows_arg(q, n, d, "q"), _rows_arg(out, n, d, "out")
+    if tree is not None or lse is not None:
+        import torch
+        tree = _words(tree, torch.int64, n, "tree")
+        lse = _words(lse, torch.float32, n * q.shape[1], "lse")
+    ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().lbv_attend(cache.handle, batch.ref, ctypes.byref(q_arg), ctypes.byref(o_arg),
+                            scale, window, tree, lse, _ptr(workspace), ws, _stream(stream)))
+
+
+def attend_status(workspace):
+    """Raises LbvError(ERR_TIMEOUT) if an attention kernel that used the
+    workspace gave up a bounded wait (synchronises the device)."""
+    _check(lib().lbv_attend_status(_ptr(workspace)))
 
 
 def sample(logits, u, token, prob=None, temperature=None, top_k=None, top_p=None, min_p=None,

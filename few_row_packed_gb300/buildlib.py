@@ -39,6 +39,7 @@ SOURCES = [
     "fused_aux.cu",
     "rope_append.cu",
     "sample.cu",
+    "attend_rows.cu",
     "tc_aux.cu",
     "tc_sign1.cu",
     "tc_affine2_g32.cu",

@@ -1,0 +1,39 @@
+// attend_internal.h -- launch parameters of the attention kernels.
+#pragma once
+
+#include <cuda.h>
+
+#include "step_internal.h"
+
+namespace lbv {
+
+struct AttendParams {
+    const uint16_t* q;               // [tokens][heads][dim], strides in elements
+    int64_t q_token, q_head;
+    uint16_t* out;
+    int64_t out_token, out_head;
+    float* lse;                      // [tokens][heads], natural log, or NULL
+    const uint64_t* tree;            // [tokens] or NULL
+    float scale_log2;                // scale * log2(e)
+    int window;                      // <= 0: none
+    int heads, group;                // query heads, query heads per kv head
+    int q_pairs;                     // q rows are 4-byte aligned
+    lbv_batch batch;
+    KvView kv;
+    // workspace
+    unsigned* status;                // error bits
+    unsigned* counters;              // one per CTA, zero between calls
+    float* partial;                  // slots of partial results
+};
+
+// Rows (new token, query head of the group) of one work item of the few-row
+// kernel, and the bytes of its partial-result slots.
+constexpr int kAttendMaxCtas = 512;
+constexpr size_t kAttendHeader = 256;            // status word, then the counters
+
+cudaError_t launch_attend_rows(const AttendParams& p, const CUtensorMap& kmap,
+                               const CUtensorMap& vmap, lbv_dtype dt, int sms, cudaStream_t st);
+// Floats of workspace the launch needs for partial results.
+size_t attend_rows_partial_floats(int dim, int sms);
+
+}  // namespace lbv

@@ -8,6 +8,7 @@
 #include <cstdio>
 #include <new>
 
+#include "attend_internal.h"
 #include "step_internal.h"
 
 namespace {
@@ -83,6 +84,44 @@ lbv_status check_cache(const char* fn, const lbv_kv_cache* c)
     return LBV_OK;
 }
 
+// The driver's tensor-map encoder, found once; NULL without a driver.
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+
+EncodeTiled encode_tiled()
+{
+    static const EncodeTiled fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            return (EncodeTiled) nullptr;
+        }
+        return (EncodeTiled)p;
+    }();
+    return fn;
+}
+
+// Boxes of 64 elements of one head by min(page_size, 64) slots of one page, in
+// 128-byte rows swizzled as ldmatrix and tcgen05 read them.
+bool make_map(const lbv::KvView& v, lbv_dtype dtype, void* base, CUtensorMap* map)
+{
+    const EncodeTiled fn = encode_tiled();
+    if (!fn)
+        return false;
+    const cuuint64_t page = (cuuint64_t)1 << v.page_shift;
+    const cuuint64_t dims[4] = {(cuuint64_t)v.dim, page, (cuuint64_t)v.heads, (cuuint64_t)v.pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)v.token_stride * 2, (cuuint64_t)v.head_stride * 2,
+                                   (cuuint64_t)v.page_stride * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)(page < 64 ? page : 64), 1, 1};
+    const cuuint32_t one[4] = {1, 1, 1, 1};
+    return fn(map, dtype == LBV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+              4, base, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 // ---------------------------------------------------------------------------
@@ -139,9 +178,17 @@ lbv_status lbv_kv_cache_create(void* k, void* v, int pages, int page_size, int h
     c->view = {static_cast<uint16_t*>(k), static_cast<uint16_t*>(v), page_stride, token_stride,
                head_stride, pages, shift, heads, head_dim};
     c->dtype = dtype;
-    if (cudaGetDevice(&c->device) != cudaSuccess) {
+    c->sms = 0;
+    if (cudaGetDevice(&c->device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&c->sms, cudaDevAttrMultiProcessorCount, c->device) != cudaSuccess) {
         cudaGetLastError();
         c->device = -1;
+    }
+    c->maps = c->device >= 0 && make_map(c->view, dtype, k, &c->kmap) &&
+              make_map(c->view, dtype, v, &c->vmap);
+    if (c->device >= 0 && !c->maps) {
+        delete c;
+        return fail(LBV_ERR_CUDA, "%s: the driver has no tensor map for this layout", fn);
     }
     *out = c;
     return LBV_OK;
@@ -289,6 +336,94 @@ lbv_status lbv_rope_append(const lbv_rope* rope, const lbv_batch* batch, const l
                                                   rope->layout, vec, (cudaStream_t)stream);
     if (e != cudaSuccess)
         return cuda_fail(e, "lbv_rope_append: launch");
+    return LBV_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Attention over the paged cache
+
+size_t lbv_attend_workspace_bytes(const lbv_kv_cache* cache, const lbv_batch* batch, int heads)
+{
+    if (!cache || !batch || heads < 1)
+        return 0;
+    return lbv::kAttendHeader + lbv::kAttendMaxCtas * sizeof(unsigned) +
+           lbv::attend_rows_partial_floats(cache->view.dim, cache->sms) * sizeof(float);
+}
+
+lbv_status lbv_attend(const lbv_kv_cache* cache, const lbv_batch* batch, const lbv_rows* q,
+                      const lbv_rows* out, float scale, int window, const uint64_t* tree,
+                      float* lse, void* workspace, size_t workspace_bytes, lbv_stream stream)
+{
+    const char* fn = "lbv_attend";
+    lbv::set_error(LBV_OK, "");
+    lbv_status st = check_batch(fn, batch);
+    if (st == LBV_OK)
+        st = check_rows(fn, "q", q, batch->tokens);
+    if (st == LBV_OK)
+        st = check_rows(fn, "out", out, batch->tokens);
+    if (st == LBV_OK)
+        st = check_cache(fn, cache);
+    if (st != LBV_OK)
+        return st;
+    if (q->dtype != cache->dtype || out->dtype != cache->dtype)
+        return fail(LBV_ERR_INVALID_ARG, "%s: q or out is not of the cache's dtype", fn);
+    if (q->heads != out->heads || q->heads % cache->view.heads != 0)
+        return fail(LBV_ERR_INVALID_ARG, "%s: %d query and %d output heads over %d cache heads", fn,
+                    q->heads, out->heads, cache->view.heads);
+    if (!std::isfinite(scale) || window < 0)
+        return fail(LBV_ERR_INVALID_ARG, "%s: scale=%g window=%d", fn, (double)scale, window);
+    if (!aligned(tree, 8) || !aligned(lse, 4))
+        return fail(LBV_ERR_INVALID_ARG, "%s: tree or lse misaligned", fn);
+    if (batch->tokens == 0)
+        return LBV_OK;
+    if (!workspace || !aligned(workspace, 256) ||
+        workspace_bytes < lbv_attend_workspace_bytes(cache, batch, q->heads))
+        return fail(LBV_ERR_WORKSPACE, "%s: workspace NULL, not 256-byte aligned or %zu < %zu bytes",
+                    fn, workspace_bytes, lbv_attend_workspace_bytes(cache, batch, q->heads));
+    lbv::AttendParams p;
+    p.q = static_cast<const uint16_t*>(q->data);
+    p.q_token = q->token_stride;
+    p.q_head = q->head_stride;
+    p.out = static_cast<uint16_t*>(out->data);
+    p.out_token = out->token_stride;
+    p.out_head = out->head_stride;
+    p.lse = lse;
+    p.tree = tree;
+    p.scale_log2 = scale * 1.44269504088896341f;
+    p.window = window;
+    p.heads = q->heads;
+    p.group = q->heads / cache->view.heads;
+    p.q_pairs = aligned(q->data, 4) && q->token_stride % 2 == 0 && q->head_stride % 2 == 0;
+    p.batch = *batch;
+    p.kv = cache->view;
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    p.status = reinterpret_cast<unsigned*>(ws);
+    p.counters = reinterpret_cast<unsigned*>(ws + lbv::kAttendHeader);
+    p.partial = reinterpret_cast<float*>(ws + lbv::kAttendHeader +
+                                         lbv::kAttendMaxCtas * sizeof(unsigned));
+    const cudaError_t e = lbv::launch_attend_rows(p, cache->kmap, cache->vmap, cache->dtype,
+                                                  cache->sms, (cudaStream_t)stream);
+    if (e != cudaSuccess)
+        return cuda_fail(e, "lbv_attend: launch");
+    return LBV_OK;
+}
+
+lbv_status lbv_attend_status(void* workspace)
+{
+    const char* fn = "lbv_attend_status";
+    lbv::set_error(LBV_OK, "");
+    if (!workspace)
+        return fail(LBV_ERR_INVALID_ARG, "%s: workspace is NULL", fn);
+    unsigned word = 0;
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e == cudaSuccess)
+        e = cudaMemcpy(&word, workspace, sizeof word, cudaMemcpyDeviceToHost);
+    if (e == cudaSuccess && word)
+        e = cudaMemset(workspace, 0, lbv::kAttendHeader + lbv::kAttendMaxCtas * sizeof(unsigned));
+    if (e != cudaSuccess)
+        return cuda_fail(e, fn);
+    if (word)
+        return fail(LBV_ERR_TIMEOUT, "an attention kernel gave up waiting for its copies");
     return LBV_OK;
 }
 

@@ -3,6 +3,7 @@
 // shared by step_api.cpp and the kernels' files.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -66,7 +67,9 @@ cudaError_t launch_sample(const SampleParams& p, int rows, lbv_dtype dt, cudaStr
 struct lbv_kv_cache {
     lbv::KvView view;
     lbv_dtype dtype;
-    int device;                      // -1: created without a device
+    int device, sms;                 // -1: created without a device
+    bool maps;                       // the tensor maps are there
+    CUtensorMap kmap, vmap;          // boxes of 64 elements x the slots of a page in 64 keys
 };
 
 struct lbv_rope {

@@ -550,6 +550,45 @@ LBV_API lbv_status lbv_rope_append(const lbv_rope* rope, const lbv_batch* batch,
                                    const lbv_rows* k, const lbv_rows* v, const lbv_rows* q_out,
                                    const int32_t* positions, lbv_stream stream);
 
+/* Bytes of the workspace lbv_attend needs for this cache, a batch (its counts
+ * alone are read) and so many query heads; 0 for NULL. */
+LBV_API size_t lbv_attend_workspace_bytes(const lbv_kv_cache* cache, const lbv_batch* batch,
+                                          int heads);
+
+/*
+ * Attention of every new token of the batch over its request's context:
+ *   out[t][h] = sum_j softmax_j(scale q[t][h] . k_j) v_j,   k, v of cache head
+ *   h / (q->heads / cache heads),
+ * over the keys j that token i of request r (cache position P = kv_len - n + i)
+ * sees: those below kv_len that the block table maps, and
+ *   without tree: j <= P;
+ *   with tree (dev uint64 [tokens]): every key before the request's new tokens,
+ *     and new token b < 64 where bit b of the token's word is set (a token sees
+ *     itself only by its own bit; new tokens past the 64th are seen by none);
+ *   with window > 0, also j > P - window (0: no window).
+ * lse (dev fp32 [tokens][heads], or NULL) = the natural log of the sum of
+ * exp(scale q . k_j).  A row that sees nothing gets out 0 and lse -inf.
+ *   q, out: rows of the cache's dtype; q->heads a multiple of the cache's
+ * heads.  Sums and softmax are fp32, the probabilities enter the second
+ * product in the cache's dtype, out is rounded once.  Cache slots at or past
+ * kv_len may hold anything; keys and values below it are taken to be finite.
+ * A mapped page outside the cache reads as zeros.
+ *   workspace: dev, 256-byte aligned, lbv_attend_workspace_bytes(); zeroed once
+ * by the caller, left ready for the next call by every call; calls that may
+ * run at the same time need distinct ones.  The result does not depend on
+ * timing.  Errors: LBV_ERR_INVALID_ARG, LBV_ERR_WORKSPACE.  The library
+ * allocates nothing.
+ */
+LBV_API lbv_status lbv_attend(const lbv_kv_cache* cache, const lbv_batch* batch, const lbv_rows* q,
+                              const lbv_rows* out, float scale, int window, const uint64_t* tree,
+                              float* lse, void* workspace, size_t workspace_bytes,
+                              lbv_stream stream);
+
+/* LBV_ERR_TIMEOUT if an attention kernel that used the workspace gave up a
+ * bounded wait since the last check (its output is then incomplete), else
+ * LBV_OK; clears the record.  Synchronises with the device. */
+LBV_API lbv_status lbv_attend_status(void* workspace);
+
 /* How lbv_sample draws: dev arrays with one entry per row, each may be NULL. */
 typedef struct lbv_sample_rules {
     const float* temperature;    /* NULL: 1; a row with T <= 0 (or NaN) takes its
