@@ -40,6 +40,7 @@ SOURCES = [
     "rope_append.cu",
     "sample.cu",
     "attend_rows.cu",
+    "attend_tiles.cu",
     "tc_aux.cu",
     "tc_sign1.cu",
     "tc_affine2_g32.cu",

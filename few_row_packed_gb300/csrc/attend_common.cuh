@@ -149,5 +149,98 @@ __device__ __forceinline__ bool sees(const AttendParams& p, const Request& q, in
     return s && key < q.keys && (p.window <= 0 || key > pos - p.window);
 }
 
+// The same for 32 keys from key0 on, as bits.
+__device__ __forceinline__ uint32_t seen32(const AttendParams& p, const Request& q, int pos, uint64_t w,
+                                           int key0)
+{
+    // keys [lo, hi) relative to key0, cut to 0..32
+    int hi = (p.tree ? q.keys : min(q.keys, pos + 1)) - key0;
+    int lo = p.window > 0 ? pos - p.window + 1 - key0 : 0;
+    hi = max(0, min(hi, 32));
+    lo = max(0, min(lo, 32));
+    uint32_t see = (uint32_t)((1ull << hi) - 1) & ~(uint32_t)((1ull << lo) - 1);
+    if (p.tree) {
+        const int j = key0 - q.first;                   // new token of the first of the keys
+        uint64_t t = j <= -32 ? ~0ull : j < 0 ? (w << -j) | ((1ull << -j) - 1) : j < 64 ? w >> j : 0;
+        see &= (uint32_t)t;
+    }
+    return see;
+}
+
+// Stores N 16-bit values (packed in pairs) of an output row, as wide as its
+// address allows.
+template <int N>
+__device__ __forceinline__ void store_row(uint16_t* d, const uint32_t* r)
+{
+    const uintptr_t a = reinterpret_cast<uintptr_t>(d);
+    if (N % 8 == 0 && (a & 15) == 0) {
+#pragma unroll
+        for (int k = 0; k < N / 8; ++k)
+            reinterpret_cast<uint4*>(d)[k] = make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+    } else if ((a & 3) == 0) {
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k)
+            reinterpret_cast<uint32_t*>(d)[k] = r[k];
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            d[k] = (uint16_t)(r[k >> 1] >> (16 * (k & 1)));
+    }
+}
+
+// The natural log of a row's sum relative to 2^top.
+__device__ __forceinline__ float lse_of(float top, float sum)
+{
+    return sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945f;
+}
+
+// Writes a row's four elements from 4 d4 on (o / sum, rounded once), and with
+// the first of them its lse.  A row that saw nothing (sum 0) gets 0.
+template <int DT>
+__device__ __forceinline__ void finish4(const AttendParams& p, const Request& q, int kv_head, int row,
+                                        int d4, float4 o, float top, float sum)
+{
+    const int i = row / p.group, g = row - i * p.group;
+    const int64_t tok = q.q0 + i;
+    const int head = kv_head * p.group + g;
+    const float f = 1.f / sum;
+    const uint32_t r[2] = {sum == 0.f ? 0u : pack2<DT>(o.x * f, o.y * f),
+                           sum == 0.f ? 0u : pack2<DT>(o.z * f, o.w * f)};
+    store_row<4>(p.out + tok * p.out_token + (int64_t)head * p.out_head + d4 * 4, r);
+    if (p.lse && d4 == 0)
+        p.lse[tok * p.heads + head] = lse_of(top, sum);
+}
+
+// Partial results of an item: slot 2 c + 1 of the CTA c0 it starts in, slot 2 c
+// of the others; a slot holds o [ROWS][D], the reference maxima [ROWS] and the
+// sums [ROWS].  join_parts adds them in CTA order, by the threads tid < threads.
+template <int DT, int D, int ROWS>
+__device__ __forceinline__ void join_parts(const AttendParams& p, const Request& q, int kv_head,
+                                           int row0, int rows, int c0, int c1, int tid, int threads)
+{
+    auto part = [&](int c) {
+        return p.partial + (size_t)(2 * c + (c == c0)) * (ROWS * (D + 2));
+    };
+    for (int i = tid; i < rows * (D / 4); i += threads) {
+        const int row = i / (D / 4), d4 = i % (D / 4);
+        float top = -INFINITY;
+#pragma unroll 4
+        for (int c = c0; c <= c1; ++c)
+            top = fmaxf(top, __ldcg(part(c) + ROWS * D + row));
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f;
+#pragma unroll 4
+        for (int c = c0; c <= c1; ++c) {
+            const float* s = part(c);
+            const float m = __ldcg(s + ROWS * D + row);
+            const float f = m == -INFINITY ? 0.f : ex2(m - top);
+            const float4 a = __ldcg(reinterpret_cast<const float4*>(s + row * D + d4 * 4));
+            sum += f * __ldcg(s + ROWS * (D + 1) + row);
+            o.x += f * a.x, o.y += f * a.y, o.z += f * a.z, o.w += f * a.w;
+        }
+        finish4<DT>(p, q, kv_head, row0 + row, d4, o, top, sum);
+    }
+}
+
 }  // namespace att
 }  // namespace lbv

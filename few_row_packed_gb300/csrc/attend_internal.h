@@ -17,7 +17,7 @@ struct AttendParams {
     float scale_log2;                // scale * log2(e)
     int window;                      // <= 0: none
     int heads, group;                // query heads, query heads per kv head
-    int q_pairs;                     // q rows are 4-byte aligned
+    int q_pairs, q_wide;             // q rows are 4-byte, 16-byte aligned
     lbv_batch batch;
     KvView kv;
     // workspace
@@ -26,14 +26,15 @@ struct AttendParams {
     float* partial;                  // slots of partial results
 };
 
-// Rows (new token, query head of the group) of one work item of the few-row
-// kernel, and the bytes of its partial-result slots.
-constexpr int kAttendMaxCtas = 512;
+constexpr int kAttendMaxCtas = 512;              // CTAs of a launch, and counters
 constexpr size_t kAttendHeader = 256;            // status word, then the counters
 
 cudaError_t launch_attend_rows(const AttendParams& p, const CUtensorMap& kmap,
                                const CUtensorMap& vmap, lbv_dtype dt, int sms, cudaStream_t st);
-// Floats of workspace the launch needs for partial results.
+cudaError_t launch_attend_tiles(const AttendParams& p, const CUtensorMap& kmap,
+                                const CUtensorMap& vmap, lbv_dtype dt, int sms, cudaStream_t st);
+// Floats of workspace the launches need for partial results.
 size_t attend_rows_partial_floats(int dim, int sms);
+size_t attend_tiles_partial_floats(int dim, int sms);
 
 }  // namespace lbv

@@ -518,25 +518,6 @@ __global__ void __launch_bounds__(Geo<D, MT, WM>::THREADS, Geo<D, MT, WM>::CTAS)
         const int c0 = whole ? 0 : w.cta_of(w.item);
         const int c1 = whole ? 0 : w.cta_of(w.item + (unsigned)w.s.blocks - 1);
         float* slot = p.partial + (size_t)(2 * blockIdx.x + (c0 == (int)blockIdx.x)) * G::SLOT;
-        auto finish = [&](int row, int d4, float4 v, float top, float sum) {
-            const int i = (w.row0 + row) / p.group, g = w.row0 + row - i * p.group;
-            const int64_t tok = w.q.q0 + i;
-            const int head = w.head * p.group + g;
-            const float f = sum > 0.f ? 1.f / sum : 0.f;
-            uint16_t* d = p.out + tok * p.out_token + head * p.out_head + d4 * 4;
-            const uint16_t r[4] = {pack1<DT>(v.x * f), pack1<DT>(v.y * f), pack1<DT>(v.z * f),
-                                   pack1<DT>(v.w * f)};
-            if ((reinterpret_cast<uintptr_t>(d) & 7) == 0) {
-                *reinterpret_cast<ushort4*>(d) = make_ushort4(r[0], r[1], r[2], r[3]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    d[e] = r[e];
-            }
-            if (p.lse && d4 == 0)
-                p.lse[tok * p.heads + head] =
-                    sum > 0.f ? (top + log2f(sum)) * 0.693147180559945f : -INFINITY;
-        };
         for (int i = ctid; i < w.rows * (D / 4); i += G::WARPS * 32) {
             const int row = i / (D / 4), d4 = i % (D / 4);
             const float4 v = *reinterpret_cast<const float4*>(obuf + row * G::OLD + d4 * 4);
@@ -548,7 +529,7 @@ __global__ void __launch_bounds__(Geo<D, MT, WM>::THREADS, Geo<D, MT, WM>::CTAS)
             for (int k = 0; k < kKeyWarps; ++k)
                 sum += top == -INFINITY ? 0.f : lbuf[k * ROWS + row] * ex2(mbuf[k * ROWS + row] - top);
             if (whole) {
-                finish(row, d4, v, top, sum);
+                finish4<DT>(p, w.q, w.head, w.row0 + row, d4, v, top, sum);
             } else {
                 *reinterpret_cast<float4*>(slot + row * D + d4 * 4) = v;
                 if (d4 == 0) {
@@ -565,25 +546,7 @@ __global__ void __launch_bounds__(Geo<D, MT, WM>::THREADS, Geo<D, MT, WM>::CTAS)
             named_bar_sync(1, G::WARPS * 32);
             if (*flag) {                                         // every part is there: join them
                 __threadfence();
-                auto part_of = [&](int c) {
-                    return p.partial + (size_t)(2 * c + (c == c0)) * G::SLOT;
-                };
-                for (int i = ctid; i < w.rows * (D / 4); i += G::WARPS * 32) {
-                    const int row = i / (D / 4), d4 = i % (D / 4);
-                    float top = -INFINITY;
-                    for (int c = c0; c <= c1; ++c)
-                        top = fmaxf(top, __ldcg(part_of(c) + ROWS * D + row));
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    float sum = 0.f;
-                    for (int c = c0; c <= c1; ++c) {
-                        const float* s = part_of(c);
-                        const float f = top == -INFINITY ? 0.f : ex2(__ldcg(s + ROWS * D + row) - top);
-                        const float4 a = __ldcg(reinterpret_cast<const float4*>(s + row * D + d4 * 4));
-                        sum += f * __ldcg(s + ROWS * (D + 1) + row);
-                        v.x += f * a.x, v.y += f * a.y, v.z += f * a.z, v.w += f * a.w;
-                    }
-                    finish(row, d4, v, top, sum);
-                }
+                join_parts<DT, D, ROWS>(p, w.q, w.head, w.row0, w.rows, c0, c1, ctid, G::WARPS * 32);
                 if (ctid == 0)
                     p.counters[c0] = 0;                          // as the next call finds it
             }

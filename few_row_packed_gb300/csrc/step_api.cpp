@@ -346,8 +346,10 @@ size_t lbv_attend_workspace_bytes(const lbv_kv_cache* cache, const lbv_batch* ba
 {
     if (!cache || !batch || heads < 1)
         return 0;
+    const size_t rows = lbv::attend_rows_partial_floats(cache->view.dim, cache->sms);
+    const size_t tiles = lbv::attend_tiles_partial_floats(cache->view.dim, cache->sms);
     return lbv::kAttendHeader + lbv::kAttendMaxCtas * sizeof(unsigned) +
-           lbv::attend_rows_partial_floats(cache->view.dim, cache->sms) * sizeof(float);
+           (rows > tiles ? rows : tiles) * sizeof(float);
 }
 
 lbv_status lbv_attend(const lbv_kv_cache* cache, const lbv_batch* batch, const lbv_rows* q,
@@ -390,10 +392,11 @@ lbv_status lbv_attend(const lbv_kv_cache* cache, const lbv_batch* batch, const l
     p.lse = lse;
     p.tree = tree;
     p.scale_log2 = scale * 1.44269504088896341f;
-    p.window = window;
+    p.window = window < (1 << 30) ? window : 0;    // no context is that long
     p.heads = q->heads;
     p.group = q->heads / cache->view.heads;
     p.q_pairs = aligned(q->data, 4) && q->token_stride % 2 == 0 && q->head_stride % 2 == 0;
+    p.q_wide = aligned(q->data, 16) && q->token_stride % 8 == 0 && q->head_stride % 8 == 0;
     p.batch = *batch;
     p.kv = cache->view;
     unsigned char* ws = static_cast<unsigned char*>(workspace);
@@ -401,8 +404,12 @@ lbv_status lbv_attend(const lbv_kv_cache* cache, const lbv_batch* batch, const l
     p.counters = reinterpret_cast<unsigned*>(ws + lbv::kAttendHeader);
     p.partial = reinterpret_cast<float*>(ws + lbv::kAttendHeader +
                                          lbv::kAttendMaxCtas * sizeof(unsigned));
-    const cudaError_t e = lbv::launch_attend_rows(p, cache->kmap, cache->vmap, cache->dtype,
-                                                  cache->sms, (cudaStream_t)stream);
+    // Rows (new token times query head of a group) of an average request, whose
+    // lengths the host does not know.  Both kernels are right for every length.
+    const int64_t rows = ((int64_t)batch->tokens + batch->requests - 1) / batch->requests * p.group;
+    const auto launch = rows <= 16 ? lbv::launch_attend_rows : lbv::launch_attend_tiles;
+    const cudaError_t e = launch(p, cache->kmap, cache->vmap, cache->dtype, cache->sms,
+                                 (cudaStream_t)stream);
     if (e != cudaSuccess)
         return cuda_fail(e, "lbv_attend: launch");
     return LBV_OK;

@@ -572,7 +572,7 @@ LBV_API size_t lbv_attend_workspace_bytes(const lbv_kv_cache* cache, const lbv_b
  * heads.  Sums and softmax are fp32, the probabilities enter the second
  * product in the cache's dtype, out is rounded once.  Cache slots at or past
  * kv_len may hold anything; keys and values below it are taken to be finite.
- * A mapped page outside the cache reads as zeros.
+ * Contexts are shorter than 2^30.  A mapped page outside the cache reads as zeros.
  *   workspace: dev, 256-byte aligned, lbv_attend_workspace_bytes(); zeroed once
  * by the caller, left ready for the next call by every call; calls that may
  * run at the same time need distinct ones.  The result does not depend on
