@@ -42,6 +42,7 @@ ROPE_BY_PARTS = 2
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_WORKSPACE, ERR_TIMEOUT, ERR_BOUNDS = range(7)
 
+_byref = ctypes.byref
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # LBV_LIBRARY=checked selects liblbv_checked.so, the build whose kernels check
 # their copy and buffer ranges; the default is the release liblbv.so
@@ -185,7 +186,8 @@ def _ptr(t):
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: building the Stream object costs more than a launch
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -458,13 +460,16 @@ def dequant_fp16(plan: Plan, Wp, W, stream=None):
 
 # --- the verify step around the matmul ------------------------------------------------
 
-def _dtype_id(t) -> int:
-    import torch
-    try:
-        return {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}[t.dtype]
-    except KeyError:
-        raise LbvError(ERR_INVALID_ARG, f"tensor of {t.dtype}: float16, bfloat16 or float32 "
-                                        "is wanted") from None
+_dtype_ids = {}        # torch dtype -> lbv_dtype
+
+
+def _dtype_id(dtype) -> int:
+    if not _dtype_ids:
+        import torch
+        _dtype_ids.update({torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
+    if dtype not in _dtype_ids:
+        raise LbvError(ERR_INVALID_ARG, f"tensor of {dtype}: float16, bfloat16 or float32 is wanted")
+    return _dtype_ids[dtype]
 
 
 def _words(t, dtype, n: int, what: str):
@@ -490,7 +495,7 @@ class KVCache:
                                             "dimension")
         h = ctypes.c_void_p()
         _check(lib().lbv_kv_cache_create(k.data_ptr(), v.data_ptr(), *k.shape, *k.stride()[:3],
-                                         _dtype_id(k), ctypes.byref(h)))
+                                         _dtype_id(k.dtype), ctypes.byref(h)))
         self.handle = h
         self.k, self.v, self.dtype = k, v, k.dtype
         self.pages, self.page_size, self.heads, self.head_dim = k.shape
@@ -536,7 +541,7 @@ def _rows_arg(t, tokens: int, head_dim: int, what: str):
             or not t.is_cuda:
         raise LbvError(ERR_INVALID_ARG, f"{what}: {tuple(shape)} with strides {stride} on "
                                         f"{t.device}; [{tokens}, heads, {head_dim}] is wanted")
-    return _RowsArg(t.data_ptr(), shape[1], _dtype_id(t), stride[0], stride[1])
+    return _RowsArg(t.data_ptr(), shape[1], _dtype_id(t.dtype), stride[0], stride[1])
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = ROPE_NONE,
@@ -579,14 +584,16 @@ def rope_append(rope: Rope, batch: Batch, cache: KVCache, q, k, v, q_out, positi
     be None.  positions: int32 [tokens] rotary positions (default: the cache
     positions)."""
     n, d = batch.tokens, cache.head_dim
-    k_arg, v_arg = _rows_arg(k, n, d, "k"), _rows_arg(v, n, d, "v")
-    q_arg = None if q is None else ctypes.byref(_rows_arg(q, n, d, "q"))
-    o_arg = None if q_out is None else ctypes.byref(_rows_arg(q_out, n, d, "q_out"))
+    q_arg = None if q is None else _byref(_rows_arg(q, n, d, "q"))
+    o_arg = None if q_out is None else _byref(_rows_arg(q_out, n, d, "q_out"))
     if positions is not None:
         import torch
         positions = _words(positions, torch.int32, n, "positions")
-    _check(lib().lbv_rope_append(rope.handle, batch.ref, cache.handle, q_arg, ctypes.byref(k_arg),
-                                 ctypes.byref(v_arg), o_arg, positions, _stream(stream)))
+    status = lib().lbv_rope_append(rope.handle, batch.ref, cache.handle, q_arg,
+                                   _byref(_rows_arg(k, n, d, "k")), _byref(_rows_arg(v, n, d, "v")),
+                                   o_arg, positions, _stream(stream))
+    if status:
+        _check(status)
 
 
 def attend_workspace_bytes(cache: KVCache, batch: Batch, heads: int) -> int:
@@ -604,14 +611,16 @@ def attend(cache: KVCache, batch: Batch, q, out, scale: float, window: int = 0, 
     [tokens, heads]; workspace: attend_workspace_bytes, zeroed once.  See
     lbv_attend."""
     n, d = batch.tokens, cache.head_dim
-    q_arg, o_arg = _rows_arg(q, n, d, "q"), _rows_arg(out, n, d, "out")
+    q_arg, o_arg = _byref(_rows_arg(q, n, d, "q")), _byref(_rows_arg(out, n, d, "out"))
     if tree is not None or lse is not None:
         import torch
         tree = _words(tree, torch.int64, n, "tree")
         lse = _words(lse, torch.float32, n * q.shape[1], "lse")
     ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().lbv_attend(cache.handle, batch.ref, ctypes.byref(q_arg), ctypes.byref(o_arg),
-                            scale, window, tree, lse, _ptr(workspace), ws, _stream(stream)))
+    status = lib().lbv_attend(cache.handle, batch.ref, q_arg, o_arg, scale, window, tree, lse,
+                              _ptr(workspace), ws, _stream(stream))
+    if status:
+        _check(status)
 
 
 def attend_status(workspace):
@@ -640,10 +649,11 @@ def sample(logits, u, token, prob=None, temperature=None, top_k=None, top_p=None
                       _words(top_p, f32, m, "top_p"), _words(min_p, f32, m, "min_p"),
                       None if mask is None else mask.data_ptr(),
                       0 if mask is None else mask.stride(0), int(temperature_last))
-    _check(lib().lbv_sample(logits.data_ptr(), m, n, logits.stride(0), _dtype_id(logits),
-                            ctypes.byref(rules), _words(u, f32, m, "u"),
-                            _words(token, i32, m, "token"), _words(prob, f32, m, "prob"),
-                            _stream(stream)))
+    status = lib().lbv_sample(logits.data_ptr(), m, n, logits.stride(0), _dtype_id(logits.dtype),
+                              _byref(rules), _words(u, f32, m, "u"), _words(token, i32, m, "token"),
+                              _words(prob, f32, m, "prob"), _stream(stream))
+    if status:
+        _check(status)
 
 
 def version() -> str:

@@ -15,18 +15,24 @@
 // A row takes one thread-block cluster whose CTAs stage disjoint slices of it
 // in shared memory, so the logits are read from memory once (the bound of a
 // large batch); everything after the first pass works on chip.  Selecting
-// needs no sort:
-//   1. the row's maximum (one cluster barrier);
-//   2. a histogram of (m - l) r in steps of 1/16, cluster-wide, which bounds
-//      from the ranks, the weights and min-p how far down the kept tokens can
-//      reach; the few tokens above that bound ("candidates") are copied in
-//      index order to the first CTA, and the other CTAs are done;
-//   3. tau by a search over the bits of the (order-preserving) keys, counting
-//      and summing candidates above trial values, two bits a round;
-//   4. the index-order running sum.
-// Rows whose candidates do not fit the list (flat rows with a large top-p)
-// run steps 3 and 4 over the slices of all CTAs, with a cluster barrier in
-// each round.
+// needs no sort of the row:
+//   1. the row's maximum (a cluster barrier);
+//   2. a bound on how far down the kept tokens can reach.  Each thread's own
+//      maximum enters a histogram of (m - l) r in steps of 1/16 (a barrier): the
+//      k-th of these few thousand values is at most the row's k-th, and their
+//      weights sum to no more than the row's above the same logit, so the first
+//      bin that satisfies top-k or top-p on them lies at or below the true cut;
+//   3. the tokens above that bound, a few more than are kept, go in index order
+//      to the first CTA (a barrier), and the other CTAs are done;
+//   4. each of these candidates counts and sums those ranked before it, which
+//      decides whether it is kept, and an index-order running sum gives the
+//      token.  Up to kRanked candidates; a longer list finds tau by a search
+//      over the bits of the (order-preserving) keys, counting and summing above
+//      trial values, two bits a round.
+// Where the thread maxima do not reach the cut (a large k, a flat row with a
+// large top-p), step 2 is tried again with all logits, and where the candidates
+// do not fit the list, the search runs over the slices of all CTAs, with a
+// cluster barrier in each round.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -42,7 +48,8 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = kThreads;            // one thread per bin
-constexpr int kList = 4096;                // candidates kept in the first CTA
+constexpr int kList = 4096;                // candidates the first CTA can take
+constexpr int kRanked = 384;               // candidates ranked by pairs
 constexpr int kMaxCluster = 16;
 constexpr float kBinsPerNat = 16.f;
 constexpr float kNegInf = -__builtin_huge_valf();
@@ -53,10 +60,12 @@ struct Shared {
     unsigned hist[kBins];
     uint64_t tops[kMaxCluster];
     uint64_t sums[kWarps];                 // drawn weight of each warp's part
+    int counts[kMaxCluster];               // candidates of each CTA
     unsigned scan[kWarps];
     int pick;                              // place of the drawn token
     float pick_prob;
-    float list_x[kList];
+    uint4 pairs[kRanked];                  // key and weight of the ranked candidates
+    float list_x[kList];                   // a segment for each CTA
     int list_i[kList];
 };
 
@@ -333,6 +342,135 @@ __device__ int draw(Ctx& c, const Domain& d, const Row& row, const Kept& kept, f
     return sh.pick;
 }
 
+// Writes the slice's tokens of logit >= cut in index order to to_x, to_i (`cap`
+// of them at most) and returns how many there are.
+__device__ int collect(Ctx& c, const float* x, int n, float cut, int begin, int cap, float* to_x,
+                       int* to_i)
+{
+    Shared& sh = *c.sh;
+    // 128 logits a step: four neighbours a lane
+    const int steps = (n + 127) / 128, per = (steps + kWarps - 1) / kWarps;
+    const int g0 = min(c.warp * per, steps), g1 = min(g0 + per, steps);
+    const unsigned before = (1u << c.lane) - 1;
+    auto hits = [&](int g, float (&v)[4], unsigned (&b)[4]) {
+        const int i = g * 128 + c.lane * 4;
+        if (i + 3 < n) {
+            const float4 q = *reinterpret_cast<const float4*>(x + i);
+            v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[e] = i + e < n ? x[i + e] : kNegInf;
+        }
+        const bool any = (v[0] >= cut && i < n) || (v[1] >= cut && i + 1 < n) ||
+                         (v[2] >= cut && i + 2 < n) || (v[3] >= cut && i + 3 < n);
+        if (!__any_sync(0xffffffffu, any))
+            return 0;
+        int k = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            b[e] = __ballot_sync(0xffffffffu, v[e] >= cut && i + e < n);
+            k += __popc(b[e]);
+        }
+        return k;
+    };
+    float v[4];
+    unsigned b[4];
+    unsigned found = 0;
+    for (int g = g0; g < g1; ++g)
+        found += hits(g, v, b);
+    if (c.lane == 0)
+        sh.scan[c.warp] = found;
+    __syncthreads();
+    int at = 0, all = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        at += w < c.warp ? sh.scan[w] : 0;
+        all += sh.scan[w];
+    }
+    if (all <= cap && found)
+        for (int g = g0; g < g1; ++g) {
+            const int k = hits(g, v, b);
+            if (!k)
+                continue;
+            int to = at + __popc(b[0] & before) + __popc(b[1] & before) + __popc(b[2] & before) +
+                     __popc(b[3] & before);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if ((b[e] >> c.lane) & 1u) {
+                    to_x[to] = v[e];
+                    to_i[to] = begin + g * 128 + c.lane * 4 + e;
+                    ++to;
+                }
+            at += k;
+        }
+    return all;
+}
+
+// Draws from n <= kRanked candidates in index order, one a thread (list place
+// `at`, -1: none): what is ranked before a candidate decides whether it is kept.
+__device__ void rank_and_draw(Ctx& c, const Row& row, bool by_sum, uint64_t total, int n, int at,
+                              const SampleParams& p, int m)
+{
+    Shared& sh = *c.sh;
+    const bool in = c.tid < n;
+    const float x = in ? sh.list_x[at] : kNegInf;
+    const int index = in ? sh.list_i[at] : 0;
+    const uint32_t key = key_of(x);
+    const float wf = weight_f(x, row.top, row.filter_r);
+    const uint64_t w = in ? whole(wf) : 0;
+    if (in)
+        sh.pairs[c.tid] = make_uint4(key, (uint32_t)w, (uint32_t)(w >> 32), 0u);
+    __syncthreads();
+    unsigned rank = 0;
+    uint64_t ahead = 0;
+    if (c.warp * 32 < n) {
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) {
+            const uint4 o = sh.pairs[j];
+            if (o.x > key || (o.x == key && j < c.tid)) {
+                ++rank;
+                ahead += ((uint64_t)o.z << 32) | o.y;
+            }
+        }
+    }
+    const bool by_rank = row.k > 0;
+    bool keep = in && (!by_rank || rank < (unsigned)row.k);
+    if (by_sum) {
+        if (by_rank) {
+            uint64_t v[1] = {keep ? w : 0};
+            reduce<1>(c, false, v);
+            total = v[0];
+        }
+        keep = keep && (rank == 0 || ahead < part(fraction24(row.top_p), total));
+    }
+    keep = keep && wf >= row.min_p;
+    const uint64_t dw = keep ? whole(weight_f(x, row.top, row.draw_r)) : 0;
+    uint64_t upto = dw;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+        const uint64_t o = __shfl_up_sync(0xffffffffu, upto, s);
+        upto += c.lane >= s ? o : 0;
+    }
+    if (c.lane == 31)
+        sh.sums[c.warp] = upto;
+    __syncthreads();
+    uint64_t all = 0, below = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        below = i == c.warp ? all : below;
+        all += sh.sums[i];
+    }
+    upto += below;
+    uint32_t f = fraction24(row.u);
+    f = f > 16777215u ? 16777215u : f;
+    const uint64_t target = part(f, all);
+    if (upto > target && upto - dw <= target) {
+        p.token[m] = index;
+        if (p.prob)
+            p.prob[m] = __fdiv_rn(__ull2float_rn(dw), __ull2float_rn(all));
+    }
+}
+
 template <int DT>
 __device__ __forceinline__ float load1(const void* p, int64_t i)
 {
@@ -344,20 +482,40 @@ __device__ __forceinline__ float load1(const void* p, int64_t i)
         return __bfloat162float(__ushort_as_bfloat16(static_cast<const uint16_t*>(p)[i]));
 }
 
-// Copies n logits from element `at` on into shared memory as fp32: 16-byte
-// loads between the first and the last aligned address.
+// The thread's largest logit so far and its index in the slice (the first of
+// equal ones, as the thread's indices ascend).
+struct Best {
+    float x = kNegInf;
+    int i = -1;
+};
+
+// Copies n logits from element `at` on into shared memory as fp32, masked ones
+// and NaN as -inf, and finds the thread's maximum: 16-byte loads between the
+// first and the last aligned address.
 template <int DT>
-__device__ void stage(const void* src, int64_t at, int n, float* x, int tid)
+__device__ __forceinline__ Best stage(const void* src, int64_t at, int n, const uint32_t* words,
+                                      float* x, int tid)
 {
     constexpr int E = DT == LBV_F32 ? 4 : 8;           // elements of 16 bytes
     constexpr int SIZE = 16 / E;
+    Best best;
+    auto put = [&](int i, float v) {
+        v = __fadd_rn(v, 0.f);                         // -0 becomes +0
+        const bool out = v != v || (words && !((words[i >> 5] >> (i & 31)) & 1u));
+        v = out ? kNegInf : v;
+        x[i] = v;
+        if (v > best.x) {
+            best.x = v;
+            best.i = i;
+        }
+    };
     const uintptr_t a = reinterpret_cast<uintptr_t>(src) + (uintptr_t)at * SIZE;
     const int head = min(n, (int)(((16 - (a & 15)) & 15) / SIZE));
     const int body = (n - head) / E;
     if (tid < head)
-        x[tid] = load1<DT>(src, at + tid);
+        put(tid, load1<DT>(src, at + tid));
     const uint4* v = reinterpret_cast<const uint4*>(a + head * SIZE);
-    constexpr int U = 4;
+    constexpr int U = 8;
     for (int i = tid; i < body; i += U * kThreads) {
         uint4 w[U];
 #pragma unroll
@@ -367,28 +525,29 @@ __device__ void stage(const void* src, int64_t at, int n, float* x, int tid)
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (i + u * kThreads < body) {
-                float* d = x + head + (i + u * kThreads) * E;
+                const int d = head + (i + u * kThreads) * E;
                 const uint32_t q[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     if constexpr (DT == LBV_F32) {
-                        d[e] = __uint_as_float(q[e]);
+                        put(d + e, __uint_as_float(q[e]));
                     } else if constexpr (DT == LBV_F16) {
-                        d[2 * e] = __half2float(__ushort_as_half((uint16_t)q[e]));
-                        d[2 * e + 1] = __half2float(__ushort_as_half((uint16_t)(q[e] >> 16)));
+                        put(d + 2 * e, __half2float(__ushort_as_half((uint16_t)q[e])));
+                        put(d + 2 * e + 1, __half2float(__ushort_as_half((uint16_t)(q[e] >> 16))));
                     } else {
-                        d[2 * e] = __uint_as_float(q[e] << 16);
-                        d[2 * e + 1] = __uint_as_float(q[e] & 0xFFFF0000u);
+                        put(d + 2 * e, __uint_as_float(q[e] << 16));
+                        put(d + 2 * e + 1, __uint_as_float(q[e] & 0xFFFF0000u));
                     }
                 }
             }
     }
     for (int i = head + body * E + tid; i < n; i += kThreads)
-        x[i] = load1<DT>(src, at + i);
+        put(i, load1<DT>(src, at + i));
+    return best;
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kThreads) lbv_sample_kernel(const __grid_constant__ SampleParams p)
+__global__ void __launch_bounds__(kThreads, 2) lbv_sample_kernel(const __grid_constant__ SampleParams p)
 {
     extern __shared__ __align__(16) unsigned char smem[];
     Shared& sh = *reinterpret_cast<Shared*>(smem);
@@ -419,19 +578,12 @@ __global__ void __launch_bounds__(kThreads) lbv_sample_kernel(const __grid_const
     cl.barrier_arrive();                               // waited for before the first remote store
 
     // ---- the slice, masked, and the row's first maximum ----
-    stage<DT>(p.logits, (int64_t)m * p.ld + begin, n, x, c.tid);
     sh.hist[c.tid] = 0;
-    __syncthreads();
+    const Best mine = stage<DT>(p.logits, (int64_t)m * p.ld + begin, n,
+                                p.mask ? p.mask + (int64_t)m * p.mask_ld + begin / 32 : nullptr, x, c.tid);
     uint64_t best = 0;
-    const uint32_t* words = p.mask ? p.mask + (int64_t)m * p.mask_ld + begin / 32 : nullptr;
-    for (int i = c.tid; i < n; i += kThreads) {
-        float v = __fadd_rn(x[i], 0.f);                // -0 becomes +0
-        const bool out = v != v || (words && !((words[i >> 5] >> (i & 31)) & 1u));
-        v = out ? kNegInf : v;
-        x[i] = v;
-        const uint64_t key = ((uint64_t)key_of(v) << 32) | (0xFFFFFFFFu - (uint32_t)(begin + i));
-        best = key > best ? key : best;
-    }
+    if (n > 0)       // a row of -inf has a key above 0 too
+        best = ((uint64_t)key_of(mine.x) << 32) | (0xFFFFFFFFu - (uint32_t)(begin + mine.i));
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) {
         const uint64_t o = __shfl_xor_sync(0xffffffffu, best, s);
@@ -469,105 +621,125 @@ __global__ void __launch_bounds__(kThreads) lbv_sample_kernel(const __grid_const
     const bool by_rank = row.k > 0 && row.k < p.N, by_sum = row.top_p < 1.f;
     row.k = by_rank ? row.k : 0;
     if (by_rank || by_sum) {
-        // ---- histogram of (top - x) r; bin 0 holds the maximum ----
         const float scale = row.filter_r * kBinsPerNat;
-        auto bin_of = [&](float v) {
+        auto bin_of = [&](float v) {                   // bin 0 holds the maximum
             const float b = v == row.top ? 0.f : (row.top - v) * scale;
             return b < (float)(kBins - 1) ? (int)b : kBins - 1;
         };
-        uint64_t mass = 0;
-        for (int i = c.tid; i < n; i += kThreads) {
-            const int b = bin_of(x[i]);
-            if (b < kBins - 1)
-                atomicAdd(&sh.hist[b], 1u);
-            if (!by_rank)
-                mass += whole(weight_f(x[i], row.top, row.filter_r));
-        }
-        uint64_t v[1] = {mass};
-        reduce<1>(c, true, v);                         // orders the histograms too
-        const uint64_t total = v[0];
-        unsigned all = 0, below = 0;
-        for (int r = 0; r < c.nctas; ++r) {
-            const unsigned h = cl.map_shared_rank(&sh, r)->hist[c.tid];
-            all += h;
-            below += r < c.rank ? h : 0;
-        }
-        // The last bin a kept token can be in: the k-th token's; the one where
-        // the weights, each taken at its bin's lower edge less a little for
-        // rounding, pass top-p's share; min-p's.
-        unsigned count = all;
-        float low = (float)all * __expf(-(float)(c.tid + 1) / kBinsPerNat) * 0.999f;
-#pragma unroll
-        for (int s = 1; s < 32; s <<= 1) {
-            const unsigned o = __shfl_up_sync(0xffffffffu, count, s);
-            const float f = __shfl_up_sync(0xffffffffu, low, s);
-            count += c.lane >= s ? o : 0;
-            low += c.lane >= s ? f : 0.f;
-        }
-        if (c.lane == 31) {
-            sh.scan[c.warp] = count;
-            sh.red[0][c.warp][3] = __float_as_uint(low);
-        }
-        __syncthreads();
-        for (int w = 0; w < c.warp; ++w) {
-            count += sh.scan[w];
-            low += __uint_as_float((uint32_t)sh.red[0][w][3]);
-        }
-        bool reach = by_rank ? count >= (unsigned)row.k
-                             : low >= row.top_p * __ull2float_rn(total) * 9.094947e-13f;   // 2^-40
-        // (top-p takes its share of all that top-k kept, min-p or not)
-        const float z_min = row.min_p > 0.f && !(by_rank && by_sum) ? -logf(row.min_p) : 1e30f;
-        reach = reach || (float)c.tid > z_min * kBinsPerNat + 2.f;
-        const int short_of = __syncthreads_count(!reach);      // bins before the first that reaches
-        const int last = short_of;                             // kBins: none does
-        // candidates in total and in the CTAs before this one
-        uint64_t cut[2] = {c.tid <= last ? all : 0u, c.tid <= last ? below : 0u};
-        reduce<2>(c, false, cut);
-        if (last < kBins - 1 && cut[0] <= kList) {
-            Shared* to = cl.map_shared_rank(&sh, 0);
-            const int groups = (n + 31) / 32, per = (groups + kWarps - 1) / kWarps;
-            const int g0 = min(c.warp * per, groups), g1 = min(g0 + per, groups);
-            unsigned found = 0;
-            for (int g = g0; g < g1; ++g) {
-                const int i = g * 32 + c.lane;
-                found += __popc(__ballot_sync(0xffffffffu, i < n && bin_of(x[i]) <= last));
-            }
-            if (c.lane == 0)
-                sh.scan[c.warp] = found;
-            __syncthreads();
-            unsigned at = (unsigned)cut[1];
-            for (int w = 0; w < c.warp; ++w)
-                at += sh.scan[w];
-            if (found)
-                for (int g = g0; g < g1; ++g) {
-                    const int i = g * 32 + c.lane;
-                    const bool in = i < n && bin_of(x[i]) <= last;
-                    const unsigned set = __ballot_sync(0xffffffffu, in);
-                    if (in) {
-                        const unsigned to_i = at + __popc(set & ((1u << c.lane) - 1));
-                        if (to_i < (unsigned)kList) {
-                            to->list_x[to_i] = x[i];
-                            to->list_i[to_i] = begin + i;
-                        }
-                    }
-                    at += __popc(set);
+        uint64_t v[1] = {0}, total = 0;
+        bool listed = false;
+        for (int all = 0; all < 2 && !listed; ++all) {
+            // ---- the histogram, and with it (once) the row's weight ----
+            if (all == 0) {
+                const int b = bin_of(mine.x);
+                if (b < kBins - 1)
+                    atomicAdd(&sh.hist[b], 1u);
+                if (!by_rank)
+                    for (int i = c.tid; i < n; i += kThreads)
+                        v[0] += whole(weight_f(x[i], row.top, row.filter_r));
+                reduce<1>(c, true, v);                 // orders the histograms too
+                total = v[0];
+            } else {
+                cl.sync();                             // the first one has been read
+                sh.hist[c.tid] = 0;
+                __syncthreads();
+                for (int i = c.tid; i < n; i += kThreads) {
+                    const int b = bin_of(x[i]);
+                    if (b < kBins - 1)
+                        atomicAdd(&sh.hist[b], 1u);
                 }
+                cl.sync();
+            }
+            unsigned h[kMaxCluster];
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r)
+                h[r] = r < c.nctas ? cl.map_shared_rank(&sh, r)->hist[c.tid] : 0u;
+            unsigned here = 0;
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r)
+                here += h[r];
+            // The last bin a kept token can be in: the k-th token's; the one
+            // where the weights, each taken at its bin's lower edge less a little
+            // for rounding, pass top-p's share; min-p's.
+            unsigned count = here;
+            float low = (float)here * __expf(-(float)(c.tid + 1) / kBinsPerNat) * 0.999f;
+#pragma unroll
+            for (int s = 1; s < 32; s <<= 1) {
+                const unsigned o = __shfl_up_sync(0xffffffffu, count, s);
+                const float f = __shfl_up_sync(0xffffffffu, low, s);
+                count += c.lane >= s ? o : 0;
+                low += c.lane >= s ? f : 0.f;
+            }
+            if (c.lane == 31) {
+                sh.scan[c.warp] = count;
+                sh.red[0][c.warp][3] = __float_as_uint(low);
+            }
+            __syncthreads();
+            for (int w = 0; w < c.warp; ++w) {
+                count += sh.scan[w];
+                low += __uint_as_float((uint32_t)sh.red[0][w][3]);
+            }
+            bool reach = by_rank ? count >= (unsigned)row.k
+                                 : low >= row.top_p * __ull2float_rn(total) * 9.094947e-13f;   // 2^-40
+            // (top-p takes its share of all that top-k kept, min-p or not)
+            const float z_min = row.min_p > 0.f && !(by_rank && by_sum) ? -logf(row.min_p) : 1e30f;
+            reach = reach || (float)c.tid > z_min * kBinsPerNat + 2.f;
+            const int last = __syncthreads_count(!reach);      // bins before the first that reaches
+            if (last >= kBins - 1)
+                continue;
+            // ---- the candidates: all logits down to a little below the bin's lower edge ----
+            const float cut = isinf(row.top) ? row.top
+                                             : row.top - ((float)last + 1.05f) / scale - fabsf(row.top) * 1e-6f;
+            const int cap = kList / c.nctas;
+            Shared* to = cl.map_shared_rank(&sh, 0);
+            const int found = collect(c, x, n, cut, begin, cap, to->list_x + c.rank * cap,
+                                      to->list_i + c.rank * cap);
+            if (c.tid < c.nctas)
+                cl.map_shared_rank(&sh, c.tid)->counts[c.rank] = found;
             cl.sync();
+            listed = true;
+            for (int r = 0; r < c.nctas; ++r)
+                listed = listed && sh.counts[r] <= cap;
+        }
+        if (listed) {
             if (c.rank != 0)
                 return;
+            const int cap = kList / c.nctas;
+            int before = 0, mine_at = -1;   // thread t < kRanked takes candidate t
+            for (int r = 0; r < c.nctas; ++r) {
+                const int f = sh.counts[r];
+                if (c.tid >= before && c.tid < before + f)
+                    mine_at = r * cap + c.tid - before;
+                before += f;
+            }
+            if (before <= kRanked) {
+                rank_and_draw(c, row, by_sum, total, before, mine_at, p, m);
+                return;
+            }
             // the list moves to the start of the slice, which is done with
-            const int count_all = (int)cut[0];
-            for (int i = c.tid; i < count_all; i += kThreads)
-                x[i] = sh.list_x[i];
+            before = 0;
+            for (int r = 0; r < c.nctas; ++r) {
+                const int f = sh.counts[r];
+                for (int i = c.tid; i < f; i += kThreads)
+                    x[before + i] = sh.list_x[r * cap + i];
+                before += f;
+            }
             __syncthreads();
-            d = Domain{x, count_all, false};
+            d = Domain{x, before, false};
         }
         kept = select(c, d, row, true, total);
     }
     float prob = 0.f;
     const int place = draw(c, d, row, kept, &prob);
     if (place >= 0 && c.tid == 0) {
-        p.token[m] = d.wide ? begin + place : sh.list_i[place];
+        int at = begin + place;
+        if (!d.wide) {                                 // the list's segments, in CTA order
+            int r = 0, i = place;
+            while (i >= sh.counts[r])
+                i -= sh.counts[r++];
+            at = sh.list_i[r * (kList / c.nctas) + i];
+        }
+        p.token[m] = at;
         if (p.prob)
             p.prob[m] = prob;
     }

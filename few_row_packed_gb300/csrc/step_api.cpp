@@ -459,9 +459,8 @@ lbv_status lbv_sample(const void* logits, int M, int N, int64_t ld, lbv_dtype dt
     if (rules->mask && M > 1 && rules->mask_ld < (N + 31) / 32)
         return fail(LBV_ERR_INVALID_ARG, "%s: mask_ld=%lld < %d words", fn,
                     (long long)rules->mask_ld, (N + 31) / 32);
-    // rows as many as can be in flight at once take more CTAs each
     const int most = lbv::sample_max_slice();
-    int ctas = M <= 16 ? 8 : 4;
+    int ctas = 8;
     while (ctas < 16 && (int64_t)ctas * most < N)
         ctas *= 2;
     while (ctas > 1 && N <= ctas * 2048)
