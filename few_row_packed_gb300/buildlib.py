@@ -41,6 +41,7 @@ SOURCES = [
     "sample.cu",
     "attend_rows.cu",
     "attend_tiles.cu",
+    "attend_join.cu",
     "tc_aux.cu",
     "tc_sign1.cu",
     "tc_affine2_g32.cu",

@@ -211,34 +211,278 @@ __device__ __forceinline__ void finish4(const AttendParams& p, const Request& q,
         p.lse[tok * p.heads + head] = lse_of(top, sum);
 }
 
+// ---- work items ----
+//
+// An item is a tile of up to ROWS rows of a request (new token times query head
+// of the group) and a key/value head, over the blocks of KEYS keys that some row
+// of the tile sees, at least one (an empty row has an output too).  Its cost in
+// units: EXTRA for its queries and results, and 1 for each block, or 2 where
+// the tile has more than SINGLE rows.  The units of the batch form one sequence
+// -- request by request, tile by tile, head by head -- of which every CTA takes
+// an equal contiguous share; a block belongs to the share that holds its first
+// unit.  The host refuses batches of 2^32 units and more.
+template <int ROWS_, int KEYS_, int SINGLE, int EXTRA_>
+struct Shape {
+    static constexpr int ROWS = ROWS_, KEYS = KEYS_, EXTRA = EXTRA_;
+    static __device__ __forceinline__ int weight(int rows) { return rows > SINGLE ? 2 : 1; }
+};
+
+struct Tile {
+    int row0, rows;        // its rows
+    int lo, hi;            // keys they can see
+    int block0, blocks;
+    unsigned units;
+};
+
+template <typename S>
+__device__ __forceinline__ int tiles_of(const AttendParams& p, const Request& q)
+{
+    return (int)(((int64_t)q.n * p.group + S::ROWS - 1) / S::ROWS);
+}
+
+template <typename S>
+__device__ __forceinline__ Tile tile_of(const AttendParams& p, const Request& q, int t)
+{
+    Tile x;
+    x.row0 = t * S::ROWS;
+    x.rows = min(S::ROWS, q.n * p.group - x.row0);
+    key_range(p, q, x.row0 / p.group, (x.row0 + x.rows - 1) / p.group, x.lo, x.hi);
+    x.block0 = x.lo / S::KEYS;
+    x.blocks = max(1, (x.hi + S::KEYS - 1) / S::KEYS - x.block0);
+    x.units = S::EXTRA + (unsigned)(S::weight(x.rows) * x.blocks);
+    return x;
+}
+
+// Where a CTA's share begins: kept in shared memory for the CTA's roles.
+struct Start {
+    Request q;
+    unsigned total, item;  // units of the batch; the first unit of the share's first item
+    int ctas;              // CTAs that share them
+    int r, tile, head;
+};
+
+// Run by one warp of CTA c: at most max_ctas CTAs with min_units each.
+template <typename S>
+__device__ void find_start(const AttendParams& p, int lane, unsigned max_ctas, unsigned min_units,
+                           unsigned c, Start* out)
+{
+    auto units_of = [&](int r, Request& q) {
+        unsigned n = 0;
+        if (r < p.batch.requests) {
+            q = request_of(p, r);
+            const int tiles = tiles_of<S>(p, q);
+            for (int t = 0; t < tiles; ++t)
+                n += tile_of<S>(p, q, t).units;
+        }
+        return n * (unsigned)p.kv.heads;
+    };
+    Request q, q0;
+    const unsigned v0 = units_of(lane, q0);
+    unsigned total = __reduce_add_sync(0xffffffffu, v0);
+    for (int r0 = 32; r0 < p.batch.requests; r0 += 32)
+        total += __reduce_add_sync(0xffffffffu, units_of(r0 + lane, q));
+    const unsigned want = (total + min_units - 1) / min_units;
+    const unsigned n = want < max_ctas ? want : max_ctas;
+    if (lane == 0) {
+        out->total = total;
+        out->ctas = (int)n;
+    }
+    if (c >= n)
+        return;
+    const unsigned per = total / n, rem = total - per * n;
+    const unsigned first = c * per + min(c, rem);
+    unsigned base = 0;
+    for (int r0 = 0; r0 < p.batch.requests; r0 += 32) {
+        unsigned v = v0;
+        q = q0;
+        if (r0 > 0)
+            v = units_of(r0 + lane, q);
+        unsigned sum = v;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const unsigned o = __shfl_up_sync(0xffffffffu, sum, d);
+            sum += lane >= d ? o : 0;
+        }
+        unsigned at = base + sum - v;
+        const bool here = v && at <= first && first - at < v;
+        if (here) {
+            int t = 0;
+            unsigned units = tile_of<S>(p, q, 0).units;
+            while (first - at >= units * (unsigned)p.kv.heads) {
+                at += units * (unsigned)p.kv.heads;
+                units = tile_of<S>(p, q, ++t).units;
+            }
+            const unsigned head = (first - at) / units;
+            out->q = q;
+            out->r = r0 + lane;
+            out->tile = t;
+            out->head = (int)head;
+            out->item = at + head * units;
+        }
+        base += __shfl_sync(0xffffffffu, sum, 31);
+        if (__any_sync(0xffffffffu, here))
+            break;
+    }
+}
+
+// A role's walk over the items of its CTA's share.
+template <typename S>
+struct Walk {
+    const AttendParams& p;
+    Request q;
+    Tile x;
+    unsigned u, u_end, per, rem, item;
+    int r, t, tiles, head;
+    int b_first, b_last;   // blocks of the item in this share
+
+    __device__ Walk(const AttendParams& p_, const Start& s, unsigned c)
+        : p(p_), q(s.q), item(s.item), r(s.r), t(s.tile), head(s.head)
+    {
+        per = s.total / (unsigned)s.ctas;
+        rem = s.total - per * (unsigned)s.ctas;
+        u = c * per + min(c, rem);
+        u_end = u + per + (c < rem);
+        tiles = tiles_of<S>(p, q);
+        x = tile_of<S>(p, q, t);
+        b_first = b_last = -1;
+    }
+    // the CTA whose share holds unit v
+    __device__ int cta_of(unsigned v) const
+    {
+        const unsigned big = rem * (per + 1);
+        return (int)(v < big ? v / (per + 1) : rem + (v - big) / per);
+    }
+    // blocks of the item whose first unit lies before unit v of it
+    __device__ int blocks_before(unsigned v) const
+    {
+        const int w = S::weight(x.rows), k = (int)v - S::EXTRA;
+        return k <= 0 ? 0 : min((k + w - 1) / w, x.blocks);
+    }
+    // The next item with a block in the share.
+    __device__ bool next()
+    {
+        do {
+            if (u >= u_end)
+                return false;
+            if (u >= item + x.units) {
+                item += x.units;
+                if (++head == p.kv.heads) {
+                    head = 0;
+                    if (++t == tiles) {
+                        t = 0;
+                        do {
+                            q = request_of(p, ++r);      // units remain, so a request does
+                            tiles = tiles_of<S>(p, q);
+                        } while (tiles == 0 && r + 1 < p.batch.requests);
+                    }
+                    x = tile_of<S>(p, q, t);
+                }
+            }
+            b_first = blocks_before(u - item);
+            b_last = blocks_before(min(x.units, u_end - item));
+            u = item + min(x.units, u_end - item);
+        } while (b_first == b_last);
+        return true;
+    }
+    __device__ bool whole() const { return b_first == 0 && b_last == x.blocks; }
+    __device__ int first_cta() const { return cta_of(item + S::EXTRA); }
+    __device__ int last_cta() const
+    {
+        return cta_of(item + S::EXTRA + (unsigned)(S::weight(x.rows) * (x.blocks - 1)));
+    }
+    __device__ int key0(int b) const { return (x.block0 + b) * S::KEYS; }
+};
+
+// A partial result's item, for the kernel that joins them: written by the CTA
+// the item starts in (rows 0: no item starts there and goes on).
+struct alignas(32) JoinItem {
+    int q0, row0, rows, kv_head, parts;
+};
+
 // Partial results of an item: slot 2 c + 1 of the CTA c0 it starts in, slot 2 c
 // of the others; a slot holds o [ROWS][D], the reference maxima [ROWS] and the
-// sums [ROWS].  join_parts adds them in CTA order, by the threads tid < threads.
-template <int DT, int D, int ROWS>
+// sums [ROWS].  join_parts adds them in CTA order, by THREADS threads (tid) that
+// meet at named barrier 1.  The parts come from L2, about 0.7 us away, so each
+// of the three steps has all its loads in flight at once: the maxima and sums,
+// the factors of every part (in `scratch`, `cap` floats of shared memory), and
+// 16 loads a thread of the results.
+template <int DT, int D, int ROWS, int THREADS>
 __device__ __forceinline__ void join_parts(const AttendParams& p, const Request& q, int kv_head,
-                                           int row0, int rows, int c0, int c1, int tid, int threads)
+                                           int row0, int rows, int c0, int c1, int tid,
+                                           float* scratch, int cap)
 {
-    auto part = [&](int c) {
-        return p.partial + (size_t)(2 * c + (c == c0)) * (ROWS * (D + 2));
+    const int parts = c1 - c0 + 1;
+    auto part = [&](int k) {
+        return p.partial + (size_t)(2 * (c0 + k) + (k == 0)) * (ROWS * (D + 2));
     };
-    for (int i = tid; i < rows * (D / 4); i += threads) {
-        const int row = i / (D / 4), d4 = i % (D / 4);
-        float top = -INFINITY;
-#pragma unroll 4
-        for (int c = c0; c <= c1; ++c)
-            top = fmaxf(top, __ldcg(part(c) + ROWS * D + row));
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.f;
-#pragma unroll 4
-        for (int c = c0; c <= c1; ++c) {
-            const float* s = part(c);
-            const float m = __ldcg(s + ROWS * D + row);
-            const float f = m == -INFINITY ? 0.f : ex2(m - top);
-            const float4 a = __ldcg(reinterpret_cast<const float4*>(s + row * D + d4 * 4));
-            sum += f * __ldcg(s + ROWS * (D + 1) + row);
-            o.x += f * a.x, o.y += f * a.y, o.z += f * a.z, o.w += f * a.w;
+    const int step = min(rows, cap / (2 * parts + 2));   // rows at a time (parts: at most 512)
+    for (int r0 = 0; r0 < rows; r0 += step) {
+        const int n = min(step, rows - r0);
+        float* f = scratch;                              // [parts][n] maxima, then factors
+        float* s = f + parts * n;                        // [parts][n] sums
+        float* tops = s + parts * n;                     // [n], and the joined sums [n]
+        for (int i = tid; i < parts * n; i += THREADS) {
+            const int k = i / n, r = i - k * n;
+            f[i] = __ldcg(part(k) + ROWS * D + r0 + r);
+            s[i] = __ldcg(part(k) + ROWS * (D + 1) + r0 + r);
         }
-        finish4<DT>(p, q, kv_head, row0 + row, d4, o, top, sum);
+        named_bar_sync(1, THREADS);
+        // a row's factors: by one thread, or by a warp if the parts are many
+        const int lanes = parts > 8 ? 32 : 1, lane = tid & (lanes - 1);
+        for (int r = tid / lanes; r < n; r += THREADS / lanes) {
+            float top = -INFINITY, sum = 0.f;
+            for (int k = lane; k < parts; k += lanes)
+                top = fmaxf(top, f[k * n + r]);
+            for (int d = lanes >> 1; d > 0; d >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            for (int k = lane; k < parts; k += lanes) {
+                const float m = f[k * n + r], w = m == -INFINITY ? 0.f : ex2(m - top);
+                f[k * n + r] = w;
+                sum += w * s[k * n + r];
+            }
+            for (int d = lanes >> 1; d > 0; d >>= 1)
+                sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            if (lane == 0) {
+                tops[r] = top;
+                tops[n + r] = sum;
+            }
+        }
+        named_bar_sync(1, THREADS);
+        constexpr int U = 8;
+        const int tasks = n * (D / 4);
+        for (int i = tid; i < tasks; i += U * THREADS) {
+            float4 o[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < parts; k += 2) {
+                const float* src[2] = {part(k) + (size_t)r0 * D, part(min(k + 1, parts - 1)) + (size_t)r0 * D};
+                float4 a[2][U];
+#pragma unroll
+                for (int v = 0; v < 2; ++v)
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        if (i + u * THREADS < tasks)
+                            a[v][u] = __ldcg(reinterpret_cast<const float4*>(src[v]) + i + u * THREADS);
+#pragma unroll
+                for (int v = 0; v < 2; ++v)
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        if (i + u * THREADS < tasks && k + v < parts) {
+                            const float w = f[(k + v) * n + (i + u * THREADS) / (D / 4)];
+                            o[u].x += w * a[v][u].x, o[u].y += w * a[v][u].y;
+                            o[u].z += w * a[v][u].z, o[u].w += w * a[v][u].w;
+                        }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i + u * THREADS < tasks) {
+                    const int r = (i + u * THREADS) / (D / 4);
+                    finish4<DT>(p, q, kv_head, row0 + r0 + r, (i + u * THREADS) % (D / 4), o[u],
+                                tops[r], tops[n + r]);
+                }
+        }
+        named_bar_sync(1, THREADS);                      // scratch is free again
     }
 }
 

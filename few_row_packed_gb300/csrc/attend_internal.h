@@ -24,15 +24,24 @@ struct AttendParams {
     unsigned* status;                // error bits
     unsigned* counters;              // one per CTA, zero between calls
     float* partial;                  // slots of partial results
+    void* items;                     // one JoinItem per CTA where they are joined apart, else NULL
 };
 
 constexpr int kAttendMaxCtas = 512;              // CTAs of a launch, and counters
-constexpr size_t kAttendHeader = 256;            // status word, then the counters
+// Workspace: status word, counters, join items, partial results.
+constexpr size_t kAttendCounters = 256;
+constexpr size_t kAttendItems = kAttendCounters + kAttendMaxCtas * sizeof(unsigned);
+constexpr size_t kAttendPartial = kAttendItems + kAttendMaxCtas * 32;
 
+// p.items is where join items go if the launch joins apart.
 cudaError_t launch_attend_rows(const AttendParams& p, const CUtensorMap& kmap,
                                const CUtensorMap& vmap, lbv_dtype dt, int sms, cudaStream_t st);
 cudaError_t launch_attend_tiles(const AttendParams& p, const CUtensorMap& kmap,
                                 const CUtensorMap& vmap, lbv_dtype dt, int sms, cudaStream_t st);
+// Joins apart (attend_join.cu): when, and the launch for slots of slot_rows rows.
+bool attend_joins_apart(const AttendParams& p, int tile_rows, int ctas);
+cudaError_t launch_attend_join(const AttendParams& p, lbv_dtype dt, int slot_rows, int ctas,
+                               cudaStream_t st);
 // Floats of workspace the launches need for partial results.
 size_t attend_rows_partial_floats(int dim, int sms);
 size_t attend_tiles_partial_floats(int dim, int sms);

@@ -1,0 +1,114 @@
+// attend_join.cu -- adds the partial results of items that several CTAs share.
+// A CTA that joined its item by itself would read every part alone, at the
+// latency of L2: 24 us for 20 parts of 48 rows, as long as the call's keys and
+// values take, and 20 us for 2 parts of 256 rows.  This launch, which starts
+// while the attention kernel drains, spreads the rows over the SMs.
+//
+// One warp a row: its lanes take the parts' maxima and sums, then four elements
+// each of the results.  The parts are added in CTA order.
+#include "attend_common.cuh"
+
+namespace lbv {
+
+using namespace att;
+
+namespace {
+
+constexpr int kWarps = 4;
+
+template <int DT, int D>
+__global__ void __launch_bounds__(kWarps * 32)
+    lbv_attend_join_kernel(const __grid_constant__ AttendParams p, int slot_rows)
+{
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    const JoinItem it = static_cast<const JoinItem*>(p.items)[blockIdx.x];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int LANES = D / 4;                 // lanes that hold a row
+    constexpr int AT_ONCE = 32 / LANES;          // parts a load takes
+    const int sub = lane / LANES, d4 = lane % LANES;
+    Request q;
+    q.q0 = it.q0;
+    const size_t slot = (size_t)slot_rows * (D + 2);
+    auto part = [&](int k) {
+        return p.partial + (size_t)(2 * ((int)blockIdx.x + k) + (k == 0)) * slot;
+    };
+    for (int row = blockIdx.y * kWarps + warp; row < it.rows; row += gridDim.y * kWarps) {
+        float top = -INFINITY;
+        for (int k = lane; k < it.parts; k += 32)
+            top = fmaxf(top, part(k)[slot_rows * D + row]);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        float sum = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = 0; k0 < it.parts; k0 += 32) {
+            const int k = k0 + lane;
+            float w = 0.f;
+            if (k < it.parts) {
+                const float m = part(k)[slot_rows * D + row];
+                w = m == -INFINITY ? 0.f : ex2(m - top);
+                sum += w * part(k)[slot_rows * (D + 1) + row];
+            }
+            const int n = min(32, it.parts - k0);
+#pragma unroll 8
+            for (int j = 0; j < n; j += AT_ONCE) {
+                const float f = __shfl_sync(0xffffffffu, w, j + sub);
+                if (j + sub < n) {
+                    const float4 a = *reinterpret_cast<const float4*>(part(k0 + j + sub) + row * D + d4 * 4);
+                    o.x += f * a.x, o.y += f * a.y, o.z += f * a.z, o.w += f * a.w;
+                }
+            }
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+            sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if constexpr (AT_ONCE == 2) {
+            o.x += __shfl_xor_sync(0xffffffffu, o.x, 16), o.y += __shfl_xor_sync(0xffffffffu, o.y, 16);
+            o.z += __shfl_xor_sync(0xffffffffu, o.z, 16), o.w += __shfl_xor_sync(0xffffffffu, o.w, 16);
+        }
+        if (sub == 0)
+            finish4<DT>(p, q, it.kv_head, it.row0 + row, d4, o, top, sum);
+    }
+}
+
+template <int DT, int D>
+cudaError_t launch(const AttendParams& p, int slot_rows, int ctas, cudaStream_t st)
+{
+    cudaLaunchConfig_t cfg = {};
+    // CTAs per item: a warp for every row, or for every other one of the larger slots
+    cfg.gridDim = dim3((unsigned)ctas, (unsigned)(slot_rows <= 64 ? slot_rows / kWarps : slot_rows / (2 * kWarps)));
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, lbv_attend_join_kernel<DT, D>, p, slot_rows);
+}
+
+}  // namespace
+
+cudaError_t launch_attend_join(const AttendParams& p, lbv_dtype dt, int slot_rows, int ctas,
+                               cudaStream_t st)
+{
+    if (dt == LBV_F16)
+        return p.kv.dim == 128 ? launch<LBV_F16, 128>(p, slot_rows, ctas, st)
+                               : launch<LBV_F16, 64>(p, slot_rows, ctas, st);
+    return p.kv.dim == 128 ? launch<LBV_BF16, 128>(p, slot_rows, ctas, st)
+                           : launch<LBV_BF16, 64>(p, slot_rows, ctas, st);
+}
+
+// Whether the few-row kernel leaves its parts to this launch: where the items
+// (row tiles times kv heads, estimated from the batch's counts) have four CTAs
+// each or more.  Elsewhere the last CTA of an item joins its two or three parts
+// of 16 rows in less time than a launch takes.
+bool attend_joins_apart(const AttendParams& p, int tile_rows, int ctas)
+{
+    const int64_t rows = (int64_t)p.batch.tokens * p.group;
+    const int64_t tiles = (rows + tile_rows - 1) / tile_rows;
+    const int64_t items = (tiles > p.batch.requests ? tiles : p.batch.requests) * p.kv.heads;
+    return ctas >= 4 * items;
+}
+
+}  // namespace lbv

@@ -35,8 +35,9 @@ namespace {
 
 constexpr int kBlock = 64;                       // keys per block
 constexpr int kKeyWarps = 4;
-// A CTA gets at least this many blocks: below, joining costs more than it saves.
-constexpr int kMinBlocks = 2;
+// Units of an item beside its blocks, and the least share of a CTA (below, joining
+// costs more than it saves).
+constexpr int kExtra = 1, kMinUnits = 2;
 
 template <int D, int MT, int WM>
 struct Geo {
@@ -59,8 +60,8 @@ struct Geo {
     static constexpr int M_BUF = O_BUF + ROWS * OLD * 4;    // [kKeyWarps][ROWS] m, then sums
     static constexpr int BARS = M_BUF + 2 * kKeyWarps * ROWS * 4;
     static constexpr int FLAG = BARS + 2 * NST * 8;
-    static constexpr int STARTS = FLAG + 16;                // [requests + 1] first units
-    static constexpr int BASE = STARTS;
+    static constexpr int START = FLAG + 16;                 // where the CTA's share begins
+    static constexpr int BYTES = START + 64;
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4])
@@ -96,104 +97,6 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Units of a request: its row tiles times kv heads times blocks of keys.  Every
-// tile is given the blocks of the whole request (the tiles of few tokens
-// differ by a block at most); a tile skips those it does not see.
-struct Share {
-    int tiles, block0, blocks;
-};
-
-template <int ROWS>
-__device__ __forceinline__ Share share_of(const AttendParams& p, const Request& q)
-{
-    Share s;
-    s.tiles = (int)(((int64_t)q.n * p.group + ROWS - 1) / ROWS);
-    int lo, hi;
-    key_range(p, q, 0, q.n - 1, lo, hi);
-    s.block0 = lo / kBlock;
-    s.blocks = max(1, (hi + kBlock - 1) / kBlock - s.block0);   // an empty row has an output too
-    return s;
-}
-
-// A CTA's walk over its units, item by item.
-template <int ROWS>
-struct Walk {
-    const AttendParams& p;
-    const unsigned long long* starts;
-    unsigned long long u, u_end, total;
-    int ctas, r;
-    // the current segment
-    Request q;
-    Share s;
-    int tile, head, b_first, b_last;       // blocks [b_first, b_last) of the item
-    unsigned long long item;               // the item's first unit
-    int row0, rows, i0, i1;                // its rows, and their first and last token
-    int lo, hi;                            // keys they can see
-
-    __device__ Walk(const AttendParams& p_, const unsigned long long* st, unsigned long long tot,
-                    int n, int c)
-        : p(p_), starts(st), total(tot), ctas(n), r(-1)
-    {
-        u = first_of(c);
-        u_end = first_of(c + 1);
-        if (u < u_end) {
-            int a = 0, b = p.batch.requests;           // starts[a] <= u < starts[b]
-            while (b - a > 1) {
-                const int m = (a + b) / 2;
-                (starts[m] <= u ? a : b) = m;
-            }
-            r = a;
-            load();
-        }
-    }
-    __device__ unsigned long long first_of(int c) const
-    {
-        return (unsigned long long)c * total / (unsigned)ctas;
-    }
-    // the CTA whose share holds unit v
-    __device__ int cta_of(unsigned long long v) const
-    {
-        return (int)(((v + 1) * (unsigned)ctas - 1) / total);
-    }
-    __device__ void load()
-    {
-        q = request_of(p, r);
-        s = share_of<ROWS>(p, q);
-    }
-    __device__ bool next()
-    {
-        if (u >= u_end)
-            return false;
-        while (u >= starts[r + 1]) {
-            ++r;
-            if (starts[r] < starts[r + 1])
-                load();
-        }
-        const unsigned long long local = u - starts[r];
-        const unsigned long long it = local / (unsigned)s.blocks;
-        tile = (int)(it / (unsigned)p.kv.heads);
-        head = (int)(it - (unsigned long long)tile * (unsigned)p.kv.heads);
-        item = starts[r] + it * (unsigned)s.blocks;
-        b_first = (int)(u - item);
-        const unsigned long long end = item + (unsigned)s.blocks;
-        b_last = (int)((end < u_end ? end : u_end) - item);
-        u = item + (unsigned)b_last;
-        row0 = tile * ROWS;
-        rows = min(ROWS, q.n * p.group - row0);
-        i0 = row0 / p.group;
-        i1 = (row0 + rows - 1) / p.group;
-        key_range(p, q, i0, i1, lo, hi);
-        return true;
-    }
-    __device__ bool whole() const { return b_first == 0 && b_last == s.blocks; }
-    // first key of block b of the item; false if no row sees any of it
-    __device__ bool block(int b, int& k0) const
-    {
-        k0 = (s.block0 + b) * kBlock;
-        return k0 < hi && k0 + kBlock > lo;
-    }
-};
-
 template <int DT, int D, int MT, int WM>
 __global__ void __launch_bounds__(Geo<D, MT, WM>::THREADS, Geo<D, MT, WM>::CTAS)
     lbv_attend_rows_kernel(const __grid_constant__ AttendParams p,
@@ -202,10 +105,11 @@ __global__ void __launch_bounds__(Geo<D, MT, WM>::THREADS, Geo<D, MT, WM>::CTAS)
 {
     using G = Geo<D, MT, WM>;
     constexpr int ROWS = G::ROWS;
+    using S = Shape<ROWS, kBlock, ROWS, kExtra>;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    unsigned long long* starts = reinterpret_cast<unsigned long long*>(smem + G::STARTS);
+    Start* start = reinterpret_cast<Start*>(smem + G::START);
     auto full = [&](int st) { return sbase + G::BARS + st * 8; };
     auto empty = [&](int st) { return sbase + G::BARS + (G::NST + st) * 8; };
 
@@ -216,37 +120,14 @@ __global__ void __launch_bounds__(Geo<D, MT, WM>::THREADS, Geo<D, MT, WM>::CTAS)
         }
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
-    // first unit of every request
-    if (warp == 0) {
-        unsigned long long base = 0;
-        for (int r0 = 0; r0 < p.batch.requests; r0 += 32) {
-            const int r = r0 + lane;
-            unsigned long long v = 0;
-            if (r < p.batch.requests) {
-                const Request q = request_of(p, r);
-                const Share s = share_of<ROWS>(p, q);
-                v = (unsigned long long)s.tiles * (unsigned)p.kv.heads * (unsigned)s.blocks;
-            }
-            unsigned long long sum = v;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const unsigned long long o = __shfl_up_sync(0xffffffffu, sum, d);
-                sum += lane >= d ? o : 0;
-            }
-            if (r < p.batch.requests)
-                starts[r] = base + sum - v;
-            base += __shfl_sync(0xffffffffu, sum, 31);
-        }
-        if (lane == 0)
-            starts[p.batch.requests] = base;
-    }
+    if (p.items && tid == 128)
+        static_cast<JoinItem*>(p.items)[blockIdx.x].rows = 0;
+    if (warp == 0)
+        find_start<S>(p, lane, gridDim.x, kMinUnits, blockIdx.x, start);
     __syncthreads();
-    const unsigned long long total = starts[p.batch.requests];
-    const unsigned long long want = (total + kMinBlocks - 1) / kMinBlocks;
-    const int ctas = (int)(want < gridDim.x ? want : gridDim.x);
-    if ((int)blockIdx.x >= ctas)
+    if ((int)blockIdx.x >= start->ctas)
         return;
-    Walk<ROWS> w(p, starts, total, ctas, blockIdx.x);
+    Walk<S> w(p, *start, blockIdx.x);
     bool ok = true;
 
     if (warp < 4) {
@@ -261,10 +142,7 @@ __global__ void __launch_bounds__(Geo<D, MT, WM>::THREADS, Geo<D, MT, WM>::CTAS)
         while (w.next()) {
             const int* table = p.batch.block_table + (int64_t)w.r * p.batch.table_stride;
             for (int b = w.b_first; b < w.b_last; ++b) {
-                int k0;
-                if (!w.block(b, k0))
-                    continue;
-                const int st = n % G::NST;
+                const int st = n % G::NST, k0 = w.key0(b);
                 if (n >= G::NST && ok)
                     ok = mbar_wait(empty(st), (uint32_t)((n / G::NST - 1) & 1));
                 ++n;
@@ -280,7 +158,7 @@ __global__ void __launch_bounds__(Geo<D, MT, WM>::THREADS, Geo<D, MT, WM>::CTAS)
                     const int key = k0 + piece * slots;
                     const int at = key >> p.kv.page_shift;
                     int page = -1;                               // fills zeros
-                    if (key < w.hi && key + slots > w.lo)
+                    if (key < w.x.hi && key + slots > w.x.lo)
                         page = table[at];
                     const uint32_t dst = sbase + st * G::STAGE + part * G::HALF + piece * slots * 128;
                     tma_box(dst, part < D / 64 ? &kmap : &vmap, (part % (D / 64)) * 64,
@@ -318,7 +196,7 @@ __global__ void __launch_bounds__(Geo<D, MT, WM>::THREADS, Geo<D, MT, WM>::CTAS)
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int row = w.row0 + (wm * MT + mt) * 16 + h * 8 + (lane >> 2);
+                const int row = w.x.row0 + (wm * MT + mt) * 16 + h * 8 + (lane >> 2);
                 const bool in = row < w.q.n * p.group;
                 const int i = row / p.group, g = row - i * p.group;
                 pos[mt][h] = in ? w.q.first + i : INT_MIN / 2;
@@ -348,14 +226,11 @@ __global__ void __launch_bounds__(Geo<D, MT, WM>::THREADS, Geo<D, MT, WM>::CTAS)
                 o[mt][j][0] = o[mt][j][1] = o[mt][j][2] = o[mt][j][3] = 0.f;
         }
         // keys below `open_lo` or at `open_hi` and past are hidden from some row
-        const int open_hi = p.tree ? min(w.q.keys, w.q.first) : min(w.q.keys, w.q.first + w.i0 + 1);
-        const int open_lo = p.window > 0 ? w.q.first + w.i1 - p.window + 1 : 0;
+        const int open_hi = p.tree ? min(w.q.keys, w.q.first) : min(w.q.keys, w.q.first + w.x.row0 / p.group + 1);
+        const int open_lo = p.window > 0 ? w.q.first + (w.x.row0 + w.x.rows - 1) / p.group - p.window + 1 : 0;
 
         for (int b = w.b_first; b < w.b_last; ++b) {
-            int k0;
-            if (!w.block(b, k0))
-                continue;
-            const int st = n % G::NST;
+            const int st = n % G::NST, k0 = w.key0(b);
             if (ok)
                 ok = mbar_wait(full(st), (uint32_t)((n / G::NST) & 1));
             ++n;
@@ -515,10 +390,10 @@ __global__ void __launch_bounds__(Geo<D, MT, WM>::THREADS, Geo<D, MT, WM>::CTAS)
         }
         // row totals (in the first warp's slots)
         const bool whole = w.whole();
-        const int c0 = whole ? 0 : w.cta_of(w.item);
-        const int c1 = whole ? 0 : w.cta_of(w.item + (unsigned)w.s.blocks - 1);
+        const int c0 = whole ? 0 : w.first_cta();
+        const int c1 = whole ? 0 : w.last_cta();
         float* slot = p.partial + (size_t)(2 * blockIdx.x + (c0 == (int)blockIdx.x)) * G::SLOT;
-        for (int i = ctid; i < w.rows * (D / 4); i += G::WARPS * 32) {
+        for (int i = ctid; i < w.x.rows * (D / 4); i += G::WARPS * 32) {
             const int row = i / (D / 4), d4 = i % (D / 4);
             const float4 v = *reinterpret_cast<const float4*>(obuf + row * G::OLD + d4 * 4);
             float top = mbuf[row], sum = 0.f;
@@ -529,7 +404,7 @@ __global__ void __launch_bounds__(Geo<D, MT, WM>::THREADS, Geo<D, MT, WM>::CTAS)
             for (int k = 0; k < kKeyWarps; ++k)
                 sum += top == -INFINITY ? 0.f : lbuf[k * ROWS + row] * ex2(mbuf[k * ROWS + row] - top);
             if (whole) {
-                finish4<DT>(p, w.q, w.head, w.row0 + row, d4, v, top, sum);
+                finish4<DT>(p, w.q, w.head, w.x.row0 + row, d4, v, top, sum);
             } else {
                 *reinterpret_cast<float4*>(slot + row * D + d4 * 4) = v;
                 if (d4 == 0) {
@@ -538,7 +413,10 @@ __global__ void __launch_bounds__(Geo<D, MT, WM>::THREADS, Geo<D, MT, WM>::CTAS)
                 }
             }
         }
-        if (!whole) {
+        if (!whole && p.items) {
+            if (ctid == 0 && c0 == (int)blockIdx.x)
+                static_cast<JoinItem*>(p.items)[c0] = {w.q.q0, w.x.row0, w.x.rows, w.head, c1 - c0 + 1};
+        } else if (!whole) {
             __threadfence();
             named_bar_sync(1, G::WARPS * 32);
             if (ctid == 0)
@@ -546,7 +424,8 @@ __global__ void __launch_bounds__(Geo<D, MT, WM>::THREADS, Geo<D, MT, WM>::CTAS)
             named_bar_sync(1, G::WARPS * 32);
             if (*flag) {                                         // every part is there: join them
                 __threadfence();
-                join_parts<DT, D, ROWS>(p, w.q, w.head, w.row0, w.rows, c0, c1, ctid, G::WARPS * 32);
+                join_parts<DT, D, ROWS, G::WARPS * 32>(p, w.q, w.head, w.x.row0, w.x.rows, c0, c1, ctid,
+                                                       obuf, ROWS * G::OLD);
                 if (ctid == 0)
                     p.counters[c0] = 0;                          // as the next call finds it
             }
@@ -557,33 +436,23 @@ __global__ void __launch_bounds__(Geo<D, MT, WM>::THREADS, Geo<D, MT, WM>::CTAS)
         atomicOr(p.status, 1u);
 }
 
-template <int DT, int D, int MT, int WM>
+template <int DT, int D>
 cudaError_t launch(const AttendParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int sms,
                    cudaStream_t st)
 {
-    using G = Geo<D, MT, WM>;
-    const size_t smem = G::BASE + ((size_t)p.batch.requests + 1) * 8;
-    auto kernel = lbv_attend_rows_kernel<DT, D, MT, WM>;
-    const cudaError_t e = cudaFuncSetAttribute(
-        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    using G = Geo<D, 1, 1>;
+    auto kernel = lbv_attend_rows_kernel<DT, D, 1, 1>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, G::BYTES);
     if (e != cudaSuccess)
         return e;
-    const int ctas = sms * G::CTAS;
-    kernel<<<ctas < kAttendMaxCtas ? ctas : kAttendMaxCtas, G::THREADS, smem, st>>>(p, kmap, vmap);
-    return cudaGetLastError();
-}
-
-template <int DT, int D>
-cudaError_t launch_rows(const AttendParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                        int sms, cudaStream_t st)
-{
-    // rows of an average request, whose lengths the host does not know
-    const int64_t rows = ((int64_t)p.batch.tokens + p.batch.requests - 1) / p.batch.requests * p.group;
-    if (rows <= 16)
-        return launch<DT, D, 1, 1>(p, kmap, vmap, sms, st);
-    if (rows <= 32)
-        return launch<DT, D, 2, 1>(p, kmap, vmap, sms, st);
-    return launch<DT, D, 2, 2>(p, kmap, vmap, sms, st);
+    const int ctas = sms * G::CTAS < kAttendMaxCtas ? sms * G::CTAS : kAttendMaxCtas;
+    AttendParams a = p;
+    const bool apart = attend_joins_apart(p, G::ROWS, ctas);
+    if (!apart)
+        a.items = nullptr;
+    kernel<<<ctas, G::THREADS, G::BYTES, st>>>(a, kmap, vmap);
+    e = cudaGetLastError();
+    return e == cudaSuccess && apart ? launch_attend_join(a, (lbv_dtype)DT, G::ROWS, ctas, st) : e;
 }
 
 }  // namespace
@@ -592,10 +461,10 @@ cudaError_t launch_attend_rows(const AttendParams& p, const CUtensorMap& kmap,
                                const CUtensorMap& vmap, lbv_dtype dt, int sms, cudaStream_t st)
 {
     if (dt == LBV_F16)
-        return p.kv.dim == 128 ? launch_rows<LBV_F16, 128>(p, kmap, vmap, sms, st)
-                               : launch_rows<LBV_F16, 64>(p, kmap, vmap, sms, st);
-    return p.kv.dim == 128 ? launch_rows<LBV_BF16, 128>(p, kmap, vmap, sms, st)
-                           : launch_rows<LBV_BF16, 64>(p, kmap, vmap, sms, st);
+        return p.kv.dim == 128 ? launch<LBV_F16, 128>(p, kmap, vmap, sms, st)
+                               : launch<LBV_F16, 64>(p, kmap, vmap, sms, st);
+    return p.kv.dim == 128 ? launch<LBV_BF16, 128>(p, kmap, vmap, sms, st)
+                           : launch<LBV_BF16, 64>(p, kmap, vmap, sms, st);
 }
 
 size_t attend_rows_partial_floats(int dim, int sms)

@@ -15,8 +15,9 @@
 //   * A row's reference maximum moves only when it grew by more than 8 (see
 //     attend_rows.cu); only then are its sums in tensor memory rescaled, by the
 //     row's own thread.
-//   * The (item, block) pairs of the batch are divided evenly over one CTA per
-//     SM, as in attend_rows.cu; a causal tile counts the blocks that it sees.
+//   * The blocks of the batch are divided evenly over one CTA per SM, as in
+//     attend_rows.cu; a causal tile counts those that it sees.  The parts of a
+//     divided item are added by a launch of their own (attend_join.cu).
 #include "attend_common.cuh"
 
 namespace lbv {
@@ -28,10 +29,27 @@ namespace {
 constexpr int kKeys = 128;                       // keys per block
 constexpr int kTile = 128;                       // rows per stream
 constexpr int kRows = 2 * kTile;                 // rows per item
-constexpr int kMinBlocks = 2;                    // least share of a CTA
+// Units of an item beside its blocks (a block of two row tiles counts as two
+// units), and the least share of a CTA.
+constexpr int kExtra = 2, kMinUnits = 4;
+using Items = Shape<kRows, kKeys, kTile, kExtra>;
 constexpr int kThreads = 384;                    // copies and MMAs, then the two streams
-// Registers a thread after the split: 168 * 384 at launch = 56 * 128 + 224 * 256.
-constexpr int kRegsControl = 56, kRegsStream = 224;
+// Registers a thread after the split: 168 * 384 at launch = 88 * 128 + 208 * 256.
+constexpr int kRegsControl = 88, kRegsStream = 208;
+
+constexpr int kItems = 4;                        // items the roles may be apart
+
+// What the roles need to know of an item.
+struct alignas(16) Item {
+    Request q;
+    int r, row0, rows, head, lo, hi;
+    int key0, nb;          // its first key and its blocks in this share; 0 blocks: no more items
+    int slot0;             // ring slots used before it
+    int c0, c1;            // CTAs that hold a part of it
+    __device__ bool dual() const { return rows > kTile; }
+    __device__ bool whole() const { return c0 == c1; }
+};
+static_assert(sizeof(Item) == 64, "ring entry");
 
 template <int D>
 struct Geo {
@@ -41,15 +59,17 @@ struct Geo {
     static constexpr int RING = 2 * SLOT;
     static constexpr int NSLOT = D == 128 ? 5 : 10;
     static constexpr int BARS = RING + NSLOT * SLOT;
-    static constexpr int NBARS = 2 * NSLOT + 8;
+    static constexpr int NBARS = 2 * NSLOT + 8 + 2 * kItems;
     static constexpr int STATS = BARS + NBARS * 8;          // [2][128] m and sums of the streams
-    static constexpr int START = STATS + 2 * kTile * 8;     // where the CTA's share begins
-    static constexpr int WORDS = START + 48;                // tensor-memory address, join flag
+    static constexpr int ITEMS = STATS + 2 * kTile * 8;     // ring of items
+    static constexpr int WORDS = ITEMS + kItems * 64;       // tensor-memory address
     static constexpr int BYTES = WORDS + 16;
+    // where the CTA's share begins: read before the streams' first statistics
+    static constexpr int START = STATS;
     static constexpr int PARTIAL = kRows * (D + 2);         // floats of one partial result
     // tensor memory columns
     static constexpr uint32_t S0 = 0, O0 = 256;             // S of stream s at S0 + 128 s
-    static_assert(BYTES <= 227 * 1024, "shared memory");
+    static_assert(BYTES <= 227 * 1024 && sizeof(Start) <= 2 * kTile * 8, "shared memory");
 };
 
 // ---- tcgen05 ----
@@ -79,21 +99,31 @@ __device__ __forceinline__ void tmem_ld32(uint32_t at, float (&d)[32])
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t at, float (&d)[16])
+{
+    uint32_t* r = reinterpret_cast<uint32_t*>(d);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15}, [%16];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(at)
+        : "memory");
+}
+
 __device__ __forceinline__ void tmem_wait_ld()
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&r)[32])
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16])
 {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-        "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n"
-        ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
-        "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
-        "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
-        "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+        "%13,%14,%15,%16};\n" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]),
+        "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+        "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 
@@ -144,155 +174,56 @@ __host__ __device__ constexpr uint32_t idesc(int n, bool b_n_major)
            ((uint32_t)b_n_major << 16) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// ---- the CTA's share of the batch ----
-
-// The share's first item: request, tile, head, and the item's first unit.
-struct Start {
-    unsigned long long total, item;
-    int r, tile, head;
-};
-
-__device__ __forceinline__ int tiles_of(const AttendParams& p, const Request& q)
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 {
-    return (int)(((int64_t)q.n * p.group + kRows - 1) / kRows);
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+          "l"(reinterpret_cast<uint64_t&>(c)));
+    return d;
 }
 
-// Keys and blocks of a tile of a request.
-struct Tile {
-    int row0, rows, i0, i1, lo, hi, block0, blocks;
-};
-
-__device__ __forceinline__ Tile tile_of(const AttendParams& p, const Request& q, int t)
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
 {
-    Tile x;
-    x.row0 = t * kRows;
-    x.rows = min(kRows, q.n * p.group - x.row0);
-    x.i0 = x.row0 / p.group;
-    x.i1 = (x.row0 + x.rows - 1) / p.group;
-    key_range(p, q, x.i0, x.i1, x.lo, x.hi);
-    x.block0 = x.lo / kKeys;
-    x.blocks = max(1, (x.hi + kKeys - 1) / kKeys - x.block0);    // an empty row has an output too
-    return x;
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;\n"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return d;
 }
 
-__device__ __forceinline__ unsigned long long units_of(const AttendParams& p, const Request& q)
+// Stores row `row` of a request and kv head (zeros if it is not `in` the item) as
+// row `trow` of a Q tile at `tile`, in the layout of the copies.
+template <int D>
+__device__ __forceinline__ void store_q(const AttendParams& p, int q0, int kv_head, int row, bool in,
+                                        unsigned char* tile, int trow)
 {
-    unsigned long long n = 0;
-    const int tiles = tiles_of(p, q);
-    for (int t = 0; t < tiles; ++t)
-        n += (unsigned)tile_of(p, q, t).blocks;
-    return n * (unsigned)p.kv.heads;
-}
-
-// Run by one warp: the batch's units, and where CTA c of n begins.
-__device__ void find_start(const AttendParams& p, int lane, int max_ctas, int c, Start* out)
-{
-    unsigned long long total = 0, base = 0;
-    for (int pass = 0; pass < 2; ++pass) {
-        unsigned long long first = 0;
-        if (pass == 1) {
-            const unsigned long long want = (total + kMinBlocks - 1) / kMinBlocks;
-            const unsigned n = want < (unsigned)max_ctas ? (unsigned)want : (unsigned)max_ctas;
-            if ((unsigned)c >= n)
-                break;
-            first = (unsigned long long)c * total / n;
-        }
-        for (int r0 = 0; r0 < p.batch.requests; r0 += 32) {
-            const int r = r0 + lane;
-            unsigned long long v = 0;
-            Request q;
-            if (r < p.batch.requests) {
-                q = request_of(p, r);
-                v = units_of(p, q);
-            }
-            unsigned long long sum = v;
+    const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+    const int i = row / p.group;
+    const uint16_t* src = p.q + (int64_t)(q0 + i) * p.q_token +
+                          (int64_t)(kv_head * p.group + row - i * p.group) * p.q_head;
+    unsigned char* dst = tile + trow * 128;
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const unsigned long long o = __shfl_up_sync(0xffffffffu, sum, d);
-                sum += lane >= d ? o : 0;
+    for (int ch = 0; ch < D / 8; ++ch) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (in && p.scale_log2 != 0.f) {
+            if (p.q_wide) {
+                v = *reinterpret_cast<const uint4*>(src + ch * 8);
+            } else {
+                uint32_t e[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    e[k] = (uint32_t)src[ch * 8 + 2 * k] | ((uint32_t)src[ch * 8 + 2 * k + 1] << 16);
+                v = make_uint4(e[0], e[1], e[2], e[3]);
             }
-            if (pass == 0) {
-                total += __shfl_sync(0xffffffffu, sum, 31);
-                continue;
-            }
-            const unsigned long long at = base + sum - v;
-            if (v && at <= first && first < at + v) {
-                unsigned long long u = at;
-                int t = 0;
-                Tile x = tile_of(p, q, 0);
-                while (u + (unsigned long long)x.blocks * (unsigned)p.kv.heads <= first) {
-                    u += (unsigned long long)x.blocks * (unsigned)p.kv.heads;
-                    x = tile_of(p, q, ++t);
-                }
-                const int head = (int)((first - u) / (unsigned)x.blocks);
-                out->r = r;
-                out->tile = t;
-                out->head = head;
-                out->item = u + (unsigned long long)head * (unsigned)x.blocks;
-            }
-            base += __shfl_sync(0xffffffffu, sum, 31);
+            v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
         }
+        *reinterpret_cast<uint4*>(dst + (ch >> 3) * Geo<D>::HALF + (((ch & 7) ^ (trow & 7)) << 4)) = v;
     }
-    if (lane == 0)
-        out->total = total;
+    fence_proxy_async_smem();
 }
-
-// A role's walk over the CTA's items.
-struct Walk {
-    const AttendParams& p;
-    unsigned long long u, u_end, total, item;
-    int ctas, r, t, tiles, head;
-    bool fresh;
-    Request q;
-    Tile x;
-    int b_first, b_last;                   // blocks of the item in this share
-
-    __device__ Walk(const AttendParams& p_, const Start& s, int n, int c)
-        : p(p_), total(s.total), item(s.item), ctas(n), r(s.r), t(s.tile), head(s.head), fresh(true)
-    {
-        u = first_of(c);
-        u_end = first_of(c + 1);
-        q = request_of(p, r);
-        tiles = tiles_of(p, q);
-        x = tile_of(p, q, t);
-    }
-    __device__ unsigned long long first_of(int c) const
-    {
-        return (unsigned long long)c * total / (unsigned)ctas;
-    }
-    __device__ int cta_of(unsigned long long v) const
-    {
-        return (int)(((v + 1) * (unsigned)ctas - 1) / total);
-    }
-    __device__ bool next()
-    {
-        if (u >= u_end)
-            return false;
-        if (!fresh) {
-            item += (unsigned)x.blocks;
-            if (++head == p.kv.heads) {
-                head = 0;
-                if (++t == tiles) {
-                    t = 0;
-                    do {
-                        q = request_of(p, ++r);          // units remain, so a request does
-                        tiles = tiles_of(p, q);
-                    } while (tiles == 0 && r + 1 < p.batch.requests);
-                }
-                x = tile_of(p, q, t);
-            }
-        }
-        fresh = false;
-        b_first = (int)(u - item);
-        const unsigned long long end = item + (unsigned)x.blocks;
-        b_last = (int)((end < u_end ? end : u_end) - item);
-        u = item + (unsigned)b_last;
-        return true;
-    }
-    __device__ bool whole() const { return b_first == 0 && b_last == x.blocks; }
-    __device__ bool dual() const { return x.rows > kTile; }
-    __device__ int key0(int b) const { return (x.block0 + b) * kKeys; }
-};
 
 template <int DT, int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -306,7 +237,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     Start* start = reinterpret_cast<Start*>(smem + G::START);
     uint32_t& tmem_slot = *reinterpret_cast<uint32_t*>(smem + G::WORDS);
-    int& flag = *reinterpret_cast<int*>(smem + G::WORDS + 4);        // this CTA joins the parts
     auto bar = [&](int i) { return sbase + G::BARS + i * 8; };
     auto full = [&](int i) { return bar(i); };
     auto empty = [&](int i) { return bar(G::NSLOT + i); };
@@ -314,6 +244,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto s_full = [&](int s) { return bar(2 * G::NSLOT + 1 + s); };  // S of stream s is complete
     auto p_full = [&](int s) { return bar(2 * G::NSLOT + 3 + s); };  // P replaced it
     auto o_done = [&](int s) { return bar(2 * G::NSLOT + 5 + s); };  // O has the block
+    auto item_full = [&](int i) { return bar(2 * G::NSLOT + 7 + i % kItems); };
+    auto item_empty = [&](int i) { return bar(2 * G::NSLOT + 7 + kItems + i % kItems); };
+    const Item* items = reinterpret_cast<const Item*>(smem + G::ITEMS);
 
     if (tid == 0) {
         for (int i = 0; i < G::NSLOT; ++i) {
@@ -326,15 +259,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(p_full(s), 4);
             mbar_init(o_done(s), 1);
         }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(item_full(i), 1);
+            mbar_init(item_empty(i), 10);                // copies, MMAs, eight warps of the streams
+        }
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
+    if (tid == 128)
+        static_cast<JoinItem*>(p.items)[blockIdx.x].rows = 0;
     if (warp == 0)
-        find_start(p, lane, gridDim.x, blockIdx.x, start);
-    __syncthreads();
-    const unsigned long long want = (start->total + kMinBlocks - 1) / kMinBlocks;
-    const int ctas = (int)(want < gridDim.x ? want : gridDim.x);
-    if ((int)blockIdx.x >= ctas)
-        return;
+        find_start<Items>(p, lane, gridDim.x, kMinUnits, blockIdx.x, start);
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&tmem_slot))
                      : "memory");
@@ -344,22 +278,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
+    const Start share = *start;
+    const bool work = (int)blockIdx.x < share.ctas;
+    __syncthreads();                                     // its place becomes the statistics'
     bool ok = true;
 
-    if (warp < 4) {
+    auto wait = [&](uint32_t b, uint32_t parity) {
+        if (ok)
+            ok = mbar_wait(b, parity);
+    };
+    // item i of the share, as the scheduler wrote it
+    auto item_at = [&](int i) -> const Item& {
+        wait(item_full(i), (uint32_t)((i / kItems) & 1));
+        return items[i % kItems];
+    };
+
+    if (!work) {
+        // fewer units than CTAs
+    } else if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsControl));
         if (warp == 0) {
             // ---- copies: K and V of each block in turn ----
-            Walk w(p, *start, ctas, blockIdx.x);
             const int slots = min(64, 1 << p.kv.page_shift);         // rows of a box
             const int boxes = kKeys / slots;
             int n = 0;
-            while (w.next()) {
+            for (int it = 0;; ++it) {
+                const Item& w = item_at(it);
+                if (!__all_sync(0xffffffffu, ok) || w.nb == 0)
+                    break;
                 const int* table = p.batch.block_table + (int64_t)w.r * p.batch.table_stride;
-                for (int i = 2 * w.b_first; i < 2 * w.b_last; ++i) {
-                    const int st = n % G::NSLOT, k0 = w.key0(i >> 1);
-                    if (n >= G::NSLOT && ok)
-                        ok = mbar_wait(empty(st), (uint32_t)((n / G::NSLOT - 1) & 1));
+                for (int i = 0; i < 2 * w.nb; ++i) {
+                    const int st = n % G::NSLOT, k0 = w.key0 + (i >> 1) * kKeys;
+                    if (n >= G::NSLOT)
+                        wait(empty(st), (uint32_t)((n / G::NSLOT - 1) & 1));
                     ++n;
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok)
@@ -371,32 +322,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int piece = b % boxes, half = b / boxes;
                         const int key = k0 + piece * slots;
                         int page = -1;                               // fills zeros
-                        if (key < w.x.hi && key + slots > w.x.lo)
+                        if (key < w.hi && key + slots > w.lo)
                             page = table[key >> p.kv.page_shift];
                         tma_box(sbase + G::RING + st * G::SLOT + half * G::HALF + piece * slots * 128,
                                 (i & 1) ? &vmap : &kmap, half * 64,
                                 key & ((1 << p.kv.page_shift) - 1), w.head, page, full(st));
                     }
                 }
+                if (lane == 0)
+                    mbar_arrive(item_empty(it));
             }
             // the ring drains before shared memory goes away
             for (int i = 0; i < G::NSLOT; ++i)
-                if (n - 1 - i >= 0 && ok)
-                    ok = mbar_wait(empty((n - 1 - i) % G::NSLOT),
-                                   (uint32_t)(((n - 1 - i) / G::NSLOT) & 1));
+                if (n - 1 - i >= 0)
+                    wait(empty((n - 1 - i) % G::NSLOT), (uint32_t)(((n - 1 - i) / G::NSLOT) & 1));
         } else if (warp == 1 && lane == 0) {
             // ---- MMAs ----
-            Walk w(p, *start, ctas, blockIdx.x);
             constexpr uint32_t id_s = idesc<DT>(kKeys, false), id_o = idesc<DT>(D, true);
-            auto wait = [&](uint32_t b, uint32_t parity) {
-                if (ok)
-                    ok = mbar_wait(b, parity);
-            };
-            int n = 0, items = 0;                        // slots before this item, items so far
             int np[2] = {0, 0};                          // blocks of each stream so far
-            while (w.next()) {
-                const int nb = w.b_last - w.b_first;
-                wait(q_full, (uint32_t)(items++ & 1));
+            for (int it = 0;; ++it) {
+                const Item& w = item_at(it);
+                if (!ok || w.nb == 0)
+                    break;
+                const int nb = w.nb, n = w.slot0;
+                const bool dual = w.dual();
+                wait(q_full, (uint32_t)(it & 1));
+                mbar_arrive(item_empty(it));
                 tc_fence_after();
                 auto k_slot = [&](int j) { return n + 2 * j; };
                 auto v_slot = [&](int j) { return n + 2 * j + 1; };
@@ -420,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                desc128(b + ks * 2048, G::HALF), id_o, add || ks > 0);
                     commit(o_done(s));
                 };
-                if (w.dual()) {
+                if (dual) {
                     arrived(k_slot(0));
                     score(0, 0, 0);
                     score(1, 1, 0);
@@ -456,18 +407,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                n += 2 * nb;
             }
             // the last MMAs end before tensor memory goes away
             for (int s = 0; s < 2; ++s)
                 if (np[s])
                     wait(o_done(s), (uint32_t)((np[s] - 1) & 1));
+        } else if (warp == 2) {
+            // ---- the share's items ----
+            Walk<Items> w(p, share, blockIdx.x);
+            Item* out = reinterpret_cast<Item*>(smem + G::ITEMS);
+            int slot0 = 0;
+            for (int it = 0;; ++it) {
+                const bool more = w.next();
+                if (it >= kItems)
+                    wait(item_empty(it), (uint32_t)((it / kItems - 1) & 1));
+                if (lane == 0) {
+                    const int nb = more ? w.b_last - w.b_first : 0;
+                    out[it % kItems] = {w.q, w.r, w.x.row0, w.x.rows, w.head, w.x.lo, w.x.hi,
+                                        w.key0(w.b_first), nb, slot0, w.first_cta(), w.last_cta()};
+                    mbar_arrive(item_full(it));          // releases the stores
+                    slot0 += 2 * nb;
+                }
+                if (!more || !__all_sync(0xffffffffu, ok))
+                    break;
+            }
         }
         __syncwarp();
     } else {
         // ---- the streams: one row a thread ----
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegsStream));
-        Walk w(p, *start, ctas, blockIdx.x);
         const int s = (warp >> 2) - 1;                               // stream
         const int trow = tid & 127;                                  // row within the tile
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -475,142 +443,139 @@ __global__ void __launch_bounds__(kThreads, 1)
         float2* stats = reinterpret_cast<float2*>(smem + G::STATS);
         // scores are c times Q's: a negative scale negates Q, a zero one clears it
         const float c = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
-        const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
-        int n = 0, done = 0;             // slots before this item; blocks of this stream so far
-        while (w.next()) {
+        int done = 0;                    // blocks of this stream so far
+        // Stores this thread's row of an item's Q.  The MMAs that read the Q tiles of
+        // the item before are complete: their scores have been read.
+        auto enter = [&](const Item& w) {
             const bool dual = w.dual();
-            const int nb = w.b_last - w.b_first;
-            // this thread's row of the item, and its Q into shared memory
             const int item_row = dual ? s * kTile + trow : trow;
-            const bool in = item_row < w.x.rows;
-            const int row = w.x.row0 + item_row;
-            const int i = row / p.group, g = row - i * p.group;
-            const int64_t tok = w.q.q0 + i;
-            const int head = w.head * p.group + g;
-            const int pos = in ? w.q.first + i : INT_MIN / 2;
-            const uint64_t word = in && p.tree ? p.tree[tok] : 0;
-            if (dual || s == 0) {
-                const uint16_t* src = p.q + tok * p.q_token + (int64_t)head * p.q_head;
-                unsigned char* dst = smem + G::Q + s * G::SLOT + trow * 128;
-#pragma unroll
-                for (int ch = 0; ch < D / 8; ++ch) {
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (in && p.scale_log2 != 0.f) {
-                        if (p.q_wide) {
-                            v = *reinterpret_cast<const uint4*>(src + ch * 8);
-                        } else {
-                            uint32_t e[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                e[k] = (uint32_t)src[ch * 8 + 2 * k] |
-                                       ((uint32_t)src[ch * 8 + 2 * k + 1] << 16);
-                            v = make_uint4(e[0], e[1], e[2], e[3]);
-                        }
-                        v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
-                    }
-                    *reinterpret_cast<uint4*>(dst + (ch >> 3) * G::HALF + (((ch & 7) ^ (trow & 7)) << 4)) = v;
-                }
-                fence_proxy_async_smem();
-            }
+            const bool in = item_row < w.rows;
+            if (dual || s == 0)
+                store_q<D>(p, w.q.q0, w.head, w.row0 + item_row, in, smem + G::Q + s * G::SLOT, trow);
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(q_full);
-            // keys at `open_hi` and past, or below `open_lo`, are hidden from some row of the tile
-            const int r0 = w.x.row0 + (dual ? s * kTile : 0);
-            const int r1 = min(r0 + kTile, w.x.row0 + w.x.rows) - 1;
-            const int open_hi = p.tree ? min(w.q.keys, w.q.first)
-                                       : min(w.q.keys, w.q.first + r0 / p.group + 1);
-            const int open_lo = p.window > 0 ? w.q.first + r1 / p.group - p.window + 1 : 0;
-            const bool idle = r0 + (warp & 3) * 32 > r1;             // no row in this warp
+        };
+        bool more = item_at(0).nb > 0 && ok;
+        if (more)
+            enter(items[0]);
+        for (int it = 0; more; ++it) {
+            const Item& w = items[it % kItems];
+            const bool dual = w.dual();
+            const int nb = w.nb;
+            const int item_row = dual ? s * kTile + trow : trow;
             float m = -INFINITY;
             float2 l = make_float2(0.f, 0.f);
             int mine = 0;                                            // blocks of this item
-            for (int j = dual ? 0 : s; j < nb; j += dual ? 1 : 2, ++mine, ++done) {
-                const int k0 = w.key0(w.b_first + j);
-                if (ok)
-                    ok = mbar_wait(s_full(s), (uint32_t)(done & 1));
-                tc_fence_after();
-                if (!idle) {
-                    float t[4][32];
+            {
+                const bool in = item_row < w.rows;
+                const int i = (w.row0 + item_row) / p.group;
+                const int pos = in ? w.q.first + i : INT_MIN / 2;
+                const uint64_t word = in && p.tree ? p.tree[w.q.q0 + i] : 0;
+                // keys at `open_hi` and past, or below `open_lo`, are hidden from some
+                // row of the tile
+                const int r0 = w.row0 + (dual ? s * kTile : 0);
+                const int r1 = min(r0 + kTile, w.row0 + w.rows) - 1;
+                const int open_hi = p.tree ? min(w.q.keys, w.q.first)
+                                           : min(w.q.keys, w.q.first + r0 / p.group + 1);
+                const int open_lo = p.window > 0 ? w.q.first + r1 / p.group - p.window + 1 : 0;
+                const bool idle = r0 + (warp & 3) * 32 > r1;         // no row in this warp
+                for (int j = dual ? 0 : s; j < nb; j += dual ? 1 : 2, ++mine, ++done) {
+                    const int k0 = w.key0 + j * kKeys;
+                    wait(s_full(s), (uint32_t)(done & 1));
+                    tc_fence_after();
+                    if (!idle) {
+                        float t[4][32];
+                        const bool masked = k0 + kKeys > open_hi || k0 < open_lo;
+                        uint32_t see[4];
+                        if (masked)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        tmem_ld32(s_at + e * 32, t[e]);
-                    tmem_wait_ld();
-                    if (k0 + kKeys > open_hi || k0 < open_lo) {
+                            for (int e = 0; e < 4; ++e)
+                                see[e] = seen32(p, w.q, pos, word, k0 + e * 32);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint32_t see = seen32(p, w.q, pos, word, k0 + e * 32);
+                        for (int e = 0; e < 4; ++e)
+                            tmem_ld32(s_at + e * 32, t[e]);
+                        tmem_wait_ld();
+                        if (masked)
 #pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                t[e][k] = (see >> k) & 1u ? t[e][k] : -INFINITY;
-                        }
-                    }
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int e = 0; e < 128; e += 2)
-                        top = fmaxf(top, fmaxf(t[e >> 5][e & 31], t[e >> 5][(e & 31) + 1]));
-                    top *= c;
-                    const bool moved = top > m + 8.f;                // also from -inf
-                    if (__any_sync(0xffffffffu, moved)) {
-                        const float f = moved ? ex2(m - top) : 1.f;
-                        m = moved ? top : m;
-                        l.x *= f, l.y *= f;
-                        if (mine > 0) {
-                            if (ok)
-                                ok = mbar_wait(o_done(s), (uint32_t)((done - 1) & 1));
-                            tc_fence_after();
-#pragma unroll 1
-                            for (int e = 0; e < D / 32; ++e) {
-                                float o[32];
-                                tmem_ld32(o_at + s * 128 + e * 32, o);
-                                tmem_wait_ld();
-                                uint32_t r[32];
+                            for (int e = 0; e < 4; ++e)
 #pragma unroll
                                 for (int k = 0; k < 32; ++k)
-                                    r[k] = __float_as_uint(o[k] * f);
-                                tmem_st32(o_at + s * 128 + e * 32, r);
+                                    t[e][k] = (see[e] >> k) & 1u ? t[e][k] : -INFINITY;
+                        float tops[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            tops[e] = fmaxf(t[e][0], t[e][1]);
+#pragma unroll
+                            for (int k = 2; k < 32; k += 2)
+                                tops[e] = fmaxf(tops[e], fmaxf(t[e][k], t[e][k + 1]));
+                        }
+                        const float top = c * fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                        const bool moved = top > m + 8.f;            // also from -inf
+                        if (__any_sync(0xffffffffu, moved)) {
+                            const float f = moved ? ex2(m - top) : 1.f;
+                            m = moved ? top : m;
+                            l.x *= f, l.y *= f;
+                            if (mine > 0) {
+                                wait(o_done(s), (uint32_t)((done - 1) & 1));
+                                tc_fence_after();
+#pragma unroll 1
+                                for (int e = 0; e < D / 16; ++e) {
+                                    float o[16];
+                                    tmem_ld16(o_at + s * 128 + e * 16, o);
+                                    tmem_wait_ld();
+                                    uint32_t r[16];
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k)
+                                        r[k] = __float_as_uint(o[k] * f);
+                                    tmem_st16(o_at + s * 128 + e * 16, r);
+                                }
                             }
                         }
-                    }
-                    const float ref = m == -INFINITY ? 0.f : -m;
+                        const float ref = m == -INFINITY ? 0.f : -m;
+                        const float2 c2 = make_float2(c, c), ref2 = make_float2(ref, ref);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t r[32];
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t r[16];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float a = ex2(fmaf(t[2 * h + (e >> 4)][(2 * e) & 31], c, ref));
-                            const float b = ex2(fmaf(t[2 * h + (e >> 4)][((2 * e) & 31) + 1], c, ref));
-                            l.x += a, l.y += b;
-                            r[e] = pack2<DT>(a, b);
+                            for (int k = 0; k < 16; ++k) {
+                                float2 v = fma2(make_float2(t[e][2 * k], t[e][2 * k + 1]), c2, ref2);
+                                v.x = ex2(v.x), v.y = ex2(v.y);
+                                l = add2(l, v);
+                                r[k] = pack2<DT>(v.x, v.y);
+                            }
+                            tmem_st16(s_at + e * 16, r);
                         }
-                        tmem_st32(s_at + h * 32, r);
+                        tmem_wait_st();
                     }
-                    tmem_wait_st();
-                }
-                // slots past the context may hold anything: NaN times 0 is not 0
-                if (k0 + kKeys > w.q.keys) {
-                    const int v = n + 2 * j + 1;
-                    if (ok)
-                        ok = mbar_wait(full(v % G::NSLOT), (uint32_t)((v / G::NSLOT) & 1));
-                    if (k0 + trow >= w.q.keys) {
-                        unsigned char* z = smem + G::RING + (v % G::NSLOT) * G::SLOT + trow * 128;
+                    // slots past the context may hold anything: NaN times 0 is not 0
+                    if (k0 + kKeys > w.q.keys) {
+                        const int v = w.slot0 + 2 * j + 1;
+                        wait(full(v % G::NSLOT), (uint32_t)((v / G::NSLOT) & 1));
+                        if (k0 + trow >= w.q.keys) {
+                            unsigned char* z = smem + G::RING + (v % G::NSLOT) * G::SLOT + trow * 128;
 #pragma unroll
-                        for (int e = 0; e < D / 8; ++e)
-                            *reinterpret_cast<uint4*>(z + (e >> 3) * G::HALF + ((e & 7) << 4)) =
-                                make_uint4(0u, 0u, 0u, 0u);
+                            for (int e = 0; e < D / 8; ++e)
+                                *reinterpret_cast<uint4*>(z + (e >> 3) * G::HALF + ((e & 7) << 4)) =
+                                    make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        fence_proxy_async_smem();
                     }
-                    fence_proxy_async_smem();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(p_full(s));
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(p_full(s));
             }
-            n += 2 * nb;
 
-            // ---- the item's result ----
-            if (mine > 0 && ok)
-                ok = mbar_wait(o_done(s), (uint32_t)((done - 1) & 1));
+            // ---- the item's result, while the next item's first scores are computed ----
+            if (!dual)                                   // both streams read tile 0, which stream 0 stores
+                named_bar_sync(1, 256);
+            more = item_at(it + 1).nb > 0 && ok;
+            if (more)
+                enter(items[(it + 1) % kItems]);
+            if (mine > 0)
+                wait(o_done(s), (uint32_t)((done - 1) & 1));
             float sum = l.x + l.y, f0 = 1.f, f1 = 0.f;   // factors of this row in O_0 and O_1
             if (!dual) {
                 stats[s * kTile + trow] = make_float2(m, sum);
@@ -623,10 +588,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sum = f0 * a.y + f1 * b.y;
             }
             tc_fence_after();
-            const bool whole = w.whole();
-            const int c0 = whole ? 0 : w.cta_of(w.item);
-            const int c1 = whole ? 0 : w.cta_of(w.item + (unsigned)w.x.blocks - 1);
-            float* slot = p.partial + (size_t)(2 * blockIdx.x + (c0 == (int)blockIdx.x)) * G::PARTIAL;
+            const bool in = item_row < w.rows, whole = w.whole();
+            const int row = w.row0 + item_row, i = row / p.group;
+            const int64_t tok = w.q.q0 + i;
+            const int head = w.head * p.group + row - i * p.group;
+            float* slot = p.partial + (size_t)(2 * blockIdx.x + (w.c0 == (int)blockIdx.x)) * G::PARTIAL;
             // dual: all columns of the row; else the stream's half of them
             const int e0 = dual ? 0 : s * (D / 64), e1 = dual ? D / 32 : (s + 1) * (D / 64);
 #pragma unroll 1
@@ -666,22 +632,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     slot[kRows * (D + 1) + item_row] = sum;
                 }
             }
-            if (!whole) {
-                __threadfence();
-                named_bar_sync(1, 256);
-                if (tid == 128)
-                    flag = atomicAdd(p.counters + c0, 1u) == (unsigned)(c1 - c0);
-                named_bar_sync(1, 256);
-                if (flag) {                              // every part is there: join them
-                    __threadfence();
-                    join_parts<DT, D, kRows>(p, w.q, w.head, w.x.row0, w.x.rows, c0, c1, tid - 128, 256);
-                    if (tid == 128)
-                        p.counters[c0] = 0;              // as the next call finds it
-                }
-            }
-            // both streams are done reading O and the flag
+            if (!whole && tid == 128 && w.c0 == (int)blockIdx.x)
+                static_cast<JoinItem*>(p.items)[w.c0] = {w.q.q0, w.row0, w.rows, w.head,
+                                                         w.c1 - w.c0 + 1};
+            // both streams are done reading O and the statistics
             tc_fence_before();
             named_bar_sync(1, 256);
+            if (lane == 0)
+                mbar_arrive(item_empty(it));
         }
     }
     if (!ok)
@@ -698,12 +656,14 @@ cudaError_t launch(const AttendParams& p, const CUtensorMap& kmap, const CUtenso
                    cudaStream_t st)
 {
     auto kernel = lbv_attend_tiles_kernel<DT, D>;
-    const cudaError_t e = cudaFuncSetAttribute(
-        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<D>::BYTES);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Geo<D>::BYTES);
     if (e != cudaSuccess)
         return e;
-    kernel<<<sms < kAttendMaxCtas ? sms : kAttendMaxCtas, kThreads, Geo<D>::BYTES, st>>>(p, kmap, vmap);
-    return cudaGetLastError();
+    const int ctas = sms < kAttendMaxCtas ? sms : kAttendMaxCtas;
+    kernel<<<ctas, kThreads, Geo<D>::BYTES, st>>>(p, kmap, vmap);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? launch_attend_join(p, (lbv_dtype)DT, kRows, ctas, st) : e;
 }
 
 }  // namespace

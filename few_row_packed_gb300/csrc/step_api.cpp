@@ -348,8 +348,7 @@ size_t lbv_attend_workspace_bytes(const lbv_kv_cache* cache, const lbv_batch* ba
         return 0;
     const size_t rows = lbv::attend_rows_partial_floats(cache->view.dim, cache->sms);
     const size_t tiles = lbv::attend_tiles_partial_floats(cache->view.dim, cache->sms);
-    return lbv::kAttendHeader + lbv::kAttendMaxCtas * sizeof(unsigned) +
-           (rows > tiles ? rows : tiles) * sizeof(float);
+    return lbv::kAttendPartial + (rows > tiles ? rows : tiles) * sizeof(float);
 }
 
 lbv_status lbv_attend(const lbv_kv_cache* cache, const lbv_batch* batch, const lbv_rows* q,
@@ -382,6 +381,12 @@ lbv_status lbv_attend(const lbv_kv_cache* cache, const lbv_batch* batch, const l
         workspace_bytes < lbv_attend_workspace_bytes(cache, batch, q->heads))
         return fail(LBV_ERR_WORKSPACE, "%s: workspace NULL, not 256-byte aligned or %zu < %zu bytes",
                     fn, workspace_bytes, lbv_attend_workspace_bytes(cache, batch, q->heads));
+    // the kernels count blocks of keys in 32 bits: an upper bound of theirs
+    const double blocks = ((double)batch->tokens * q->heads / 16 + batch->requests * (double)cache->view.heads) *
+                          ((double)batch->table_pages * (1 << cache->view.page_shift) / 64 + 2);
+    if (blocks >= 4294967296.0)
+        return fail(LBV_ERR_UNSUPPORTED, "%s: %d tokens over tables of %d pages are too many for one call",
+                    fn, batch->tokens, batch->table_pages);
     lbv::AttendParams p;
     p.q = static_cast<const uint16_t*>(q->data);
     p.q_token = q->token_stride;
@@ -401,9 +406,9 @@ lbv_status lbv_attend(const lbv_kv_cache* cache, const lbv_batch* batch, const l
     p.kv = cache->view;
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     p.status = reinterpret_cast<unsigned*>(ws);
-    p.counters = reinterpret_cast<unsigned*>(ws + lbv::kAttendHeader);
-    p.partial = reinterpret_cast<float*>(ws + lbv::kAttendHeader +
-                                         lbv::kAttendMaxCtas * sizeof(unsigned));
+    p.counters = reinterpret_cast<unsigned*>(ws + lbv::kAttendCounters);
+    p.items = ws + lbv::kAttendItems;
+    p.partial = reinterpret_cast<float*>(ws + lbv::kAttendPartial);
     // Rows (new token times query head of a group) of an average request, whose
     // lengths the host does not know.  Both kernels are right for every length.
     const int64_t rows = ((int64_t)batch->tokens + batch->requests - 1) / batch->requests * p.group;
@@ -426,7 +431,7 @@ lbv_status lbv_attend_status(void* workspace)
     if (e == cudaSuccess)
         e = cudaMemcpy(&word, workspace, sizeof word, cudaMemcpyDeviceToHost);
     if (e == cudaSuccess && word)
-        e = cudaMemset(workspace, 0, lbv::kAttendHeader + lbv::kAttendMaxCtas * sizeof(unsigned));
+        e = cudaMemset(workspace, 0, lbv::kAttendItems);
     if (e != cudaSuccess)
         return cuda_fail(e, fn);
     if (word)
