@@ -62,6 +62,9 @@ struct Geo {
     static constexpr int FLAG = BARS + 2 * NST * 8;
     static constexpr int START = FLAG + 16;                 // where the CTA's share begins
     static constexpr int BYTES = START + 64;
+    static_assert(O_BUF % 16 == 0 && M_BUF % 16 == 0 && BARS % 8 == 0 && START % 8 == 0 &&
+                      sizeof(Start) <= 64,
+                  "alignment");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4])

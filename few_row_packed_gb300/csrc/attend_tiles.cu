@@ -11,7 +11,7 @@
 //     gives the streams two row tiles that share every block of keys; a smaller
 //     one gives them its even and its odd blocks and adds the two results.
 //   * A copy warp fills a ring of 128-byte-swizzled slots, K and V of a block in
-//     turn, by TMA; one thread issues the MMAs; commits free the slots.
+//     turn, by TMA; another warp issues the MMAs; commits free the slots.
 //   * A row's reference maximum moves only when it grew by more than 8 (see
 //     attend_rows.cu); only then are its sums in tensor memory rescaled, by the
 //     row's own thread.
@@ -59,8 +59,8 @@ struct Geo {
     static constexpr int RING = 2 * SLOT;
     static constexpr int NSLOT = D == 128 ? 5 : 10;
     static constexpr int BARS = RING + NSLOT * SLOT;
-    static constexpr int NBARS = 2 * NSLOT + 8 + 2 * kItems;
-    static constexpr int STATS = BARS + NBARS * 8;          // [2][128] m and sums of the streams
+    static constexpr int NBARS = 2 * NSLOT + 9 + 2 * kItems;
+    static constexpr int STATS = (BARS + NBARS * 8 + 15) / 16 * 16;   // [2][128] m and sums of the streams
     static constexpr int ITEMS = STATS + 2 * kTile * 8;     // ring of items
     static constexpr int WORDS = ITEMS + kItems * 64;       // tensor-memory address
     static constexpr int BYTES = WORDS + 16;
@@ -69,6 +69,7 @@ struct Geo {
     static constexpr int PARTIAL = kRows * (D + 2);         // floats of one partial result
     // tensor memory columns
     static constexpr uint32_t S0 = 0, O0 = 256;             // S of stream s at S0 + 128 s
+    static_assert(BARS % 8 == 0 && STATS % 16 == 0 && ITEMS % 16 == 0 && WORDS % 16 == 0, "alignment");
     static_assert(BYTES <= 227 * 1024 && sizeof(Start) <= 2 * kTile * 8, "shared memory");
 };
 
@@ -132,33 +133,48 @@ __device__ __forceinline__ void tmem_wait_st()
     asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+// Four steps of 16 of the contracted dimension, D (+)= A B, issued by one elected
+// lane of a converged warp: their operands stay in uniform registers that way (a
+// single thread in a branch of its own took 85 cycles an MMA to issue them).
+// `add` 0: the first step overwrites D.
+__device__ __forceinline__ void mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add)
 {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b),
-        "r"(idesc), "r"((uint32_t)add)
+        "{\n .reg .pred e, p;\n setp.ne.b32 p, %10, 0;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %5, %9, p;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %2, %6, %9, 1;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %3, %7, %9, 1;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %4, %8, %9, 1;\n}\n" ::"r"(d), "l"(a), "l"(a + 2),
+        "l"(a + 4), "l"(a + 6), "l"(b), "l"(b + 2), "l"(b + 4), "l"(b + 6), "r"(idesc), "r"(add)
         : "memory");
 }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+// The same with A (P) in tensor memory and B (V) with its rows along the
+// contracted dimension: 8 columns of A and 16 rows of B a step.
+__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add)
 {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b),
-        "r"(idesc), "r"((uint32_t)add)
+        "{\n .reg .pred e, p;\n setp.ne.b32 p, %10, 0;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %5, %9, p;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], %6, %9, 1;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], %7, %9, 1;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%4], %8, %9, 1;\n}\n" ::"r"(d), "r"(a),
+        "r"(a + 8), "r"(a + 16), "r"(a + 24), "l"(b), "l"(b + 128), "l"(b + 256), "l"(b + 384),
+        "r"(idesc), "r"(add)
         : "memory");
 }
 
-// Arrives on `bar` once every MMA this thread has issued is complete.
+// Arrives on `bar` once every MMA the elected lane has issued is complete.
 __device__ __forceinline__ void commit(uint32_t bar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar)
-                 : "memory");
+    asm volatile(
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
+        : "memory");
 }
 
 // Shared-memory matrix descriptor in 128-byte-swizzled rows: 8-row groups 1024
-// bytes apart; for an operand whose rows run along the other dimension (V),
+// bytes apart; for an operand whose rows run along the contracted dimension (V),
 // `lead` bytes between its 64-element column groups.
 __device__ __forceinline__ uint64_t desc128(uint32_t addr, uint32_t lead)
 {
@@ -204,23 +220,31 @@ __device__ __forceinline__ void store_q(const AttendParams& p, int q0, int kv_he
     const int i = row / p.group;
     const uint16_t* src = p.q + (int64_t)(q0 + i) * p.q_token +
                           (int64_t)(kv_head * p.group + row - i * p.group) * p.q_head;
-    unsigned char* dst = tile + trow * 128;
+    uint4 v[D / 8];
 #pragma unroll
-    for (int ch = 0; ch < D / 8; ++ch) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (in && p.scale_log2 != 0.f) {
-            if (p.q_wide) {
-                v = *reinterpret_cast<const uint4*>(src + ch * 8);
-            } else {
+    for (int ch = 0; ch < D / 8; ++ch)
+        v[ch] = make_uint4(0u, 0u, 0u, 0u);
+    if (in && p.scale_log2 != 0.f) {
+        if (p.q_wide) {                              // all loads in flight before the first store
+#pragma unroll
+            for (int ch = 0; ch < D / 8; ++ch)
+                v[ch] = __ldg(reinterpret_cast<const uint4*>(src) + ch);
+        } else {
+#pragma unroll
+            for (int ch = 0; ch < D / 8; ++ch) {
                 uint32_t e[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     e[k] = (uint32_t)src[ch * 8 + 2 * k] | ((uint32_t)src[ch * 8 + 2 * k + 1] << 16);
-                v = make_uint4(e[0], e[1], e[2], e[3]);
+                v[ch] = make_uint4(e[0], e[1], e[2], e[3]);
             }
-            v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
         }
-        *reinterpret_cast<uint4*>(dst + (ch >> 3) * Geo<D>::HALF + (((ch & 7) ^ (trow & 7)) << 4)) = v;
+    }
+    unsigned char* dst = tile + trow * 128;
+#pragma unroll
+    for (int ch = 0; ch < D / 8; ++ch) {
+        v[ch].x ^= flip, v[ch].y ^= flip, v[ch].z ^= flip, v[ch].w ^= flip;
+        *reinterpret_cast<uint4*>(dst + (ch >> 3) * Geo<D>::HALF + (((ch & 7) ^ (trow & 7)) << 4)) = v[ch];
     }
     fence_proxy_async_smem();
 }
@@ -242,10 +266,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto empty = [&](int i) { return bar(G::NSLOT + i); };
     const uint32_t q_full = bar(2 * G::NSLOT);                       // both Q tiles are stored
     auto s_full = [&](int s) { return bar(2 * G::NSLOT + 1 + s); };  // S of stream s is complete
-    auto p_full = [&](int s) { return bar(2 * G::NSLOT + 3 + s); };  // P replaced it
-    auto o_done = [&](int s) { return bar(2 * G::NSLOT + 5 + s); };  // O has the block
-    auto item_full = [&](int i) { return bar(2 * G::NSLOT + 7 + i % kItems); };
-    auto item_empty = [&](int i) { return bar(2 * G::NSLOT + 7 + kItems + i % kItems); };
+    auto o_done = [&](int s) { return bar(2 * G::NSLOT + 3 + s); };  // O has the block
+    auto p_full = [&](int s, int half) { return bar(2 * G::NSLOT + 5 + 2 * s + half); };  // P replaced S
+    auto item_full = [&](int i) { return bar(2 * G::NSLOT + 9 + i % kItems); };
+    auto item_empty = [&](int i) { return bar(2 * G::NSLOT + 9 + kItems + i % kItems); };
     const Item* items = reinterpret_cast<const Item*>(smem + G::ITEMS);
 
     if (tid == 0) {
@@ -256,7 +280,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(q_full, 8);
         for (int s = 0; s < 2; ++s) {
             mbar_init(s_full(s), 1);
-            mbar_init(p_full(s), 4);
+            mbar_init(p_full(s, 0), 4);
+            mbar_init(p_full(s, 1), 4);
             mbar_init(o_done(s), 1);
         }
         for (int i = 0; i < kItems; ++i) {
@@ -336,82 +361,96 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < G::NSLOT; ++i)
                 if (n - 1 - i >= 0)
                     wait(empty((n - 1 - i) % G::NSLOT), (uint32_t)(((n - 1 - i) / G::NSLOT) & 1));
-        } else if (warp == 1 && lane == 0) {
+        } else if (warp == 1) {
             // ---- MMAs ----
             constexpr uint32_t id_s = idesc<DT>(kKeys, false), id_o = idesc<DT>(D, true);
-            int np[2] = {0, 0};                          // blocks of each stream so far
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            uint32_t n = 0, np0 = 0, np1 = 0;            // ring slots, blocks of each stream so far
             for (int it = 0;; ++it) {
                 const Item& w = item_at(it);
-                if (!ok || w.nb == 0)
+                const int nb = __shfl_sync(0xffffffffu, w.nb, 0);
+                const bool dual = __shfl_sync(0xffffffffu, w.rows, 0) > kTile;
+                if (!__all_sync(0xffffffffu, ok) || nb == 0)
                     break;
-                const int nb = w.nb, n = w.slot0;
-                const bool dual = w.dual();
                 wait(q_full, (uint32_t)(it & 1));
-                mbar_arrive(item_empty(it));
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(item_empty(it));
+                __syncwarp();
                 tc_fence_after();
-                auto k_slot = [&](int j) { return n + 2 * j; };
-                auto v_slot = [&](int j) { return n + 2 * j + 1; };
-                auto arrived = [&](int i) { wait(full(i % G::NSLOT), (uint32_t)((i / G::NSLOT) & 1)); };
-                auto score = [&](int s, int tile, int j) {           // S_s = Q_tile K_j^T
-                    const uint32_t a = sbase + G::Q + tile * G::SLOT;
-                    const uint32_t b = sbase + G::RING + (k_slot(j) % G::NSLOT) * G::SLOT;
+                // K of block j is slot 2 j from the item's first, V the one after it
+                auto arrived = [&](uint32_t i) {
+                    wait(full(i % G::NSLOT), (i / G::NSLOT) & 1);
+                    __syncwarp();
+                };
+                auto release = [&](uint32_t i) { commit(empty(i % G::NSLOT)); };
+                auto score = [&](int s, int tile, uint32_t i) {      // S_s = Q_tile K^T
+                    const uint64_t a = desc128(sbase + G::Q + tile * G::SLOT, 0);
+                    const uint64_t b = desc128(sbase + G::RING + (i % G::NSLOT) * G::SLOT, 0);
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)
-                        mma_ss(tmem + G::S0 + s * 128, desc128(a + (ks / 4) * G::HALF + (ks % 4) * 32, 0),
-                               desc128(b + (ks / 4) * G::HALF + (ks % 4) * 32, 0), id_s, ks > 0);
+                    for (int h = 0; h < D / 64; ++h)
+                        mma4_ss(tm + G::S0 + s * 128, a + h * (G::HALF >> 4), b + h * (G::HALF >> 4), id_s,
+                                h > 0);
                     commit(s_full(s));
                 };
-                auto value = [&](int s, int j, bool add) {           // O_s += P_s V_j
-                    wait(p_full(s), (uint32_t)(np[s]++ & 1));
-                    tc_fence_after();
-                    const uint32_t b = sbase + G::RING + (v_slot(j) % G::NSLOT) * G::SLOT;
+                auto value = [&](int s, uint32_t& np, uint32_t i, bool add) {    // O_s += P_s V
+                    const uint64_t b = desc128(sbase + G::RING + (i % G::NSLOT) * G::SLOT, G::HALF);
 #pragma unroll
-                    for (int ks = 0; ks < kKeys / 16; ++ks)
-                        mma_ts(tmem + G::O0 + s * 128, tmem + G::S0 + s * 128 + ks * 8,
-                               desc128(b + ks * 2048, G::HALF), id_o, add || ks > 0);
+                    for (int h = 0; h < 2; ++h) {                    // 64 keys of P at a time
+                        wait(p_full(s, h), np & 1);
+                        __syncwarp();
+                        tc_fence_after();
+                        mma4_ts(tm + G::O0 + s * 128, tm + G::S0 + s * 128 + h * 32, b + h * 512, id_o,
+                                add || h > 0);
+                    }
+                    ++np;
                     commit(o_done(s));
                 };
                 if (dual) {
-                    arrived(k_slot(0));
-                    score(0, 0, 0);
-                    score(1, 1, 0);
-                    commit(empty(k_slot(0) % G::NSLOT));
-                    for (int j = 0; j < nb; ++j) {
-                        arrived(v_slot(j));
+                    arrived(n);
+                    score(0, 0, n);
+                    score(1, 1, n);
+                    release(n);
+                    for (int j = 0; j < nb; ++j, n += 2) {
+                        arrived(n + 1);
                         if (j + 1 < nb)
-                            arrived(k_slot(j + 1));
-                        value(0, j, j > 0);
+                            arrived(n + 2);
+                        value(0, np0, n + 1, j > 0);
                         if (j + 1 < nb)
-                            score(0, 0, j + 1);
-                        value(1, j, j > 0);
-                        commit(empty(v_slot(j) % G::NSLOT));
+                            score(0, 0, n + 2);
+                        value(1, np1, n + 1, j > 0);
+                        release(n + 1);
                         if (j + 1 < nb) {
-                            score(1, 1, j + 1);
-                            commit(empty(k_slot(j + 1) % G::NSLOT));
+                            score(1, 1, n + 2);
+                            release(n + 2);
                         }
                     }
                 } else {
                     for (int j = 0; j < 2 && j < nb; ++j) {
-                        arrived(k_slot(j));
-                        score(j, 0, j);
-                        commit(empty(k_slot(j) % G::NSLOT));
+                        arrived(n + 2 * j);
+                        score(j, 0, n + 2 * j);
+                        release(n + 2 * j);
                     }
-                    for (int j = 0; j < nb; ++j) {
-                        arrived(v_slot(j));
-                        value(j & 1, j, j > 1);
-                        commit(empty(v_slot(j) % G::NSLOT));
+                    for (int j = 0; j < nb; ++j, n += 2) {
+                        arrived(n + 1);
+                        if (j & 1)
+                            value(1, np1, n + 1, j > 1);
+                        else
+                            value(0, np0, n + 1, j > 1);
+                        release(n + 1);
                         if (j + 2 < nb) {
-                            arrived(k_slot(j + 2));
-                            score(j & 1, 0, j + 2);
-                            commit(empty(k_slot(j + 2) % G::NSLOT));
+                            arrived(n + 4);
+                            score(j & 1, 0, n + 4);
+                            release(n + 4);
                         }
                     }
                 }
             }
             // the last MMAs end before tensor memory goes away
-            for (int s = 0; s < 2; ++s)
-                if (np[s])
-                    wait(o_done(s), (uint32_t)((np[s] - 1) & 1));
+            if (np0)
+                wait(o_done(0), (np0 - 1) & 1);
+            if (np1)
+                wait(o_done(1), (np1 - 1) & 1);
         } else if (warp == 2) {
             // ---- the share's items ----
             Walk<Items> w(p, share, blockIdx.x);
@@ -484,8 +523,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int k0 = w.key0 + j * kKeys;
                     wait(s_full(s), (uint32_t)(done & 1));
                     tc_fence_after();
+                    // slots past the context may hold anything: NaN times 0 is not 0
+                    if (k0 + kKeys > w.q.keys) {
+                        const int v = w.slot0 + 2 * j + 1;
+                        wait(full(v % G::NSLOT), (uint32_t)((v / G::NSLOT) & 1));
+                        if (k0 + trow >= w.q.keys) {
+                            unsigned char* z = smem + G::RING + (v % G::NSLOT) * G::SLOT + trow * 128;
+#pragma unroll
+                            for (int e = 0; e < D / 8; ++e)
+                                *reinterpret_cast<uint4*>(z + (e >> 3) * G::HALF + ((e & 7) << 4)) =
+                                    make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        fence_proxy_async_smem();
+                    }
+                    float t[4][32];
                     if (!idle) {
-                        float t[4][32];
                         const bool masked = k0 + kKeys > open_hi || k0 < open_lo;
                         uint32_t see[4];
                         if (masked)
@@ -502,6 +554,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                                 for (int k = 0; k < 32; ++k)
                                     t[e][k] = (see[e] >> k) & 1u ? t[e][k] : -INFINITY;
+                    }
+                    // P of 32 keys and its sum, for the reference m
+                    uint32_t r[16];
+                    float2 part;
+                    auto exps = [&](int e) {
+                        const float ref = m == -INFINITY ? 0.f : -m;
+                        part = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            float2 v = fma2(make_float2(t[e][2 * k], t[e][2 * k + 1]), make_float2(c, c),
+                                            make_float2(ref, ref));
+                            v.x = ex2(v.x), v.y = ex2(v.y);
+                            part = add2(part, v);
+                            r[k] = pack2<DT>(v.x, v.y);
+                        }
+                    };
+                    if (!idle) {
+                        // the first 32 keys with the reference as it is, while the block's
+                        // maximum is found; once more if that moves the reference
+                        exps(0);
                         float tops[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -524,47 +596,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     float o[16];
                                     tmem_ld16(o_at + s * 128 + e * 16, o);
                                     tmem_wait_ld();
-                                    uint32_t r[16];
 #pragma unroll
                                     for (int k = 0; k < 16; ++k)
                                         r[k] = __float_as_uint(o[k] * f);
                                     tmem_st16(o_at + s * 128 + e * 16, r);
                                 }
                             }
+                            exps(0);
                         }
-                        const float ref = m == -INFINITY ? 0.f : -m;
-                        const float2 c2 = make_float2(c, c), ref2 = make_float2(ref, ref);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint32_t r[16];
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                float2 v = fma2(make_float2(t[e][2 * k], t[e][2 * k + 1]), c2, ref2);
-                                v.x = ex2(v.x), v.y = ex2(v.y);
-                                l = add2(l, v);
-                                r[k] = pack2<DT>(v.x, v.y);
-                            }
-                            tmem_st16(s_at + e * 16, r);
-                        }
+                        l = add2(l, part);
+                        tmem_st16(s_at, r);
+                        exps(1);
+                        l = add2(l, part);
+                        tmem_st16(s_at + 16, r);
                         tmem_wait_st();
-                    }
-                    // slots past the context may hold anything: NaN times 0 is not 0
-                    if (k0 + kKeys > w.q.keys) {
-                        const int v = w.slot0 + 2 * j + 1;
-                        wait(full(v % G::NSLOT), (uint32_t)((v / G::NSLOT) & 1));
-                        if (k0 + trow >= w.q.keys) {
-                            unsigned char* z = smem + G::RING + (v % G::NSLOT) * G::SLOT + trow * 128;
-#pragma unroll
-                            for (int e = 0; e < D / 8; ++e)
-                                *reinterpret_cast<uint4*>(z + (e >> 3) * G::HALF + ((e & 7) << 4)) =
-                                    make_uint4(0u, 0u, 0u, 0u);
-                        }
-                        fence_proxy_async_smem();
                     }
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive(p_full(s));
+                        mbar_arrive(p_full(s, 0));
+                    if (!idle) {
+#pragma unroll
+                        for (int e = 2; e < 4; ++e) {
+                            exps(e);
+                            l = add2(l, part);
+                            tmem_st16(s_at + e * 16, r);
+                        }
+                        tmem_wait_st();
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(p_full(s, 1));
                 }
             }
 
