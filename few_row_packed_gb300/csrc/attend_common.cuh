@@ -80,6 +80,16 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
         : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map)
+{
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(map) : "memory");
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p)
+{
+    asm volatile("prefetch.global.L2 [%0];\n" ::"l"(p) : "memory");
+}
+
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
@@ -167,13 +177,25 @@ __device__ __forceinline__ uint32_t seen32(const AttendParams& p, const Request&
     return see;
 }
 
+// 32 bytes to a 32-byte-aligned address: a whole sector by one thread.
+__device__ __forceinline__ void store32(void* d, const uint32_t* r)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(d), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 // Stores N 16-bit values (packed in pairs) of an output row, as wide as its
 // address allows.
 template <int N>
 __device__ __forceinline__ void store_row(uint16_t* d, const uint32_t* r)
 {
     const uintptr_t a = reinterpret_cast<uintptr_t>(d);
-    if (N % 8 == 0 && (a & 15) == 0) {
+    if (N % 16 == 0 && (a & 31) == 0) {
+#pragma unroll
+        for (int k = 0; k < N / 16; ++k)
+            store32(d + 16 * k, r + 8 * k);
+    } else if (N % 8 == 0 && (a & 15) == 0) {
 #pragma unroll
         for (int k = 0; k < N / 8; ++k)
             reinterpret_cast<uint4*>(d)[k] = make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
@@ -261,26 +283,36 @@ struct Start {
     int r, tile, head;
 };
 
-// Run by one warp of CTA c: at most max_ctas CTAs with min_units each.
+// Run by one warp of CTA c: at most max_ctas CTAs with min_units each.  Few requests
+// have several lanes each, which take their tiles in turn.
 template <typename S>
-__device__ void find_start(const AttendParams& p, int lane, unsigned max_ctas, unsigned min_units,
-                           unsigned c, Start* out)
+__device__ __forceinline__ void find_start(const AttendParams& p, int lane, unsigned max_ctas,
+                                           unsigned min_units, unsigned c, Start* out)
 {
-    auto units_of = [&](int r, Request& q) {
+    int shift = 5;                                       // 2^shift requests at a time
+    while (shift > 0 && p.batch.requests <= 1 << (shift - 1))
+        --shift;
+    const int at_once = 1 << shift, sub = lane >> shift, subs = 32 >> shift;
+    auto units_of = [&](int r, Request& q) {             // of request r + lane % at_once
+        r += lane & (at_once - 1);
         unsigned n = 0;
         if (r < p.batch.requests) {
             q = request_of(p, r);
             const int tiles = tiles_of<S>(p, q);
-            for (int t = 0; t < tiles; ++t)
+            for (int t = sub; t < tiles; t += subs)
                 n += tile_of<S>(p, q, t).units;
         }
+        for (int d = at_once; d < 32; d <<= 1)
+            n += __shfl_xor_sync(0xffffffffu, n, d);
         return n * (unsigned)p.kv.heads;
     };
     Request q, q0;
-    const unsigned v0 = units_of(lane, q0);
-    unsigned total = __reduce_add_sync(0xffffffffu, v0);
-    for (int r0 = 32; r0 < p.batch.requests; r0 += 32)
-        total += __reduce_add_sync(0xffffffffu, units_of(r0 + lane, q));
+    const unsigned v0 = units_of(0, q0);
+    unsigned total = __reduce_add_sync(0xffffffffu, sub == 0 ? v0 : 0u);
+    for (int r0 = at_once; r0 < p.batch.requests; r0 += at_once) {
+        const unsigned v = units_of(r0, q);
+        total += __reduce_add_sync(0xffffffffu, sub == 0 ? v : 0u);
+    }
     const unsigned want = (total + min_units - 1) / min_units;
     const unsigned n = want < max_ctas ? want : max_ctas;
     if (lane == 0) {
@@ -292,36 +324,55 @@ __device__ void find_start(const AttendParams& p, int lane, unsigned max_ctas, u
     const unsigned per = total / n, rem = total - per * n;
     const unsigned first = c * per + min(c, rem);
     unsigned base = 0;
-    for (int r0 = 0; r0 < p.batch.requests; r0 += 32) {
+    for (int r0 = 0; r0 < p.batch.requests; r0 += at_once) {
         unsigned v = v0;
         q = q0;
         if (r0 > 0)
-            v = units_of(r0 + lane, q);
-        unsigned sum = v;
+            v = units_of(r0, q);
+        unsigned sum = sub == 0 ? v : 0u;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const unsigned o = __shfl_up_sync(0xffffffffu, sum, d);
             sum += lane >= d ? o : 0;
         }
         unsigned at = base + sum - v;
-        const bool here = v && at <= first && first - at < v;
-        if (here) {
-            int t = 0;
-            unsigned units = tile_of<S>(p, q, 0).units;
-            while (first - at >= units * (unsigned)p.kv.heads) {
-                at += units * (unsigned)p.kv.heads;
-                units = tile_of<S>(p, q, ++t).units;
-            }
-            const unsigned head = (first - at) / units;
-            out->q = q;
-            out->r = r0 + lane;
-            out->tile = t;
-            out->head = (int)head;
-            out->item = at + head * units;
-        }
+        const unsigned here = __ballot_sync(0xffffffffu, sub == 0 && v && at <= first && first - at < v);
         base += __shfl_sync(0xffffffffu, sum, 31);
-        if (__any_sync(0xffffffffu, here))
-            break;
+        if (!here)
+            continue;
+        // the request is found: its tiles, 32 at a time
+        const int from = __ffs(here) - 1;
+        Request f;
+        f.q0 = __shfl_sync(0xffffffffu, q.q0, from);
+        f.n = __shfl_sync(0xffffffffu, q.n, from);
+        f.kv = __shfl_sync(0xffffffffu, q.kv, from);
+        f.first = __shfl_sync(0xffffffffu, q.first, from);
+        f.keys = __shfl_sync(0xffffffffu, q.keys, from);
+        at = __shfl_sync(0xffffffffu, at, from);
+        const int tiles = tiles_of<S>(p, f);
+        for (int t0 = 0; t0 < tiles; t0 += 32) {
+            const unsigned units = t0 + lane < tiles ? tile_of<S>(p, f, t0 + lane).units : 0;
+            const unsigned w = units * (unsigned)p.kv.heads;
+            unsigned upto = w;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const unsigned o = __shfl_up_sync(0xffffffffu, upto, d);
+                upto += lane >= d ? o : 0;
+            }
+            const unsigned mine = at + upto - w;
+            if (w && mine <= first && first - mine < w) {
+                const unsigned head = (first - mine) / units;
+                out->q = f;
+                out->r = r0 + from;
+                out->tile = t0 + lane;
+                out->head = (int)head;
+                out->item = mine + head * units;
+            }
+            at += __shfl_sync(0xffffffffu, upto, 31);
+            if (at > first)
+                break;
+        }
+        break;
     }
 }
 

@@ -16,13 +16,32 @@ namespace {
 
 constexpr int kWarps = 4;
 
+constexpr int kLook = (kAttendMaxCtas + 31) / 32;
+
 template <int DT, int D>
 __global__ void __launch_bounds__(kWarps * 32)
-    lbv_attend_join_kernel(const __grid_constant__ AttendParams p, int slot_rows)
+    lbv_attend_join_kernel(const __grid_constant__ AttendParams p, int slot_rows, int ctas)
 {
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    const JoinItem it = static_cast<const JoinItem*>(p.items)[blockIdx.x];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // the blockIdx.x-th divided item is the one that starts in CTA c0
+    const JoinItem* items = static_cast<const JoinItem*>(p.items);
+    bool divided[kLook];
+#pragma unroll
+    for (int i = 0; i < kLook; ++i)
+        divided[i] = i * 32 + lane < ctas && __ldcg(&items[i * 32 + lane].rows) > 0;
+    int before = 0, c0 = -1;
+#pragma unroll
+    for (int i = 0; i < kLook; ++i) {
+        const unsigned set = __ballot_sync(0xffffffffu, divided[i]);
+        if (divided[i] && before + __popc(set & ((1u << lane) - 1)) == (int)blockIdx.x)
+            c0 = i * 32 + lane;
+        before += __popc(set);
+    }
+    c0 = __reduce_max_sync(0xffffffffu, c0);
+    if (c0 < 0)
+        return;
+    const JoinItem it = items[c0];
     constexpr int LANES = D / 4;                 // lanes that hold a row
     constexpr int AT_ONCE = 32 / LANES;          // parts a load takes
     const int sub = lane / LANES, d4 = lane % LANES;
@@ -30,33 +49,54 @@ __global__ void __launch_bounds__(kWarps * 32)
     q.q0 = it.q0;
     const size_t slot = (size_t)slot_rows * (D + 2);
     auto part = [&](int k) {
-        return p.partial + (size_t)(2 * ((int)blockIdx.x + k) + (k == 0)) * slot;
+        return p.partial + (size_t)(2 * (c0 + k) + (k == 0)) * slot;
     };
     for (int row = blockIdx.y * kWarps + warp; row < it.rows; row += gridDim.y * kWarps) {
-        float top = -INFINITY;
-        for (int k = lane; k < it.parts; k += 32)
-            top = fmaxf(top, part(k)[slot_rows * D + row]);
+        // the first parts' results, maxima and sums in one round of loads
+        constexpr int AHEAD = 8;
+        float4 first[AHEAD];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j)
+            if (j * AT_ONCE + sub < it.parts)
+                first[j] = __ldcg(reinterpret_cast<const float4*>(part(j * AT_ONCE + sub) + row * D) + d4);
+        float m = -INFINITY, s = 0.f;            // of the lane's part
+        if (lane < it.parts) {
+            m = __ldcg(part(lane) + slot_rows * D + row);
+            s = __ldcg(part(lane) + slot_rows * (D + 1) + row);
+        }
+        float top = m;
+        for (int k = lane + 32; k < it.parts; k += 32)
+            top = fmaxf(top, __ldcg(part(k) + slot_rows * D + row));
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        float sum = 0.f;
+        float w = m == -INFINITY ? 0.f : ex2(m - top), sum = w * s;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](float f, float4 a) {
+            o.x += f * a.x, o.y += f * a.y, o.z += f * a.z, o.w += f * a.w;
+        };
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            const float f = __shfl_sync(0xffffffffu, w, (j * AT_ONCE + sub) & 31);
+            if (j * AT_ONCE + sub < it.parts)
+                add(f, first[j]);
+        }
         for (int k0 = 0; k0 < it.parts; k0 += 32) {
-            const int k = k0 + lane;
-            float w = 0.f;
-            if (k < it.parts) {
-                const float m = part(k)[slot_rows * D + row];
-                w = m == -INFINITY ? 0.f : ex2(m - top);
-                sum += w * part(k)[slot_rows * (D + 1) + row];
+            if (k0 > 0) {
+                const int k = k0 + lane;
+                w = 0.f;
+                if (k < it.parts) {
+                    const float n = __ldcg(part(k) + slot_rows * D + row);
+                    w = n == -INFINITY ? 0.f : ex2(n - top);
+                    sum += w * __ldcg(part(k) + slot_rows * (D + 1) + row);
+                }
             }
             const int n = min(32, it.parts - k0);
 #pragma unroll 8
-            for (int j = 0; j < n; j += AT_ONCE) {
+            for (int j = k0 > 0 ? 0 : AHEAD * AT_ONCE; j < n; j += AT_ONCE) {
                 const float f = __shfl_sync(0xffffffffu, w, j + sub);
-                if (j + sub < n) {
-                    const float4 a = *reinterpret_cast<const float4*>(part(k0 + j + sub) + row * D + d4 * 4);
-                    o.x += f * a.x, o.y += f * a.y, o.z += f * a.z, o.w += f * a.w;
-                }
+                if (j + sub < n)
+                    add(f, __ldcg(reinterpret_cast<const float4*>(part(k0 + j + sub) + row * D) + d4));
             }
         }
 #pragma unroll
@@ -74,9 +114,12 @@ __global__ void __launch_bounds__(kWarps * 32)
 template <int DT, int D>
 cudaError_t launch(const AttendParams& p, int slot_rows, int ctas, cudaStream_t st)
 {
+    // divided items: no more than there are items, or CTAs
+    const int64_t items = ((int64_t)p.batch.tokens * p.group / slot_rows + p.batch.requests) * p.kv.heads;
     cudaLaunchConfig_t cfg = {};
     // CTAs per item: a warp for every row, or for every other one of the larger slots
-    cfg.gridDim = dim3((unsigned)ctas, (unsigned)(slot_rows <= 64 ? slot_rows / kWarps : slot_rows / (2 * kWarps)));
+    cfg.gridDim = dim3((unsigned)(items < ctas ? items : ctas),
+                       (unsigned)(slot_rows <= 64 ? slot_rows / kWarps : slot_rows / (2 * kWarps)));
     cfg.blockDim = dim3(kWarps * 32);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
@@ -84,7 +127,7 @@ cudaError_t launch(const AttendParams& p, int slot_rows, int ctas, cudaStream_t 
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, lbv_attend_join_kernel<DT, D>, p, slot_rows);
+    return cudaLaunchKernelEx(&cfg, lbv_attend_join_kernel<DT, D>, p, slot_rows, ctas);
 }
 
 }  // namespace

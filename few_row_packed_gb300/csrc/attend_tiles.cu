@@ -31,7 +31,7 @@ constexpr int kTile = 128;                       // rows per stream
 constexpr int kRows = 2 * kTile;                 // rows per item
 // Units of an item beside its blocks (a block of two row tiles counts as two
 // units), and the least share of a CTA.
-constexpr int kExtra = 2, kMinUnits = 4;
+constexpr int kExtra = 8, kMinUnits = 12;
 using Items = Shape<kRows, kKeys, kTile, kExtra>;
 constexpr int kThreads = 384;                    // copies and MMAs, then the two streams
 // Registers a thread after the split: 168 * 384 at launch = 88 * 128 + 208 * 256.
@@ -63,14 +63,13 @@ struct Geo {
     static constexpr int STATS = (BARS + NBARS * 8 + 15) / 16 * 16;   // [2][128] m and sums of the streams
     static constexpr int ITEMS = STATS + 2 * kTile * 8;     // ring of items
     static constexpr int WORDS = ITEMS + kItems * 64;       // tensor-memory address
-    static constexpr int BYTES = WORDS + 16;
-    // where the CTA's share begins: read before the streams' first statistics
-    static constexpr int START = STATS;
+    static constexpr int START = WORDS + 16;                // where the CTA's share begins
+    static constexpr int BYTES = START + 64;
     static constexpr int PARTIAL = kRows * (D + 2);         // floats of one partial result
     // tensor memory columns
     static constexpr uint32_t S0 = 0, O0 = 256;             // S of stream s at S0 + 128 s
     static_assert(BARS % 8 == 0 && STATS % 16 == 0 && ITEMS % 16 == 0 && WORDS % 16 == 0, "alignment");
-    static_assert(BYTES <= 227 * 1024 && sizeof(Start) <= 2 * kTile * 8, "shared memory");
+    static_assert(BYTES <= 227 * 1024 && sizeof(Start) <= 64, "shared memory");
 };
 
 // ---- tcgen05 ----
@@ -259,7 +258,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    Start* start = reinterpret_cast<Start*>(smem + G::START);
     uint32_t& tmem_slot = *reinterpret_cast<uint32_t*>(smem + G::WORDS);
     auto bar = [&](int i) { return sbase + G::BARS + i * 8; };
     auto full = [&](int i) { return bar(i); };
@@ -292,8 +290,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (tid == 128)
         static_cast<JoinItem*>(p.items)[blockIdx.x].rows = 0;
-    if (warp == 0)
-        find_start<Items>(p, lane, gridDim.x, kMinUnits, blockIdx.x, start);
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&tmem_slot))
                      : "memory");
@@ -303,9 +299,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    const Start share = *start;
-    const bool work = (int)blockIdx.x < share.ctas;
-    __syncthreads();                                     // its place becomes the statistics'
     bool ok = true;
 
     auto wait = [&](uint32_t b, uint32_t parity) {
@@ -318,12 +311,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         return items[i % kItems];
     };
 
-    if (!work) {
-        // fewer units than CTAs
-    } else if (warp < 4) {
+    if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegsControl));
         if (warp == 0) {
             // ---- copies: K and V of each block in turn ----
+            if (lane == 0) {
+                prefetch_map(&kmap);
+                prefetch_map(&vmap);
+            }
             const int slots = min(64, 1 << p.kv.page_shift);         // rows of a box
             const int boxes = kKeys / slots;
             int n = 0;
@@ -453,22 +448,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait(o_done(1), (np1 - 1) & 1);
         } else if (warp == 2) {
             // ---- the share's items ----
-            Walk<Items> w(p, share, blockIdx.x);
+            Start& start = *reinterpret_cast<Start*>(smem + G::START);
+            find_start<Items>(p, lane, gridDim.x, kMinUnits, blockIdx.x, &start);
+            __syncwarp();
             Item* out = reinterpret_cast<Item*>(smem + G::ITEMS);
-            int slot0 = 0;
-            for (int it = 0;; ++it) {
-                const bool more = w.next();
-                if (it >= kItems)
-                    wait(item_empty(it), (uint32_t)((it / kItems - 1) & 1));
+            if ((int)blockIdx.x >= start.ctas) {             // fewer units than CTAs
                 if (lane == 0) {
-                    const int nb = more ? w.b_last - w.b_first : 0;
-                    out[it % kItems] = {w.q, w.r, w.x.row0, w.x.rows, w.head, w.x.lo, w.x.hi,
-                                        w.key0(w.b_first), nb, slot0, w.first_cta(), w.last_cta()};
-                    mbar_arrive(item_full(it));          // releases the stores
-                    slot0 += 2 * nb;
+                    out[0].nb = 0;
+                    mbar_arrive(item_full(0));
                 }
-                if (!more || !__all_sync(0xffffffffu, ok))
-                    break;
+            } else {
+                Walk<Items> w(p, start, blockIdx.x);
+                int slot0 = 0;
+                for (int it = 0;; ++it) {
+                    const bool more = w.next();
+                    if (it >= kItems)
+                        wait(item_empty(it), (uint32_t)((it / kItems - 1) & 1));
+                    if (lane == 0) {
+                        const int nb = more ? w.b_last - w.b_first : 0;
+                        out[it % kItems] = {w.q, w.r, w.x.row0, w.x.rows, w.head, w.x.lo, w.x.hi,
+                                            w.key0(w.b_first), nb, slot0, w.first_cta(), w.last_cta()};
+                        mbar_arrive(item_full(it));          // releases the stores
+                        slot0 += 2 * nb;
+                    }
+                    // its queries are on the way before the streams ask for them
+                    if (more)
+                        for (int i = lane; i < w.x.rows * (D / 64); i += 32) {
+                            const int row = w.x.row0 + i / (D / 64), tok = row / p.group;
+                            prefetch_l2(p.q + (int64_t)(w.q.q0 + tok) * p.q_token +
+                                        (int64_t)(w.head * p.group + row - tok * p.group) * p.q_head +
+                                        i % (D / 64) * 64);
+                        }
+                    if (!more || !__all_sync(0xffffffffu, ok))
+                        break;
+                }
             }
         }
         __syncwarp();
@@ -680,11 +693,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         r[k] = sum == 0.f ? 0u : pack2<DT>(o[2 * k] * f, o[2 * k + 1] * f);
                     store_row<32>(p.out + tok * p.out_token + (int64_t)head * p.out_head + e * 32, r);
                 } else if (in) {
-                    float4* d = reinterpret_cast<float4*>(slot + item_row * D + e * 32);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        d[k] = sum == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                          : make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t r[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            r[i] = sum == 0.f ? 0u : __float_as_uint(o[8 * k + i]);
+                        store32(slot + item_row * D + e * 32 + 8 * k, r);
+                    }
                 }
             }
             if (in && (dual || s == 0)) {
@@ -698,9 +714,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!whole && tid == 128 && w.c0 == (int)blockIdx.x)
                 static_cast<JoinItem*>(p.items)[w.c0] = {w.q.q0, w.row0, w.rows, w.head,
                                                          w.c1 - w.c0 + 1};
-            // both streams are done reading O and the statistics
             tc_fence_before();
-            named_bar_sync(1, 256);
+            if (!dual)                                   // both streams are done reading O and the statistics
+                named_bar_sync(1, 256);
             if (lane == 0)
                 mbar_arrive(item_empty(it));
         }
