@@ -12,27 +12,28 @@
 // drawn is the first one in index order at which the running sum of the kept
 // weights passes u * total.
 //
-// A row takes one thread-block cluster whose CTAs stage disjoint slices of it
-// in shared memory, so the logits are read from memory once (the bound of a
-// large batch); everything after the first pass works on chip.  Selecting
-// needs no sort of the row:
-//   1. the row's maximum (a cluster barrier);
-//   2. a bound on how far down the kept tokens can reach.  Each thread's own
-//      maximum enters a histogram of (m - l) r in steps of 1/16 (a barrier): the
-//      k-th of these few thousand values is at most the row's k-th, and their
-//      weights sum to no more than the row's above the same logit, so the first
-//      bin that satisfies top-k or top-p on them lies at or below the true cut;
-//   3. the tokens above that bound, a few more than are kept, go in index order
-//      to the first CTA (a barrier), and the other CTAs are done;
-//   4. each of these candidates counts and sums those ranked before it, which
-//      decides whether it is kept, and an index-order running sum gives the
-//      token.  Up to kRanked candidates; a longer list finds tau by a search
-//      over the bits of the (order-preserving) keys, counting and summing above
-//      trial values, two bits a round.
+// A row takes one thread-block cluster, each CTA a slice of it.  Selecting needs
+// one pass over the logits (the bound of a large batch) and no sort:
+//   1. every thread finds the maximum of its logits, the cluster the row's;
+//   2. a bound on how far down the kept tokens can reach.  The thread maxima
+//      enter a histogram of (m - l) r in steps of 1/8: the k-th of these few
+//      thousand values is at most the row's k-th, and their weights sum to no more
+//      than the row's above the same logit, so the first bin that satisfies top-k
+//      or top-p on them lies at or below the true cut;
+//   3. the few threads whose maximum lies above the bound hand it to the first CTA;
+//      those whose next largest does too read their logits again (from L2) and hand
+//      over all above it ("candidates").  The other CTAs are done;
+//   4. it sorts them by rank; a running sum of their weights gives how many are
+//      kept; and sorts these by index, where a running sum gives the token.
 // Where the thread maxima do not reach the cut (a large k, a flat row with a
-// large top-p), step 2 is tried again with all logits, and where the candidates
-// do not fit the list, the search runs over the slices of all CTAs, with a
-// cluster barrier in each round.
+// large top-p), step 2 is tried again with all logits.  Where the candidates do
+// not fit the list, tau is found by a search over the bits of the
+// (order-preserving) keys, counting and summing above trial values, two bits a
+// round, with a cluster barrier in each.  top-p without top-k needs the row's total
+// weight: a second pass over the slice.
+//
+// Nothing of the row stays on chip, so that four CTAs share an SM: while one
+// waits at a barrier, the others' loads keep memory busy.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -45,13 +46,12 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = kThreads;            // one thread per bin
-constexpr int kList = 4096;                // candidates the first CTA can take
-constexpr int kRanked = 384;               // candidates ranked by pairs
+constexpr int kList = 8 * kThreads;        // candidates the first CTA can take
 constexpr int kMaxCluster = 16;
-constexpr float kBinsPerNat = 16.f;
+constexpr float kBinsPerNat = 8.f;
 constexpr float kNegInf = -__builtin_huge_valf();
 
 struct Shared {
@@ -61,12 +61,13 @@ struct Shared {
     uint64_t tops[kMaxCluster];
     uint64_t sums[kWarps];                 // drawn weight of each warp's part
     int counts[kMaxCluster];               // candidates of each CTA
+    int found;                             // of this CTA so far
+    int listed;                            // of all CTAs so far (in the first)
     unsigned scan[kWarps];
     int pick;                              // place of the drawn token
     float pick_prob;
-    uint4 pairs[kRanked];                  // key and weight of the ranked candidates
-    float list_x[kList];                   // a segment for each CTA
-    int list_i[kList];
+    uint64_t list[kList];                  // candidates: key, then the index's complement
+    uint64_t exchange[2][kList];           // of the sort's steps
 };
 
 // Order-preserving key of a logit (-0 made +0 before); -inf has a key above 0.
@@ -74,6 +75,11 @@ __device__ __forceinline__ uint32_t key_of(float x)
 {
     const uint32_t b = __float_as_uint(x);
     return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+
+__device__ __forceinline__ float of_key(uint32_t k)
+{
+    return __uint_as_float(k ^ (k & 0x80000000u ? 0x80000000u : 0xFFFFFFFFu));
 }
 
 // exp((x - top) r) in fp32, every operation rounded once; a token at the
@@ -84,9 +90,16 @@ __device__ __forceinline__ float weight_f(float x, float top, float r)
     return x == kNegInf ? 0.f : expf(z);
 }
 
+// floor(2^40 w) for 0 <= w <= 1: the significand moved to its place by shifts (a
+// conversion to 64 bits takes several times longer).  NaN gives 0.
 __device__ __forceinline__ uint64_t whole(float w)
 {
-    return (uint64_t)__fmul_rn(fmaxf(w, 0.f), 1099511627776.f);   // 2^40, truncated; NaN gives 0
+    const uint32_t b = __float_as_uint(w), s = (b & 0x7FFFFFu) | 0x800000u;
+    const uint32_t d = min(127u - (b >> 23), 63u);     // above 127: wraps, and 63 gives 0
+    const uint32_t hi = s >> 15, lo = s << 17;         // 2^40 for d = 0
+    const uint32_t h = d & 32u ? 0u : hi >> (d & 31u);
+    const uint32_t l = d & 32u ? hi >> (d & 31u) : __funnelshift_r(lo, hi, d);
+    return ((uint64_t)h << 32) | l;
 }
 
 // floor(f t / 2^24) for f <= 2^24
@@ -109,23 +122,15 @@ __device__ __forceinline__ uint64_t shfl_add(uint64_t v)
     return v;
 }
 
-// The tokens a search runs over: a CTA's slice of the row, cluster-wide, or
-// the candidate list of the first CTA alone.
-struct Domain {
-    const float* x;
-    int n;
-    bool wide;
-};
-
 struct Ctx {
     Shared* sh;
     int tid, warp, lane, rank, nctas, round;
 };
 
-// Sums N values over the domain's threads; every thread gets the result.
-// below[] (optional): the sums over the CTAs of lower rank.
+// Sums N values over the CTA's threads, or (wide) the cluster's; every thread
+// gets the result.  below[] (optional): the sums over the CTAs of lower rank.
 template <int N>
-__device__ __forceinline__ void reduce(Ctx& c, bool wide, uint64_t (&v)[N], uint64_t* below = nullptr)
+__device__ __noinline__ void reduce(Ctx& c, bool wide, uint64_t (&v)[N], uint64_t* below = nullptr)
 {
     Shared& sh = *c.sh;
     const int b = c.round++ & 1;
@@ -138,8 +143,10 @@ __device__ __forceinline__ void reduce(Ctx& c, bool wide, uint64_t (&v)[N], uint
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        uint64_t t = c.lane < kWarps ? sh.red[b][c.lane][i] : 0;
-        v[i] = shfl_add(t);
+        v[i] = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+            v[i] += sh.red[b][w][i];
     }
     if (wide) {
         cg::cluster_group cl = cg::this_cluster();
@@ -168,28 +175,101 @@ __device__ __forceinline__ void reduce(Ctx& c, bool wide, uint64_t (&v)[N], uint
     }
 }
 
-// The largest key t for which test(sums of f over the tokens with key >= t)
-// holds; it holds at 0.  f(x) is a count or a weight, test is monotone in t.
-template <typename F, typename Test>
-__device__ __forceinline__ uint32_t search(Ctx& c, const Domain& d, F f, Test test)
+template <int DT>
+__device__ __forceinline__ float to_f32(uint32_t bits)     // of one element
 {
-    uint32_t t = 0;
-    for (int bit = 30; bit >= 0; bit -= 2) {
-        uint64_t v[3] = {0, 0, 0};
-        const uint32_t t1 = t | (1u << bit), t2 = t | (2u << bit), t3 = t | (3u << bit);
-        for (int i = c.tid; i < d.n; i += kThreads) {
-            const uint32_t k = key_of(d.x[i]);
-            if (k >= t1) {
-                const uint64_t w = f(d.x[i]);
-                v[0] += w;
-                v[1] += k >= t2 ? w : 0;
-                v[2] += k >= t3 ? w : 0;
-            }
-        }
-        reduce<3>(c, d.wide, v);
-        t = test(t3, v[2]) ? t3 : test(t2, v[1]) ? t2 : test(t1, v[0]) ? t1 : t;
+    if constexpr (DT == LBV_F32)
+        return __uint_as_float(bits);
+    else if constexpr (DT == LBV_F16)
+        return __half2float(__ushort_as_half((uint16_t)bits));
+    else
+        return __uint_as_float(bits << 16);
+}
+
+// A CTA's slice of the row: masked logits and NaN read as -inf, -0 as +0.
+template <int DT>
+struct Slice {
+    static constexpr int SIZE = DT == LBV_F32 ? 4 : 2;
+    const unsigned char* row;              // its first element
+    const uint32_t* words;                 // its mask words, or NULL
+    int n;
+    // a logit as the search sees it; `allowed`: its mask bit
+    static __device__ __forceinline__ float clean(float v, bool allowed)
+    {
+        v = __fadd_rn(v, 0.f);
+        return v != v || !allowed ? kNegInf : v;
     }
-    return t;
+    __device__ __forceinline__ float get(int i) const
+    {
+        const uint32_t b = SIZE == 4 ? __ldg(reinterpret_cast<const uint32_t*>(row) + i)
+                                     : __ldg(reinterpret_cast<const uint16_t*>(row) + i);
+        return clean(to_f32<DT>(b), !words || ((__ldg(words + (i >> 5)) >> (i & 31)) & 1u));
+    }
+    // mask bits of logits i to last (eight of them at most)
+    __device__ __forceinline__ uint32_t allowed(int i, int last) const
+    {
+        return words ? __funnelshift_r(__ldg(words + (i >> 5)), __ldg(words + (last >> 5)), i & 31) : ~0u;
+    }
+};
+
+// Calls f(value, index) for the thread's logits of the slice, indexes ascending:
+// 16-byte loads between the first and the last aligned address, kAhead of them
+// in flight.  The loop keeps one copy of f a vector (AT_ONCE of its elements at a
+// time): a row visits each pass but a few times, and fetching unrolled code from
+// L2 took longer than running it.
+constexpr int kAhead = 4;
+
+template <int AT_ONCE, int DT, typename F>
+__device__ __forceinline__ void each(const Slice<DT>& s, int tid, F f)
+{
+    constexpr int SIZE = Slice<DT>::SIZE, E = 16 / SIZE;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(s.row);
+    const int head = min(s.n, (int)(((16 - (a & 15)) & 15) / SIZE));
+    const int body = (s.n - head) / E, tail = head + body * E;
+    const uint4* v = reinterpret_cast<const uint4*>(a + head * SIZE);
+    uint4 w[kAhead];
+    uint32_t ok[kAhead];
+    auto load = [&](int i, uint4& x, uint32_t& m) {
+        x = make_uint4(0u, 0u, 0u, 0u);
+        m = 0;
+        if (i < body) {
+            x = __ldg(v + i);
+            m = s.allowed(head + i * E, head + i * E + E - 1);
+        }
+    };
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+        load(tid + u * kThreads, w[u], ok[u]);
+    if (tid < head)
+        f(s.get(tid), tid);
+#pragma unroll 1
+    for (int i = tid; i < body; i += kThreads) {
+        const uint32_t q[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+        const uint32_t m = ok[0];
+#pragma unroll
+        for (int u = 0; u + 1 < kAhead; ++u) {
+            w[u] = w[u + 1];
+            ok[u] = ok[u + 1];
+        }
+        load(i + kAhead * kThreads, w[kAhead - 1], ok[kAhead - 1]);
+        const int d = head + i * E;
+#pragma unroll 1
+        for (int e0 = 0; e0 < E; e0 += AT_ONCE)
+#pragma unroll
+            for (int k = 0; k < AT_ONCE; ++k) {
+                const int e = e0 + k;
+                uint32_t b;
+                if constexpr (DT == LBV_F32) {
+                    b = AT_ONCE == 4 ? q[k] : e < 2 ? (e & 1 ? q[1] : q[0]) : (e & 1 ? q[3] : q[2]);
+                } else {
+                    const uint32_t r = AT_ONCE == 8 ? q[k / 2] : e < 4 ? (e < 2 ? q[0] : q[1]) : (e < 6 ? q[2] : q[3]);
+                    b = e & 1 ? r >> 16 : r & 0xFFFFu;
+                }
+                f(s.clean(to_f32<DT>(b), (m >> e) & 1u), d + e);
+            }
+    }
+    if (tail + tid < s.n)                  // fewer than E of them
+        f(s.get(tail + tid), tail + tid);
 }
 
 struct Row {
@@ -204,49 +284,68 @@ struct Kept {
     uint64_t ties;
 };
 
-__device__ Kept select(Ctx& c, const Domain& d, const Row& row, bool have_total, uint64_t total)
+// The largest key t for which test(t, sum of f over the tokens with key >= t)
+// holds; it holds at 0.  f(x) is a count or a weight, test is monotone in t.
+template <typename D, typename F, typename Test>
+__device__ __forceinline__ uint32_t search(Ctx& c, const D& d, F f, Test test)
+{
+    uint32_t t = 0;
+    for (int bit = 30; bit >= 0; bit -= 2) {
+        uint64_t s1 = 0, s2 = 0, s3 = 0;
+        const uint32_t t1 = t | (1u << bit), t2 = t | (2u << bit), t3 = t | (3u << bit);
+        each<2>(d, c.tid, [&](float x, int) {
+            const uint32_t k = key_of(x);
+            if (k >= t1) {
+                const uint64_t w = f(x);
+                s1 += w;
+                s2 += k >= t2 ? w : 0;
+                s3 += k >= t3 ? w : 0;
+            }
+        });
+        uint64_t v[3] = {s1, s2, s3};
+        reduce<3>(c, true, v);
+        t = test(t3, v[2]) ? t3 : test(t2, v[1]) ? t2 : test(t1, v[0]) ? t1 : t;
+    }
+    return t;
+}
+
+// tau and its ties by search.  total: the weight of the whole row (without top-k).
+template <typename D>
+__device__ __noinline__ Kept select(Ctx& c, const D& d, const Row& row, uint64_t total)
 {
     Kept kept = {0u, ~0ull};
     uint32_t tau_k = 0;
+    auto weight = [&](float x) { return whole(weight_f(x, row.top, row.filter_r)); };
     if (row.k > 0) {
         const uint64_t k = (uint64_t)row.k;
         tau_k = search(c, d, [](float) { return (uint64_t)1; },
                        [&](uint32_t, uint64_t n) { return n >= k; });
-        // its ties, and what lies above
-        uint64_t v[2] = {0, 0};
-        for (int i = c.tid; i < d.n; i += kThreads)
-            if (key_of(d.x[i]) > tau_k) {
-                v[0] += 1;
-                v[1] += whole(weight_f(d.x[i], row.top, row.filter_r));
+        // what lies above it
+        uint64_t n = 0, sum = 0;
+        each<2>(d, c.tid, [&](float x, int) {
+            if (key_of(x) > tau_k) {
+                n += 1;
+                sum += weight(x);
             }
-        reduce<2>(c, d.wide, v);
+        });
+        uint64_t v[2] = {n, sum};
+        reduce<2>(c, true, v);
         kept.tau = tau_k;
         kept.ties = k - v[0];
-        // fewer than k tokens may be left above a masked one: its weight is 0
-        const uint32_t b = tau_k ^ (tau_k & 0x80000000u ? 0x80000000u : 0xFFFFFFFFu);
-        total = v[1] + kept.ties * whole(weight_f(__uint_as_float(b), row.top, row.filter_r));
-    } else if (!have_total) {
-        uint64_t v[1] = {0};
-        for (int i = c.tid; i < d.n; i += kThreads)
-            v[0] += whole(weight_f(d.x[i], row.top, row.filter_r));
-        reduce<1>(c, d.wide, v);
-        total = v[0];
+        total = v[1] + kept.ties * weight(of_key(tau_k));    // a masked tau weighs 0
     }
     if (row.top_p < 1.f) {
         const uint64_t limit = part(fraction24(row.top_p), total);
         if (limit == 0)
             return Kept{key_of(row.top), 1};
-        auto weight = [&](float x) { return whole(weight_f(x, row.top, row.filter_r)); };
         const uint32_t tau = search(c, d, weight, [&](uint32_t t, uint64_t s) {
             return t <= tau_k || s >= limit;
         });
-        uint64_t v[1] = {0};
-        for (int i = c.tid; i < d.n; i += kThreads)
-            if (key_of(d.x[i]) > tau)
-                v[0] += weight(d.x[i]);
-        reduce<1>(c, d.wide, v);
-        const uint32_t b = tau ^ (tau & 0x80000000u ? 0x80000000u : 0xFFFFFFFFu);
-        const uint64_t w = weight(__uint_as_float(b));
+        uint64_t sum = 0;
+        each<2>(d, c.tid, [&](float x, int) { sum += key_of(x) > tau ? weight(x) : 0; });
+        uint64_t v[1] = {sum};
+        reduce<1>(c, true, v);
+        const uint64_t w = weight(of_key(tau));
         const uint64_t j = w ? (limit - v[0] + w - 1) / w : 1;
         kept.ties = tau == tau_k && j > kept.ties ? kept.ties : j;
         kept.tau = tau;
@@ -257,7 +356,8 @@ __device__ Kept select(Ctx& c, const Domain& d, const Row& row, bool have_total,
 // Draws from the kept tokens of the domain in index order.  Returns the place
 // in the domain, or -1 where another CTA's slice holds it; *prob its
 // probability among the kept ones.
-__device__ int draw(Ctx& c, const Domain& d, const Row& row, const Kept& kept, float* prob)
+template <typename D>
+__device__ __noinline__ int draw(Ctx& c, const D& d, const Row& row, const Kept& kept, float* prob)
 {
     Shared& sh = *c.sh;
     const int groups = (d.n + 31) / 32, per = (groups + kWarps - 1) / kWarps;
@@ -269,14 +369,14 @@ __device__ int draw(Ctx& c, const Domain& d, const Row& row, const Kept& kept, f
         unsigned mine = 0;
         for (int g = g0; g < g1; ++g) {
             const int i = g * 32 + c.lane;
-            mine += i < d.n && key_of(d.x[i]) == kept.tau;
+            mine += i < d.n && key_of(d.get(i)) == kept.tau;
         }
         mine = __reduce_add_sync(0xffffffffu, mine);
         __syncthreads();
         if (c.lane == 0)
             sh.scan[c.warp] = mine;
         uint64_t v[1] = {c.lane == 0 ? mine : 0u}, lo[1];
-        reduce<1>(c, d.wide, v, lo);       // its barrier orders the scan array
+        reduce<1>(c, true, v, lo);      // its barrier orders the scan array
         tie_base = lo[0];
         for (int w = 0; w < c.warp; ++w)
             tie_base += sh.scan[w];
@@ -284,13 +384,14 @@ __device__ int draw(Ctx& c, const Domain& d, const Row& row, const Kept& kept, f
     // visits the warp's tokens in index order: f(place, weight) by all lanes
     auto visit = [&](auto f) {
         uint64_t ties = tie_base;
+#pragma unroll 4
         for (int g = g0; g < g1; ++g) {
             const int i = g * 32 + c.lane;
-            const float x = i < d.n ? d.x[i] : kNegInf;
+            const float x = i < d.n ? d.get(i) : kNegInf;
             const uint32_t k = key_of(x);
             const bool tie = i < d.n && k == kept.tau;
             const unsigned tied = __ballot_sync(0xffffffffu, tie);
-            bool in = i < d.n && (k > kept.tau || (tie && ties + __popc(tied & before) < kept.ties));
+            const bool in = i < d.n && (k > kept.tau || (tie && ties + __popc(tied & before) < kept.ties));
             ties += __popc(tied);
             uint64_t w = 0;
             if (in && weight_f(x, row.top, row.filter_r) >= row.min_p)
@@ -308,7 +409,7 @@ __device__ int draw(Ctx& c, const Domain& d, const Row& row, const Kept& kept, f
     if (c.tid == 0)
         sh.pick = -1;
     uint64_t v[1] = {c.lane == 0 ? sum : 0}, lo[1];
-    reduce<1>(c, d.wide, v, lo);
+    reduce<1>(c, true, v, lo);
     const uint64_t total = v[0];
     uint64_t at = lo[0];
     for (int w = 0; w < c.warp; ++w)
@@ -331,8 +432,7 @@ __device__ int draw(Ctx& c, const Domain& d, const Row& row, const Kept& kept, f
             }
             if (c.lane == __ffs(past) - 1) {
                 sh.pick = i;
-                *prob = __fdiv_rn(__ull2float_rn(w), __ull2float_rn(total));
-                sh.pick_prob = *prob;
+                sh.pick_prob = __fdiv_rn(__ull2float_rn(w), __ull2float_rn(total));
             }
             return true;
         });
@@ -342,216 +442,162 @@ __device__ int draw(Ctx& c, const Domain& d, const Row& row, const Kept& kept, f
     return sh.pick;
 }
 
-// Writes the slice's tokens of logit >= cut in index order to to_x, to_i (`cap`
-// of them at most) and returns how many there are.
-__device__ int collect(Ctx& c, const float* x, int n, float cut, int begin, int cap, float* to_x,
-                       int* to_i)
+// Sorts list[0 .. 256 E) (or a smaller power of two n2, E = 1) in descending order,
+// bitonic, E elements a thread in registers (thread t: t, t + 256, ...): exchanges
+// over strides below 32 by shuffles, over 256 and more within the thread, and the
+// three between through shared memory.
+template <int E>
+__device__ __noinline__ void sort_list(Shared& sh, int n2, int tid)
 {
-    Shared& sh = *c.sh;
-    // 128 logits a step: four neighbours a lane
-    const int steps = (n + 127) / 128, per = (steps + kWarps - 1) / kWarps;
-    const int g0 = min(c.warp * per, steps), g1 = min(g0 + per, steps);
-    const unsigned before = (1u << c.lane) - 1;
-    auto hits = [&](int g, float (&v)[4], unsigned (&b)[4]) {
-        const int i = g * 128 + c.lane * 4;
-        if (i + 3 < n) {
-            const float4 q = *reinterpret_cast<const float4*>(x + i);
-            v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
-        } else {
+    uint64_t v[E];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                v[e] = i + e < n ? x[i + e] : kNegInf;
-        }
-        const bool any = (v[0] >= cut && i < n) || (v[1] >= cut && i + 1 < n) ||
-                         (v[2] >= cut && i + 2 < n) || (v[3] >= cut && i + 3 < n);
-        if (!__any_sync(0xffffffffu, any))
-            return 0;
-        int k = 0;
+    for (int q = 0; q < E; ++q)
+        v[q] = E > 1 || tid < n2 ? sh.list[tid + q * kThreads] : 0;
+    int half = 0;
+#pragma unroll 1
+    for (int size = 2; size <= n2; size *= 2)
+#pragma unroll 1
+        for (int stride = size / 2; stride > 0; stride /= 2) {
+            uint64_t o[E];
+            if (stride < 32) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            b[e] = __ballot_sync(0xffffffffu, v[e] >= cut && i + e < n);
-            k += __popc(b[e]);
-        }
-        return k;
-    };
-    float v[4];
-    unsigned b[4];
-    unsigned found = 0;
-    for (int g = g0; g < g1; ++g)
-        found += hits(g, v, b);
-    if (c.lane == 0)
-        sh.scan[c.warp] = found;
-    __syncthreads();
-    int at = 0, all = 0;
-    for (int w = 0; w < kWarps; ++w) {
-        at += w < c.warp ? sh.scan[w] : 0;
-        all += sh.scan[w];
-    }
-    if (all <= cap && found)
-        for (int g = g0; g < g1; ++g) {
-            const int k = hits(g, v, b);
-            if (!k)
-                continue;
-            int to = at + __popc(b[0] & before) + __popc(b[1] & before) + __popc(b[2] & before) +
-                     __popc(b[3] & before);
+                for (int q = 0; q < E; ++q)
+                    o[q] = __shfl_xor_sync(0xffffffffu, v[q], stride);
+            } else if (E == 1 || stride < kThreads) {
+                uint64_t* x = sh.exchange[half];
+                half ^= 1;                         // one barrier a step
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if ((b[e] >> c.lane) & 1u) {
-                    to_x[to] = v[e];
-                    to_i[to] = begin + g * 128 + c.lane * 4 + e;
-                    ++to;
-                }
-            at += k;
-        }
-    return all;
-}
-
-// Draws from n <= kRanked candidates in index order, one a thread (list place
-// `at`, -1: none): what is ranked before a candidate decides whether it is kept.
-__device__ void rank_and_draw(Ctx& c, const Row& row, bool by_sum, uint64_t total, int n, int at,
-                              const SampleParams& p, int m)
-{
-    Shared& sh = *c.sh;
-    const bool in = c.tid < n;
-    const float x = in ? sh.list_x[at] : kNegInf;
-    const int index = in ? sh.list_i[at] : 0;
-    const uint32_t key = key_of(x);
-    const float wf = weight_f(x, row.top, row.filter_r);
-    const uint64_t w = in ? whole(wf) : 0;
-    if (in)
-        sh.pairs[c.tid] = make_uint4(key, (uint32_t)w, (uint32_t)(w >> 32), 0u);
-    __syncthreads();
-    unsigned rank = 0;
-    uint64_t ahead = 0;
-    if (c.warp * 32 < n) {
-#pragma unroll 4
-        for (int j = 0; j < n; ++j) {
-            const uint4 o = sh.pairs[j];
-            if (o.x > key || (o.x == key && j < c.tid)) {
-                ++rank;
-                ahead += ((uint64_t)o.z << 32) | o.y;
+                for (int q = 0; q < E; ++q)
+                    x[tid + q * kThreads] = v[q];
+                __syncthreads();
+#pragma unroll
+                for (int q = 0; q < E; ++q)
+                    o[q] = x[(tid ^ stride) + q * kThreads];
+            } else {
+#pragma unroll
+                for (int q = 0; q < E; ++q)
+                    o[q] = stride == kThreads       ? v[q ^ (E > 1 ? 1 : 0)]
+                           : stride == 2 * kThreads ? v[q ^ (E > 2 ? 2 : 0)]
+                                                    : v[q ^ (E > 4 ? 4 : 0)];
+            }
+#pragma unroll
+            for (int q = 0; q < E; ++q) {
+                const int i = tid + q * kThreads;
+                const bool larger = ((i & stride) == 0) == ((i & size) == 0);
+                v[q] = (v[q] > o[q]) == larger ? v[q] : o[q];
             }
         }
-    }
-    const bool by_rank = row.k > 0;
-    bool keep = in && (!by_rank || rank < (unsigned)row.k);
-    if (by_sum) {
-        if (by_rank) {
-            uint64_t v[1] = {keep ? w : 0};
-            reduce<1>(c, false, v);
-            total = v[0];
-        }
-        keep = keep && (rank == 0 || ahead < part(fraction24(row.top_p), total));
-    }
-    keep = keep && wf >= row.min_p;
-    const uint64_t dw = keep ? whole(weight_f(x, row.top, row.draw_r)) : 0;
-    uint64_t upto = dw;
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < E; ++q)
+        if (E > 1 || tid < n2)
+            sh.list[tid + q * kThreads] = v[q];
+    __syncthreads();
+}
+
+__device__ __forceinline__ void sort_list(Shared& sh, int n2, int tid)
+{
+    if (n2 <= kThreads)
+        sort_list<1>(sh, n2, tid);
+    else if (n2 == 2 * kThreads)
+        sort_list<2>(sh, n2, tid);
+    else if (n2 == 4 * kThreads)
+        sort_list<4>(sh, n2, tid);
+    else
+        sort_list<8>(sh, n2, tid);
+}
+
+__device__ __forceinline__ int power_above(int n)
+{
+    return n <= 2 ? 2 : 1 << (32 - __clz(n - 1));
+}
+
+// The block's sum of v, and in `before` that of the threads before this one.
+__device__ __noinline__ uint64_t block_scan(Ctx& c, uint64_t v, uint64_t& before)
+{
+    uint64_t upto = v;
 #pragma unroll
     for (int s = 1; s < 32; s <<= 1) {
         const uint64_t o = __shfl_up_sync(0xffffffffu, upto, s);
         upto += c.lane >= s ? o : 0;
     }
+    __syncthreads();
     if (c.lane == 31)
-        sh.sums[c.warp] = upto;
+        c.sh->sums[c.warp] = upto;
     __syncthreads();
     uint64_t all = 0, below = 0;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) {
         below = i == c.warp ? all : below;
-        all += sh.sums[i];
+        all += c.sh->sums[i];
     }
-    upto += below;
+    before = below + upto - v;
+    return all;
+}
+
+// Draws from the n candidates of the list, of which every kept token is one.
+// total: the weight of the whole row (without top-k).
+__device__ __forceinline__ void draw_listed(Ctx& c, const Row& row, bool by_sum, uint64_t total, int n,
+                                            const SampleParams& p, int m)
+{
+    Shared& sh = *c.sh;
+    uint64_t* list = sh.list;
+    int n2 = power_above(n);
+    for (int i = n + c.tid; i < n2; i += kThreads)
+        list[i] = 0;
+    __syncthreads();
+    sort_list(sh, n2, c.tid);
+    // ---- how many are kept: a prefix of the ranking ----
+    const int most = row.k > 0 ? min(row.k, n) : n;
+    int per = (most + kThreads - 1) / kThreads, i0 = c.tid * per, i1 = min(i0 + per, most);
+    uint64_t limit = ~0ull, at = 0;
+    if (by_sum) {
+        uint64_t mine = 0;
+        for (int i = i0; i < i1; ++i)
+            mine += whole(weight_f(of_key((uint32_t)(list[i] >> 32)), row.top, row.filter_r));
+        const uint64_t all = block_scan(c, mine, at);
+        limit = part(fraction24(row.top_p), row.k > 0 ? all : total);
+    }
+    int kept = 0;
+    for (int i = i0; i < i1; ++i) {
+        const float w = weight_f(of_key((uint32_t)(list[i] >> 32)), row.top, row.filter_r);
+        kept += (i == 0 || at < limit) && w >= row.min_p;
+        at += by_sum ? whole(w) : 0;
+    }
+    uint64_t unused;
+    kept = (int)block_scan(c, (uint64_t)kept, unused);
+    // ---- these by index ----
+    n2 = power_above(kept);
+    __syncthreads();
+    for (int i = c.tid; i < n2; i += kThreads)
+        list[i] = i < kept ? (list[i] << 32) | (list[i] >> 32) : 0;
+    __syncthreads();
+    sort_list(sh, n2, c.tid);
+    per = (kept + kThreads - 1) / kThreads, i0 = c.tid * per, i1 = min(i0 + per, kept);
+    uint64_t mine = 0;
+    for (int i = i0; i < i1; ++i)
+        mine += whole(weight_f(of_key((uint32_t)list[i]), row.top, row.draw_r));
+    const uint64_t all = block_scan(c, mine, at);
     uint32_t f = fraction24(row.u);
     f = f > 16777215u ? 16777215u : f;
     const uint64_t target = part(f, all);
-    if (upto > target && upto - dw <= target) {
-        p.token[m] = index;
-        if (p.prob)
-            p.prob[m] = __fdiv_rn(__ull2float_rn(dw), __ull2float_rn(all));
-    }
-}
-
-template <int DT>
-__device__ __forceinline__ float load1(const void* p, int64_t i)
-{
-    if constexpr (DT == LBV_F32)
-        return static_cast<const float*>(p)[i];
-    else if constexpr (DT == LBV_F16)
-        return __half2float(__ushort_as_half(static_cast<const uint16_t*>(p)[i]));
-    else
-        return __bfloat162float(__ushort_as_bfloat16(static_cast<const uint16_t*>(p)[i]));
-}
-
-// The thread's largest logit so far and its index in the slice (the first of
-// equal ones, as the thread's indices ascend).
-struct Best {
-    float x = kNegInf;
-    int i = -1;
-};
-
-// Copies n logits from element `at` on into shared memory as fp32, masked ones
-// and NaN as -inf, and finds the thread's maximum: 16-byte loads between the
-// first and the last aligned address.
-template <int DT>
-__device__ __forceinline__ Best stage(const void* src, int64_t at, int n, const uint32_t* words,
-                                      float* x, int tid)
-{
-    constexpr int E = DT == LBV_F32 ? 4 : 8;           // elements of 16 bytes
-    constexpr int SIZE = 16 / E;
-    Best best;
-    auto put = [&](int i, float v) {
-        v = __fadd_rn(v, 0.f);                         // -0 becomes +0
-        const bool out = v != v || (words && !((words[i >> 5] >> (i & 31)) & 1u));
-        v = out ? kNegInf : v;
-        x[i] = v;
-        if (v > best.x) {
-            best.x = v;
-            best.i = i;
-        }
-    };
-    const uintptr_t a = reinterpret_cast<uintptr_t>(src) + (uintptr_t)at * SIZE;
-    const int head = min(n, (int)(((16 - (a & 15)) & 15) / SIZE));
-    const int body = (n - head) / E;
-    if (tid < head)
-        put(tid, load1<DT>(src, at + tid));
-    const uint4* v = reinterpret_cast<const uint4*>(a + head * SIZE);
-    constexpr int U = 8;
-    for (int i = tid; i < body; i += U * kThreads) {
-        uint4 w[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (i + u * kThreads < body)
-                w[u] = __ldcs(v + i + u * kThreads);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (i + u * kThreads < body) {
-                const int d = head + (i + u * kThreads) * E;
-                const uint32_t q[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if constexpr (DT == LBV_F32) {
-                        put(d + e, __uint_as_float(q[e]));
-                    } else if constexpr (DT == LBV_F16) {
-                        put(d + 2 * e, __half2float(__ushort_as_half((uint16_t)q[e])));
-                        put(d + 2 * e + 1, __half2float(__ushort_as_half((uint16_t)(q[e] >> 16))));
-                    } else {
-                        put(d + 2 * e, __uint_as_float(q[e] << 16));
-                        put(d + 2 * e + 1, __uint_as_float(q[e] & 0xFFFF0000u));
-                    }
-                }
+    if (at <= target && target < at + mine)
+        for (int i = i0; i < i1; ++i) {
+            const uint64_t w = whole(weight_f(of_key((uint32_t)list[i]), row.top, row.draw_r));
+            if (at <= target && target < at + w) {
+                p.token[m] = (int)(0xFFFFFFFFu - (uint32_t)(list[i] >> 32));
+                if (p.prob)
+                    p.prob[m] = __fdiv_rn(__ull2float_rn(w), __ull2float_rn(all));
             }
-    }
-    for (int i = head + body * E + tid; i < n; i += kThreads)
-        put(i, load1<DT>(src, at + i));
-    return best;
+            at += w;
+        }
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kThreads, 2) lbv_sample_kernel(const __grid_constant__ SampleParams p)
+__global__ void __launch_bounds__(kThreads, 4) lbv_sample_kernel(const __grid_constant__ SampleParams p)
 {
     extern __shared__ __align__(16) unsigned char smem[];
     Shared& sh = *reinterpret_cast<Shared*>(smem);
-    float* x = reinterpret_cast<float*>(smem + sizeof(Shared));
     cg::cluster_group cl = cg::this_cluster();
     Ctx c;
     c.sh = &sh;
@@ -563,8 +609,12 @@ __global__ void __launch_bounds__(kThreads, 2) lbv_sample_kernel(const __grid_co
     c.round = 0;
     const int m = blockIdx.x / p.ctas;
     const int begin = min(c.rank * p.slice, p.N);
-    const int n = min(p.slice, p.N - begin);
 
+    Slice<DT> slice;
+    slice.n = min(p.slice, p.N - begin);
+    slice.row = static_cast<const unsigned char*>(p.logits) +
+                ((int64_t)m * p.ld + begin) * Slice<DT>::SIZE;
+    slice.words = p.mask ? p.mask + (int64_t)m * p.mask_ld + begin / 32 : nullptr;
     Row row;
     const float t = p.temperature ? p.temperature[m] : 1.f;
     row.u = p.u[m];
@@ -577,13 +627,20 @@ __global__ void __launch_bounds__(kThreads, 2) lbv_sample_kernel(const __grid_co
 
     cl.barrier_arrive();                               // waited for before the first remote store
 
-    // ---- the slice, masked, and the row's first maximum ----
+    // ---- the thread's and the row's first maximum ----
+    float high = kNegInf, next = kNegInf;              // the largest logit, the next one
+    int high_at = 0;
+    each<DT == LBV_F32 ? 4 : 8>(slice, c.tid, [&](float v, int i) {
+        next = fmaxf(next, fminf(v, high));
+        high_at = v > high ? i : high_at;
+        high = fmaxf(high, v);
+    });
     sh.hist[c.tid] = 0;
-    const Best mine = stage<DT>(p.logits, (int64_t)m * p.ld + begin, n,
-                                p.mask ? p.mask + (int64_t)m * p.mask_ld + begin / 32 : nullptr, x, c.tid);
+    if (c.tid == 0)
+        sh.found = sh.listed = 0;
     uint64_t best = 0;
-    if (n > 0)       // a row of -inf has a key above 0 too
-        best = ((uint64_t)key_of(mine.x) << 32) | (0xFFFFFFFFu - (uint32_t)(begin + mine.i));
+    if (slice.n > 0)                                   // a row of -inf has a key above 0 too
+        best = ((uint64_t)key_of(high) << 32) | (0xFFFFFFFFu - (uint32_t)(begin + high_at));
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) {
         const uint64_t o = __shfl_xor_sync(0xffffffffu, best, s);
@@ -595,6 +652,7 @@ __global__ void __launch_bounds__(kThreads, 2) lbv_sample_kernel(const __grid_co
     cl.barrier_wait();
     if (c.tid < c.nctas) {
         uint64_t b = 0;
+#pragma unroll
         for (int w = 0; w < kWarps; ++w)
             b = sh.red[0][w][0] > b ? sh.red[0][w][0] : b;
         cl.map_shared_rank(&sh, c.tid)->tops[c.rank] = b;
@@ -603,8 +661,7 @@ __global__ void __launch_bounds__(kThreads, 2) lbv_sample_kernel(const __grid_co
     best = 0;
     for (int r = 0; r < c.nctas; ++r)
         best = sh.tops[r] > best ? sh.tops[r] : best;
-    const uint32_t kb = (uint32_t)(best >> 32);
-    row.top = __uint_as_float(kb ^ (kb & 0x80000000u ? 0x80000000u : 0xFFFFFFFFu));
+    row.top = of_key((uint32_t)(best >> 32));
     const int first = (int)(0xFFFFFFFFu - (uint32_t)best);
     if (best == 0 || row.top == kNegInf || greedy) {   // nothing allowed, or the maximum itself
         if (c.rank == 0 && c.tid == 0) {
@@ -616,45 +673,52 @@ __global__ void __launch_bounds__(kThreads, 2) lbv_sample_kernel(const __grid_co
         return;
     }
 
-    Domain d = {x, n, true};
     Kept kept = {0u, ~0ull};
     const bool by_rank = row.k > 0 && row.k < p.N, by_sum = row.top_p < 1.f;
     row.k = by_rank ? row.k : 0;
+    uint64_t total = 0;
     if (by_rank || by_sum) {
         const float scale = row.filter_r * kBinsPerNat;
         auto bin_of = [&](float v) {                   // bin 0 holds the maximum
             const float b = v == row.top ? 0.f : (row.top - v) * scale;
             return b < (float)(kBins - 1) ? (int)b : kBins - 1;
         };
-        uint64_t v[1] = {0}, total = 0;
-        bool listed = false;
-        for (int all = 0; all < 2 && !listed; ++all) {
+        Shared* to = cl.map_shared_rank(&sh, 0);
+        for (int all = 0; all < 2; ++all) {
             // ---- the histogram, and with it (once) the row's weight ----
             if (all == 0) {
-                const int b = bin_of(mine.x);
+                const int b = bin_of(high);
                 if (b < kBins - 1)
                     atomicAdd(&sh.hist[b], 1u);
-                if (!by_rank)
-                    for (int i = c.tid; i < n; i += kThreads)
-                        v[0] += whole(weight_f(x[i], row.top, row.filter_r));
-                reduce<1>(c, true, v);                 // orders the histograms too
-                total = v[0];
+                if (by_rank) {
+                    __syncthreads();
+                    cl.sync();
+                } else {
+                    uint64_t sum = 0;
+                    each<DT == LBV_F32 ? 4 : 8>(slice, c.tid, [&](float x, int) {
+                        sum += whole(weight_f(x, row.top, row.filter_r));
+                    });
+                    uint64_t v[1] = {sum};
+                    reduce<1>(c, true, v);             // orders the histograms too
+                    total = v[0];
+                }
             } else {
                 cl.sync();                             // the first one has been read
                 sh.hist[c.tid] = 0;
+                if (c.tid == 0)
+                    sh.found = sh.listed = 0;
                 __syncthreads();
-                for (int i = c.tid; i < n; i += kThreads) {
-                    const int b = bin_of(x[i]);
+                each<2>(slice, c.tid, [&](float x, int) {
+                    const int b = bin_of(x);
                     if (b < kBins - 1)
                         atomicAdd(&sh.hist[b], 1u);
-                }
+                });
                 cl.sync();
             }
-            unsigned h[kMaxCluster];
+            unsigned h[kMaxCluster], here = 0;
 #pragma unroll
             for (int r = 0; r < kMaxCluster; ++r)
                 h[r] = r < c.nctas ? cl.map_shared_rank(&sh, r)->hist[c.tid] : 0u;
-            unsigned here = 0;
 #pragma unroll
             for (int r = 0; r < kMaxCluster; ++r)
                 here += h[r];
@@ -690,56 +754,38 @@ __global__ void __launch_bounds__(kThreads, 2) lbv_sample_kernel(const __grid_co
             // ---- the candidates: all logits down to a little below the bin's lower edge ----
             const float cut = isinf(row.top) ? row.top
                                              : row.top - ((float)last + 1.05f) / scale - fabsf(row.top) * 1e-6f;
-            const int cap = kList / c.nctas;
-            Shared* to = cl.map_shared_rank(&sh, 0);
-            const int found = collect(c, x, n, cut, begin, cap, to->list_x + c.rank * cap,
-                                      to->list_i + c.rank * cap);
-            if (c.tid < c.nctas)
-                cl.map_shared_rank(&sh, c.tid)->counts[c.rank] = found;
-            cl.sync();
-            listed = true;
-            for (int r = 0; r < c.nctas; ++r)
-                listed = listed && sh.counts[r] <= cap;
-        }
-        if (listed) {
-            if (c.rank != 0)
-                return;
-            const int cap = kList / c.nctas;
-            int before = 0, mine_at = -1;   // thread t < kRanked takes candidate t
-            for (int r = 0; r < c.nctas; ++r) {
-                const int f = sh.counts[r];
-                if (c.tid >= before && c.tid < before + f)
-                    mine_at = r * cap + c.tid - before;
-                before += f;
-            }
-            if (before <= kRanked) {
-                rank_and_draw(c, row, by_sum, total, before, mine_at, p, m);
-                return;
-            }
-            // the list moves to the start of the slice, which is done with
-            before = 0;
-            for (int r = 0; r < c.nctas; ++r) {
-                const int f = sh.counts[r];
-                for (int i = c.tid; i < f; i += kThreads)
-                    x[before + i] = sh.list_x[r * cap + i];
-                before += f;
-            }
+            auto found = [&](float x, int i) {
+                if (x >= cut) {
+                    atomicAdd(&sh.found, 1);
+                    const int at = atomicAdd(&to->listed, 1);
+                    if (at < kList)
+                        to->list[at] = ((uint64_t)key_of(x) << 32) | (0xFFFFFFFFu - (uint32_t)(begin + i));
+                }
+            };
+            if (next >= cut)
+                each<2>(slice, c.tid, found);          // more than one: read them again
+            else
+                found(high, high_at);
             __syncthreads();
-            d = Domain{x, before, false};
+            if (c.tid < c.nctas)
+                cl.map_shared_rank(&sh, c.tid)->counts[c.rank] = sh.found;
+            cl.sync();
+            int n = 0;
+            for (int r = 0; r < c.nctas; ++r)
+                n += sh.counts[r];
+            if (n <= kList) {
+                if (c.rank == 0)
+                    draw_listed(c, row, by_sum, total, n, p, m);
+                return;
+            }
+            // (the thread maxima's bound was too low: all logits give a closer one)
         }
-        kept = select(c, d, row, true, total);
+        kept = select(c, slice, row, total);
     }
-    float prob = 0.f;
-    const int place = draw(c, d, row, kept, &prob);
-    if (place >= 0 && c.tid == 0) {
-        int at = begin + place;
-        if (!d.wide) {                                 // the list's segments, in CTA order
-            int r = 0, i = place;
-            while (i >= sh.counts[r])
-                i -= sh.counts[r++];
-            at = sh.list_i[r * (kList / c.nctas) + i];
-        }
-        p.token[m] = at;
+    float prob;
+    const int place = draw(c, slice, row, kept, &prob);
+    if (c.tid == 0 && place >= 0) {
+        p.token[m] = begin + place;
         if (p.prob)
             p.prob[m] = prob;
     }
@@ -748,10 +794,9 @@ __global__ void __launch_bounds__(kThreads, 2) lbv_sample_kernel(const __grid_co
 template <int DT>
 cudaError_t launch(const SampleParams& p, int rows, cudaStream_t st)
 {
-    const size_t smem = sizeof(Shared) + (size_t)(p.slice > kList ? p.slice : kList) * 4;
     auto kernel = lbv_sample_kernel<DT>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kMaxSampleSmem);
+                                         (int)sizeof(Shared));
     if (e == cudaSuccess && p.ctas > 8)
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess)
@@ -759,7 +804,7 @@ cudaError_t launch(const SampleParams& p, int rows, cudaStream_t st)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * p.ctas));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = sizeof(Shared);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -771,12 +816,6 @@ cudaError_t launch(const SampleParams& p, int rows, cudaStream_t st)
 }
 
 }  // namespace
-
-// Slices of at most this many logits leave room for the rest (see Shared).
-int sample_max_slice()
-{
-    return (int)((kMaxSampleSmem - sizeof(Shared)) / 4 / 32 * 32);
-}
 
 cudaError_t launch_sample(const SampleParams& p, int rows, lbv_dtype dt, cudaStream_t st)
 {

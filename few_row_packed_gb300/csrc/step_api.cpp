@@ -464,14 +464,13 @@ lbv_status lbv_sample(const void* logits, int M, int N, int64_t ld, lbv_dtype dt
     if (rules->mask && M > 1 && rules->mask_ld < (N + 31) / 32)
         return fail(LBV_ERR_INVALID_ARG, "%s: mask_ld=%lld < %d words", fn,
                     (long long)rules->mask_ld, (N + 31) / 32);
-    const int most = lbv::sample_max_slice();
-    int ctas = 8;
-    while (ctas < 16 && (int64_t)ctas * most < N)
-        ctas *= 2;
-    while (ctas > 1 && N <= ctas * 2048)
+    if (N > 1 << 23)        // sums of weights up to 2^40 stay below 2^64
+        return fail(LBV_ERR_UNSUPPORTED, "%s: N=%d exceeds %d logits a row", fn, N, 1 << 23);
+    // Few rows take 16 CTAs each, more rows than the SMs hold so many of take 8;
+    // short rows so many that a thread still has a few logits.
+    int ctas = M <= 8 ? 16 : 8;
+    while (ctas > 1 && N <= ctas * 1024)
         ctas /= 2;
-    if ((int64_t)ctas * most < N)
-        return fail(LBV_ERR_UNSUPPORTED, "%s: N=%d exceeds %d logits a row", fn, N, 16 * most);
     if (M == 0)
         return LBV_OK;
     if (!logits || !aligned(logits, elem_size(dtype)) || !u || !token)

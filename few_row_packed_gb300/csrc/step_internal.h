@@ -58,8 +58,6 @@ struct SampleParams {
     int temperature_last;
 };
 
-constexpr int kMaxSampleSmem = 224 * 1024;
-int sample_max_slice();
 cudaError_t launch_sample(const SampleParams& p, int rows, lbv_dtype dt, cudaStream_t st);
 
 }  // namespace lbv

@@ -621,8 +621,7 @@ typedef struct lbv_sample_rules {
  * running sum of kept weights in index order exceeds floor(floor(u 2^24) kept
  * / 2^24).  NaN and -inf logits are never drawn; +inf ones share all weight.  A
  * row with nothing left to draw gives token -1 and prob 0.
- *   N at most about 740 thousand (LBV_ERR_UNSUPPORTED).  The library allocates
- * nothing.
+ *   N at most 2^23 (LBV_ERR_UNSUPPORTED).  The library allocates nothing.
  */
 LBV_API lbv_status lbv_sample(const void* logits, int M, int N, int64_t ld, lbv_dtype dtype,
                               const lbv_sample_rules* rules, const float* u, int32_t* token,

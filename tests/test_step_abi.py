@@ -117,7 +117,7 @@ def test_sample_refusals(L):
                dict(r=lbv._RulesArg(top_k=4097)),
                dict(m=2, r=lbv._RulesArg(mask=4096, mask_ld=3))):
         assert call(**kw) == INF, kw
-    assert call(n=1 << 20, ld=1 << 20) == lbv.ERR_UNSUPPORTED
+    assert call(n=1 << 24, ld=1 << 24) == lbv.ERR_UNSUPPORTED
     assert call(m=0, logits=None, u=None, token=None) == lbv.OK
 
 
