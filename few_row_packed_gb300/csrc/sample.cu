@@ -13,7 +13,7 @@
 // weights passes u * total.
 //
 // A row takes one thread-block cluster, each CTA a slice of it.  Selecting needs
-// one pass over the logits (the bound of a large batch) and no sort:
+// one pass over the logits (the bound of a large batch) and no sort of the row:
 //   1. every thread finds the maximum of its logits, the cluster the row's;
 //   2. a bound on how far down the kept tokens can reach.  The thread maxima
 //      enter a histogram of (m - l) r in steps of 1/8: the k-th of these few
@@ -50,9 +50,16 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = kThreads;            // one thread per bin
 constexpr int kList = 8 * kThreads;        // candidates the first CTA can take
+constexpr int kAhead = 4;                  // vectors of a thread on their way
 constexpr int kMaxCluster = 16;
 constexpr float kBinsPerNat = 8.f;
 constexpr float kNegInf = -__builtin_huge_valf();
+
+// Vectors of 16 bytes (and their two mask words) on the way to each thread.
+struct Ring {
+    uint4 v[kAhead][kThreads];
+    uint32_t words[kAhead][kThreads][2];
+};
 
 struct Shared {
     uint64_t red[2][kWarps][4];            // block reductions, two in flight
@@ -67,7 +74,10 @@ struct Shared {
     int pick;                              // place of the drawn token
     float pick_prob;
     uint64_t list[kList];                  // candidates: key, then the index's complement
-    uint64_t exchange[2][kList];           // of the sort's steps
+    union {
+        Ring ring;                         // of the passes over the slice
+        uint64_t exchange[2][kList];       // of the sort's steps, after them
+    };
 };
 
 // Order-preserving key of a logit (-0 made +0 before); -inf has a key above 0.
@@ -205,54 +215,57 @@ struct Slice {
                                      : __ldg(reinterpret_cast<const uint16_t*>(row) + i);
         return clean(to_f32<DT>(b), !words || ((__ldg(words + (i >> 5)) >> (i & 31)) & 1u));
     }
-    // mask bits of logits i to last (eight of them at most)
-    __device__ __forceinline__ uint32_t allowed(int i, int last) const
-    {
-        return words ? __funnelshift_r(__ldg(words + (i >> 5)), __ldg(words + (last >> 5)), i & 31) : ~0u;
-    }
 };
 
-// Calls f(value, index) for the thread's logits of the slice, indexes ascending:
-// 16-byte loads between the first and the last aligned address, kAhead of them
-// in flight.  The loop keeps one copy of f a vector (AT_ONCE of its elements at a
-// time): a row visits each pass but a few times, and fetching unrolled code from
-// L2 took longer than running it.
-constexpr int kAhead = 4;
+__device__ __forceinline__ void copy_async(void* to, const void* from, int bytes)
+{
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(to);
+    if (bytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(d), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(d), "l"(from) : "memory");
+}
 
+// Calls f(value, index) for the thread's logits of the slice, indexes ascending:
+// 16-byte copies between the first and the last aligned address, several of them
+// in flight, into places of the ring that only this thread reads (in registers, a
+// rotation of the buffers would wait for the copy that was just asked for).
+// AT_ONCE elements of a vector are unrolled.
 template <int AT_ONCE, int DT, typename F>
-__device__ __forceinline__ void each(const Slice<DT>& s, int tid, F f)
+__device__ __forceinline__ void each(const Slice<DT>& s, int tid, Ring& ring, F f)
 {
     constexpr int SIZE = Slice<DT>::SIZE, E = 16 / SIZE;
     const uintptr_t a = reinterpret_cast<uintptr_t>(s.row);
     const int head = min(s.n, (int)(((16 - (a & 15)) & 15) / SIZE));
     const int body = (s.n - head) / E, tail = head + body * E;
     const uint4* v = reinterpret_cast<const uint4*>(a + head * SIZE);
-    uint4 w[kAhead];
-    uint32_t ok[kAhead];
-    auto load = [&](int i, uint4& x, uint32_t& m) {
-        x = make_uint4(0u, 0u, 0u, 0u);
-        m = 0;
+    auto ask = [&](int i, int st) {
         if (i < body) {
-            x = __ldg(v + i);
-            m = s.allowed(head + i * E, head + i * E + E - 1);
+            copy_async(&ring.v[st][tid], v + i, 16);
+            if (s.words) {
+                const int d = head + i * E;
+                copy_async(&ring.words[st][tid][0], s.words + (d >> 5), 4);
+                copy_async(&ring.words[st][tid][1], s.words + ((d + E - 1) >> 5), 4);
+            }
         }
+        asm volatile("cp.async.commit_group;\n" ::: "memory");
     };
-#pragma unroll
+#pragma unroll 1
     for (int u = 0; u < kAhead; ++u)
-        load(tid + u * kThreads, w[u], ok[u]);
+        ask(tid + u * kThreads, u);
     if (tid < head)
         f(s.get(tid), tid);
+    int st = 0;
 #pragma unroll 1
     for (int i = tid; i < body; i += kThreads) {
-        const uint32_t q[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
-        const uint32_t m = ok[0];
-#pragma unroll
-        for (int u = 0; u + 1 < kAhead; ++u) {
-            w[u] = w[u + 1];
-            ok[u] = ok[u + 1];
-        }
-        load(i + kAhead * kThreads, w[kAhead - 1], ok[kAhead - 1]);
+        asm volatile("cp.async.wait_group %0;\n" ::"n"(kAhead - 1) : "memory");
+        const uint4 w = ring.v[st][tid];
         const int d = head + i * E;
+        const uint32_t m =
+            s.words ? __funnelshift_r(ring.words[st][tid][0], ring.words[st][tid][1], d & 31) : ~0u;
+        ask(i + kAhead * kThreads, st);
+        st = st + 1 == kAhead ? 0 : st + 1;
+        const uint32_t q[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll 1
         for (int e0 = 0; e0 < E; e0 += AT_ONCE)
 #pragma unroll
@@ -268,6 +281,7 @@ __device__ __forceinline__ void each(const Slice<DT>& s, int tid, F f)
                 f(s.clean(to_f32<DT>(b), (m >> e) & 1u), d + e);
             }
     }
+    asm volatile("cp.async.wait_all;\n" ::: "memory");
     if (tail + tid < s.n)                  // fewer than E of them
         f(s.get(tail + tid), tail + tid);
 }
@@ -293,7 +307,7 @@ __device__ __forceinline__ uint32_t search(Ctx& c, const D& d, F f, Test test)
     for (int bit = 30; bit >= 0; bit -= 2) {
         uint64_t s1 = 0, s2 = 0, s3 = 0;
         const uint32_t t1 = t | (1u << bit), t2 = t | (2u << bit), t3 = t | (3u << bit);
-        each<2>(d, c.tid, [&](float x, int) {
+        each<2>(d, c.tid, c.sh->ring, [&](float x, int) {
             const uint32_t k = key_of(x);
             if (k >= t1) {
                 const uint64_t w = f(x);
@@ -322,7 +336,7 @@ __device__ __noinline__ Kept select(Ctx& c, const D& d, const Row& row, uint64_t
                        [&](uint32_t, uint64_t n) { return n >= k; });
         // what lies above it
         uint64_t n = 0, sum = 0;
-        each<2>(d, c.tid, [&](float x, int) {
+        each<2>(d, c.tid, c.sh->ring, [&](float x, int) {
             if (key_of(x) > tau_k) {
                 n += 1;
                 sum += weight(x);
@@ -342,7 +356,7 @@ __device__ __noinline__ Kept select(Ctx& c, const D& d, const Row& row, uint64_t
             return t <= tau_k || s >= limit;
         });
         uint64_t sum = 0;
-        each<2>(d, c.tid, [&](float x, int) { sum += key_of(x) > tau ? weight(x) : 0; });
+        each<2>(d, c.tid, c.sh->ring, [&](float x, int) { sum += key_of(x) > tau ? weight(x) : 0; });
         uint64_t v[1] = {sum};
         reduce<1>(c, true, v);
         const uint64_t w = weight(of_key(tau));
@@ -442,10 +456,10 @@ __device__ __noinline__ int draw(Ctx& c, const D& d, const Row& row, const Kept&
     return sh.pick;
 }
 
-// Sorts list[0 .. 256 E) (or a smaller power of two n2, E = 1) in descending order,
-// bitonic, E elements a thread in registers (thread t: t, t + 256, ...): exchanges
-// over strides below 32 by shuffles, over 256 and more within the thread, and the
-// three between through shared memory.
+// Sorts list[0 .. kThreads E) (or a smaller power of two n2, E = 1) in descending order,
+// bitonic, E elements a thread in registers (thread t: t, t + kThreads, ...): exchanges
+// over strides below 32 by shuffles, over kThreads and more within the thread, and those
+// between through shared memory.
 template <int E>
 __device__ __noinline__ void sort_list(Shared& sh, int n2, int tid)
 {
@@ -630,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 4) lbv_sample_kernel(const __grid_co
     // ---- the thread's and the row's first maximum ----
     float high = kNegInf, next = kNegInf;              // the largest logit, the next one
     int high_at = 0;
-    each<DT == LBV_F32 ? 4 : 8>(slice, c.tid, [&](float v, int i) {
+    each<DT == LBV_F32 ? 4 : 8>(slice, c.tid, sh.ring, [&](float v, int i) {
         next = fmaxf(next, fminf(v, high));
         high_at = v > high ? i : high_at;
         high = fmaxf(high, v);
@@ -695,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 4) lbv_sample_kernel(const __grid_co
                     cl.sync();
                 } else {
                     uint64_t sum = 0;
-                    each<DT == LBV_F32 ? 4 : 8>(slice, c.tid, [&](float x, int) {
+                    each<DT == LBV_F32 ? 4 : 8>(slice, c.tid, sh.ring, [&](float x, int) {
                         sum += whole(weight_f(x, row.top, row.filter_r));
                     });
                     uint64_t v[1] = {sum};
@@ -708,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 4) lbv_sample_kernel(const __grid_co
                 if (c.tid == 0)
                     sh.found = sh.listed = 0;
                 __syncthreads();
-                each<2>(slice, c.tid, [&](float x, int) {
+                each<2>(slice, c.tid, sh.ring, [&](float x, int) {
                     const int b = bin_of(x);
                     if (b < kBins - 1)
                         atomicAdd(&sh.hist[b], 1u);
@@ -763,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 4) lbv_sample_kernel(const __grid_co
                 }
             };
             if (next >= cut)
-                each<2>(slice, c.tid, found);          // more than one: read them again
+                each<2>(slice, c.tid, sh.ring, found);          // more than one: read them again
             else
                 found(high, high_at);
             __syncthreads();
