@@ -455,8 +455,8 @@ struct alignas(32) JoinItem {
 // sums [ROWS].  join_parts adds them in CTA order, by THREADS threads (tid) that
 // meet at named barrier 1.  The parts come from L2, about 0.7 us away, so each
 // of the three steps has all its loads in flight at once: the maxima and sums,
-// the factors of every part (in `scratch`, `cap` floats of shared memory), and
-// 16 loads a thread of the results.
+// the factors of every part (in `scratch`, `cap` >= 2 parts + 2 floats of shared
+// memory), and 16 loads a thread of the results.
 template <int DT, int D, int ROWS, int THREADS>
 __device__ __forceinline__ void join_parts(const AttendParams& p, const Request& q, int kv_head,
                                            int row0, int rows, int c0, int c1, int tid,

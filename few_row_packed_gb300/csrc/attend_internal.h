@@ -17,7 +17,7 @@ struct AttendParams {
     float scale_log2;                // scale * log2(e)
     int window;                      // <= 0: none
     int heads, group;                // query heads, query heads per kv head
-    int q_pairs, q_wide;             // q rows are 4-byte, 16-byte aligned
+    int q_wide;                      // q rows are 16-byte aligned
     lbv_batch batch;
     KvView kv;
     // workspace
@@ -32,6 +32,13 @@ constexpr int kAttendMaxCtas = 512;              // CTAs of a launch, and counte
 constexpr size_t kAttendCounters = 256;
 constexpr size_t kAttendItems = kAttendCounters + kAttendMaxCtas * sizeof(unsigned);
 constexpr size_t kAttendPartial = kAttendItems + kAttendMaxCtas * 32;
+
+// Rows (new token times query head of a group) of an average request, whose
+// lengths the host does not know.
+inline int64_t attend_average_rows(const AttendParams& p)
+{
+    return ((int64_t)p.batch.tokens + p.batch.requests - 1) / p.batch.requests * p.group;
+}
 
 // p.items is where join items go if the launch joins apart.
 cudaError_t launch_attend_rows(const AttendParams& p, const CUtensorMap& kmap,

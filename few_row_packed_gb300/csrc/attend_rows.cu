@@ -17,14 +17,18 @@
 //     whose blocks lie in several CTAs leaves partial results (m, sum, o) in the
 //     workspace; the CTA that arrives last adds them in CTA order, so the
 //     result does not depend on timing.
-//   * A producer warp (its warpgroup gives its registers to the others) copies blocks with TMA (a box is 64 elements of a head
-//     times the slots of a page in the block) into a ring of 128-byte-swizzled
-//     stages, so that ldmatrix reads them without bank conflicts.
-//   * Four warps take 16 keys each of a block (WM > 1: as many sets of them
-//     share the rows): mma.sync m16n8k16 with the rows as M.  A tile of 16 rows
-//     is the natural size of a verify call; the 128-row tiles of tcgen05 would
-//     be mostly padding.  The warps' results meet in shared memory once per
-//     item.
+//   * A producer warp copies blocks with TMA (a box is 64 elements of a head times
+//     the slots of a page in the block) into a ring of 128-byte-swizzled stages, so
+//     that ldmatrix reads them without bank conflicts.
+//   * Four warps share a block: each takes the scores of 16 keys (mma.sync
+//     m16n8k16 with the rows as M), they agree on the rows' references, exchange
+//     their probabilities through shared memory, and each adds up a quarter of the
+//     head's elements over all 64 keys.  So no sums have to be joined at an item's
+//     end, and the accumulators take a quarter of the registers.  One tile of 16
+//     rows a read of the keys is what mma.sync sustains beside memory: it takes
+//     about 32 cycles an instruction and SM quarter, and tiles of 32 rows ran 1.4
+//     times slower than memory (310 us for 64 requests of one token, 220 with 16
+//     rows).  Larger tiles go to the tensor-memory kernel (attend_tiles.cu).
 #include "attend_common.cuh"
 
 namespace lbv {
@@ -39,32 +43,30 @@ constexpr int kKeyWarps = 4;
 // costs more than it saves).
 constexpr int kExtra = 1, kMinUnits = 2;
 
-template <int D, int MT, int WM>
+template <int D>
 struct Geo {
-    static constexpr int ROWS = 16 * MT * WM;
-    static constexpr int WARPS = kKeyWarps * WM;
-    static constexpr int THREADS = WARPS * 32 + 128;        // the producer's warpgroup first
+    static constexpr int ROWS = 16;
+    static constexpr int THREADS = kKeyWarps * 32 + 32;     // and the producer
     static constexpr int HALF = kBlock * 128;               // 64 elements of 64 keys
     static constexpr int STAGE = 2 * (D / 64) * HALF;       // K then V
-    // about 96 KB of ring where two CTAs share an SM, else 160
-    static constexpr int CTAS = WM == 1 ? 2 : 1;
-    // Registers a thread after the warpgroups' split.  The launch holds 128
-    // (256 threads, two CTAs) or 168 (384 threads) times its threads:
-    // 128 * 256 = 40 * 128 + 216 * 128, 168 * 384 = 40 * 128 + 232 * 256.
-    static constexpr int REGS_PRODUCER = 40, REGS_ROWS = WM == 1 ? 216 : 232;
-    static constexpr int NST = (CTAS == 2 ? 98304 : 163840) / STAGE;
-    static constexpr int OLD = D + 4;                       // floats per row of the join buffer
+    static constexpr int CTAS = 2;                          // on an SM
+    static constexpr int NST = 98304 / STAGE;
     static constexpr int SLOT = ROWS * (D + 2);             // floats of one partial result
-    // shared memory
-    static constexpr int O_BUF = NST * STAGE;
-    static constexpr int M_BUF = O_BUF + ROWS * OLD * 4;    // [kKeyWarps][ROWS] m, then sums
-    static constexpr int BARS = M_BUF + 2 * kKeyWarps * ROWS * 4;
+    static constexpr int PLD = kBlock * 2 + 16;             // bytes of a row of probabilities
+    // shared memory; the probabilities' place is also the join's scratch, which takes
+    // 2 floats a part for one row at least
+    static constexpr int P_BUF = NST * STAGE;
+    static constexpr int P_BYTES = ROWS * PLD > 4352 ? ROWS * PLD : 4352;
+    static constexpr int Q_BUF = P_BUF + P_BYTES;           // the item's queries
+    static constexpr int QLD = D * 2 + 16;                  // bytes of a row of them
+    static constexpr int M_BUF = Q_BUF + ROWS * QLD;        // [kKeyWarps][ROWS] block maxima, sums
+    static constexpr int BARS = M_BUF + kKeyWarps * ROWS * 4;
     static constexpr int FLAG = BARS + 2 * NST * 8;
     static constexpr int START = FLAG + 16;                 // where the CTA's share begins
     static constexpr int BYTES = START + 64;
-    static_assert(O_BUF % 16 == 0 && M_BUF % 16 == 0 && BARS % 8 == 0 && START % 8 == 0 &&
-                      sizeof(Start) <= 64,
-                  "alignment");
+    static_assert(P_BUF % 16 == 0 && Q_BUF % 16 == 0 && M_BUF % 16 == 0 && BARS % 8 == 0 &&
+                      START % 8 == 0 && sizeof(Start) <= 64 && P_BYTES / 4 >= 2 * kAttendMaxCtas + 2,
+                  "layout");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4])
@@ -100,13 +102,13 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int DT, int D, int MT, int WM>
-__global__ void __launch_bounds__(Geo<D, MT, WM>::THREADS, Geo<D, MT, WM>::CTAS)
+template <int DT, int D>
+__global__ void __launch_bounds__(Geo<D>::THREADS, Geo<D>::CTAS)
     lbv_attend_rows_kernel(const __grid_constant__ AttendParams p,
                            const __grid_constant__ CUtensorMap kmap,
                            const __grid_constant__ CUtensorMap vmap)
 {
-    using G = Geo<D, MT, WM>;
+    using G = Geo<D>;
     constexpr int ROWS = G::ROWS;
     using S = Shape<ROWS, kBlock, ROWS, kExtra>;
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -119,11 +121,11 @@ __global__ void __launch_bounds__(Geo<D, MT, WM>::THREADS, Geo<D, MT, WM>::CTAS)
     if (tid == 0) {
         for (int i = 0; i < G::NST; ++i) {
             mbar_init(full(i), 1);
-            mbar_init(empty(i), G::WARPS);
+            mbar_init(empty(i), kKeyWarps);
         }
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
-    if (p.items && tid == 128)
+    if (p.items && tid == 0)
         static_cast<JoinItem*>(p.items)[blockIdx.x].rows = 0;
     if (warp == 0)
         find_start<S>(p, lane, gridDim.x, kMinUnits, blockIdx.x, start);
@@ -133,11 +135,8 @@ __global__ void __launch_bounds__(Geo<D, MT, WM>::THREADS, Geo<D, MT, WM>::CTAS)
     Walk<S> w(p, *start, blockIdx.x);
     bool ok = true;
 
-    if (warp < 4) {
+    if (warp == kKeyWarps) {
         // ---- producer ----
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(G::REGS_PRODUCER));
-        if (warp != 0)
-            return;
         const int slots = min(kBlock, 1 << p.kv.page_shift);     // rows of a box
         const int boxes = kBlock / slots;                        // per 64 elements
         const int total_boxes = boxes * (D / 64) * 2;
@@ -179,58 +178,64 @@ __global__ void __launch_bounds__(Geo<D, MT, WM>::THREADS, Geo<D, MT, WM>::CTAS)
     }
 
     // ---- the rows ----
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(G::REGS_ROWS));
-    const int ctid = tid - 128;
-    const int kw = warp & (kKeyWarps - 1), wm = warp / kKeyWarps - 1;
-    float* obuf = reinterpret_cast<float*>(smem + G::O_BUF);
-    float* mbuf = reinterpret_cast<float*>(smem + G::M_BUF);
-    float* lbuf = mbuf + kKeyWarps * ROWS;
+    constexpr int TEAM = kKeyWarps * 32;                         // threads beside the producer
+    unsigned char* pbuf = smem + G::P_BUF;
+    float* tops = reinterpret_cast<float*>(smem + G::M_BUF);
     int* flag = reinterpret_cast<int*>(smem + G::FLAG);
-    // ldmatrix lane addresses within a stage (16 keys of this warp)
-    const int k_key = kw * 16 + ((lane >> 4) << 3) + (lane & 7), k_chunk = (lane >> 3) & 1;
-    const int v_key = kw * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), v_chunk = lane >> 4;
+    const int r0 = lane >> 2;                                    // the thread's rows: r0 and r0 + 8
+    // ldmatrix lane addresses: 16 keys of this warp in K, 16 keys of a step in V, the
+    // rows of a step in P and Q
+    const int k_key = warp * 16 + ((lane >> 4) << 3) + (lane & 7), k_chunk = (lane >> 3) & 1;
+    const int v_key = (((lane >> 3) & 1) << 3) + (lane & 7), v_chunk = warp * (D / 32) + (lane >> 4);
+    const uint32_t p_lane = sbase + G::P_BUF + (lane & 15) * G::PLD + (lane >> 4) * 16;
+    const uint32_t q_lane = sbase + G::Q_BUF + (lane & 15) * G::QLD + (lane >> 4) * 16;
+    constexpr int NT = D / 32;                                   // 8-element tiles of this warp's quarter
     int n = 0;
     while (w.next()) {
-        // Q fragments of the warp's rows, and what its rows see
-        uint32_t qf[MT][D / 16][4];
-        int pos[MT][2];
-        uint64_t words[MT][2];
+        // the queries by way of shared memory, and what the rows see
+        for (int i = tid; i < ROWS * (D / 8); i += TEAM) {
+            const int r = i / (D / 8), ch = i % (D / 8), row = w.x.row0 + r;
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (r < w.x.rows) {
+                const int t = row / p.group;
+                const uint16_t* src = p.q + (int64_t)(w.q.q0 + t) * p.q_token +
+                                      (int64_t)(w.head * p.group + row - t * p.group) * p.q_head + ch * 8;
+                if (p.q_wide) {
+                    v = __ldg(reinterpret_cast<const uint4*>(src));
+                } else {
+                    uint32_t e[4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int row = w.x.row0 + (wm * MT + mt) * 16 + h * 8 + (lane >> 2);
-                const bool in = row < w.q.n * p.group;
-                const int i = row / p.group, g = row - i * p.group;
-                pos[mt][h] = in ? w.q.first + i : INT_MIN / 2;
-                words[mt][h] = in && p.tree ? p.tree[w.q.q0 + i] : 0;
-                const uint16_t* src = p.q + (int64_t)(w.q.q0 + i) * p.q_token +
-                                      (int64_t)(w.head * p.group + g) * p.q_head + (lane & 3) * 2;
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const uint16_t* a = src + ks * 16 + c * 8;
-                        uint32_t v = 0;
-                        if (in)
-                            v = p.q_pairs ? *reinterpret_cast<const uint32_t*>(a)
-                                          : (uint32_t)a[0] | ((uint32_t)a[1] << 16);
-                        qf[mt][ks][c * 2 + h] = v;
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        e[k] = (uint32_t)src[2 * k] | ((uint32_t)src[2 * k + 1] << 16);
+                    v = make_uint4(e[0], e[1], e[2], e[3]);
+                }
             }
-        float o[MT][D / 8][4];
-        float m[MT][2], l[MT][2];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            m[mt][0] = m[mt][1] = -INFINITY;
-            l[mt][0] = l[mt][1] = 0.f;
-#pragma unroll
-            for (int j = 0; j < D / 8; ++j)
-                o[mt][j][0] = o[mt][j][1] = o[mt][j][2] = o[mt][j][3] = 0.f;
+            *reinterpret_cast<uint4*>(smem + G::Q_BUF + r * G::QLD + ch * 16) = v;
         }
+        int pos[2];
+        uint64_t words[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const bool in = r0 + h * 8 < w.x.rows;
+            const int i = (w.x.row0 + r0 + h * 8) / p.group;
+            pos[h] = in ? w.q.first + i : INT_MIN / 2;
+            words[h] = in && p.tree ? p.tree[w.q.q0 + i] : 0;
+        }
+        named_bar_sync(1, TEAM);
+        uint32_t qf[D / 16][4];
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+            ldsm4(q_lane + ks * 32, qf[ks]);
+        float o[NT][4];
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
         // keys below `open_lo` or at `open_hi` and past are hidden from some row
-        const int open_hi = p.tree ? min(w.q.keys, w.q.first) : min(w.q.keys, w.q.first + w.x.row0 / p.group + 1);
-        const int open_lo = p.window > 0 ? w.q.first + (w.x.row0 + w.x.rows - 1) / p.group - p.window + 1 : 0;
+        const int open_hi = p.tree ? min(w.q.keys, w.q.first)
+                                   : min(w.q.keys, w.q.first + w.x.row0 / p.group + 1);
+        const int open_lo =
+            p.window > 0 ? w.q.first + (w.x.row0 + w.x.rows - 1) / p.group - p.window + 1 : 0;
 
         for (int b = w.b_first; b < w.b_last; ++b) {
             const int st = n % G::NST, k0 = w.key0(b);
@@ -238,202 +243,165 @@ __global__ void __launch_bounds__(Geo<D, MT, WM>::THREADS, Geo<D, MT, WM>::CTAS)
                 ok = mbar_wait(full(st), (uint32_t)((n / G::NST) & 1));
             ++n;
             const uint32_t ks_base = sbase + st * G::STAGE, vs_base = ks_base + (D / 64) * G::HALF;
-            const int my0 = k0 + kw * 16;                        // this warp's 16 keys
-            // slots past the context may hold anything: NaN times 0 is not 0
-            if (my0 + 16 > w.q.keys) {
+            const int my0 = k0 + warp * 16;                      // this warp's 16 keys
+            // slots past the context may hold anything: NaN times 0 is not 0 (the other
+            // warps read V after the barriers below)
+            const bool tail = k0 + kBlock > w.q.keys;
+            if (tail)
                 for (int i = lane; i < 16 * (D / 8); i += 32) {
                     const int key = i / (D / 8), ch = i % (D / 8);
                     if (my0 + key >= w.q.keys)
                         *reinterpret_cast<uint4*>(smem + (vs_base - sbase) + (ch >> 3) * G::HALF +
-                                                  (kw * 16 + key) * 128 + ((ch & 7) << 4)) =
+                                                  (warp * 16 + key) * 128 + ((ch & 7) << 4)) =
                             make_uint4(0u, 0u, 0u, 0u);
                 }
-                __syncwarp();
-            }
-            float s[MT][2][4];
+            float s[2][4];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    s[mt][j][0] = s[mt][j][1] = s[mt][j][2] = s[mt][j][3] = 0.f;
+            for (int j = 0; j < 2; ++j)
+                s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
                 uint32_t kf[4];
                 const int ch = ks * 2 + k_chunk;
                 ldsm4(ks_base + (ch >> 3) * G::HALF + k_key * 128 + (((ch & 7) ^ (k_key & 7)) << 4), kf);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    mma<DT>(s[mt][0], qf[mt][ks], kf[0], kf[1]);
-                    mma<DT>(s[mt][1], qf[mt][ks], kf[2], kf[3]);
-                }
+                mma<DT>(s[0], qf[ks], kf[0], kf[1]);
+                mma<DT>(s[1], qf[ks], kf[2], kf[3]);
             }
             const bool masked = my0 + 16 > open_hi || my0 < open_lo;
-            bool moved = false;
-            float shrink[MT][2];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int h = 0; h < 2; ++h) {
+                float top = -INFINITY;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float top = -INFINITY;
+                for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float& t = s[mt][j][h * 2 + e];
-                            t *= p.scale_log2;
-                            if (masked) {
-                                const int key = my0 + j * 8 + (lane & 3) * 2 + e;
-                                if (!sees(p, w.q, pos[mt][h], words[mt][h], key))
-                                    t = -INFINITY;
-                            }
-                            top = fmaxf(top, t);
-                        }
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    shrink[mt][h] = 1.f;
-                    if (top > m[mt][h] + 8.f) {                  // also from -inf
-                        shrink[mt][h] = ex2(m[mt][h] - top);
-                        m[mt][h] = top;
-                        moved = true;
+                    for (int e = 0; e < 2; ++e) {
+                        float& t = s[j][h * 2 + e];
+                        t *= p.scale_log2;
+                        if (masked && !sees(p, w.q, pos[h], words[h], my0 + j * 8 + (lane & 3) * 2 + e))
+                            t = -INFINITY;
+                        top = fmaxf(top, t);
                     }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                if ((lane & 3) == 0)
+                    tops[warp * ROWS + h * 8 + r0] = top;
+            }
+            named_bar_sync(1, TEAM);
+            // the block's maxima, the same for every warp
+            bool moved = false;
+            float shrink[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float* t = tops + h * 8 + r0;
+                const float top = fmaxf(fmaxf(t[0], t[ROWS]), fmaxf(t[2 * ROWS], t[3 * ROWS]));
+                shrink[h] = 1.f;
+                if (top > m[h] + 8.f) {                          // also from -inf
+                    shrink[h] = ex2(m[h] - top);
+                    m[h] = top;
+                    moved = true;
                 }
+                const float ref = m[h] == -INFINITY ? 0.f : m[h];
+                l[h] *= shrink[h];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float a = ex2(s[j][h * 2] - ref), c = ex2(s[j][h * 2 + 1] - ref);
+                    l[h] += a + c;                               // of this warp's keys
+                    *reinterpret_cast<uint32_t*>(pbuf + (h * 8 + r0) * G::PLD +
+                                                 (warp * 16 + j * 8 + (lane & 3) * 2) * 2) = pack2<DT>(a, c);
+                }
+            }
             if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        l[mt][h] *= shrink[mt][h];
-#pragma unroll
-                        for (int j = 0; j < D / 8; ++j) {
-                            o[mt][j][h * 2] *= shrink[mt][h];
-                            o[mt][j][h * 2 + 1] *= shrink[mt][h];
-                        }
-                    }
-            }
-            uint32_t pf[MT][4];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float ref = m[mt][h] == -INFINITY ? 0.f : m[mt][h];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float a = ex2(s[mt][j][h * 2] - ref), c = ex2(s[mt][j][h * 2 + 1] - ref);
-                        l[mt][h] += a + c;
-                        pf[mt][j * 2 + h] = pack2<DT>(a, c);
-                    }
-                }
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j) {
-                uint32_t vf[4];
-                const int ch = j * 2 + v_chunk;
-                ldsm4t(vs_base + (ch >> 3) * G::HALF + v_key * 128 + (((ch & 7) ^ (v_key & 7)) << 4), vf);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    mma<DT>(o[mt][2 * j], pf[mt], vf[0], vf[1]);
-                    mma<DT>(o[mt][2 * j + 1], pf[mt], vf[2], vf[3]);
+                for (int j = 0; j < NT; ++j) {
+                    o[j][0] *= shrink[0], o[j][1] *= shrink[0];
+                    o[j][2] *= shrink[1], o[j][3] *= shrink[1];
                 }
             }
-            if (my0 + 16 > w.q.keys)
+            named_bar_sync(1, TEAM);
+#pragma unroll
+            for (int ks = 0; ks < kBlock / 16; ++ks) {
+                uint32_t pf[4];
+                ldsm4(p_lane + ks * 32, pf);
+#pragma unroll
+                for (int j = 0; j < NT / 2; ++j) {
+                    uint32_t vf[4];
+                    const int ch = j * 2 + v_chunk, key = ks * 16 + v_key;
+                    ldsm4t(vs_base + (ch >> 3) * G::HALF + key * 128 + (((ch & 7) ^ (key & 7)) << 4), vf);
+                    mma<DT>(o[2 * j], pf, vf[0], vf[1]);
+                    mma<DT>(o[2 * j + 1], pf, vf[2], vf[3]);
+                }
+            }
+            if (tail)
                 fence_proxy_async_smem();                        // own stores before the next copy
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(empty(st));
         }
 
-        // ---- the warps' results meet ----
+        // ---- the item's result: each warp has a quarter of the elements ----
+        named_bar_sync(1, TEAM);                                 // the last maxima have been read
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                l[mt][h] += __shfl_xor_sync(0xffffffffu, l[mt][h], 1);
-                l[mt][h] += __shfl_xor_sync(0xffffffffu, l[mt][h], 2);
-                const int row = (wm * MT + mt) * 16 + h * 8 + (lane >> 2);
-                if ((lane & 3) == 0) {
-                    mbuf[kw * ROWS + row] = m[mt][h];
-                    lbuf[kw * ROWS + row] = l[mt][h];
-                }
-            }
-        named_bar_sync(1, G::WARPS * 32);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int row = (wm * MT + mt) * 16 + h * 8 + (lane >> 2);
-                float top = mbuf[row];
-#pragma unroll
-                for (int k = 1; k < kKeyWarps; ++k)
-                    top = fmaxf(top, mbuf[k * ROWS + row]);
-                const float f = top == -INFINITY ? 0.f : ex2(m[mt][h] - top);
-#pragma unroll
-                for (int j = 0; j < D / 8; ++j) {
-                    o[mt][j][h * 2] *= f;
-                    o[mt][j][h * 2 + 1] *= f;
-                }
-            }
-        for (int k = 0; k < kKeyWarps; ++k) {
-            if (kw == k)
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int row = (wm * MT + mt) * 16 + h * 8 + (lane >> 2);
-                        float2* d = reinterpret_cast<float2*>(obuf + row * G::OLD + (lane & 3) * 2);
-#pragma unroll
-                        for (int j = 0; j < D / 8; ++j) {
-                            float2 v = make_float2(o[mt][j][h * 2], o[mt][j][h * 2 + 1]);
-                            if (k > 0) {
-                                const float2 a = d[j * 4];
-                                v.x += a.x, v.y += a.y;
-                            }
-                            d[j * 4] = v;
-                        }
-                    }
-            named_bar_sync(1, G::WARPS * 32);
+        for (int h = 0; h < 2; ++h) {
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+            if ((lane & 3) == 0)
+                tops[warp * ROWS + h * 8 + r0] = l[h];
         }
-        // row totals (in the first warp's slots)
+        named_bar_sync(1, TEAM);
         const bool whole = w.whole();
         const int c0 = whole ? 0 : w.first_cta();
         const int c1 = whole ? 0 : w.last_cta();
         float* slot = p.partial + (size_t)(2 * blockIdx.x + (c0 == (int)blockIdx.x)) * G::SLOT;
-        for (int i = ctid; i < w.x.rows * (D / 4); i += G::WARPS * 32) {
-            const int row = i / (D / 4), d4 = i % (D / 4);
-            const float4 v = *reinterpret_cast<const float4*>(obuf + row * G::OLD + d4 * 4);
-            float top = mbuf[row], sum = 0.f;
 #pragma unroll
-            for (int k = 1; k < kKeyWarps; ++k)
-                top = fmaxf(top, mbuf[k * ROWS + row]);
-#pragma unroll
-            for (int k = 0; k < kKeyWarps; ++k)
-                sum += top == -INFINITY ? 0.f : lbuf[k * ROWS + row] * ex2(mbuf[k * ROWS + row] - top);
+        for (int h = 0; h < 2; ++h) {
+            const int r = h * 8 + r0, row = w.x.row0 + r;
+            if (r >= w.x.rows)
+                continue;
+            const float* t = tops + r;
+            const float sum = (t[0] + t[ROWS]) + (t[2 * ROWS] + t[3 * ROWS]);
+            const int i = row / p.group, head = w.head * p.group + row - i * p.group;
+            const int64_t tok = w.q.q0 + i;
+            const bool first = warp == 0 && (lane & 3) == 0;
+            const int e0 = warp * (D / 4) + (lane & 3) * 2;
             if (whole) {
-                finish4<DT>(p, w.q, w.head, w.x.row0 + row, d4, v, top, sum);
+                const float f = 1.f / sum;
+                uint16_t* d = p.out + tok * p.out_token + (int64_t)head * p.out_head + e0;
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const uint32_t v = sum == 0.f ? 0u : pack2<DT>(o[j][h * 2] * f, o[j][h * 2 + 1] * f);
+                    store_row<2>(d + j * 8, &v);
+                }
+                if (p.lse && first)
+                    p.lse[tok * p.heads + head] = lse_of(m[h], sum);
             } else {
-                *reinterpret_cast<float4*>(slot + row * D + d4 * 4) = v;
-                if (d4 == 0) {
-                    slot[ROWS * D + row] = top;
-                    slot[ROWS * (D + 1) + row] = sum;
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    *reinterpret_cast<float2*>(slot + r * D + e0 + j * 8) =
+                        make_float2(o[j][h * 2], o[j][h * 2 + 1]);
+                if (first) {
+                    slot[ROWS * D + r] = m[h];
+                    slot[ROWS * (D + 1) + r] = sum;
                 }
             }
         }
         if (!whole && p.items) {
-            if (ctid == 0 && c0 == (int)blockIdx.x)
+            if (tid == 0 && c0 == (int)blockIdx.x)
                 static_cast<JoinItem*>(p.items)[c0] = {w.q.q0, w.x.row0, w.x.rows, w.head, c1 - c0 + 1};
         } else if (!whole) {
             __threadfence();
-            named_bar_sync(1, G::WARPS * 32);
-            if (ctid == 0)
+            named_bar_sync(1, TEAM);
+            if (tid == 0)
                 *flag = atomicAdd(p.counters + c0, 1u) == (unsigned)(c1 - c0);
-            named_bar_sync(1, G::WARPS * 32);
+            named_bar_sync(1, TEAM);
             if (*flag) {                                         // every part is there: join them
                 __threadfence();
-                join_parts<DT, D, ROWS, G::WARPS * 32>(p, w.q, w.head, w.x.row0, w.x.rows, c0, c1, ctid,
-                                                       obuf, ROWS * G::OLD);
-                if (ctid == 0)
+                join_parts<DT, D, ROWS, TEAM>(p, w.q, w.head, w.x.row0, w.x.rows, c0, c1, tid,
+                                              reinterpret_cast<float*>(pbuf), G::P_BYTES / 4);
+                if (tid == 0)
                     p.counters[c0] = 0;                          // as the next call finds it
             }
+            named_bar_sync(1, TEAM);                             // the flag has been read
         }
-        named_bar_sync(1, G::WARPS * 32);                        // buffers free for the next item
     }
     if (!ok && lane == 0)
         atomicOr(p.status, 1u);
@@ -443,8 +411,8 @@ template <int DT, int D>
 cudaError_t launch(const AttendParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int sms,
                    cudaStream_t st)
 {
-    using G = Geo<D, 1, 1>;
-    auto kernel = lbv_attend_rows_kernel<DT, D, 1, 1>;
+    using G = Geo<D>;
+    auto kernel = lbv_attend_rows_kernel<DT, D>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, G::BYTES);
     if (e != cudaSuccess)
         return e;
@@ -472,9 +440,9 @@ cudaError_t launch_attend_rows(const AttendParams& p, const CUtensorMap& kmap,
 
 size_t attend_rows_partial_floats(int dim, int sms)
 {
-    // two slots per CTA of the launch with the most rows times CTAs
+    // two slots per CTA
     const int a = sms * 2 < kAttendMaxCtas ? sms * 2 : kAttendMaxCtas;
-    return (size_t)2 * a * 64 * (dim + 2);
+    return (size_t)2 * a * 16 * (dim + 2);
 }
 
 }  // namespace lbv

@@ -400,7 +400,6 @@ lbv_status lbv_attend(const lbv_kv_cache* cache, const lbv_batch* batch, const l
     p.window = window < (1 << 30) ? window : 0;    // no context is that long
     p.heads = q->heads;
     p.group = q->heads / cache->view.heads;
-    p.q_pairs = aligned(q->data, 4) && q->token_stride % 2 == 0 && q->head_stride % 2 == 0;
     p.q_wide = aligned(q->data, 16) && q->token_stride % 8 == 0 && q->head_stride % 8 == 0;
     p.batch = *batch;
     p.kv = cache->view;
@@ -409,10 +408,8 @@ lbv_status lbv_attend(const lbv_kv_cache* cache, const lbv_batch* batch, const l
     p.counters = reinterpret_cast<unsigned*>(ws + lbv::kAttendCounters);
     p.items = ws + lbv::kAttendItems;
     p.partial = reinterpret_cast<float*>(ws + lbv::kAttendPartial);
-    // Rows (new token times query head of a group) of an average request, whose
-    // lengths the host does not know.  Both kernels are right for every length.
-    const int64_t rows = ((int64_t)batch->tokens + batch->requests - 1) / batch->requests * p.group;
-    const auto launch = rows <= 16 ? lbv::launch_attend_rows : lbv::launch_attend_tiles;
+    // both kernels are right for every length
+    const auto launch = lbv::attend_average_rows(p) <= 16 ? lbv::launch_attend_rows : lbv::launch_attend_tiles;
     const cudaError_t e = launch(p, cache->kmap, cache->vmap, cache->dtype, cache->sms,
                                  (cudaStream_t)stream);
     if (e != cudaSuccess)
