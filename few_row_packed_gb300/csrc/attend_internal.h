@@ -27,7 +27,7 @@ struct AttendParams {
     void* items;                     // one JoinItem per CTA where they are joined apart, else NULL
 };
 
-constexpr int kAttendMaxCtas = 512;              // CTAs of a launch, and counters
+constexpr int kAttendMaxCtas = 608;              // CTAs of a launch (152 SMs x 4), and counters
 // Workspace: status word, counters, join items, partial results.
 constexpr size_t kAttendCounters = 256;
 constexpr size_t kAttendItems = kAttendCounters + kAttendMaxCtas * sizeof(unsigned);

@@ -41,7 +41,7 @@ constexpr int kBlock = 64;                       // keys per block
 constexpr int kKeyWarps = 4;
 // Units of an item beside its blocks, and the least share of a CTA (below, joining
 // costs more than it saves).
-constexpr int kExtra = 1, kMinUnits = 2;
+constexpr int kExtra = 3, kMinUnits = 2;
 
 template <int D>
 struct Geo {
@@ -49,15 +49,16 @@ struct Geo {
     static constexpr int THREADS = kKeyWarps * 32 + 32;     // and the producer
     static constexpr int HALF = kBlock * 128;               // 64 elements of 64 keys
     static constexpr int STAGE = 2 * (D / 64) * HALF;       // K then V
-    static constexpr int CTAS = 2;                          // on an SM
-    static constexpr int NST = 98304 / STAGE;
+    // CTAs on an SM, which share about 192 KB of ring: a block of small heads is
+    // short, and more of them have to be under way
+    static constexpr int CTAS = D == 64 ? 4 : 2;
+    static constexpr int NST = 196608 / CTAS / STAGE;
     static constexpr int SLOT = ROWS * (D + 2);             // floats of one partial result
     static constexpr int PLD = kBlock * 2 + 16;             // bytes of a row of probabilities
-    // shared memory; the probabilities' place is also the join's scratch, which takes
-    // 2 floats a part for one row at least
+    // shared memory; from the probabilities to the barriers it is also the join's
+    // scratch, which takes 2 floats a part for one row at least
     static constexpr int P_BUF = NST * STAGE;
-    static constexpr int P_BYTES = ROWS * PLD > 4352 ? ROWS * PLD : 4352;
-    static constexpr int Q_BUF = P_BUF + P_BYTES;           // the item's queries
+    static constexpr int Q_BUF = P_BUF + ROWS * PLD + 16;   // the item's queries
     static constexpr int QLD = D * 2 + 16;                  // bytes of a row of them
     static constexpr int M_BUF = Q_BUF + ROWS * QLD;        // [kKeyWarps][ROWS] block maxima, sums
     static constexpr int BARS = M_BUF + kKeyWarps * ROWS * 4;
@@ -65,7 +66,7 @@ struct Geo {
     static constexpr int START = FLAG + 16;                 // where the CTA's share begins
     static constexpr int BYTES = START + 64;
     static_assert(P_BUF % 16 == 0 && Q_BUF % 16 == 0 && M_BUF % 16 == 0 && BARS % 8 == 0 &&
-                      START % 8 == 0 && sizeof(Start) <= 64 && P_BYTES / 4 >= 2 * kAttendMaxCtas + 2,
+                      START % 8 == 0 && sizeof(Start) <= 64 && (BARS - P_BUF) / 4 >= 2 * kAttendMaxCtas + 2,
                   "layout");
 };
 
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, Geo<D>::CTAS)
             if (*flag) {                                         // every part is there: join them
                 __threadfence();
                 join_parts<DT, D, ROWS, TEAM>(p, w.q, w.head, w.x.row0, w.x.rows, c0, c1, tid,
-                                              reinterpret_cast<float*>(pbuf), G::P_BYTES / 4);
+                                              reinterpret_cast<float*>(pbuf), (G::BARS - G::P_BUF) / 4);
                 if (tid == 0)
                     p.counters[c0] = 0;                          // as the next call finds it
             }
@@ -441,7 +442,8 @@ cudaError_t launch_attend_rows(const AttendParams& p, const CUtensorMap& kmap,
 size_t attend_rows_partial_floats(int dim, int sms)
 {
     // two slots per CTA
-    const int a = sms * 2 < kAttendMaxCtas ? sms * 2 : kAttendMaxCtas;
+    const int ctas = sms * (dim == 64 ? Geo<64>::CTAS : Geo<128>::CTAS);
+    const int a = ctas < kAttendMaxCtas ? ctas : kAttendMaxCtas;
     return (size_t)2 * a * 16 * (dim + 2);
 }
 
