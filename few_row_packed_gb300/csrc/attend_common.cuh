@@ -108,13 +108,14 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     return r;
 }
 
+// The two values as they were rounded.
 template <int DT>
-__device__ __forceinline__ uint16_t pack1(float x)
+__device__ __forceinline__ float2 unpack2(uint32_t r)
 {
     if constexpr (DT == LBV_F16)
-        return __half_as_ushort(__float2half_rn(x));
+        return __half22float2(reinterpret_cast<const __half2&>(r));
     else
-        return __bfloat16_as_ushort(__float2bfloat16_rn(x));
+        return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xFFFF0000u));
 }
 
 // A request's share of the batch.
@@ -217,10 +218,12 @@ __device__ __forceinline__ float lse_of(float top, float sum)
 }
 
 // Writes a row's four elements from 4 d4 on (o / sum, rounded once), and with
-// the first of them its lse.  A row that saw nothing (sum 0) gets 0.
+// the first of them its lse.  A row that saw nothing (sum 0) gets 0.  `sum` adds the
+// probabilities as they entered the product with V, so that a row that one key
+// dominates gets that key's value; `exact` adds them unrounded, for the lse.
 template <int DT>
 __device__ __forceinline__ void finish4(const AttendParams& p, const Request& q, int kv_head, int row,
-                                        int d4, float4 o, float top, float sum)
+                                        int d4, float4 o, float top, float sum, float exact)
 {
     const int i = row / p.group, g = row - i * p.group;
     const int64_t tok = q.q0 + i;
@@ -230,7 +233,7 @@ __device__ __forceinline__ void finish4(const AttendParams& p, const Request& q,
                            sum == 0.f ? 0u : pack2<DT>(o.z * f, o.w * f)};
     store_row<4>(p.out + tok * p.out_token + (int64_t)head * p.out_head + d4 * 4, r);
     if (p.lse && d4 == 0)
-        p.lse[tok * p.heads + head] = lse_of(top, sum);
+        p.lse[tok * p.heads + head] = lse_of(top, exact);
 }
 
 // ---- work items ----
@@ -452,10 +455,10 @@ struct alignas(32) JoinItem {
 
 // Partial results of an item: slot 2 c + 1 of the CTA c0 it starts in, slot 2 c
 // of the others; a slot holds o [ROWS][D], the reference maxima [ROWS] and the
-// sums [ROWS].  join_parts adds them in CTA order, by THREADS threads (tid) that
+// sums [ROWS] of rounded and of exact probabilities.  join_parts adds them in CTA order, by THREADS threads (tid) that
 // meet at named barrier 1.  The parts come from L2, about 0.7 us away, so each
 // of the three steps has all its loads in flight at once: the maxima and sums,
-// the factors of every part (in `scratch`, `cap` >= 2 parts + 2 floats of shared
+// the factors of every part (in `scratch`, `cap` >= 2 parts + 3 floats of shared
 // memory), and 16 loads a thread of the results.
 template <int DT, int D, int ROWS, int THREADS>
 __device__ __forceinline__ void join_parts(const AttendParams& p, const Request& q, int kv_head,
@@ -464,14 +467,14 @@ __device__ __forceinline__ void join_parts(const AttendParams& p, const Request&
 {
     const int parts = c1 - c0 + 1;
     auto part = [&](int k) {
-        return p.partial + (size_t)(2 * (c0 + k) + (k == 0)) * (ROWS * (D + 2));
+        return p.partial + (size_t)(2 * (c0 + k) + (k == 0)) * (ROWS * (D + 3));
     };
-    const int step = min(rows, cap / (2 * parts + 2));   // rows at a time (parts: at most 512)
+    const int step = min(rows, cap / (2 * parts + 3));   // rows at a time (parts: at most 512)
     for (int r0 = 0; r0 < rows; r0 += step) {
         const int n = min(step, rows - r0);
         float* f = scratch;                              // [parts][n] maxima, then factors
         float* s = f + parts * n;                        // [parts][n] sums
-        float* tops = s + parts * n;                     // [n], and the joined sums [n]
+        float* tops = s + parts * n;                     // [n], and the joined sums, twice [n]
         for (int i = tid; i < parts * n; i += THREADS) {
             const int k = i / n, r = i - k * n;
             f[i] = __ldcg(part(k) + ROWS * D + r0 + r);
@@ -481,7 +484,7 @@ __device__ __forceinline__ void join_parts(const AttendParams& p, const Request&
         // a row's factors: by one thread, or by a warp if the parts are many
         const int lanes = parts > 8 ? 32 : 1, lane = tid & (lanes - 1);
         for (int r = tid / lanes; r < n; r += THREADS / lanes) {
-            float top = -INFINITY, sum = 0.f;
+            float top = -INFINITY, sum = 0.f, exact = 0.f;
             for (int k = lane; k < parts; k += lanes)
                 top = fmaxf(top, f[k * n + r]);
             for (int d = lanes >> 1; d > 0; d >>= 1)
@@ -490,12 +493,17 @@ __device__ __forceinline__ void join_parts(const AttendParams& p, const Request&
                 const float m = f[k * n + r], w = m == -INFINITY ? 0.f : ex2(m - top);
                 f[k * n + r] = w;
                 sum += w * s[k * n + r];
+                if (p.lse)
+                    exact += w * __ldcg(part(k) + ROWS * (D + 2) + r0 + r);
             }
-            for (int d = lanes >> 1; d > 0; d >>= 1)
+            for (int d = lanes >> 1; d > 0; d >>= 1) {
                 sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                exact += __shfl_xor_sync(0xffffffffu, exact, d);
+            }
             if (lane == 0) {
                 tops[r] = top;
                 tops[n + r] = sum;
+                tops[2 * n + r] = exact;
             }
         }
         named_bar_sync(1, THREADS);
@@ -530,7 +538,7 @@ __device__ __forceinline__ void join_parts(const AttendParams& p, const Request&
                 if (i + u * THREADS < tasks) {
                     const int r = (i + u * THREADS) / (D / 4);
                     finish4<DT>(p, q, kv_head, row0 + r0 + r, (i + u * THREADS) % (D / 4), o[u],
-                                tops[r], tops[n + r]);
+                                tops[r], tops[n + r], tops[2 * n + r]);
                 }
         }
         named_bar_sync(1, THREADS);                      // scratch is free again

@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     const int sub = lane / LANES, d4 = lane % LANES;
     Request q;
     q.q0 = it.q0;
-    const size_t slot = (size_t)slot_rows * (D + 2);
+    const size_t slot = (size_t)slot_rows * (D + 3);
     auto part = [&](int k) {
         return p.partial + (size_t)(2 * (c0 + k) + (k == 0)) * slot;
     };
@@ -59,10 +59,11 @@ __global__ void __launch_bounds__(kWarps * 32)
         for (int j = 0; j < AHEAD; ++j)
             if (j * AT_ONCE + sub < it.parts)
                 first[j] = __ldcg(reinterpret_cast<const float4*>(part(j * AT_ONCE + sub) + row * D) + d4);
-        float m = -INFINITY, s = 0.f;            // of the lane's part
+        float m = -INFINITY, s = 0.f, x = 0.f;   // of the lane's part
         if (lane < it.parts) {
             m = __ldcg(part(lane) + slot_rows * D + row);
             s = __ldcg(part(lane) + slot_rows * (D + 1) + row);
+            x = __ldcg(part(lane) + slot_rows * (D + 2) + row);
         }
         float top = m;
         for (int k = lane + 32; k < it.parts; k += 32)
@@ -70,7 +71,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        float w = m == -INFINITY ? 0.f : ex2(m - top), sum = w * s;
+        float w = m == -INFINITY ? 0.f : ex2(m - top), sum = w * s, exact = w * x;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         auto add = [&](float f, float4 a) {
             o.x += f * a.x, o.y += f * a.y, o.z += f * a.z, o.w += f * a.w;
@@ -89,6 +90,7 @@ __global__ void __launch_bounds__(kWarps * 32)
                     const float n = __ldcg(part(k) + slot_rows * D + row);
                     w = n == -INFINITY ? 0.f : ex2(n - top);
                     sum += w * __ldcg(part(k) + slot_rows * (D + 1) + row);
+                    exact += w * __ldcg(part(k) + slot_rows * (D + 2) + row);
                 }
             }
             const int n = min(32, it.parts - k0);
@@ -100,14 +102,16 @@ __global__ void __launch_bounds__(kWarps * 32)
             }
         }
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1)
+        for (int d = 16; d > 0; d >>= 1) {
             sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            exact += __shfl_xor_sync(0xffffffffu, exact, d);
+        }
         if constexpr (AT_ONCE == 2) {
             o.x += __shfl_xor_sync(0xffffffffu, o.x, 16), o.y += __shfl_xor_sync(0xffffffffu, o.y, 16);
             o.z += __shfl_xor_sync(0xffffffffu, o.z, 16), o.w += __shfl_xor_sync(0xffffffffu, o.w, 16);
         }
         if (sub == 0)
-            finish4<DT>(p, q, it.kv_head, it.row0 + row, d4, o, top, sum);
+            finish4<DT>(p, q, it.kv_head, it.row0 + row, d4, o, top, sum, exact);
     }
 }
 

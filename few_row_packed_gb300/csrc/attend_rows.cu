@@ -53,20 +53,20 @@ struct Geo {
     // short, and more of them have to be under way
     static constexpr int CTAS = D == 64 ? 4 : 2;
     static constexpr int NST = 196608 / CTAS / STAGE;
-    static constexpr int SLOT = ROWS * (D + 2);             // floats of one partial result
+    static constexpr int SLOT = ROWS * (D + 3);             // floats of one partial result
     static constexpr int PLD = kBlock * 2 + 16;             // bytes of a row of probabilities
     // shared memory; from the probabilities to the barriers it is also the join's
     // scratch, which takes 2 floats a part for one row at least
     static constexpr int P_BUF = NST * STAGE;
     static constexpr int Q_BUF = P_BUF + ROWS * PLD + 16;   // the item's queries
     static constexpr int QLD = D * 2 + 16;                  // bytes of a row of them
-    static constexpr int M_BUF = Q_BUF + ROWS * QLD;        // [kKeyWarps][ROWS] block maxima, sums
-    static constexpr int BARS = M_BUF + kKeyWarps * ROWS * 4;
+    static constexpr int M_BUF = Q_BUF + ROWS * QLD;        // [kKeyWarps][ROWS] block maxima; sums, twice
+    static constexpr int BARS = M_BUF + 2 * kKeyWarps * ROWS * 4;
     static constexpr int FLAG = BARS + 2 * NST * 8;
     static constexpr int START = FLAG + 16;                 // where the CTA's share begins
     static constexpr int BYTES = START + 64;
     static_assert(P_BUF % 16 == 0 && Q_BUF % 16 == 0 && M_BUF % 16 == 0 && BARS % 8 == 0 &&
-                      START % 8 == 0 && sizeof(Start) <= 64 && (BARS - P_BUF) / 4 >= 2 * kAttendMaxCtas + 2,
+                      START % 8 == 0 && sizeof(Start) <= 64 && (BARS - P_BUF) / 4 >= 2 * kAttendMaxCtas + 3,
                   "layout");
 };
 
@@ -228,7 +228,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, Geo<D>::CTAS)
         for (int ks = 0; ks < D / 16; ++ks)
             ldsm4(q_lane + ks * 32, qf[ks]);
         float o[NT][4];
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        float m[2] = {-INFINITY, -INFINITY};
+        float l[2] = {0.f, 0.f}, x[2] = {0.f, 0.f};  // sums of rounded, of exact probabilities
 #pragma unroll
         for (int j = 0; j < NT; ++j)
             o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
@@ -303,12 +304,16 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, Geo<D>::CTAS)
                 }
                 const float ref = m[h] == -INFINITY ? 0.f : m[h];
                 l[h] *= shrink[h];
+                x[h] *= shrink[h];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const float a = ex2(s[j][h * 2] - ref), c = ex2(s[j][h * 2 + 1] - ref);
-                    l[h] += a + c;                               // of this warp's keys
+                    const uint32_t r = pack2<DT>(a, c);
+                    const float2 v = unpack2<DT>(r);
+                    x[h] += a + c;                               // of this warp's keys
+                    l[h] += v.x + v.y;
                     *reinterpret_cast<uint32_t*>(pbuf + (h * 8 + r0) * G::PLD +
-                                                 (warp * 16 + j * 8 + (lane & 3) * 2) * 2) = pack2<DT>(a, c);
+                                                 (warp * 16 + j * 8 + (lane & 3) * 2) * 2) = r;
                 }
             }
             if (__any_sync(0xffffffffu, moved)) {
@@ -345,8 +350,12 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, Geo<D>::CTAS)
         for (int h = 0; h < 2; ++h) {
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-            if ((lane & 3) == 0)
+            x[h] += __shfl_xor_sync(0xffffffffu, x[h], 1);
+            x[h] += __shfl_xor_sync(0xffffffffu, x[h], 2);
+            if ((lane & 3) == 0) {
                 tops[warp * ROWS + h * 8 + r0] = l[h];
+                tops[(kKeyWarps + warp) * ROWS + h * 8 + r0] = x[h];
+            }
         }
         named_bar_sync(1, TEAM);
         const bool whole = w.whole();
@@ -360,6 +369,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, Geo<D>::CTAS)
                 continue;
             const float* t = tops + r;
             const float sum = (t[0] + t[ROWS]) + (t[2 * ROWS] + t[3 * ROWS]);
+            const float exact = (t[4 * ROWS] + t[5 * ROWS]) + (t[6 * ROWS] + t[7 * ROWS]);
             const int i = row / p.group, head = w.head * p.group + row - i * p.group;
             const int64_t tok = w.q.q0 + i;
             const bool first = warp == 0 && (lane & 3) == 0;
@@ -373,7 +383,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, Geo<D>::CTAS)
                     store_row<2>(d + j * 8, &v);
                 }
                 if (p.lse && first)
-                    p.lse[tok * p.heads + head] = lse_of(m[h], sum);
+                    p.lse[tok * p.heads + head] = lse_of(m[h], exact);
             } else {
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
@@ -382,6 +392,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, Geo<D>::CTAS)
                 if (first) {
                     slot[ROWS * D + r] = m[h];
                     slot[ROWS * (D + 1) + r] = sum;
+                    slot[ROWS * (D + 2) + r] = exact;
                 }
             }
         }
@@ -444,7 +455,7 @@ size_t attend_rows_partial_floats(int dim, int sms)
     // two slots per CTA
     const int ctas = sms * (dim == 64 ? Geo<64>::CTAS : Geo<128>::CTAS);
     const int a = ctas < kAttendMaxCtas ? ctas : kAttendMaxCtas;
-    return (size_t)2 * a * 16 * (dim + 2);
+    return (size_t)2 * a * 16 * (dim + 3);
 }
 
 }  // namespace lbv

@@ -61,15 +61,16 @@ struct Geo {
     static constexpr int BARS = RING + NSLOT * SLOT;
     static constexpr int NBARS = 2 * NSLOT + 9 + 2 * kItems;
     static constexpr int STATS = (BARS + NBARS * 8 + 15) / 16 * 16;   // [2][128] m and sums of the streams
-    static constexpr int ITEMS = STATS + 2 * kTile * 8;     // ring of items
+    static constexpr int RATIOS = STATS + 2 * kTile * 8;    // [2][128] exact over rounded sums
+    static constexpr int ITEMS = RATIOS + 2 * kTile * 2;    // ring of items
     static constexpr int WORDS = ITEMS + kItems * 64;       // tensor-memory address
-    static constexpr int START = WORDS + 16;                // where the CTA's share begins
-    static constexpr int BYTES = START + 64;
-    static constexpr int PARTIAL = kRows * (D + 2);         // floats of one partial result
+    static constexpr int START = STATS;                     // the share's begin, before the first statistics
+    static constexpr int BYTES = WORDS + 16;
+    static constexpr int PARTIAL = kRows * (D + 3);         // floats of one partial result
     // tensor memory columns
     static constexpr uint32_t S0 = 0, O0 = 256;             // S of stream s at S0 + 128 s
     static_assert(BARS % 8 == 0 && STATS % 16 == 0 && ITEMS % 16 == 0 && WORDS % 16 == 0, "alignment");
-    static_assert(BYTES <= 227 * 1024 && sizeof(Start) <= 64, "shared memory");
+    static_assert(BYTES <= 227 * 1024 && sizeof(Start) <= 2 * kTile * 8, "shared memory");
 };
 
 // ---- tcgen05 ----
@@ -493,6 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_at = tmem + lanes + G::S0 + s * 128, o_at = tmem + lanes + G::O0;
         float2* stats = reinterpret_cast<float2*>(smem + G::STATS);
+        int16_t* ratios = reinterpret_cast<int16_t*>(smem + G::RATIOS);
         // scores are c times Q's: a negative scale negates Q, a zero one clears it
         const float c = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
         int done = 0;                    // blocks of this stream so far
@@ -517,7 +519,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int nb = w.nb;
             const int item_row = dual ? s * kTile + trow : trow;
             float m = -INFINITY;
-            float2 l = make_float2(0.f, 0.f);
+            // sums of the probabilities as they enter the product, and exact
+            float2 l = make_float2(0.f, 0.f), x = make_float2(0.f, 0.f);
             int mine = 0;                                            // blocks of this item
             {
                 const bool in = item_row < w.rows;
@@ -583,6 +586,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             r[k] = pack2<DT>(v.x, v.y);
                         }
                     };
+                    float2 block = make_float2(0.f, 0.f);            // the block's sum
+                    bool heavy = false;                              // one key is half of the sum or more
                     if (!idle) {
                         // the first 32 keys with the reference as it is, while the block's
                         // maximum is found; once more if that moves the reference
@@ -600,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (__any_sync(0xffffffffu, moved)) {
                             const float f = moved ? ex2(m - top) : 1.f;
                             m = moved ? top : m;
-                            l.x *= f, l.y *= f;
+                            l.x *= f, l.y *= f, x.x *= f, x.y *= f;
                             if (mine > 0) {
                                 wait(o_done(s), (uint32_t)((done - 1) & 1));
                                 tc_fence_after();
@@ -617,10 +622,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             exps(0);
                         }
-                        l = add2(l, part);
+                        heavy = 2.f * ex2(top - m) >= x.x + x.y;
+                        block = part;
                         tmem_st16(s_at, r);
                         exps(1);
-                        l = add2(l, part);
+                        block = add2(block, part);
                         tmem_st16(s_at + 16, r);
                         tmem_wait_st();
                     }
@@ -629,13 +635,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0)
                         mbar_arrive(p_full(s, 0));
                     if (!idle) {
+                        const bool few = __any_sync(0xffffffffu, heavy);
 #pragma unroll
                         for (int e = 2; e < 4; ++e) {
                             exps(e);
-                            l = add2(l, part);
+                            block = add2(block, part);
                             tmem_st16(s_at + e * 16, r);
                         }
                         tmem_wait_st();
+                        x = add2(x, block);
+                        // What V is multiplied with is rounded: a row that few keys dominate is
+                        // divided by the sum of the rounded values, so that it gets those keys'
+                        // values; elsewhere the roundings cancel.
+                        if (few) {
+                            block = make_float2(0.f, 0.f);
+#pragma unroll 1
+                            for (int e = 0; e < 4; ++e) {
+                                float v[16];
+                                tmem_ld16(s_at + e * 16, v);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < 16; ++k)
+                                    block = add2(block, unpack2<DT>(__float_as_uint(v[k])));
+                            }
+                        }
+                        l = add2(l, block);
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -652,9 +676,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 enter(items[(it + 1) % kItems]);
             if (mine > 0)
                 wait(o_done(s), (uint32_t)((done - 1) & 1));
-            float sum = l.x + l.y, f0 = 1.f, f1 = 0.f;   // factors of this row in O_0 and O_1
+            float sum = l.x + l.y, exact = x.x + x.y;
+            float f0 = 1.f, f1 = 0.f;                    // factors of this row in O_0 and O_1
             if (!dual) {
                 stats[s * kTile + trow] = make_float2(m, sum);
+                // the sums differ by less than 2^-8 of them, kept to 2^-23
+                ratios[s * kTile + trow] =
+                    sum > 0.f ? (int16_t)max(-32767, min(32767, __float2int_rn((exact / sum - 1.f) * 4194304.f)))
+                              : (int16_t)0;
                 tc_fence_before();
                 named_bar_sync(1, 256);
                 const float2 a = stats[trow], b = stats[kTile + trow];
@@ -662,6 +691,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 f0 = a.x == -INFINITY ? 0.f : ex2(a.x - m);
                 f1 = b.x == -INFINITY ? 0.f : ex2(b.x - m);
                 sum = f0 * a.y + f1 * b.y;
+                exact = f0 * a.y * (1.f + ratios[trow] * (1.f / 4194304.f)) +
+                        f1 * b.y * (1.f + ratios[kTile + trow] * (1.f / 4194304.f));
             }
             tc_fence_after();
             const bool in = item_row < w.rows, whole = w.whole();
@@ -705,10 +736,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (in && (dual || s == 0)) {
                 if (whole && p.lse) {
-                    p.lse[tok * p.heads + head] = lse_of(m, sum);
+                    p.lse[tok * p.heads + head] = lse_of(m, exact);
                 } else if (!whole) {
                     slot[kRows * D + item_row] = m;
                     slot[kRows * (D + 1) + item_row] = sum;
+                    slot[kRows * (D + 2) + item_row] = exact;
                 }
             }
             if (!whole && tid == 128 && w.c0 == (int)blockIdx.x)
@@ -759,7 +791,7 @@ cudaError_t launch_attend_tiles(const AttendParams& p, const CUtensorMap& kmap,
 
 size_t attend_tiles_partial_floats(int dim, int sms)
 {
-    return (size_t)2 * (sms < kAttendMaxCtas ? sms : kAttendMaxCtas) * kRows * (dim + 2);
+    return (size_t)2 * (sms < kAttendMaxCtas ? sms : kAttendMaxCtas) * kRows * (dim + 3);
 }
 
 }  // namespace lbv
