@@ -20,20 +20,36 @@
 //      thousand values is at most the row's k-th, and their weights sum to no more
 //      than the row's above the same logit, so the first bin that satisfies top-k
 //      or top-p on them lies at or below the true cut;
-//   3. the few threads whose maximum lies above the bound hand it to the first CTA;
-//      those whose next largest does too read their logits again (from L2) and hand
-//      over all above it ("candidates").  The other CTAs are done;
+//   3. the few threads whose maximum lies above the bound list it; those whose next
+//      largest does too read their logits again (from L2) and list all above it
+//      ("candidates").  The lists of all CTAs are joined in the first, the others are
+//      done;
 //   4. it sorts them by rank; a running sum of their weights gives how many are
 //      kept; and sorts these by index, where a running sum gives the token.
-// Where the thread maxima do not reach the cut (a large k, a flat row with a
-// large top-p), step 2 is tried again with all logits.  Where the candidates do
-// not fit the list, tau is found by a search over the bits of the
-// (order-preserving) keys, counting and summing above trial values, two bits a
-// round, with a cluster barrier in each.  top-p without top-k needs the row's total
-// weight: a second pass over the slice.
+// top-p without top-k needs the row's total weight: a second pass over the slice.
+// Where the thread maxima do not reach the cut (a large k, a flat row with a large
+// top-p) or the candidates do not fit the list, a finer histogram counts and weighs
+// all tokens above the bound.  Down to the bin that holds tau they may fit after all;
+// if not, the tokens of that bin alone are listed and sorted, which gives tau, and the
+// token is drawn from the slices: one pass for the weight of each, and two short ones
+// by the CTA that holds the token.  Where even the bin does not fit (thousands of
+// equal logits), tau is found by a search over the bits of the (order-preserving)
+// keys, counting and summing above trial values, two bits a round.  Rows without
+// rules are drawn from the slices straight away.
 //
 // Nothing of the row stays on chip, so that four CTAs share an SM: while one
 // waits at a barrier, the others' loads keep memory busy.
+//
+// What bounds it: for few rows the chain of barriers and latencies, for many the
+// instructions of a pass (some 30 per logit and exp) and of the sort, then memory.
+// Time of a call with 256 rows of 128,256 bf16 logits / 8 rows of 151,936 fp32 / 1 row
+// of 128,256 fp32, in us, where reading the logits once takes 9.7 / 0.7 / 0.1:
+//     temperature 0 (the maximum)      30 /  9 /  9
+//     top-k 50                         67 / 17 / 17
+//     no rule                         156 / 33 / 27
+//     top-p 0.5, <= 2048 kept         367 / 83 / 46
+//     top-p 0.9, some 15,000 kept     458 / 79 / 62    (by the bit search: 1125 / 207 / 133)
+//     top-k 5000                      345 / 65 / 51    (by the bit search: 1031 / 188 / 125)
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -51,8 +67,11 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBins = kThreads;            // one thread per bin
 constexpr int kList = 8 * kThreads;        // candidates the first CTA can take
 constexpr int kAhead = 4;                  // vectors of a thread on their way
+constexpr int kParts = 8;                  // of a warp's tokens, in the index-order sum
 constexpr int kMaxCluster = 16;
 constexpr float kBinsPerNat = 8.f;
+constexpr int kFine = 4 * kThreads;        // bins of a row with many candidates
+constexpr float kFinePerNat = 32.f;
 constexpr float kNegInf = -__builtin_huge_valf();
 
 // Vectors of 16 bytes (and their two mask words) on the way to each thread.
@@ -61,21 +80,33 @@ struct Ring {
     uint32_t words[kAhead][kThreads][2];
 };
 
+// Tokens by (m - l) r in steps of 1/32: how many, and their weight.
+struct Fine {
+    uint64_t sum[kFine];
+    unsigned count[kFine];
+};
+
 struct Shared {
-    uint64_t red[2][kWarps][4];            // block reductions, two in flight
-    uint64_t all[2][kMaxCluster][4];       // cluster reductions: one slot per CTA
+    uint64_t red[3][kWarps][4];            // of reductions, by their buffer
+    uint64_t all[3][kMaxCluster][4];       // one slot per CTA
     unsigned hist[kBins];
     uint64_t tops[kMaxCluster];
     uint64_t sums[kWarps];                 // drawn weight of each warp's part
     int counts[kMaxCluster];               // candidates of each CTA
     int found;                             // of this CTA so far
-    int listed;                            // of all CTAs so far (in the first)
     unsigned scan[kWarps];
     int pick;                              // place of the drawn token
     float pick_prob;
-    uint64_t list[kList];                  // candidates: key, then the index's complement
+    int bin, bin_count, above_count;       // a bin of Fine, its tokens, and what lies above
+    uint64_t above_sum;
+    uint64_t result[3];                    // tau, its ties, the weight down to them
+    union {
+        uint64_t list[kList];              // candidates: key, then the index's complement
+        Fine fine;
+    };
     union {
         Ring ring;                         // of the passes over the slice
+        Fine merged;                       // the cluster's, between them
         uint64_t exchange[2][kList];       // of the sort's steps, after them
     };
 };
@@ -134,21 +165,27 @@ __device__ __forceinline__ uint64_t shfl_add(uint64_t v)
 
 struct Ctx {
     Shared* sh;
-    int tid, warp, lane, rank, nctas, round;
+    int tid, warp, lane, rank, nctas;
 };
 
-// Sums N values over the CTA's threads, or (wide) the cluster's; every thread
-// gets the result.  below[] (optional): the sums over the CTAs of lower rank.
+// Sums N values over the cluster's threads; every thread gets the result.  below[]
+// and own[] (optional): the sums over the CTAs of lower rank, and over this one.
+// buffer: another one than the last call's, unless a cluster barrier came between.
+// (Functions that are not inlined take their structures by value: one whose address
+// is taken lives in memory, and the passes over the logits would read it each time.)
 template <int N>
-__device__ __noinline__ void reduce(Ctx& c, bool wide, uint64_t (&v)[N], uint64_t* below = nullptr)
+__device__ __noinline__ void reduce(Ctx c, int buffer, uint64_t (&v)[N], uint64_t* below = nullptr,
+                                    uint64_t* own = nullptr)
 {
     Shared& sh = *c.sh;
-    const int b = c.round++ & 1;
+    auto& red = sh.red[buffer];
+    auto& all = sh.all[buffer];
+    cg::cluster_group cl = cg::this_cluster();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         v[i] = shfl_add(v[i]);
         if (c.lane == 0)
-            sh.red[b][c.warp][i] = v[i];
+            red[c.warp][i] = v[i];
     }
     __syncthreads();
 #pragma unroll
@@ -156,32 +193,27 @@ __device__ __noinline__ void reduce(Ctx& c, bool wide, uint64_t (&v)[N], uint64_
         v[i] = 0;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w)
-            v[i] += sh.red[b][w][i];
+            v[i] += red[w][i];
+        if (own)
+            own[i] = v[i];
     }
-    if (wide) {
-        cg::cluster_group cl = cg::this_cluster();
-        if (c.tid < c.nctas) {
-            Shared* to = cl.map_shared_rank(c.sh, c.tid);
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                to->all[b][c.rank][i] = v[i];
-        }
-        cl.sync();
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            uint64_t t = 0, lo = 0;
-            for (int r = 0; r < c.nctas; ++r) {
-                lo = r == c.rank ? t : lo;
-                t += sh.all[b][r][i];
-            }
-            v[i] = t;
-            if (below)
-                below[i] = lo;
-        }
-    } else if (below) {
+    if (c.tid < c.nctas) {
+        uint64_t* to = &cl.map_shared_rank(c.sh, c.tid)->all[buffer][c.rank][0];
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            below[i] = 0;
+            to[i] = v[i];
+    }
+    cl.sync();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        uint64_t t = 0, lo = 0;
+        for (int r = 0; r < c.nctas; ++r) {
+            lo = r == c.rank ? t : lo;
+            t += all[r][i];
+        }
+        v[i] = t;
+        if (below)
+            below[i] = lo;
     }
 }
 
@@ -301,7 +333,7 @@ struct Kept {
 // The largest key t for which test(t, sum of f over the tokens with key >= t)
 // holds; it holds at 0.  f(x) is a count or a weight, test is monotone in t.
 template <typename D, typename F, typename Test>
-__device__ __forceinline__ uint32_t search(Ctx& c, const D& d, F f, Test test)
+__device__ __forceinline__ uint32_t search(Ctx c, const D& d, F f, Test test)
 {
     uint32_t t = 0;
     for (int bit = 30; bit >= 0; bit -= 2) {
@@ -317,7 +349,7 @@ __device__ __forceinline__ uint32_t search(Ctx& c, const D& d, F f, Test test)
             }
         });
         uint64_t v[3] = {s1, s2, s3};
-        reduce<3>(c, true, v);
+        reduce<3>(c, (bit >> 1) & 1, v);
         t = test(t3, v[2]) ? t3 : test(t2, v[1]) ? t2 : test(t1, v[0]) ? t1 : t;
     }
     return t;
@@ -325,7 +357,7 @@ __device__ __forceinline__ uint32_t search(Ctx& c, const D& d, F f, Test test)
 
 // tau and its ties by search.  total: the weight of the whole row (without top-k).
 template <typename D>
-__device__ __noinline__ Kept select(Ctx& c, const D& d, const Row& row, uint64_t total)
+__device__ __noinline__ Kept select(Ctx c, D d, Row row, uint64_t total)
 {
     Kept kept = {0u, ~0ull};
     uint32_t tau_k = 0;
@@ -343,7 +375,7 @@ __device__ __noinline__ Kept select(Ctx& c, const D& d, const Row& row, uint64_t
             }
         });
         uint64_t v[2] = {n, sum};
-        reduce<2>(c, true, v);
+        reduce<2>(c, 2, v);                            // a search uses 1, 0, ..., 1, 0
         kept.tau = tau_k;
         kept.ties = k - v[0];
         total = v[1] + kept.ties * weight(of_key(tau_k));    // a masked tau weighs 0
@@ -358,81 +390,112 @@ __device__ __noinline__ Kept select(Ctx& c, const D& d, const Row& row, uint64_t
         uint64_t sum = 0;
         each<2>(d, c.tid, c.sh->ring, [&](float x, int) { sum += key_of(x) > tau ? weight(x) : 0; });
         uint64_t v[1] = {sum};
-        reduce<1>(c, true, v);
+        reduce<1>(c, 1, v);
         const uint64_t w = weight(of_key(tau));
         const uint64_t j = w ? (limit - v[0] + w - 1) / w : 1;
         kept.ties = tau == tau_k && j > kept.ties ? kept.ties : j;
         kept.tau = tau;
     }
+    cg::this_cluster().sync();                         // every buffer is free again
     return kept;
 }
 
-// Draws from the kept tokens of the domain in index order.  Returns the place
-// in the domain, or -1 where another CTA's slice holds it; *prob its
-// probability among the kept ones.
-template <typename D>
-__device__ __noinline__ int draw(Ctx& c, const D& d, const Row& row, const Kept& kept, float* prob)
+// Draws from the kept tokens of all slices in index order: one pass gives each CTA's
+// weight, and the CTA in which the running sum passes u's share looks for the token.
+// Returns its place in the slice, or -1 in the other CTAs; *prob its probability
+// among the kept ones.
+template <int DT>
+__device__ __noinline__ int draw(Ctx c, Slice<DT> d, Row row, Kept kept, float* prob)
 {
     Shared& sh = *c.sh;
+    auto weight = [&](float x) {
+        const float w = weight_f(x, row.top, row.draw_r);
+        const float f = row.filter_r == row.draw_r || row.min_p <= 0.f ? w : weight_f(x, row.top, row.filter_r);
+        return f >= row.min_p || row.min_p <= 0.f ? whole(w) : 0;
+    };
+    uint64_t sum = 0;
+    unsigned equal = 0;
+    each<DT == LBV_F32 ? 4 : 8>(d, c.tid, sh.ring, [&](float x, int) {
+        const uint32_t k = key_of(x);
+        sum += k > kept.tau ? weight(x) : 0;
+        equal += k == kept.tau;
+    });
+    uint64_t all[2] = {sum, equal}, below[2], here[2];
+    reduce<2>(c, 2, all, below, here);
+    const uint64_t tie_w = all[1] ? weight(of_key(kept.tau)) : 0;
+    const uint64_t ties_below = min(kept.ties, below[1]), ties_upto = min(kept.ties, below[1] + here[1]);
+    const uint64_t total = all[0] + min(kept.ties, all[1]) * tie_w;
+    uint64_t at = below[0] + ties_below * tie_w;
+    uint32_t f = fraction24(row.u);
+    f = f > 16777215u ? 16777215u : f;
+    const uint64_t target = part(f, total);
+    if (target < at || target >= at + here[0] + (ties_upto - ties_below) * tie_w)
+        return -1;
     const int groups = (d.n + 31) / 32, per = (groups + kWarps - 1) / kWarps;
     const int g0 = min(c.warp * per, groups), g1 = min(g0 + per, groups);
     const unsigned before = (1u << c.lane) - 1;
     // ties in index order ahead of this warp
-    uint64_t tie_base = 0;
-    if (kept.ties != ~0ull) {
+    uint64_t tie_base = below[1];
+    if (kept.ties < all[1]) {
         unsigned mine = 0;
+#pragma unroll 8
         for (int g = g0; g < g1; ++g) {
             const int i = g * 32 + c.lane;
             mine += i < d.n && key_of(d.get(i)) == kept.tau;
         }
         mine = __reduce_add_sync(0xffffffffu, mine);
-        __syncthreads();
         if (c.lane == 0)
             sh.scan[c.warp] = mine;
-        uint64_t v[1] = {c.lane == 0 ? mine : 0u}, lo[1];
-        reduce<1>(c, true, v, lo);      // its barrier orders the scan array
-        tie_base = lo[0];
+        __syncthreads();
         for (int w = 0; w < c.warp; ++w)
             tie_base += sh.scan[w];
     }
-    // visits the warp's tokens in index order: f(place, weight) by all lanes
-    auto visit = [&](auto f) {
-        uint64_t ties = tie_base;
-#pragma unroll 4
-        for (int g = g0; g < g1; ++g) {
+    // visits groups [a, b) of the warp's in index order, `ties` of tau's before them:
+    // f(place, weight) by all lanes
+    auto visit = [&](int a, int b, uint64_t& ties, auto f) {
+#pragma unroll 8
+        for (int g = a; g < b; ++g) {
             const int i = g * 32 + c.lane;
             const float x = i < d.n ? d.get(i) : kNegInf;
             const uint32_t k = key_of(x);
             const bool tie = i < d.n && k == kept.tau;
             const unsigned tied = __ballot_sync(0xffffffffu, tie);
-            const bool in = i < d.n && (k > kept.tau || (tie && ties + __popc(tied & before) < kept.ties));
+            const bool in = k > kept.tau || (tie && ties + __popc(tied & before) < kept.ties);
             ties += __popc(tied);
-            uint64_t w = 0;
-            if (in && weight_f(x, row.top, row.filter_r) >= row.min_p)
-                w = whole(weight_f(x, row.top, row.draw_r));
-            if (f(i, w))
+            if (f(i, in ? weight(x) : 0))
                 return;
         }
     };
-    uint64_t sum = 0;
-    visit([&](int, uint64_t w) { sum += w; return false; });
-    sum = shfl_add(sum);
-    __syncthreads();
+    // the weight of the warp's tokens, by parts, with the ties before each
+    const int step = (g1 - g0 + kParts - 1) / kParts;
+    uint64_t ties = tie_base, my_sum = 0, my_ties = 0;              // of part `lane`
+    sum = 0;
+    for (int q = 0; q < kParts; ++q) {
+        const int a = min(g0 + q * step, g1), b = min(a + step, g1);
+        my_ties = c.lane == q ? ties : my_ties;
+        uint64_t s = 0;
+        visit(a, b, ties, [&](int, uint64_t w) { s += w; return false; });
+        s = shfl_add(s);
+        my_sum = c.lane == q ? s : my_sum;
+        sum += s;
+    }
     if (c.lane == 0)
         sh.sums[c.warp] = sum;
     if (c.tid == 0)
         sh.pick = -1;
-    uint64_t v[1] = {c.lane == 0 ? sum : 0}, lo[1];
-    reduce<1>(c, true, v, lo);
-    const uint64_t total = v[0];
-    uint64_t at = lo[0];
+    __syncthreads();
     for (int w = 0; w < c.warp; ++w)
         at += sh.sums[w];
-    uint32_t f = fraction24(row.u);
-    f = f > 16777215u ? 16777215u : f;
-    const uint64_t target = part(f, total);
     if (target >= at && target < at + sum) {
-        visit([&](int i, uint64_t w) {
+        int q = 0;
+        uint64_t s = __shfl_sync(0xffffffffu, my_sum, 0);
+        while (target >= at + s) {
+            at += s;
+            s = __shfl_sync(0xffffffffu, my_sum, ++q);
+        }
+        ties = __shfl_sync(0xffffffffu, my_ties, q);
+        const int a = min(g0 + q * step, g1), b = min(a + step, g1);
+        visit(a, b, ties, [&](int i, uint64_t w) {
             uint64_t upto = w;
 #pragma unroll
             for (int s = 1; s < 32; s <<= 1) {
@@ -527,7 +590,7 @@ __device__ __forceinline__ int power_above(int n)
 }
 
 // The block's sum of v, and in `before` that of the threads before this one.
-__device__ __noinline__ uint64_t block_scan(Ctx& c, uint64_t v, uint64_t& before)
+__device__ __noinline__ uint64_t block_scan(Ctx c, uint64_t v, uint64_t& before)
 {
     uint64_t upto = v;
 #pragma unroll
@@ -549,9 +612,241 @@ __device__ __noinline__ uint64_t block_scan(Ctx& c, uint64_t v, uint64_t& before
     return all;
 }
 
+// Lists in the first CTA the tokens that visit(found) finds in each slice; returns
+// their number, and lists nothing where they are more than fit.
+template <typename Visit>
+__device__ __forceinline__ int gather(Ctx c, int begin, Visit visit)
+{
+    Shared& sh = *c.sh;
+    cg::cluster_group cl = cg::this_cluster();
+    visit([&](float x, int i) {
+        const int at = atomicAdd(&sh.found, 1);
+        if (at < kList)
+            sh.list[at] = ((uint64_t)key_of(x) << 32) | (0xFFFFFFFFu - (uint32_t)(begin + i));
+    });
+    __syncthreads();
+    const int here = sh.found;
+    if (c.tid < c.nctas)
+        cl.map_shared_rank(&sh, c.tid)->counts[c.rank] = here;
+    cl.sync();
+    int n = 0, before = 0;
+    for (int r = 0; r < c.nctas; ++r) {
+        before = r == c.rank ? n : before;
+        n += sh.counts[r];
+    }
+    if (n <= kList) {
+        Shared* to = cl.map_shared_rank(&sh, 0);
+        if (c.rank > 0)
+            for (int i = c.tid; i < here; i += kThreads)
+                to->list[before + i] = sh.list[i];
+        cl.sync();
+    }
+    return n;
+}
+
+// For a row with many candidates, all of them >= cut.  Returns kSearch where the finer
+// histogram does not resolve it, kByValue with tau and its ties, or the number of
+// candidates where, with the finer bound, they fit the list after all.
+// total: the weight of the whole row (without top-k).
+constexpr int kSearch = -2, kByValue = -1;
+
+template <int DT>
+__device__ __noinline__ int select_binned(Ctx c, Slice<DT> slice, Row row, float cut,
+                                          uint64_t total, int begin, Kept& kept)
+{
+    Shared& sh = *c.sh;
+    cg::cluster_group cl = cg::this_cluster();
+    const bool by_sum = row.top_p < 1.f;
+    const float scale = row.filter_r * kFinePerNat;
+    auto bin_of = [&](float v) {                       // below the cut: none of the bins
+        const float b = v == row.top ? 0.f : (row.top - v) * scale;
+        return v >= cut && b < (float)kFine ? (int)b : kFine;
+    };
+    for (int i = c.tid; i < kFine; i += kThreads) {
+        sh.fine.sum[i] = 0;
+        sh.fine.count[i] = 0;
+    }
+    __syncthreads();
+    each<2>(slice, c.tid, sh.ring, [&](float x, int) {
+        const int b = bin_of(x);
+        if (b < kFine) {
+            atomicAdd(&sh.fine.count[b], 1u);
+            const uint64_t w = by_sum ? whole(weight_f(x, row.top, row.filter_r)) : 0;
+            if (w)
+                atomicAdd(reinterpret_cast<unsigned long long*>(&sh.fine.sum[b]), (unsigned long long)w);
+        }
+    });
+    // Each CTA merges its share of the bins (nctas is a power of two): neighbouring
+    // lanes read a bin of all CTAs, and hand each the sum.
+    __syncthreads();
+    cl.sync();
+    {
+        Shared* peer = cl.map_shared_rank(&sh, c.tid & (c.nctas - 1));
+        uint64_t s[4];
+        unsigned n[4];
+        int b[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            b[q] = (c.rank * kFine + q * kThreads + c.tid) / c.nctas;
+            s[q] = peer->fine.sum[b[q]];
+            n[q] = peer->fine.count[b[q]];
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            for (int d = c.nctas / 2; d > 0; d >>= 1) {
+                s[q] += __shfl_xor_sync(0xffffffffu, s[q], d);
+                n[q] += __shfl_xor_sync(0xffffffffu, n[q], d);
+            }
+            peer->merged.sum[b[q]] = s[q];
+            peer->merged.count[b[q]] = n[q];
+        }
+    }
+    cl.sync();
+    // this thread's four bins, and what lies above them
+    uint64_t sums[4], sum_at, count_at;
+    unsigned counts[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        sums[q] = sh.merged.sum[4 * c.tid + q];
+        counts[q] = sh.merged.count[4 * c.tid + q];
+    }
+    block_scan(c, (sums[0] + sums[1]) + (sums[2] + sums[3]), sum_at);
+    block_scan(c, (counts[0] + counts[1]) + (counts[2] + counts[3]), count_at);
+    // the bin in which the running count (or weight) reaches `want`
+    auto locate = [&](bool by_count, uint64_t want) {
+        __syncthreads();
+        if (c.tid == 0)
+            sh.bin = -1;
+        __syncthreads();
+        uint64_t n = count_at, s = sum_at;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint64_t from = by_count ? n : s, to = by_count ? n + counts[q] : s + sums[q];
+            if (from < want && want <= to) {
+                sh.bin = 4 * c.tid + q;
+                sh.bin_count = (int)counts[q];
+                sh.above_count = (int)n;
+                sh.above_sum = s;
+            }
+            n += counts[q];
+            s += sums[q];
+        }
+        __syncthreads();
+        return sh.bin;
+    };
+    // the tokens of bins [b0, b1] into the first CTA's list
+    auto list_bins = [&](int b0, int b1) {
+        return gather(c, begin, [&](auto found) {
+            each<2>(slice, c.tid, sh.ring, [&](float x, int i) {
+                const int b = bin_of(x);
+                if (b >= b0 && b <= b1)
+                    found(x, i);
+            });
+        });
+    };
+    // tau by the tokens of a bin in order of rank: the first `most` of them, or as
+    // many as bring the weight from `above` up to `limit`
+    int listed = -1;
+    auto resolve = [&](int bin, int n, uint64_t above, int most, uint64_t limit) {
+        if (c.tid == 0)
+            sh.found = 0;
+        cl.sync();                                     // the last results have been read
+        if (bin != listed)
+            list_bins(bin, bin);
+        if (c.rank == 0) {
+            if (bin != listed) {
+                const int n2 = power_above(n);
+                for (int i = n + c.tid; i < n2; i += kThreads)
+                    sh.list[i] = 0;
+                __syncthreads();
+                sort_list(sh, n2, c.tid);
+            }
+            const int per = (most + kThreads - 1) / kThreads, i0 = c.tid * per, i1 = min(i0 + per, most);
+            uint64_t mine = 0, at;
+            for (int i = i0; i < i1; ++i)
+                mine += whole(weight_f(of_key((uint32_t)(sh.list[i] >> 32)), row.top, row.filter_r));
+            const uint64_t all = block_scan(c, mine, at);
+            if (c.tid == 0)
+                sh.pick = most;
+            __syncthreads();
+            at += above;
+            if (at < limit && limit <= at + mine)
+                for (int i = i0; i < i1; ++i) {
+                    at += whole(weight_f(of_key((uint32_t)(sh.list[i] >> 32)), row.top, row.filter_r));
+                    if (at >= limit) {
+                        sh.pick = i + 1;
+                        break;
+                    }
+                }
+            __syncthreads();
+            const int taken = sh.pick;
+            const uint32_t tau = (uint32_t)(sh.list[taken - 1] >> 32);
+            uint64_t greater = 0, unused;
+            for (int i = c.tid; i < n; i += kThreads)
+                greater += (uint32_t)(sh.list[i] >> 32) > tau;
+            greater = block_scan(c, greater, unused);
+            if (c.tid < c.nctas) {
+                Shared* o = cl.map_shared_rank(&sh, c.tid);
+                o->result[0] = tau;
+                o->result[1] = (uint64_t)taken - greater;
+                o->result[2] = above + all;
+            }
+        }
+        listed = bin;
+        cl.sync();
+        kept.tau = (uint32_t)sh.result[0];
+        kept.ties = sh.result[1];
+    };
+    // Below a cut that min-p gave neither top-k nor top-p need be reached: then min-p
+    // alone decides, and all tokens are kept here.
+    const int unreached = cut > kNegInf ? kByValue : kSearch;
+    int bin_k = kFine, count_k = 0, need = 0;
+    uint64_t above_k = 0;
+    auto list_down_to = [&](int bin) {
+        if (c.tid == 0)
+            sh.found = 0;
+        cl.sync();                                     // the histograms have been read
+        return list_bins(0, bin);
+    };
+    if (row.k > 0) {
+        bin_k = locate(true, (uint64_t)row.k);
+        if (bin_k < 0)
+            return unreached;
+        count_k = sh.bin_count;
+        above_k = sh.above_sum;
+        need = row.k - sh.above_count;
+        if (sh.above_count + count_k <= kList)
+            return list_down_to(bin_k);
+        if (count_k > kList)
+            return kSearch;
+        resolve(bin_k, count_k, above_k, need, ~0ull);
+        total = sh.result[2];
+    }
+    if (by_sum) {
+        const uint64_t limit = part(fraction24(row.top_p), total);
+        if (limit == 0) {
+            kept = Kept{key_of(row.top), 1};
+            return kByValue;
+        }
+        const int bin = locate(false, limit);
+        if (bin < 0)
+            return unreached;
+        const int count = sh.bin_count;
+        if (row.k == 0 && sh.above_count + count <= kList)
+            return list_down_to(bin);
+        if (count > kList)
+            return kSearch;
+        if (bin < bin_k)
+            resolve(bin, count, sh.above_sum, count, limit);
+        else
+            resolve(bin_k, count_k, above_k, need, limit);
+    }
+    return kByValue;
+}
+
 // Draws from the n candidates of the list, of which every kept token is one.
 // total: the weight of the whole row (without top-k).
-__device__ __forceinline__ void draw_listed(Ctx& c, const Row& row, bool by_sum, uint64_t total, int n,
+__device__ __forceinline__ void draw_listed(Ctx c, const Row& row, bool by_sum, uint64_t total, int n,
                                             const SampleParams& p, int m)
 {
     Shared& sh = *c.sh;
@@ -620,7 +915,6 @@ __global__ void __launch_bounds__(kThreads, 4) lbv_sample_kernel(const __grid_co
     c.lane = c.tid & 31;
     c.nctas = p.ctas;
     c.rank = blockIdx.x % p.ctas;
-    c.round = 0;
     const int m = blockIdx.x / p.ctas;
     const int begin = min(c.rank * p.slice, p.N);
 
@@ -651,7 +945,7 @@ __global__ void __launch_bounds__(kThreads, 4) lbv_sample_kernel(const __grid_co
     });
     sh.hist[c.tid] = 0;
     if (c.tid == 0)
-        sh.found = sh.listed = 0;
+        sh.found = 0;
     uint64_t best = 0;
     if (slice.n > 0)                                   // a row of -inf has a key above 0 too
         best = ((uint64_t)key_of(high) << 32) | (0xFFFFFFFFu - (uint32_t)(begin + high_at));
@@ -690,111 +984,84 @@ __global__ void __launch_bounds__(kThreads, 4) lbv_sample_kernel(const __grid_co
     Kept kept = {0u, ~0ull};
     const bool by_rank = row.k > 0 && row.k < p.N, by_sum = row.top_p < 1.f;
     row.k = by_rank ? row.k : 0;
-    uint64_t total = 0;
-    if (by_rank || by_sum) {
+    if (by_rank || by_sum || row.min_p > 0.f) {
+        // ---- the histogram, and with it the row's weight ----
         const float scale = row.filter_r * kBinsPerNat;
-        auto bin_of = [&](float v) {                   // bin 0 holds the maximum
-            const float b = v == row.top ? 0.f : (row.top - v) * scale;
-            return b < (float)(kBins - 1) ? (int)b : kBins - 1;
-        };
-        Shared* to = cl.map_shared_rank(&sh, 0);
-        for (int all = 0; all < 2; ++all) {
-            // ---- the histogram, and with it (once) the row's weight ----
-            if (all == 0) {
-                const int b = bin_of(high);
-                if (b < kBins - 1)
-                    atomicAdd(&sh.hist[b], 1u);
-                if (by_rank) {
-                    __syncthreads();
-                    cl.sync();
-                } else {
-                    uint64_t sum = 0;
-                    each<DT == LBV_F32 ? 4 : 8>(slice, c.tid, sh.ring, [&](float x, int) {
-                        sum += whole(weight_f(x, row.top, row.filter_r));
-                    });
-                    uint64_t v[1] = {sum};
-                    reduce<1>(c, true, v);             // orders the histograms too
-                    total = v[0];
-                }
-            } else {
-                cl.sync();                             // the first one has been read
-                sh.hist[c.tid] = 0;
-                if (c.tid == 0)
-                    sh.found = sh.listed = 0;
-                __syncthreads();
-                each<2>(slice, c.tid, sh.ring, [&](float x, int) {
-                    const int b = bin_of(x);
-                    if (b < kBins - 1)
-                        atomicAdd(&sh.hist[b], 1u);
-                });
-                cl.sync();
-            }
-            unsigned h[kMaxCluster], here = 0;
-#pragma unroll
-            for (int r = 0; r < kMaxCluster; ++r)
-                h[r] = r < c.nctas ? cl.map_shared_rank(&sh, r)->hist[c.tid] : 0u;
-#pragma unroll
-            for (int r = 0; r < kMaxCluster; ++r)
-                here += h[r];
-            // The last bin a kept token can be in: the k-th token's; the one
-            // where the weights, each taken at its bin's lower edge less a little
-            // for rounding, pass top-p's share; min-p's.
-            unsigned count = here;
-            float low = (float)here * __expf(-(float)(c.tid + 1) / kBinsPerNat) * 0.999f;
-#pragma unroll
-            for (int s = 1; s < 32; s <<= 1) {
-                const unsigned o = __shfl_up_sync(0xffffffffu, count, s);
-                const float f = __shfl_up_sync(0xffffffffu, low, s);
-                count += c.lane >= s ? o : 0;
-                low += c.lane >= s ? f : 0.f;
-            }
-            if (c.lane == 31) {
-                sh.scan[c.warp] = count;
-                sh.red[0][c.warp][3] = __float_as_uint(low);
-            }
+        const float depth = high == row.top ? 0.f : (row.top - high) * scale;  // bin 0 holds the maximum
+        if (depth < (float)(kBins - 1))
+            atomicAdd(&sh.hist[(int)depth], 1u);
+        uint64_t total = 0;
+        if (by_sum && !by_rank) {
+            uint64_t sum = 0;
+            each<DT == LBV_F32 ? 4 : 8>(slice, c.tid, sh.ring, [&](float x, int) {
+                sum += whole(weight_f(x, row.top, row.filter_r));
+            });
+            uint64_t v[1] = {sum};
+            reduce<1>(c, 2, v);                        // orders the histograms too
+            total = v[0];
+        } else {
             __syncthreads();
-            for (int w = 0; w < c.warp; ++w) {
-                count += sh.scan[w];
-                low += __uint_as_float((uint32_t)sh.red[0][w][3]);
-            }
-            bool reach = by_rank ? count >= (unsigned)row.k
-                                 : low >= row.top_p * __ull2float_rn(total) * 9.094947e-13f;   // 2^-40
-            // (top-p takes its share of all that top-k kept, min-p or not)
-            const float z_min = row.min_p > 0.f && !(by_rank && by_sum) ? -logf(row.min_p) : 1e30f;
-            reach = reach || (float)c.tid > z_min * kBinsPerNat + 2.f;
-            const int last = __syncthreads_count(!reach);      // bins before the first that reaches
-            if (last >= kBins - 1)
-                continue;
-            // ---- the candidates: all logits down to a little below the bin's lower edge ----
-            const float cut = isinf(row.top) ? row.top
-                                             : row.top - ((float)last + 1.05f) / scale - fabsf(row.top) * 1e-6f;
-            auto found = [&](float x, int i) {
-                if (x >= cut) {
-                    atomicAdd(&sh.found, 1);
-                    const int at = atomicAdd(&to->listed, 1);
-                    if (at < kList)
-                        to->list[at] = ((uint64_t)key_of(x) << 32) | (0xFFFFFFFFu - (uint32_t)(begin + i));
-                }
-            };
-            if (next >= cut)
-                each<2>(slice, c.tid, sh.ring, found);          // more than one: read them again
-            else
-                found(high, high_at);
-            __syncthreads();
-            if (c.tid < c.nctas)
-                cl.map_shared_rank(&sh, c.tid)->counts[c.rank] = sh.found;
             cl.sync();
-            int n = 0;
-            for (int r = 0; r < c.nctas; ++r)
-                n += sh.counts[r];
-            if (n <= kList) {
-                if (c.rank == 0)
-                    draw_listed(c, row, by_sum, total, n, p, m);
-                return;
-            }
-            // (the thread maxima's bound was too low: all logits give a closer one)
         }
-        kept = select(c, slice, row, total);
+        unsigned h[kMaxCluster], count = 0;
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+            h[r] = r < c.nctas ? cl.map_shared_rank(&sh, r)->hist[c.tid] : 0u;
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+            count += h[r];
+        // The last bin a kept token can be in: the k-th token's; the one where the
+        // weights, each taken at its bin's lower edge less a little for rounding, pass
+        // top-p's share; min-p's.
+        float low = (float)count * __expf(-(float)(c.tid + 1) / kBinsPerNat) * 0.999f;
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+            const unsigned o = __shfl_up_sync(0xffffffffu, count, s);
+            const float f = __shfl_up_sync(0xffffffffu, low, s);
+            count += c.lane >= s ? o : 0;
+            low += c.lane >= s ? f : 0.f;
+        }
+        if (c.lane == 31) {
+            sh.scan[c.warp] = count;
+            sh.red[0][c.warp][3] = __float_as_uint(low);
+        }
+        __syncthreads();
+        for (int w = 0; w < c.warp; ++w) {
+            count += sh.scan[w];
+            low += __uint_as_float((uint32_t)sh.red[0][w][3]);
+        }
+        bool reach = by_rank ? count >= (unsigned)row.k
+                             : by_sum && low >= row.top_p * __ull2float_rn(total) * 9.094947e-13f;   // 2^-40
+        // (top-p takes its share of all that top-k kept, min-p or not)
+        const float z_min = row.min_p > 0.f && !(by_rank && by_sum) ? -logf(row.min_p) : 1e30f;
+        reach = reach || (float)c.tid > z_min * kBinsPerNat + 2.f;
+        const int last = __syncthreads_count(!reach);  // bins before the first that reaches
+        // ---- the candidates: all logits down to a little below the bin's lower edge ----
+        float cut = kNegInf;
+        int n = kSearch;
+        if (last < kBins - 1) {
+            cut = isinf(row.top) ? row.top
+                                 : row.top - ((float)last + 1.05f) / scale - fabsf(row.top) * 1e-6f;
+            n = gather(c, begin, [&](auto found) {
+                if (next >= cut)                       // more than one: read them again
+                    each<2>(slice, c.tid, sh.ring, [&](float x, int i) {
+                        if (x >= cut)
+                            found(x, i);
+                    });
+                else if (high >= cut)
+                    found(high, high_at);
+            });
+        }
+        if ((n == kSearch || n > kList) && (by_rank || by_sum)) {
+            n = select_binned(c, slice, row, cut, total, begin, kept);
+            if (n == kSearch)
+                kept = select(c, slice, row, total);
+        }
+        if (n >= 0 && n <= kList) {
+            if (c.rank == 0)
+                draw_listed(c, row, by_sum, total, n, p, m);
+            return;
+        }
     }
     float prob;
     const int place = draw(c, slice, row, kept, &prob);

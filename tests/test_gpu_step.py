@@ -439,6 +439,26 @@ def test_sample(n, dtype, rule, last):
     check_sample(f64(x), u, token, prob, last, **RULES[rule])
 
 
+@pytest.mark.parametrize("last", [False, True])
+@pytest.mark.parametrize("grid", [0.0, 2.0 ** -6, 0.5])
+def test_sample_many_candidates(grid, last):
+    """Rows of which thousands of tokens are kept, without and with many equal logits."""
+    rules = dict(temperature=[1., 1., .9, 1.3, 1.2, 2., 1.5, 2.5],
+                 top_k=[1500, 3000, 20000, 60000, 0, 0, 0, 5000],
+                 top_p=[1., 1., 1., .9, .95, .999, 1., .6],
+                 min_p=[0., 0., 1e-3, 0., 0., 1e-4, 1e-5, 0.])
+    g = torch.Generator(device="cuda").manual_seed(17)
+    x = 2.5 * torch.randn((8, 151936), generator=g, device="cuda")
+    if grid:
+        x = (x / grid).round() * grid
+    for m in (8, 24):                                   # rows to both cluster sizes
+        u = torch.rand(m, generator=g, device="cuda").cpu().numpy()
+        many = {k: v * (m // 8) for k, v in rules.items()}
+        rows = x.repeat(m // 8, 1)
+        token, prob = draw(rows, u, last, **many)
+        check_sample(f64(rows), u, token, prob, last, **many)
+
+
 @pytest.mark.parametrize("n", [64, 4000, 40001, 151936])
 def test_sample_equal_logits(n):
     """All logits equal: every count is exact, ties go by index."""
