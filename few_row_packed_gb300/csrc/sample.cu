@@ -14,14 +14,15 @@
 //
 // A row takes one thread-block cluster, each CTA a slice of it.  Selecting needs
 // one pass over the logits (the bound of a large batch) and no sort of the row:
-//   1. every thread finds the maximum of its logits, the cluster the row's;
+//   1. every thread finds the maximum of its vectors of 16 bytes and the largest of
+//      these, the cluster the row's;
 //   2. a bound on how far down the kept tokens can reach.  The thread maxima
 //      enter a histogram of (m - l) r in steps of 1/8: the k-th of these few
 //      thousand values is at most the row's k-th, and their weights sum to no more
 //      than the row's above the same logit, so the first bin that satisfies top-k
 //      or top-p on them lies at or below the true cut;
-//   3. the few threads whose maximum lies above the bound list it; those whose next
-//      largest does too read their logits again (from L2) and list all above it
+//   3. the few threads whose largest vector reaches above the bound read it again
+//      (from L2), those with a second one all of theirs, and list all logits above it
 //      ("candidates").  The lists of all CTAs are joined in the first, the others are
 //      done;
 //   4. it sorts them by rank; a running sum of their weights gives how many are
@@ -41,15 +42,17 @@
 // waits at a barrier, the others' loads keep memory busy.
 //
 // What bounds it: for few rows the chain of barriers and latencies, for many the
-// instructions of a pass (some 30 per logit and exp) and of the sort, then memory.
-// Time of a call with 256 rows of 128,256 bf16 logits / 8 rows of 151,936 fp32 / 1 row
-// of 128,256 fp32, in us, where reading the logits once takes 9.7 / 0.7 / 0.1:
-//     temperature 0 (the maximum)      30 /  9 /  9
-//     top-k 50                         67 / 17 / 17
-//     no rule                         156 / 33 / 27
-//     top-p 0.5, <= 2048 kept         367 / 83 / 46
-//     top-p 0.9, some 15,000 kept     458 / 79 / 62    (by the bit search: 1125 / 207 / 133)
-//     top-k 5000                      345 / 65 / 51    (by the bit search: 1031 / 188 / 125)
+// instructions of a pass (2 a logit for the maximum, taken by vectors; some 25 for a
+// weight) and of the sort, then memory.  Time of a call with 256 rows of 128,256 bf16
+// logits / 8 rows of 151,936 fp32 / 1 row of 128,256 fp32, in us, where reading the
+// logits once takes 9.7 / 0.7 / 0.1:
+//     temperature 0 (the maximum)      21 /  9 /  9    (maximum by elements: 30 / 9 / 9)
+//     top-k 50                         60 / 17 / 17
+//     no rule                         118 / 31 / 25
+//     top-p 0.5, <= 2048 kept         325 / 81 / 44
+//     top-p 0.9, some 15,000 kept     416 / 74 / 58    (by the bit search: 1125 / 207 / 133)
+//     top-k 5000                      299 / 62 / 48    (by the bit search: 1031 / 188 / 125)
+// All logits equal, which the search has to settle: up to 4270 / 285 / 208.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -124,11 +127,12 @@ __device__ __forceinline__ float of_key(uint32_t k)
 }
 
 // exp((x - top) r) in fp32, every operation rounded once; a token at the
-// maximum weighs exactly 1 (the maximum may be +inf), a masked one 0.
+// maximum weighs exactly 1 (the maximum may be +inf), a masked one 0 (z may be NaN
+// where r is 0).
 __device__ __forceinline__ float weight_f(float x, float top, float r)
 {
     const float z = x == top ? 0.f : __fmul_rn(__fsub_rn(x, top), r);
-    return x == kNegInf ? 0.f : expf(z);
+    return fmaxf(expf(z), 0.f);
 }
 
 // floor(2^40 w) for 0 <= w <= 1: the significand moved to its place by shifts (a
@@ -232,20 +236,62 @@ __device__ __forceinline__ float to_f32(uint32_t bits)     // of one element
 template <int DT>
 struct Slice {
     static constexpr int SIZE = DT == LBV_F32 ? 4 : 2;
+    static constexpr int E = 16 / SIZE;    // elements of a vector
     const unsigned char* row;              // its first element
     const uint32_t* words;                 // its mask words, or NULL
     int n;
-    // a logit as the search sees it; `allowed`: its mask bit
-    static __device__ __forceinline__ float clean(float v, bool allowed)
+    static __device__ __forceinline__ float clean(float v)
     {
         v = __fadd_rn(v, 0.f);
-        return v != v || !allowed ? kNegInf : v;
+        return v != v ? kNegInf : v;
     }
     __device__ __forceinline__ float get(int i) const
     {
         const uint32_t b = SIZE == 4 ? __ldg(reinterpret_cast<const uint32_t*>(row) + i)
                                      : __ldg(reinterpret_cast<const uint16_t*>(row) + i);
-        return clean(to_f32<DT>(b), !words || ((__ldg(words + (i >> 5)) >> (i & 31)) & 1u));
+        return !words || ((__ldg(words + (i >> 5)) >> (i & 31)) & 1u) ? clean(to_f32<DT>(b)) : kNegInf;
+    }
+    // elements before the first aligned address, and up to the last
+    __device__ __forceinline__ int head() const
+    {
+        return min(n, (int)(((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / SIZE));
+    }
+    __device__ __forceinline__ int tail() const { return head() + (n - head()) / E * E; }
+    // a vector with the elements whose bit in m is 0 made -inf
+    static __device__ __forceinline__ void hide(uint32_t (&q)[4], uint32_t m)
+    {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if constexpr (DT == LBV_F32) {
+                q[k] = (m >> k) & 1u ? q[k] : 0xFF800000u;
+            } else {
+                const uint32_t keep = ((m >> 2 * k) & 1u ? 0xFFFFu : 0u) |
+                                      ((m >> (2 * k + 1)) & 1u ? 0xFFFF0000u : 0u);
+                q[k] = (q[k] & keep) | ((DT == LBV_F16 ? 0xFC00FC00u : 0xFF80FF80u) & ~keep);
+            }
+    }
+    static __device__ __forceinline__ float element(const uint32_t (&q)[4], int e)   // constant e
+    {
+        return DT == LBV_F32 ? clean(to_f32<DT>(q[e & 3]))
+                             : clean(to_f32<DT>(e & 1 ? q[e / 2 & 3] >> 16 : q[e / 2 & 3] & 0xFFFFu));
+    }
+    // the largest element (NaN only if all are; the sign of a zero is open)
+    static __device__ __forceinline__ float largest(const uint32_t (&q)[4])
+    {
+        if constexpr (DT == LBV_F32) {
+            return fmaxf(fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1])),
+                         fmaxf(__uint_as_float(q[2]), __uint_as_float(q[3])));
+        } else if constexpr (DT == LBV_F16) {
+            __half2 h[4];
+            memcpy(h, q, 16);
+            const __half2 v = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+            return fmaxf(__low2float(v), __high2float(v));
+        } else {
+            __nv_bfloat162 h[4];
+            memcpy(h, q, 16);
+            const __nv_bfloat162 v = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+            return fmaxf(__low2float(v), __high2float(v));
+        }
     }
 };
 
@@ -258,19 +304,17 @@ __device__ __forceinline__ void copy_async(void* to, const void* from, int bytes
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(d), "l"(from) : "memory");
 }
 
-// Calls f(value, index) for the thread's logits of the slice, indexes ascending:
-// 16-byte copies between the first and the last aligned address, several of them
-// in flight, into places of the ring that only this thread reads (in registers, a
+// Calls vec(words, first index) for the thread's vectors of the slice, and one(value,
+// index) for a logit before the first aligned address or after the last; indexes
+// ascend, but for that the ones come first and last.  16-byte copies, several of them in
+// flight, go into places of the ring that only this thread reads (in registers, a
 // rotation of the buffers would wait for the copy that was just asked for).
-// AT_ONCE elements of a vector are unrolled.
-template <int AT_ONCE, int DT, typename F>
-__device__ __forceinline__ void each(const Slice<DT>& s, int tid, Ring& ring, F f)
+template <int DT, typename V, typename F>
+__device__ __forceinline__ void each_vector(const Slice<DT>& s, int tid, Ring& ring, V vec, F one)
 {
-    constexpr int SIZE = Slice<DT>::SIZE, E = 16 / SIZE;
-    const uintptr_t a = reinterpret_cast<uintptr_t>(s.row);
-    const int head = min(s.n, (int)(((16 - (a & 15)) & 15) / SIZE));
-    const int body = (s.n - head) / E, tail = head + body * E;
-    const uint4* v = reinterpret_cast<const uint4*>(a + head * SIZE);
+    constexpr int SIZE = Slice<DT>::SIZE, E = Slice<DT>::E;
+    const int head = s.head(), body = (s.n - head) / E, tail = head + body * E;
+    const uint4* v = reinterpret_cast<const uint4*>(s.row + head * SIZE);
     auto ask = [&](int i, int st) {
         if (i < body) {
             copy_async(&ring.v[st][tid], v + i, 16);
@@ -286,36 +330,68 @@ __device__ __forceinline__ void each(const Slice<DT>& s, int tid, Ring& ring, F 
     for (int u = 0; u < kAhead; ++u)
         ask(tid + u * kThreads, u);
     if (tid < head)
-        f(s.get(tid), tid);
+        one(s.get(tid), tid);
     int st = 0;
 #pragma unroll 1
     for (int i = tid; i < body; i += kThreads) {
         asm volatile("cp.async.wait_group %0;\n" ::"n"(kAhead - 1) : "memory");
         const uint4 w = ring.v[st][tid];
         const int d = head + i * E;
-        const uint32_t m =
-            s.words ? __funnelshift_r(ring.words[st][tid][0], ring.words[st][tid][1], d & 31) : ~0u;
+        uint32_t q[4] = {w.x, w.y, w.z, w.w};
+        if (s.words)
+            s.hide(q, __funnelshift_r(ring.words[st][tid][0], ring.words[st][tid][1], d & 31));
         ask(i + kAhead * kThreads, st);
         st = st + 1 == kAhead ? 0 : st + 1;
-        const uint32_t q[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll 1
-        for (int e0 = 0; e0 < E; e0 += AT_ONCE)
-#pragma unroll
-            for (int k = 0; k < AT_ONCE; ++k) {
-                const int e = e0 + k;
-                uint32_t b;
-                if constexpr (DT == LBV_F32) {
-                    b = AT_ONCE == 4 ? q[k] : e < 2 ? (e & 1 ? q[1] : q[0]) : (e & 1 ? q[3] : q[2]);
-                } else {
-                    const uint32_t r = AT_ONCE == 8 ? q[k / 2] : e < 4 ? (e < 2 ? q[0] : q[1]) : (e < 6 ? q[2] : q[3]);
-                    b = e & 1 ? r >> 16 : r & 0xFFFFu;
-                }
-                f(s.clean(to_f32<DT>(b), (m >> e) & 1u), d + e);
-            }
+        vec(q, d);
     }
     asm volatile("cp.async.wait_all;\n" ::: "memory");
     if (tail + tid < s.n)                  // fewer than E of them
-        f(s.get(tail + tid), tail + tid);
+        one(s.get(tail + tid), tail + tid);
+}
+
+// Calls f(value, index) for the thread's logits of the slice, two of a vector unrolled.
+template <int DT, typename F>
+__device__ __forceinline__ void each(const Slice<DT>& s, int tid, Ring& ring, F f)
+{
+    each_vector(s, tid, ring, [&](uint32_t (&q)[4], int d) {
+#pragma unroll 1
+        for (int e = 0; e < Slice<DT>::E; e += 2) {
+            uint32_t two[4];
+            if constexpr (DT == LBV_F32) {
+                two[0] = e ? q[2] : q[0];
+                two[1] = e ? q[3] : q[1];
+            } else {
+                two[0] = e < 4 ? (e < 2 ? q[0] : q[1]) : (e < 6 ? q[2] : q[3]);
+            }
+            f(s.element(two, 0), d + e);
+            f(s.element(two, 1), d + e + 1);
+        }
+    }, f);
+}
+
+// The sum of whole(f(value)) over the thread's logits.  f gives 0 to 1; adding a power
+// of two, rounded towards zero, leaves the integer part of 2^17 f in the low bits of the
+// sum, and that of 2^40 times the remainder in those of a second one; their biases are
+// taken off once a vector.
+template <int DT, typename F>
+__device__ __forceinline__ uint64_t sum_whole(const Slice<DT>& s, int tid, Ring& ring, F f)
+{
+    constexpr int E = Slice<DT>::E;
+    constexpr uint32_t kHigh = 0x42800000u, kLow = 0x37000000u;        // 2^6, 2^-17
+    uint64_t sum = 0;
+    each_vector(s, tid, ring, [&](uint32_t (&q)[4], int) {
+        uint32_t high = 0, low = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float w = f(s.element(q, e));
+            const float a = __fadd_rz(w, __uint_as_float(kHigh));
+            const float rest = __fsub_rn(w, __fsub_rn(a, __uint_as_float(kHigh)));
+            high += __float_as_uint(a);
+            low += __float_as_uint(__fadd_rz(rest, __uint_as_float(kLow)));
+        }
+        sum += ((uint64_t)(high - E * kHigh) << 23) + (low - E * kLow);
+    }, [&](float x, int) { sum += whole(f(x)); });
+    return sum;
 }
 
 struct Row {
@@ -339,7 +415,7 @@ __device__ __forceinline__ uint32_t search(Ctx c, const D& d, F f, Test test)
     for (int bit = 30; bit >= 0; bit -= 2) {
         uint64_t s1 = 0, s2 = 0, s3 = 0;
         const uint32_t t1 = t | (1u << bit), t2 = t | (2u << bit), t3 = t | (3u << bit);
-        each<2>(d, c.tid, c.sh->ring, [&](float x, int) {
+        each(d, c.tid, c.sh->ring, [&](float x, int) {
             const uint32_t k = key_of(x);
             if (k >= t1) {
                 const uint64_t w = f(x);
@@ -368,7 +444,7 @@ __device__ __noinline__ Kept select(Ctx c, D d, Row row, uint64_t total)
                        [&](uint32_t, uint64_t n) { return n >= k; });
         // what lies above it
         uint64_t n = 0, sum = 0;
-        each<2>(d, c.tid, c.sh->ring, [&](float x, int) {
+        each(d, c.tid, c.sh->ring, [&](float x, int) {
             if (key_of(x) > tau_k) {
                 n += 1;
                 sum += weight(x);
@@ -388,7 +464,7 @@ __device__ __noinline__ Kept select(Ctx c, D d, Row row, uint64_t total)
             return t <= tau_k || s >= limit;
         });
         uint64_t sum = 0;
-        each<2>(d, c.tid, c.sh->ring, [&](float x, int) { sum += key_of(x) > tau ? weight(x) : 0; });
+        each(d, c.tid, c.sh->ring, [&](float x, int) { sum += key_of(x) > tau ? weight(x) : 0; });
         uint64_t v[1] = {sum};
         reduce<1>(c, 1, v);
         const uint64_t w = weight(of_key(tau));
@@ -408,17 +484,17 @@ template <int DT>
 __device__ __noinline__ int draw(Ctx c, Slice<DT> d, Row row, Kept kept, float* prob)
 {
     Shared& sh = *c.sh;
-    auto weight = [&](float x) {
+    auto share = [&](float x) {            // of a token that the ranking keeps
         const float w = weight_f(x, row.top, row.draw_r);
         const float f = row.filter_r == row.draw_r || row.min_p <= 0.f ? w : weight_f(x, row.top, row.filter_r);
-        return f >= row.min_p || row.min_p <= 0.f ? whole(w) : 0;
+        return f >= row.min_p || row.min_p <= 0.f ? w : 0.f;
     };
-    uint64_t sum = 0;
+    auto weight = [&](float x) { return whole(share(x)); };
+    const float tau = kept.tau ? of_key(kept.tau) : kNegInf;
     unsigned equal = 0;
-    each<DT == LBV_F32 ? 4 : 8>(d, c.tid, sh.ring, [&](float x, int) {
-        const uint32_t k = key_of(x);
-        sum += k > kept.tau ? weight(x) : 0;
-        equal += k == kept.tau;
+    uint64_t sum = sum_whole(d, c.tid, sh.ring, [&](float x) {
+        equal += x == tau;
+        return x > tau ? share(x) : 0.f;
     });
     uint64_t all[2] = {sum, equal}, below[2], here[2];
     reduce<2>(c, 2, all, below, here);
@@ -667,7 +743,7 @@ __device__ __noinline__ int select_binned(Ctx c, Slice<DT> slice, Row row, float
         sh.fine.count[i] = 0;
     }
     __syncthreads();
-    each<2>(slice, c.tid, sh.ring, [&](float x, int) {
+    each(slice, c.tid, sh.ring, [&](float x, int) {
         const int b = bin_of(x);
         if (b < kFine) {
             atomicAdd(&sh.fine.count[b], 1u);
@@ -737,7 +813,7 @@ __device__ __noinline__ int select_binned(Ctx c, Slice<DT> slice, Row row, float
     // the tokens of bins [b0, b1] into the first CTA's list
     auto list_bins = [&](int b0, int b1) {
         return gather(c, begin, [&](auto found) {
-            each<2>(slice, c.tid, sh.ring, [&](float x, int i) {
+            each(slice, c.tid, sh.ring, [&](float x, int i) {
                 const int b = bin_of(x);
                 if (b >= b0 && b <= b1)
                     found(x, i);
@@ -936,13 +1012,17 @@ __global__ void __launch_bounds__(kThreads, 4) lbv_sample_kernel(const __grid_co
     cl.barrier_arrive();                               // waited for before the first remote store
 
     // ---- the thread's and the row's first maximum ----
-    float high = kNegInf, next = kNegInf;              // the largest logit, the next one
+    // (by vectors: the largest and the next largest of their maxima)
+    float high = kNegInf, next = kNegInf;
     int high_at = 0;
-    each<DT == LBV_F32 ? 4 : 8>(slice, c.tid, sh.ring, [&](float v, int i) {
+    auto higher = [&](float v, int i) {
         next = fmaxf(next, fminf(v, high));
         high_at = v > high ? i : high_at;
         high = fmaxf(high, v);
-    });
+    };
+    each_vector(slice, c.tid, sh.ring, [&](uint32_t (&q)[4], int d) { higher(slice.largest(q), d); },
+                higher);
+    high = __fadd_rn(high, 0.f);                       // -0 to +0
     sh.hist[c.tid] = 0;
     if (c.tid == 0)
         sh.found = 0;
@@ -972,11 +1052,17 @@ __global__ void __launch_bounds__(kThreads, 4) lbv_sample_kernel(const __grid_co
     row.top = of_key((uint32_t)(best >> 32));
     const int first = (int)(0xFFFFFFFFu - (uint32_t)best);
     if (best == 0 || row.top == kNegInf || greedy) {   // nothing allowed, or the maximum itself
-        if (c.rank == 0 && c.tid == 0) {
+        const Slice<DT> all = {slice.row - (int64_t)begin * Slice<DT>::SIZE,
+                               slice.words ? slice.words - begin / 32 : nullptr, p.N};
+        const int i = first + c.lane;                  // the first of its vector
+        if (c.rank == 0 && c.warp == 0) {
             const bool none = best == 0 || row.top == kNegInf;
-            p.token[m] = none ? -1 : first;
-            if (p.prob)
-                p.prob[m] = none ? 0.f : 1.f;
+            const unsigned at = __ballot_sync(0xffffffffu, i >= 0 && i < p.N && all.get(i) == row.top);
+            if (c.lane == 0) {
+                p.token[m] = none ? -1 : first + __ffs(at) - 1;
+                if (p.prob)
+                    p.prob[m] = none ? 0.f : 1.f;
+            }
         }
         return;
     }
@@ -992,11 +1078,9 @@ __global__ void __launch_bounds__(kThreads, 4) lbv_sample_kernel(const __grid_co
             atomicAdd(&sh.hist[(int)depth], 1u);
         uint64_t total = 0;
         if (by_sum && !by_rank) {
-            uint64_t sum = 0;
-            each<DT == LBV_F32 ? 4 : 8>(slice, c.tid, sh.ring, [&](float x, int) {
-                sum += whole(weight_f(x, row.top, row.filter_r));
-            });
-            uint64_t v[1] = {sum};
+            uint64_t v[1] = {sum_whole(slice, c.tid, sh.ring, [&](float x) {
+                return weight_f(x, row.top, row.filter_r);
+            })};
             reduce<1>(c, 2, v);                        // orders the histograms too
             total = v[0];
         } else {
@@ -1043,13 +1127,22 @@ __global__ void __launch_bounds__(kThreads, 4) lbv_sample_kernel(const __grid_co
             cut = isinf(row.top) ? row.top
                                  : row.top - ((float)last + 1.05f) / scale - fabsf(row.top) * 1e-6f;
             n = gather(c, begin, [&](auto found) {
-                if (next >= cut)                       // more than one: read them again
-                    each<2>(slice, c.tid, sh.ring, [&](float x, int i) {
+                if (next >= cut) {                     // in several vectors: read all again
+                    each(slice, c.tid, sh.ring, [&](float x, int i) {
                         if (x >= cut)
                             found(x, i);
                     });
-                else if (high >= cut)
-                    found(high, high_at);
+                } else if (high >= cut) {
+                    float x[Slice<DT>::E];
+                    const int one = high_at < slice.head() || high_at >= slice.tail();
+#pragma unroll
+                    for (int e = 0; e < Slice<DT>::E; ++e)
+                        x[e] = e == 0 || !one ? slice.get(high_at + e) : kNegInf;
+#pragma unroll
+                    for (int e = 0; e < Slice<DT>::E; ++e)
+                        if (x[e] >= cut && (e == 0 || !one))
+                            found(x[e], high_at + e);
+                }
             });
         }
         if ((n == kSearch || n > kList) && (by_rank || by_sum)) {
