@@ -178,6 +178,13 @@ __device__ __forceinline__ uint32_t seen32(const AttendParams& p, const Request&
     return see;
 }
 
+// The new token of an item's row (a division by the group, in two instructions: code
+// that runs once an item is not in the instruction cache, and costs by its length).
+__device__ __forceinline__ int token_of(const AttendParams& p, int row)
+{
+    return (int)(__umulhi(2u * (uint32_t)row, p.group_mul) >> p.group_shift);
+}
+
 // 32 bytes to a 32-byte-aligned address: a whole sector by one thread.
 __device__ __forceinline__ void store32(void* d, const uint32_t* r)
 {
@@ -225,7 +232,7 @@ template <int DT>
 __device__ __forceinline__ void finish4(const AttendParams& p, const Request& q, int kv_head, int row,
                                         int d4, float4 o, float top, float sum, float exact)
 {
-    const int i = row / p.group, g = row - i * p.group;
+    const int i = token_of(p, row), g = row - i * p.group;
     const int64_t tok = q.q0 + i;
     const int head = kv_head * p.group + g;
     const float f = 1.f / sum;
@@ -241,15 +248,20 @@ __device__ __forceinline__ void finish4(const AttendParams& p, const Request& q,
 // An item is a tile of up to ROWS rows of a request (new token times query head
 // of the group) and a key/value head, over the blocks of KEYS keys that some row
 // of the tile sees, at least one (an empty row has an output too).  Its cost in
-// units: EXTRA for its queries and results, and 1 for each block, or 2 where
+// units: EXTRA for its queries and results, and NARROW for each block, or WIDE where
 // the tile has more than SINGLE rows.  The units of the batch form one sequence
 // -- request by request, tile by tile, head by head -- of which every CTA takes
 // an equal contiguous share; a block belongs to the share that holds its first
 // unit.  The host refuses batches of 2^32 units and more.
-template <int ROWS_, int KEYS_, int SINGLE, int EXTRA_>
+template <int ROWS_, int KEYS_, int EXTRA_, int NARROW = 1, int WIDE = NARROW, int SINGLE = ROWS_>
 struct Shape {
     static constexpr int ROWS = ROWS_, KEYS = KEYS_, EXTRA = EXTRA_;
-    static __device__ __forceinline__ int weight(int rows) { return rows > SINGLE ? 2 : 1; }
+    static __device__ __forceinline__ int weight(int rows) { return rows > SINGLE ? WIDE : NARROW; }
+    // k units in blocks, rounded up
+    static __device__ __forceinline__ int blocks(int rows, int k)
+    {
+        return rows > SINGLE ? (k + WIDE - 1) / WIDE : (k + NARROW - 1) / NARROW;
+    }
 };
 
 struct Tile {
@@ -271,7 +283,7 @@ __device__ __forceinline__ Tile tile_of(const AttendParams& p, const Request& q,
     Tile x;
     x.row0 = t * S::ROWS;
     x.rows = min(S::ROWS, q.n * p.group - x.row0);
-    key_range(p, q, x.row0 / p.group, (x.row0 + x.rows - 1) / p.group, x.lo, x.hi);
+    key_range(p, q, token_of(p, x.row0), token_of(p, x.row0 + x.rows - 1), x.lo, x.hi);
     x.block0 = x.lo / S::KEYS;
     x.blocks = max(1, (x.hi + S::KEYS - 1) / S::KEYS - x.block0);
     x.units = S::EXTRA + (unsigned)(S::weight(x.rows) * x.blocks);
@@ -409,8 +421,8 @@ struct Walk {
     // blocks of the item whose first unit lies before unit v of it
     __device__ int blocks_before(unsigned v) const
     {
-        const int w = S::weight(x.rows), k = (int)v - S::EXTRA;
-        return k <= 0 ? 0 : min((k + w - 1) / w, x.blocks);
+        const int k = (int)v - S::EXTRA;
+        return k <= 0 ? 0 : min(S::blocks(x.rows, k), x.blocks);
     }
     // The next item with a block in the share.
     __device__ bool next()

@@ -17,6 +17,8 @@ struct AttendParams {
     float scale_log2;                // scale * log2(e)
     int window;                      // <= 0: none
     int heads, group;                // query heads, query heads per kv head
+    uint32_t group_mul;              // row / group = (2 row * group_mul >> 32) >> group_shift
+    int group_shift;
     int q_wide;                      // q rows are 16-byte aligned
     lbv_batch batch;
     KvView kv;

@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, Geo<D>::CTAS)
 {
     using G = Geo<D>;
     constexpr int ROWS = G::ROWS;
-    using S = Shape<ROWS, kBlock, ROWS, kExtra>;
+    using S = Shape<ROWS, kBlock, kExtra>;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, Geo<D>::CTAS)
             const int r = i / (D / 8), ch = i % (D / 8), row = w.x.row0 + r;
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
             if (r < w.x.rows) {
-                const int t = row / p.group;
+                const int t = token_of(p, row);
                 const uint16_t* src = p.q + (int64_t)(w.q.q0 + t) * p.q_token +
                                       (int64_t)(w.head * p.group + row - t * p.group) * p.q_head + ch * 8;
                 if (p.q_wide) {
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, Geo<D>::CTAS)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const bool in = r0 + h * 8 < w.x.rows;
-            const int i = (w.x.row0 + r0 + h * 8) / p.group;
+            const int i = token_of(p, w.x.row0 + r0 + h * 8);
             pos[h] = in ? w.q.first + i : INT_MIN / 2;
             words[h] = in && p.tree ? p.tree[w.q.q0 + i] : 0;
         }
@@ -235,9 +235,9 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, Geo<D>::CTAS)
             o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
         // keys below `open_lo` or at `open_hi` and past are hidden from some row
         const int open_hi = p.tree ? min(w.q.keys, w.q.first)
-                                   : min(w.q.keys, w.q.first + w.x.row0 / p.group + 1);
+                                   : min(w.q.keys, w.q.first + token_of(p, w.x.row0) + 1);
         const int open_lo =
-            p.window > 0 ? w.q.first + (w.x.row0 + w.x.rows - 1) / p.group - p.window + 1 : 0;
+            p.window > 0 ? w.q.first + token_of(p, w.x.row0 + w.x.rows - 1) - p.window + 1 : 0;
 
         for (int b = w.b_first; b < w.b_last; ++b) {
             const int st = n % G::NST, k0 = w.key0(b);
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, Geo<D>::CTAS)
             const float* t = tops + r;
             const float sum = (t[0] + t[ROWS]) + (t[2 * ROWS] + t[3 * ROWS]);
             const float exact = (t[4 * ROWS] + t[5 * ROWS]) + (t[6 * ROWS] + t[7 * ROWS]);
-            const int i = row / p.group, head = w.head * p.group + row - i * p.group;
+            const int i = token_of(p, row), head = w.head * p.group + row - i * p.group;
             const int64_t tok = w.q.q0 + i;
             const bool first = warp == 0 && (lane & 3) == 0;
             const int e0 = warp * (D / 4) + (lane & 3) * 2;

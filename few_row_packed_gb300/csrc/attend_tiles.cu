@@ -29,10 +29,12 @@ namespace {
 constexpr int kKeys = 128;                       // keys per block
 constexpr int kTile = 128;                       // rows per stream
 constexpr int kRows = 2 * kTile;                 // rows per item
-// Units of an item beside its blocks (a block of two row tiles counts as two
-// units), and the least share of a CTA.
-constexpr int kExtra = 8, kMinUnits = 12;
-using Items = Shape<kRows, kKeys, kTile, kExtra>;
+// Units of an item: its queries and results, a block of one row tile, a block of two;
+// and the least share of a CTA.  A unit is 0.42 us of a long item.  (A prompt's and a
+// mixed batch's time with 8/1/2 of 0.84 us: 533 and 166 us; 12/1/2: 534 and 160; these:
+// 530 and 157; 40/3/4: 534 and 165.)
+constexpr int kExtra = 24, kNarrow = 3, kWide = 4, kMinUnits = 24;
+using Items = Shape<kRows, kKeys, kExtra, kNarrow, kWide, kTile>;
 constexpr int kThreads = 384;                    // copies and MMAs, then the two streams
 // Registers a thread after the split: 168 * 384 at launch = 88 * 128 + 208 * 256.
 constexpr int kRegsControl = 88, kRegsStream = 208;
@@ -217,7 +219,7 @@ __device__ __forceinline__ void store_q(const AttendParams& p, int q0, int kv_he
                                         unsigned char* tile, int trow)
 {
     const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
-    const int i = row / p.group;
+    const int i = token_of(p, row);
     const uint16_t* src = p.q + (int64_t)(q0 + i) * p.q_token +
                           (int64_t)(kv_head * p.group + row - i * p.group) * p.q_head;
     uint4 v[D / 8];
@@ -247,6 +249,26 @@ __device__ __forceinline__ void store_q(const AttendParams& p, int q0, int kv_he
         *reinterpret_cast<uint4*>(dst + (ch >> 3) * Geo<D>::HALF + (((ch & 7) ^ (trow & 7)) << 4)) = v[ch];
     }
     fence_proxy_async_smem();
+}
+
+// The same by asynchronous copies, for aligned rows and a scale of 0 or more; the
+// thread waits for them later.
+template <int D>
+__device__ __forceinline__ void fetch_q(const AttendParams& p, int q0, int kv_head, int row, bool in,
+                                        uint32_t tile, int trow)
+{
+    const int i = token_of(p, row);
+    const uint16_t* src = in ? p.q + (int64_t)(q0 + i) * p.q_token +
+                                   (int64_t)(kv_head * p.group + row - i * p.group) * p.q_head
+                             : p.q;
+    const uint32_t bytes = in && p.scale_log2 != 0.f ? 16u : 0u;         // the rest is filled with zeros
+    const uint32_t dst = tile + trow * 128;
+#pragma unroll
+    for (int ch = 0; ch < D / 8; ++ch)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
+                         dst + (ch >> 3) * Geo<D>::HALF + (((ch & 7) ^ (trow & 7)) << 4)),
+                     "l"(src + (bytes ? ch * 8 : 0)), "r"(bytes)
+                     : "memory");
 }
 
 template <int DT, int D>
@@ -475,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // its queries are on the way before the streams ask for them
                     if (more)
                         for (int i = lane; i < w.x.rows * (D / 64); i += 32) {
-                            const int row = w.x.row0 + i / (D / 64), tok = row / p.group;
+                            const int row = w.x.row0 + i / (D / 64), tok = token_of(p, row);
                             prefetch_l2(p.q + (int64_t)(w.q.q0 + tok) * p.q_token +
                                         (int64_t)(w.head * p.group + row - tok * p.group) * p.q_head +
                                         i % (D / 64) * 64);
@@ -522,9 +544,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // sums of the probabilities as they enter the product, and exact
             float2 l = make_float2(0.f, 0.f), x = make_float2(0.f, 0.f);
             int mine = 0;                                            // blocks of this item
+            bool fetched = false;                                    // the next item's queries are on the way
             {
                 const bool in = item_row < w.rows;
-                const int i = (w.row0 + item_row) / p.group;
+                const int i = token_of(p, w.row0 + item_row);
                 const int pos = in ? w.q.first + i : INT_MIN / 2;
                 const uint64_t word = in && p.tree ? p.tree[w.q.q0 + i] : 0;
                 // keys at `open_hi` and past, or below `open_lo`, are hidden from some
@@ -532,13 +555,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int r0 = w.row0 + (dual ? s * kTile : 0);
                 const int r1 = min(r0 + kTile, w.row0 + w.rows) - 1;
                 const int open_hi = p.tree ? min(w.q.keys, w.q.first)
-                                           : min(w.q.keys, w.q.first + r0 / p.group + 1);
-                const int open_lo = p.window > 0 ? w.q.first + r1 / p.group - p.window + 1 : 0;
+                                           : min(w.q.keys, w.q.first + token_of(p, r0) + 1);
+                const int open_lo = p.window > 0 ? w.q.first + token_of(p, r1) - p.window + 1 : 0;
                 const bool idle = r0 + (warp & 3) * 32 > r1;         // no row in this warp
                 for (int j = dual ? 0 : s; j < nb; j += dual ? 1 : 2, ++mine, ++done) {
                     const int k0 = w.key0 + j * kKeys;
                     wait(s_full(s), (uint32_t)(done & 1));
                     tc_fence_after();
+                    // the last scores of two row tiles: this stream's Q is free, and the copy
+                    // of the next takes as long as this block
+                    if (dual && j + 1 == nb && p.q_wide && p.scale_log2 >= 0.f) {
+                        const Item& v = item_at(it + 1);
+                        if (v.nb > 0 && ok && (v.dual() || s == 0)) {
+                            const int row = (v.dual() ? s * kTile : 0) + trow;
+                            fetch_q<D>(p, v.q.q0, v.head, v.row0 + row, row < v.rows,
+                                       sbase + G::Q + s * G::SLOT, trow);
+                            fetched = true;
+                        }
+                    }
                     // slots past the context may hold anything: NaN times 0 is not 0
                     if (k0 + kKeys > w.q.keys) {
                         const int v = w.slot0 + 2 * j + 1;
@@ -554,22 +588,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     float t[4][32];
                     if (!idle) {
-                        const bool masked = k0 + kKeys > open_hi || k0 < open_lo;
-                        uint32_t see[4];
-                        if (masked)
+                        // masked scores are overwritten in place (rare, so short code)
+                        if (k0 + kKeys > open_hi || k0 < open_lo) {
+#pragma unroll 1
+                            for (int e = 0; e < 8; ++e) {
+                                const uint32_t see = seen32(p, w.q, pos, word, k0 + (e & ~1) * 16) >> (e & 1) * 16;
+                                float u[16];
+                                uint32_t r[16];
+                                tmem_ld16(s_at + e * 16, u);
+                                tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                see[e] = seen32(p, w.q, pos, word, k0 + e * 32);
+                                for (int k = 0; k < 16; ++k)
+                                    r[k] = (see >> k) & 1u ? __float_as_uint(u[k]) : 0xFF800000u;
+                                tmem_st16(s_at + e * 16, r);
+                            }
+                            tmem_wait_st();
+                        }
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             tmem_ld32(s_at + e * 32, t[e]);
                         tmem_wait_ld();
-                        if (masked)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-#pragma unroll
-                                for (int k = 0; k < 32; ++k)
-                                    t[e][k] = (see[e] >> k) & 1u ? t[e][k] : -INFINITY;
                     }
                     // P of 32 keys and its sum, for the reference m
                     uint32_t r[16];
@@ -672,8 +710,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!dual)                                   // both streams read tile 0, which stream 0 stores
                 named_bar_sync(1, 256);
             more = item_at(it + 1).nb > 0 && ok;
-            if (more)
+            if (fetched) {
+                asm volatile("cp.async.wait_all;\n" ::: "memory");
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(q_full);
+            } else if (more) {
                 enter(items[(it + 1) % kItems]);
+            }
             if (mine > 0)
                 wait(o_done(s), (uint32_t)((done - 1) & 1));
             float sum = l.x + l.y, exact = x.x + x.y;
@@ -696,12 +741,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
             const bool in = item_row < w.rows, whole = w.whole();
-            const int row = w.row0 + item_row, i = row / p.group;
+            const int row = w.row0 + item_row, i = token_of(p, row);
             const int64_t tok = w.q.q0 + i;
             const int head = w.head * p.group + row - i * p.group;
             float* slot = p.partial + (size_t)(2 * blockIdx.x + (w.c0 == (int)blockIdx.x)) * G::PARTIAL;
             // dual: all columns of the row; else the stream's half of them
             const int e0 = dual ? 0 : s * (D / 64), e1 = dual ? D / 32 : (s + 1) * (D / 64);
+            // (the quotient is rounded to 16 bits: an approximate reciprocal, off by 2^-23, will do)
+            const float f = sum > 0.f ? __fdividef(1.f, sum) : 0.f;
 #pragma unroll 1
             for (int e = e0; e < e1; ++e) {
                 float o[32];
@@ -717,7 +764,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_wait_ld();
                 }
                 if (in && whole) {
-                    const float f = sum > 0.f ? 1.f / sum : 0.f;
                     uint32_t r[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k)

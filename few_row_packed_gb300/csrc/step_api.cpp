@@ -381,10 +381,10 @@ lbv_status lbv_attend(const lbv_kv_cache* cache, const lbv_batch* batch, const l
         workspace_bytes < lbv_attend_workspace_bytes(cache, batch, q->heads))
         return fail(LBV_ERR_WORKSPACE, "%s: workspace NULL, not 256-byte aligned or %zu < %zu bytes",
                     fn, workspace_bytes, lbv_attend_workspace_bytes(cache, batch, q->heads));
-    // the kernels count blocks of keys in 32 bits: an upper bound of theirs
-    const double blocks = ((double)batch->tokens * q->heads / 16 + batch->requests * (double)cache->view.heads) *
-                          ((double)batch->table_pages * (1 << cache->view.page_shift) / 64 + 2);
-    if (blocks >= 4294967296.0)
+    // the kernels count the costs of blocks of keys in 32 bits: an upper bound of theirs
+    const double units = ((double)batch->tokens * q->heads / 16 + batch->requests * (double)cache->view.heads) *
+                         ((double)batch->table_pages * (1 << cache->view.page_shift) / 32 + 32);
+    if (units >= 4294967296.0)
         return fail(LBV_ERR_UNSUPPORTED, "%s: %d tokens over tables of %d pages are too many for one call",
                     fn, batch->tokens, batch->table_pages);
     lbv::AttendParams p;
@@ -400,6 +400,10 @@ lbv_status lbv_attend(const lbv_kv_cache* cache, const lbv_batch* batch, const l
     p.window = window < (1 << 30) ? window : 0;    // no context is that long
     p.heads = q->heads;
     p.group = q->heads / cache->view.heads;
+    // the reciprocal rounded up at 31 + ceil(log2 group) bits divides all rows below 2^31
+    for (p.group_shift = 0; (1ll << p.group_shift) < p.group; ++p.group_shift) {
+    }
+    p.group_mul = (uint32_t)(((1ull << (31 + p.group_shift)) + p.group - 1) / p.group);
     p.q_wide = aligned(q->data, 16) && q->token_stride % 8 == 0 && q->head_stride % 8 == 0;
     p.batch = *batch;
     p.kv = cache->view;
