@@ -275,6 +275,25 @@ def test_attend_scale(scale):
     check_attend(s, q, out, lse, scale=scale)
 
 
+@pytest.mark.parametrize("dim, dtype, window, scale, wide", [
+    (128, "bf16", 0, None, True), (128, "f16", 100, -0.05, True), (64, "bf16", 0, None, False),
+])
+def test_attend_many_items(dim, dtype, window, scale, wide):
+    """More row tiles than SMs, of one to two hundred rows and more: every CTA goes
+    from item to item of different kinds."""
+    g = np.random.default_rng(dim)
+    q_len = [int(n) for n in g.choice([1, 2, 40, 63, 64, 65, 127, 128, 129, 150], 48)]
+    kv_len = [n + int(g.integers(0, 300)) for n in q_len]
+    s = Setup(q_len, kv_len, kv_heads=8, dim=dim, dtype=dtype, page=16)
+    q = s.rows(16, scale=2.0)
+    if not wide:                                        # rows at odd strides
+        room = torch.empty((q.shape[0], 16, dim + 1), dtype=q.dtype, device="cuda")
+        room[..., :dim] = q
+        q = room[..., :dim]
+    out, lse, _ = run_attend(s, q, scale=scale, window=window)
+    check_attend(s, q, out, lse, scale=scale, window=window)
+
+
 def test_attend_growing_maximum():
     """Scores that rise along the context, so that the reference keeps moving."""
     s = Setup([1], [400], kv_heads=1, dim=64, dtype="f16", page=16)
