@@ -22,7 +22,10 @@ template <int DT, int D>
 __global__ void __launch_bounds__(kWarps * 32)
     lbv_attend_join_kernel(const __grid_constant__ AttendParams p, int slot_rows, int ctas)
 {
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    after_previous();
+    // The next launch may take its places now.  (The attention kernels do not let this one
+    // in before their end: its blocks would hold places beside them, 1.3 us more.)
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // the blockIdx.x-th divided item is the one that starts in CTA c0
     const JoinItem* items = static_cast<const JoinItem*>(p.items);
@@ -120,18 +123,10 @@ cudaError_t launch(const AttendParams& p, int slot_rows, int ctas, cudaStream_t 
 {
     // divided items: no more than there are items, or CTAs
     const int64_t items = ((int64_t)p.batch.tokens * p.group / slot_rows + p.batch.requests) * p.kv.heads;
-    cudaLaunchConfig_t cfg = {};
     // CTAs per item: a warp for every row, or for every other one of the larger slots
-    cfg.gridDim = dim3((unsigned)(items < ctas ? items : ctas),
-                       (unsigned)(slot_rows <= 64 ? slot_rows / kWarps : slot_rows / (2 * kWarps)));
-    cfg.blockDim = dim3(kWarps * 32);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, lbv_attend_join_kernel<DT, D>, p, slot_rows, ctas);
+    const dim3 grid((unsigned)(items < ctas ? items : ctas),
+                    (unsigned)(slot_rows <= 64 ? slot_rows / kWarps : slot_rows / (2 * kWarps)));
+    return launch_after(lbv_attend_join_kernel<DT, D>, grid, kWarps * 32, 0, st, p, slot_rows, ctas);
 }
 
 }  // namespace

@@ -126,6 +126,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, Geo<D>::CTAS)
         }
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
+    after_previous();
     if (p.items && tid == 0)
         static_cast<JoinItem*>(p.items)[blockIdx.x].rows = 0;
     if (warp == 0)
@@ -433,8 +434,7 @@ cudaError_t launch(const AttendParams& p, const CUtensorMap& kmap, const CUtenso
     const bool apart = attend_joins_apart(p, G::ROWS, ctas);
     if (!apart)
         a.items = nullptr;
-    kernel<<<ctas, G::THREADS, G::BYTES, st>>>(a, kmap, vmap);
-    e = cudaGetLastError();
+    e = launch_after(kernel, dim3((unsigned)ctas), G::THREADS, G::BYTES, st, a, kmap, vmap);
     return e == cudaSuccess && apart ? launch_attend_join(a, (lbv_dtype)DT, G::ROWS, ctas, st) : e;
 }
 

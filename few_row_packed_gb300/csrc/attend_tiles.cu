@@ -311,8 +311,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
-    if (tid == 128)
-        static_cast<JoinItem*>(p.items)[blockIdx.x].rows = 0;
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&tmem_slot))
                      : "memory");
@@ -323,6 +321,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     bool ok = true;
+    after_previous();
+    if (tid == 128)
+        static_cast<JoinItem*>(p.items)[blockIdx.x].rows = 0;
 
     auto wait = [&](uint32_t b, uint32_t parity) {
         if (ok)
@@ -818,8 +819,7 @@ cudaError_t launch(const AttendParams& p, const CUtensorMap& kmap, const CUtenso
     if (e != cudaSuccess)
         return e;
     const int ctas = sms < kAttendMaxCtas ? sms : kAttendMaxCtas;
-    kernel<<<ctas, kThreads, Geo<D>::BYTES, st>>>(p, kmap, vmap);
-    e = cudaGetLastError();
+    e = launch_after(kernel, dim3((unsigned)ctas), kThreads, Geo<D>::BYTES, st, p, kmap, vmap);
     return e == cudaSuccess ? launch_attend_join(p, (lbv_dtype)DT, kRows, ctas, st) : e;
 }
 

@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(kThreads) lbv_rope_append_kernel(const __grid_
     const int step = kThreads * gridDim.y;
     const int first = blockIdx.y * kThreads + threadIdx.x;
 
+    after_previous();
     float x0[kAhead][4], x1[kAhead][4];
     auto fetch = [&](int it, float (&a)[4], float (&b)[4]) {
         const Item m = item_of<HALF>(p, it, per_head_shift);
@@ -204,11 +205,8 @@ cudaError_t launch(const RopeParams& p, bool vec, cudaStream_t st)
     const int per = p.batch.tokens < 256 ? 1 : kAhead;
     const dim3 grid((unsigned)p.batch.tokens,
                     (unsigned)((total + kThreads * per - 1) / (kThreads * per)));
-    if (vec)
-        lbv_rope_append_kernel<SRC, DST, HALF, true><<<grid, kThreads, 0, st>>>(p);
-    else
-        lbv_rope_append_kernel<SRC, DST, HALF, false><<<grid, kThreads, 0, st>>>(p);
-    return cudaGetLastError();
+    return vec ? launch_after(lbv_rope_append_kernel<SRC, DST, HALF, true>, grid, kThreads, 0, st, p)
+               : launch_after(lbv_rope_append_kernel<SRC, DST, HALF, false>, grid, kThreads, 0, st, p);
 }
 
 template <int SRC>

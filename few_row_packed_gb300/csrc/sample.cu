@@ -992,6 +992,7 @@ __global__ void __launch_bounds__(kThreads, 4) lbv_sample_kernel(const __grid_co
     c.nctas = p.ctas;
     c.rank = blockIdx.x % p.ctas;
     const int m = blockIdx.x / p.ctas;
+    after_previous();
     const int begin = min(c.rank * p.slice, p.N);
 
     Slice<DT> slice;
@@ -1180,12 +1181,14 @@ cudaError_t launch(const SampleParams& p, int rows, cudaStream_t st)
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = sizeof(Shared);
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = (unsigned)p.ctas;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
