@@ -16,35 +16,63 @@ namespace {
 
 constexpr int kWarps = 4;
 
-constexpr int kLook = (kAttendMaxCtas + 31) / 32;
+constexpr int kLook = 5;                         // items a lane looks at at a time
+constexpr int kFew = 4;                          // parts for which a warp takes kFew rows at once
 
+// direct: the grid has a column for every CTA, else one for every divided item.
 template <int DT, int D>
 __global__ void __launch_bounds__(kWarps * 32)
-    lbv_attend_join_kernel(const __grid_constant__ AttendParams p, int slot_rows, int ctas)
+    lbv_attend_join_kernel(const __grid_constant__ AttendParams p, int slot_rows, int ctas, bool direct)
 {
     after_previous();
     // The next launch may take its places now.  (The attention kernels do not let this one
     // in before their end: its blocks would hold places beside them, 1.3 us more.)
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // the blockIdx.x-th divided item is the one that starts in CTA c0
     const JoinItem* items = static_cast<const JoinItem*>(p.items);
-    bool divided[kLook];
+    auto load = [&](int c, int4& i, int& parts) {
+        i = __ldcg(reinterpret_cast<const int4*>(items + c));
+        parts = __ldcg(&items[c].parts);
+    };
+    JoinItem it;
+    int c0 = -1;                                 // the CTA the item starts in
+    int4 i;
+    if (direct) {
+        c0 = blockIdx.x;
+        load(c0, i, it.parts);
+        if (i.z <= 0)
+            return;
+    } else {
+        int before = 0;
+        for (int b = 0; b < ctas && c0 < 0; b += 32 * kLook) {
+            int4 look[kLook];
+            int parts[kLook];
 #pragma unroll
-    for (int i = 0; i < kLook; ++i)
-        divided[i] = i * 32 + lane < ctas && __ldcg(&items[i * 32 + lane].rows) > 0;
-    int before = 0, c0 = -1;
+            for (int k = 0; k < kLook; ++k) {
+                look[k] = make_int4(0, 0, 0, 0);
+                parts[k] = 0;
+                if (b + k * 32 + lane < ctas)
+                    load(b + k * 32 + lane, look[k], parts[k]);
+            }
 #pragma unroll
-    for (int i = 0; i < kLook; ++i) {
-        const unsigned set = __ballot_sync(0xffffffffu, divided[i]);
-        if (divided[i] && before + __popc(set & ((1u << lane) - 1)) == (int)blockIdx.x)
-            c0 = i * 32 + lane;
-        before += __popc(set);
+            for (int k = 0; k < kLook; ++k) {
+                const unsigned set = __ballot_sync(0xffffffffu, look[k].z > 0);
+                const unsigned here = __ballot_sync(
+                    0xffffffffu, look[k].z > 0 && before + __popc(set & ((1u << lane) - 1)) == (int)blockIdx.x);
+                before += __popc(set);
+                if (here) {
+                    const int from = __ffs(here) - 1;
+                    c0 = b + k * 32 + from;
+                    i = make_int4(__shfl_sync(0xffffffffu, look[k].x, from), __shfl_sync(0xffffffffu, look[k].y, from),
+                                  __shfl_sync(0xffffffffu, look[k].z, from), __shfl_sync(0xffffffffu, look[k].w, from));
+                    it.parts = __shfl_sync(0xffffffffu, parts[k], from);
+                }
+            }
+        }
+        if (c0 < 0)
+            return;
     }
-    c0 = __reduce_max_sync(0xffffffffu, c0);
-    if (c0 < 0)
-        return;
-    const JoinItem it = items[c0];
+    it.q0 = i.x, it.row0 = i.y, it.rows = i.z, it.kv_head = i.w;
     constexpr int LANES = D / 4;                 // lanes that hold a row
     constexpr int AT_ONCE = 32 / LANES;          // parts a load takes
     const int sub = lane / LANES, d4 = lane % LANES;
@@ -54,6 +82,56 @@ __global__ void __launch_bounds__(kWarps * 32)
     auto part = [&](int k) {
         return p.partial + (size_t)(2 * (c0 + k) + (k == 0)) * slot;
     };
+    if (it.parts <= kFew) {
+        // kFew rows at once: their results, and by lane kFew r + k the maximum and the
+        // sums of row r in part k
+        for (int row0 = (blockIdx.y * kWarps + warp) * kFew; row0 < it.rows; row0 += gridDim.y * kWarps * kFew) {
+            float4 a[kFew][kFew / AT_ONCE];
+#pragma unroll
+            for (int r = 0; r < kFew; ++r)
+#pragma unroll
+                for (int j = 0; j < kFew / AT_ONCE; ++j)
+                    if (row0 + r < it.rows && j * AT_ONCE + sub < it.parts)
+                        a[r][j] = __ldcg(reinterpret_cast<const float4*>(part(j * AT_ONCE + sub) + (row0 + r) * D) + d4);
+            const int my = row0 + lane / kFew, k = lane % kFew;
+            float m = -INFINITY, s = 0.f, x = 0.f;
+            if (lane < kFew * kFew && my < it.rows && k < it.parts) {
+                m = __ldcg(part(k) + slot_rows * D + my);
+                s = __ldcg(part(k) + slot_rows * (D + 1) + my);
+                x = __ldcg(part(k) + slot_rows * (D + 2) + my);
+            }
+            float top = m;
+#pragma unroll
+            for (int d = 1; d < kFew; d <<= 1)
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float w = m == -INFINITY ? 0.f : ex2(m - top);
+            float sum = w * s, exact = w * x;
+#pragma unroll
+            for (int d = 1; d < kFew; d <<= 1) {
+                sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                exact += __shfl_xor_sync(0xffffffffu, exact, d);
+            }
+#pragma unroll
+            for (int r = 0; r < kFew; ++r) {
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int j = 0; j < kFew / AT_ONCE; ++j) {
+                    const float f = __shfl_sync(0xffffffffu, w, r * kFew + j * AT_ONCE + sub);
+                    if (row0 + r < it.rows && j * AT_ONCE + sub < it.parts)
+                        o.x += f * a[r][j].x, o.y += f * a[r][j].y, o.z += f * a[r][j].z, o.w += f * a[r][j].w;
+                }
+                if constexpr (AT_ONCE == 2) {
+                    o.x += __shfl_xor_sync(0xffffffffu, o.x, 16), o.y += __shfl_xor_sync(0xffffffffu, o.y, 16);
+                    o.z += __shfl_xor_sync(0xffffffffu, o.z, 16), o.w += __shfl_xor_sync(0xffffffffu, o.w, 16);
+                }
+                const float t = __shfl_sync(0xffffffffu, top, r * kFew), l = __shfl_sync(0xffffffffu, sum, r * kFew),
+                            e = __shfl_sync(0xffffffffu, exact, r * kFew);
+                if (sub == 0 && row0 + r < it.rows)
+                    finish4<DT>(p, q, it.kv_head, it.row0 + row0 + r, d4, o, t, l, e);
+            }
+        }
+        return;
+    }
     for (int row = blockIdx.y * kWarps + warp; row < it.rows; row += gridDim.y * kWarps) {
         // the first parts' results, maxima and sums in one round of loads
         constexpr int AHEAD = 8;
@@ -123,10 +201,12 @@ cudaError_t launch(const AttendParams& p, int slot_rows, int ctas, cudaStream_t 
 {
     // divided items: no more than there are items, or CTAs
     const int64_t items = ((int64_t)p.batch.tokens * p.group / slot_rows + p.batch.requests) * p.kv.heads;
-    // CTAs per item: a warp for every row, or for every other one of the larger slots
-    const dim3 grid((unsigned)(items < ctas ? items : ctas),
-                    (unsigned)(slot_rows <= 64 ? slot_rows / kWarps : slot_rows / (2 * kWarps)));
-    return launch_after(lbv_attend_join_kernel<DT, D>, grid, kWarps * 32, 0, st, p, slot_rows, ctas);
+    // CTAs per item: a warp for every row, or for every other one of the larger slots;
+    // with many items, of few parts each, for kFew rows
+    const bool direct = items >= ctas;
+    const int rows = slot_rows <= 64 ? kWarps : kWarps * (direct ? kFew : 2);
+    const dim3 grid((unsigned)(direct ? ctas : items), (unsigned)((slot_rows + rows - 1) / rows));
+    return launch_after(lbv_attend_join_kernel<DT, D>, grid, kWarps * 32, 0, st, p, slot_rows, ctas, direct);
 }
 
 }  // namespace
