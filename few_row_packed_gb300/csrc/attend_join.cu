@@ -19,10 +19,11 @@ constexpr int kWarps = 4;
 constexpr int kLook = 5;                         // items a lane looks at at a time
 constexpr int kFew = 4;                          // parts for which a warp takes kFew rows at once
 
-// direct: the grid has a column for every CTA, else one for every divided item.
-template <int DT, int D>
+// DIRECT: the grid has a column for every CTA, else one for every divided item (few, of
+// many parts).
+template <int DT, int D, bool DIRECT>
 __global__ void __launch_bounds__(kWarps * 32)
-    lbv_attend_join_kernel(const __grid_constant__ AttendParams p, int slot_rows, int ctas, bool direct)
+    lbv_attend_join_kernel(const __grid_constant__ AttendParams p, int slot_rows, int ctas)
 {
     after_previous();
     // The next launch may take its places now.  (The attention kernels do not let this one
@@ -37,7 +38,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     JoinItem it;
     int c0 = -1;                                 // the CTA the item starts in
     int4 i;
-    if (direct) {
+    if (DIRECT) {
         c0 = blockIdx.x;
         load(c0, i, it.parts);
         if (i.z <= 0)
@@ -134,7 +135,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
     for (int row = blockIdx.y * kWarps + warp; row < it.rows; row += gridDim.y * kWarps) {
         // the first parts' results, maxima and sums in one round of loads
-        constexpr int AHEAD = 8;
+        constexpr int AHEAD = DIRECT ? 8 : 20 / AT_ONCE;
         float4 first[AHEAD];
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j)
@@ -206,7 +207,8 @@ cudaError_t launch(const AttendParams& p, int slot_rows, int ctas, cudaStream_t 
     const bool direct = items >= ctas;
     const int rows = slot_rows <= 64 ? kWarps : kWarps * (direct ? kFew : 2);
     const dim3 grid((unsigned)(direct ? ctas : items), (unsigned)((slot_rows + rows - 1) / rows));
-    return launch_after(lbv_attend_join_kernel<DT, D>, grid, kWarps * 32, 0, st, p, slot_rows, ctas, direct);
+    return launch_after(direct ? lbv_attend_join_kernel<DT, D, true> : lbv_attend_join_kernel<DT, D, false>, grid,
+                        kWarps * 32, 0, st, p, slot_rows, ctas);
 }
 
 }  // namespace
