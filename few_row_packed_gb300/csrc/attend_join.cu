@@ -17,12 +17,12 @@ namespace {
 constexpr int kWarps = 4;
 
 constexpr int kLook = 5;                         // items a lane looks at at a time
-constexpr int kFew = 4;                          // parts for which a warp takes kFew rows at once
+constexpr int kFew = 2, kAtOnce = 4;             // of kFew parts a warp takes kAtOnce rows at once
 
 // DIRECT: the grid has a column for every CTA, else one for every divided item (few, of
 // many parts).
 template <int DT, int D, bool DIRECT>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, DIRECT ? 6 : 2)
     lbv_attend_join_kernel(const __grid_constant__ AttendParams p, int slot_rows, int ctas)
 {
     after_previous();
@@ -84,39 +84,34 @@ __global__ void __launch_bounds__(kWarps * 32)
         return p.partial + (size_t)(2 * (c0 + k) + (k == 0)) * slot;
     };
     if (it.parts <= kFew) {
-        // kFew rows at once: their results, and by lane kFew r + k the maximum and the
-        // sums of row r in part k
-        for (int row0 = (blockIdx.y * kWarps + warp) * kFew; row0 < it.rows; row0 += gridDim.y * kWarps * kFew) {
-            float4 a[kFew][kFew / AT_ONCE];
+        // their results, and by lane kFew r + k the maximum and the sums of row r in part k
+        for (int row0 = (blockIdx.y * kWarps + warp) * kAtOnce; row0 < it.rows;
+             row0 += gridDim.y * kWarps * kAtOnce) {
+            constexpr int LOADS = kFew / AT_ONCE;
+            float4 a[kAtOnce][LOADS];
 #pragma unroll
-            for (int r = 0; r < kFew; ++r)
+            for (int r = 0; r < kAtOnce; ++r)
 #pragma unroll
-                for (int j = 0; j < kFew / AT_ONCE; ++j)
+                for (int j = 0; j < LOADS; ++j)
                     if (row0 + r < it.rows && j * AT_ONCE + sub < it.parts)
                         a[r][j] = __ldcg(reinterpret_cast<const float4*>(part(j * AT_ONCE + sub) + (row0 + r) * D) + d4);
             const int my = row0 + lane / kFew, k = lane % kFew;
             float m = -INFINITY, s = 0.f, x = 0.f;
-            if (lane < kFew * kFew && my < it.rows && k < it.parts) {
+            if (lane < kFew * kAtOnce && my < it.rows && k < it.parts) {
                 m = __ldcg(part(k) + slot_rows * D + my);
                 s = __ldcg(part(k) + slot_rows * (D + 1) + my);
                 x = __ldcg(part(k) + slot_rows * (D + 2) + my);
             }
-            float top = m;
-#pragma unroll
-            for (int d = 1; d < kFew; d <<= 1)
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float top = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
             const float w = m == -INFINITY ? 0.f : ex2(m - top);
             float sum = w * s, exact = w * x;
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            exact += __shfl_xor_sync(0xffffffffu, exact, 1);
 #pragma unroll
-            for (int d = 1; d < kFew; d <<= 1) {
-                sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                exact += __shfl_xor_sync(0xffffffffu, exact, d);
-            }
-#pragma unroll
-            for (int r = 0; r < kFew; ++r) {
+            for (int r = 0; r < kAtOnce; ++r) {
                 float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int j = 0; j < kFew / AT_ONCE; ++j) {
+                for (int j = 0; j < LOADS; ++j) {
                     const float f = __shfl_sync(0xffffffffu, w, r * kFew + j * AT_ONCE + sub);
                     if (row0 + r < it.rows && j * AT_ONCE + sub < it.parts)
                         o.x += f * a[r][j].x, o.y += f * a[r][j].y, o.z += f * a[r][j].z, o.w += f * a[r][j].w;
@@ -203,9 +198,9 @@ cudaError_t launch(const AttendParams& p, int slot_rows, int ctas, cudaStream_t 
     // divided items: no more than there are items, or CTAs
     const int64_t items = ((int64_t)p.batch.tokens * p.group / slot_rows + p.batch.requests) * p.kv.heads;
     // CTAs per item: a warp for every row, or for every other one of the larger slots;
-    // with many items, of few parts each, for kFew rows
+    // with many items, of few parts each, for kAtOnce rows
     const bool direct = items >= ctas;
-    const int rows = slot_rows <= 64 ? kWarps : kWarps * (direct ? kFew : 2);
+    const int rows = slot_rows <= 64 ? kWarps : kWarps * (direct ? kAtOnce : 2);
     const dim3 grid((unsigned)(direct ? ctas : items), (unsigned)((slot_rows + rows - 1) / rows));
     return launch_after(direct ? lbv_attend_join_kernel<DT, D, true> : lbv_attend_join_kernel<DT, D, false>, grid,
                         kWarps * 32, 0, st, p, slot_rows, ctas);
