@@ -18,6 +18,15 @@
 //   * The blocks of the batch are divided evenly over one CTA per SM, as in
 //     attend_rows.cu; a causal tile counts those that it sees.  The parts of a
 //     divided item are added by a launch of their own (attend_join.cu).
+//
+// What bounds it (48 query over 8 key/value heads of 128, bf16): in long items the
+// hand-over of S and P, with the tensor cores 70 % busy: 2048 tokens at the end of 16,384
+// take 512 us, 1,510 TFLOP/s.  In short ones their ends, during which the tensor cores
+// wait: code that runs once an item is fetched anew and takes some 25 clocks an
+// instruction, where the block's loop takes 9; 16 requests of 1 to 600 tokens take 137 us,
+// their operations at the same rate 84.  With few blocks the start: 5 us to the first
+// scores and 5 more to fetch the block's code, some 20 KB; 8 tokens after 32,771 take
+// 36 us, their keys and values 20.
 #include "attend_common.cuh"
 
 namespace lbv {
@@ -30,9 +39,9 @@ constexpr int kKeys = 128;                       // keys per block
 constexpr int kTile = 128;                       // rows per stream
 constexpr int kRows = 2 * kTile;                 // rows per item
 // Units of an item: its queries and results, a block of one row tile, a block of two;
-// and the least share of a CTA.  A unit is 0.42 us of a long item.  (A prompt's and a
-// mixed batch's time with 8/1/2 of 0.84 us: 533 and 166 us; 12/1/2: 534 and 160; these:
-// 530 and 157; 40/3/4: 534 and 165.)
+// and the least share of a CTA.  A unit is 0.2 us of a long item.  (16 requests of 1 to
+// 600 tokens, us: 16/3/4 139, these 137, 28/3/4 139, 24/4/4 139, 36/4/5 139; a prompt's
+// chunk is the same within 1 %.)
 constexpr int kExtra = 24, kNarrow = 3, kWide = 4, kMinUnits = 24;
 using Items = Shape<kRows, kKeys, kExtra, kNarrow, kWide, kTile>;
 constexpr int kThreads = 384;                    // copies and MMAs, then the two streams
