@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -72,6 +73,10 @@ class _RowsArg(ctypes.Structure):
     """lbv_rows."""
     _fields_ = [("data", ctypes.c_void_p), ("heads", ctypes.c_int), ("dtype", ctypes.c_int),
                 ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+# the same bytes, made in half the time (four of them are a third of a call)
+_pack_rows = struct.Struct("@Piiqq").pack
 
 
 class _RulesArg(ctypes.Structure):
@@ -534,14 +539,16 @@ class Batch:
         self.requests, self.tokens = n, int(tokens)
 
 
-def _rows_arg(t, tokens: int, head_dim: int, what: str):
+def _rows_arg(t, tokens: int, head_dim: int, what: str) -> bytes:
     """lbv_rows of a [tokens, heads, head_dim] device tensor."""
     shape, stride = t.shape, t.stride()
     if len(shape) != 3 or shape[0] < tokens or shape[2] != head_dim or stride[2] != 1 \
             or not t.is_cuda:
         raise LbvError(ERR_INVALID_ARG, f"{what}: {tuple(shape)} with strides {stride} on "
                                         f"{t.device}; [{tokens}, heads, {head_dim}] is wanted")
-    return _RowsArg(t.data_ptr(), shape[1], _dtype_id(t.dtype), stride[0], stride[1])
+    dtype = t.dtype
+    return _pack_rows(t.data_ptr(), shape[1], _dtype_ids.get(dtype) or _dtype_id(dtype), stride[0],
+                      stride[1])
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = ROPE_NONE,
@@ -584,13 +591,13 @@ def rope_append(rope: Rope, batch: Batch, cache: KVCache, q, k, v, q_out, positi
     be None.  positions: int32 [tokens] rotary positions (default: the cache
     positions)."""
     n, d = batch.tokens, cache.head_dim
-    q_arg = None if q is None else _byref(_rows_arg(q, n, d, "q"))
-    o_arg = None if q_out is None else _byref(_rows_arg(q_out, n, d, "q_out"))
+    q_arg = None if q is None else _rows_arg(q, n, d, "q")
+    o_arg = None if q_out is None else _rows_arg(q_out, n, d, "q_out")
     if positions is not None:
         import torch
         positions = _words(positions, torch.int32, n, "positions")
     status = lib().lbv_rope_append(rope.handle, batch.ref, cache.handle, q_arg,
-                                   _byref(_rows_arg(k, n, d, "k")), _byref(_rows_arg(v, n, d, "v")),
+                                   _rows_arg(k, n, d, "k"), _rows_arg(v, n, d, "v"),
                                    o_arg, positions, _stream(stream))
     if status:
         _check(status)
@@ -611,7 +618,7 @@ def attend(cache: KVCache, batch: Batch, q, out, scale: float, window: int = 0, 
     [tokens, heads]; workspace: attend_workspace_bytes, zeroed once.  See
     lbv_attend."""
     n, d = batch.tokens, cache.head_dim
-    q_arg, o_arg = _byref(_rows_arg(q, n, d, "q")), _byref(_rows_arg(out, n, d, "out"))
+    q_arg, o_arg = _rows_arg(q, n, d, "q"), _rows_arg(out, n, d, "out")
     if tree is not None or lse is not None:
         import torch
         tree = _words(tree, torch.int64, n, "tree")
