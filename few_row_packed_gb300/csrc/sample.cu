@@ -32,11 +32,12 @@
 // top-p) or the candidates do not fit the list, a finer histogram counts and weighs
 // all tokens above the bound.  Down to the bin that holds tau they may fit after all;
 // if not, the tokens of that bin alone are listed and sorted, which gives tau, and the
-// token is drawn from the slices: one pass for the weight of each, and two short ones
-// by the CTA that holds the token.  Where even the bin does not fit (thousands of
-// equal logits), tau is found by a search over the bits of the (order-preserving)
-// keys, counting and summing above trial values, two bits a round.  Rows without
-// rules are drawn from the slices straight away.
+// token is drawn from the slices: a pass sums the weights by warps' segments, and the CTA
+// and warp in whose segment the token lies find it (or, where some of tau's equals are
+// left out, the CTA by visiting its slice in index order).  Where even the bin does not fit
+// (thousands of equal logits), tau is found by a search over the bits of the
+// (order-preserving) keys, counting and summing above trial values, two bits a round.
+// Rows with neither top-k nor top-p are drawn from the slices straight away.
 //
 // Nothing of the row stays on chip, so that four CTAs share an SM: while one
 // waits at a barrier, the others' loads keep memory busy.
@@ -46,13 +47,13 @@
 // weight) and of the sort, then memory.  Time of a call with 256 rows of 128,256 bf16
 // logits / 8 rows of 151,936 fp32 / 1 row of 128,256 fp32, in us, where reading the
 // logits once takes 9.7 / 0.7 / 0.1:
-//     temperature 0 (the maximum)      21 /  9 /  9    (maximum by elements: 30 / 9 / 9)
-//     top-k 50                         60 / 17 / 17
-//     no rule                         118 / 31 / 25
-//     top-p 0.5, <= 2048 kept         325 / 81 / 44
-//     top-p 0.9, some 15,000 kept     416 / 74 / 58    (by the bit search: 1125 / 207 / 133)
-//     top-k 5000                      299 / 62 / 48    (by the bit search: 1031 / 188 / 125)
-// All logits equal, which the search has to settle: up to 4270 / 285 / 208.
+//     temperature 0 (the maximum)      19 /  9 /  9    (maximum by elements: 30 / 9 / 9)
+//     top-k 50                         58 / 14 / 14
+//     no rule, or min-p                84 / 16 / 12    (by visits in index order: 116 / 28 / 22)
+//     top-p 0.5, some 2,000 kept      321 / 55 / 42
+//     top-p 0.9, some 15,000 kept     418 / 58 / 45    (by the bit search: 1125 / 207 / 133)
+//     top-k 5000                      300 / 46 / 36    (by the bit search: 1031 / 188 / 125)
+// All logits equal, which the search has to settle: up to 4290 / 284 / 205.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -71,6 +72,7 @@ constexpr int kBins = kThreads;            // one thread per bin
 constexpr int kList = 8 * kThreads;        // candidates the first CTA can take
 constexpr int kAhead = 4;                  // vectors of a thread on their way
 constexpr int kParts = 8;                  // of a warp's tokens, in the index-order sum
+constexpr int kSegs = kList;               // sums of a slice's segments that are kept
 constexpr int kMaxCluster = 16;
 constexpr float kBinsPerNat = 8.f;
 constexpr int kFine = 4 * kThreads;        // bins of a row with many candidates
@@ -372,24 +374,34 @@ __device__ __forceinline__ void each(const Slice<DT>& s, int tid, Ring& ring, F 
 // The sum of whole(f(value)) over the thread's logits.  f gives 0 to 1; adding a power
 // of two, rounded towards zero, leaves the integer part of 2^17 f in the low bits of the
 // sum, and that of 2^40 times the remainder in those of a second one; their biases are
-// taken off once a vector.
+// taken off once a vector.  seg (optional): the sum over each warp's vectors of a round, in
+// index order, for the first kSegs rounds and warps.
 template <int DT, typename F>
-__device__ __forceinline__ uint64_t sum_whole(const Slice<DT>& s, int tid, Ring& ring, F f)
+__device__ __forceinline__ uint64_t sum_whole(const Slice<DT>& s, int tid, Ring& ring, uint64_t* seg, F f)
 {
     constexpr int E = Slice<DT>::E;
     constexpr uint32_t kHigh = 0x42800000u, kLow = 0x37000000u;        // 2^6, 2^-17
     uint64_t sum = 0;
+    int at = tid >> 5, rest = (s.n - s.head()) / E - (tid & ~31);      // the warp's segment; vectors from its first on
     each_vector(s, tid, ring, [&](uint32_t (&q)[4], int) {
         uint32_t high = 0, low = 0;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const float w = f(s.element(q, e));
             const float a = __fadd_rz(w, __uint_as_float(kHigh));
-            const float rest = __fsub_rn(w, __fsub_rn(a, __uint_as_float(kHigh)));
+            const float over = __fsub_rn(w, __fsub_rn(a, __uint_as_float(kHigh)));
             high += __float_as_uint(a);
-            low += __float_as_uint(__fadd_rz(rest, __uint_as_float(kLow)));
+            low += __float_as_uint(__fadd_rz(over, __uint_as_float(kLow)));
         }
-        sum += ((uint64_t)(high - E * kHigh) << 23) + (low - E * kLow);
+        high -= E * kHigh, low -= E * kLow;
+        sum += ((uint64_t)high << 23) + low;
+        if (seg) {                                                     // 2^20 and 2^26 a lane at most
+            const unsigned lanes = rest >= 32 ? 0xffffffffu : (1u << rest) - 1;
+            high = __reduce_add_sync(lanes, high), low = __reduce_add_sync(lanes, low);
+            if ((tid & 31) == 0 && at < kSegs)
+                seg[at] = ((uint64_t)high << 23) + low;
+            at += kWarps, rest -= kThreads;
+        }
     }, [&](float x, int) { sum += whole(f(x)); });
     return sum;
 }
@@ -476,6 +488,29 @@ __device__ __noinline__ Kept select(Ctx c, D d, Row row, uint64_t total)
     return kept;
 }
 
+// The block's sum of v, and in `before` that of the threads before this one.
+__device__ __noinline__ uint64_t block_scan(Ctx c, uint64_t v, uint64_t& before)
+{
+    uint64_t upto = v;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+        const uint64_t o = __shfl_up_sync(0xffffffffu, upto, s);
+        upto += c.lane >= s ? o : 0;
+    }
+    __syncthreads();
+    if (c.lane == 31)
+        c.sh->sums[c.warp] = upto;
+    __syncthreads();
+    uint64_t all = 0, below = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        below = i == c.warp ? all : below;
+        all += c.sh->sums[i];
+    }
+    before = below + upto - v;
+    return all;
+}
+
 // Draws from the kept tokens of all slices in index order: one pass gives each CTA's
 // weight, and the CTA in which the running sum passes u's share looks for the token.
 // Returns its place in the slice, or -1 in the other CTAs; *prob its probability
@@ -490,11 +525,13 @@ __device__ __noinline__ int draw(Ctx c, Slice<DT> d, Row row, Kept kept, float* 
         return f >= row.min_p || row.min_p <= 0.f ? w : 0.f;
     };
     auto weight = [&](float x) { return whole(share(x)); };
-    const float tau = kept.tau ? of_key(kept.tau) : kNegInf;
+    // all of tau's are kept, or those above it and some of its own
+    const bool ties_out = kept.ties != ~0ull;
+    const float tau = kept.tau ? of_key(kept.tau) : kNegInf, from = ties_out ? of_key(kept.tau + 1) : tau;
     unsigned equal = 0;
-    uint64_t sum = sum_whole(d, c.tid, sh.ring, [&](float x) {
-        equal += x == tau;
-        return x > tau ? share(x) : 0.f;
+    uint64_t sum = sum_whole(d, c.tid, sh.ring, sh.list, [&](float x) {
+        equal += ties_out && x == tau;
+        return x >= from ? share(x) : 0.f;
     });
     uint64_t all[2] = {sum, equal}, below[2], here[2];
     reduce<2>(c, 2, all, below, here);
@@ -507,6 +544,70 @@ __device__ __noinline__ int draw(Ctx c, Slice<DT> d, Row row, Kept kept, float* 
     const uint64_t target = part(f, total);
     if (target < at || target >= at + here[0] + (ties_upto - ties_below) * tie_w)
         return -1;
+    // ---- by the segments' sums, where ties need no count ----
+    const int head = d.head(), body = (d.n - head) / Slice<DT>::E;
+    const int segs = (body + kThreads - 1) / kThreads * kWarps;
+    if (!ties_out && segs <= kSegs) {
+        uint64_t first = at, before;
+        if (head > 0)
+            first += block_scan(c, c.tid < head ? weight(d.get(c.tid)) : 0, before);
+        const int each_of = (segs + kThreads - 1) / kThreads, s0 = c.tid * each_of, s1 = min(s0 + each_of, segs);
+        auto seg = [&](int i) { return i / kWarps * kThreads + i % kWarps * 32 < body ? sh.list[i] : 0; };
+        uint64_t mine = 0;
+        for (int i = s0; i < s1; ++i)
+            mine += seg(i);
+        if (c.tid == 0)
+            sh.bin = sh.pick = -1;
+        const uint64_t sums = block_scan(c, mine, before);       // its barriers order sh.bin and the segments
+        before += first;
+        if (target >= before && target < before + mine)
+            for (int i = s0; i < s1; ++i) {
+                const uint64_t w = seg(i);
+                if (target < before + w) {
+                    sh.bin = i;
+                    sh.above_sum = before;
+                    break;
+                }
+                before += w;
+            }
+        __syncthreads();
+        if (target >= first && target < first + sums) {          // else in the few logits around them
+            if (c.warp == 0) {
+                constexpr int E = Slice<DT>::E;
+                const int v = sh.bin / kWarps * kThreads + sh.bin % kWarps * 32 + c.lane, i0 = head + v * E;
+                float x[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    x[e] = v < body ? d.get(i0 + e) : kNegInf;
+                uint64_t w[E], mine = 0;
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    w[e] = x[e] >= from ? weight(x[e]) : 0;
+                    mine += w[e];
+                }
+                uint64_t upto = mine;
+#pragma unroll
+                for (int s = 1; s < 32; s <<= 1) {
+                    const uint64_t o = __shfl_up_sync(0xffffffffu, upto, s);
+                    upto += c.lane >= s ? o : 0;
+                }
+                uint64_t here = sh.above_sum + upto - mine;
+                if (target >= here && target < here + mine)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        if (target >= here && target < here + w[e]) {
+                            sh.pick = i0 + e;
+                            sh.pick_prob = __fdiv_rn(__ull2float_rn(w[e]), __ull2float_rn(total));
+                        }
+                        here += w[e];
+                    }
+            }
+            __syncthreads();
+            *prob = sh.pick_prob;
+            return sh.pick;
+        }
+    }
+    // ---- by visits in index order ----
     const int groups = (d.n + 31) / 32, per = (groups + kWarps - 1) / kWarps;
     const int g0 = min(c.warp * per, groups), g1 = min(g0 + per, groups);
     const unsigned before = (1u << c.lane) - 1;
@@ -663,29 +764,6 @@ __device__ __forceinline__ void sort_list(Shared& sh, int n2, int tid)
 __device__ __forceinline__ int power_above(int n)
 {
     return n <= 2 ? 2 : 1 << (32 - __clz(n - 1));
-}
-
-// The block's sum of v, and in `before` that of the threads before this one.
-__device__ __noinline__ uint64_t block_scan(Ctx c, uint64_t v, uint64_t& before)
-{
-    uint64_t upto = v;
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-        const uint64_t o = __shfl_up_sync(0xffffffffu, upto, s);
-        upto += c.lane >= s ? o : 0;
-    }
-    __syncthreads();
-    if (c.lane == 31)
-        c.sh->sums[c.warp] = upto;
-    __syncthreads();
-    uint64_t all = 0, below = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-        below = i == c.warp ? all : below;
-        all += c.sh->sums[i];
-    }
-    before = below + upto - v;
-    return all;
 }
 
 // Lists in the first CTA the tokens that visit(found) finds in each slice; returns
@@ -857,14 +935,17 @@ __device__ __noinline__ int select_binned(Ctx c, Slice<DT> slice, Row row, float
             __syncthreads();
             const int taken = sh.pick;
             const uint32_t tau = (uint32_t)(sh.list[taken - 1] >> 32);
-            uint64_t greater = 0, unused;
-            for (int i = c.tid; i < n; i += kThreads)
-                greater += (uint32_t)(sh.list[i] >> 32) > tau;
-            greater = block_scan(c, greater, unused);
+            uint64_t counts = 0, unused;               // above tau, and equal to it
+            for (int i = c.tid; i < n; i += kThreads) {
+                const uint32_t k = (uint32_t)(sh.list[i] >> 32);
+                counts += (k > tau ? 1 : 0) + ((uint64_t)(k == tau) << 32);
+            }
+            counts = block_scan(c, counts, unused);
+            const uint64_t ties = (uint64_t)taken - (counts & 0xFFFFFFFFu);
             if (c.tid < c.nctas) {
                 Shared* o = cl.map_shared_rank(&sh, c.tid);
                 o->result[0] = tau;
-                o->result[1] = (uint64_t)taken - greater;
+                o->result[1] = ties == counts >> 32 ? ~0ull : ties;
                 o->result[2] = above + all;
             }
         }
@@ -873,6 +954,10 @@ __device__ __noinline__ int select_binned(Ctx c, Slice<DT> slice, Row row, float
         kept.tau = (uint32_t)sh.result[0];
         kept.ties = sh.result[1];
     };
+    // So many candidates are sorted in less time than drawing from the slices takes: with the
+    // larger clusters of a few rows (8 rows of 151,936 fp32, 2,000 candidates: 80 us sorted, 55
+    // from the slices), and with the smaller ones (256 rows of 128,256 bf16: 321 and 362).
+    const int sorted = c.nctas > 8 ? 2 * kThreads : kList;
     // Below a cut that min-p gave neither top-k nor top-p need be reached: then min-p
     // alone decides, and all tokens are kept here.
     const int unreached = cut > kNegInf ? kByValue : kSearch;
@@ -891,7 +976,7 @@ __device__ __noinline__ int select_binned(Ctx c, Slice<DT> slice, Row row, float
         count_k = sh.bin_count;
         above_k = sh.above_sum;
         need = row.k - sh.above_count;
-        if (sh.above_count + count_k <= kList)
+        if (sh.above_count + count_k <= sorted)
             return list_down_to(bin_k);
         if (count_k > kList)
             return kSearch;
@@ -908,7 +993,7 @@ __device__ __noinline__ int select_binned(Ctx c, Slice<DT> slice, Row row, float
         if (bin < 0)
             return unreached;
         const int count = sh.bin_count;
-        if (row.k == 0 && sh.above_count + count <= kList)
+        if (row.k == 0 && sh.above_count + count <= sorted)
             return list_down_to(bin);
         if (count > kList)
             return kSearch;
@@ -1071,7 +1156,7 @@ __global__ void __launch_bounds__(kThreads, 4) lbv_sample_kernel(const __grid_co
     Kept kept = {0u, ~0ull};
     const bool by_rank = row.k > 0 && row.k < p.N, by_sum = row.top_p < 1.f;
     row.k = by_rank ? row.k : 0;
-    if (by_rank || by_sum || row.min_p > 0.f) {
+    if (by_rank || by_sum) {
         // ---- the histogram, and with it the row's weight ----
         const float scale = row.filter_r * kBinsPerNat;
         const float depth = high == row.top ? 0.f : (row.top - high) * scale;  // bin 0 holds the maximum
@@ -1079,7 +1164,7 @@ __global__ void __launch_bounds__(kThreads, 4) lbv_sample_kernel(const __grid_co
             atomicAdd(&sh.hist[(int)depth], 1u);
         uint64_t total = 0;
         if (by_sum && !by_rank) {
-            uint64_t v[1] = {sum_whole(slice, c.tid, sh.ring, [&](float x) {
+            uint64_t v[1] = {sum_whole(slice, c.tid, sh.ring, nullptr, [&](float x) {
                 return weight_f(x, row.top, row.filter_r);
             })};
             reduce<1>(c, 2, v);                        // orders the histograms too
@@ -1146,7 +1231,7 @@ __global__ void __launch_bounds__(kThreads, 4) lbv_sample_kernel(const __grid_co
                 }
             });
         }
-        if ((n == kSearch || n > kList) && (by_rank || by_sum)) {
+        if (n == kSearch || n > kList) {
             n = select_binned(c, slice, row, cut, total, begin, kept);
             if (n == kSearch)
                 kept = select(c, slice, row, total);
