@@ -9,6 +9,8 @@
 // round trips to L2 and the launch: 96 rows of some 19 parts take 5 us after the attention
 // kernel's end (2 the launch, 2 to find the item, 1.5 the parts), 152 items of 256
 // rows 9 (40 MB read).
+#include <algorithm>
+
 #include "attend_common.cuh"
 
 namespace lbv {
@@ -200,11 +202,14 @@ cudaError_t launch(const AttendParams& p, int slot_rows, int ctas, cudaStream_t 
 {
     // divided items: no more than there are items, or CTAs
     const int64_t items = ((int64_t)p.batch.tokens * p.group / slot_rows + p.batch.requests) * p.kv.heads;
-    // CTAs per item: a warp for every row, or for every other one of the larger slots;
-    // with many items, of few parts each, for kAtOnce rows
-    const bool direct = items >= ctas;
-    const int rows = slot_rows <= 64 ? kWarps : kWarps * (direct ? kAtOnce : 2);
-    const dim3 grid((unsigned)(direct ? ctas : items), (unsigned)((slot_rows + rows - 1) / rows));
+    // A column for every CTA where the items have up to eight parts on average, else for
+    // every item; blocks for the rows of an item of twice the average (more are taken in
+    // turn).  Blocks without work cost too: with a column for each of 106 undivided items and
+    // 32 blocks for the largest slot, the launch took 28 us.
+    const bool direct = items * 8 >= ctas;
+    const int64_t rows = std::min<int64_t>(slot_rows, 2 * attend_average_rows(p));
+    const int per = slot_rows <= 64 ? kWarps : kWarps * (direct ? kAtOnce : 2);
+    const dim3 grid((unsigned)(direct ? ctas : items), (unsigned)((rows + per - 1) / per));
     return launch_after(direct ? lbv_attend_join_kernel<DT, D, true> : lbv_attend_join_kernel<DT, D, false>, grid,
                         kWarps * 32, 0, st, p, slot_rows, ctas);
 }
