@@ -41,8 +41,9 @@ constexpr int kRows = 2 * kTile;                 // rows per item
 // Units of an item: its queries and results, a block of one row tile, a block of two;
 // and the least share of a CTA.  A unit is 0.2 us of a long item.  (16 requests of 1 to
 // 600 tokens, us: 16/3/4 139, these 137, 28/3/4 139, 24/4/4 139, 36/4/5 139; a prompt's
-// chunk is the same within 1 %.)
-constexpr int kExtra = 24, kNarrow = 3, kWide = 4, kMinUnits = 24;
+// chunk is the same within 1 %.  The least share: 40 small batches take 4 % less with 8 or
+// 12 than with 24, 12 % less than with 48; 20 tokens over 3,943 keys 15.6 and 20.3 us.)
+constexpr int kExtra = 24, kNarrow = 3, kWide = 4, kMinUnits = 12;
 using Items = Shape<kRows, kKeys, kExtra, kNarrow, kWide, kTile>;
 constexpr int kThreads = 384;                    // copies and MMAs, then the two streams
 // Registers a thread after the split: 168 * 384 at launch = 88 * 128 + 208 * 256.
