@@ -528,6 +528,7 @@ __device__ __noinline__ int draw(Ctx c, Slice<DT> d, Row row, Kept kept, float* 
     // all of tau's are kept, or those above it and some of its own
     const bool ties_out = kept.ties != ~0ull;
     const float tau = kept.tau ? of_key(kept.tau) : kNegInf, from = ties_out ? of_key(kept.tau + 1) : tau;
+    auto kept_weight = [&](float x) { return x >= from ? weight(x) : 0; };
     unsigned equal = 0;
     uint64_t sum = sum_whole(d, c.tid, sh.ring, sh.list, [&](float x) {
         equal += ties_out && x == tau;
@@ -550,7 +551,7 @@ __device__ __noinline__ int draw(Ctx c, Slice<DT> d, Row row, Kept kept, float* 
     if (!ties_out && segs <= kSegs) {
         uint64_t first = at, before;
         if (head > 0)
-            first += block_scan(c, c.tid < head ? weight(d.get(c.tid)) : 0, before);
+            first += block_scan(c, c.tid < head ? kept_weight(d.get(c.tid)) : 0, before);
         const int each_of = (segs + kThreads - 1) / kThreads, s0 = c.tid * each_of, s1 = min(s0 + each_of, segs);
         auto seg = [&](int i) { return i / kWarps * kThreads + i % kWarps * 32 < body ? sh.list[i] : 0; };
         uint64_t mine = 0;
@@ -582,7 +583,7 @@ __device__ __noinline__ int draw(Ctx c, Slice<DT> d, Row row, Kept kept, float* 
                 uint64_t w[E], mine = 0;
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
-                    w[e] = x[e] >= from ? weight(x[e]) : 0;
+                    w[e] = kept_weight(x[e]);
                     mine += w[e];
                 }
                 uint64_t upto = mine;
