@@ -520,8 +520,9 @@ class KVCache:
 class Batch:
     """The new tokens of one step (lbv_batch): q_start int32 [requests + 1],
     kv_len int32 [requests] (new tokens included), block_table int32
-    [requests, table_pages], all on the device and kept alive here; `tokens` is
-    the number of rows of the token-major tensors."""
+    [requests, table_pages] (rows may be apart, but do not overlap), all on the
+    device and kept alive here; `tokens` is the number of rows of the token-major
+    tensors."""
 
     def __init__(self, q_start, kv_len, block_table, tokens: int):
         import torch
@@ -530,10 +531,15 @@ class Batch:
                 or block_table.dtype != torch.int32 or not block_table.is_cuda:
             raise LbvError(ERR_INVALID_ARG, "block_table: an int32 device tensor [requests, pages] "
                                             "is wanted")
+        stride, pages = block_table.stride(0), block_table.shape[1]
+        if stride < pages:
+            if n > 1:
+                raise LbvError(ERR_INVALID_ARG, f"block_table: rows of {pages} pages overlap at a "
+                                                f"stride of {stride}")
+            stride = pages                  # a single row's stride is of no use
         self.arg = _BatchArg(_words(q_start, torch.int32, n + 1, "q_start"),
                              _words(kv_len, torch.int32, n, "kv_len"), block_table.data_ptr(), n,
-                             int(tokens), max(block_table.stride(0), block_table.shape[1]),
-                             block_table.shape[1])
+                             int(tokens), stride, pages)
         self.ref = ctypes.byref(self.arg)
         self.q_start, self.kv_len, self.block_table = q_start, kv_len, block_table
         self.requests, self.tokens = n, int(tokens)
