@@ -383,6 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 key & ((1 << p.kv.page_shift) - 1), w.head, page, full(st));
                     }
                 }
+                __syncwarp();                                        // every lane has read the item
                 if (lane == 0)
                     mbar_arrive(item_empty(it));
             }
@@ -806,6 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             if (!dual)                                   // both streams are done reading O and the statistics
                 named_bar_sync(1, 256);
+            __syncwarp();                                // every lane has read the item
             if (lane == 0)
                 mbar_arrive(item_empty(it));
         }
