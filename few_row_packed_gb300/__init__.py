@@ -155,6 +155,7 @@ def lib():
             "lbv_attend_workspace_bytes": (S, [P, P, I]),
             "lbv_attend": (st, [P, P, P, P, F, I, P, P, P, S, P]),
             "lbv_attend_status": (st, [P]),
+            "lbv_attend_test_wait": (st, [P, P, P, P, F, I, P, P, P, S, I, P]),
             "lbv_sample": (st, [P, I, I, L64, I, P, P, P, P, P]),
             "lbv_last_error": (ctypes.c_char_p, []),
             "lbv_version": (ctypes.c_char_p, []),
@@ -640,6 +641,17 @@ def attend_status(workspace):
     """Raises LbvError(ERR_TIMEOUT) if an attention kernel that used the
     workspace gave up a bounded wait (synchronises the device)."""
     _check(lib().lbv_attend_status(_ptr(workspace)))
+
+
+def attend_test_wait(cache: KVCache, batch: Batch, q, out, scale: float, workspace, left_out: int,
+                     window: int = 0, stream=None):
+    """Test export: attend with short waits, whose first CTA leaves out one copy
+    (lbv_attend_test_wait)."""
+    n, d = batch.tokens, cache.head_dim
+    _check(lib().lbv_attend_test_wait(cache.handle, batch.ref, _rows_arg(q, n, d, "q"),
+                                      _rows_arg(out, n, d, "out"), scale, window, None, None, _ptr(workspace),
+                                      workspace.numel() * workspace.element_size(), left_out,
+                                      _stream(stream)))
 
 
 def sample(logits, u, token, prob=None, temperature=None, top_k=None, top_p=None, min_p=None,

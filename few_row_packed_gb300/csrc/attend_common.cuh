@@ -45,14 +45,14 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
     return ok != 0;
 }
 
-// Bounded wait (about a second of SM cycles): false if it gave up.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity)
+// Bounded wait (`limit` SM clocks): false if it gave up.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, unsigned limit)
 {
     if (mbar_try(bar, parity))
         return true;
     const long long t0 = clock64();
     while (!mbar_try(bar, parity))
-        if (clock64() - t0 > (1ll << 31))
+        if (clock64() - t0 > (long long)limit)
             return false;
     return true;
 }

@@ -27,7 +27,12 @@ struct AttendParams {
     unsigned* counters;              // one per CTA, zero between calls
     float* partial;                  // slots of partial results
     void* items;                     // one JoinItem per CTA where they are joined apart, else NULL
+    unsigned wait_limit;             // clocks until a wait gives up
+    int left_out;                    // test only: the copy that the first CTA leaves out, or -1
 };
+
+constexpr unsigned kAttendWaitLimit = 1u << 31;  // about a second
+constexpr unsigned kAttendTestLimit = 1u << 20;  // half a millisecond
 
 constexpr int kAttendMaxCtas = 608;              // CTAs of a launch (152 SMs x 4), and counters
 // Workspace: status word, counters, join items, partial results.

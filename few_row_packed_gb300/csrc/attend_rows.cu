@@ -148,18 +148,18 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, Geo<D>::CTAS)
         const int slots = min(kBlock, 1 << p.kv.page_shift);     // rows of a box
         const int boxes = kBlock / slots;                        // per 64 elements
         const int total_boxes = boxes * (D / 64) * 2;
-        int n = 0;
-        while (w.next()) {
+        int n = 0;                                               // blocks asked for
+        while (ok && w.next()) {
             const int* table = p.batch.block_table + (int64_t)w.r * p.batch.table_stride;
             for (int b = w.b_first; b < w.b_last; ++b) {
                 const int st = n % G::NST, k0 = w.key0(b);
-                if (n >= G::NST && ok)
-                    ok = mbar_wait(empty(st), (uint32_t)((n / G::NST - 1) & 1));
-                ++n;
-                if (!__all_sync(0xffffffffu, ok)) {              // a reader is stuck: no more copies
-                    ok = false;
+                if (n >= G::NST)
+                    ok = mbar_wait(empty(st), (uint32_t)((n / G::NST - 1) & 1), p.wait_limit);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)                                         // a reader is stuck: no more copies
+                    break;
+                if (n++ == p.left_out && blockIdx.x == 0)
                     continue;
-                }
                 if (lane == 0)
                     mbar_expect_tx(full(st), G::STAGE);
                 __syncwarp();
@@ -176,10 +176,11 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, Geo<D>::CTAS)
                 }
             }
         }
-        // the ring drains before shared memory goes away
+        // the copies land before shared memory goes away, also after a wait that ran out
         for (int i = 0; i < G::NST; ++i)
-            if (n - 1 - i >= 0 && ok)
-                ok = mbar_wait(empty((n - 1 - i) % G::NST), (uint32_t)(((n - 1 - i) / G::NST) & 1));
+            if (n - 1 - i >= 0 && !mbar_wait(full((n - 1 - i) % G::NST), (uint32_t)(((n - 1 - i) / G::NST) & 1),
+                                             p.wait_limit))
+                ok = false;
         if (!ok && lane == 0)
             atomicOr(p.status, 1u);
         return;
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, Geo<D>::CTAS)
         for (int b = w.b_first; b < w.b_last; ++b) {
             const int st = n % G::NST, k0 = w.key0(b);
             if (ok)
-                ok = mbar_wait(full(st), (uint32_t)((n / G::NST) & 1));
+                ok = mbar_wait(full(st), (uint32_t)((n / G::NST) & 1), p.wait_limit);
             ++n;
             const uint32_t ks_base = sbase + st * G::STAGE, vs_base = ks_base + (D / 64) * G::HALF;
             const int my0 = k0 + warp * 16;                      // this warp's 16 keys

@@ -71,7 +71,7 @@ struct Geo {
     static constexpr int RING = 2 * SLOT;
     static constexpr int NSLOT = D == 128 ? 5 : 10;
     static constexpr int BARS = RING + NSLOT * SLOT;
-    static constexpr int NBARS = 2 * NSLOT + 9 + 2 * kItems;
+    static constexpr int NBARS = 2 * NSLOT + 10 + 2 * kItems;
     static constexpr int STATS = (BARS + NBARS * 8 + 15) / 16 * 16;   // [2][128] m and sums of the streams
     static constexpr int RATIOS = STATS + 2 * kTile * 8;    // [2][128] exact over rounded sums
     static constexpr int ITEMS = RATIOS + 2 * kTile * 2;    // ring of items
@@ -301,6 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto p_full = [&](int s, int half) { return bar(2 * G::NSLOT + 5 + 2 * s + half); };  // P replaced S
     auto item_full = [&](int i) { return bar(2 * G::NSLOT + 9 + i % kItems); };
     auto item_empty = [&](int i) { return bar(2 * G::NSLOT + 9 + kItems + i % kItems); };
+    const uint32_t mmas_done = bar(2 * G::NSLOT + 9 + 2 * kItems);   // every MMA of the CTA
     const Item* items = reinterpret_cast<const Item*>(smem + G::ITEMS);
 
     if (tid == 0) {
@@ -309,6 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(empty(i), 1);
         }
         mbar_init(q_full, 8);
+        mbar_init(mmas_done, 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(s_full(s), 1);
             mbar_init(p_full(s, 0), 4);
@@ -337,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     auto wait = [&](uint32_t b, uint32_t parity) {
         if (ok)
-            ok = mbar_wait(b, parity);
+            ok = mbar_wait(b, parity, p.wait_limit);
     };
     // item i of the share, as the scheduler wrote it
     auto item_at = [&](int i) -> const Item& {
@@ -355,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const int slots = min(64, 1 << p.kv.page_shift);         // rows of a box
             const int boxes = kKeys / slots;
-            int n = 0;
+            int n = 0;                                               // slots asked for
             for (int it = 0;; ++it) {
                 const Item& w = item_at(it);
                 if (!__all_sync(0xffffffffu, ok) || w.nb == 0)
@@ -365,9 +367,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int st = n % G::NSLOT, k0 = w.key0 + (i >> 1) * kKeys;
                     if (n >= G::NSLOT)
                         wait(empty(st), (uint32_t)((n / G::NSLOT - 1) & 1));
-                    ++n;
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok)
+                        break;
+                    if (n++ == p.left_out && blockIdx.x == 0)
                         continue;
                     if (lane == 0)
                         mbar_expect_tx(full(st), G::SLOT);
@@ -387,7 +390,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0)
                     mbar_arrive(item_empty(it));
             }
-            // the ring drains before shared memory goes away
+            // the copies land before shared memory goes away, also after a wait that ran
+            // out, and so do the commits that free their slots
+            for (int i = 0; i < G::NSLOT; ++i)
+                if (n - 1 - i >= 0 && !mbar_wait(full((n - 1 - i) % G::NSLOT),
+                                                 (uint32_t)(((n - 1 - i) / G::NSLOT) & 1), p.wait_limit))
+                    ok = false;
             for (int i = 0; i < G::NSLOT; ++i)
                 if (n - 1 - i >= 0)
                     wait(empty((n - 1 - i) % G::NSLOT), (uint32_t)(((n - 1 - i) / G::NSLOT) & 1));
@@ -476,11 +484,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            // the last MMAs end before tensor memory goes away
-            if (np0)
-                wait(o_done(0), (np0 - 1) & 1);
-            if (np1)
-                wait(o_done(1), (np1 - 1) & 1);
+            // the last MMAs end before tensor memory goes away, also after a wait that ran out
+            __syncwarp();
+            commit(mmas_done);
+            if (!mbar_wait(mmas_done, 0, p.wait_limit))
+                ok = false;
         } else if (warp == 2) {
             // ---- the share's items ----
             Start& start = *reinterpret_cast<Start*>(smem + G::START);

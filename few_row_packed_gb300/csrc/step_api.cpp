@@ -351,11 +351,11 @@ size_t lbv_attend_workspace_bytes(const lbv_kv_cache* cache, const lbv_batch* ba
     return lbv::kAttendPartial + (rows > tiles ? rows : tiles) * sizeof(float);
 }
 
-lbv_status lbv_attend(const lbv_kv_cache* cache, const lbv_batch* batch, const lbv_rows* q,
-                      const lbv_rows* out, float scale, int window, const uint64_t* tree,
-                      float* lse, void* workspace, size_t workspace_bytes, lbv_stream stream)
+// lbv_attend, by the name `fn`; left_out >= 0: the test of the bounded waits.
+static lbv_status attend(const char* fn, const lbv_kv_cache* cache, const lbv_batch* batch, const lbv_rows* q,
+                         const lbv_rows* out, float scale, int window, const uint64_t* tree, float* lse,
+                         void* workspace, size_t workspace_bytes, int left_out, lbv_stream stream)
 {
-    const char* fn = "lbv_attend";
     lbv::set_error(LBV_OK, "");
     lbv_status st = check_batch(fn, batch);
     if (st == LBV_OK)
@@ -412,6 +412,8 @@ lbv_status lbv_attend(const lbv_kv_cache* cache, const lbv_batch* batch, const l
     p.counters = reinterpret_cast<unsigned*>(ws + lbv::kAttendCounters);
     p.items = ws + lbv::kAttendItems;
     p.partial = reinterpret_cast<float*>(ws + lbv::kAttendPartial);
+    p.wait_limit = left_out < 0 ? lbv::kAttendWaitLimit : lbv::kAttendTestLimit;
+    p.left_out = left_out;
     // both kernels are right for every length
     const auto launch = lbv::attend_average_rows(p) <= 16 ? lbv::launch_attend_rows : lbv::launch_attend_tiles;
     const cudaError_t e = launch(p, cache->kmap, cache->vmap, cache->dtype, cache->sms,
@@ -419,6 +421,26 @@ lbv_status lbv_attend(const lbv_kv_cache* cache, const lbv_batch* batch, const l
     if (e != cudaSuccess)
         return cuda_fail(e, "lbv_attend: launch");
     return LBV_OK;
+}
+
+lbv_status lbv_attend(const lbv_kv_cache* cache, const lbv_batch* batch, const lbv_rows* q,
+                      const lbv_rows* out, float scale, int window, const uint64_t* tree,
+                      float* lse, void* workspace, size_t workspace_bytes, lbv_stream stream)
+{
+    return attend("lbv_attend", cache, batch, q, out, scale, window, tree, lse, workspace, workspace_bytes, -1,
+                  stream);
+}
+
+lbv_status lbv_attend_test_wait(const lbv_kv_cache* cache, const lbv_batch* batch, const lbv_rows* q,
+                                const lbv_rows* out, float scale, int window, const uint64_t* tree,
+                                float* lse, void* workspace, size_t workspace_bytes, int left_out,
+                                lbv_stream stream)
+{
+    const char* fn = "lbv_attend_test_wait";
+    if (left_out < 0)
+        return fail(LBV_ERR_INVALID_ARG, "%s: left_out=%d", fn, left_out);
+    return attend(fn, cache, batch, q, out, scale, window, tree, lse, workspace, workspace_bytes, left_out,
+                  stream);
 }
 
 lbv_status lbv_attend_status(void* workspace)

@@ -67,3 +67,12 @@ def test_batch_refuses_tables_whose_rows_overlap(requests, pages, stride):
 def test_batch_keeps_the_tables_stride(requests, pages, stride, want):
     b = batch(requests, pages, stride)
     assert (b.arg.table_stride, b.arg.table_pages, b.arg.requests) == (want, pages, requests)
+
+
+def test_attend_test_wait_refusals():
+    lbv.build()
+    call = lbv.lib().lbv_attend_test_wait
+    assert call(None, None, None, None, 1.0, 0, None, None, None, 0, -1, None) == lbv.ERR_INVALID_ARG
+    assert "left_out" in lbv.last_error()
+    assert call(None, None, None, None, 1.0, 0, None, None, None, 0, 0, None) == lbv.ERR_INVALID_ARG
+    assert "batch is NULL" in lbv.last_error()
