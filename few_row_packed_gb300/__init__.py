@@ -643,14 +643,14 @@ def attend_status(workspace):
     _check(lib().lbv_attend_status(_ptr(workspace)))
 
 
-def attend_test_wait(cache: KVCache, batch: Batch, q, out, scale: float, workspace, left_out: int,
+def attend_test_wait(cache: KVCache, batch: Batch, q, out, scale: float, workspace, copies: int,
                      window: int = 0, stream=None):
-    """Test export: attend with short waits, whose first CTA leaves out one copy
-    (lbv_attend_test_wait)."""
+    """Test export: attend with short waits, whose first CTA stops after `copies`
+    copies (lbv_attend_test_wait)."""
     n, d = batch.tokens, cache.head_dim
     _check(lib().lbv_attend_test_wait(cache.handle, batch.ref, _rows_arg(q, n, d, "q"),
                                       _rows_arg(out, n, d, "out"), scale, window, None, None, _ptr(workspace),
-                                      workspace.numel() * workspace.element_size(), left_out,
+                                      workspace.numel() * workspace.element_size(), copies,
                                       _stream(stream)))
 
 

@@ -28,7 +28,7 @@ struct AttendParams {
     float* partial;                  // slots of partial results
     void* items;                     // one JoinItem per CTA where they are joined apart, else NULL
     unsigned wait_limit;             // clocks until a wait gives up
-    int left_out;                    // test only: the copy that the first CTA leaves out, or -1
+    unsigned first_copies;           // test only: copies that the first CTA makes (~0u: all)
 };
 
 constexpr unsigned kAttendWaitLimit = 1u << 31;  // about a second

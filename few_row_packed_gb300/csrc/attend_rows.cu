@@ -153,13 +153,16 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, Geo<D>::CTAS)
             const int* table = p.batch.block_table + (int64_t)w.r * p.batch.table_stride;
             for (int b = w.b_first; b < w.b_last; ++b) {
                 const int st = n % G::NST, k0 = w.key0(b);
-                if (n >= G::NST)
-                    ok = mbar_wait(empty(st), (uint32_t)((n / G::NST - 1) & 1), p.wait_limit);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok)                                         // a reader is stuck: no more copies
+                // A stage is asked for again when it has been read, and its last copies have
+                // landed (readers that gave up free it all the same).
+                if (n >= G::NST) {
+                    const uint32_t parity = (uint32_t)((n / G::NST - 1) & 1);
+                    ok = mbar_wait(empty(st), parity, p.wait_limit) && mbar_wait(full(st), parity, p.wait_limit);
+                }
+                ok = __all_sync(0xffffffffu, ok && ((unsigned)n < p.first_copies || blockIdx.x > 0));
+                if (!ok)                                         // no more copies
                     break;
-                if (n++ == p.left_out && blockIdx.x == 0)
-                    continue;
+                ++n;
                 if (lane == 0)
                     mbar_expect_tx(full(st), G::STAGE);
                 __syncwarp();

@@ -365,13 +365,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int* table = p.batch.block_table + (int64_t)w.r * p.batch.table_stride;
                 for (int i = 0; i < 2 * w.nb; ++i) {
                     const int st = n % G::NSLOT, k0 = w.key0 + (i >> 1) * kKeys;
-                    if (n >= G::NSLOT)
+                    // read, and its last copy landed (see attend_rows.cu)
+                    if (n >= G::NSLOT) {
                         wait(empty(st), (uint32_t)((n / G::NSLOT - 1) & 1));
-                    ok = __all_sync(0xffffffffu, ok);
+                        wait(full(st), (uint32_t)((n / G::NSLOT - 1) & 1));
+                    }
+                    ok = __all_sync(0xffffffffu, ok && ((unsigned)n < p.first_copies || blockIdx.x > 0));
                     if (!ok)
                         break;
-                    if (n++ == p.left_out && blockIdx.x == 0)
-                        continue;
+                    ++n;
                     if (lane == 0)
                         mbar_expect_tx(full(st), G::SLOT);
                     __syncwarp();

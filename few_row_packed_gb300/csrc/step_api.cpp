@@ -351,10 +351,10 @@ size_t lbv_attend_workspace_bytes(const lbv_kv_cache* cache, const lbv_batch* ba
     return lbv::kAttendPartial + (rows > tiles ? rows : tiles) * sizeof(float);
 }
 
-// lbv_attend, by the name `fn`; left_out >= 0: the test of the bounded waits.
+// lbv_attend, by the name `fn`; copies >= 0: the test of the bounded waits.
 static lbv_status attend(const char* fn, const lbv_kv_cache* cache, const lbv_batch* batch, const lbv_rows* q,
                          const lbv_rows* out, float scale, int window, const uint64_t* tree, float* lse,
-                         void* workspace, size_t workspace_bytes, int left_out, lbv_stream stream)
+                         void* workspace, size_t workspace_bytes, int copies, lbv_stream stream)
 {
     lbv::set_error(LBV_OK, "");
     lbv_status st = check_batch(fn, batch);
@@ -412,8 +412,8 @@ static lbv_status attend(const char* fn, const lbv_kv_cache* cache, const lbv_ba
     p.counters = reinterpret_cast<unsigned*>(ws + lbv::kAttendCounters);
     p.items = ws + lbv::kAttendItems;
     p.partial = reinterpret_cast<float*>(ws + lbv::kAttendPartial);
-    p.wait_limit = left_out < 0 ? lbv::kAttendWaitLimit : lbv::kAttendTestLimit;
-    p.left_out = left_out;
+    p.wait_limit = copies < 0 ? lbv::kAttendWaitLimit : lbv::kAttendTestLimit;
+    p.first_copies = copies < 0 ? ~0u : (unsigned)copies;
     // both kernels are right for every length
     const auto launch = lbv::attend_average_rows(p) <= 16 ? lbv::launch_attend_rows : lbv::launch_attend_tiles;
     const cudaError_t e = launch(p, cache->kmap, cache->vmap, cache->dtype, cache->sms,
@@ -433,13 +433,13 @@ lbv_status lbv_attend(const lbv_kv_cache* cache, const lbv_batch* batch, const l
 
 lbv_status lbv_attend_test_wait(const lbv_kv_cache* cache, const lbv_batch* batch, const lbv_rows* q,
                                 const lbv_rows* out, float scale, int window, const uint64_t* tree,
-                                float* lse, void* workspace, size_t workspace_bytes, int left_out,
+                                float* lse, void* workspace, size_t workspace_bytes, int copies,
                                 lbv_stream stream)
 {
     const char* fn = "lbv_attend_test_wait";
-    if (left_out < 0)
-        return fail(LBV_ERR_INVALID_ARG, "%s: left_out=%d", fn, left_out);
-    return attend(fn, cache, batch, q, out, scale, window, tree, lse, workspace, workspace_bytes, left_out,
+    if (copies < 0)
+        return fail(LBV_ERR_INVALID_ARG, "%s: copies=%d", fn, copies);
+    return attend(fn, cache, batch, q, out, scale, window, tree, lse, workspace, workspace_bytes, copies,
                   stream);
 }
 

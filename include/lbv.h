@@ -591,16 +591,16 @@ LBV_API lbv_status lbv_attend_status(void* workspace);
 
 /*
  * Test export: lbv_attend whose waits give up after about half a millisecond
- * (in place of a second) and whose first CTA leaves out its copy number
- * left_out (>= 0; a block of keys and values in the few-row kernel, one of
- * either in the tensor-memory kernel), so that what waits for it gives up.  The
+ * (in place of a second) and whose first CTA stops copying after `copies` (>= 0)
+ * copies (a block of keys and values in the few-row kernel, one of either in
+ * the tensor-memory kernel), so that what waits for the next one gives up.  The
  * call ends, lbv_attend_status reports LBV_ERR_TIMEOUT, and what other CTAs
  * computed is right.
  */
 LBV_API lbv_status lbv_attend_test_wait(const lbv_kv_cache* cache, const lbv_batch* batch,
                                         const lbv_rows* q, const lbv_rows* out, float scale,
                                         int window, const uint64_t* tree, float* lse,
-                                        void* workspace, size_t workspace_bytes, int left_out,
+                                        void* workspace, size_t workspace_bytes, int copies,
                                         lbv_stream stream);
 
 /* How lbv_sample draws: dev arrays with one entry per row, each may be NULL. */

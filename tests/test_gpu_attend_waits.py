@@ -1,6 +1,6 @@
 """Bounded waits of the attention kernels that run out, on the GPU, without a
 fault: the test export shortens the waits to half a millisecond and has the first
-CTA leave out one of its copies.  What waits for it gives up, the kernel ends, the
+CTA stop copying.  What waits for the next copy gives up, the kernel ends, the
 workspace reports the timeout once, what other CTAs computed is right, and the
 next call with the same workspace is exact."""
 import time
@@ -21,13 +21,13 @@ def built():
     lbv.build()
 
 
-def run_out(c, left_out, safe):
+def run_out(c, copies, safe):
     """`safe`: the rows and heads that the first CTA has no part in."""
     want, lse = c.attend()
     out = torch.full_like(want, 7.0)
     torch.cuda.synchronize()
     t0 = time.perf_counter()
-    lbv.attend_test_wait(c.cache, c.batch, c.q, out, c.scale, c.workspace, left_out)
+    lbv.attend_test_wait(c.cache, c.batch, c.q, out, c.scale, c.workspace, copies)
     torch.cuda.synchronize()
     assert time.perf_counter() - t0 < 5.0
     with pytest.raises(lbv.LbvError) as e:
@@ -47,8 +47,8 @@ ROWS = {
 }
 
 
-@pytest.mark.parametrize("left_out", [0, 1, 5])
+@pytest.mark.parametrize("copies", [0, 1, 5])
 @pytest.mark.parametrize("name", list(ROWS))
-def test_few_row_kernel(name, left_out):
+def test_few_row_kernel(name, copies):
     args, safe = ROWS[name]
-    run_out(Case(*args), left_out, safe)
+    run_out(Case(*args), copies, safe)

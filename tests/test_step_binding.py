@@ -73,6 +73,6 @@ def test_attend_test_wait_refusals():
     lbv.build()
     call = lbv.lib().lbv_attend_test_wait
     assert call(None, None, None, None, 1.0, 0, None, None, None, 0, -1, None) == lbv.ERR_INVALID_ARG
-    assert "left_out" in lbv.last_error()
+    assert "copies" in lbv.last_error()
     assert call(None, None, None, None, 1.0, 0, None, None, None, 0, 0, None) == lbv.ERR_INVALID_ARG
     assert "batch is NULL" in lbv.last_error()
