@@ -71,7 +71,7 @@ struct Geo {
     static constexpr int RING = 2 * SLOT;
     static constexpr int NSLOT = D == 128 ? 5 : 10;
     static constexpr int BARS = RING + NSLOT * SLOT;
-    static constexpr int NBARS = 2 * NSLOT + 10 + 2 * kItems;
+    static constexpr int NBARS = 2 * NSLOT + 11 + 2 * kItems;
     static constexpr int STATS = (BARS + NBARS * 8 + 15) / 16 * 16;   // [2][128] m and sums of the streams
     static constexpr int RATIOS = STATS + 2 * kTile * 8;    // [2][128] exact over rounded sums
     static constexpr int ITEMS = RATIOS + 2 * kTile * 2;    // ring of items
@@ -302,6 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto item_full = [&](int i) { return bar(2 * G::NSLOT + 9 + i % kItems); };
     auto item_empty = [&](int i) { return bar(2 * G::NSLOT + 9 + kItems + i % kItems); };
     const uint32_t mmas_done = bar(2 * G::NSLOT + 9 + 2 * kItems);   // every MMA of the CTA
+    const uint32_t together = bar(2 * G::NSLOT + 10 + 2 * kItems);   // both streams have come as far
     const Item* items = reinterpret_cast<const Item*>(smem + G::ITEMS);
 
     if (tid == 0) {
@@ -311,6 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(q_full, 8);
         mbar_init(mmas_done, 1);
+        mbar_init(together, 8);
         for (int s = 0; s < 2; ++s) {
             mbar_init(s_full(s), 1);
             mbar_init(p_full(s, 0), 4);
@@ -337,13 +339,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 128)
         static_cast<JoinItem*>(p.items)[blockIdx.x].rows = 0;
 
+    // After a wait that ran out, `ok` false, a thread waits for nothing more, goes on to its
+    // item's end and leaves there with its warp.  Warps meet at bounded waits alone, so
+    // that those it leaves behind run out too.
     auto wait = [&](uint32_t b, uint32_t parity) {
         if (ok)
             ok = mbar_wait(b, parity, p.wait_limit);
     };
-    // item i of the share, as the scheduler wrote it
+    // item i of the share, as the scheduler wrote it, for a whole warp; valid if `ok`
     auto item_at = [&](int i) -> const Item& {
         wait(item_full(i), (uint32_t)((i / kItems) & 1));
+        ok = __all_sync(0xffffffffu, ok);
         return items[i % kItems];
     };
 
@@ -360,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int n = 0;                                               // slots asked for
             for (int it = 0;; ++it) {
                 const Item& w = item_at(it);
-                if (!__all_sync(0xffffffffu, ok) || w.nb == 0)
+                if (!ok || w.nb == 0)
                     break;
                 const int* table = p.batch.block_table + (int64_t)w.r * p.batch.table_stride;
                 for (int i = 0; i < 2 * w.nb; ++i) {
@@ -410,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Item& w = item_at(it);
                 const int nb = __shfl_sync(0xffffffffu, w.nb, 0);
                 const bool dual = __shfl_sync(0xffffffffu, w.rows, 0) > kTile;
-                if (!__all_sync(0xffffffffu, ok) || nb == 0)
+                if (!ok || nb == 0)
                     break;
                 wait(q_full, (uint32_t)(it & 1));
                 __syncwarp();
@@ -509,6 +515,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool more = w.next();
                     if (it >= kItems)
                         wait(item_empty(it), (uint32_t)((it / kItems - 1) & 1));
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok)                                 // its place is still read
+                        break;
                     if (lane == 0) {
                         const int nb = more ? w.b_last - w.b_first : 0;
                         out[it % kItems] = {w.q, w.r, w.x.row0, w.x.rows, w.head, w.x.lo, w.x.hi,
@@ -524,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         (int64_t)(w.head * p.group + row - tok * p.group) * p.q_head +
                                         i % (D / 64) * 64);
                         }
-                    if (!more || !__all_sync(0xffffffffu, ok))
+                    if (!more)
                         break;
                 }
             }
@@ -542,6 +551,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // scores are c times Q's: a negative scale negates Q, a zero one clears it
         const float c = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
         int done = 0;                    // blocks of this stream so far
+        int met = 0;                     // meetings of the two streams so far
+        auto meet = [&] {
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(together);
+            wait(together, (uint32_t)(met++ & 1));
+        };
         // Stores this thread's row of an item's Q.  The MMAs that read the Q tiles of
         // the item before are complete: their scores have been read.
         auto enter = [&](const Item& w) {
@@ -730,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
             // ---- the item's result, while the next item's first scores are computed ----
             if (!dual)                                   // both streams read tile 0, which stream 0 stores
-                named_bar_sync(1, 256);
+                meet();
             more = item_at(it + 1).nb > 0 && ok;
             if (fetched) {
                 asm volatile("cp.async.wait_all;\n" ::: "memory");
@@ -752,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sum > 0.f ? (int16_t)max(-32767, min(32767, __float2int_rn((exact / sum - 1.f) * 4194304.f)))
                               : (int16_t)0;
                 tc_fence_before();
-                named_bar_sync(1, 256);
+                meet();
                 const float2 a = stats[trow], b = stats[kTile + trow];
                 m = fmaxf(a.x, b.x);
                 f0 = a.x == -INFINITY ? 0.f : ex2(a.x - m);
@@ -816,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                          w.c1 - w.c0 + 1};
             tc_fence_before();
             if (!dual)                                   // both streams are done reading O and the statistics
-                named_bar_sync(1, 256);
+                meet();
             __syncwarp();                                // every lane has read the item
             if (lane == 0)
                 mbar_arrive(item_empty(it));

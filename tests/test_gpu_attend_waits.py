@@ -52,3 +52,21 @@ ROWS = {
 def test_few_row_kernel(name, copies):
     args, safe = ROWS[name]
     run_out(Case(*args), copies, safe)
+
+
+TILES = {
+    # items of one and of two row tiles in turn, several in each CTA
+    "many items": (([40, 150, 3, 129, 64] * 24, [400, 420, 90, 500, 64] * 24, 16, 8, 128, "bf16", 16),
+                   lambda t: t[772:]),
+    "small heads": (([150, 40] * 60, [1500, 1300] * 60, 8, 4, 64, "f16", 32), lambda t: t[570:]),
+    # one row tile over every CTA, and two
+    "one request": (([16], [30011], 48, 8, 128, "f16", 16), lambda t: t[:, 6:]),
+    "a chunk": (([200], [30000], 16, 8, 128, "bf16", 64), lambda t: t[:, 2:]),
+}
+
+
+@pytest.mark.parametrize("copies", [0, 1, 2, 3, 6, 9])
+@pytest.mark.parametrize("name", list(TILES))
+def test_tile_kernel(name, copies):
+    args, safe = TILES[name]
+    run_out(Case(*args), copies, safe)
