@@ -189,6 +189,11 @@ def _ptr(t):
     return t.data_ptr()
 
 
+def _device() -> int:
+    import torch
+    return torch._C._cuda_getDevice()
+
+
 def _stream(stream):
     if stream is None:
         import torch
@@ -478,13 +483,13 @@ def _dtype_id(dtype) -> int:
     return _dtype_ids[dtype]
 
 
-def _words(t, dtype, n: int, what: str):
-    """Address of a contiguous device tensor of at least n elements, or None."""
+def _words(t, dtype, n: int, what: str, device: int):
+    """Address of a contiguous tensor of at least n elements on `device`, or None."""
     if t is None:
         return None
-    if t.dtype != dtype or t.numel() < n or not t.is_contiguous() or not t.is_cuda:
+    if t.dtype != dtype or t.numel() < n or not t.is_contiguous() or t.get_device() != device:
         raise LbvError(ERR_INVALID_ARG, f"{what}: {t.dtype} {tuple(t.shape)} on {t.device}; a "
-                                        f"contiguous {dtype} device tensor of {n} is wanted")
+                                        f"contiguous {dtype} tensor of {n} on cuda:{device} is wanted")
     return t.data_ptr()
 
 
@@ -496,8 +501,9 @@ class KVCache:
     def __init__(self, k, v):
         if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
             raise LbvError(ERR_INVALID_ARG, "k and v have the same 4-d shape, strides and dtype")
-        if k.stride(3) != 1 or not (k.is_cuda and v.is_cuda):
-            raise LbvError(ERR_INVALID_ARG, "k and v are device tensors with a contiguous last "
+        self.device = k.get_device()
+        if k.stride(3) != 1 or self.device < 0 or v.get_device() != self.device:
+            raise LbvError(ERR_INVALID_ARG, "k and v are tensors of one device with a contiguous last "
                                             "dimension")
         h = ctypes.c_void_p()
         _check(lib().lbv_kv_cache_create(k.data_ptr(), v.data_ptr(), *k.shape, *k.stride()[:3],
@@ -522,14 +528,15 @@ class Batch:
     """The new tokens of one step (lbv_batch): q_start int32 [requests + 1],
     kv_len int32 [requests] (new tokens included), block_table int32
     [requests, table_pages] (rows may be apart, but do not overlap), all on the
-    device and kept alive here; `tokens` is the number of rows of the token-major
-    tensors."""
+    cache's device and kept alive here; `tokens` is the number of rows of the
+    token-major tensors."""
 
     def __init__(self, q_start, kv_len, block_table, tokens: int):
         import torch
         n = kv_len.numel()
+        self.device = block_table.get_device()
         if block_table.dim() != 2 or block_table.shape[0] != n or block_table.stride(1) != 1 \
-                or block_table.dtype != torch.int32 or not block_table.is_cuda:
+                or block_table.dtype != torch.int32 or self.device < 0:
             raise LbvError(ERR_INVALID_ARG, "block_table: an int32 device tensor [requests, pages] "
                                             "is wanted")
         stride, pages = block_table.stride(0), block_table.shape[1]
@@ -538,21 +545,29 @@ class Batch:
                 raise LbvError(ERR_INVALID_ARG, f"block_table: rows of {pages} pages overlap at a "
                                                 f"stride of {stride}")
             stride = pages                  # a single row's stride is of no use
-        self.arg = _BatchArg(_words(q_start, torch.int32, n + 1, "q_start"),
-                             _words(kv_len, torch.int32, n, "kv_len"), block_table.data_ptr(), n,
-                             int(tokens), stride, pages)
+        self.arg = _BatchArg(_words(q_start, torch.int32, n + 1, "q_start", self.device),
+                             _words(kv_len, torch.int32, n, "kv_len", self.device),
+                             block_table.data_ptr(), n, int(tokens), stride, pages)
         self.ref = ctypes.byref(self.arg)
         self.q_start, self.kv_len, self.block_table = q_start, kv_len, block_table
         self.requests, self.tokens = n, int(tokens)
 
 
-def _rows_arg(t, tokens: int, head_dim: int, what: str) -> bytes:
-    """lbv_rows of a [tokens, heads, head_dim] device tensor."""
+def _sizes(batch: Batch, cache: KVCache):
+    """Tokens, head_dim and device of a call."""
+    if batch.device != cache.device:
+        raise LbvError(ERR_INVALID_ARG, f"the batch is on cuda:{batch.device}, the cache on "
+                                        f"cuda:{cache.device}")
+    return batch.tokens, cache.head_dim, cache.device
+
+
+def _rows_arg(t, tokens: int, head_dim: int, what: str, device: int) -> bytes:
+    """lbv_rows of a [tokens, heads, head_dim] tensor on `device`."""
     shape, stride = t.shape, t.stride()
     if len(shape) != 3 or shape[0] < tokens or shape[2] != head_dim or stride[2] != 1 \
-            or not t.is_cuda:
-        raise LbvError(ERR_INVALID_ARG, f"{what}: {tuple(shape)} with strides {stride} on "
-                                        f"{t.device}; [{tokens}, heads, {head_dim}] is wanted")
+            or t.get_device() != device:
+        raise LbvError(ERR_INVALID_ARG, f"{what}: {tuple(shape)} with strides {stride} on {t.device}; "
+                                        f"[{tokens}, heads, {head_dim}] on cuda:{device} is wanted")
     dtype = t.dtype
     return _pack_rows(t.data_ptr(), shape[1], _dtype_ids.get(dtype) or _dtype_id(dtype), stride[0],
                       stride[1])
@@ -597,17 +612,27 @@ def rope_append(rope: Rope, batch: Batch, cache: KVCache, q, k, v, q_out, positi
     of one dtype (fp32, fp16, bf16), q_out of the cache's dtype; q and q_out may
     be None.  positions: int32 [tokens] rotary positions (default: the cache
     positions)."""
-    n, d = batch.tokens, cache.head_dim
-    q_arg = None if q is None else _rows_arg(q, n, d, "q")
-    o_arg = None if q_out is None else _rows_arg(q_out, n, d, "q_out")
+    n, d, device = _sizes(batch, cache)
+    q_arg = None if q is None else _rows_arg(q, n, d, "q", device)
+    o_arg = None if q_out is None else _rows_arg(q_out, n, d, "q_out", device)
     if positions is not None:
         import torch
-        positions = _words(positions, torch.int32, n, "positions")
+        positions = _words(positions, torch.int32, n, "positions", device)
     status = lib().lbv_rope_append(rope.handle, batch.ref, cache.handle, q_arg,
-                                   _rows_arg(k, n, d, "k"), _rows_arg(v, n, d, "v"),
+                                   _rows_arg(k, n, d, "k", device), _rows_arg(v, n, d, "v", device),
                                    o_arg, positions, _stream(stream))
     if status:
         _check(status)
+
+
+def _workspace_arg(t, device: int):
+    """Address and bytes of a workspace."""
+    if t is None:
+        return None, 0
+    if not t.is_contiguous() or t.get_device() != device:
+        raise LbvError(ERR_WORKSPACE, f"workspace: {tuple(t.shape)} on {t.device}; a contiguous tensor on "
+                                      f"cuda:{device} is wanted")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def attend_workspace_bytes(cache: KVCache, batch: Batch, heads: int) -> int:
@@ -624,15 +649,14 @@ def attend(cache: KVCache, batch: Batch, q, out, scale: float, window: int = 0, 
     words of the request's new tokens each one sees (default: causal); lse: fp32
     [tokens, heads]; workspace: attend_workspace_bytes, zeroed once.  See
     lbv_attend."""
-    n, d = batch.tokens, cache.head_dim
-    q_arg, o_arg = _rows_arg(q, n, d, "q"), _rows_arg(out, n, d, "out")
+    n, d, device = _sizes(batch, cache)
+    q_arg, o_arg = _rows_arg(q, n, d, "q", device), _rows_arg(out, n, d, "out", device)
     if tree is not None or lse is not None:
         import torch
-        tree = _words(tree, torch.int64, n, "tree")
-        lse = _words(lse, torch.float32, n * q.shape[1], "lse")
-    ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        tree = _words(tree, torch.int64, n, "tree", device)
+        lse = _words(lse, torch.float32, n * q.shape[1], "lse", device)
     status = lib().lbv_attend(cache.handle, batch.ref, q_arg, o_arg, scale, window, tree, lse,
-                              _ptr(workspace), ws, _stream(stream))
+                              *_workspace_arg(workspace, device), _stream(stream))
     if status:
         _check(status)
 
@@ -647,11 +671,10 @@ def attend_test_wait(cache: KVCache, batch: Batch, q, out, scale: float, workspa
                      window: int = 0, stream=None):
     """Test export: attend with short waits, whose first CTA stops after `copies`
     copies (lbv_attend_test_wait)."""
-    n, d = batch.tokens, cache.head_dim
-    _check(lib().lbv_attend_test_wait(cache.handle, batch.ref, _rows_arg(q, n, d, "q"),
-                                      _rows_arg(out, n, d, "out"), scale, window, None, None, _ptr(workspace),
-                                      workspace.numel() * workspace.element_size(), copies,
-                                      _stream(stream)))
+    n, d, device = _sizes(batch, cache)
+    _check(lib().lbv_attend_test_wait(cache.handle, batch.ref, _rows_arg(q, n, d, "q", device),
+                                      _rows_arg(out, n, d, "out", device), scale, window, None, None,
+                                      *_workspace_arg(workspace, device), copies, _stream(stream)))
 
 
 def sample(logits, u, token, prob=None, temperature=None, top_k=None, top_p=None, min_p=None,
@@ -662,21 +685,25 @@ def sample(logits, u, token, prob=None, temperature=None, top_k=None, top_p=None
     [M]; mask: int32 [M, ceil(N / 32)] bits of the allowed tokens; each may be
     None.  See lbv_sample."""
     import torch
-    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1) or not logits.is_cuda:
-        raise LbvError(ERR_INVALID_ARG, "logits: a device tensor [M, N] with contiguous rows is "
-                                        "wanted")
+    device = logits.get_device()
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1) or device != _device():
+        raise LbvError(ERR_INVALID_ARG, f"logits: {tuple(logits.shape)} on {logits.device}; a tensor [M, N] "
+                                        "with contiguous rows on the current device is wanted")
     m, n = logits.shape
     f32, i32 = torch.float32, torch.int32
     if mask is not None and (mask.dim() != 2 or mask.shape[0] < m or mask.shape[1] * 32 < n
-                             or mask.stride(1) != 1 or mask.dtype != i32 or not mask.is_cuda):
-        raise LbvError(ERR_INVALID_ARG, "mask: an int32 device tensor [M, ceil(N / 32)] is wanted")
-    rules = _RulesArg(_words(temperature, f32, m, "temperature"), _words(top_k, i32, m, "top_k"),
-                      _words(top_p, f32, m, "top_p"), _words(min_p, f32, m, "min_p"),
+                             or mask.stride(1) != 1 or mask.dtype != i32 or mask.get_device() != device):
+        raise LbvError(ERR_INVALID_ARG, "mask: an int32 tensor [M, ceil(N / 32)] on the logits' device is "
+                                        "wanted")
+    rules = _RulesArg(_words(temperature, f32, m, "temperature", device),
+                      _words(top_k, i32, m, "top_k", device), _words(top_p, f32, m, "top_p", device),
+                      _words(min_p, f32, m, "min_p", device),
                       None if mask is None else mask.data_ptr(),
                       0 if mask is None else mask.stride(0), int(temperature_last))
     status = lib().lbv_sample(logits.data_ptr(), m, n, logits.stride(0), _dtype_id(logits.dtype),
-                              _byref(rules), _words(u, f32, m, "u"), _words(token, i32, m, "token"),
-                              _words(prob, f32, m, "prob"), _stream(stream))
+                              _byref(rules), _words(u, f32, m, "u", device),
+                              _words(token, i32, m, "token", device), _words(prob, f32, m, "prob", device),
+                              _stream(stream))
     if status:
         _check(status)
 

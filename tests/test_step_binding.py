@@ -8,10 +8,9 @@ torch = pytest.importorskip("torch")
 
 
 class Fake:
-    """A device tensor as the binding looks at it."""
-    is_cuda = True
+    """A device tensor as the binding looks at it (device -1: host memory)."""
 
-    def __init__(self, shape, stride=None, dtype=torch.int32):
+    def __init__(self, shape, stride=None, dtype=torch.int32, device=0):
         self.shape, self.dtype = tuple(shape), dtype
         if stride is None:
             stride, n = [], 1
@@ -19,7 +18,13 @@ class Fake:
                 stride.insert(0, n)
                 n *= s
         self._stride = tuple(stride)
-        self.device = "cuda:0"
+        self.index, self.device, self.is_cuda = device, f"device {device}", device >= 0
+
+    def get_device(self):
+        return self.index
+
+    def element_size(self):
+        return {torch.float16: 2, torch.uint8: 1, torch.int64: 8}.get(self.dtype, 4)
 
     def dim(self):
         return len(self.shape)
@@ -76,3 +81,62 @@ def test_attend_test_wait_refusals():
     assert "copies" in lbv.last_error()
     assert call(None, None, None, None, 1.0, 0, None, None, None, 0, 0, None) == lbv.ERR_INVALID_ARG
     assert "batch is NULL" in lbv.last_error()
+
+
+@pytest.fixture()
+def setup(monkeypatch):
+    lbv.build()
+    monkeypatch.setattr(lbv, "_device", lambda: 0)
+    shape, half = [4, 16, 2, 64], torch.float16
+    cache = lbv.KVCache(Fake(shape, dtype=half), Fake(shape, dtype=half))
+    return cache, batch(1, 4, (4, 1))
+
+
+def refused(call, status=lbv.ERR_INVALID_ARG):
+    """A refusal of the binding's own: the library, which has no device here, was not reached."""
+    with pytest.raises(lbv.LbvError) as e:
+        call()
+    assert e.value.status == status
+    assert "lbv_" not in str(e.value)
+
+
+@pytest.mark.parametrize("device", [1, -1])
+def test_tensors_on_another_device_are_refused(setup, device):
+    cache, b = setup
+    half, f32, i32 = torch.float16, torch.float32, torch.int32
+    shape = [4, 16, 2, 64]
+    refused(lambda: lbv.KVCache(Fake(shape, dtype=half, device=device), Fake(shape, dtype=half)))
+    refused(lambda: lbv.KVCache(Fake(shape, dtype=half), Fake(shape, dtype=half, device=device)))
+    for which in range(3):
+        at = [device if i == which else 0 for i in range(3)]
+        refused(lambda: lbv.Batch(Fake([2], device=at[0]), Fake([1], device=at[1]), Fake([1, 4], device=at[2]), 1))
+    rope = lbv.Rope(lbv.rope_frequencies(64))
+    if device > 0:
+        other = lbv.Batch(*(Fake(s, device=device) for s in ([2], [1], [1, 4])), 1)
+        row = Fake([1, 2, 64], dtype=half)
+        refused(lambda: lbv.rope_append(rope, other, cache, None, row, row, None))
+        refused(lambda: lbv.attend(cache, other, row, row, 1.0))
+    for which in range(5):
+        at = [device if i == which else 0 for i in range(5)]
+        q, k, v, out = (Fake([1, 2, 64], dtype=half, device=i) for i in at[:4])
+        refused(lambda: lbv.rope_append(rope, b, cache, q, k, v, out, positions=Fake([1], device=at[4])))
+    for which in range(5):
+        at = [device if i == which else 0 for i in range(5)]
+        q, out = (Fake([1, 2, 64], dtype=half, device=i) for i in at[:2])
+        refused(lambda: lbv.attend(cache, b, q, out, 1.0, tree=Fake([1], dtype=torch.int64, device=at[2]),
+                                   lse=Fake([1, 2], dtype=f32, device=at[3]),
+                                   workspace=Fake([1 << 26], dtype=torch.uint8, device=at[4])),
+                lbv.ERR_WORKSPACE if which == 4 else lbv.ERR_INVALID_ARG)
+    for which in range(9):
+        at = [device if i == which else 0 for i in range(9)]
+        f = [Fake([3], dtype=f32, device=i) for i in at[:5]]
+        w = [Fake([3], dtype=i32, device=i) for i in at[5:7]]
+        refused(lambda: lbv.sample(Fake([3, 50], dtype=f32, device=at[7]), f[0], w[0], prob=f[1], temperature=f[2],
+                                   top_k=w[1], top_p=f[3], min_p=f[4], mask=Fake([3, 2], device=at[8])))
+
+
+def test_workspace_that_repeats_its_bytes_is_refused(setup):
+    cache, b = setup
+    q = Fake([1, 2, 64], dtype=torch.float16)
+    refused(lambda: lbv.attend(cache, b, q, q, 1.0, workspace=Fake([1 << 26], (0,), torch.uint8)),
+            lbv.ERR_WORKSPACE)
