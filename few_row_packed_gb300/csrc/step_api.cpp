@@ -167,6 +167,11 @@ lbv_status lbv_kv_cache_create(void* k, void* v, int pages, int page_size, int h
         if (ext[i] > 1 && st[i] < inner)
             return fail(LBV_ERR_INVALID_ARG, "%s: strides (%lld, %lld, %lld) overlap", fn,
                         (long long)page_stride, (long long)token_stride, (long long)head_stride);
+        // (an extent of 2^62 elements and more is no device's, and would pass 64 bits)
+        if (ext[i] > 1 && st[i] > (((int64_t)1 << 62) - inner) / (ext[i] - 1))
+            return fail(LBV_ERR_INVALID_ARG, "%s: strides (%lld, %lld, %lld) of %d pages, %d slots, %d heads", fn,
+                        (long long)page_stride, (long long)token_stride, (long long)head_stride, pages,
+                        page_size, heads);
         inner = st[i] * (ext[i] - 1) + inner;
     }
     lbv_kv_cache* c = new (std::nothrow) lbv_kv_cache();

@@ -1,5 +1,7 @@
 """CPU tests of what the Python binding refuses before anything reaches the
 device: tensors are stood in for by objects with a tensor's attributes."""
+import ctypes
+
 import pytest
 
 import few_row_packed_gb300 as lbv
@@ -140,3 +142,15 @@ def test_workspace_that_repeats_its_bytes_is_refused(setup):
     q = Fake([1, 2, 64], dtype=torch.float16)
     refused(lambda: lbv.attend(cache, b, q, q, 1.0, workspace=Fake([1 << 26], (0,), torch.uint8)),
             lbv.ERR_WORKSPACE)
+
+
+@pytest.mark.parametrize("pages, strides", [
+    # 2^31 pages of 2^34 elements: their extent wraps 64 bits, and tokens and pages overlap
+    (2 ** 31 - 1, (2 ** 34, 2 ** 37, 128)),
+    (2 ** 31 - 1, (2 ** 37, 256, 128)),
+])
+def test_cache_whose_extent_passes_64_bits_is_refused(pages, strides):
+    lbv.build()
+    h = ctypes.c_void_p()
+    st = lbv.lib().lbv_kv_cache_create(4096, 8192, pages, 16, 2, 128, *strides, lbv.F16, ctypes.byref(h))
+    assert st == lbv.ERR_INVALID_ARG and not h.value
