@@ -505,6 +505,9 @@ class KVCache:
         if k.stride(3) != 1 or self.device < 0 or v.get_device() != self.device:
             raise LbvError(ERR_INVALID_ARG, "k and v are tensors of one device with a contiguous last "
                                             "dimension")
+        if self.device != _device():        # the handle is made for the current device
+            raise LbvError(ERR_INVALID_ARG, f"k and v are on cuda:{self.device}, which is not the current "
+                                            "device")
         h = ctypes.c_void_p()
         _check(lib().lbv_kv_cache_create(k.data_ptr(), v.data_ptr(), *k.shape, *k.stride()[:3],
                                          _dtype_id(k.dtype), ctypes.byref(h)))

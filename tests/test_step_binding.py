@@ -102,6 +102,17 @@ def refused(call, status=lbv.ERR_INVALID_ARG):
     assert "lbv_" not in str(e.value)
 
 
+def test_cache_on_another_than_the_current_device_is_refused(monkeypatch):
+    """Its handle, with the size and maps of the current device, would otherwise launch there."""
+    lbv.build()
+    shape, half = [4, 16, 2, 64], torch.float16
+    k, v = (Fake(shape, dtype=half, device=1) for _ in range(2))
+    monkeypatch.setattr(lbv, "_device", lambda: 0)
+    refused(lambda: lbv.KVCache(k, v))
+    monkeypatch.setattr(lbv, "_device", lambda: 1)
+    assert lbv.KVCache(k, v).device == 1
+
+
 @pytest.mark.parametrize("device", [1, -1])
 def test_tensors_on_another_device_are_refused(setup, device):
     cache, b = setup
