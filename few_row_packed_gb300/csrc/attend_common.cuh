@@ -481,7 +481,7 @@ __device__ __forceinline__ void join_parts(const AttendParams& p, const Request&
     auto part = [&](int k) {
         return p.partial + (size_t)(2 * (c0 + k) + (k == 0)) * (ROWS * (D + 3));
     };
-    const int step = min(rows, cap / (2 * parts + 3));   // rows at a time (parts: at most 512)
+    const int step = min(rows, cap / (2 * parts + 3));   // rows at a time (at most kAttendMaxCtas parts)
     for (int r0 = 0; r0 < rows; r0 += step) {
         const int n = min(step, rows - r0);
         float* f = scratch;                              // [parts][n] maxima, then factors

@@ -31,7 +31,7 @@
 //     rows).  Larger tiles go to the tensor-memory kernel (attend_tiles.cu).
 //
 // 64 requests of one token over 500 to 16,384 keys, 48 query over 8 key/value heads of
-// 128: 216 us with the join, 6.5 TB/s, 96 % of what a copy reaches.  One request over
+// 128: 216 to 220 us with the join, 6.4 to 6.5 TB/s, 94 to 96 % of what a copy reaches.  One request over
 // 2,011 keys: 9.5 us, of round trips to memory.  32 requests of 1 to 8 tokens, 32 query
 // over 8 heads of 64, window 4096: 50 us, 61 %; a third of them has two row tiles, which
 // read their keys twice (60 us by the tensor-memory kernel).

@@ -21,9 +21,9 @@
 //
 // What bounds it (48 query over 8 key/value heads of 128, bf16): in long items the
 // hand-over of S and P, with the tensor cores 70 % busy: 2048 tokens at the end of 16,384
-// take 513 us, 1,507 TFLOP/s.  In short ones their ends, during which the tensor cores
-// wait: code that runs once an item is fetched anew and takes some 25 clocks an
-// instruction, where the block's loop takes 9; 16 requests of 1 to 600 tokens take 137 us,
+// take 510 to 525 us, 1,470 to 1,520 TFLOP/s.  In short ones their ends, during which the
+// tensor cores wait: code that runs once an item is fetched anew and takes some 25 clocks an
+// instruction, where the block's loop takes 9; 16 requests of 1 to 600 tokens take 139 us,
 // their operations at the same rate 84.  With few blocks the start: 5 us to the first
 // scores and 5 more to fetch the block's code, some 20 KB; 8 tokens after 32,771 take
 // 36 us, their keys and values 20.
@@ -40,7 +40,7 @@ constexpr int kTile = 128;                       // rows per stream
 constexpr int kRows = 2 * kTile;                 // rows per item
 // Units of an item: its queries and results, a block of one row tile, a block of two;
 // and the least share of a CTA.  A unit is 0.2 us of a long item.  (16 requests of 1 to
-// 600 tokens, us: 16/3/4 139, these 137, 28/3/4 139, 24/4/4 139, 36/4/5 139; a prompt's
+// 600 tokens, us: 16/3/4 141, these 139, 28/3/4 141, 24/4/4 143, 36/4/5 142; a prompt's
 // chunk is the same within 1 %.  The least share: 40 small batches take 4 % less with 8 or
 // 12 than with 24, 12 % less than with 48; 20 tokens over 3,943 keys 15.6 and 20.3 us.)
 constexpr int kExtra = 24, kNarrow = 3, kWide = 4, kMinUnits = 12;
@@ -341,7 +341,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // After a wait that ran out, `ok` false, a thread waits for nothing more, goes on to its
     // item's end and leaves there with its warp.  Warps meet at bounded waits alone, so
-    // that those it leaves behind run out too.
+    // that those it leaves behind run out too.  (The streams at a hardware barrier in place
+    // of `together`: 137 us for the 139 above, and no end if one of them left.)
     auto wait = [&](uint32_t b, uint32_t parity) {
         if (ok)
             ok = mbar_wait(b, parity, p.wait_limit);

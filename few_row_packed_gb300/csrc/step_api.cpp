@@ -494,7 +494,8 @@ lbv_status lbv_sample(const void* logits, int M, int N, int64_t ld, lbv_dtype dt
                     (long long)rules->mask_ld, (N + 31) / 32);
     if (N > 1 << 23)        // sums of weights up to 2^40 stay below 2^64
         return fail(LBV_ERR_UNSUPPORTED, "%s: N=%d exceeds %d logits a row", fn, N, 1 << 23);
-    // Up to 8 rows take 16 CTAs each (one row of 151936: 14.7 us, 17.0 with 8); of more,
+    // Up to 8 rows take 16 CTAs each (one row of 151936, top-k and top-p: 14.0 us, 17.0
+    // with 8; 8 rows, top-p and min-p: 32.4 and 35.5); of more,
     // 8 CTAs each keep four on every SM.  Short rows take fewer, so that a thread still
     // has a few logits.
     int ctas = M <= 8 ? 16 : 8;

@@ -462,11 +462,12 @@ LBV_API lbv_status lbv_rows_histogram(uint64_t* counts);
  * cache position kv_len[r] - n_r + i.  Position p of request r lives in slot
  * p % page_size of page block_table[r][p / page_size].  All arrays are dev
  * int32, read by the kernels when they run.  Rows at or past
- * q_start[requests] belong to no request: they are neither read nor written. */
+ * q_start[requests] belong to no request: nothing is written for them, and what
+ * they hold does not matter (the append may load it). */
 typedef struct lbv_batch {
     const int32_t* q_start;      /* [requests + 1], ascending, q_start[0] >= 0    */
     const int32_t* kv_len;       /* [requests]                                    */
-    const int32_t* block_table;  /* [requests][table_stride]                      */
+    const int32_t* block_table;  /* [requests][table_stride], rows do not overlap */
     int requests;                /* 1..4096                                       */
     int tokens;                  /* rows of the token-major tensors, >= 0         */
     int table_stride;            /* >= table_pages                                */
@@ -508,7 +509,11 @@ typedef enum {
     LBV_ROPE_BY_PARTS = 2      /* f_j * ((1 - g) / factor + g), g = clamp((r - low) /
                                   (high - low), 0, 1) with r = trained * f_j / 2 pi the
                                   turns of pair j in the trained length (Peng et al.
-                                  2023, "YaRN", section 3.2)                        */
+                                  2023, "YaRN", section 3.2).  Engines also ramp over
+                                  the pair's index j between two bounds (rounded to
+                                  whole pairs or not); a checkpoint that runs with those
+                                  frequencies needs them given to lbv_rope_create as
+                                  they are.                                         */
 } lbv_rope_scaling;
 
 /* Host helper: radians per position of the rot_dim/2 pairs.  rot_dim even,
@@ -551,7 +556,9 @@ LBV_API lbv_status lbv_rope_append(const lbv_rope* rope, const lbv_batch* batch,
                                    const int32_t* positions, lbv_stream stream);
 
 /* Bytes of the workspace lbv_attend needs for this cache, a batch (its counts
- * alone are read) and so many query heads; 0 for NULL. */
+ * alone are read) and so many query heads; 0 for NULL.  They hold the parts of
+ * the larger kernel for every SM (41 MB for heads of 128, 21 MB for 64, on 152
+ * SMs), so one workspace serves batches of every size over caches of its head_dim. */
 LBV_API size_t lbv_attend_workspace_bytes(const lbv_kv_cache* cache, const lbv_batch* batch,
                                           int heads);
 
@@ -570,7 +577,13 @@ LBV_API size_t lbv_attend_workspace_bytes(const lbv_kv_cache* cache, const lbv_b
  * exp(scale q . k_j).  A row that sees nothing gets out 0 and lse -inf.
  *   q, out: rows of the cache's dtype; q->heads a multiple of the cache's
  * heads.  Sums and softmax are fp32, the probabilities enter the second
- * product in the cache's dtype, out is rounded once.  Cache slots at or past
+ * product in the cache's dtype, out is rounded once.  What the product is divided
+ * by adds the rounded probabilities in the few-row kernel (up to 16 rows, new
+ * tokens times query heads of a group, a request on average); in the
+ * tensor-memory kernel (more rows) those of blocks where one key is half of a row's
+ * sum so far, and the unrounded ones of the others.  So the same request may
+ * differ by the rounding of the probabilities between batches of either kind.
+ * lse adds the unrounded ones in both.  Cache slots at or past
  * kv_len may hold anything; keys and values below it are taken to be finite.
  * Contexts are shorter than 2^30.  A mapped page outside the cache reads as zeros.
  *   workspace: dev, 256-byte aligned, lbv_attend_workspace_bytes(); zeroed once
@@ -673,7 +686,8 @@ LBV_API const char* lbv_version(void);
  * partial slots against their buffer.  A failed test sets the status word's
  * bounds bit (LBV_ERR_BOUNDS from lbv_plan_device_status) and skips the access;
  * the kernel still ends, and its output is then wrong.  It stands in for a
- * memory checker where none can run.
+ * memory checker where none can run.  The kernels around the matmul (append,
+ * attention, sampling) have no such tests: they are the same in both builds.
  */
 LBV_API int lbv_checked_build(void);
 
