@@ -21,7 +21,7 @@
 //
 // What bounds it (48 query over 8 key/value heads of 128, bf16): in long items the
 // hand-over of S and P, with the tensor cores 70 % busy: 2048 tokens at the end of 16,384
-// take 510 to 525 us, 1,470 to 1,520 TFLOP/s.  In short ones their ends, during which the
+// take 510 to 530 us, 1,460 to 1,520 TFLOP/s.  In short ones their ends, during which the
 // tensor cores wait: code that runs once an item is fetched anew and takes some 25 clocks an
 // instruction, where the block's loop takes 9; 16 requests of 1 to 600 tokens take 139 us,
 // their operations at the same rate 84.  With few blocks the start: 5 us to the first
