@@ -201,9 +201,10 @@ def work(case):
 # --- a cache in 4 bits ---------------------------------------------------------------
 #
 # Bytes [pages][heads][chunks of C = min(page, 64) slots][K codes, V codes, scales]: codes are
-# [dim / 64][C][32] bytes, element 2 b in the low half of byte b; scales [K, V][dim / 64][C]
-# are pairs (scale, bias) of the cache's 16-bit type.  An element is code * scale + bias,
-# rounded to that type.
+# [dim / 64][C][32] bytes, in each 32-bit word the even ones of 8 elements in the low half and
+# the odd ones in the high half, from the lowest bits on; scales [K, V][dim / 64][C] are pairs
+# (scale, bias) of the cache's 16-bit type.  An element is code * scale + bias, rounded to
+# that type.
 
 def _page_bytes(c):
     return c["page"] * c["kv_heads"] * (c["dim"] // GROUP) * 72
@@ -226,7 +227,8 @@ def _places4(c, slot):
 
 def _values4(codes, scales, wide):
     """Elements (one more dimension in place of the bytes) in `wide`."""
-    code = torch.stack((codes & 15, codes >> 4), -1).flatten(-2)
+    code = torch.stack((codes & 15, codes >> 4), -1).unflatten(-2, (8, 2, 2))      # word, odd, byte, half
+    code = code.movedim(-3, -1).flatten(-4)
     x = code.to(wide) * scales[..., 0, None].to(wide) + scales[..., 1, None].to(wide)
     return x.to(scales.dtype).to(wide)
 
@@ -389,7 +391,8 @@ def _quantised(x, dt):
     step = scale.float()[..., None]
     code = (x - bias.float()[..., None]) * torch.where(step > 0, 1 / step, 0)
     code = code.round().clamp(0, 15).to(torch.uint8)
-    return code[..., 0::2] | code[..., 1::2] << 4, torch.stack((scale, bias), -1)
+    code = code.unflatten(-1, (8, 2, 2, 2)).movedim(-1, -3)                         # word, odd, byte, half
+    return (code[..., 0] | code[..., 1] << 4).flatten(-3), torch.stack((scale, bias), -1)
 
 
 def _plain_append(s):
@@ -579,12 +582,13 @@ def _exact_rows(s, r, kv):
         cols = []
         for part in range(parts):
             p = which * parts + part
-            byte = raw[:, :, p * plane:(p + 1) * plane].reshape(-1, c["kv_heads"], size, 32).double()
+            word = raw[:, :, p * plane:(p + 1) * plane].contiguous().view(torch.int32)
+            word = word.reshape(-1, c["kv_heads"], size, 8, 1).long() & 0xFFFFFFFF
             at = 2 * parts * plane + 4 * size * p
             pair = raw[:, :, at:at + 4 * size].contiguous().view(DTYPES[c["dtype"]])
             pair = pair.reshape(-1, c["kv_heads"], size, 2).double()
-            high = (byte / 16).floor()
-            both = torch.stack((byte - 16 * high, high), -1).reshape(-1, c["kv_heads"], size, GROUP)
+            bits = torch.tensor([4 * (i // 2) + 16 * (i % 2) for i in range(8)], device="cuda")
+            both = (word >> bits & 15).reshape(-1, c["kv_heads"], size, GROUP).double()
             cols.append((both * pair[..., :1] + pair[..., 1:]).to(DTYPES[c["dtype"]]).double())
         x = torch.cat(cols, -1).transpose(1, 2)
         out.append(x.reshape(-1, c["kv_heads"], c["dim"])[:kv])
