@@ -148,12 +148,18 @@ def lib():
             "lbv_dequant_fp16": (st, [P, P, P, P]),
             "lbv_kv_cache_create": (st, [P, P, I, I, I, I, L64, L64, L64, I, ctypes.POINTER(P)]),
             "lbv_kv_cache_destroy": (st, [P]),
+            "lbv_kv_cache4_page_bytes": (S, [I, I, I]),
+            "lbv_kv_cache4_create": (st, [P, I, I, I, I, I, ctypes.POINTER(P)]),
+            "lbv_kv_read": (st, [P, P, P, P, P]),
+            "lbv_kv_keep": (st, [P, P, P, P, P]),
+            "lbv_kv_copy_pages": (st, [P, P, P, I, P]),
             "lbv_rope_frequencies": (st, [I, D, I, D, D, D, D, P]),
             "lbv_rope_create": (st, [P, I, I, F, ctypes.POINTER(P)]),
             "lbv_rope_destroy": (st, [P]),
             "lbv_rope_append": (st, [P] * 9),
             "lbv_attend_workspace_bytes": (S, [P, P, I]),
             "lbv_attend": (st, [P, P, P, P, F, I, P, P, P, S, P]),
+            "lbv_attend_sinks": (st, [P, P, P, P, F, I, I, P, P, P, S, P]),
             "lbv_attend_status": (st, [P]),
             "lbv_attend_test_wait": (st, [P, P, P, P, F, I, P, P, P, S, I, P]),
             "lbv_sample": (st, [P, I, I, L64, I, P, P, P, P, P]),
@@ -527,6 +533,39 @@ class KVCache:
             pass
 
 
+def kv_cache4_page_bytes(page_size: int, heads: int, head_dim: int) -> int:
+    """Bytes of a page of a cache held in 4 bits."""
+    n = int(lib().lbv_kv_cache4_page_bytes(page_size, heads, head_dim))
+    if n == 0:
+        raise LbvError(ERR_UNSUPPORTED, f"page_size {page_size} (a power of two, 8..1024), {heads} heads of "
+                                        f"{head_dim} (64 or 128)")
+    return n
+
+
+class KVCache4(KVCache):
+    """A caller's paged cache held in 4 bits, a scale and a bias for each 64 elements
+    of a head (lbv_kv_cache4_create): data is a contiguous uint8 device tensor
+    [pages, kv_cache4_page_bytes(page_size, heads, head_dim)], kept alive here; dtype
+    (fp16 or bf16) is the type of its values.  Stands wherever a KVCache does."""
+
+    def __init__(self, data, page_size: int, heads: int, head_dim: int, dtype):
+        import torch
+        n = kv_cache4_page_bytes(page_size, heads, head_dim)
+        self.device = data.get_device()
+        if data.dim() != 2 or data.shape[1] != n or data.dtype != torch.uint8 or not data.is_contiguous() \
+                or self.device < 0:
+            raise LbvError(ERR_INVALID_ARG, f"data: {data.dtype} {tuple(data.shape)} on {data.device}; a contiguous "
+                                            f"uint8 device tensor [pages, {n}] is wanted")
+        if self.device != _device():        # the handle is made for the current device
+            raise LbvError(ERR_INVALID_ARG, f"data is on cuda:{self.device}, which is not the current device")
+        h = ctypes.c_void_p()
+        _check(lib().lbv_kv_cache4_create(data.data_ptr(), data.shape[0], page_size, heads, head_dim,
+                                          _dtype_id(dtype), ctypes.byref(h)))
+        self.handle = h
+        self.data, self.dtype = data, dtype
+        self.pages, self.page_size, self.heads, self.head_dim = data.shape[0], page_size, heads, head_dim
+
+
 class Batch:
     """The new tokens of one step (lbv_batch): q_start int32 [requests + 1],
     kv_len int32 [requests] (new tokens included), block_table int32
@@ -628,6 +667,47 @@ def rope_append(rope: Rope, batch: Batch, cache: KVCache, q, k, v, q_out, positi
         _check(status)
 
 
+def kv_read(batch: Batch, cache: KVCache, k, v, stream=None):
+    """The keys and values of the batch's new tokens as the cache holds them, into k
+    and v: [tokens, heads, head_dim] of the cache's dtype; one of them may be None.
+    See lbv_kv_read."""
+    n, d, device = _sizes(batch, cache)
+    status = lib().lbv_kv_read(batch.ref, cache.handle,
+                               None if k is None else _rows_arg(k, n, d, "k", device),
+                               None if v is None else _rows_arg(v, n, d, "v", device), _stream(stream))
+    if status:
+        _check(status)
+
+
+def kv_keep(batch: Batch, cache: KVCache, kept, left=None, stream=None):
+    """Keeps the new tokens of each request whose bits are set in kept (int64
+    [requests]) and closes them up behind their context; left (int32 [requests],
+    apart from the batch's tensors, optional) = the contexts' new lengths.  See
+    lbv_kv_keep."""
+    import torch
+    device = _sizes(batch, cache)[2]
+    if kept is None:
+        raise LbvError(ERR_INVALID_ARG, "kept: an int64 tensor [requests] is wanted")
+    status = lib().lbv_kv_keep(batch.ref, cache.handle,
+                               _words(kept, torch.int64, batch.requests, "kept", device),
+                               _words(left, torch.int32, batch.requests, "left", device), _stream(stream))
+    if status:
+        _check(status)
+
+
+def kv_copy_pages(cache: KVCache, src, dst, stream=None):
+    """Copies page src[i] of the cache to page dst[i] (int32 tensors of one length on
+    its device).  See lbv_kv_copy_pages."""
+    import torch
+    if src is None or dst is None or src.numel() != dst.numel():
+        raise LbvError(ERR_INVALID_ARG, "src and dst: two int32 tensors of one length are wanted")
+    n = src.numel()
+    status = lib().lbv_kv_copy_pages(cache.handle, _words(src, torch.int32, n, "src", cache.device),
+                                     _words(dst, torch.int32, n, "dst", cache.device), n, _stream(stream))
+    if status:
+        _check(status)
+
+
 def _workspace_arg(t, device: int):
     """Address and bytes of a workspace."""
     if t is None:
@@ -645,21 +725,22 @@ def attend_workspace_bytes(cache: KVCache, batch: Batch, heads: int) -> int:
 
 
 def attend(cache: KVCache, batch: Batch, q, out, scale: float, window: int = 0, tree=None,
-           lse=None, workspace=None, stream=None):
+           lse=None, workspace=None, stream=None, sinks: int = 0):
     """out[t, h] = attention of new token t's query head h over its request's
     context in the cache; q, out: [tokens, heads, head_dim] of the cache's
     dtype.  window > 0: only the last `window` positions; tree: int64 [tokens]
     words of the request's new tokens each one sees (default: causal); lse: fp32
-    [tokens, heads]; workspace: attend_workspace_bytes, zeroed once.  See
-    lbv_attend."""
+    [tokens, heads]; workspace: attend_workspace_bytes, zeroed once; sinks: first
+    positions of a context that stay visible behind the window.  See lbv_attend and
+    lbv_attend_sinks."""
     n, d, device = _sizes(batch, cache)
     q_arg, o_arg = _rows_arg(q, n, d, "q", device), _rows_arg(out, n, d, "out", device)
     if tree is not None or lse is not None:
         import torch
         tree = _words(tree, torch.int64, n, "tree", device)
         lse = _words(lse, torch.float32, n * q.shape[1], "lse", device)
-    status = lib().lbv_attend(cache.handle, batch.ref, q_arg, o_arg, scale, window, tree, lse,
-                              *_workspace_arg(workspace, device), _stream(stream))
+    status = lib().lbv_attend_sinks(cache.handle, batch.ref, q_arg, o_arg, scale, window, sinks, tree, lse,
+                                    *_workspace_arg(workspace, device), _stream(stream))
     if status:
         _check(status)
 

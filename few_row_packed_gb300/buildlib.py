@@ -38,9 +38,12 @@ SOURCES = [
     "verify_q4_0.cu",
     "fused_aux.cu",
     "rope_append.cu",
+    "append4.cu",
+    "cache_ops.cu",
     "sample.cu",
     "attend_rows.cu",
     "attend_tiles.cu",
+    "attend4_tiles.cu",
     "attend_join.cu",
     "tc_aux.cu",
     "tc_sign1.cu",

@@ -1,0 +1,204 @@
+// append4.cu -- rotary positions of the new tokens, and the append to a cache of 4 bits.
+//
+// The rotation is that of rope_append.cu; a group x of 64 rotated elements is then held
+// as codes of 4 bits between its bounds:
+//     bias = round16(min x), scale = round16((max x - min x) / 15),
+//     code = round((x - bias) * (1 / scale)) in 0..15.
+// A thread has 8 neighbours of a head, so a group is 8 lanes, whose minimum and maximum
+// meet in three exchanges, and whose codes are 32 neighbouring bytes.  With halves
+// that pair up, a thread loads its elements' partners too: they are another thread's own, so
+// they come from L1, and any rotated part of a head is treated alike.
+//
+// Bound by memory: every element is read once, queries leave as 16 bits, keys and
+// values as 4.5.
+#include "kv4.cuh"
+#include "rope_rows.cuh"
+
+namespace lbv {
+
+using namespace rope;
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kAhead = 4;             // pieces of 8 elements a thread keeps in flight
+
+// Where a piece comes from and goes to.
+struct Piece {
+    int which;             // 0 q, 1 k, 2 v
+    int head, at;          // its first element in the head
+};
+
+__device__ __forceinline__ Piece piece_of(const RopeParams& p, int it, int per_head_shift)
+{
+    Piece m;
+    const int row = it >> per_head_shift;
+    m.which = row < p.q_heads ? 0 : row < p.q_heads + p.kv.heads ? 1 : 2;
+    m.head = m.which == 0 ? row : m.which == 1 ? row - p.q_heads : row - p.q_heads - p.kv.heads;
+    m.at = (it - (row << per_head_shift)) * 8;
+    return m;
+}
+
+// Offset of the partners of the four elements from `at` on.
+__device__ __forceinline__ int partner(int at, int rot)
+{
+    const int half = rot >> 1;        // a multiple of 4
+    return at < half ? at + half : at - half;
+}
+
+template <int SRC, int DST, bool HALF, bool VEC>
+__global__ void __launch_bounds__(kThreads) lbv_rope_append4_kernel(const __grid_constant__ RopeParams p)
+{
+    __shared__ float2 turn[kMaxRot / 2];
+    __shared__ int where[2];                       // request (-1: none), cache position
+    const int tok = blockIdx.x, lane = threadIdx.x & 31;
+    const int per_head_shift = p.kv.dim == 128 ? 4 : 3;
+    const int total = (p.q_heads + 2 * p.kv.heads) << per_head_shift;
+    const int step = kThreads * gridDim.y;
+    const int first = blockIdx.y * kThreads + threadIdx.x;
+
+    after_previous();
+    float x[kAhead][8], y[kAhead][8];              // the elements, and their partners
+    auto fetch = [&](int it, float (&a)[8], float (&b)[8]) {
+        const Piece m = piece_of(p, it, per_head_shift);
+        const int64_t row = tok * p.src_token[m.which] + m.head * p.src_head[m.which];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            load4<SRC, VEC>(p.src[m.which], row + m.at + 4 * h, reinterpret_cast<float(&)[4]>(a[4 * h]));
+            if (HALF && m.which < 2 && m.at < p.rot)
+                load4<SRC, VEC>(p.src[m.which], row + partner(m.at + 4 * h, p.rot),
+                                reinterpret_cast<float(&)[4]>(b[4 * h]));
+        }
+    };
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+        if (first + u * step < total)
+            fetch(first + u * step, x[u], y[u]);
+
+    find_token<kThreads>(p.batch, tok, where);
+    const int req = where[0], pos = where[1];
+    if (req < 0)
+        return;                                    // a row of no request
+    if (threadIdx.x < (p.rot >> 1))
+        turn[threadIdx.x] = turn_of(p, threadIdx.x, p.positions ? p.positions[tok] : pos);
+    const int page = page_of(p.batch, p.kv, req, pos);
+    const int slot = pos & ((1 << p.kv.page_shift) - 1);
+    __syncthreads();
+
+    // all lanes of a warp come here together; the pieces past the last do nothing
+    auto finish = [&](int it, float (&a)[8], float (&b)[8]) {
+        const bool in = it < total;
+        const Piece m = piece_of(p, in ? it : 0, per_head_shift);
+        if (in && m.which < 2 && m.at < p.rot) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int o = m.at + 4 * h, half = p.rot >> 1;
+                if constexpr (HALF) {
+                    // the sums of rope_append.cu, in the same order
+                    const bool low = o < half;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 t = turn[(low ? o : o - half) + i];
+                        float& v = a[4 * h + i];
+                        const float w = b[4 * h + i];
+                        v = low ? v * t.x - w * t.y : v * t.x + w * t.y;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 t = turn[(o >> 1) + i];
+                        float &v = a[4 * h + 2 * i], &w = a[4 * h + 2 * i + 1];
+                        const float n = v * t.x - w * t.y;
+                        w = w * t.x + v * t.y;
+                        v = n;
+                    }
+                }
+            }
+        }
+        if (in && m.which == 0) {
+            uint16_t* d = p.q_out + tok * p.out_token + m.head * p.out_head + m.at;
+            store4<DST, VEC>(d, reinterpret_cast<float(&)[4]>(a[0]));
+            store4<DST, VEC>(d + 4, reinterpret_cast<float(&)[4]>(a[4]));
+        }
+        // the group's bounds, by its 8 lanes
+        constexpr float kMost = DST == LBV_F16 ? 32768.f : 8.5070591730234616e37f;    // 2^15, 2^126
+        float lo = a[0], hi = a[0];
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            lo = fminf(lo, a[i]), hi = fmaxf(hi, a[i]);
+            odd = odd || !(fabsf(a[i]) <= kMost);
+        }
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) {
+            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, d));
+            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, d));
+        }
+        odd = (__ballot_sync(0xffffffffu, odd) >> (lane & 24)) & 0xFFu;
+        if (!in || m.which == 0 || page < 0)
+            return;
+        uint16_t bias = from_f32<DST>(lo), scale = from_f32<DST>(__fdiv_rn(hi - lo, 15.f));
+        float s = to_f32<DST>(scale);
+        if (!(s >= 1.17549435e-38f))               // its reciprocal would not be finite
+            s = 0.f, scale = 0;
+        const float low = to_f32<DST>(bias), inverse = s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
+        uint32_t word = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            word |= (uint32_t)max(0, min(15, __float2int_rn((a[i] - low) * inverse))) << (4 * (i >> 1) + 16 * (i & 1));
+        if (odd)
+            scale = 0x7FFF;                        // NaN in both types
+        const int cs = kv4::chunk_shift(p.kv), at = slot & ((1 << cs) - 1);
+        const int planes = p.kv.dim >> 5, plane = (m.which - 1) * (planes >> 1) + (m.at >> 6);
+        uint8_t* c = kv4::chunk(p.kv, page, m.head, slot);
+        *reinterpret_cast<uint32_t*>(c + kv4::codes_at(plane, at, cs) + ((m.at >> 3) & 7) * 4) = word;
+        if ((m.at & 63) == 0)
+            *reinterpret_cast<uint32_t*>(c + kv4::scale_at(planes, plane, at, cs)) = scale | ((uint32_t)bias << 16);
+    };
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+        if (first - lane + u * step < total)
+            finish(first + u * step, x[u], y[u]);
+    for (int it = first + kAhead * step; it - lane < total; it += step) {
+        if (it < total)
+            fetch(it, x[0], y[0]);
+        __syncwarp();                              // q_out may be q: a head is one warp's, its partners are loaded
+        finish(it, x[0], y[0]);
+    }
+}
+
+template <int SRC, int DST, bool HALF>
+cudaError_t launch(const RopeParams& p, bool vec, cudaStream_t st)
+{
+    const int total = (p.q_heads + 2 * p.kv.heads) * (p.kv.dim / 8);
+    // few tokens: one piece a thread, so that the whole call is in flight at once
+    const int per = p.batch.tokens < 256 ? 1 : kAhead;
+    const dim3 grid((unsigned)p.batch.tokens,
+                    (unsigned)((total + kThreads * per - 1) / (kThreads * per)));
+    return vec ? launch_after(lbv_rope_append4_kernel<SRC, DST, HALF, true>, grid, kThreads, 0, st, p)
+               : launch_after(lbv_rope_append4_kernel<SRC, DST, HALF, false>, grid, kThreads, 0, st, p);
+}
+
+template <int SRC>
+cudaError_t launch_src(const RopeParams& p, lbv_dtype dst, lbv_rope_layout layout, bool vec,
+                       cudaStream_t st)
+{
+    if (dst == LBV_F16)
+        return layout == LBV_ROPE_HALF ? launch<SRC, LBV_F16, true>(p, vec, st)
+                                       : launch<SRC, LBV_F16, false>(p, vec, st);
+    return layout == LBV_ROPE_HALF ? launch<SRC, LBV_BF16, true>(p, vec, st)
+                                   : launch<SRC, LBV_BF16, false>(p, vec, st);
+}
+
+}  // namespace
+
+cudaError_t launch_rope_append4(const RopeParams& p, lbv_dtype src, lbv_dtype dst,
+                                lbv_rope_layout layout, bool vec, cudaStream_t st)
+{
+    if (src == LBV_F32)
+        return launch_src<LBV_F32>(p, dst, layout, vec, st);
+    return src == LBV_F16 ? launch_src<LBV_F16>(p, dst, layout, vec, st)
+                          : launch_src<LBV_BF16>(p, dst, layout, vec, st);
+}
+
+}  // namespace lbv

@@ -118,6 +118,12 @@ __device__ __forceinline__ float2 unpack2(uint32_t r)
         return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xFFFF0000u));
 }
 
+// Whether a copy of keys [key, key + n) is of use to a tile that sees [lo, hi) and the sinks.
+__device__ __forceinline__ bool wanted(const AttendParams& p, int lo, int hi, int key, int n)
+{
+    return key < hi && (key + n > lo || key < p.sinks);
+}
+
 // A request's share of the batch.
 struct Request {
     int q0, n;             // first row, new tokens
@@ -138,7 +144,7 @@ __device__ __forceinline__ Request request_of(const AttendParams& p, int r)
     return q;
 }
 
-// Keys [lo, hi) that new tokens i0..i1 of a request can see.
+// Keys [lo, hi) that new tokens i0..i1 of a request can see, beside the sinks.
 __device__ __forceinline__ void key_range(const AttendParams& p, const Request& q, int i0, int i1,
                                           int& lo, int& hi)
 {
@@ -157,21 +163,20 @@ __device__ __forceinline__ bool sees(const AttendParams& p, const Request& q, in
     } else {
         s = key <= pos;
     }
-    return s && key < q.keys && (p.window <= 0 || key > pos - p.window);
+    return s && key < q.keys && (p.window <= 0 || key > pos - p.window || key < p.sinks);
 }
 
-// The same for 32 keys from key0 on, as bits.
-__device__ __forceinline__ uint32_t seen32(const AttendParams& p, const Request& q, int pos, uint64_t w,
+// The same for 32 keys from key0 on, as bits; `first` and `keys` of the request.
+__device__ __forceinline__ uint32_t seen32(const AttendParams& p, int first, int keys, int pos, uint64_t w,
                                            int key0)
 {
-    // keys [lo, hi) relative to key0, cut to 0..32
-    int hi = (p.tree ? q.keys : min(q.keys, pos + 1)) - key0;
-    int lo = p.window > 0 ? pos - p.window + 1 - key0 : 0;
-    hi = max(0, min(hi, 32));
-    lo = max(0, min(lo, 32));
-    uint32_t see = (uint32_t)((1ull << hi) - 1) & ~(uint32_t)((1ull << lo) - 1);
+    // the keys below x, cut to these 32
+    auto below = [&](int x) { return (uint32_t)((1ull << max(0, min(x - key0, 32))) - 1); };
+    uint32_t see = below(p.tree ? keys : min(keys, pos + 1));
+    if (p.window > 0)
+        see &= ~below(pos - p.window + 1) | below(p.sinks);
     if (p.tree) {
-        const int j = key0 - q.first;                   // new token of the first of the keys
+        const int j = key0 - first;                     // new token of the first of the keys
         uint64_t t = j <= -32 ? ~0ull : j < 0 ? (w << -j) | ((1ull << -j) - 1) : j < 64 ? w >> j : 0;
         see &= (uint32_t)t;
     }
@@ -247,7 +252,8 @@ __device__ __forceinline__ void finish4(const AttendParams& p, const Request& q,
 //
 // An item is a tile of up to ROWS rows of a request (new token times query head
 // of the group) and a key/value head, over the blocks of KEYS keys that some row
-// of the tile sees, at least one (an empty row has an output too).  Its cost in
+// of the tile sees, at least one (an empty row has an output too): those of the sinks,
+// and those from the first window on.  Its cost in
 // units: EXTRA for its queries and results, and NARROW for each block, or WIDE where
 // the tile has more than SINGLE rows.  The units of the batch form one sequence
 // -- request by request, tile by tile, head by head -- of which every CTA takes
@@ -266,8 +272,9 @@ struct Shape {
 
 struct Tile {
     int row0, rows;        // its rows
-    int lo, hi;            // keys they can see
-    int block0, blocks;
+    int lo, hi;            // keys they can see, beside the sinks
+    int near, gap;         // blocks of the sinks; blocks left out behind them
+    int blocks;
     unsigned units;
 };
 
@@ -284,8 +291,10 @@ __device__ __forceinline__ Tile tile_of(const AttendParams& p, const Request& q,
     x.row0 = t * S::ROWS;
     x.rows = min(S::ROWS, q.n * p.group - x.row0);
     key_range(p, q, token_of(p, x.row0), token_of(p, x.row0 + x.rows - 1), x.lo, x.hi);
-    x.block0 = x.lo / S::KEYS;
-    x.blocks = max(1, (x.hi + S::KEYS - 1) / S::KEYS - x.block0);
+    // (a window that reaches the sinks' last block leaves no block out)
+    x.near = x.lo > 0 ? (min(p.sinks, x.hi) + S::KEYS - 1) / S::KEYS : 0;
+    x.gap = max(0, x.lo / S::KEYS - x.near);
+    x.blocks = max(1, x.near + max(0, (x.hi + S::KEYS - 1) / S::KEYS - x.near - x.gap));
     x.units = S::EXTRA + (unsigned)(S::weight(x.rows) * x.blocks);
     return x;
 }
@@ -456,7 +465,7 @@ struct Walk {
     {
         return cta_of(item + S::EXTRA + (unsigned)(S::weight(x.rows) * (x.blocks - 1)));
     }
-    __device__ int key0(int b) const { return (x.block0 + b) * S::KEYS; }
+    __device__ int key0(int b) const { return (b < x.near ? b : b + x.gap) * S::KEYS; }
 };
 
 // A partial result's item, for the kernel that joins them: written by the CTA

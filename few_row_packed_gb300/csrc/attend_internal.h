@@ -16,6 +16,7 @@ struct AttendParams {
     const uint64_t* tree;            // [tokens] or NULL
     float scale_log2;                // scale * log2(e)
     int window;                      // <= 0: none
+    int sinks;                       // first positions that stay visible behind a window (0 without one)
     int heads, group;                // query heads, query heads per kv head
     uint32_t group_mul;              // row / group = (2 row * group_mul >> 32) >> group_shift
     int group_shift;
@@ -52,6 +53,9 @@ cudaError_t launch_attend_rows(const AttendParams& p, const CUtensorMap& kmap,
                                const CUtensorMap& vmap, lbv_dtype dt, int sms, cudaStream_t st);
 cudaError_t launch_attend_tiles(const AttendParams& p, const CUtensorMap& kmap,
                                 const CUtensorMap& vmap, lbv_dtype dt, int sms, cudaStream_t st);
+// Over a cache of 4 bits (the maps are not used).
+cudaError_t launch_attend4_tiles(const AttendParams& p, const CUtensorMap& kmap,
+                                 const CUtensorMap& vmap, lbv_dtype dt, int sms, cudaStream_t st);
 // Joins apart (attend_join.cu): when, and the launch for slots of slot_rows rows.
 bool attend_joins_apart(const AttendParams& p, int tile_rows, int ctas);
 cudaError_t launch_attend_join(const AttendParams& p, lbv_dtype dt, int slot_rows, int ctas,

@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, Geo<D>::CTAS)
                     const int key = k0 + piece * slots;
                     const int at = key >> p.kv.page_shift;
                     int page = -1;                               // fills zeros
-                    if (key < w.x.hi && key + slots > w.x.lo)
+                    if (wanted(p, w.x.lo, w.x.hi, key, slots))
                         page = table[at];
                     const uint32_t dst = sbase + st * G::STAGE + part * G::HALF + piece * slots * 128;
                     tma_box(dst, part < D / 64 ? &kmap : &vmap, (part % (D / 64)) * 64,

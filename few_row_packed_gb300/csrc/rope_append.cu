@@ -18,75 +18,16 @@
 // wide.  8191 tokens of 48 + 8 + 8 heads of 128, fp32 to bf16: 61 us, 6.6 TB/s, 97 % of
 // what a copy reaches; 8 tokens 2.4 us, 64 requests of 1 to 8 tokens 4.3 us, a launch and
 // one round trip to memory.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include "step_internal.h"
+#include "rope_rows.cuh"
 
 namespace lbv {
+
+using namespace rope;
 
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kAhead = 4;             // items a thread keeps in flight
-
-template <int DT>
-__device__ __forceinline__ float to_f32(uint16_t x)
-{
-    if constexpr (DT == LBV_F16)
-        return __half2float(__ushort_as_half(x));
-    else
-        return __bfloat162float(__ushort_as_bfloat16(x));
-}
-
-template <int DT>
-__device__ __forceinline__ uint16_t from_f32(float x)
-{
-    if constexpr (DT == LBV_F16)
-        return __half_as_ushort(__float2half_rn(x));
-    else
-        return __bfloat16_as_ushort(__float2bfloat16_rn(x));
-}
-
-template <int SRC, bool VEC>
-__device__ __forceinline__ void load4(const void* base, int64_t at, float (&x)[4])
-{
-    if constexpr (SRC == LBV_F32) {
-        const float* s = static_cast<const float*>(base) + at;
-        if constexpr (VEC) {
-            const float4 v = *reinterpret_cast<const float4*>(s);
-            x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                x[i] = s[i];
-        }
-    } else {
-        const uint16_t* s = static_cast<const uint16_t*>(base) + at;
-        if constexpr (VEC) {
-            const ushort4 v = *reinterpret_cast<const ushort4*>(s);
-            x[0] = to_f32<SRC>(v.x), x[1] = to_f32<SRC>(v.y);
-            x[2] = to_f32<SRC>(v.z), x[3] = to_f32<SRC>(v.w);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                x[i] = to_f32<SRC>(s[i]);
-        }
-    }
-}
-
-template <int DST, bool VEC>
-__device__ __forceinline__ void store4(uint16_t* d, const float (&x)[4])
-{
-    if constexpr (VEC) {
-        *reinterpret_cast<ushort4*>(d) = make_ushort4(from_f32<DST>(x[0]), from_f32<DST>(x[1]),
-                                                      from_f32<DST>(x[2]), from_f32<DST>(x[3]));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            d[i] = from_f32<DST>(x[i]);
-    }
-}
 
 // Where an item comes from and goes to.
 struct Item {
@@ -134,35 +75,15 @@ __global__ void __launch_bounds__(kThreads) lbv_rope_append_kernel(const __grid_
         if (first + u * step < total)
             fetch(first + u * step, x0[u], x1[u]);
 
-    if (threadIdx.x == 0)
-        where[0] = -1;
-    __syncthreads();
-    for (int r = threadIdx.x; r < p.batch.requests; r += kThreads) {
-        const int lo = p.batch.q_start[r], hi = p.batch.q_start[r + 1];
-        if (lo <= tok && tok < hi) {
-            where[0] = r;
-            where[1] = p.batch.kv_len[r] - hi + tok;
-        }
-    }
-    __syncthreads();
+    find_token<kThreads>(p.batch, tok, where);
     const int req = where[0], pos = where[1];
     if (req < 0)
         return;                                    // a row of no request
-    if (threadIdx.x < (p.rot >> 1)) {
-        const int at = p.positions ? p.positions[tok] : pos;
-        const uint64_t f = (uint64_t)(int64_t)at * p.turns[threadIdx.x];
-        float s, c;
-        sincospif((float)(int32_t)(f >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31 half turns
-        turn[threadIdx.x] = make_float2(c * p.factor, s * p.factor);
-    }
-    int64_t slot = -1;
-    const int page_at = pos >> p.kv.page_shift;
-    if (pos >= 0 && page_at < p.batch.table_pages) {
-        const int page = p.batch.block_table[(int64_t)req * p.batch.table_stride + page_at];
-        if (page >= 0 && page < p.kv.pages)
-            slot = page * p.kv.page_stride +
-                   (pos & ((1 << p.kv.page_shift) - 1)) * p.kv.token_stride;
-    }
+    if (threadIdx.x < (p.rot >> 1))
+        turn[threadIdx.x] = turn_of(p, threadIdx.x, p.positions ? p.positions[tok] : pos);
+    const int page = page_of(p.batch, p.kv, req, pos);
+    const int64_t slot = page < 0 ? -1 : page * p.kv.page_stride +
+                                             (pos & ((1 << p.kv.page_shift) - 1)) * p.kv.token_stride;
     __syncthreads();
 
     auto finish = [&](int it, float (&a)[4], float (&b)[4]) {

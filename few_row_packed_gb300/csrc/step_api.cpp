@@ -9,6 +9,7 @@
 #include <new>
 
 #include "attend_internal.h"
+#include "kv4.cuh"
 #include "step_internal.h"
 
 namespace {
@@ -181,7 +182,7 @@ lbv_status lbv_kv_cache_create(void* k, void* v, int pages, int page_size, int h
     while ((1 << shift) < page_size)
         ++shift;
     c->view = {static_cast<uint16_t*>(k), static_cast<uint16_t*>(v), page_stride, token_stride,
-               head_stride, pages, shift, heads, head_dim};
+               head_stride, pages, shift, heads, head_dim, nullptr};
     c->dtype = dtype;
     c->sms = 0;
     if (cudaGetDevice(&c->device) != cudaSuccess ||
@@ -194,6 +195,49 @@ lbv_status lbv_kv_cache_create(void* k, void* v, int pages, int page_size, int h
     if (c->device >= 0 && !c->maps) {
         delete c;
         return fail(LBV_ERR_CUDA, "%s: the driver has no tensor map for this layout", fn);
+    }
+    *out = c;
+    return LBV_OK;
+}
+
+size_t lbv_kv_cache4_page_bytes(int page_size, int heads, int head_dim)
+{
+    if (page_size < 8 || page_size > 1024 || (page_size & (page_size - 1)) != 0 || heads < 1 || heads > 65535 ||
+        (head_dim != 64 && head_dim != 128))
+        return 0;
+    return (size_t)page_size * heads * lbv::kv4::slot_bytes(head_dim);
+}
+
+lbv_status lbv_kv_cache4_create(void* data, int pages, int page_size, int heads, int head_dim,
+                                lbv_dtype dtype, lbv_kv_cache** out)
+{
+    const char* fn = "lbv_kv_cache4_create";
+    lbv::set_error(LBV_OK, "");
+    if (!out)
+        return fail(LBV_ERR_INVALID_ARG, "%s: out is NULL", fn);
+    *out = nullptr;
+    if (!data || !aligned(data, 16))
+        return fail(LBV_ERR_INVALID_ARG, "%s: data is null or not 16-byte aligned", fn);
+    if (!is16(dtype))
+        return fail(LBV_ERR_INVALID_ARG, "%s: unknown cache dtype %d", fn, (int)dtype);
+    if (pages < 1 || heads < 1 || heads > 65535)
+        return fail(LBV_ERR_INVALID_ARG, "%s: pages=%d heads=%d", fn, pages, heads);
+    if (lbv_kv_cache4_page_bytes(page_size, heads, head_dim) == 0)
+        return fail(LBV_ERR_UNSUPPORTED, "%s: page_size %d (a power of two, 8..1024), head_dim %d (64 or 128)", fn,
+                    page_size, head_dim);
+    lbv_kv_cache* c = new (std::nothrow) lbv_kv_cache();
+    if (!c)
+        return fail(LBV_ERR_INVALID_ARG, "%s: out of host memory", fn);
+    int shift = 0;
+    while ((1 << shift) < page_size)
+        ++shift;
+    c->view = {nullptr, nullptr, 0, 0, 0, pages, shift, heads, head_dim, static_cast<uint8_t*>(data)};
+    c->dtype = dtype;
+    c->sms = 0;
+    if (cudaGetDevice(&c->device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&c->sms, cudaDevAttrMultiProcessorCount, c->device) != cudaSuccess) {
+        cudaGetLastError();
+        c->device = -1;
     }
     *out = c;
     return LBV_OK;
@@ -337,11 +381,95 @@ lbv_status lbv_rope_append(const lbv_rope* rope, const lbv_batch* batch, const l
     p.q_heads = q ? q->heads : 0;
     p.rot = rope->rot;
     p.factor = rope->factor;
-    const cudaError_t e = lbv::launch_rope_append(p, (lbv_dtype)k->dtype, cache->dtype,
-                                                  rope->layout, vec, (cudaStream_t)stream);
+    const auto launch = cache->view.packed ? lbv::launch_rope_append4 : lbv::launch_rope_append;
+    const cudaError_t e = launch(p, (lbv_dtype)k->dtype, cache->dtype, rope->layout, vec, (cudaStream_t)stream);
     if (e != cudaSuccess)
         return cuda_fail(e, "lbv_rope_append: launch");
     return LBV_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Reading, closing up and copying what a paged cache holds
+
+lbv_status lbv_kv_read(const lbv_batch* batch, const lbv_kv_cache* cache, const lbv_rows* k,
+                       const lbv_rows* v, lbv_stream stream)
+{
+    const char* fn = "lbv_kv_read";
+    lbv::set_error(LBV_OK, "");
+    lbv_status st = check_batch(fn, batch);
+    const lbv_rows* rows[2] = {k, v};
+    if (st == LBV_OK && !k && !v)
+        return fail(LBV_ERR_INVALID_ARG, "%s: k and v are NULL", fn);
+    for (int i = 0; i < 2; ++i)
+        if (st == LBV_OK && rows[i])
+            st = check_rows(fn, i ? "v" : "k", rows[i], batch->tokens);
+    if (st == LBV_OK)
+        st = check_cache(fn, cache);
+    if (st != LBV_OK)
+        return st;
+    lbv::ReadParams p = {};
+    p.wide = 1;
+    for (int i = 0; i < 2; ++i) {
+        const lbv_rows* r = rows[i];
+        if (!r)
+            continue;
+        if (r->dtype != cache->dtype || r->heads != cache->view.heads)
+            return fail(LBV_ERR_INVALID_ARG, "%s: %s is not of the cache's dtype with its %d heads", fn, i ? "v" : "k",
+                        cache->view.heads);
+        p.out[i] = static_cast<uint16_t*>(r->data);
+        p.out_token[i] = r->token_stride;
+        p.out_head[i] = r->head_stride;
+        p.wide = p.wide && aligned(r->data, 16) && r->token_stride % 8 == 0 && r->head_stride % 8 == 0;
+    }
+    if (batch->tokens == 0)
+        return LBV_OK;
+    p.batch = *batch;
+    p.kv = cache->view;
+    const cudaError_t e = lbv::launch_kv_read(p, cache->dtype, (cudaStream_t)stream);
+    return e == cudaSuccess ? LBV_OK : cuda_fail(e, "lbv_kv_read: launch");
+}
+
+lbv_status lbv_kv_keep(const lbv_batch* batch, const lbv_kv_cache* cache, const uint64_t* kept, int32_t* left,
+                       lbv_stream stream)
+{
+    const char* fn = "lbv_kv_keep";
+    lbv::set_error(LBV_OK, "");
+    lbv_status st = check_batch(fn, batch);
+    if (st == LBV_OK && (!kept || !aligned(kept, 8) || !aligned(left, 4)))
+        return fail(LBV_ERR_INVALID_ARG, "%s: kept is NULL, or kept or left misaligned", fn);
+    if (st == LBV_OK)
+        st = check_cache(fn, cache);
+    if (st != LBV_OK)
+        return st;
+    // left is written while other blocks still read the batch's counts and kept
+    auto apart = [&](const void* q, size_t words) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(left), b = reinterpret_cast<uintptr_t>(q);
+        return !left || a + (size_t)batch->requests * 4 <= b || b + words * 4 <= a;
+    };
+    if (!apart(batch->kv_len, batch->requests) || !apart(batch->q_start, (size_t)batch->requests + 1) ||
+        !apart(kept, (size_t)batch->requests * 2) ||
+        !apart(batch->block_table, (size_t)(batch->requests - 1) * batch->table_stride + batch->table_pages))
+        return fail(LBV_ERR_INVALID_ARG, "%s: left overlaps an input", fn);
+    const cudaError_t e = lbv::launch_kv_keep(*batch, cache->view, kept, left, (cudaStream_t)stream);
+    return e == cudaSuccess ? LBV_OK : cuda_fail(e, "lbv_kv_keep: launch");
+}
+
+lbv_status lbv_kv_copy_pages(const lbv_kv_cache* cache, const int32_t* src, const int32_t* dst, int count,
+                             lbv_stream stream)
+{
+    const char* fn = "lbv_kv_copy_pages";
+    lbv::set_error(LBV_OK, "");
+    if (count < 0 || (count > 0 && (!src || !dst)) || !aligned(src, 4) || !aligned(dst, 4))
+        return fail(LBV_ERR_INVALID_ARG, "%s: count=%d, or src or dst null or misaligned", fn, count);
+    const lbv_status st = check_cache(fn, cache);
+    if (st != LBV_OK)
+        return st;
+    if (count == 0)
+        return LBV_OK;
+    if (count > cache->view.pages)      // pages that are dst of two pairs
+        return fail(LBV_ERR_INVALID_ARG, "%s: count=%d of %d pages", fn, count, cache->view.pages);
+    const cudaError_t e = lbv::launch_kv_copy_pages(cache->view, src, dst, count, (cudaStream_t)stream);
+    return e == cudaSuccess ? LBV_OK : cuda_fail(e, "lbv_kv_copy_pages: launch");
 }
 
 // ---------------------------------------------------------------------------
@@ -358,8 +486,8 @@ size_t lbv_attend_workspace_bytes(const lbv_kv_cache* cache, const lbv_batch* ba
 
 // lbv_attend, by the name `fn`; copies >= 0: the test of the bounded waits.
 static lbv_status attend(const char* fn, const lbv_kv_cache* cache, const lbv_batch* batch, const lbv_rows* q,
-                         const lbv_rows* out, float scale, int window, const uint64_t* tree, float* lse,
-                         void* workspace, size_t workspace_bytes, int copies, lbv_stream stream)
+                         const lbv_rows* out, float scale, int window, int sinks, const uint64_t* tree,
+                         float* lse, void* workspace, size_t workspace_bytes, int copies, lbv_stream stream)
 {
     lbv::set_error(LBV_OK, "");
     lbv_status st = check_batch(fn, batch);
@@ -376,8 +504,8 @@ static lbv_status attend(const char* fn, const lbv_kv_cache* cache, const lbv_ba
     if (q->heads != out->heads || q->heads % cache->view.heads != 0)
         return fail(LBV_ERR_INVALID_ARG, "%s: %d query and %d output heads over %d cache heads", fn,
                     q->heads, out->heads, cache->view.heads);
-    if (!std::isfinite(scale) || window < 0)
-        return fail(LBV_ERR_INVALID_ARG, "%s: scale=%g window=%d", fn, (double)scale, window);
+    if (!std::isfinite(scale) || window < 0 || sinks < 0)
+        return fail(LBV_ERR_INVALID_ARG, "%s: scale=%g window=%d sinks=%d", fn, (double)scale, window, sinks);
     if (!aligned(tree, 8) || !aligned(lse, 4))
         return fail(LBV_ERR_INVALID_ARG, "%s: tree or lse misaligned", fn);
     if (batch->tokens == 0)
@@ -403,6 +531,7 @@ static lbv_status attend(const char* fn, const lbv_kv_cache* cache, const lbv_ba
     p.tree = tree;
     p.scale_log2 = scale * 1.44269504088896341f;
     p.window = window < (1 << 30) ? window : 0;    // no context is that long
+    p.sinks = p.window == 0 ? 0 : sinks < (1 << 30) ? sinks : 1 << 30;
     p.heads = q->heads;
     p.group = q->heads / cache->view.heads;
     // the reciprocal rounded up at 31 + ceil(log2 group) bits divides all rows below 2^31
@@ -420,7 +549,9 @@ static lbv_status attend(const char* fn, const lbv_kv_cache* cache, const lbv_ba
     p.wait_limit = copies < 0 ? lbv::kAttendWaitLimit : lbv::kAttendTestLimit;
     p.first_copies = copies < 0 ? ~0u : (unsigned)copies;
     // both kernels are right for every length
-    const auto launch = lbv::attend_average_rows(p) <= 16 ? lbv::launch_attend_rows : lbv::launch_attend_tiles;
+    const auto launch = p.kv.packed                        ? lbv::launch_attend4_tiles
+                        : lbv::attend_average_rows(p) <= 16 ? lbv::launch_attend_rows
+                                                            : lbv::launch_attend_tiles;
     const cudaError_t e = launch(p, cache->kmap, cache->vmap, cache->dtype, cache->sms,
                                  (cudaStream_t)stream);
     if (e != cudaSuccess)
@@ -432,8 +563,16 @@ lbv_status lbv_attend(const lbv_kv_cache* cache, const lbv_batch* batch, const l
                       const lbv_rows* out, float scale, int window, const uint64_t* tree,
                       float* lse, void* workspace, size_t workspace_bytes, lbv_stream stream)
 {
-    return attend("lbv_attend", cache, batch, q, out, scale, window, tree, lse, workspace, workspace_bytes, -1,
+    return attend("lbv_attend", cache, batch, q, out, scale, window, 0, tree, lse, workspace, workspace_bytes, -1,
                   stream);
+}
+
+lbv_status lbv_attend_sinks(const lbv_kv_cache* cache, const lbv_batch* batch, const lbv_rows* q,
+                            const lbv_rows* out, float scale, int window, int sinks, const uint64_t* tree,
+                            float* lse, void* workspace, size_t workspace_bytes, lbv_stream stream)
+{
+    return attend("lbv_attend_sinks", cache, batch, q, out, scale, window, sinks, tree, lse, workspace,
+                  workspace_bytes, -1, stream);
 }
 
 lbv_status lbv_attend_test_wait(const lbv_kv_cache* cache, const lbv_batch* batch, const lbv_rows* q,
@@ -444,7 +583,7 @@ lbv_status lbv_attend_test_wait(const lbv_kv_cache* cache, const lbv_batch* batc
     const char* fn = "lbv_attend_test_wait";
     if (copies < 0)
         return fail(LBV_ERR_INVALID_ARG, "%s: copies=%d", fn, copies);
-    return attend(fn, cache, batch, q, out, scale, window, tree, lse, workspace, workspace_bytes, copies,
+    return attend(fn, cache, batch, q, out, scale, window, 0, tree, lse, workspace, workspace_bytes, copies,
                   stream);
 }
 

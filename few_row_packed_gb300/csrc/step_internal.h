@@ -20,6 +20,7 @@ struct KvView {
     uint16_t* v;
     int64_t page_stride, token_stride, head_stride;
     int pages, page_shift, heads, dim;
+    uint8_t* packed;                 // a cache of 4 bits (kv4.cuh), else NULL
 };
 
 // Frequencies of a rotation in 2^-64 turns per position.
@@ -41,6 +42,24 @@ struct RopeParams {
 
 cudaError_t launch_rope_append(const RopeParams& p, lbv_dtype src, lbv_dtype dst,
                                lbv_rope_layout layout, bool vec, cudaStream_t st);
+
+// The append to a cache of 4 bits (append4.cu).
+cudaError_t launch_rope_append4(const RopeParams& p, lbv_dtype src, lbv_dtype dst,
+                                lbv_rope_layout layout, bool vec, cudaStream_t st);
+
+struct ReadParams {
+    lbv_batch batch;
+    KvView kv;
+    uint16_t* out[2];                // k, v rows; one may be NULL
+    int64_t out_token[2], out_head[2];
+    int wide;                        // rows are 16-byte aligned
+};
+
+cudaError_t launch_kv_read(const ReadParams& p, lbv_dtype dt, cudaStream_t st);
+cudaError_t launch_kv_keep(const lbv_batch& b, const KvView& kv, const uint64_t* kept, int32_t* left,
+                           cudaStream_t st);
+cudaError_t launch_kv_copy_pages(const KvView& kv, const int32_t* src, const int32_t* dst, int count,
+                                 cudaStream_t st);
 
 struct SampleParams {
     const void* logits;              // [rows][ld]

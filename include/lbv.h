@@ -498,6 +498,25 @@ LBV_API lbv_status lbv_kv_cache_create(void* k, void* v, int pages, int page_siz
                                        int64_t head_stride, lbv_dtype dtype, lbv_kv_cache** out);
 LBV_API lbv_status lbv_kv_cache_destroy(lbv_kv_cache* cache);
 
+/*
+ * A paged cache held in 4 bits.  An element is round(code * scale + bias), rounded once
+ * to the cache's dtype (fp16 or bf16), for a code of 0..15 and the scale and bias
+ * (of that dtype) of its 64 elements of a head: 4.5 bits an element.  A page is
+ * lbv_kv_cache4_page_bytes() bytes (0 for sizes that lbv_kv_cache4_create refuses),
+ *     [heads][page_size / C][chunk of C = min(page_size, 64) slots]
+ * and a chunk of keys (K) and values (V)
+ *     codes  [K, V][head_dim / 64][C][32] bytes: word w (32 bits, little-endian) has element
+ *            8 w + i in the bits from 4 (i / 2) + 16 (i % 2) on,
+ *     scales [K, V][head_dim / 64][C] pairs of (scale, bias).
+ * data: dev, 16-byte aligned, `pages` pages one after the other.  The handle is one
+ * of lbv_kv_cache: lbv_rope_append (which rounds to the nearest code),
+ * lbv_attend, lbv_kv_read, lbv_kv_keep and lbv_kv_copy_pages take it as they take a
+ * cache of 16 bits.  Sizes and errors as lbv_kv_cache_create.
+ */
+LBV_API size_t lbv_kv_cache4_page_bytes(int page_size, int heads, int head_dim);
+LBV_API lbv_status lbv_kv_cache4_create(void* data, int pages, int page_size, int heads,
+                                        int head_dim, lbv_dtype dtype, lbv_kv_cache** out);
+
 typedef enum {
     LBV_ROPE_HALF = 0,         /* pair j of a head: elements j and j + rot_dim/2   */
     LBV_ROPE_INTERLEAVED = 1   /* pair j of a head: elements 2j and 2j + 1          */
@@ -546,6 +565,10 @@ LBV_API lbv_status lbv_rope_destroy(lbv_rope* rope);
  * Sums are fp32, rounded once.  A token whose slot does not exist (a negative
  * position, one past the block table, a page outside the cache) has its key
  * and value left out; its query is rotated all the same.
+ * A cache of 4 bits gets, for each 64 elements x of a rotated key or a value (fp32):
+ * bias = min x and scale = (max x - min x) / 15, each rounded to the cache's dtype, and the codes
+ * (x - bias) * (1 / scale), rounded to the nearest whole number in 0..15 (all 0 where the scale is 0 or
+ * below 2^-126).  A group with a NaN or a magnitude above 2^15 (fp16) or 2^126 (bf16) reads as NaN.
  * Errors: LBV_ERR_INVALID_ARG for null or misaligned pointers, sizes that do
  * not agree and dtypes that cannot be; LBV_ERR_UNSUPPORTED if rot_dim exceeds
  * the head.  The library allocates nothing.
@@ -597,6 +620,15 @@ LBV_API lbv_status lbv_attend(const lbv_kv_cache* cache, const lbv_batch* batch,
                               float* lse, void* workspace, size_t workspace_bytes,
                               lbv_stream stream);
 
+/* lbv_attend whose first `sinks` (>= 0) positions of a request stay visible behind a
+ * window: with window > 0, key j is seen if j > P - window or j < sinks, beside the
+ * other conditions.  Only the pages of those positions and of the windows are read.
+ * lbv_attend is this call with sinks 0; without a window sinks change nothing. */
+LBV_API lbv_status lbv_attend_sinks(const lbv_kv_cache* cache, const lbv_batch* batch,
+                                    const lbv_rows* q, const lbv_rows* out, float scale, int window,
+                                    int sinks, const uint64_t* tree, float* lse, void* workspace,
+                                    size_t workspace_bytes, lbv_stream stream);
+
 /* LBV_ERR_TIMEOUT if an attention kernel that used the workspace gave up a
  * bounded wait since the last check (its output is then incomplete), else
  * LBV_OK; clears the record.  Synchronises with the device. */
@@ -615,6 +647,39 @@ LBV_API lbv_status lbv_attend_test_wait(const lbv_kv_cache* cache, const lbv_bat
                                         int window, const uint64_t* tree, float* lse,
                                         void* workspace, size_t workspace_bytes, int copies,
                                         lbv_stream stream);
+
+/*
+ * The keys and values of the batch's new tokens as they are held: k[t][h] and v[t][h]
+ * (rows of the cache's dtype with the cache's heads; one of them may be NULL) for every
+ * row t of a request.  With q_start over whole contexts it reads those.  A token whose slot
+ * does not exist reads as zeros.  Errors: LBV_ERR_INVALID_ARG.
+ */
+LBV_API lbv_status lbv_kv_read(const lbv_batch* batch, const lbv_kv_cache* cache, const lbv_rows* k,
+                               const lbv_rows* v, lbv_stream stream);
+
+/*
+ * Keeps some of the batch's new tokens and closes up the cache behind the context they
+ * follow: of request r the new tokens b < 64 whose bit b of kept[r] (dev uint64
+ * [requests]) is set move, in order, to the cache positions kv_len - n, kv_len - n + 1, ...;
+ * left[r] (dev int32 [requests], or NULL) = kv_len - n + their number.  Bits at or
+ * past n do not count; new tokens past the 64th are dropped.  What the slots from left[r] to
+ * kv_len hold afterwards does not matter.  Keys keep the rotary positions that they were
+ * appended with.  A move from or to a slot that does not exist is left out.
+ * The slots of the new tokens belong to one request each; left is apart from the batch's
+ * arrays and from kept.  Errors: LBV_ERR_INVALID_ARG.
+ */
+LBV_API lbv_status lbv_kv_keep(const lbv_batch* batch, const lbv_kv_cache* cache, const uint64_t* kept,
+                               int32_t* left, lbv_stream stream);
+
+/*
+ * Copies page src[i] to page dst[i], keys and values of every slot, for i < count (dev
+ * int32 arrays; at most the cache's pages): for requests that share pages and write to one of them, or to close up a cache.
+ * A pair with a page outside the cache is left out.  No page is dst of one pair and
+ * src or dst of another (the page would hold a mixture).  Errors:
+ * LBV_ERR_INVALID_ARG.
+ */
+LBV_API lbv_status lbv_kv_copy_pages(const lbv_kv_cache* cache, const int32_t* src, const int32_t* dst,
+                                     int count, lbv_stream stream);
 
 /* How lbv_sample draws: dev arrays with one entry per row, each may be NULL. */
 typedef struct lbv_sample_rules {

@@ -45,7 +45,7 @@ def gather(cache, table, page_size, count):
     return out
 
 
-def attend(q, k_cache, v_cache, q_start, kv_len, table, scale, window=0, tree=None):
+def attend(q, k_cache, v_cache, q_start, kv_len, table, scale, window=0, tree=None, sinks=0):
     """Returns out, lse, and what tolerances are made of: A = sum p |v| / sum p,
     V = sum |v| / sum 2^(t - max t), S = max_j scale sum |q_d k_d|."""
     rows, heads, dim = q.shape
@@ -68,7 +68,7 @@ def attend(q, k_cache, v_cache, q_start, kv_len, table, scale, window=0, tree=No
                 bit = np.array([(w >> int(x)) & 1 if 0 <= x < 64 else 0 for x in j - first], bool)
                 see = (j < first) | bit
             if window:
-                see = see & (j > first + i - window)
+                see = see & ((j > first + i - window) | (j < sinks))
             if not see.any():
                 continue
             for h in range(heads):
