@@ -327,7 +327,8 @@ def prepare(case, seed):
         if c["op"] != "copy":
             s["batch"] = lbv.Batch(s["start"], s["length"], s["table"], t)
         if c["op"] == "append":
-            s["rope"] = lbv.Rope(_frequencies(c),
+            # the frequencies that the plain form turns by: whole numbers of 2^-TURN turns
+            s["rope"] = lbv.Rope(s["turns"].cpu().numpy() * (2 * np.pi / 2 ** TURN),
                                  lbv.ROPE_HALF if c["layout"] == "half" else lbv.ROPE_INTERLEAVED)
         if c["op"] == "attend":
             s["work"] = torch.zeros(lbv.attend_workspace_bytes(s["cache"], s["batch"], c["heads"]),
