@@ -43,6 +43,7 @@ SOURCES = [
     "sample.cu",
     "attend_rows.cu",
     "attend_tiles.cu",
+    "attend4_rows.cu",
     "attend4_tiles.cu",
     "attend_join.cu",
     "tc_aux.cu",

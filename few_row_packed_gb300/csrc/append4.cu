@@ -9,6 +9,12 @@
 // that pair up, a thread loads its elements' partners too: they are another thread's own, so
 // they come from L1, and any rotated part of a head is treated alike.
 //
+// A code is a decision: values that differ in their last bit may fall on two sides of a
+// border.  So the arithmetic is that of elementary fp32 operations, the angle in
+// radians and every product and sum rounded by itself: a program that follows the
+// definition gets the same codes.  (The angle's fraction of a turn is exact to 2^-40 before
+// that; its rounding to fp32 is off by up to 4e-7, a millionth of a step between codes.)
+//
 // Bound by memory: every element is read once, queries leave as 16 bits, keys and
 // values as 4.5.
 #include "kv4.cuh"
@@ -37,6 +43,25 @@ __device__ __forceinline__ Piece piece_of(const RopeParams& p, int it, int per_h
     m.head = m.which == 0 ? row : m.which == 1 ? row - p.q_heads : row - p.q_heads - p.kv.heads;
     m.at = (it - (row << per_head_shift)) * 8;
     return m;
+}
+
+// cos and sin of pair j at position `at`, times the factor.
+__device__ __forceinline__ float2 turn32_of(const RopeParams& p, int j, int at)
+{
+    const uint64_t f = (uint64_t)(int64_t)at * p.turns[j];
+    const float angle = __fmul_rn(__ull2float_rn(f >> 24), (float)(6.283185307179586476925 / 1099511627776.0));
+    return make_float2(__fmul_rn(cosf(angle), p.factor), __fmul_rn(sinf(angle), p.factor));
+}
+
+// a b - c d and a b + c d, each step rounded.
+__device__ __forceinline__ float cross(float a, float b, float c, float d)
+{
+    return __fsub_rn(__fmul_rn(a, b), __fmul_rn(c, d));
+}
+
+__device__ __forceinline__ float dot(float a, float b, float c, float d)
+{
+    return __fadd_rn(__fmul_rn(a, b), __fmul_rn(c, d));
 }
 
 // Offset of the partners of the four elements from `at` on.
@@ -80,7 +105,7 @@ __global__ void __launch_bounds__(kThreads) lbv_rope_append4_kernel(const __grid
     if (req < 0)
         return;                                    // a row of no request
     if (threadIdx.x < (p.rot >> 1))
-        turn[threadIdx.x] = turn_of(p, threadIdx.x, p.positions ? p.positions[tok] : pos);
+        turn[threadIdx.x] = turn32_of(p, threadIdx.x, p.positions ? p.positions[tok] : pos);
     const int page = page_of(p.batch, p.kv, req, pos);
     const int slot = pos & ((1 << p.kv.page_shift) - 1);
     __syncthreads();
@@ -94,22 +119,21 @@ __global__ void __launch_bounds__(kThreads) lbv_rope_append4_kernel(const __grid
             for (int h = 0; h < 2; ++h) {
                 const int o = m.at + 4 * h, half = p.rot >> 1;
                 if constexpr (HALF) {
-                    // the sums of rope_append.cu, in the same order
                     const bool low = o < half;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float2 t = turn[(low ? o : o - half) + i];
                         float& v = a[4 * h + i];
                         const float w = b[4 * h + i];
-                        v = low ? v * t.x - w * t.y : v * t.x + w * t.y;
+                        v = low ? cross(v, t.x, w, t.y) : dot(v, t.x, w, t.y);
                     }
                 } else {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const float2 t = turn[(o >> 1) + i];
                         float &v = a[4 * h + 2 * i], &w = a[4 * h + 2 * i + 1];
-                        const float n = v * t.x - w * t.y;
-                        w = w * t.x + v * t.y;
+                        const float n = cross(v, t.x, w, t.y);
+                        w = dot(w, t.x, v, t.y);
                         v = n;
                     }
                 }
@@ -137,7 +161,7 @@ __global__ void __launch_bounds__(kThreads) lbv_rope_append4_kernel(const __grid
         odd = (__ballot_sync(0xffffffffu, odd) >> (lane & 24)) & 0xFFu;
         if (!in || m.which == 0 || page < 0)
             return;
-        uint16_t bias = from_f32<DST>(lo), scale = from_f32<DST>(__fdiv_rn(hi - lo, 15.f));
+        uint16_t bias = from_f32<DST>(lo), scale = from_f32<DST>(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
         float s = to_f32<DST>(scale);
         if (!(s >= 1.17549435e-38f))               // its reciprocal would not be finite
             s = 0.f, scale = 0;
@@ -145,7 +169,7 @@ __global__ void __launch_bounds__(kThreads) lbv_rope_append4_kernel(const __grid
         uint32_t word = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            word |= (uint32_t)max(0, min(15, __float2int_rn((a[i] - low) * inverse))) << (4 * (i >> 1) + 16 * (i & 1));
+            word |= (uint32_t)max(0, min(15, __float2int_rn(__fmul_rn(__fsub_rn(a[i], low), inverse)))) << (4 * (i >> 1) + 16 * (i & 1));
         if (odd)
             scale = 0x7FFF;                        // NaN in both types
         const int cs = kv4::chunk_shift(p.kv), at = slot & ((1 << cs) - 1);

@@ -54,6 +54,8 @@ cudaError_t launch_attend_rows(const AttendParams& p, const CUtensorMap& kmap,
 cudaError_t launch_attend_tiles(const AttendParams& p, const CUtensorMap& kmap,
                                 const CUtensorMap& vmap, lbv_dtype dt, int sms, cudaStream_t st);
 // Over a cache of 4 bits (the maps are not used).
+cudaError_t launch_attend4_rows(const AttendParams& p, const CUtensorMap& kmap,
+                                const CUtensorMap& vmap, lbv_dtype dt, int sms, cudaStream_t st);
 cudaError_t launch_attend4_tiles(const AttendParams& p, const CUtensorMap& kmap,
                                  const CUtensorMap& vmap, lbv_dtype dt, int sms, cudaStream_t st);
 // Joins apart (attend_join.cu): when, and the launch for slots of slot_rows rows.
@@ -63,5 +65,6 @@ cudaError_t launch_attend_join(const AttendParams& p, lbv_dtype dt, int slot_row
 // Floats of workspace the launches need for partial results.
 size_t attend_rows_partial_floats(int dim, int sms);
 size_t attend_tiles_partial_floats(int dim, int sms);
+size_t attend4_rows_partial_floats(int dim, int sms);
 
 }  // namespace lbv

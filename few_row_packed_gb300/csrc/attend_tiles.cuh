@@ -32,6 +32,7 @@
 #pragma once
 
 #include "attend_common.cuh"
+#include "attend_tc.cuh"
 #include "kv4.cuh"
 
 namespace lbv {
@@ -99,123 +100,6 @@ struct Geo {
     static_assert(BARS % 8 == 0 && STATS % 16 == 0 && ITEMS % 16 == 0 && WORDS % 16 == 0, "alignment");
     static_assert(BYTES <= 227 * 1024 && sizeof(Start) <= 2 * kTile * 8, "shared memory");
 };
-
-// ---- tcgen05 ----
-
-__device__ __forceinline__ void tc_fence_before()
-{
-    asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
-}
-
-__device__ __forceinline__ void tc_fence_after()
-{
-    asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
-}
-
-__device__ __forceinline__ void tmem_ld32(uint32_t at, float (&d)[32])
-{
-    uint32_t* r = reinterpret_cast<uint32_t*>(d);
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(at)
-        : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld16(uint32_t at, float (&d)[16])
-{
-    uint32_t* r = reinterpret_cast<uint32_t*>(d);
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-        "%14,%15}, [%16];\n"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15])
-        : "r"(at)
-        : "memory");
-}
-
-__device__ __forceinline__ void tmem_wait_ld()
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16])
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-        "%13,%14,%15,%16};\n" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]),
-        "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
-        "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-
-__device__ __forceinline__ void tmem_wait_st()
-{
-    asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
-}
-
-// Four steps of 16 of the contracted dimension, D (+)= A B, issued by one elected
-// lane of a converged warp: their operands stay in uniform registers that way (a
-// single thread in a branch of its own took 85 cycles an MMA to issue them).
-// `add` 0: the first step overwrites D.
-__device__ __forceinline__ void mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add)
-{
-    asm volatile(
-        "{\n .reg .pred e, p;\n setp.ne.b32 p, %10, 0;\n elect.sync _|e, 0xffffffff;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %5, %9, p;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %2, %6, %9, 1;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %3, %7, %9, 1;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %4, %8, %9, 1;\n}\n" ::"r"(d), "l"(a), "l"(a + 2),
-        "l"(a + 4), "l"(a + 6), "l"(b), "l"(b + 2), "l"(b + 4), "l"(b + 6), "r"(idesc), "r"(add)
-        : "memory");
-}
-
-// The same with A (P) in tensor memory and B (V) with its rows along the
-// contracted dimension: 8 columns of A and 16 rows of B a step.
-__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add)
-{
-    asm volatile(
-        "{\n .reg .pred e, p;\n setp.ne.b32 p, %10, 0;\n elect.sync _|e, 0xffffffff;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %5, %9, p;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], %6, %9, 1;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], %7, %9, 1;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%4], %8, %9, 1;\n}\n" ::"r"(d), "r"(a),
-        "r"(a + 8), "r"(a + 16), "r"(a + 24), "l"(b), "l"(b + 128), "l"(b + 256), "l"(b + 384),
-        "r"(idesc), "r"(add)
-        : "memory");
-}
-
-// Arrives on `bar` once every MMA the elected lane has issued is complete.
-__device__ __forceinline__ void commit(uint32_t bar)
-{
-    asm volatile(
-        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
-        : "memory");
-}
-
-// Shared-memory matrix descriptor in 128-byte-swizzled rows: 8-row groups 1024
-// bytes apart; for an operand whose rows run along the contracted dimension (V),
-// `lead` bytes between its 64-element column groups.
-__device__ __forceinline__ uint64_t desc128(uint32_t addr, uint32_t lead)
-{
-    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lead >> 4) & 0x3FFFu) << 16) |
-           ((uint64_t)(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
-
-// kind::f16, fp32 sums, M = 128; bit 16: B is N-major.
-template <int DT>
-__host__ __device__ constexpr uint32_t idesc(int n, bool b_n_major)
-{
-    return (1u << 4) | ((uint32_t)(DT == LBV_BF16) << 7) | ((uint32_t)(DT == LBV_BF16) << 10) |
-           ((uint32_t)b_n_major << 16) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
-}
 
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
@@ -296,47 +180,24 @@ __device__ __forceinline__ void fetch_q(const AttendParams& p, int q0, int kv_he
                      : "memory");
 }
 
-// A key's or value's row of a cache of 4 bits, as it is held.
-template <int D>
-struct Held {
-    uint4 codes[D / 32];
-    uint32_t scales[D / 64];
-
-    // Plane 0 (key) or 1 (value) of slot s in chunk c; zeros without a chunk.
-    __device__ __forceinline__ void load(const uint8_t* c, int which, int s, int cs)
-    {
+// The values of a row as it is held to row `row` of a slot at `dst`, in the layout of the
+// copies.
+template <int DT, int D>
+__device__ __forceinline__ void expand_row(const kv4::Held<D>& h, unsigned char* dst, int row)
+{
 #pragma unroll
-        for (int part = 0; part < D / 64; ++part) {
-            const int plane = which * (D / 64) + part;
-            codes[2 * part] = codes[2 * part + 1] = make_uint4(0u, 0u, 0u, 0u);
-            scales[part] = 0;
-            if (c) {
-                const uint4* src = reinterpret_cast<const uint4*>(c + kv4::codes_at(plane, s, cs));
-                codes[2 * part] = __ldg(src), codes[2 * part + 1] = __ldg(src + 1);
-                scales[part] = __ldg(reinterpret_cast<const uint32_t*>(c + kv4::scale_at(D / 32, plane, s, cs)));
-            }
+    for (int part = 0; part < D / 64; ++part) {
+        const uint32_t s = kv4::both_scales(h.scales[part]), b = kv4::both_biases(h.scales[part]);
+        unsigned char* d = dst + part * Geo<D>::HALF + row * 128;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint32_t v[4];
+            kv4::expand<DT>(h.codes[part][i], s, b, v);
+            *reinterpret_cast<uint4*>(d + ((i ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
         }
     }
-
-    // The row's values to row `row` of a slot at `dst`, in the layout of the copies.
-    template <int DT>
-    __device__ __forceinline__ void expand(unsigned char* dst, int row) const
-    {
-#pragma unroll
-        for (int part = 0; part < D / 64; ++part) {
-            const uint32_t s = kv4::both_scales(scales[part]), b = kv4::both_biases(scales[part]);
-            unsigned char* d = dst + part * Geo<D>::HALF + row * 128;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint4 c = codes[2 * part + (i >> 2)];
-                uint32_t v[4];
-                kv4::expand<DT>((i & 3) == 0 ? c.x : (i & 3) == 1 ? c.y : (i & 3) == 2 ? c.z : c.w, s, b, v);
-                *reinterpret_cast<uint4*>(d + ((i ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
-            }
-        }
-        fence_proxy_async_smem();
-    }
-};
+    fence_proxy_async_smem();
+}
 
 template <int DT, int D, bool KV4>
 __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
@@ -620,7 +481,7 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
                 return page < 0 || page >= p.kv.pages ? nullptr : kv4::chunk(p.kv, page, w.head, slot_at(j));
             };
             // Fills the next slot; false if it gave up.
-            auto fill = [&](const Held<D>& h) {
+            auto fill = [&](const kv4::Held<D>& h) {
                 const int st = n % G::NSLOT;
                 if (n >= G::NSLOT)
                     wait(empty(st), (uint32_t)((n / G::NSLOT - 1) & 1));
@@ -628,7 +489,7 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
                 if (!ok)
                     return false;
                 ++n;
-                h.template expand<DT>(smem + G::RING + st * G::SLOT, row);
+                expand_row<DT, D>(h, smem + G::RING + st * G::SLOT, row);
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(full(st));
@@ -636,7 +497,7 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
             };
             // what a thread waits for is asked for while the slot before it is filled: V during
             // K, the next block's K during V, its page a block ahead
-            Held<D> k, v;
+            kv4::Held<D> k, v;
             const uint8_t* c = chunk_at(page_at(0), 0);
             k.load(c, 0, slot_at(0) & ((1 << cs) - 1), cs);
             for (int j = 0; j < w.nb; ++j) {

@@ -56,6 +56,39 @@ __device__ __forceinline__ int scale_at(int planes, int plane, int s, int cs)
     return (planes * 32 << cs) + ((plane << cs) + s) * 4;
 }
 
+// 32 bytes from a 32-byte-aligned address: a row of codes in one load.
+__device__ __forceinline__ void load32(const void* src, uint32_t (&r)[8])
+{
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "l"(src)
+                 : "memory");
+}
+
+// A key's or a value's row as it is held.
+template <int D>
+struct Held {
+    uint32_t codes[D / 64][8];
+    uint32_t scales[D / 64];
+
+    // The key (which 0) or value (1) of slot s in chunk c; zeros without a chunk.
+    __device__ __forceinline__ void load(const uint8_t* c, int which, int s, int cs)
+    {
+#pragma unroll
+        for (int part = 0; part < D / 64; ++part) {
+            const int plane = which * (D / 64) + part;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                codes[part][i] = 0;
+            scales[part] = 0;
+            if (c) {
+                load32(c + codes_at(plane, s, cs), codes[part]);
+                scales[part] = *reinterpret_cast<const volatile uint32_t*>(c + scale_at(D / 32, plane, s, cs));
+            }
+        }
+    }
+};
+
 // The pairs at the four places of a word w: out[i] = code * scale + bias, rounded once,
 // of the codes in bits 4 i and 4 i + 16 on (of one slot's word elements 2 i and 2 i + 1).
 //

@@ -3,6 +3,7 @@
 // attention and the sampler.  Nothing here aborts or allocates device memory.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -216,8 +217,8 @@ lbv_status lbv_kv_cache4_create(void* data, int pages, int page_size, int heads,
     if (!out)
         return fail(LBV_ERR_INVALID_ARG, "%s: out is NULL", fn);
     *out = nullptr;
-    if (!data || !aligned(data, 16))
-        return fail(LBV_ERR_INVALID_ARG, "%s: data is null or not 16-byte aligned", fn);
+    if (!data || !aligned(data, 32))
+        return fail(LBV_ERR_INVALID_ARG, "%s: data is null or not 32-byte aligned", fn);
     if (!is16(dtype))
         return fail(LBV_ERR_INVALID_ARG, "%s: unknown cache dtype %d", fn, (int)dtype);
     if (pages < 1 || heads < 1 || heads > 65535)
@@ -479,7 +480,8 @@ size_t lbv_attend_workspace_bytes(const lbv_kv_cache* cache, const lbv_batch* ba
 {
     if (!cache || !batch || heads < 1)
         return 0;
-    const size_t rows = lbv::attend_rows_partial_floats(cache->view.dim, cache->sms);
+    const size_t rows = std::max(lbv::attend_rows_partial_floats(cache->view.dim, cache->sms),
+                                 lbv::attend4_rows_partial_floats(cache->view.dim, cache->sms));
     const size_t tiles = lbv::attend_tiles_partial_floats(cache->view.dim, cache->sms);
     return lbv::kAttendPartial + (rows > tiles ? rows : tiles) * sizeof(float);
 }
@@ -549,9 +551,9 @@ static lbv_status attend(const char* fn, const lbv_kv_cache* cache, const lbv_ba
     p.wait_limit = copies < 0 ? lbv::kAttendWaitLimit : lbv::kAttendTestLimit;
     p.first_copies = copies < 0 ? ~0u : (unsigned)copies;
     // both kernels are right for every length
-    const auto launch = p.kv.packed                        ? lbv::launch_attend4_tiles
-                        : lbv::attend_average_rows(p) <= 16 ? lbv::launch_attend_rows
-                                                            : lbv::launch_attend_tiles;
+    const int64_t rows = lbv::attend_average_rows(p);
+    const auto launch = p.kv.packed ? (rows <= 48 ? lbv::launch_attend4_rows : lbv::launch_attend4_tiles)
+                                    : (rows <= 16 ? lbv::launch_attend_rows : lbv::launch_attend_tiles);
     const cudaError_t e = launch(p, cache->kmap, cache->vmap, cache->dtype, cache->sms,
                                  (cudaStream_t)stream);
     if (e != cudaSuccess)

@@ -508,7 +508,7 @@ LBV_API lbv_status lbv_kv_cache_destroy(lbv_kv_cache* cache);
  *     codes  [K, V][head_dim / 64][C][32] bytes: word w (32 bits, little-endian) has element
  *            8 w + i in the bits from 4 (i / 2) + 16 (i % 2) on,
  *     scales [K, V][head_dim / 64][C] pairs of (scale, bias).
- * data: dev, 16-byte aligned, `pages` pages one after the other.  The handle is one
+ * data: dev, 32-byte aligned, `pages` pages one after the other.  The handle is one
  * of lbv_kv_cache: lbv_rope_append (which rounds to the nearest code),
  * lbv_attend, lbv_kv_read, lbv_kv_keep and lbv_kv_copy_pages take it as they take a
  * cache of 16 bits.  Sizes and errors as lbv_kv_cache_create.
@@ -568,7 +568,9 @@ LBV_API lbv_status lbv_rope_destroy(lbv_rope* rope);
  * A cache of 4 bits gets, for each 64 elements x of a rotated key or a value (fp32):
  * bias = min x and scale = (max x - min x) / 15, each rounded to the cache's dtype, and the codes
  * (x - bias) * (1 / scale), rounded to the nearest whole number in 0..15 (all 0 where the scale is 0 or
- * below 2^-126).  A group with a NaN or a magnitude above 2^15 (fp16) or 2^126 (bf16) reads as NaN.
+ * below 2^-126).  So that equal inputs give equal codes wherever the definition is followed,
+ * every operation is rounded by itself there: the angle's fraction of a turn is cut to 2^-40 and
+ * taken to fp32 radians, whose cos and sin are fp32, and so are products and sums.  A group with a NaN or a magnitude above 2^15 (fp16) or 2^126 (bf16) reads as NaN.
  * Errors: LBV_ERR_INVALID_ARG for null or misaligned pointers, sizes that do
  * not agree and dtypes that cannot be; LBV_ERR_UNSUPPORTED if rot_dim exceeds
  * the head.  The library allocates nothing.
