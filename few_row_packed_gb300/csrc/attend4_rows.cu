@@ -36,38 +36,69 @@ namespace {
 constexpr int kKeys = 128;                       // keys per block, one a thread
 // Units of a block and of an item beside its blocks; the least share of a group.
 constexpr int kBlockUnits = 4, kExtra = 6, kMinUnits = 4;
+// A reference that every score passes, negated: nothing has been seen yet.
+constexpr float kNone = 1e30f;
 
 // N: rows of an item, 16 or 48.
 template <int D, int N>
 struct Geo4 {
-    // groups of four warps: as many as shared memory has room for
-    static constexpr int GROUPS = N == 16 ? 4 : 3;
+    // groups of four warps, and stages of values as they are held: what shared memory has room for
+    static constexpr int GROUPS = D == 64 && N == 16 ? 4 : 3;
+    static constexpr int VST = N == 16 ? 2 : 1;
     static constexpr int THREADS = GROUPS * 128;
     static constexpr int HALF = kKeys * 128;                // 64 elements of 128 keys
-    // a group's shared memory: V; P, whose rows have room for 64; Q; what the rows need
+    // a group's operands: V in rows of 128 bytes, P in rows of 16 probabilities, Q
     static constexpr int V = 0;
     static constexpr int P = D / 64 * HALF;
-    static constexpr int Q = P + HALF;
+    static constexpr int PCHUNK = kKeys * 32;
+    static constexpr int Q = P + N / 16 * PCHUNK;
     static constexpr int QHALF = N * 128;
-    static constexpr int INFO = Q + D / 64 * QHALF;
-    static constexpr int WORDS = INFO;                      // uint64 [N]: the rows' words of the tree
+    static constexpr int SIZE = Q + D / 64 * QHALF;
+    // behind the groups' operands, what else each has: a block's keys and values as they are
+    // held (codes, then scales), and what the rows need
+    static constexpr int CODES = kKeys * 32 * (D / 64), HELD = kKeys * 36 * (D / 64);
+    static constexpr int KHELD = 0;
+    static constexpr int VHELD = HELD;
+    static constexpr int WORDS = VHELD + VST * HELD;        // uint64 [N]: the rows' words of the tree
     static constexpr int POS = WORDS + 8 * N;               // int [N]: their positions
-    static constexpr int REF = POS + 4 * N;                 // float [N]: references
-    static constexpr int LIMIT = REF + 4 * N;               // what a score passes to move them
-    static constexpr int MINUS = LIMIT + 4 * N;             // what is added to a score
-    static constexpr int FACTOR = MINUS + 4 * N;            // of the sums, when they move
-    static constexpr int PARTS = FACTOR + 4 * N;            // [4][N]: warps' maxima and sums
-    static constexpr int BARS = PARTS + 16 * N;
-    static constexpr int START = BARS + 16;
-    static constexpr int SIZE = (START + 64 + 1023) / 1024 * 1024;
-    static constexpr int TMEM = GROUPS * SIZE;              // tensor-memory address
+    static constexpr int MINUS = POS + 4 * N;               // float [N]: their references, negated
+    static constexpr int PARTS = MINUS + 4 * N;             // [4][N]: warps' maxima and sums; factors
+    static constexpr int BARS = PARTS + 16 * N;             // scores, output, keys, values [2]
+    static constexpr int THERE = BARS + 40;                 // chunks that exist: keys, values [2]
+    static constexpr int START = THERE + 16;
+    static constexpr int MORE = (START + 64 + 127) / 128 * 128;
+    static constexpr int TMEM = GROUPS * (SIZE + MORE);     // tensor-memory address
     static constexpr int BYTES = TMEM + 16;
     // a group's tensor memory columns
     static constexpr uint32_t K_COL = 0, S_COL = D / 2, O_COL = S_COL + N, COLUMNS = O_COL + N;
     static constexpr int SLOT = N * (D + 3);                // floats of one partial result
-    static_assert(INFO % 16 == 0 && BARS % 8 == 0 && START % 8 == 0 && sizeof(Start) <= 64, "layout");
-    static_assert(BYTES <= 227 * 1024 && GROUPS * COLUMNS <= 512 && N <= 64, "room");
+    static_assert(SIZE % 1024 == 0 && BARS % 8 == 0 && START % 8 == 0 && sizeof(Start) <= 64, "layout");
+    static_assert(BYTES <= 227 * 1024 && GROUPS * COLUMNS <= 512, "room");
 };
+
+// `bytes` of global memory to shared memory.
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void load16(uint32_t at, uint32_t* r)
+{
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t load4(uint32_t at)
+{
+    uint32_t r;
+    asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(r) : "r"(at) : "memory");
+    return r;
+}
 
 // Whether any of the group's threads says so; all of them meet here.
 __device__ __forceinline__ bool any_of_group(int bar, bool mine)
@@ -100,17 +131,18 @@ __global__ void __launch_bounds__(Geo4<D, N>::THREADS, 1)
     extern __shared__ __align__(1024) unsigned char smem_all[];
     const int tid = threadIdx.x, group = tid >> 7, row = tid & 127, warp = (tid >> 5) & 3, lane = tid & 31;
     unsigned char* smem = smem_all + group * G::SIZE;
-    const uint32_t sbase = smem_u32(smem);
-    const uint32_t s_full = sbase + G::BARS, o_done = s_full + 8;
+    unsigned char* more = smem_all + G::GROUPS * G::SIZE + group * G::MORE;
+    const uint32_t sbase = smem_u32(smem), mbase = smem_u32(more);
+    const uint32_t s_full = mbase + G::BARS, o_done = s_full + 8, k_full = s_full + 16, v_full = s_full + 24;
     uint32_t& tmem_slot = *reinterpret_cast<uint32_t*>(smem_all + G::TMEM);
-    Start* start = reinterpret_cast<Start*>(smem + G::START);
+    Start* start = reinterpret_cast<Start*>(more + G::START);
     // shares go to the SMs first, then to their groups
     const int share = group * gridDim.x + blockIdx.x;
     const int bar = 1 + group;
 
     if (row == 0) {
-        mbar_init(s_full, 1);
-        mbar_init(o_done, 1);
+        for (int i = 0; i < 3 + G::VST; ++i)
+            mbar_init(s_full + 8 * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     if (tid < 32) {
@@ -126,20 +158,26 @@ __global__ void __launch_bounds__(Geo4<D, N>::THREADS, 1)
         find_start<S>(p, lane, gridDim.x * G::GROUPS, kMinUnits, share, start);
     __syncthreads();
     tc_fence_after();
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem_slot, 0) + group * G::COLUMNS;
-    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    // (all 512 columns are this CTA's, so they begin at 0)
+    const uint32_t tm = group * G::COLUMNS, lanes = (uint32_t)(warp * 32) << 16;
     const uint32_t k_at = tm + lanes + G::K_COL, s_at = tm + lanes + G::S_COL, o_at = tm + lanes + G::O_COL;
     bool ok = true;
 
     if (share < start->ctas) {
-        uint64_t* words = reinterpret_cast<uint64_t*>(smem + G::WORDS);
-        int* pos = reinterpret_cast<int*>(smem + G::POS);
-        float* ref = reinterpret_cast<float*>(smem + G::REF);
-        float* limit = reinterpret_cast<float*>(smem + G::LIMIT);
-        float* minus = reinterpret_cast<float*>(smem + G::MINUS);
-        float* factor = reinterpret_cast<float*>(smem + G::FACTOR);
-        float* parts = reinterpret_cast<float*>(smem + G::PARTS);
-        const int cs = kv4::chunk_shift(p.kv), slot_mask = (1 << p.kv.page_shift) - 1, chunk_mask = (1 << cs) - 1;
+        uint64_t* words = reinterpret_cast<uint64_t*>(more + G::WORDS);
+        int* pos = reinterpret_cast<int*>(more + G::POS);
+        float* minus = reinterpret_cast<float*>(more + G::MINUS);
+        float* parts = reinterpret_cast<float*>(more + G::PARTS);
+        const int cs = kv4::chunk_shift(p.kv), page_mask = (1 << p.kv.page_shift) - 1;
+        const int64_t page_bytes = kv4::page_bytes(p.kv);
+        // where this key is held: its chunk of the block, its first row of codes and its first pair
+        const int chunk = row >> cs, first = ((chunk * (D / 64) - chunk) << cs) + row;
+        const uint32_t codes = mbase + first * 32, pairs = mbase + G::CODES + first * 4;
+        // Its rows of V and of P, with the chunk 0 of their swizzles.  (Of V's codes the half
+        // goes first that leaves the lanes' banks apart.)
+        const int turn = (row >> 2) & 1;
+        const uint32_t v_row = sbase + G::V + row * 128 + (((row & 7) ^ (turn << 2)) << 4);
+        const uint32_t p_row = sbase + G::P + row * 32 + (turn << 4);
         // scores are c times the products; a scale of zero clears Q
         const float c = p.scale_log2 == 0.f ? 1.f : p.scale_log2;
         const float hidden = c < 0.f ? INFINITY : -INFINITY;
@@ -147,32 +185,85 @@ __global__ void __launch_bounds__(Geo4<D, N>::THREADS, 1)
             if (ok)
                 ok = mbar_wait(b, parity, p.wait_limit);
         };
+        // The products, issued by a warp of the group: with the group as a constant every operand
+        // is one, too (in registers of the threads' own they took some 130 instructions a
+        // product, for which the other warps waited).
+        const uint32_t sall = smem_u32(smem_all), mall = sall + G::GROUPS * G::SIZE;
+        auto score = [&] {                                       // S^T = K Q^T
+            tc_fence_after();
+#pragma unroll
+            for (int g = 0; g < G::GROUPS; ++g)
+                if (group == g) {
+                    const uint64_t b = desc128(sall + g * G::SIZE + G::Q, 0);
+#pragma unroll
+                    for (int h = 0; h < D / 64; ++h)
+                        mma4_tk(g * G::COLUMNS + G::S_COL, g * G::COLUMNS + G::K_COL + h * 32, b + h * (G::QHALF >> 4),
+                                idesc<DT>(N, false), h > 0);
+                    commit(mall + g * G::MORE + G::BARS);
+                }
+        };
+        auto value = [&](bool more) {                            // O^T (+)= V^T P^T
+            tc_fence_after();
+#pragma unroll
+            for (int g = 0; g < G::GROUPS; ++g)
+                if (group == g) {
+                    // (heads of 64 elements: the rows past them are what lies behind V, and not used)
+                    const uint64_t a = desc128(sall + g * G::SIZE + G::V, G::HALF),
+                                   b = desc32(sall + g * G::SIZE + G::P, G::PCHUNK);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)                  // 64 keys at a time
+                        mma4_rr(g * G::COLUMNS + G::O_COL, a + h * 512, b + h * 128, idesc<DT>(N, true, true),
+                                more || h > 0);
+                    commit(mall + g * G::MORE + G::BARS + 8);
+                }
+        };
         Walk<S> w(p, *start, share);
         int n = 0;                                               // blocks so far
+        int asked_k = 0, asked_v = 0;                            // copies so far (warp 3)
         while (w.next()) {
-            const int rows = w.x.rows, nb = w.b_last - w.b_first;
+            const int rows = w.x.rows, nb = w.b_last - w.b_first, n0 = n;
             const int* table = p.batch.block_table + (int64_t)w.r * p.batch.table_stride;
-            // this thread's key of block j of the share, its page (-1: zeros) and its chunk
-            auto key_of = [&](int j) { return w.key0(w.b_first + j) + row; };
-            auto page_of = [&](int j) {
-                const int key = key_of(j);
-                return j < nb && wanted(p, w.x.lo, w.x.hi, key, 1) ? table[key >> p.kv.page_shift] : -1;
+            const uint8_t* base = kv4::chunk(p.kv, 0, w.head, 0);
+            auto key0 = [&](int j) { return w.key0(w.b_first + j); };
+
+            // ---- copies, by warp 3: lanes 2 i and 2 i + 1 have the codes and the pairs of chunk i ----
+            auto page_of = [&](int j) {                          // the chunk's page in block j, -1: none
+                const int key = key0(j) + ((lane >> 1) << cs);
+                const bool in = j < nb && (lane >> 1) << cs < kKeys && wanted(p, w.x.lo, w.x.hi, key, 1 << cs);
+                return in ? table[key >> p.kv.page_shift] : -1;
             };
-            auto chunk_of = [&](int page, int j) -> const uint8_t* {
-                return page < 0 || page >= p.kv.pages ? nullptr
-                                                      : kv4::chunk(p.kv, page, w.head, key_of(j) & slot_mask);
+            auto copy = [&](int which, int j, int page, int& asked) {
+                if (j >= nb || !((unsigned)(n0 + j) < p.first_copies || share > 0))
+                    return;                                      // (the test of the bounded waits)
+                const bool go = page >= 0 && page < p.kv.pages;
+                const unsigned there = __ballot_sync(0xffffffffu, go);
+                const int st = which ? (n0 + j) % G::VST : 0;
+                const uint32_t b = which ? v_full + st * 8 : k_full;
+                const uint32_t size = lane & 1 ? 4 * (D / 64) << cs : 32 * (D / 64) << cs;
+                if (lane == 0) {
+                    reinterpret_cast<uint32_t*>(more + G::THERE)[which + st] = there;
+                    mbar_expect_tx(b, (__popc(there) / 2) * (36 * (D / 64) << cs));
+                }
+                __syncwarp();
+                if (go) {
+                    const int s = (key0(j) + ((lane >> 1) << cs)) & page_mask;
+                    const uint8_t* src = base + page * page_bytes + (s >> cs) * (kv4::slot_bytes(D) << cs) +
+                                         (lane & 1 ? (D << cs) : 0) + which * size;
+                    const uint32_t dst = mbase + (which ? G::VHELD + st * G::HELD : G::KHELD) +
+                                         (lane & 1 ? G::CODES : 0) + (lane >> 1) * size;
+                    bulk_copy(dst, src, size, b);
+                }
+                ++asked;
             };
-            kv4::Held<D> k, v;
-            int page1;                                           // of the next block
-            {
-                const int page0 = page_of(0);
+            int page0 = -1, page1 = -1, page2 = -1;              // of the next blocks
+            if (warp == 3) {
+                page0 = page_of(0);
                 page1 = page_of(1);
-                const uint8_t* at = chunk_of(page0, 0);
-                const int s = key_of(0) & chunk_mask;
-                k.load(at, 0, s, cs);
-                v.load(at, 1, s, cs);
+                copy(0, 0, page0, asked_k);
+                copy(1, 0, page0, asked_v);
             }
-            // the queries, and what the rows see
+
+            // ---- the queries, and what the rows see ----
             for (int i = row; i < rows * (D / 8); i += 128) {
                 const int r = i / (D / 8), ch = i % (D / 8), qrow = w.x.row0 + r;
                 const int t = token_of(p, qrow);
@@ -181,7 +272,7 @@ __global__ void __launch_bounds__(Geo4<D, N>::THREADS, 1)
                 uint4 x = make_uint4(0u, 0u, 0u, 0u);
                 if (p.scale_log2 == 0.f) {
                 } else if (p.q_wide) {
-                    x = __ldg(reinterpret_cast<const uint4*>(src));
+                    x = *reinterpret_cast<const uint4*>(src);
                 } else {
                     uint32_t e[4];
 #pragma unroll
@@ -197,176 +288,265 @@ __global__ void __launch_bounds__(Geo4<D, N>::THREADS, 1)
                 const int i = token_of(p, w.x.row0 + row);
                 pos[row] = row < rows ? w.q.first + i : INT_MIN / 2;
                 words[row] = row < rows && p.tree ? p.tree[w.q.q0 + i] : 0;
-                ref[row] = limit[row] = -INFINITY;
-                minus[row] = 0.f;
+                minus[row] = kNone;
             }
-            float x[N];                                          // this key's share of the rows' sums
+            float2 x[N / 2];                                     // this key's share of the rows' sums
 #pragma unroll
-            for (int r = 0; r < N; ++r)
-                x[r] = 0.f;
+            for (int r = 0; r < N / 2; ++r)
+                x[r] = make_float2(0.f, 0.f);
             // keys below `open_lo` or at `open_hi` and past are hidden from some row
             const int open_hi = p.tree ? min(w.q.keys, w.q.first)
                                        : min(w.q.keys, w.q.first + token_of(p, w.x.row0) + 1);
             const int open_lo =
                 p.window > 0 ? w.q.first + token_of(p, w.x.row0 + rows - 1) - p.window + 1 : 0;
+            if (warp == 3)
+                page2 = page_of(2);
 
-            for (int j = 0; j < nb; ++j, ++n) {
-                const int key = key_of(j), page2 = page_of(j + 2);
-                const bool masked = key - row + kKeys > open_hi || key - row < open_lo;
-                const uint8_t* next = chunk_of(page1, j + 1);
-                const int next_s = key_of(j + 1) & chunk_mask;
-                page1 = page2;
-                // ---- the key ----
+            // Whether block j's key (value) of this thread exists; slots past the context hold anything.
+            auto there = [&](int which, int j) {
+                const uint32_t mask = load4(mbase + G::THERE + 4 * which);
+                return ((mask >> (2 * chunk)) & 1) && key0(j) + row < w.x.hi;
+            };
+            // Block j's key to tensor memory, and its scores asked for.
+            auto key_in = [&](int j) {
+                wait(k_full, (uint32_t)((n0 + j) & 1));
+                const bool is = there(0, j);
 #pragma unroll
                 for (int part = 0; part < D / 64; ++part) {
-                    const uint32_t sc = kv4::both_scales(k.scales[part]), bi = kv4::both_biases(k.scales[part]);
-                    uint32_t e[32];
+                    const uint32_t sb = is ? load4(pairs + G::KHELD + (part * 4 << cs)) : 0u;
+                    const uint32_t sc = kv4::both_scales(sb), bi = kv4::both_biases(sb);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        kv4::expand<DT>(k.codes[part][i], sc, bi, reinterpret_cast<uint32_t(&)[4]>(e[4 * i]));
-                    tmem_st32(k_at + part * 32, e);
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t held[4], e[16];
+                        load16(codes + G::KHELD + (part * 32 << cs) + h * 16, held);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            kv4::expand<DT>(held[i], sc, bi, reinterpret_cast<uint32_t(&)[4]>(e[4 * i]));
+                        tmem_st16(k_at + part * 32 + h * 16, e);
+                    }
                 }
-                k.load(next, 0, next_s, cs);
                 tmem_wait_st();
                 tc_fence_before();
-                named_bar_sync(bar, 128);
-                // (the test of the bounded waits leaves the product out)
-                if (warp == 0 && ((unsigned)n < p.first_copies || share > 0)) {
-                    tc_fence_after();
-                    const uint64_t b = desc128(sbase + G::Q, 0);
-#pragma unroll
-                    for (int h = 0; h < D / 64; ++h)
-                        mma4_tk(tm + G::S_COL, tm + G::K_COL + h * 32, b + h * (G::QHALF >> 4), idesc<DT>(N, false),
-                                h > 0);
-                    commit(s_full);
-                }
-                // ---- the value, when the last block's has been used ----
-                if (n > 0)
-                    wait(o_done, (uint32_t)((n - 1) & 1));
+                named_bar_sync(bar, 128);                        // K is read and in
+                if (warp == 0)
+                    score();
+            };
+            // Its value to shared memory, when the last block's has been used.
+            auto value_in = [&](int j) {
+                if (n0 + j > 0)
+                    wait(o_done, (uint32_t)((n0 + j - 1) & 1));
+                const int st = (n0 + j) % G::VST;
+                wait(v_full + st * 8, (uint32_t)(((n0 + j) / G::VST) & 1));
+                const bool is = there(1 + st, j);
+                const uint32_t at = G::VHELD + st * G::HELD;
 #pragma unroll
                 for (int part = 0; part < D / 64; ++part) {
-                    const uint32_t sc = kv4::both_scales(v.scales[part]), bi = kv4::both_biases(v.scales[part]);
+                    const uint32_t sb = is ? load4(pairs + at + (part * 4 << cs)) : 0u;
+                    const uint32_t sc = kv4::both_scales(sb), bi = kv4::both_biases(sb);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        uint32_t e[4];
-                        kv4::expand<DT>(v.codes[part][i], sc, bi, e);
-                        *reinterpret_cast<uint4*>(smem + G::V + part * G::HALF + row * 128 + ((i ^ (row & 7)) << 4)) =
-                            make_uint4(e[0], e[1], e[2], e[3]);
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t held[4];
+                        load16((codes + at + (part * 32 << cs)) ^ ((turn ^ h) << 4), held);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t e[4];
+                            kv4::expand<DT>(held[i], sc, bi, e);
+                            store16((v_row ^ ((4 * h + i) << 4)) + part * G::HALF, e);
+                        }
                     }
                 }
-                v.load(next, 1, next_s, cs);
-                // ---- the key's scores, 16 rows at a time ----
-                wait(s_full, (uint32_t)(n & 1));
-                tc_fence_after();
-                float t[16];
-                auto scores = [&](int ch) {
-                    tmem_ld16(s_at + ch * 16, t);
-                    tmem_wait_ld();
-                    if (masked) {
+            };
+            float t[16];
+            // scores of 16 rows
+            auto scores = [&](int ch, int k0) {
+                tmem_ld16(s_at + ch * 16, t);
+                tmem_wait_ld();
+                if (k0 + kKeys > open_hi || k0 < open_lo) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (!sees(p, w.q, pos[ch * 16 + i], words[ch * 16 + i], key))
-                                t[i] = hidden;
-                    }
-                };
-                bool over = false;
-#pragma unroll
-                for (int ch = 0; ch < CH; ++ch)
-                    if (ch * 16 < rows) {
-                        scores(ch);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            over = over || (ch * 16 + i < rows && t[i] * c > limit[ch * 16 + i]);
-                    }
-                if (any_of_group(bar, over)) {
-                    // some reference moves: the block's maxima
-#pragma unroll
-                    for (int ch = 0; ch < CH; ++ch)
-                        if (ch * 16 < rows) {
-                            if (CH > 1)
-                                scores(ch);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const float top = warp_max(t[i] * c);
-                                if (lane == 0)
-                                    parts[warp * N + ch * 16 + i] = top;
-                            }
-                        }
-                    named_bar_sync(bar, 128);
-                    if (row < rows) {
-                        const float* q = parts + row;
-                        const float top = fmaxf(fmaxf(q[0], q[N]), fmaxf(q[2 * N], q[3 * N]));
-                        float f = 1.f;
-                        if (top > limit[row]) {                  // also from -inf
-                            f = ex2(ref[row] - top);
-                            ref[row] = top;
-                            limit[row] = top + 8.f;
-                            minus[row] = -top;
-                        }
-                        factor[row] = f;
-                    }
-                    named_bar_sync(bar, 128);
-#pragma unroll
-                    for (int ch = 0; ch < CH; ++ch)
-                        if (ch * 16 < rows) {
-                            float o[16];
-                            if (j > 0) {
-                                tmem_ld16(o_at + ch * 16, o);
-                                tmem_wait_ld();
-                            }
-                            uint32_t r[16];
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const float f = ch * 16 + i < rows ? factor[ch * 16 + i] : 1.f;
-                                x[ch * 16 + i] *= f;
-                                r[i] = __float_as_uint(o[i] * f);
-                            }
-                            if (j > 0)
-                                tmem_st16(o_at + ch * 16, r);
-                        }
-                    tmem_wait_st();
+                    for (int i = 0; i < 16; ++i)
+                        if (!sees(p, w.q, pos[ch * 16 + i], words[ch * 16 + i], k0 + row))
+                            t[i] = hidden;
                 }
+            };
+            // exponents of two of the chunk's rows, and the largest of those of 8 rows
+            auto exponents = [&](int ch, int at) {
+                return fma2(make_float2(t[at], t[at + 1]), make_float2(c, c),
+                            *reinterpret_cast<const float2*>(minus + ch * 16 + at));
+            };
+            auto larger = [&](float top, float2 e, int r) {
+                if (r < rows)
+                    top = fmaxf(top, e.x);
+                if (r + 1 < rows)
+                    top = fmaxf(top, e.y);
+                return top;
+            };
+            // Probabilities of 8 rows from h * 8 on of the chunk, kept and as a part of the key's row
+            // of P; the largest of their exponents.
+            float2 weight[CH == 1 ? 8 : 4];
+            auto weigh = [&](int ch, int h) {
+                float top = -INFINITY;
+                uint32_t r[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 e = exponents(ch, h * 8 + 2 * i);
+                    top = larger(top, e, ch * 16 + h * 8 + 2 * i);
+                    float2& y = weight[(CH == 1 ? h * 4 : 0) + i];
+                    y = make_float2(ex2(e.x), ex2(e.y));
+                    r[i] = pack2<DT>(y.x, y.y);
+                }
+                store16((p_row ^ (h << 4)) + ch * G::PCHUNK, r);
+                return top;
+            };
+            auto add = [&](int ch, int h) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x[ch * 8 + h * 4 + i] = add2(x[ch * 8 + h * 4 + i], weight[(CH == 1 ? h * 4 : 0) + i]);
+            };
+            // Moves the references that the block's maxima pass by more than 8, and the sums with
+            // them.  (Of more than a chunk the scores are in tensor memory still.)
+            auto move = [&](int j) {
 #pragma unroll
                 for (int ch = 0; ch < CH; ++ch)
                     if (ch * 16 < rows) {
                         if (CH > 1)
-                            scores(ch);
+                            scores(ch, key0(j));
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            if (ch * 16 + h * 8 < rows) {
-                                uint32_t r[4];
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const int at = h * 8 + 2 * i;
-                                    const float a = ex2(fmaf(t[at], c, minus[ch * 16 + at]));
-                                    const float b = ex2(fmaf(t[at + 1], c, minus[ch * 16 + at + 1]));
-                                    x[ch * 16 + at] += a;
-                                    x[ch * 16 + at + 1] += b;
-                                    r[i] = pack2<DT>(a, b);
-                                }
-                                *reinterpret_cast<uint4*>(smem + G::P + row * 128 + (((ch * 2 + h) ^ (row & 7)) << 4)) =
-                                    make_uint4(r[0], r[1], r[2], r[3]);
-                            }
+                        for (int i = 0; i < 16; ++i) {
+                            const float most = warp_max(t[i] * c);
+                            if (lane == 0)
+                                parts[warp * N + ch * 16 + i] = most;
+                        }
                     }
-                fence_proxy_async_smem();
-                tc_fence_before();
                 named_bar_sync(bar, 128);
-                if (warp == 0) {
-                    tc_fence_after();
-                    // (heads of 64 elements: the rows past them are P's, and not used)
-                    const uint64_t a = desc128(sbase + G::V, G::HALF), b = desc128(sbase + G::P, G::HALF);
+                if (row < rows) {
+                    float* q = parts + row;
+                    const float most = fmaxf(fmaxf(q[0], q[N]), fmaxf(q[2 * N], q[3 * N]));
+                    float f = 1.f;
+                    if (most + minus[row] > 8.f) {
+                        f = ex2(-minus[row] - most);
+                        minus[row] = -most;
+                    }
+                    q[0] = f;                                    // the factor of the row's sums
+                }
+                named_bar_sync(bar, 128);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)                  // 64 keys at a time
-                        mma4_rr(tm + G::O_COL, a + h * 512, b + h * 512, idesc<DT>(N, true, true), j > 0 || h > 0);
-                    commit(o_done);
+                for (int ch = 0; ch < CH; ++ch)
+                    if (ch * 16 < rows) {
+                        float o[16];
+                        if (j > 0) {
+                            tmem_ld16(o_at + ch * 16, o);
+                            tmem_wait_ld();
+                        }
+                        uint32_t r[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float f = ch * 16 + i < rows ? parts[ch * 16 + i] : 1.f;
+                            (i & 1 ? x[ch * 8 + i / 2].y : x[ch * 8 + i / 2].x) *= f;
+                            r[i] = __float_as_uint(o[i] * f);
+                        }
+                        if (j > 0)
+                            tmem_st16(o_at + ch * 16, r);
+                    }
+                tmem_wait_st();
+            };
+
+            if (CH == 1) {
+                // A block's scores are computed while the block before it is weighed: they stay
+                // in registers, and the next key takes their place.
+#pragma unroll 1
+                for (int j = -1; j < nb; ++j) {
+                    if (j >= 0) {
+                        wait(s_full, (uint32_t)((n0 + j) & 1));
+                        tc_fence_after();
+                        scores(0, key0(j));
+                    }
+                    if (j + 1 < nb) {
+                        key_in(j + 1);
+                        if (warp == 3) {
+                            copy(0, j + 2, page1, asked_k);
+                            if (j >= 0)                          // its stage's last use is over
+                                copy(1, j + 1, page0, asked_v);
+                            page0 = page1;
+                            page1 = page2;
+                            page2 = page_of(j + 4);
+                        }
+                    }
+                    if (j < 0)
+                        continue;
+                    value_in(j);
+                    float top = weigh(0, 0);
+                    if (rows > 8)
+                        top = fmaxf(top, weigh(0, 1));
+                    fence_proxy_async_smem();
+                    tc_fence_before();
+                    if (any_of_group(bar, top > 8.f)) {
+                        move(j);
+                        weigh(0, 0);
+                        if (rows > 8)
+                            weigh(0, 1);
+                        fence_proxy_async_smem();
+                        tc_fence_before();
+                        named_bar_sync(bar, 128);
+                    }
+                    add(0, 0);
+                    if (rows > 8)
+                        add(0, 1);
+                    if (warp == 1)
+                        value(j > 0);
+                }
+            } else {
+                // of more rows the scores stay in tensor memory: their exponents are looked at, and
+                // then weighed
+#pragma unroll 1
+                for (int j = 0; j < nb; ++j) {
+                    key_in(j);
+                    if (warp == 3)
+                        copy(0, j + 1, page1, asked_k);
+                    value_in(j);
+                    wait(s_full, (uint32_t)((n0 + j) & 1));
+                    tc_fence_after();
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int ch = 0; ch < CH; ++ch)
+                        if (ch * 16 < rows) {
+                            scores(ch, key0(j));
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                top = larger(top, exponents(ch, 2 * i), ch * 16 + 2 * i);
+                        }
+                    const bool moved = any_of_group(bar, top > 8.f);
+                    if (warp == 3) {                             // V is read
+                        copy(1, j + 1, page1, asked_v);
+                        page1 = page2;
+                        page2 = page_of(j + 3);
+                    }
+                    if (moved)
+                        move(j);
+#pragma unroll
+                    for (int ch = 0; ch < CH; ++ch)
+                        if (ch * 16 < rows) {
+                            scores(ch, key0(j));
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                if (ch * 16 + h * 8 < rows) {
+                                    weigh(ch, h);
+                                    add(ch, h);
+                                }
+                        }
+                    fence_proxy_async_smem();
+                    tc_fence_before();
+                    named_bar_sync(bar, 128);
+                    if (warp == 1)
+                        value(j > 0);
                 }
             }
+            n += nb;
 
             // ---- the item's result: a thread has an element of every row ----
 #pragma unroll
             for (int r = 0; r < N; ++r)
                 if (r < rows) {
-                    float s = x[r];
+                    float s = r & 1 ? x[r / 2].y : x[r / 2].x;
 #pragma unroll
                     for (int d = 16; d > 0; d >>= 1)
                         s += __shfl_xor_sync(0xffffffffu, s, d);
@@ -406,12 +586,12 @@ __global__ void __launch_bounds__(Geo4<D, N>::THREADS, 1)
             if (row < rows) {
                 const float s = sum_of(row);
                 if (!whole) {
-                    slot[N * D + row] = ref[row];
+                    slot[N * D + row] = -minus[row];
                     slot[N * (D + 1) + row] = slot[N * (D + 2) + row] = s;
                 } else if (p.lse) {
                     const int qrow = w.x.row0 + row, tok = token_of(p, qrow);
                     p.lse[(int64_t)(w.q.q0 + tok) * p.heads + w.head * p.group + qrow - tok * p.group] =
-                        lse_of(ref[row], s);
+                        lse_of(-minus[row], s);
                 }
             }
             if (!whole && row == 0 && c0 == share)
@@ -419,9 +599,17 @@ __global__ void __launch_bounds__(Geo4<D, N>::THREADS, 1)
             tc_fence_before();
             named_bar_sync(bar, 128);                            // what the rows need has been read
         }
-        // the last product ends before tensor memory goes away, also after a wait that ran out
-        if (n > 0 && !mbar_wait(o_done, (uint32_t)((n - 1) & 1), p.wait_limit))
-            ok = false;
+        // the last products and copies end before tensor and shared memory go away, also after a
+        // wait that ran out
+        bool end = true;
+        if (n > 0)
+            end = mbar_wait(s_full, (uint32_t)((n - 1) & 1), p.wait_limit) &&
+                  mbar_wait(o_done, (uint32_t)((n - 1) & 1), p.wait_limit);
+        if (asked_k > 0)
+            end = mbar_wait(k_full, (uint32_t)((asked_k - 1) & 1), p.wait_limit) && end;
+        for (int i = asked_v - 1; i >= 0 && i >= asked_v - G::VST; --i)
+            end = mbar_wait(v_full + i % G::VST * 8, (uint32_t)((i / G::VST) & 1), p.wait_limit) && end;
+        ok = ok && end;
         if (!ok)
             atomicOr(p.status, 1u);
     }
@@ -448,7 +636,7 @@ cudaError_t launch(const AttendParams& p, int sms, cudaStream_t st)
 template <int DT, int D>
 cudaError_t launch_rows(const AttendParams& p, int sms, cudaStream_t st)
 {
-    return attend_average_rows(p) <= 16 ? launch<DT, D, 16>(p, sms, st) : launch<DT, D, 48>(p, sms, st);
+    return launch<DT, D, 16>(p, sms, st);
 }
 
 }  // namespace

@@ -198,6 +198,13 @@ __device__ __forceinline__ void store32(void* d, const uint32_t* r)
                  : "memory");
 }
 
+// 16 bytes to shared memory.
+__device__ __forceinline__ void store16(uint32_t at, const uint32_t (&r)[4])
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+
 // Stores N 16-bit values (packed in pairs) of an output row, as wide as its
 // address allows.
 template <int N>

@@ -123,7 +123,7 @@ __device__ __forceinline__ void mma4_tk(uint32_t d, uint32_t a, uint64_t b, uint
 }
 
 // The same with both operands in shared memory with their rows along the contracted
-// dimension: 16 rows of each a step.
+// dimension: 16 rows of each a step, of 128 bytes in A and of 32 in B.
 __device__ __forceinline__ void mma4_rr(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add)
 {
     asm volatile(
@@ -132,7 +132,7 @@ __device__ __forceinline__ void mma4_rr(uint32_t d, uint64_t a, uint64_t b, uint
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %2, %6, %9, 1;\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %3, %7, %9, 1;\n"
         " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %4, %8, %9, 1;\n}\n" ::"r"(d), "l"(a), "l"(a + 128),
-        "l"(a + 256), "l"(a + 384), "l"(b), "l"(b + 128), "l"(b + 256), "l"(b + 384), "r"(idesc), "r"(add)
+        "l"(a + 256), "l"(a + 384), "l"(b), "l"(b + 32), "l"(b + 64), "l"(b + 96), "r"(idesc), "r"(add)
         : "memory");
 }
 
@@ -154,12 +154,40 @@ __device__ __forceinline__ uint64_t desc128(uint32_t addr, uint32_t lead)
            ((uint64_t)(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
+// The same for rows of 32 bytes (16 elements) along the contracted dimension, swizzled
+// within 256 bytes: 8-row groups 256 bytes apart, 16-element column groups `lead` bytes.
+__device__ __forceinline__ uint64_t desc32(uint32_t addr, uint32_t lead)
+{
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lead >> 4) & 0x3FFFu) << 16) |
+           ((uint64_t)(256u >> 4) << 32) | (1ull << 46) | (6ull << 61);
+}
+
 // kind::f16, fp32 sums, M = 128; bits 15 and 16: A is M-major, B is N-major.
 template <int DT>
 __host__ __device__ constexpr uint32_t idesc(int n, bool b_n_major, bool a_m_major = false)
 {
     return (1u << 4) | ((uint32_t)a_m_major << 15) | ((uint32_t)(DT == LBV_BF16) << 7) | ((uint32_t)(DT == LBV_BF16) << 10) |
            ((uint32_t)b_n_major << 16) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+          "l"(reinterpret_cast<uint64_t&>(c)));
+    return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;\n"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return d;
 }
 
 }  // namespace att

@@ -101,26 +101,6 @@ struct Geo {
     static_assert(BYTES <= 227 * 1024 && sizeof(Start) <= 2 * kTile * 8, "shared memory");
 };
 
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
-{
-    float2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;\n"
-        : "=l"(reinterpret_cast<uint64_t&>(d))
-        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
-          "l"(reinterpret_cast<uint64_t&>(c)));
-    return d;
-}
-
-__device__ __forceinline__ float2 add2(float2 a, float2 b)
-{
-    float2 d;
-    asm("add.rn.f32x2 %0, %1, %2;\n"
-        : "=l"(reinterpret_cast<uint64_t&>(d))
-        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
-    return d;
-}
-
 // Stores row `row` of a request and kv head (zeros if it is not `in` the item) as
 // row `trow` of a Q tile at `tile`, in the layout of the copies.
 template <int D>
@@ -183,17 +163,16 @@ __device__ __forceinline__ void fetch_q(const AttendParams& p, int q0, int kv_he
 // The values of a row as it is held to row `row` of a slot at `dst`, in the layout of the
 // copies.
 template <int DT, int D>
-__device__ __forceinline__ void expand_row(const kv4::Held<D>& h, unsigned char* dst, int row)
+__device__ __forceinline__ void expand_row(const kv4::Held<D>& h, uint32_t dst, int row)
 {
 #pragma unroll
     for (int part = 0; part < D / 64; ++part) {
-        const uint32_t s = kv4::both_scales(h.scales[part]), b = kv4::both_biases(h.scales[part]);
-        unsigned char* d = dst + part * Geo<D>::HALF + row * 128;
+        const uint32_t s = kv4::both_scales(h.scales(part)), b = kv4::both_biases(h.scales(part));
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             uint32_t v[4];
             kv4::expand<DT>(h.codes[part][i], s, b, v);
-            *reinterpret_cast<uint4*>(d + ((i ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+            store16(((dst + row * 128 + ((row & 7) << 4)) ^ (i << 4)) + part * Geo<D>::HALF, v);
         }
     }
     fence_proxy_async_smem();
@@ -466,6 +445,7 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
         // ---- a cache of 4 bits: one key of a block a thread, its K and its V in turn ----
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(R::EXPAND));
         const int row = tid & 127, cs = kv4::chunk_shift(p.kv);
+        const int64_t page_bytes = kv4::page_bytes(p.kv);
         int n = 0;                                               // slots filled
         for (int it = 0;; ++it) {
             const Item& w = item_at(it);
@@ -476,9 +456,10 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
                 const int key = w.key_of(j) + row;
                 return j < w.nb && wanted(p, w.lo, w.hi, key, 1) ? table[key >> p.kv.page_shift] : -1;
             };
-            auto slot_at = [&](int j) { return (w.key_of(j) + row) & ((1 << p.kv.page_shift) - 1); };
-            auto chunk_at = [&](int page, int j) -> const uint8_t* {
-                return page < 0 || page >= p.kv.pages ? nullptr : kv4::chunk(p.kv, page, w.head, slot_at(j));
+            const uint8_t* base = kv4::chunk(p.kv, 0, w.head, 0);
+            auto slot_at = [&](int page, int j) {
+                return kv4::slot_of<D>(base, page_bytes, page < p.kv.pages ? page : -1,
+                                       (w.key_of(j) + row) & ((1 << p.kv.page_shift) - 1), cs);
             };
             // Fills the next slot; false if it gave up.
             auto fill = [&](const kv4::Held<D>& h) {
@@ -489,7 +470,7 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
                 if (!ok)
                     return false;
                 ++n;
-                expand_row<DT, D>(h, smem + G::RING + st * G::SLOT, row);
+                expand_row<DT, D>(h, sbase + G::RING + st * G::SLOT, row);
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(full(st));
@@ -498,15 +479,15 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
             // what a thread waits for is asked for while the slot before it is filled: V during
             // K, the next block's K during V, its page a block ahead
             kv4::Held<D> k, v;
-            const uint8_t* c = chunk_at(page_at(0), 0);
-            k.load(c, 0, slot_at(0) & ((1 << cs) - 1), cs);
+            kv4::Slot at = slot_at(page_at(0), 0);
+            k.load(at, 0, cs);
             for (int j = 0; j < w.nb; ++j) {
                 const int next = page_at(j + 1);
-                v.load(c, 1, slot_at(j) & ((1 << cs) - 1), cs);
+                v.load(at, 1, cs);
                 if (!fill(k))
                     break;
-                c = chunk_at(next, j + 1);
-                k.load(c, 0, slot_at(j + 1) & ((1 << cs) - 1), cs);
+                at = slot_at(next, j + 1);
+                k.load(at, 0, cs);
                 if (!fill(v))
                     break;
             }

@@ -65,29 +65,58 @@ __device__ __forceinline__ void load32(const void* src, uint32_t (&r)[8])
                  : "memory");
 }
 
+// A slot of a head: its first row of codes, and its first scale and bias.  A slot that
+// does not exist reads as zeros: its codes are those of any slot, without scales.
+struct Slot {
+    const uint8_t* codes;
+    const uint8_t* scales;
+    bool there;
+};
+
+// Slot s of a page (-1: none) of a head, whose pages begin at `base` + page * page_bytes.
+template <int D>
+__device__ __forceinline__ Slot slot_of(const uint8_t* base, int64_t page_bytes, int page, int s, int cs)
+{
+    Slot x;
+    x.there = page >= 0;
+    const uint8_t* chunk = base + (x.there ? page : 0) * page_bytes + (s >> cs) * (D / 64 * kSlotBytes << cs);
+    s &= (1 << cs) - 1;
+    x.codes = chunk + s * 32;
+    x.scales = chunk + (D << cs) + s * 4;
+    return x;
+}
+
 // A key's or a value's row as it is held.
 template <int D>
 struct Held {
     uint32_t codes[D / 64][8];
-    uint32_t scales[D / 64];
+    uint32_t pairs[D / 64];
+    bool there;
 
-    // The key (which 0) or value (1) of slot s in chunk c; zeros without a chunk.
-    __device__ __forceinline__ void load(const uint8_t* c, int which, int s, int cs)
+    // The key (which 0) or value (1) of a slot.
+    __device__ __forceinline__ void load(const Slot& s, int which, int cs)
     {
 #pragma unroll
         for (int part = 0; part < D / 64; ++part) {
             const int plane = which * (D / 64) + part;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                codes[part][i] = 0;
-            scales[part] = 0;
-            if (c) {
-                load32(c + codes_at(plane, s, cs), codes[part]);
-                scales[part] = *reinterpret_cast<const volatile uint32_t*>(c + scale_at(D / 32, plane, s, cs));
-            }
+            load32(s.codes + (plane * 32 << cs), codes[part]);
+            pairs[part] = *reinterpret_cast<const volatile uint32_t*>(s.scales + (plane * 4 << cs));
         }
+        there = s.there;
     }
+
+    // (scale, bias) of 64 elements.  (Not before they are used: whoever looks at them waits for
+    // the load.)
+    __device__ __forceinline__ uint32_t scales(int part) const { return there ? pairs[part] : 0u; }
 };
+
+// (x & mask) | bits, in one instruction.
+__device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t mask, uint32_t bits)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;\n" : "=r"(r) : "r"(x), "r"(mask), "r"(bits));
+    return r;
+}
 
 // The pairs at the four places of a word w: out[i] = code * scale + bias, rounded once,
 // of the codes in bits 4 i and 4 i + 16 on (of one slot's word elements 2 i and 2 i + 1).
@@ -105,7 +134,7 @@ __device__ __forceinline__ void expand(uint32_t w, uint32_t scale2, uint32_t bia
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const uint32_t x = w >> (8 * i);
-            const uint32_t lo = (x & 0x000F000Fu) | 0x64006400u, hi = (x & 0x00F000F0u) | 0x64006400u;
+            const uint32_t lo = pick(x, 0x000F000Fu, 0x64006400u), hi = pick(x, 0x00F000F0u, 0x64006400u);
             const __half2 a = __hadd2(reinterpret_cast<const __half2&>(lo), one);
             const __half2 c = __hfma2(reinterpret_cast<const __half2&>(hi), sixteenth, many);
             reinterpret_cast<__half2&>(out[2 * i]) = __hfma2(a, s, b);
@@ -117,7 +146,7 @@ __device__ __forceinline__ void expand(uint32_t w, uint32_t scale2, uint32_t bia
         const __nv_bfloat162 one = __float2bfloat162_rn(-128.f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t lo = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+            const uint32_t lo = pick(w >> (4 * i), 0x000F000Fu, 0x43004300u);
             const __nv_bfloat162 a = __hadd2(reinterpret_cast<const __nv_bfloat162&>(lo), one);
             reinterpret_cast<__nv_bfloat162&>(out[i]) = __hfma2(a, s, b);
         }
