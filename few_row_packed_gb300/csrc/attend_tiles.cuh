@@ -163,7 +163,7 @@ __device__ __forceinline__ void fetch_q(const AttendParams& p, int q0, int kv_he
 // The values of a row as it is held to row `row` of a slot at `dst`, in the layout of the
 // copies.
 template <int DT, int D>
-__device__ __forceinline__ void expand_row(const kv4::Held<D>& h, uint32_t dst, int row)
+__device__ __forceinline__ void expand_row(const kv4::Held<D>& h, const kv4::Constants& c, uint32_t dst, int row)
 {
 #pragma unroll
     for (int part = 0; part < D / 64; ++part) {
@@ -171,7 +171,7 @@ __device__ __forceinline__ void expand_row(const kv4::Held<D>& h, uint32_t dst, 
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             uint32_t v[4];
-            kv4::expand<DT>(h.codes[part][i], s, b, v);
+            kv4::expand<DT>(h.codes[part][i], s, b, c, v);
             store16(((dst + row * 128 + ((row & 7) << 4)) ^ (i << 4)) + part * Geo<D>::HALF, v);
         }
     }
@@ -446,6 +446,7 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(R::EXPAND));
         const int row = tid & 127, cs = kv4::chunk_shift(p.kv);
         const int64_t page_bytes = kv4::page_bytes(p.kv);
+        const kv4::Constants constants = kv4::constants<DT>();
         int n = 0;                                               // slots filled
         for (int it = 0;; ++it) {
             const Item& w = item_at(it);
@@ -470,7 +471,7 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
                 if (!ok)
                     return false;
                 ++n;
-                expand_row<DT, D>(h, sbase + G::RING + st * G::SLOT, row);
+                expand_row<DT, D>(h, constants, sbase + G::RING + st * G::SLOT, row);
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(full(st));

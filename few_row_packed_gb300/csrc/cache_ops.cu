@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(kThreads) lbv_kv_read_kernel(const __grid_cons
                 const uint32_t w =
                     *reinterpret_cast<const uint32_t*>(c + kv4::codes_at(plane, s, cs) + ((at >> 3) & 7) * 4);
                 uint32_t x[4];
-                kv4::expand<DT>(w, kv4::both_scales(sb), kv4::both_biases(sb), x);
+                kv4::expand<DT>(w, kv4::both_scales(sb), kv4::both_biases(sb), kv4::constants<DT>(), x);
                 v = make_uint4(x[0], x[1], x[2], x[3]);
             } else {
                 const uint16_t* src = (which ? p.kv.v : p.kv.k) + page * p.kv.page_stride +

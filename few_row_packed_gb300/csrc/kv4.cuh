@@ -111,11 +111,27 @@ struct Held {
 };
 
 // (x & mask) | bits, in one instruction.
-__device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t mask, uint32_t bits)
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t bits)
 {
     uint32_t r;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;\n" : "=r"(r) : "r"(x), "r"(mask), "r"(bits));
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;\n" : "=r"(r) : "r"(x), "n"(MASK), "r"(bits));
     return r;
+}
+
+// Constants of expand() that an instruction cannot hold beside another: kept in registers, by a
+// kernel that makes them once.  (Left to the compiler they were made anew for every word.)
+struct Constants {
+    uint32_t bits, many;
+};
+
+template <int DT>
+__device__ __forceinline__ Constants constants()
+{
+    Constants c;
+    asm volatile("mov.b32 %0, %1;\n" : "=r"(c.bits) : "n"(DT == LBV_F16 ? 0x64006400 : 0x43004300));
+    asm volatile("mov.b32 %0, %1;\n" : "=r"(c.many) : "n"(0xD400D400));      // -64, -64
+    return c;
 }
 
 // The pairs at the four places of a word w: out[i] = code * scale + bias, rounded once,
@@ -125,16 +141,17 @@ __device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t mask, uint32_t bit
 // instruction; the subtraction of that number is exact.  (fp16 has room for the code four bits
 // up, too: 1024 + 16 c, so a shift serves two pairs.)
 template <int DT>
-__device__ __forceinline__ void expand(uint32_t w, uint32_t scale2, uint32_t bias2, uint32_t (&out)[4])
+__device__ __forceinline__ void expand(uint32_t w, uint32_t scale2, uint32_t bias2, const Constants& k,
+                                       uint32_t (&out)[4])
 {
     if constexpr (DT == LBV_F16) {
         const __half2 s = reinterpret_cast<const __half2&>(scale2), b = reinterpret_cast<const __half2&>(bias2);
-        const __half2 one = __float2half2_rn(-1024.f), sixteenth = __float2half2_rn(0.0625f),
-                      many = __float2half2_rn(-64.f);
+        const __half2 many = reinterpret_cast<const __half2&>(k.many);
+        const __half2 one = __float2half2_rn(-1024.f), sixteenth = __float2half2_rn(0.0625f);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const uint32_t x = w >> (8 * i);
-            const uint32_t lo = pick(x, 0x000F000Fu, 0x64006400u), hi = pick(x, 0x00F000F0u, 0x64006400u);
+            const uint32_t lo = pick<0x000F000Fu>(x, k.bits), hi = pick<0x00F000F0u>(x, k.bits);
             const __half2 a = __hadd2(reinterpret_cast<const __half2&>(lo), one);
             const __half2 c = __hfma2(reinterpret_cast<const __half2&>(hi), sixteenth, many);
             reinterpret_cast<__half2&>(out[2 * i]) = __hfma2(a, s, b);
@@ -146,7 +163,7 @@ __device__ __forceinline__ void expand(uint32_t w, uint32_t scale2, uint32_t bia
         const __nv_bfloat162 one = __float2bfloat162_rn(-128.f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t lo = pick(w >> (4 * i), 0x000F000Fu, 0x43004300u);
+            const uint32_t lo = pick<0x000F000Fu>(w >> (4 * i), k.bits);
             const __nv_bfloat162 a = __hadd2(reinterpret_cast<const __nv_bfloat162&>(lo), one);
             reinterpret_cast<__nv_bfloat162&>(out[i]) = __hfma2(a, s, b);
         }
