@@ -2,23 +2,25 @@
 // decoding, verify calls, trees of drafted tokens).
 //
 // The sums of attend_rows.cu.  A quarter of the bytes leaves a quarter of the time for
-// everything else, so the products are turned around: keys are the 128 rows of the
-// tensor core's tile and the queries, a few, its columns,
-//     S^T = K Q^T (128 keys x N rows),   O^T += V^T P^T (D x N rows).
-// An MMA's time then goes by its operands' bytes, not by padded rows, and
-//   * two threads have a key, half of its elements and half of the rows each.  They expand
-//     its codes and write it to tensor memory, where the first product takes it from; they
-//     get its scores from there, mask them, take the exponentials, and add them up for
-//     themselves, one sum a row, joined with the other keys' at the item's end;
-//   * they write its values and probabilities to shared memory as a row each, which are
-//     the second product's operands as they are: rows along the contracted dimension.
-// A group of eight such warps does this block by block for a share of its own, with a
-// warp beside it that copies the codes a block ahead (bulk copies: a chunk's keys, values
-// and scales are stretches of memory) and issues the products.  The groups of a CTA
-// have nothing to do with one another but the SM, whose schedulers take one's arithmetic while
-// another waits.  Shares, items and references are those of attend_common.cuh (a reference
-// moves when a score passes it by more than 8); the parts of divided items are added by a
-// launch of their own (attend_join.cu).
+// everything else, so what a key costs in instructions counts: 13 to expand 8 codes, and
+// as little as can be beside them.
+//   * The products are turned around: keys (then elements of a head) are the 16 rows of an
+//     mma.sync tile and the queries its 8 columns,
+//         S^T = K Q^T,   O^T += V^T P^T,
+//     so that 8 rows (a decoded token's query heads) take half the instructions that they
+//     take as rows.  Codes are expanded in the registers of the lane that holds them as an
+//     operand, once for all rows of the item: which element a place of the contraction
+//     stands for is free, so a lane takes 16 neighbours of a key (8 bytes of codes) and, of
+//     a value, the same 8 elements of two keys (two permutes bring them together).  The
+//     probabilities change places by movmatrix.
+//   * A team of four warps has a share of the batch.  A warp has 16 keys of every block and
+//     a running maximum, sums and results of its own: the warps meet at an item's ends alone.
+//   * A warp beside each team finds its items and copies blocks of 64 keys by bulk copies: a
+//     chunk of a head, keys, values and scales, is one stretch of memory.  Keys are dealt to
+//     a tile's rows in an order that leaves the lanes' shared-memory banks apart for keys
+//     and values alike.  It hands most of its registers to the teams.
+// Shares, items and references are those of attend_rows.cu, with a team in place of a CTA; the
+// parts of divided items are added by a launch of their own (attend_join.cu).
 //
 // The divisor adds the probabilities before their rounding to 16 bits (off by 2^-9 of a
 // value for a row that one key dominates; the values themselves are held to 2^-5).
@@ -34,84 +36,53 @@ using namespace att;
 
 namespace {
 
-constexpr int kKeys = 128;                       // keys per block
-constexpr int kTeam = 256;                       // threads of a group, without its warp for copies
-constexpr int kGroups = 3;
-// Units of a block and of an item beside its blocks; the least share of a group.
-constexpr int kBlockUnits = 4, kExtra = 6, kMinUnits = 4;
+constexpr int kBlock = 64;                       // keys per block
+constexpr int kKeyWarps = 4, kTeam = kKeyWarps * 32;
+// Units of an item beside its blocks, and the least share of a team.
+constexpr int kExtra = 3, kMinUnits = 2;
 // A reference that every score passes, negated: nothing has been seen yet.
 constexpr float kNone = 1e30f;
-constexpr int kItems = 4;                        // items known at a time: of three blocks, and one more
+constexpr int kItems = 8;                        // items that a team's warps may be apart: stages, and one
 
-// What a group needs to know of an item.
+// What a team needs to know of an item.
 struct alignas(16) Item {
     int q0, first, keys;   // of its request
-    int row0, rows, head, hi, r;
+    int row0, rows, head;
     int key0, nb;          // its first key and its blocks in this share; 0 blocks: no more items
     int skip, jump;        // keys left out before block `jump` (behind the sinks)
     int c0, c1;            // shares that hold a part of it
-    int unused[2];
-    __device__ int key_of(int j) const { return key0 + j * kKeys + (j >= jump ? skip : 0); }
+    __device__ int key_of(int j) const { return key0 + j * kBlock + (j >= jump ? skip : 0); }
 };
-static_assert(sizeof(Item) == 64, "ring entry");
+static_assert(sizeof(Item) == 48, "ring entry");
 
-// N: rows of an item, 16 or 48.
-template <int D, int N>
-struct Geo4 {
-    static constexpr int VST = N == 16 ? 2 : 1;             // stages of values as they are held
-    static constexpr int THREADS = kGroups * (kTeam + 32);
-    static constexpr int HALF = kKeys * 128;                // 64 elements of 128 keys
-    // a group's operands: V in rows of 128 bytes, P in rows of 16 probabilities, Q
-    static constexpr int V = 0;
-    static constexpr int P = D / 64 * HALF;
-    static constexpr int PCHUNK = kKeys * 32;
-    static constexpr int Q = P + N / 16 * PCHUNK;
-    static constexpr int QHALF = N * 128;
-    static constexpr int SIZE = Q + D / 64 * QHALF;
-    // behind the groups' operands, what else each has: a block's keys and values as they are
-    // held (codes, then scales), and what the rows need
-    static constexpr int CODES = kKeys * 32 * (D / 64), HELD = kKeys * 36 * (D / 64);
-    static constexpr int KHELD = 0;
-    static constexpr int VHELD = HELD;
-    static constexpr int ITEMS = VHELD + VST * HELD;
+// NT: tiles of 8 rows of an item.
+template <int D, int NT>
+struct Geo {
+    static constexpr int ROWS = 8 * NT;
+    // teams on an SM, and registers a thread after the split: 96 * 640 at launch = 104 * 512 +
+    // 64 * 128, 128 * 512 = 152 * 384 + 56 * 128, 168 * 384 = 232 * 256 + 40 * 128
+    static constexpr int TEAMS = NT == 1 ? 4 : NT == 2 ? 3 : 2;
+    static constexpr int REGS = NT == 1 ? 104 : NT == 2 ? 152 : 232, HELPER = NT == 1 ? 64 : NT == 2 ? 56 : 40;
+    static constexpr int THREADS = TEAMS * kTeam + 128;
+    static constexpr int STAGE = kBlock * 72 * (D / 64);
+    static constexpr int NST = D == 64 ? 6 : 4;
+    static constexpr int SLOT = ROWS * (D + 3);             // floats of one partial result
+    // a team's shared memory: the ring, the warps' results, queries of more than two tiles as
+    // the lanes hold them
+    static constexpr int JOIN = NST * STAGE;
+    static constexpr int JROWS = NT == 4 ? 16 : ROWS;       // rows joined at a time
+    static constexpr int QUERIES = JOIN + kKeyWarps * JROWS * D * 4;
+    static constexpr int STATS = QUERIES + (NT == 4 ? NT * 32 * (D / 8) * 4 : 0);   // [4][ROWS] maxima, sums
+    static constexpr int ITEMS = STATS + 2 * kKeyWarps * ROWS * 4;
     static constexpr int START = ITEMS;                     // where the share begins, before its first item
-    static constexpr int POS = ITEMS + kItems * 64;         // int [N]: the rows' positions
-    static constexpr int MINUS = POS + 4 * N;               // float [N]: their references, negated
-    static constexpr int PARTS = MINUS + 4 * N;             // [4][N]: warps' maxima and sums; factors
-    static constexpr int BARS = PARTS + 16 * N;
-    static constexpr int NBARS = 7 + kItems;
-    static constexpr int THERE = BARS + 8 * NBARS;          // chunks that exist: keys, values [2]
-    static constexpr int MORE = (THERE + 12 + 31) / 32 * 32;
-    static constexpr int TMEM = kGroups * (SIZE + MORE);    // tensor-memory address
-    static constexpr int BYTES = TMEM + 16;
-    // a group's tensor memory columns
-    static constexpr uint32_t K_COL = 0, S_COL = D / 2, O_COL = S_COL + N, COLUMNS = O_COL + N;
-    static constexpr int SLOT = N * (D + 3);                // floats of one partial result
-    static_assert(SIZE % 1024 == 0 && ITEMS % 16 == 0 && BARS % 8 == 0 && sizeof(Start) <= kItems * 64, "layout");
-    static_assert(BYTES <= 227 * 1024 && kGroups * COLUMNS <= 512, "room");
+    static constexpr int BARS = ITEMS + kItems * 48;        // full, empty, items
+    static constexpr int THERE = BARS + (2 * NST + kItems) * 8;     // a block's chunks that exist
+    static constexpr int SIZE = (THERE + NST * 4 + 127) / 128 * 128;
+    static constexpr int BYTES = TEAMS * SIZE;
+    static_assert(ITEMS % 16 == 0 && BARS % 8 == 0 && sizeof(Start) <= kItems * 48 && NST + 1 < kItems, "layout");
+    static_assert(BYTES <= 227 * 1024, "room");
 };
 
-// mbar_wait after a try that failed, for waits that are long as a rule: out of line of the
-// code around it, and the warp sleeps up to 0.1 ms at a time.
-__device__ __noinline__ bool mbar_sleep(uint32_t bar, uint32_t parity, unsigned limit)
-{
-    const long long t0 = clock64();
-    for (;;) {
-        uint32_t ok;
-        asm volatile(
-            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-            " selp.u32 %0, 1, 0, p;\n}\n"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity), "r"(100000u)
-            : "memory");
-        if (ok)
-            return true;
-        if (clock64() - t0 > (long long)limit)
-            return false;
-    }
-}
-
-// `bytes` of global memory to shared memory.
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
 {
     asm volatile(
@@ -120,632 +91,527 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
         : "memory");
 }
 
-__device__ __forceinline__ void load16(uint32_t at, uint32_t (&r)[4])
-{
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(at)
-                 : "memory");
-}
-
-__device__ __forceinline__ uint32_t load4(uint32_t at)
+__device__ __forceinline__ uint32_t lds(uint32_t at)
 {
     uint32_t r;
     asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(r) : "r"(at) : "memory");
     return r;
 }
 
-__device__ __forceinline__ void store8(uint32_t at, uint32_t a, uint32_t b)
+__device__ __forceinline__ uint2 lds2(uint32_t at)
 {
-    asm volatile("st.shared.v2.b32 [%0], {%1,%2};\n" ::"r"(at), "r"(a), "r"(b) : "memory");
+    uint2 r;
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];\n" : "=r"(r.x), "=r"(r.y) : "r"(at) : "memory");
+    return r;
 }
 
-// Whether any of the group's threads says so; all of them meet here.
-__device__ __forceinline__ bool any_of_group(int bar, bool mine)
+template <int DT>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if constexpr (DT == LBV_F16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7},"
+            " {%8,%9}, {%0,%1,%2,%3};\n"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7},"
+            " {%8,%9}, {%0,%1,%2,%3};\n"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The 8 x 8 matrix of 16-bit values that the warp holds, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
+    return r;
+}
+
+// Whether any of the team's threads says so; all of them meet here.
+__device__ __forceinline__ bool any_of_team(int bar, bool mine)
 {
     uint32_t any;
     asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.b32 p, %2, 0;\n bar.red.or.pred q, %1, 256, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %2, 0;\n bar.red.or.pred q, %1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
         : "=r"(any)
         : "r"(bar), "r"((uint32_t)mine)
         : "memory");
     return any != 0;
 }
 
-// The largest of a warp's 32 values.
-__device__ __forceinline__ float warp_max(float x)
-{
-    int b = __float_as_int(x);
-    b ^= (b >> 31) & 0x7FFFFFFF;                 // ordered as the floats are
-    b = __reduce_max_sync(0xffffffffu, b);
-    return __int_as_float(b ^ ((b >> 31) & 0x7FFFFFFF));
-}
-
-template <int DT, int D, int N>
-__global__ void __launch_bounds__(Geo4<D, N>::THREADS, 1)
+template <int DT, int D, int NT>
+__global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
     lbv_attend4_rows_kernel(const __grid_constant__ AttendParams p)
 {
-    using G = Geo4<D, N>;
-    using S = Shape<N, kKeys, kExtra, kBlockUnits>;
-    constexpr bool kAhead = N == 16;             // scores stay in registers, the next key's are asked for early
-    constexpr int NC = N / 8;                    // 8 rows at a time, 4 of them a thread's
+    using G = Geo<D, NT>;
+    constexpr int ROWS = G::ROWS, PARTS = D / 64;
+    using S = Shape<ROWS, kBlock, kExtra>;
     extern __shared__ __align__(1024) unsigned char smem_all[];
     const int tid = threadIdx.x, lane = tid & 31;
-    const bool helper = tid >= kGroups * kTeam;  // the warp beside a group
-    const int group = helper ? (tid - kGroups * kTeam) >> 5 : tid / kTeam;
-    const int row = tid & 127, half = (tid >> 7) & 1, warp = (tid >> 5) & 3;   // key; part of it; lanes of tensor memory
-    unsigned char* smem = smem_all + group * G::SIZE;
-    unsigned char* more = smem_all + kGroups * G::SIZE + group * G::MORE;
-    const uint32_t sbase = smem_u32(smem), mbase = smem_u32(more);
-    auto bar_at = [&](int i) { return mbase + G::BARS + 8 * i; };
-    const uint32_t s_full = bar_at(0), o_done = bar_at(1);   // products are complete
-    const uint32_t k_in = bar_at(2), p_in = bar_at(3);       // their operands are there
-    const uint32_t k_full = bar_at(4), v_full = bar_at(5);   // copies have arrived (v_full: two)
-    auto item_full = [&](int i) { return bar_at(7 + i % kItems); };
-    uint32_t& tmem_slot = *reinterpret_cast<uint32_t*>(smem_all + G::TMEM);
-    Item* items = reinterpret_cast<Item*>(more + G::ITEMS);
-    const int share = group * gridDim.x + blockIdx.x;        // the SMs first, then their groups
+    const bool helper = tid >= G::TEAMS * kTeam;             // (its last warps may have no team)
+    const int team = helper ? (tid - G::TEAMS * kTeam) >> 5 : tid / kTeam, warp = (tid >> 5) & 3;
+    unsigned char* smem = smem_all + team * G::SIZE;
+    const uint32_t sbase = smem_u32(smem);
+    const int share = team * gridDim.x + blockIdx.x;         // the SMs first, then their teams
+    auto full = [&](int st) { return sbase + G::BARS + st * 8; };
+    auto empty = [&](int st) { return sbase + G::BARS + (G::NST + st) * 8; };
+    auto item_full = [&](int i) { return sbase + G::BARS + (2 * G::NST + i % kItems) * 8; };
+    Item* items = reinterpret_cast<Item*>(smem + G::ITEMS);
 
-    if (helper && lane == 0) {
-        for (int i = 0; i < G::NBARS; ++i)
-            mbar_init(bar_at(i), i == 2 ? 8 : 1);
+    if (tid % kTeam == 0 && !helper) {
+        for (int i = 0; i < G::NST; ++i) {
+            mbar_init(full(i), 1);
+            mbar_init(empty(i), kKeyWarps);
+        }
+        for (int i = 0; i < kItems; ++i)
+            mbar_init(item_full(i), 1);
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
-    if (tid < 32) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&tmem_slot))
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
-        tc_fence_before();
-    }
     __syncthreads();
-    tc_fence_after();
     after_previous();
     bool ok = true;
-    auto wait = [&](uint32_t b, uint32_t parity) {
-        if (!mbar_try(b, parity) && ok)
-            ok = mbar_sleep(b, parity, p.wait_limit);
-    };
-    const int cs = kv4::chunk_shift(p.kv);
+    const int cs = kv4::chunk_shift(p.kv), chunk_bytes = kv4::slot_bytes(D) << cs;
 
     if (helper) {
-        // ---- copies and products ----
+        // ---- the share's items, and copies: a lane has a chunk of a block ----
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(G::HELPER));
+        if (team >= G::TEAMS)
+            return;
         if (lane == 0)
             static_cast<JoinItem*>(p.items)[share].rows = 0;
-        Start* start = reinterpret_cast<Start*>(more + G::START);
-        find_start<S>(p, lane, gridDim.x * kGroups, kMinUnits, share, start);
+        Start* start = reinterpret_cast<Start*>(smem + G::START);
+        find_start<S>(p, lane, gridDim.x * G::TEAMS, kMinUnits, share, start);
         __syncwarp();
         const Start begin = *start;
-        __syncwarp();
-        int published = 0;
-        auto publish = [&](const Item& x) {                  // by lane 0
-            items[published % kItems] = x;
-            mbar_arrive(item_full(published));               // releases the stores
-        };
-        if (share >= begin.ctas) {                           // fewer units than groups
+        __syncwarp();                                        // the items take its place
+        const int64_t page_bytes = kv4::page_bytes(p.kv);
+        int it = 0, n = 0;                                   // items published, blocks asked for
+        auto publish = [&](const Item& x) {
             if (lane == 0) {
-                Item none = {};
-                publish(none);
+                items[it % kItems] = x;
+                mbar_arrive(item_full(it));                  // releases the stores
             }
-        } else {
-            const int page_mask = (1 << p.kv.page_shift) - 1;
-            const int64_t page_bytes = kv4::page_bytes(p.kv);
-            // lanes 2 i and 2 i + 1 have the codes and the pairs of chunk i
-            const int chunk0 = (lane >> 1) << cs;
-            const uint32_t size = lane & 1 ? 4 * (D / 64) << cs : 32 * (D / 64) << cs;
+            ++it;
+        };
+        if (share < begin.ctas) {
             Walk<S> w(p, begin, share);
-            // A block of the share: where this lane's chunk of it lies, if it exists.
-            struct Block {
-                int page, offset, head;
-                bool any, first, last, full;                 // full: every key of it exists
-            };
-            int j = 0, nb = 0;                               // of the item that `ahead` is of
-            auto next_block = [&]() -> Block {
-                Block x = {-1, 0, 0, true, false, false, false};
-                if (++j >= nb) {
-                    x.any = w.next();
-                    j = 0;
-                    nb = x.any ? w.b_last - w.b_first : 0;
-                    x.first = true;
+            while (ok && w.next()) {
+                const int* table = p.batch.block_table + (int64_t)w.r * p.batch.table_stride;
+                const uint8_t* base = kv4::chunk(p.kv, 0, w.head, 0);
+                auto page_of = [&](int b) {                  // of the lane's chunk, -1: zeros
+                    const int key = w.key0(b) + (lane << cs);
+                    return b < w.b_last && lane << cs < kBlock && wanted(p, w.x.lo, w.x.hi, key, 1 << cs)
+                               ? table[key >> p.kv.page_shift]
+                               : -1;
+                };
+                int next = page_of(w.b_first);
+#pragma unroll 1
+                for (int b = w.b_first; b < w.b_last; ++b) {
+                    const int st = n % G::NST, page = next;
+                    next = page_of(b + 1);
+                    // A stage is asked for again when it has been read, and its last copies have
+                    // landed (readers that gave up free it all the same).
+                    if (n >= G::NST) {
+                        const uint32_t parity = (uint32_t)((n / G::NST - 1) & 1);
+                        ok = mbar_wait(empty(st), parity, p.wait_limit) &&
+                             mbar_wait(full(st), parity, p.wait_limit);
+                    }
+                    ok = __all_sync(0xffffffffu, ok && ((unsigned)n < p.first_copies || share > 0));
+                    if (!ok)                                 // no more copies, and no more items: places
+                        break;                               // of those that are known may still be read
+                    if (b == w.b_first) {
+                        const bool whole = w.whole(), split = b < w.x.near;      // sinks, then a window
+                        publish({w.q.q0, w.q.first, w.q.keys, w.x.row0, w.x.rows, w.head, w.key0(b),
+                                 w.b_last - b, split ? w.x.gap * kBlock : 0, w.x.near - b,
+                                 whole ? 0 : w.first_cta(), whole ? 0 : w.last_cta()});
+                    }
+                    ++n;
+                    const bool go = page >= 0 && page < p.kv.pages;
+                    const unsigned there = __ballot_sync(0xffffffffu, go);
                     if (lane == 0) {
-                        const bool split = w.b_first < w.x.near;     // sinks, then a window
-                        const bool whole = w.whole();
-                        Item it = {w.q.q0, w.q.first, w.q.keys, w.x.row0, w.x.rows, w.head, w.x.hi, w.r,
-                                   w.key0(w.b_first), nb, split ? w.x.gap * kKeys : 0, w.x.near - w.b_first,
-                                   whole ? 0 : w.first_cta(), whole ? 0 : w.last_cta(), {0, 0}};
-                        publish(it);
+                        // all ones: every key of the block exists
+                        const int chunks = __popc(there);
+                        reinterpret_cast<uint32_t*>(smem + G::THERE)[st] =
+                            chunks == kBlock >> cs && w.key0(b) + kBlock <= w.q.keys ? ~0u : there;
+                        mbar_expect_tx(full(st), chunks * chunk_bytes);
                     }
-                    ++published;
-                }
-                if (x.any) {
-                    const int key = w.key0(w.b_first + j) + chunk0;
-                    if (chunk0 < kKeys && wanted(p, w.x.lo, w.x.hi, key, 1 << cs))
-                        x.page = p.batch.block_table[(int64_t)w.r * p.batch.table_stride + (key >> p.kv.page_shift)];
-                    x.offset = ((key & page_mask) >> cs) * (kv4::slot_bytes(D) << cs) + (lane & 1 ? D << cs : 0);
-                    x.head = w.head;
-                    x.last = j + 1 == nb;
-                    x.full = w.key0(w.b_first + j) + kKeys <= w.x.hi;
-                }
-                return x;
-            };
-            // Copies its keys (0) or values (1).  (The test of the bounded waits leaves some out.)
-            int asked_k = 0, asked_v = 0;
-            auto copy = [&](int which, const Block& x, int& asked) {
-                if (!x.any || !((unsigned)asked < p.first_copies || share > 0))
-                    return;
-                const bool go = x.page >= 0 && x.page < p.kv.pages;
-                const unsigned there = __ballot_sync(0xffffffffu, go);
-                const int st = which ? asked % G::VST : 0;
-                const uint32_t b = which ? v_full + st * 8 : k_full;
-                if (lane == 0) {
-                    const int chunks = __popc(there) / 2;
-                    reinterpret_cast<uint32_t*>(more + G::THERE)[which + st] =
-                        x.full && chunks == kKeys >> cs ? ~0u : there & 0x55555555u;
-                    mbar_expect_tx(b, chunks * (36 * (D / 64) << cs));
-                }
-                __syncwarp();
-                if (go)
-                    bulk_copy(mbase + (which ? G::VHELD + st * G::HELD : G::KHELD) + (lane & 1 ? G::CODES : 0) +
-                                  (lane >> 1) * size,
-                              kv4::chunk(p.kv, 0, x.head, 0) + x.page * page_bytes + x.offset + which * size, size, b);
-                ++asked;
-            };
-            // The products: with the group as a constant every operand is one, too (in registers
-            // of the threads' own they took some 130 instructions a product).
-            const uint32_t sall = smem_u32(smem_all), mall = sall + kGroups * G::SIZE;
-            auto score = [&](int n) {                        // S^T = K Q^T
-                wait(k_in, (uint32_t)(n & 1));
-                __syncwarp();
-                tc_fence_after();
-#pragma unroll
-                for (int g = 0; g < kGroups; ++g)
-                    if (group == g) {
-                        const uint64_t b = desc128(sall + g * G::SIZE + G::Q, 0);
-#pragma unroll
-                        for (int h = 0; h < D / 64; ++h)
-                            mma4_tk(g * G::COLUMNS + G::S_COL, g * G::COLUMNS + G::K_COL + h * 32,
-                                    b + h * (G::QHALF >> 4), idesc<DT>(N, false), h > 0);
-                        commit(mall + g * G::MORE + G::BARS);
+                    __syncwarp();
+                    if (go) {
+                        const int s = (w.key0(b) + (lane << cs)) & ((1 << p.kv.page_shift) - 1);
+                        bulk_copy(sbase + st * G::STAGE + lane * chunk_bytes,
+                                  base + page * page_bytes + (s >> cs) * chunk_bytes, chunk_bytes, full(st));
                     }
-            };
-            auto value = [&](int n, bool add) {              // O^T (+)= V^T P^T
-                wait(p_in, (uint32_t)(n & 1));
-                __syncwarp();
-                tc_fence_after();
-#pragma unroll
-                for (int g = 0; g < kGroups; ++g)
-                    if (group == g) {
-                        // (heads of 64 elements: the rows past them are what lies behind V, and not used)
-                        const uint64_t a = desc128(sall + g * G::SIZE + G::V, G::HALF),
-                                       b = desc32(sall + g * G::SIZE + G::P, G::PCHUNK);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)          // 64 keys at a time
-                            mma4_rr(g * G::COLUMNS + G::O_COL, a + h * 512, b + h * 128, idesc<DT>(N, true, true),
-                                    add || h > 0);
-                        commit(mall + g * G::MORE + G::BARS + 8);
-                    }
-            };
-            Block now = next_block(), ahead;                 // blocks n and n + 1
-            copy(0, now, asked_k);
-            copy(1, now, asked_v);
-            ahead = next_block();
-            bool before = false;                             // block n - 1 was its item's first
-            int n = 0, scored = 0, valued = 0;
-            // (After a wait that ran out nothing more is published: the group's warps may be
-            // anywhere in the items that it knows.)
-            auto fine = [&] { return ok = __all_sync(0xffffffffu, ok); };
-            for (; now.any; ++n) {
-                score(n);
-                ++scored;
-                if (!fine())
-                    break;
-                copy(0, ahead, asked_k);                     // the keys have been read
-                const Block after = ahead.any ? next_block() : ahead;
-                if (kAhead && !now.first)
-                    value(n - 1, !before), ++valued;
-                if (kAhead)
-                    copy(1, ahead, asked_v);                 // its stage's last use is over
-                if (!kAhead || now.last)
-                    value(n, !now.first), ++valued;
-                if (!kAhead)
-                    copy(1, ahead, asked_v);
-                if (!fine())
-                    break;
-                before = now.first;
-                now = ahead;
-                ahead = after;
+                }
             }
-            // the last products and copies end before tensor and shared memory go away, also
-            // after a wait that ran out
-            __syncwarp();
-            bool end = true;
-            if (scored > 0)
-                end = mbar_wait(s_full, (uint32_t)((scored - 1) & 1), p.wait_limit);
-            if (valued > 0)
-                end = mbar_wait(o_done, (uint32_t)((valued - 1) & 1), p.wait_limit) && end;
-            if (asked_k > 0)
-                end = mbar_wait(k_full, (uint32_t)((asked_k - 1) & 1), p.wait_limit) && end;
-            for (int i = asked_v - 1; i >= 0 && i >= asked_v - G::VST; --i)
-                end = mbar_wait(v_full + i % G::VST * 8, (uint32_t)((i / G::VST) & 1), p.wait_limit) && end;
-            ok = ok && end;
         }
-    } else {
-        // ---- the keys ----
-        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-        // (all 512 columns are this CTA's, so they begin at 0)
-        const uint32_t tm = group * G::COLUMNS + lanes;
-        const uint32_t k_at = tm + G::K_COL + half * (D / 4), s_at = tm + G::S_COL + half * 4,
-                       o_at = tm + G::O_COL + half * 4;
-        const int bar = 1 + group;
-        int* pos = reinterpret_cast<int*>(more + G::POS);
-        float* minus = reinterpret_cast<float*>(more + G::MINUS);
-        float* parts = reinterpret_cast<float*>(more + G::PARTS);
-        // where this key is held: its chunk of the block, this half's first row of codes and pair
-        constexpr int W = D / 64;                            // vectors of 16 bytes of codes a thread has
-        const int chunk = row >> cs, first = ((chunk * (D / 64) - chunk) << cs) + row + (D == 128 ? half << cs : 0);
-        const uint32_t codes = mbase + first * 32 + (D == 64 ? half * 16 : 0), pairs = mbase + G::CODES + first * 4;
-        // Its rows of V and of P, with the chunk 0 of their swizzles.  (Of V's two vectors of codes
-        // the one goes first that leaves the lanes' banks apart.)
-        const int turn = (row >> 2) & 1, swap = D == 128 ? turn : 0;
-        const uint32_t v_row = sbase + G::V + (D == 128 ? half * G::HALF : 0) + row * 128 +
-                               (((row & 7) ^ (D == 128 ? swap << 2 : half << 2)) << 4);
-        const uint32_t p_row = sbase + G::P + row * 32 + (turn << 4) + half * 8;
-        // scores are c times the products; a scale of zero clears Q
-        const float c = p.scale_log2 == 0.f ? 1.f : p.scale_log2;
-        const float hidden = c < 0.f ? INFINITY : -INFINITY;
-        const kv4::Constants constants = kv4::constants<DT>();
-        int n0 = 0;                                          // blocks before the item
-        for (int it = 0;; ++it) {
-            // one warp waits for the item, and all of them hear whether it came
-            bool stop = false;
-            if (half == 0 && warp == 0) {
-                wait(item_full(it), (uint32_t)((it / kItems) & 1));
-                stop = !ok || items[it % kItems].nb == 0;
-            }
-            if (any_of_group(bar, stop))
-                break;
-            const Item& w = items[it % kItems];
-            const int rows = w.rows, nb = w.nb, hi = w.hi;
-            // the queries (zeros for the rows that fill up 8), and what the rows see
-            for (int i = tid % kTeam; i < (rows + 7) / 8 * 8 * (D / 8); i += kTeam) {
-                const int r = i / (D / 8), ch = i % (D / 8), qrow = w.row0 + r;
-                const int t = token_of(p, qrow);
-                const uint16_t* src = p.q + (int64_t)(w.q0 + t) * p.q_token +
-                                      (int64_t)(w.head * p.group + qrow - t * p.group) * p.q_head + ch * 8;
-                uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (p.scale_log2 == 0.f || r >= rows) {
+        if (ok)
+            publish(Item{});
+        // the copies land before shared memory goes away, also after a wait that ran out
+        for (int i = 0; i < G::NST; ++i)
+            if (n - 1 - i >= 0 && !mbar_wait(full((n - 1 - i) % G::NST), (uint32_t)(((n - 1 - i) / G::NST) & 1),
+                                             p.wait_limit))
+                ok = false;
+        if (!ok && lane == 0)
+            atomicOr(p.status, 1u);
+        return;
+    }
+
+    // ---- the keys ----
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(G::REGS));
+    const int g = lane >> 2, t = lane & 3, bar = 1 + team;
+    // Row g of a tile is key g, or its neighbour for g >= 4, of this warp's 16 (and row g + 8 the
+    // eighth after it): the keys of a quad's lanes, and of its 2 t-th and 2 t + 1-th rows, then
+    // lie in four different rows of 32 bytes modulo 128.
+    auto key_at = [](int r) { return r ^ ((r >> 2) & 1); };
+    auto codes_of = [&](int key) { return (key >> cs) * chunk_bytes + (key & ((1 << cs) - 1)) * 32; };
+    auto pair_of = [&](int key) { return (key >> cs) * chunk_bytes + (D << cs) + (key & ((1 << cs) - 1)) * 4; };
+    const int k_key = warp * 16 + key_at(g), v_key0 = warp * 16 + key_at(2 * t), v_key1 = warp * 16 + key_at(2 * t + 1);
+    const uint32_t plane = 32u << cs, pairs = 4u << cs;      // from one plane to the next
+    const uint32_t eighth = cs == 3 ? (uint32_t)chunk_bytes : 256u;      // eight keys on: codes, pairs
+    const uint32_t eighth4 = cs == 3 ? (uint32_t)chunk_bytes : 32u;
+    const uint32_t k_at = sbase + codes_of(k_key) + t * 8, k_pair = sbase + pair_of(k_key);
+    const uint32_t v_at = sbase + codes_of(v_key0) + PARTS * plane + g * 4,
+                   v_pair = sbase + pair_of(v_key0) + PARTS * pairs;
+    const int v_next = (v_key1 - v_key0) * 32, v_next4 = (v_key1 - v_key0) * 4;
+    const kv4::Constants constants = kv4::constants<DT>();
+    // scores are c times the products; a scale of zero clears Q
+    const float c = p.scale_log2 == 0.f ? 1.f : p.scale_log2;
+    const float hidden = c < 0.f ? INFINITY : -INFINITY;
+    float* joint = reinterpret_cast<float*>(smem + G::JOIN);
+    float* stats = reinterpret_cast<float*>(smem + G::STATS);
+    int n = 0;
+    for (int it = 0;; ++it) {
+        // one warp waits for the item, and all of them hear whether it came
+        bool stop = false;
+        if (warp == 0) {
+            if (ok)
+                ok = mbar_wait(item_full(it), (uint32_t)((it / kItems) & 1), p.wait_limit);
+            stop = !ok || items[it % kItems].nb == 0;
+        }
+        if (any_of_team(bar, stop))
+            break;
+        const Item& w = items[it % kItems];
+        const int nb = w.nb, item_rows = w.rows;
+        // The queries as the second operand: lane (g, t) has elements 16 t to 16 t + 15 of each
+        // part of row g, a pair a register.
+        constexpr int QR = D / 8, QT = NT == 4 ? 1 : NT;         // registers a tile; tiles kept in them
+        uint32_t qf[QT][QR];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const int row = w.row0 + 8 * i + g;
+            const bool in = 8 * i + g < item_rows && p.scale_log2 != 0.f;
+            const int tok = token_of(p, row);
+            const uint16_t* src = p.q + (int64_t)(w.q0 + (in ? tok : 0)) * p.q_token +
+                                  (int64_t)(w.head * p.group + (in ? row - tok * p.group : 0)) * p.q_head + t * 16;
+            uint32_t(&q)[QR] = qf[NT == 4 ? 0 : i];
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part) {
+                if (!in) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        q[part * 8 + e] = 0;
                 } else if (p.q_wide) {
-                    x = *reinterpret_cast<const uint4*>(src);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(src + part * 64 + h * 8);
+                        q[part * 8 + 4 * h] = v.x, q[part * 8 + 4 * h + 1] = v.y;
+                        q[part * 8 + 4 * h + 2] = v.z, q[part * 8 + 4 * h + 3] = v.w;
+                    }
                 } else {
-                    uint32_t e[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        e[j] = (uint32_t)src[2 * j] | ((uint32_t)src[2 * j + 1] << 16);
-                    x = make_uint4(e[0], e[1], e[2], e[3]);
-                }
-                *reinterpret_cast<uint4*>(smem + G::Q + (ch >> 3) * G::QHALF + r * 128 +
-                                          (((ch & 7) ^ (r & 7)) << 4)) = x;
-            }
-            fence_proxy_async_smem();
-            if (tid % kTeam < N) {
-                const int r = tid % kTeam, i = token_of(p, w.row0 + r);
-                pos[r] = r < rows ? w.first + i : INT_MIN / 2;
-                minus[r] = r < rows ? kNone : 0.f;
-            }
-            named_bar_sync(bar, kTeam);
-            float2 x[2 * NC];                                // this key's share of the rows' sums
-#pragma unroll
-            for (int i = 0; i < 2 * NC; ++i)
-                x[i] = make_float2(0.f, 0.f);
-            // keys below `open_lo` or at `open_hi` and past are hidden from some row
-            const int open_hi = p.tree ? min(w.keys, w.first) : min(w.keys, w.first + token_of(p, w.row0) + 1);
-            const int open_lo = p.window > 0 ? w.first + token_of(p, w.row0 + rows - 1) - p.window + 1 : 0;
-
-            // A thread's (scale, bias) of a plane, zeros where its key does not exist: slots past the
-            // context hold anything.  (All ones: every key of the block exists.)
-            auto pair_of = [&](int which, uint32_t at, int j) {
-                const uint32_t mask = load4(mbase + G::THERE + 4 * which);
-                uint32_t sb = load4(pairs + at);
-                if (mask != ~0u)
-                    sb = ((mask >> (2 * chunk)) & 1) && w.key_of(j) + row < hi ? sb : 0u;
-                return sb;
-            };
-            // Block j's key to tensor memory, and its scores asked for.
-            auto key_in = [&](int j) {
-                wait(k_full, (uint32_t)(n0 + j) & 1);
-                const uint32_t sb = pair_of(0, G::KHELD, j);
-                const uint32_t sc = kv4::both_scales(sb), bi = kv4::both_biases(sb);
-#pragma unroll
-                for (int h = 0; h < W; ++h) {
-                    uint32_t held[4], e[16];
-                    load16(codes + G::KHELD + h * 16, held);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        kv4::expand<DT>(held[i], sc, bi, constants, reinterpret_cast<uint32_t(&)[4]>(e[4 * i]));
-                    tmem_st16(k_at + h * 16, e);
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(k_in);
-            };
-            // Its value to shared memory, when the last block's has been used.
-            auto value_in = [&](int j) {
-                if (n0 + j > 0)
-                    wait(o_done, (uint32_t)((n0 + j - 1) & 1));
-                const int st = (n0 + j) % G::VST;
-                wait(v_full + st * 8, (uint32_t)(((n0 + j) / G::VST) & 1));
-                const uint32_t at = G::VHELD + st * G::HELD, sb = pair_of(1 + st, at, j);
-                const uint32_t sc = kv4::both_scales(sb), bi = kv4::both_biases(sb);
-#pragma unroll
-                for (int h = 0; h < W; ++h) {
-                    uint32_t held[4];
-                    load16((codes + at) ^ ((swap ^ h) << 4), held);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t e[4];
-                        kv4::expand<DT>(held[i], sc, bi, constants, e);
-                        store16(v_row ^ ((4 * h + i) << 4), e);
-                    }
-                }
-            };
-            // scores of this thread's 4 of 8 rows
-            auto scores = [&](int ch, float (&t)[4], int k0) {
-                tmem_ld4(s_at + ch * 8, t);
-                tmem_wait_ld();
-                if (k0 > open_hi - kKeys || k0 < open_lo) {
-                    Request q;
-                    q.first = w.first, q.keys = w.keys;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = ch * 8 + half * 4 + i;
-                        const uint64_t word = p.tree && r < rows ? p.tree[w.q0 + pos[r] - w.first] : 0;
-                        if (!sees(p, q, pos[r], word, k0 + row))
-                            t[i] = hidden;
-                    }
-                }
-            };
-            // their exponents, two at a time
-            auto exponents = [&](int ch, int i, const float (&t)[4]) {
-                return fma2(make_float2(t[2 * i], t[2 * i + 1]), make_float2(c, c),
-                            *reinterpret_cast<const float2*>(minus + ch * 8 + half * 4 + 2 * i));
-            };
-            // Their probabilities, kept in y and as a part of the key's row of P; the largest exponent.
-            auto weigh = [&](int ch, const float (&t)[4], float2 (&y)[2]) {
-                const float2 a = exponents(ch, 0, t), b = exponents(ch, 1, t);
-                y[0] = make_float2(ex2(a.x), ex2(a.y));
-                y[1] = make_float2(ex2(b.x), ex2(b.y));
-                store8((p_row ^ ((ch & 1) << 4)) + (ch >> 1) * G::PCHUNK, pack2<DT>(y[0].x, y[0].y),
-                       pack2<DT>(y[1].x, y[1].y));
-                return fmaxf(fmaxf(a.x, a.y), fmaxf(b.x, b.y));
-            };
-            auto add = [&](int ch, const float2 (&y)[2]) {
-                x[2 * ch] = add2(x[2 * ch], y[0]);
-                x[2 * ch + 1] = add2(x[2 * ch + 1], y[1]);
-            };
-            // Moves the references that the block's maxima pass by more than 8, and the sums with them.
-            auto most_of = [&](int ch, const float (&t)[4]) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float most = warp_max(t[i] * c);
-                    if (lane == 0)
-                        parts[warp * N + ch * 8 + half * 4 + i] = most;
-                }
-            };
-            auto move = [&](int j) {
-                named_bar_sync(bar, kTeam);
-                if (tid % kTeam < rows) {
-                    float *q = parts + tid % kTeam, *m = minus + tid % kTeam;
-                    const float most = fmaxf(fmaxf(q[0], q[N]), fmaxf(q[2 * N], q[3 * N]));
-                    float f = 1.f;
-                    if (most + *m > 8.f) {
-                        f = ex2(-*m - most);
-                        *m = -most;
-                    }
-                    q[0] = f;                                // the factor of the row's sums
-                }
-                named_bar_sync(bar, kTeam);
-#pragma unroll
-                for (int ch = 0; ch < NC; ++ch)
-                    if (ch * 8 < rows) {
-                        float o[4], f[4];
-                        if (j > 0) {
-                            tmem_ld4(o_at + ch * 8, o);
-                            tmem_wait_ld();
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int r = ch * 8 + half * 4 + i;
-                            f[i] = r < rows ? parts[r] : 1.f;
-                            o[i] *= f[i];
-                        }
-                        x[2 * ch].x *= f[0], x[2 * ch].y *= f[1];
-                        x[2 * ch + 1].x *= f[2], x[2 * ch + 1].y *= f[3];
-                        if (j > 0)
-                            tmem_st4(o_at + ch * 8, o);
-                    }
-                tmem_wait_st();
-            };
-            auto done = [&] {                                // P and V are in: by one thread, after the others
-                if (tid % kTeam == 0)
-                    mbar_arrive(p_in);
-            };
-
-            if (kAhead) {
-                // A block's scores are computed while the block before it is weighed: they stay
-                // in registers, and the next key takes their place.
-                key_in(0);
-#pragma unroll 1
-                for (int j = 0; j < nb; ++j) {
-                    float t[NC][4];
-                    float2 y[NC][2];
-                    wait(s_full, (uint32_t)((n0 + j) & 1));
-                    tc_fence_after();
-#pragma unroll
-                    for (int ch = 0; ch < NC; ++ch)
-                        if (ch * 8 < rows)
-                            scores(ch, t[ch], w.key_of(j));
-                    if (j + 1 < nb)
-                        key_in(j + 1);
-                    value_in(j);
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int ch = 0; ch < NC; ++ch)
-                        if (ch * 8 < rows)
-                            top = fmaxf(top, weigh(ch, t[ch], y[ch]));
-                    fence_proxy_async_smem();
-                    tc_fence_before();
-                    if (any_of_group(bar, top > 8.f)) {
-#pragma unroll
-                        for (int ch = 0; ch < NC; ++ch)
-                            if (ch * 8 < rows)
-                                most_of(ch, t[ch]);
-                        move(j);
-#pragma unroll
-                        for (int ch = 0; ch < NC; ++ch)
-                            if (ch * 8 < rows)
-                                weigh(ch, t[ch], y[ch]);
-                        fence_proxy_async_smem();
-                        tc_fence_before();
-                        named_bar_sync(bar, kTeam);
-                    }
-                    done();
-#pragma unroll
-                    for (int ch = 0; ch < NC; ++ch)
-                        if (ch * 8 < rows)
-                            add(ch, y[ch]);
-                }
-            } else {
-                // of more rows the scores stay in tensor memory: their exponents are looked at, and
-                // then weighed
-#pragma unroll 1
-                for (int j = 0; j < nb; ++j) {
-                    const int k0 = w.key_of(j);
-                    float t[4];
-                    key_in(j);
-                    value_in(j);
-                    wait(s_full, (uint32_t)((n0 + j) & 1));
-                    tc_fence_after();
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int ch = 0; ch < NC; ++ch)
-                        if (ch * 8 < rows) {
-                            scores(ch, t, k0);
-                            const float2 a = exponents(ch, 0, t), b = exponents(ch, 1, t);
-                            top = fmaxf(top, fmaxf(fmaxf(a.x, a.y), fmaxf(b.x, b.y)));
-                        }
-                    if (any_of_group(bar, top > 8.f)) {
-#pragma unroll
-                        for (int ch = 0; ch < NC; ++ch)
-                            if (ch * 8 < rows) {
-                                scores(ch, t, k0);
-                                most_of(ch, t);
-                            }
-                        move(j);
-                    }
-#pragma unroll
-                    for (int ch = 0; ch < NC; ++ch)
-                        if (ch * 8 < rows) {
-                            float2 y[2];
-                            scores(ch, t, k0);
-                            weigh(ch, t, y);
-                            add(ch, y);
-                        }
-                    fence_proxy_async_smem();
-                    tc_fence_before();
-                    named_bar_sync(bar, kTeam);
-                    done();
+                    for (int e = 0; e < 8; ++e)
+                        q[part * 8 + e] = (uint32_t)src[part * 64 + 2 * e] | ((uint32_t)src[part * 64 + 2 * e + 1] << 16);
                 }
             }
-            n0 += nb;
-
-            // ---- the item's result: a thread has an element of its rows ----
+            // (the same for every warp, and each writes it all: the values are alike)
+            if (NT == 4) {
 #pragma unroll
-            for (int ch = 0; ch < NC; ++ch)
-                if (ch * 8 < rows) {
-                    float s[4] = {x[2 * ch].x, x[2 * ch].y, x[2 * ch + 1].x, x[2 * ch + 1].y};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                        for (int d = 16; d > 0; d >>= 1)
-                            s[i] += __shfl_xor_sync(0xffffffffu, s[i], d);
-                        if (lane == 0)
-                            parts[warp * N + ch * 8 + half * 4 + i] = s[i];
-                    }
-                }
-            named_bar_sync(bar, kTeam);
-            wait(o_done, (uint32_t)((n0 - 1) & 1));
-            tc_fence_after();
-            const bool whole = w.c0 == w.c1;
-            float* slot = p.partial + (size_t)(2 * share + (w.c0 == share)) * G::SLOT;
-            auto sum_of = [&](int r) { return (parts[r] + parts[N + r]) + (parts[2 * N + r] + parts[3 * N + r]); };
-#pragma unroll
-            for (int ch = 0; ch < NC; ++ch)
-                if (ch * 8 < rows) {
-                    float o[4];
-                    tmem_ld4(o_at + ch * 8, o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = ch * 8 + half * 4 + i;
-                        if (r < rows && row < D) {
-                            if (whole) {
-                                const int qrow = w.row0 + r, tok = token_of(p, qrow);
-                                const float s = sum_of(r);
-                                const uint32_t y = s > 0.f ? pack2<DT>(o[i] / s, 0.f) : 0u;
-                                p.out[(int64_t)(w.q0 + tok) * p.out_token +
-                                      (int64_t)(w.head * p.group + qrow - tok * p.group) * p.out_head + row] =
-                                    (uint16_t)y;
-                            } else {
-                                slot[r * D + row] = o[i];
-                            }
-                        }
-                    }
-                }
-            if (tid % kTeam < rows) {
-                const int r = tid % kTeam;
-                const float s = sum_of(r);
-                if (!whole) {
-                    slot[N * D + r] = -minus[r];
-                    slot[N * (D + 1) + r] = slot[N * (D + 2) + r] = s;
-                } else if (p.lse) {
-                    const int qrow = w.row0 + r, tok = token_of(p, qrow);
-                    p.lse[(int64_t)(w.q0 + tok) * p.heads + w.head * p.group + qrow - tok * p.group] =
-                        lse_of(-minus[r], s);
-                }
+                for (int e = 0; e < QR / 4; ++e)
+                    *reinterpret_cast<uint4*>(smem + G::QUERIES + ((i * (QR / 4) + e) * 32 + lane) * 16) =
+                        make_uint4(q[4 * e], q[4 * e + 1], q[4 * e + 2], q[4 * e + 3]);
             }
-            if (!whole && tid % kTeam == 0 && w.c0 == share)
-                static_cast<JoinItem*>(p.items)[w.c0] = {w.q0, w.row0, rows, w.head, w.c1 - w.c0 + 1};
-            tc_fence_before();
-            named_bar_sync(bar, kTeam);                      // what the rows need has been read
         }
+        if (NT == 4)
+            named_bar_sync(bar, kTeam);
+        float o[NT][D / 16][4];                                  // tile (part, i): elements 64 part + 8 g + 2 i, and the next
+        float2 minus[NT], l[NT];                                 // references, negated, and sums of rows 2 t and 2 t + 1
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            minus[i] = make_float2(kNone, kNone);
+            l[i] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+                o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
+        }
+        // keys below `open_lo` or at `open_hi` and past are hidden from some row
+        const int open_hi = p.tree ? min(w.keys, w.first)
+                                   : min(w.keys, w.first + token_of(p, w.row0) + 1);
+        const int open_lo =
+            p.window > 0 ? w.first + token_of(p, w.row0 + item_rows - 1) - p.window + 1 : 0;
+
+#pragma unroll 1
+        for (int j = 0; j < nb; ++j, ++n) {
+            const int st = n % G::NST, k0 = w.key_of(j);
+            if (ok)
+                ok = mbar_wait(full(st), (uint32_t)((n / G::NST) & 1), p.wait_limit);
+            const uint32_t stage = st * G::STAGE;
+            const uint32_t there = lds(sbase + G::THERE + st * 4);
+            // whether a key of the block exists: slots past the context hold anything
+            auto exists = [&](int key) { return ((there >> (key >> cs)) & 1) && k0 + key < w.keys; };
+            // ---- scores of 16 keys ----
+            float s[NT][4];
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+                s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+            uint32_t kp[PARTS][2];                               // (scale, bias) of rows g and g + 8
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    kp[part][h] = lds(k_pair + stage + part * pairs + h * eighth4);
+            if (there != ~0u) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (!exists(k_key + 8 * h)) {
+#pragma unroll
+                        for (int part = 0; part < PARTS; ++part)
+                            kp[part][h] = 0;
+                    }
+            }
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part) {
+                uint2 v[2];
+                uint32_t sc[2], bi[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    v[h] = lds2(k_at + stage + part * plane + h * eighth);
+                    sc[h] = kv4::both_scales(kp[part][h]), bi[h] = kv4::both_biases(kp[part][h]);
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {                    // words of 8 elements
+                    uint32_t e[2][4];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        kv4::expand<DT>(u ? v[h].y : v[h].x, sc[h], bi[h], constants, e[h]);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {                // 4 of them a step
+                        const uint32_t a[4] = {e[0][2 * k], e[1][2 * k], e[0][2 * k + 1], e[1][2 * k + 1]};
+#pragma unroll
+                        for (int i = 0; i < NT; ++i) {
+                            const int at = part * 8 + u * 4 + k * 2;
+                            if (NT == 4) {
+                                const uint2 q = lds2(sbase + G::QUERIES +
+                                                     ((i * (QR / 4) + at / 4) * 32 + lane) * 16 + (at % 4) * 4);
+                                mma<DT>(s[i], a, q.x, q.y);
+                            } else {
+                                mma<DT>(s[i], a, qf[i][at], qf[i][at + 1]);
+                            }
+                        }
+                    }
+                }
+            }
+            // ---- their probabilities ----
+            if (k0 + warp * 16 + 16 > open_hi || k0 + warp * 16 < open_lo) {     // rare, so short code
+                Request q;
+                q.first = w.first, q.keys = w.keys;
+                uint32_t see = 0;
+#pragma unroll 1
+                for (int e = 0; e < 4 * NT; ++e) {
+                    const int r = (e >> 2) * 8 + 2 * t + (e & 1), tok = token_of(p, w.row0 + r);
+                    const uint64_t word = p.tree && r < item_rows ? p.tree[w.q0 + tok] : 0;
+                    if (r < item_rows && sees(p, q, q.first + tok, word, k0 + k_key + ((e >> 1) & 1) * 8))
+                        see |= 1u << e;
+                }
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        s[i][e] = (see >> (4 * i + e)) & 1 ? s[i][e] : hidden;
+            }
+            // exponents, for the references as they are
+            float2 x[NT][2];
+            auto exponents = [&] {
+                float top = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        x[i][h] = fma2(make_float2(s[i][2 * h], s[i][2 * h + 1]), make_float2(c, c), minus[i]);
+                        top = fmaxf(top, fmaxf(x[i][h].x, x[i][h].y));
+                    }
+                return top;
+            };
+            if (__any_sync(0xffffffffu, exponents() > 8.f)) {
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float& from = h ? minus[i].y : minus[i].x;
+                        float top = fmaxf(c * s[i][h], c * s[i][2 + h]);
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                        if (top + from > 8.f) {
+                            const float f = ex2(-from - top);
+                            from = -top;
+                            (h ? l[i].y : l[i].x) *= f;
+#pragma unroll
+                            for (int j = 0; j < D / 16; ++j)
+                                o[i][j][h] *= f, o[i][j][2 + h] *= f;
+                        }
+                    }
+                exponents();
+            }
+            uint32_t pf[NT][2];
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float2 y = make_float2(ex2(x[i][h].x), ex2(x[i][h].y));
+                    l[i] = add2(l[i], y);
+                    pf[i][h] = transposed(pack2<DT>(y.x, y.y));
+                }
+            // ---- and their values ----
+            uint32_t vp[PARTS][2][2];                            // (scale, bias) of a lane's four keys
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t at = v_pair + stage + part * pairs + h * eighth4;
+                    vp[part][h][0] = lds(at), vp[part][h][1] = lds(at + v_next4);
+                }
+            if (there != ~0u) {
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+                    if (!exists((h & 1 ? v_key1 : v_key0) + 8 * (h >> 1))) {
+#pragma unroll
+                        for (int part = 0; part < PARTS; ++part)
+                            vp[part][h >> 1][h & 1] = 0;
+                    }
+            }
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part) {
+                uint32_t e[2][2][4];                             // keys' halves, even and odd elements
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t at = v_at + stage + part * plane + h * eighth;
+                    const uint32_t x = lds(at), y = lds(at + v_next);
+                    const uint32_t sc = __byte_perm(vp[part][h][0], vp[part][h][1], 0x5410),
+                                   bi = __byte_perm(vp[part][h][0], vp[part][h][1], 0x7632);
+                    kv4::expand<DT>(__byte_perm(x, y, 0x5410), sc, bi, constants, e[h][0]);
+                    kv4::expand<DT>(__byte_perm(x, y, 0x7632), sc, bi, constants, e[h][1]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t a[4] = {e[0][0][j], e[0][1][j], e[1][0][j], e[1][1][j]};
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+                        mma<DT>(o[i][part * 4 + j], a, pf[i][0], pf[i][1]);
+                }
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(empty(st));
+        }
+
+        // ---- the item's result: the warps' sums are joined ----
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float sum = h ? l[i].y : l[i].x;
+                sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                if (g == 0) {
+                    stats[warp * ROWS + 8 * i + 2 * t + h] = h ? -minus[i].y : -minus[i].x;
+                    stats[(kKeyWarps + warp) * ROWS + 8 * i + 2 * t + h] = sum;
+                }
+            }
+        named_bar_sync(bar, kTeam);
+        const int c0 = w.c0, c1 = w.c1;
+        const bool whole = c0 == c1;
+        Request q;
+        q.q0 = w.q0;
+        float* slot = p.partial + (size_t)(2 * share + (c0 == share)) * G::SLOT;
+        auto top_of = [&](int r) {
+            const float* q = stats + r;
+            return fmaxf(fmaxf(q[0], q[ROWS]), fmaxf(q[2 * ROWS], q[3 * ROWS]));
+        };
+#pragma unroll
+        for (int r0 = 0; r0 < ROWS; r0 += G::JROWS) {
+            if (r0 >= item_rows)
+                break;
+            if (r0 > 0)
+                named_bar_sync(bar, kTeam);                         // the rows before have been added
+#pragma unroll
+            for (int i = 0; i < G::JROWS / 8; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int tile = r0 / 8 + i, r = 8 * tile + 2 * t + h;
+                    const float f = ex2((h ? -minus[tile].y : -minus[tile].x) - top_of(r));
+                    float* d = joint + (warp * G::JROWS + 8 * i + 2 * t + h) * D + 8 * g;
+#pragma unroll
+                    for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+                        for (int j = 0; j < 4; j += 2)
+                            *reinterpret_cast<float4*>(d + part * 64 + 2 * j) =
+                                make_float4(f * o[tile][part * 4 + j][h], f * o[tile][part * 4 + j][2 + h],
+                                            f * o[tile][part * 4 + j + 1][h], f * o[tile][part * 4 + j + 1][2 + h]);
+                }
+            named_bar_sync(bar, kTeam);
+            const int rows = min(G::JROWS, item_rows - r0);
+            for (int i = tid % kTeam; i < rows * (D / 4); i += kTeam) {
+                const int r = i / (D / 4), d4 = i % (D / 4);
+                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+                float total = 0.f;
+                const float top = top_of(r0 + r);
+#pragma unroll
+                for (int k = 0; k < kKeyWarps; ++k) {
+                    const float4 a = *reinterpret_cast<const float4*>(joint + (k * G::JROWS + r) * D + 4 * d4);
+                    sum.x += a.x, sum.y += a.y, sum.z += a.z, sum.w += a.w;
+                    total += ex2(stats[k * ROWS + r0 + r] - top) * stats[(kKeyWarps + k) * ROWS + r0 + r];
+                }
+                if (whole) {
+                    finish4<DT>(p, q, w.head, w.row0 + r0 + r, d4, sum, top, total, total);
+                } else {
+                    *reinterpret_cast<float4*>(slot + (r0 + r) * D + 4 * d4) = sum;
+                    if (d4 == 0) {
+                        slot[ROWS * D + r0 + r] = top;
+                        slot[ROWS * (D + 1) + r0 + r] = slot[ROWS * (D + 2) + r0 + r] = total;
+                    }
+                }
+            }
+        }
+        if (!whole && tid % kTeam == 0 && c0 == share)
+            static_cast<JoinItem*>(p.items)[c0] = {w.q0, w.row0, item_rows, w.head, c1 - c0 + 1};
+        named_bar_sync(bar, kTeam);                                 // statistics and results have been read
     }
-    if (!ok)
+    if (!ok && lane == 0)
         atomicOr(p.status, 1u);
-    __syncthreads();
-    if (tid < 32) {
-        tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem_slot) : "memory");
-    }
 }
 
-template <int DT, int D, int N>
+template <int DT, int D, int NT>
 cudaError_t launch(const AttendParams& p, int sms, cudaStream_t st)
 {
-    using G = Geo4<D, N>;
-    auto kernel = lbv_attend4_rows_kernel<DT, D, N>;
+    using G = Geo<D, NT>;
+    auto kernel = lbv_attend4_rows_kernel<DT, D, NT>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, G::BYTES);
     if (e != cudaSuccess)
         return e;
-    const int ctas = std::min(sms, kAttendMaxCtas / kGroups);
+    const int ctas = std::min(sms, kAttendMaxCtas / G::TEAMS);
     e = launch_after(kernel, dim3((unsigned)ctas), G::THREADS, G::BYTES, st, p);
-    return e == cudaSuccess ? launch_attend_join(p, (lbv_dtype)DT, N, ctas * kGroups, st) : e;
+    return e == cudaSuccess ? launch_attend_join(p, (lbv_dtype)DT, G::ROWS, ctas * G::TEAMS, st) : e;
 }
 
 template <int DT, int D>
 cudaError_t launch_rows(const AttendParams& p, int sms, cudaStream_t st)
 {
-    return attend_average_rows(p) <= 16 ? launch<DT, D, 16>(p, sms, st) : launch<DT, D, 48>(p, sms, st);
+    const int64_t rows = attend_average_rows(p);
+    return rows <= 8 ? launch<DT, D, 1>(p, sms, st) : rows <= 16 ? launch<DT, D, 2>(p, sms, st) : launch<DT, D, 4>(p, sms, st);
 }
 
 }  // namespace
@@ -760,8 +626,8 @@ cudaError_t launch_attend4_rows(const AttendParams& p, const CUtensorMap&, const
 
 size_t attend4_rows_partial_floats(int dim, int sms)
 {
-    // two slots a group
-    return (size_t)2 * kGroups * std::min(sms, kAttendMaxCtas / kGroups) * 48 * (dim + 3);
+    // two slots a team: two teams an SM with 32 rows, more than three with 16 or four with 8
+    return (size_t)2 * 2 * std::min(sms, kAttendMaxCtas / 2) * 32 * (dim + 3);
 }
 
 }  // namespace lbv
