@@ -83,28 +83,6 @@ struct Geo {
     static_assert(BYTES <= 227 * 1024, "room");
 };
 
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
-{
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
-        "l"(src), "r"(bytes), "r"(bar)
-        : "memory");
-}
-
-__device__ __forceinline__ uint32_t lds(uint32_t at)
-{
-    uint32_t r;
-    asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(r) : "r"(at) : "memory");
-    return r;
-}
-
-__device__ __forceinline__ uint2 lds2(uint32_t at)
-{
-    uint2 r;
-    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];\n" : "=r"(r.x), "=r"(r.y) : "r"(at) : "memory");
-    return r;
-}
-
 template <int DT>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
@@ -358,7 +336,7 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
             if (ok)
                 ok = mbar_wait(full(st), (uint32_t)((n / G::NST) & 1), p.wait_limit);
             const uint32_t stage = st * G::STAGE;
-            const uint32_t there = lds(sbase + G::THERE + st * 4);
+            const uint32_t there = load4(sbase + G::THERE + st * 4);
             // whether a key of the block exists: slots past the context hold anything
             auto exists = [&](int key) { return ((there >> (key >> cs)) & 1) && k0 + key < w.keys; };
             // ---- scores of 16 keys ----
@@ -371,7 +349,7 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
             for (int part = 0; part < PARTS; ++part)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    kp[part][h] = lds(k_pair + stage + part * pairs + h * eighth4);
+                    kp[part][h] = load4(k_pair + stage + part * pairs + h * eighth4);
             if (there != ~0u) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -387,7 +365,7 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
                 uint32_t sc[2], bi[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    v[h] = lds2(k_at + stage + part * plane + h * eighth);
+                    v[h] = load8(k_at + stage + part * plane + h * eighth);
                     sc[h] = kv4::both_scales(kp[part][h]), bi[h] = kv4::both_biases(kp[part][h]);
                 }
 #pragma unroll
@@ -403,7 +381,7 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
                         for (int i = 0; i < NT; ++i) {
                             const int at = part * 8 + u * 4 + k * 2;
                             if (NT == 4) {
-                                const uint2 q = lds2(sbase + G::QUERIES +
+                                const uint2 q = load8(sbase + G::QUERIES +
                                                      ((i * (QR / 4) + at / 4) * 32 + lane) * 16 + (at % 4) * 4);
                                 mma<DT>(s[i], a, q.x, q.y);
                             } else {
@@ -481,7 +459,7 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const uint32_t at = v_pair + stage + part * pairs + h * eighth4;
-                    vp[part][h][0] = lds(at), vp[part][h][1] = lds(at + v_next4);
+                    vp[part][h][0] = load4(at), vp[part][h][1] = load4(at + v_next4);
                 }
             if (there != ~0u) {
 #pragma unroll
@@ -498,7 +476,7 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const uint32_t at = v_at + stage + part * plane + h * eighth;
-                    const uint32_t x = lds(at), y = lds(at + v_next);
+                    const uint32_t x = load4(at), y = load4(at + v_next);
                     const uint32_t sc = __byte_perm(vp[part][h][0], vp[part][h][1], 0x5410),
                                    bi = __byte_perm(vp[part][h][0], vp[part][h][1], 0x7632);
                     kv4::expand<DT>(__byte_perm(x, y, 0x5410), sc, bi, constants, e[h][0]);

@@ -198,6 +198,37 @@ __device__ __forceinline__ void store32(void* d, const uint32_t* r)
                  : "memory");
 }
 
+// `bytes` of global memory to shared memory.
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t load4(uint32_t at)
+{
+    uint32_t r;
+    asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(r) : "r"(at) : "memory");
+    return r;
+}
+
+__device__ __forceinline__ uint2 load8(uint32_t at)
+{
+    uint2 r;
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];\n" : "=r"(r.x), "=r"(r.y) : "r"(at) : "memory");
+    return r;
+}
+
+__device__ __forceinline__ void load16(uint32_t at, uint32_t (&r)[4])
+{
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+
 // 16 bytes to shared memory.
 __device__ __forceinline__ void store16(uint32_t at, const uint32_t (&r)[4])
 {

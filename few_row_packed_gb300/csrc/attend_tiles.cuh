@@ -51,15 +51,17 @@ constexpr int kRows = 2 * kTile;                 // rows per item
 // 12 than with 24, 12 % less than with 48; 20 tokens over 3,943 keys 15.6 and 20.3 us.)
 constexpr int kExtra = 24, kNarrow = 3, kWide = 4, kMinUnits = 12;
 using Items = Shape<kRows, kKeys, kExtra, kNarrow, kWide, kTile>;
-// Warps: copies and MMAs, then the two streams; over a cache of 4 bits four more, which expand it.
+// Warps: copies and MMAs, then the two streams; over a cache of 4 bits four more, which expand what
+// the copies bring into the slots.
 template <bool KV4>
 struct Roles {
     static constexpr int THREADS = KV4 ? 512 : 384;
     // registers a thread after the split: 168 * 384 at launch = 88 * 128 + 208 * 256, and
     // 128 * 512 = (80 + 80) * 128 + 176 * 256
     static constexpr int CONTROL = KV4 ? 80 : 88, STREAM = KV4 ? 176 : 208, EXPAND = 80;
-    // who fills a slot, and who reads an item (fillers, MMAs, eight warps of the streams)
-    static constexpr int FILLERS = KV4 ? 4 : 1, READERS = FILLERS + 9;
+    // who fills a slot, and who reads an item (copies, MMAs, eight warps of the streams, and
+    // those that expand)
+    static constexpr int FILLERS = KV4 ? 4 : 1, READERS = KV4 ? 14 : 10;
 };
 
 constexpr int kItems = 4;                        // items the roles may be apart
@@ -79,16 +81,21 @@ struct alignas(16) Item {
 };
 static_assert(sizeof(Item) == 64, "ring entry");
 
-template <int D>
+template <int D, bool KV4>
 struct Geo {
     static constexpr int HALF = kKeys * 128;                // 64 elements of 128 rows
     static constexpr int SLOT = (D / 64) * HALF;            // one block's K or V; one Q tile
     static constexpr int Q = 0;
     static constexpr int RING = 2 * SLOT;
-    static constexpr int NSLOT = D == 128 ? 5 : 10;
-    static constexpr int BARS = RING + NSLOT * SLOT;
-    static constexpr int NBARS = 2 * NSLOT + 11 + 2 * kItems;
-    static constexpr int STATS = (BARS + NBARS * 8 + 15) / 16 * 16;   // [2][128] m and sums of the streams
+    static constexpr int NSLOT = (D == 128 ? 5 : 10) - (KV4 ? 128 / D : 0);
+    // 4 bits: a ring of a block's keys or values as they are held, codes and then scales
+    static constexpr int HELD = RING + NSLOT * SLOT;
+    static constexpr int CODES = kKeys * 32 * (D / 64), HSLOT = kKeys * 36 * (D / 64);
+    static constexpr int NHELD = KV4 ? (D == 128 ? 3 : 6) : 0;
+    static constexpr int BARS = HELD + NHELD * HSLOT;
+    static constexpr int NBARS = 2 * NSLOT + 11 + 2 * kItems + 2 * NHELD;
+    static constexpr int THERE = BARS + NBARS * 8;          // their chunks that exist
+    static constexpr int STATS = (THERE + NHELD * 4 + 15) / 16 * 16;   // [2][128] m and sums of the streams
     static constexpr int RATIOS = STATS + 2 * kTile * 8;    // [2][128] exact over rounded sums
     static constexpr int ITEMS = RATIOS + 2 * kTile * 2;    // ring of items
     static constexpr int WORDS = ITEMS + kItems * 64;       // tensor-memory address
@@ -135,7 +142,7 @@ __device__ __forceinline__ void store_q(const AttendParams& p, int q0, int kv_he
 #pragma unroll
     for (int ch = 0; ch < D / 8; ++ch) {
         v[ch].x ^= flip, v[ch].y ^= flip, v[ch].z ^= flip, v[ch].w ^= flip;
-        *reinterpret_cast<uint4*>(dst + (ch >> 3) * Geo<D>::HALF + (((ch & 7) ^ (trow & 7)) << 4)) = v[ch];
+        *reinterpret_cast<uint4*>(dst + (ch >> 3) * kKeys * 128 + (((ch & 7) ^ (trow & 7)) << 4)) = v[ch];
     }
     fence_proxy_async_smem();
 }
@@ -155,27 +162,9 @@ __device__ __forceinline__ void fetch_q(const AttendParams& p, int q0, int kv_he
 #pragma unroll
     for (int ch = 0; ch < D / 8; ++ch)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
-                         dst + (ch >> 3) * Geo<D>::HALF + (((ch & 7) ^ (trow & 7)) << 4)),
+                         dst + (ch >> 3) * kKeys * 128 + (((ch & 7) ^ (trow & 7)) << 4)),
                      "l"(src + (bytes ? ch * 8 : 0)), "r"(bytes)
                      : "memory");
-}
-
-// The values of a row as it is held to row `row` of a slot at `dst`, in the layout of the
-// copies.
-template <int DT, int D>
-__device__ __forceinline__ void expand_row(const kv4::Held<D>& h, const kv4::Constants& c, uint32_t dst, int row)
-{
-#pragma unroll
-    for (int part = 0; part < D / 64; ++part) {
-        const uint32_t s = kv4::both_scales(h.scales(part)), b = kv4::both_biases(h.scales(part));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            uint32_t v[4];
-            kv4::expand<DT>(h.codes[part][i], s, b, c, v);
-            store16(((dst + row * 128 + ((row & 7) << 4)) ^ (i << 4)) + part * Geo<D>::HALF, v);
-        }
-    }
-    fence_proxy_async_smem();
 }
 
 template <int DT, int D, bool KV4>
@@ -184,7 +173,7 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
                             const __grid_constant__ CUtensorMap kmap,
                             const __grid_constant__ CUtensorMap vmap)
 {
-    using G = Geo<D>;
+    using G = Geo<D, KV4>;
     using R = Roles<KV4>;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t sbase = smem_u32(smem);
@@ -201,6 +190,8 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
     auto item_empty = [&](int i) { return bar(2 * G::NSLOT + 9 + kItems + i % kItems); };
     const uint32_t mmas_done = bar(2 * G::NSLOT + 9 + 2 * kItems);   // every MMA of the CTA
     const uint32_t together = bar(2 * G::NSLOT + 10 + 2 * kItems);   // both streams have come as far
+    auto held_full = [&](int i) { return bar(2 * G::NSLOT + 11 + 2 * kItems + i); };
+    auto held_empty = [&](int i) { return bar(2 * G::NSLOT + 11 + 2 * kItems + G::NHELD + i); };
     const Item* items = reinterpret_cast<const Item*>(smem + G::ITEMS);
 
     if (tid == 0) {
@@ -216,6 +207,10 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
             mbar_init(p_full(s, 0), 4);
             mbar_init(p_full(s, 1), 4);
             mbar_init(o_done(s), 1);
+        }
+        for (int i = 0; i < G::NHELD; ++i) {
+            mbar_init(held_full(i), 1);
+            mbar_init(held_empty(i), 4);
         }
         for (int i = 0; i < kItems; ++i) {
             mbar_init(item_full(i), 1);
@@ -254,7 +249,68 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(R::CONTROL));
-        if (warp == 0 && !KV4) {
+        if (KV4 && warp == 0) {
+            // ---- copies as the rows are held: K and V of each block in turn; lanes 2 i and
+            // 2 i + 1 have the codes and the scales of chunk i ----
+            const int cs = kv4::chunk_shift(p.kv), chunk0 = (lane >> 1) << cs;
+            const int64_t page_bytes = kv4::page_bytes(p.kv);
+            const uint32_t size = lane & 1 ? 4 * (D / 64) << cs : 32 * (D / 64) << cs;
+            int n = 0;                                               // copies so far
+            for (int it = 0;; ++it) {
+                const Item& w = item_at(it);
+                if (!ok || w.nb == 0)
+                    break;
+                const int* table = p.batch.block_table + (int64_t)w.r * p.batch.table_stride;
+                const uint8_t* base = kv4::chunk(p.kv, 0, w.head, 0) + (lane & 1 ? D << cs : 0);
+                auto page_of = [&](int j) {                          // of the chunk in block j, -1: zeros
+                    const int key = w.key_of(j) + chunk0;
+                    return j < w.nb && chunk0 < kKeys && wanted(p, w.lo, w.hi, key, 1 << cs)
+                               ? table[key >> p.kv.page_shift]
+                               : -1;
+                };
+                int page = -1, next = page_of(0);
+                for (int i = 0; i < 2 * w.nb; ++i) {
+                    const int st = n % max(G::NHELD, 1), k0 = w.key_of(i >> 1);
+                    if ((i & 1) == 0) {
+                        page = next;
+                        next = page_of((i >> 1) + 1);
+                    }
+                    // read, and its last copy landed (see attend_rows.cu)
+                    if (n >= G::NHELD) {
+                        wait(held_empty(st), (uint32_t)((n / max(G::NHELD, 1) - 1) & 1));
+                        wait(held_full(st), (uint32_t)((n / max(G::NHELD, 1) - 1) & 1));
+                    }
+                    ok = __all_sync(0xffffffffu, ok && ((unsigned)n < p.first_copies || blockIdx.x > 0));
+                    if (!ok)
+                        break;
+                    ++n;
+                    const bool go = page >= 0 && page < p.kv.pages;
+                    const unsigned there = __ballot_sync(0xffffffffu, go);
+                    if (lane == 0) {
+                        // all ones: every key of the block exists
+                        const int chunks = __popc(there) / 2;
+                        reinterpret_cast<uint32_t*>(smem + G::THERE)[st] =
+                            chunks == kKeys >> cs && k0 + kKeys <= w.keys ? ~0u : there & 0x55555555u;
+                        mbar_expect_tx(held_full(st), chunks * (36 * (D / 64) << cs));
+                    }
+                    __syncwarp();
+                    if (go) {
+                        const int s = (k0 + chunk0) & ((1 << p.kv.page_shift) - 1);
+                        bulk_copy(sbase + G::HELD + st * G::HSLOT + (lane & 1 ? G::CODES : 0) + (lane >> 1) * size,
+                                  base + page * page_bytes + (s >> cs) * (kv4::slot_bytes(D) << cs) + (i & 1) * size,
+                                  size, held_full(st));
+                    }
+                }
+                __syncwarp();                                        // every lane has read the item
+                if (lane == 0)
+                    mbar_arrive(item_empty(it));
+            }
+            // the copies land before shared memory goes away, also after a wait that ran out
+            for (int i = 0; i < G::NHELD; ++i)
+                if (n - 1 - i >= 0 && !mbar_wait(held_full((n - 1 - i) % max(G::NHELD, 1)),
+                                                 (uint32_t)(((n - 1 - i) / max(G::NHELD, 1)) & 1), p.wait_limit))
+                    ok = false;
+        } else if (warp == 0) {
             // ---- copies: K and V of each block in turn ----
             if (lane == 0) {
                 prefetch_map(&kmap);
@@ -444,55 +500,59 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
     } else if (KV4 && warp >= 12) {
         // ---- a cache of 4 bits: one key of a block a thread, its K and its V in turn ----
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(R::EXPAND));
-        const int row = tid & 127, cs = kv4::chunk_shift(p.kv);
-        const int64_t page_bytes = kv4::page_bytes(p.kv);
+        const int row = tid & 127, cs = kv4::chunk_shift(p.kv), chunk = row >> cs;
+        const int first = ((chunk * (D / 64) - chunk) << cs) + row;  // its first row of codes
+        const uint32_t codes = sbase + G::HELD + first * 32, pairs = sbase + G::HELD + G::CODES + first * 4;
+        // (the vector of codes goes first that leaves the lanes' banks apart)
+        const int turn = (row >> 2) & 1;
+        const uint32_t to = sbase + G::RING + row * 128 + (((row & 7) ^ (turn << 2)) << 4);
         const kv4::Constants constants = kv4::constants<DT>();
-        int n = 0;                                               // slots filled
+        int n = 0;                                                   // slots filled
         for (int it = 0;; ++it) {
             const Item& w = item_at(it);
             if (!ok || w.nb == 0)
                 break;
-            const int* table = p.batch.block_table + (int64_t)w.r * p.batch.table_stride;
-            auto page_at = [&](int j) {                          // of this thread's key in block j, -1: zeros
-                const int key = w.key_of(j) + row;
-                return j < w.nb && wanted(p, w.lo, w.hi, key, 1) ? table[key >> p.kv.page_shift] : -1;
-            };
-            const uint8_t* base = kv4::chunk(p.kv, 0, w.head, 0);
-            auto slot_at = [&](int page, int j) {
-                return kv4::slot_of<D>(base, page_bytes, page < p.kv.pages ? page : -1,
-                                       (w.key_of(j) + row) & ((1 << p.kv.page_shift) - 1), cs);
-            };
-            // Fills the next slot; false if it gave up.
-            auto fill = [&](const kv4::Held<D>& h) {
-                const int st = n % G::NSLOT;
+            for (int i = 0; i < 2 * w.nb; ++i) {
+                const int st = n % max(G::NHELD, 1), slot = n % G::NSLOT;
+                wait(held_full(st), (uint32_t)((n / max(G::NHELD, 1)) & 1));
+                const uint32_t at = st * G::HSLOT, there = load4(sbase + G::THERE + 4 * st);
+                uint32_t held[D / 32][4], pair[D / 64];
+#pragma unroll
+                for (int part = 0; part < D / 64; ++part) {
+                    load16((codes + at + (part * 32 << cs)) ^ (turn << 4), held[2 * part]);
+                    load16((codes + at + (part * 32 << cs)) ^ ((turn ^ 1) << 4), held[2 * part + 1]);
+                    pair[part] = load4(pairs + at + (part * 4 << cs));
+                }
+                // slots past the context hold anything
+                if (there != ~0u && !(((there >> (2 * chunk)) & 1) && w.key_of(i >> 1) + row < w.keys)) {
+#pragma unroll
+                    for (int part = 0; part < D / 64; ++part)
+                        pair[part] = 0;
+                }
                 if (n >= G::NSLOT)
-                    wait(empty(st), (uint32_t)((n / G::NSLOT - 1) & 1));
-                ok = __all_sync(0xffffffffu, ok && ((unsigned)n < p.first_copies || blockIdx.x > 0));
+                    wait(empty(slot), (uint32_t)((n / G::NSLOT - 1) & 1));
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok)
-                    return false;
+                    break;
                 ++n;
-                expand_row<DT, D>(h, constants, sbase + G::RING + st * G::SLOT, row);
+                if (lane == 0)                                       // every lane has read
+                    mbar_arrive(held_empty(st));
+#pragma unroll
+                for (int part = 0; part < D / 64; ++part) {
+                    const uint32_t sc = kv4::both_scales(pair[part]), bi = kv4::both_biases(pair[part]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        uint32_t v[4];
+                        kv4::expand<DT>(held[2 * part + (e >> 2)][e & 3], sc, bi, constants, v);
+                        store16((to ^ (e << 4)) + slot * G::SLOT + part * G::HALF, v);
+                    }
+                }
+                fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(full(st));
-                return true;
-            };
-            // what a thread waits for is asked for while the slot before it is filled: V during
-            // K, the next block's K during V, its page a block ahead
-            kv4::Held<D> k, v;
-            kv4::Slot at = slot_at(page_at(0), 0);
-            k.load(at, 0, cs);
-            for (int j = 0; j < w.nb; ++j) {
-                const int next = page_at(j + 1);
-                v.load(at, 1, cs);
-                if (!fill(k))
-                    break;
-                at = slot_at(next, j + 1);
-                k.load(at, 0, cs);
-                if (!fill(v))
-                    break;
+                    mbar_arrive(full(slot));
             }
-            __syncwarp();                                        // every lane has read the item
+            __syncwarp();                                            // every lane has read the item
             if (lane == 0)
                 mbar_arrive(item_empty(it));
         }
@@ -815,11 +875,11 @@ cudaError_t launch(const AttendParams& p, const CUtensorMap& kmap, const CUtenso
 {
     auto kernel = lbv_attend_tiles_kernel<DT, D, KV4>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         Geo<D>::BYTES);
+                                         Geo<D, KV4>::BYTES);
     if (e != cudaSuccess)
         return e;
     const int ctas = sms < kAttendMaxCtas ? sms : kAttendMaxCtas;
-    e = launch_after(kernel, dim3((unsigned)ctas), Roles<KV4>::THREADS, Geo<D>::BYTES, st, p, kmap, vmap);
+    e = launch_after(kernel, dim3((unsigned)ctas), Roles<KV4>::THREADS, Geo<D, KV4>::BYTES, st, p, kmap, vmap);
     return e == cudaSuccess ? launch_attend_join(p, (lbv_dtype)DT, kRows, ctas, st) : e;
 }
 

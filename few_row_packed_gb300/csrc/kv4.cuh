@@ -56,60 +56,6 @@ __device__ __forceinline__ int scale_at(int planes, int plane, int s, int cs)
     return (planes * 32 << cs) + ((plane << cs) + s) * 4;
 }
 
-// 32 bytes from a 32-byte-aligned address: a row of codes in one load.
-__device__ __forceinline__ void load32(const void* src, uint32_t (&r)[8])
-{
-    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "l"(src)
-                 : "memory");
-}
-
-// A slot of a head: its first row of codes, and its first scale and bias.  A slot that
-// does not exist reads as zeros: its codes are those of any slot, without scales.
-struct Slot {
-    const uint8_t* codes;
-    const uint8_t* scales;
-    bool there;
-};
-
-// Slot s of a page (-1: none) of a head, whose pages begin at `base` + page * page_bytes.
-template <int D>
-__device__ __forceinline__ Slot slot_of(const uint8_t* base, int64_t page_bytes, int page, int s, int cs)
-{
-    Slot x;
-    x.there = page >= 0;
-    const uint8_t* chunk = base + (x.there ? page : 0) * page_bytes + (s >> cs) * (D / 64 * kSlotBytes << cs);
-    s &= (1 << cs) - 1;
-    x.codes = chunk + s * 32;
-    x.scales = chunk + (D << cs) + s * 4;
-    return x;
-}
-
-// A key's or a value's row as it is held.
-template <int D>
-struct Held {
-    uint32_t codes[D / 64][8];
-    uint32_t pairs[D / 64];
-    bool there;
-
-    // The key (which 0) or value (1) of a slot.
-    __device__ __forceinline__ void load(const Slot& s, int which, int cs)
-    {
-#pragma unroll
-        for (int part = 0; part < D / 64; ++part) {
-            const int plane = which * (D / 64) + part;
-            load32(s.codes + (plane * 32 << cs), codes[part]);
-            pairs[part] = *reinterpret_cast<const volatile uint32_t*>(s.scales + (plane * 4 << cs));
-        }
-        there = s.there;
-    }
-
-    // (scale, bias) of 64 elements.  (Not before they are used: whoever looks at them waits for
-    // the load.)
-    __device__ __forceinline__ uint32_t scales(int part) const { return there ? pairs[part] : 0u; }
-};
-
 // (x & mask) | bits, in one instruction.
 template <uint32_t MASK>
 __device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t bits)
