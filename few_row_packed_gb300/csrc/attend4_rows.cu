@@ -10,8 +10,9 @@
 //     so that 8 rows (a decoded token's query heads) take half the instructions that they
 //     take as rows.  Codes are expanded in the registers of the lane that holds them as an
 //     operand, once for all rows of the item: which element a place of the contraction
-//     stands for is free, so a lane takes 16 neighbours of a key (8 bytes of codes) and, of
-//     a value, the same 8 elements of two keys (two permutes bring them together).  The
+//     stands for is free, so a lane takes a quarter of a key (in one load, with one
+//     scale and bias) and, of a value, the same eighth of two keys (two permutes a word bring
+//     them together).  The
 //     probabilities change places by movmatrix.
 //   * A team of four warps has a share of the batch.  A warp has 16 keys of every block and
 //     a running maximum, sums and results of its own: the warps meet at an item's ends alone.
@@ -36,10 +37,13 @@ using namespace att;
 
 namespace {
 
-constexpr int kBlock = 64;                       // keys per block
-constexpr int kKeyWarps = 4, kTeam = kKeyWarps * 32;
+// Keys per block, 16 a warp.  (128, 32 a warp, save what a block costs beside its keys, and divide
+// small batches less evenly: 64 requests of one token 101 us in place of 107, a window of
+// 2,048 over 32 requests 33 in place of 29, four tokens after 200,000 108 in place of 93.)
+constexpr int kBlock = 64;
 // Units of an item beside its blocks, and the least share of a team.
 constexpr int kExtra = 3, kMinUnits = 2;
+constexpr int kKeyWarps = 4, kTeam = kKeyWarps * 32;
 // A reference that every score passes, negated: nothing has been seen yet.
 constexpr float kNone = 1e30f;
 constexpr int kItems = 8;                        // items that a team's warps may be apart: stages, and one
@@ -60,9 +64,9 @@ template <int D, int NT>
 struct Geo {
     static constexpr int ROWS = 8 * NT;
     // teams on an SM, and registers a thread after the split: 96 * 640 at launch = 104 * 512 +
-    // 64 * 128, 128 * 512 = 152 * 384 + 56 * 128, 168 * 384 = 232 * 256 + 40 * 128
-    static constexpr int TEAMS = NT == 1 ? 4 : NT == 2 ? 3 : 2;
-    static constexpr int REGS = NT == 1 ? 104 : NT == 2 ? 152 : 232, HELPER = NT == 1 ? 64 : NT == 2 ? 56 : 40;
+    // 64 * 128, 128 * 512 = 152 * 384 + 56 * 128
+    static constexpr int TEAMS = NT == 1 ? 4 : 3;
+    static constexpr int REGS = NT == 1 ? 104 : 152, HELPER = NT == 1 ? 64 : 56;
     static constexpr int THREADS = TEAMS * kTeam + 128;
     static constexpr int STAGE = kBlock * 72 * (D / 64);
     static constexpr int NST = D == 64 ? 6 : 4;
@@ -70,9 +74,9 @@ struct Geo {
     // a team's shared memory: the ring, the warps' results, queries of more than two tiles as
     // the lanes hold them
     static constexpr int JOIN = NST * STAGE;
-    static constexpr int JROWS = NT == 4 ? 16 : ROWS;       // rows joined at a time
+    static constexpr int JROWS = NT == 3 ? 8 : ROWS;       // rows joined at a time
     static constexpr int QUERIES = JOIN + kKeyWarps * JROWS * D * 4;
-    static constexpr int STATS = QUERIES + (NT == 4 ? NT * 32 * (D / 8) * 4 : 0);   // [4][ROWS] maxima, sums
+    static constexpr int STATS = QUERIES + (NT == 3 ? NT * 32 * (D / 8) * 4 : 0);   // [4][ROWS] maxima, sums
     static constexpr int ITEMS = STATS + 2 * kKeyWarps * ROWS * 4;
     static constexpr int START = ITEMS;                     // where the share begins, before its first item
     static constexpr int BARS = ITEMS + kItems * 48;        // full, empty, items
@@ -247,13 +251,19 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
     auto codes_of = [&](int key) { return (key >> cs) * chunk_bytes + (key & ((1 << cs) - 1)) * 32; };
     auto pair_of = [&](int key) { return (key >> cs) * chunk_bytes + (D << cs) + (key & ((1 << cs) - 1)) * 4; };
     const int k_key = warp * 16 + key_at(g), v_key0 = warp * 16 + key_at(2 * t), v_key1 = warp * 16 + key_at(2 * t + 1);
-    const uint32_t plane = 32u << cs, pairs = 4u << cs;      // from one plane to the next
-    const uint32_t eighth = cs == 3 ? (uint32_t)chunk_bytes : 256u;      // eight keys on: codes, pairs
-    const uint32_t eighth4 = cs == 3 ? (uint32_t)chunk_bytes : 32u;
-    const uint32_t k_at = sbase + codes_of(k_key) + t * 8, k_pair = sbase + pair_of(k_key);
-    const uint32_t v_at = sbase + codes_of(v_key0) + PARTS * plane + g * 4,
-                   v_pair = sbase + pair_of(v_key0) + PARTS * pairs;
-    const int v_next = (v_key1 - v_key0) * 32, v_next4 = (v_key1 - v_key0) * 4;
+    // eight keys on: codes, pairs
+    const uint32_t far = (uint32_t)chunk_bytes;
+    const uint32_t eight = cs == 3 ? far : 256u, eight4 = cs == 3 ? far : 32u;
+    // a quarter of a key, a lane's own t-th; an eighth of two values, its g-th: the plane of 64
+    // elements it is in, and the bytes in a row of it
+    const uint32_t k_part = D == 128 ? t >> 1 : 0, v_part = PARTS + (D == 128 ? g >> 2 : 0);
+    const uint32_t k_at = sbase + codes_of(k_key) + (k_part * 32 << cs) + (D == 128 ? (t & 1) * 16 : t * 8),
+                   k_pair = sbase + pair_of(k_key) + (k_part * 4 << cs);
+    const uint32_t v_bytes = (v_part * 32 << cs) + (D == 128 ? (g & 3) * 8 : g * 4);
+    const uint32_t v_at0 = sbase + codes_of(v_key0) + v_bytes, v_at1 = sbase + codes_of(v_key1) + v_bytes;
+    // The two values' pairs are neighbours, for t >= 2 the other way round: what to take of them.
+    const uint32_t v_pair = sbase + pair_of(warp * 16 + 2 * t) + (v_part * 4 << cs);
+    const uint32_t take_scales = t < 2 ? 0x5410 : 0x1054, take_biases = t < 2 ? 0x7632 : 0x3276;
     const kv4::Constants constants = kv4::constants<DT>();
     // scores are c times the products; a scale of zero clears Q
     const float c = p.scale_log2 == 0.f ? 1.f : p.scale_log2;
@@ -273,9 +283,9 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
             break;
         const Item& w = items[it % kItems];
         const int nb = w.nb, item_rows = w.rows;
-        // The queries as the second operand: lane (g, t) has elements 16 t to 16 t + 15 of each
-        // part of row g, a pair a register.
-        constexpr int QR = D / 8, QT = NT == 4 ? 1 : NT;         // registers a tile; tiles kept in them
+        // The queries as the second operand: lane (g, t) has the t-th quarter of row g, a pair of
+        // elements a register.
+        constexpr int QR = D / 8, QT = NT == 3 ? 1 : NT;         // registers a tile; tiles kept in them
         uint32_t qf[QT][QR];
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
@@ -283,38 +293,34 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
             const bool in = 8 * i + g < item_rows && p.scale_log2 != 0.f;
             const int tok = token_of(p, row);
             const uint16_t* src = p.q + (int64_t)(w.q0 + (in ? tok : 0)) * p.q_token +
-                                  (int64_t)(w.head * p.group + (in ? row - tok * p.group : 0)) * p.q_head + t * 16;
-            uint32_t(&q)[QR] = qf[NT == 4 ? 0 : i];
+                                  (int64_t)(w.head * p.group + (in ? row - tok * p.group : 0)) * p.q_head + t * (D / 4);
+            uint32_t(&q)[QR] = qf[NT == 3 ? 0 : i];
+            if (!in) {
 #pragma unroll
-            for (int part = 0; part < PARTS; ++part) {
-                if (!in) {
+                for (int e = 0; e < QR; ++e)
+                    q[e] = 0;
+            } else if (p.q_wide) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        q[part * 8 + e] = 0;
-                } else if (p.q_wide) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(src + part * 64 + h * 8);
-                        q[part * 8 + 4 * h] = v.x, q[part * 8 + 4 * h + 1] = v.y;
-                        q[part * 8 + 4 * h + 2] = v.z, q[part * 8 + 4 * h + 3] = v.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        q[part * 8 + e] = (uint32_t)src[part * 64 + 2 * e] | ((uint32_t)src[part * 64 + 2 * e + 1] << 16);
+                for (int h = 0; h < QR / 4; ++h) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(src + h * 8);
+                    q[4 * h] = v.x, q[4 * h + 1] = v.y, q[4 * h + 2] = v.z, q[4 * h + 3] = v.w;
                 }
+            } else {
+#pragma unroll
+                for (int e = 0; e < QR; ++e)
+                    q[e] = (uint32_t)src[2 * e] | ((uint32_t)src[2 * e + 1] << 16);
             }
             // (the same for every warp, and each writes it all: the values are alike)
-            if (NT == 4) {
+            if (NT == 3) {
 #pragma unroll
                 for (int e = 0; e < QR / 4; ++e)
                     *reinterpret_cast<uint4*>(smem + G::QUERIES + ((i * (QR / 4) + e) * 32 + lane) * 16) =
                         make_uint4(q[4 * e], q[4 * e + 1], q[4 * e + 2], q[4 * e + 3]);
             }
         }
-        if (NT == 4)
+        if (NT == 3)
             named_bar_sync(bar, kTeam);
-        float o[NT][D / 16][4];                                  // tile (part, i): elements 64 part + 8 g + 2 i, and the next
+        float o[NT][D / 16][4];                                  // tile j: elements g D / 8 + 2 j, and the next
         float2 minus[NT], l[NT];                                 // references, negated, and sums of rows 2 t and 2 t + 1
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
@@ -335,54 +341,53 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
             const int st = n % G::NST, k0 = w.key_of(j);
             if (ok)
                 ok = mbar_wait(full(st), (uint32_t)((n / G::NST) & 1), p.wait_limit);
-            const uint32_t stage = st * G::STAGE;
             const uint32_t there = load4(sbase + G::THERE + st * 4);
             // whether a key of the block exists: slots past the context hold anything
             auto exists = [&](int key) { return ((there >> (key >> cs)) & 1) && k0 + key < w.keys; };
+            const uint32_t stage = st * G::STAGE;
             // ---- scores of 16 keys ----
             float s[NT][4];
 #pragma unroll
             for (int i = 0; i < NT; ++i)
                 s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
-            uint32_t kp[PARTS][2];                               // (scale, bias) of rows g and g + 8
+            {
+                constexpr int W = D / 32;                        // words of 8 elements
+                uint32_t v[2][W], sc[2], bi[2];
 #pragma unroll
-            for (int part = 0; part < PARTS; ++part)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    kp[part][h] = load4(k_pair + stage + part * pairs + h * eighth4);
-            if (there != ~0u) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (!exists(k_key + 8 * h)) {
-#pragma unroll
-                        for (int part = 0; part < PARTS; ++part)
-                            kp[part][h] = 0;
+                for (int h = 0; h < 2; ++h) {                    // rows g and g + 8
+                    if constexpr (W == 4) {
+                        load16(k_at + stage + h * eight, v[h]);
+                    } else {
+                        const uint2 x = load8(k_at + stage + h * eight);
+                        v[h][0] = x.x, v[h][1] = x.y;
                     }
-            }
+                    sc[h] = load4(k_pair + stage + h * eight4);
+                }
+                if (there != ~0u) {
 #pragma unroll
-            for (int part = 0; part < PARTS; ++part) {
-                uint2 v[2];
-                uint32_t sc[2], bi[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    v[h] = load8(k_at + stage + part * plane + h * eighth);
-                    sc[h] = kv4::both_scales(kp[part][h]), bi[h] = kv4::both_biases(kp[part][h]);
+                    for (int h = 0; h < 2; ++h)
+                        sc[h] = exists(k_key + 8 * h) ? sc[h] : 0u;
                 }
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {                    // words of 8 elements
+                for (int h = 0; h < 2; ++h) {
+                    bi[h] = kv4::both_biases(sc[h]);
+                    sc[h] = kv4::both_scales(sc[h]);
+                }
+#pragma unroll
+                for (int u = 0; u < W; ++u) {
                     uint32_t e[2][4];
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        kv4::expand<DT>(u ? v[h].y : v[h].x, sc[h], bi[h], constants, e[h]);
+                        kv4::expand<DT>(v[h][u], sc[h], bi[h], constants, e[h]);
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {                // 4 of them a step
                         const uint32_t a[4] = {e[0][2 * k], e[1][2 * k], e[0][2 * k + 1], e[1][2 * k + 1]};
 #pragma unroll
                         for (int i = 0; i < NT; ++i) {
-                            const int at = part * 8 + u * 4 + k * 2;
-                            if (NT == 4) {
+                            const int at = u * 4 + k * 2;
+                            if (NT == 3) {
                                 const uint2 q = load8(sbase + G::QUERIES +
-                                                     ((i * (QR / 4) + at / 4) * 32 + lane) * 16 + (at % 4) * 4);
+                                                      ((i * (QR / 4) + at / 4) * 32 + lane) * 16 + (at % 4) * 4);
                                 mma<DT>(s[i], a, q.x, q.y);
                             } else {
                                 mma<DT>(s[i], a, qf[i][at], qf[i][at + 1]);
@@ -392,7 +397,8 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
                 }
             }
             // ---- their probabilities ----
-            if (k0 + warp * 16 + 16 > open_hi || k0 + warp * 16 < open_lo) {     // rare, so short code
+            const int key0 = k0 + warp * 16;
+            if (key0 + 16 > open_hi || key0 < open_lo) {         // rare, so short code
                 Request q;
                 q.first = w.first, q.keys = w.keys;
                 uint32_t see = 0;
@@ -400,7 +406,7 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
                 for (int e = 0; e < 4 * NT; ++e) {
                     const int r = (e >> 2) * 8 + 2 * t + (e & 1), tok = token_of(p, w.row0 + r);
                     const uint64_t word = p.tree && r < item_rows ? p.tree[w.q0 + tok] : 0;
-                    if (r < item_rows && sees(p, q, q.first + tok, word, k0 + k_key + ((e >> 1) & 1) * 8))
+                    if (r < item_rows && sees(p, q, q.first + tok, word, key0 + key_at(g) + ((e >> 1) & 1) * 8))
                         see |= 1u << e;
                 }
 #pragma unroll
@@ -453,42 +459,40 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
                     pf[i][h] = transposed(pack2<DT>(y.x, y.y));
                 }
             // ---- and their values ----
-            uint32_t vp[PARTS][2][2];                            // (scale, bias) of a lane's four keys
-#pragma unroll
-            for (int part = 0; part < PARTS; ++part)
+            {
+                constexpr int W = D / 64;                        // words of 8 elements
+                uint32_t e[W][2][2][4];                          // pairs of keys, even and odd elements
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint32_t at = v_pair + stage + part * pairs + h * eighth4;
-                    vp[part][h][0] = load4(at), vp[part][h][1] = load4(at + v_next4);
-                }
-            if (there != ~0u) {
-#pragma unroll
-                for (int h = 0; h < 4; ++h)
-                    if (!exists((h & 1 ? v_key1 : v_key0) + 8 * (h >> 1))) {
-#pragma unroll
-                        for (int part = 0; part < PARTS; ++part)
-                            vp[part][h >> 1][h & 1] = 0;
+                    uint32_t x[W], y[W];
+                    if constexpr (W == 2) {
+                        const uint2 a = load8(v_at0 + stage + h * eight), b = load8(v_at1 + stage + h * eight);
+                        x[0] = a.x, x[1] = a.y, y[0] = b.x, y[1] = b.y;
+                    } else {
+                        x[0] = load4(v_at0 + stage + h * eight), y[0] = load4(v_at1 + stage + h * eight);
                     }
-            }
+                    uint2 f = load8(v_pair + stage + h * eight4);
+                    if (there != ~0u) {
+                        const int key = warp * 16 + 8 * h + 2 * t;
+                        f.x = exists(key) ? f.x : 0u;
+                        f.y = exists(key + 1) ? f.y : 0u;
+                    }
+                    const uint32_t sc = __byte_perm(f.x, f.y, take_scales), bi = __byte_perm(f.x, f.y, take_biases);
 #pragma unroll
-            for (int part = 0; part < PARTS; ++part) {
-                uint32_t e[2][2][4];                             // keys' halves, even and odd elements
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t at = v_at + stage + part * plane + h * eighth;
-                    const uint32_t x = load4(at), y = load4(at + v_next);
-                    const uint32_t sc = __byte_perm(vp[part][h][0], vp[part][h][1], 0x5410),
-                                   bi = __byte_perm(vp[part][h][0], vp[part][h][1], 0x7632);
-                    kv4::expand<DT>(__byte_perm(x, y, 0x5410), sc, bi, constants, e[h][0]);
-                    kv4::expand<DT>(__byte_perm(x, y, 0x7632), sc, bi, constants, e[h][1]);
+                    for (int u = 0; u < W; ++u) {
+                        kv4::expand<DT>(__byte_perm(x[u], y[u], 0x5410), sc, bi, constants, e[u][h][0]);
+                        kv4::expand<DT>(__byte_perm(x[u], y[u], 0x7632), sc, bi, constants, e[u][h][1]);
+                    }
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t a[4] = {e[0][0][j], e[0][1][j], e[1][0][j], e[1][1][j]};
+                for (int u = 0; u < W; ++u)
 #pragma unroll
-                    for (int i = 0; i < NT; ++i)
-                        mma<DT>(o[i][part * 4 + j], a, pf[i][0], pf[i][1]);
-                }
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t a[4] = {e[u][0][0][j], e[u][0][1][j], e[u][1][0][j], e[u][1][1][j]};
+#pragma unroll
+                        for (int i = 0; i < NT; ++i)
+                            mma<DT>(o[i][u * 4 + j], a, pf[i][0], pf[i][1]);
+                    }
             }
             __syncwarp();
             if (lane == 0)
@@ -531,14 +535,11 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
                 for (int h = 0; h < 2; ++h) {
                     const int tile = r0 / 8 + i, r = 8 * tile + 2 * t + h;
                     const float f = ex2((h ? -minus[tile].y : -minus[tile].x) - top_of(r));
-                    float* d = joint + (warp * G::JROWS + 8 * i + 2 * t + h) * D + 8 * g;
+                    float* d = joint + (warp * G::JROWS + 8 * i + 2 * t + h) * D + g * (D / 8);
 #pragma unroll
-                    for (int part = 0; part < PARTS; ++part)
-#pragma unroll
-                        for (int j = 0; j < 4; j += 2)
-                            *reinterpret_cast<float4*>(d + part * 64 + 2 * j) =
-                                make_float4(f * o[tile][part * 4 + j][h], f * o[tile][part * 4 + j][2 + h],
-                                            f * o[tile][part * 4 + j + 1][h], f * o[tile][part * 4 + j + 1][2 + h]);
+                    for (int j = 0; j < D / 16; j += 2)
+                        *reinterpret_cast<float4*>(d + 2 * j) = make_float4(f * o[tile][j][h], f * o[tile][j][2 + h],
+                                                                            f * o[tile][j + 1][h], f * o[tile][j + 1][2 + h]);
                 }
             named_bar_sync(bar, kTeam);
             const int rows = min(G::JROWS, item_rows - r0);
@@ -589,7 +590,7 @@ template <int DT, int D>
 cudaError_t launch_rows(const AttendParams& p, int sms, cudaStream_t st)
 {
     const int64_t rows = attend_average_rows(p);
-    return rows <= 8 ? launch<DT, D, 1>(p, sms, st) : rows <= 16 ? launch<DT, D, 2>(p, sms, st) : launch<DT, D, 4>(p, sms, st);
+    return rows <= 8 ? launch<DT, D, 1>(p, sms, st) : rows <= 16 ? launch<DT, D, 2>(p, sms, st) : launch<DT, D, 3>(p, sms, st);
 }
 
 }  // namespace
@@ -604,8 +605,8 @@ cudaError_t launch_attend4_rows(const AttendParams& p, const CUtensorMap&, const
 
 size_t attend4_rows_partial_floats(int dim, int sms)
 {
-    // two slots a team: two teams an SM with 32 rows, more than three with 16 or four with 8
-    return (size_t)2 * 2 * std::min(sms, kAttendMaxCtas / 2) * 32 * (dim + 3);
+    // two slots a team: three teams an SM with 24 rows, more than four with 8
+    return (size_t)2 * 3 * std::min(sms, kAttendMaxCtas / 3) * 24 * (dim + 3);
 }
 
 }  // namespace lbv

@@ -552,7 +552,7 @@ static lbv_status attend(const char* fn, const lbv_kv_cache* cache, const lbv_ba
     p.first_copies = copies < 0 ? ~0u : (unsigned)copies;
     // both kernels are right for every length
     const int64_t rows = lbv::attend_average_rows(p);
-    const auto launch = p.kv.packed ? (rows <= 16 ? lbv::launch_attend4_rows : lbv::launch_attend4_tiles)
+    const auto launch = p.kv.packed ? (rows <= 24 ? lbv::launch_attend4_rows : lbv::launch_attend4_tiles)
                                     : (rows <= 16 ? lbv::launch_attend_rows : lbv::launch_attend_tiles);
     const cudaError_t e = launch(p, cache->kmap, cache->vmap, cache->dtype, cache->sms,
                                  (cudaStream_t)stream);
