@@ -4,10 +4,11 @@
 // as codes of 4 bits between its bounds:
 //     bias = round16(min x), scale = round16((max x - min x) / 15),
 //     code = round((x - bias) * (1 / scale)) in 0..15.
-// A thread has 8 neighbours of a head, so a group is 8 lanes, whose minimum and maximum
-// meet in three exchanges, and whose codes are 32 neighbouring bytes.  With halves
-// that pair up, a thread loads its elements' partners too: they are another thread's own, so
-// they come from L1, and any rotated part of a head is treated alike.
+// Queries are items of two groups of four elements, as in rope_append.cu.  Of keys and values
+// a thread has 8 neighbours, so a group of 64 is 8 lanes, whose minimum and maximum meet in three
+// exchanges, and whose codes are 32 neighbouring bytes.  With halves that pair up it loads
+// its elements' partners when it rotates them: they are another thread's own, so they
+// come from L1, and any rotated part of a head is treated alike.
 //
 // A code is a decision: values that differ in their last bit may fall on two sides of a
 // border.  So the arithmetic is that of elementary fp32 operations, the angle in
@@ -27,23 +28,7 @@ using namespace rope;
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;             // pieces of 8 elements a thread keeps in flight
-
-// Where a piece comes from and goes to.
-struct Piece {
-    int which;             // 0 q, 1 k, 2 v
-    int head, at;          // its first element in the head
-};
-
-__device__ __forceinline__ Piece piece_of(const RopeParams& p, int it, int per_head_shift)
-{
-    Piece m;
-    const int row = it >> per_head_shift;
-    m.which = row < p.q_heads ? 0 : row < p.q_heads + p.kv.heads ? 1 : 2;
-    m.head = m.which == 0 ? row : m.which == 1 ? row - p.q_heads : row - p.q_heads - p.kv.heads;
-    m.at = (it - (row << per_head_shift)) * 8;
-    return m;
-}
+constexpr int kAhead = 4;             // items a thread keeps in flight
 
 // cos and sin of pair j at position `at`, times the factor.
 __device__ __forceinline__ float2 turn32_of(const RopeParams& p, int j, int at)
@@ -64,13 +49,6 @@ __device__ __forceinline__ float dot(float a, float b, float c, float d)
     return __fadd_rn(__fmul_rn(a, b), __fmul_rn(c, d));
 }
 
-// Offset of the partners of the four elements from `at` on.
-__device__ __forceinline__ int partner(int at, int rot)
-{
-    const int half = rot >> 1;        // a multiple of 4
-    return at < half ? at + half : at - half;
-}
-
 template <int SRC, int DST, bool HALF, bool VEC>
 __global__ void __launch_bounds__(kThreads) lbv_rope_append4_kernel(const __grid_constant__ RopeParams p)
 {
@@ -78,27 +56,39 @@ __global__ void __launch_bounds__(kThreads) lbv_rope_append4_kernel(const __grid
     __shared__ int where[2];                       // request (-1: none), cache position
     const int tok = blockIdx.x, lane = threadIdx.x & 31;
     const int per_head_shift = p.kv.dim == 128 ? 4 : 3;
-    const int total = (p.q_heads + 2 * p.kv.heads) << per_head_shift;
+    // items of queries, then, from a warp's first lane on, keys and values
+    const int queries = p.q_heads << per_head_shift, keys = (queries + 31) & ~31;
+    const int total = keys + (2 * p.kv.heads << per_head_shift);
     const int step = kThreads * gridDim.y;
     const int first = blockIdx.y * kThreads + threadIdx.x;
 
     after_previous();
-    float x[kAhead][8], y[kAhead][8];              // the elements, and their partners
-    auto fetch = [&](int it, float (&a)[8], float (&b)[8]) {
-        const Piece m = piece_of(p, it, per_head_shift);
-        const int64_t row = tok * p.src_token[m.which] + m.head * p.src_head[m.which];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            load4<SRC, VEC>(p.src[m.which], row + m.at + 4 * h, reinterpret_cast<float(&)[4]>(a[4 * h]));
-            if (HALF && m.which < 2 && m.at < p.rot)
-                load4<SRC, VEC>(p.src[m.which], row + partner(m.at + 4 * h, p.rot),
-                                reinterpret_cast<float(&)[4]>(b[4 * h]));
-        }
+    float x0[kAhead][4], x1[kAhead][4];
+    // where eight neighbours of a key or value are: head (values after keys), first element
+    auto piece_of = [&](int it, int& which, int& head, int& at) {
+        const int e = it - keys, row = e >> per_head_shift;
+        which = row >= p.kv.heads ? 2 : 1;
+        head = row - (which - 1) * p.kv.heads;
+        at = (e - (row << per_head_shift)) * 8;
     };
+    auto fetch = [&](int it, float (&a)[4], float (&b)[4]) {
+        int which = 0, head, o0, o1;
+        if (it < keys) {
+            const Item m = item_of<HALF>(p, it, per_head_shift);
+            head = m.head, o0 = m.o0, o1 = m.o1;
+        } else {
+            piece_of(it, which, head, o0);
+            o1 = o0 + 4;
+        }
+        const int64_t at = tok * p.src_token[which] + head * p.src_head[which];
+        load4<SRC, VEC>(p.src[which], at + o0, a);
+        load4<SRC, VEC>(p.src[which], at + o1, b);
+    };
+    auto is = [&](int it) { return it < queries || (it >= keys && it < total); };
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
-        if (first + u * step < total)
-            fetch(first + u * step, x[u], y[u]);
+        if (is(first + u * step))
+            fetch(first + u * step, x0[u], x1[u]);
 
     find_token<kThreads>(p.batch, tok, where);
     const int req = where[0], pos = where[1];
@@ -110,22 +100,43 @@ __global__ void __launch_bounds__(kThreads) lbv_rope_append4_kernel(const __grid
     const int slot = pos & ((1 << p.kv.page_shift) - 1);
     __syncthreads();
 
-    // all lanes of a warp come here together; the pieces past the last do nothing
-    auto finish = [&](int it, float (&a)[8], float (&b)[8]) {
+    auto query = [&](int it, float (&a)[4], float (&b)[4]) {
+        const Item m = item_of<HALF>(p, it, per_head_shift);
+        if (m.pair >= 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 t = turn[m.pair + i];
+                float& x = HALF ? a[i] : i < 2 ? a[2 * i] : b[2 * i - 4];
+                float& y = HALF ? b[i] : i < 2 ? a[2 * i + 1] : b[2 * i - 3];
+                const float xn = cross(x, t.x, y, t.y);
+                y = dot(y, t.x, x, t.y);
+                x = xn;
+            }
+        }
+        uint16_t* d = p.q_out + tok * p.out_token + m.head * p.out_head;
+        store4<DST, VEC>(d + m.o0, a);
+        store4<DST, VEC>(d + m.o1, b);
+    };
+    // all lanes of a warp come here together; those past the last do nothing
+    auto held = [&](int it, float (&x0)[4], float (&x1)[4]) {
         const bool in = it < total;
-        const Piece m = piece_of(p, in ? it : 0, per_head_shift);
-        if (in && m.which < 2 && m.at < p.rot) {
+        int which, head, at;
+        piece_of(in ? it : keys, which, head, at);
+        float a[8] = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
+        if (in && which == 1 && at < p.rot) {
+            const int half = p.rot >> 1;           // a multiple of 4
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int o = m.at + 4 * h, half = p.rot >> 1;
+                const int o = at + 4 * h;
                 if constexpr (HALF) {
                     const bool low = o < half;
+                    float b[4];
+                    load4<SRC, VEC>(p.src[1], tok * p.src_token[1] + head * p.src_head[1] + (low ? o + half : o - half), b);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float2 t = turn[(low ? o : o - half) + i];
                         float& v = a[4 * h + i];
-                        const float w = b[4 * h + i];
-                        v = low ? cross(v, t.x, w, t.y) : dot(v, t.x, w, t.y);
+                        v = low ? cross(v, t.x, b[i], t.y) : dot(v, t.x, b[i], t.y);
                     }
                 } else {
 #pragma unroll
@@ -138,11 +149,6 @@ __global__ void __launch_bounds__(kThreads) lbv_rope_append4_kernel(const __grid
                     }
                 }
             }
-        }
-        if (in && m.which == 0) {
-            uint16_t* d = p.q_out + tok * p.out_token + m.head * p.out_head + m.at;
-            store4<DST, VEC>(d, reinterpret_cast<float(&)[4]>(a[0]));
-            store4<DST, VEC>(d + 4, reinterpret_cast<float(&)[4]>(a[4]));
         }
         // the group's bounds, by its 8 lanes
         constexpr float kMost = DST == LBV_F16 ? 32768.f : 8.5070591730234616e37f;    // 2^15, 2^126
@@ -159,7 +165,7 @@ __global__ void __launch_bounds__(kThreads) lbv_rope_append4_kernel(const __grid
             hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, d));
         }
         odd = (__ballot_sync(0xffffffffu, odd) >> (lane & 24)) & 0xFFu;
-        if (!in || m.which == 0 || page < 0)
+        if (!in || page < 0)
             return;
         uint16_t bias = from_f32<DST>(lo), scale = from_f32<DST>(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
         float s = to_f32<DST>(scale);
@@ -169,33 +175,39 @@ __global__ void __launch_bounds__(kThreads) lbv_rope_append4_kernel(const __grid
         uint32_t word = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            word |= (uint32_t)max(0, min(15, __float2int_rn(__fmul_rn(__fsub_rn(a[i], low), inverse)))) << (4 * (i >> 1) + 16 * (i & 1));
+            word |= (uint32_t)max(0, min(15, __float2int_rn(__fmul_rn(__fsub_rn(a[i], low), inverse))))
+                    << (4 * (i >> 1) + 16 * (i & 1));
         if (odd)
             scale = 0x7FFF;                        // NaN in both types
-        const int cs = kv4::chunk_shift(p.kv), at = slot & ((1 << cs) - 1);
-        const int planes = p.kv.dim >> 5, plane = (m.which - 1) * (planes >> 1) + (m.at >> 6);
-        uint8_t* c = kv4::chunk(p.kv, page, m.head, slot);
-        *reinterpret_cast<uint32_t*>(c + kv4::codes_at(plane, at, cs) + ((m.at >> 3) & 7) * 4) = word;
-        if ((m.at & 63) == 0)
-            *reinterpret_cast<uint32_t*>(c + kv4::scale_at(planes, plane, at, cs)) = scale | ((uint32_t)bias << 16);
+        const int cs = kv4::chunk_shift(p.kv), to = slot & ((1 << cs) - 1);
+        const int planes = p.kv.dim >> 5, plane = (which - 1) * (planes >> 1) + (at >> 6);
+        uint8_t* c = kv4::chunk(p.kv, page, head, slot);
+        *reinterpret_cast<uint32_t*>(c + kv4::codes_at(plane, to, cs) + ((at >> 3) & 7) * 4) = word;
+        if ((at & 63) == 0)
+            *reinterpret_cast<uint32_t*>(c + kv4::scale_at(planes, plane, to, cs)) = scale | ((uint32_t)bias << 16);
+    };
+    auto finish = [&](int it, float (&a)[4], float (&b)[4]) {
+        if (it - lane >= keys)                     // a warp has either
+            held(it, a, b);
+        else if (it < queries)
+            query(it, a, b);
     };
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
         if (first - lane + u * step < total)
-            finish(first + u * step, x[u], y[u]);
+            finish(first + u * step, x0[u], x1[u]);
     for (int it = first + kAhead * step; it - lane < total; it += step) {
-        if (it < total)
-            fetch(it, x[0], y[0]);
-        __syncwarp();                              // q_out may be q: a head is one warp's, its partners are loaded
-        finish(it, x[0], y[0]);
+        if (is(it))
+            fetch(it, x0[0], x1[0]);
+        finish(it, x0[0], x1[0]);
     }
 }
 
 template <int SRC, int DST, bool HALF>
 cudaError_t launch(const RopeParams& p, bool vec, cudaStream_t st)
 {
-    const int total = (p.q_heads + 2 * p.kv.heads) * (p.kv.dim / 8);
-    // few tokens: one piece a thread, so that the whole call is in flight at once
+    const int total = (p.q_heads * (p.kv.dim / 8) + 31) / 32 * 32 + 2 * p.kv.heads * (p.kv.dim / 8);
+    // few tokens: one item a thread, so that the whole call is in flight at once
     const int per = p.batch.tokens < 256 ? 1 : kAhead;
     const dim3 grid((unsigned)p.batch.tokens,
                     (unsigned)((total + kThreads * per - 1) / (kThreads * per)));

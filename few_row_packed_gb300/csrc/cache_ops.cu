@@ -14,51 +14,78 @@ constexpr int kThreads = 256;
 
 // ---- tokens as rows ----
 //
-// One block a token: a thread takes 8 elements of a head's key or value.
+// A thread takes 8 elements of a head's key or value, a block kTokens tokens: what a
+// token's place takes is four loads that wait for one another, so many are under way.
+
+constexpr int kTokens = 4;
 
 template <int DT, bool PACKED>
 __global__ void __launch_bounds__(kThreads) lbv_kv_read_kernel(const __grid_constant__ ReadParams p)
 {
-    __shared__ int where[2];
-    const int tok = blockIdx.x;
+    __shared__ int where[kTokens][2];              // request, then page (-1: reads as zeros, -2: no request); slot
+    const int tok0 = blockIdx.x * kTokens, tid = threadIdx.x;
     after_previous();
-    find_token<kThreads>(p.batch, tok, where);
-    const int req = where[0], pos = where[1];
-    if (req < 0)
-        return;                                    // a row of no request
-    const int page = page_of(p.batch, p.kv, req, pos);
-    const int slot = pos & ((1 << p.kv.page_shift) - 1);
+    if (tid < kTokens)
+        where[tid][0] = -1;
+    __syncthreads();
+    for (int r = tid; r < p.batch.requests; r += kThreads) {
+        const int lo = p.batch.q_start[r], hi = p.batch.q_start[r + 1];
+        for (int tok = max(lo, tok0); tok < min(min(hi, p.batch.tokens), tok0 + kTokens); ++tok) {
+            where[tok - tok0][0] = r;
+            where[tok - tok0][1] = p.batch.kv_len[r] - hi + tok;
+        }
+    }
+    __syncthreads();
+    if (tid < kTokens) {
+        const int req = where[tid][0], pos = where[tid][1];
+        where[tid][0] = req < 0 ? -2 : page_of(p.batch, p.kv, req, pos);
+        where[tid][1] = pos & ((1 << p.kv.page_shift) - 1);
+    }
+    __syncthreads();
     const int shift = p.kv.dim == 128 ? 4 : 3, per = p.kv.heads << shift;
-    for (int it = blockIdx.y * kThreads + threadIdx.x; it < 2 * per; it += kThreads * gridDim.y) {
+    const int units = 2 * per, step = kThreads * gridDim.y;
+    for (int it = blockIdx.y * kThreads + tid; it < units; it += step) {
         const int which = it >= per, e = it - which * per, head = e >> shift, at = (e - (head << shift)) * 8;
         if (!p.out[which])
             continue;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (page >= 0) {
+        uint4 v[kTokens];
+        uint32_t pair[kTokens], word[kTokens];
+#pragma unroll
+        for (int i = 0; i < kTokens; ++i) {        // all of them in flight
+            const int page = where[i][0], slot = where[i][1];
+            v[i] = make_uint4(0u, 0u, 0u, 0u);
+            pair[i] = word[i] = 0;
+            if (page < 0)
+                continue;
             if constexpr (PACKED) {
                 const int cs = kv4::chunk_shift(p.kv), s = slot & ((1 << cs) - 1), planes = p.kv.dim >> 5;
                 const int plane = which * (planes >> 1) + (at >> 6);
                 const uint8_t* c = kv4::chunk(p.kv, page, head, slot);
-                const uint32_t sb = *reinterpret_cast<const uint32_t*>(c + kv4::scale_at(planes, plane, s, cs));
-                const uint32_t w =
-                    *reinterpret_cast<const uint32_t*>(c + kv4::codes_at(plane, s, cs) + ((at >> 3) & 7) * 4);
-                uint32_t x[4];
-                kv4::expand<DT>(w, kv4::both_scales(sb), kv4::both_biases(sb), kv4::constants<DT>(), x);
-                v = make_uint4(x[0], x[1], x[2], x[3]);
+                pair[i] = *reinterpret_cast<const uint32_t*>(c + kv4::scale_at(planes, plane, s, cs));
+                word[i] = *reinterpret_cast<const uint32_t*>(c + kv4::codes_at(plane, s, cs) + ((at >> 3) & 7) * 4);
             } else {
-                const uint16_t* src = (which ? p.kv.v : p.kv.k) + page * p.kv.page_stride +
-                                      slot * p.kv.token_stride + head * p.kv.head_stride + at;
-                v = *reinterpret_cast<const uint4*>(src);
+                v[i] = *reinterpret_cast<const uint4*>((which ? p.kv.v : p.kv.k) + page * p.kv.page_stride +
+                                                       slot * p.kv.token_stride + head * p.kv.head_stride + at);
             }
         }
-        uint16_t* d = p.out[which] + tok * p.out_token[which] + head * p.out_head[which] + at;
-        if (p.wide) {
-            *reinterpret_cast<uint4*>(d) = v;
-        } else {
-            const uint32_t r[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                d[i] = (uint16_t)(r[i >> 1] >> (16 * (i & 1)));
+        for (int i = 0; i < kTokens; ++i) {
+            if (where[i][0] == -2)
+                continue;                          // a row of no request
+            if constexpr (PACKED) {
+                uint32_t x[4];
+                kv4::expand<DT>(word[i], kv4::both_scales(pair[i]), kv4::both_biases(pair[i]), kv4::constants<DT>(), x);
+                v[i] = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+            uint16_t* d = p.out[which] + (tok0 + i) * p.out_token[which] + head * p.out_head[which] + at;
+            if (p.wide) {
+                *reinterpret_cast<uint4*>(d) = v[i];
+            } else {
+                const uint32_t r[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    d[j] = (uint16_t)(r[j >> 1] >> (16 * (j & 1)));
+            }
         }
     }
 }
@@ -214,7 +241,8 @@ __global__ void __launch_bounds__(kThreads) lbv_kv_copy_kernel(const __grid_cons
 template <int DT>
 cudaError_t launch_read(const ReadParams& p, cudaStream_t st)
 {
-    const dim3 grid((unsigned)p.batch.tokens, (unsigned)((2 * p.kv.heads * (p.kv.dim / 8) + kThreads - 1) / kThreads));
+    const dim3 grid((unsigned)((p.batch.tokens + kTokens - 1) / kTokens),
+                    (unsigned)((2 * p.kv.heads * (p.kv.dim / 8) + kThreads - 1) / kThreads));
     return p.kv.packed ? launch_after(lbv_kv_read_kernel<DT, true>, grid, kThreads, 0, st, p)
                        : launch_after(lbv_kv_read_kernel<DT, false>, grid, kThreads, 0, st, p);
 }

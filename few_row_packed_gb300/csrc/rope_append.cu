@@ -29,28 +29,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kAhead = 4;             // items a thread keeps in flight
 
-// Where an item comes from and goes to.
-struct Item {
-    int which;             // 0 q, 1 k, 2 v
-    int head;
-    int o0, o1;            // offsets of its two groups of four elements
-    int pair;              // first of its four pairs, -1: copied as it is
-};
-
-template <bool HALF>
-__device__ __forceinline__ Item item_of(const RopeParams& p, int it, int per_head_shift)
-{
-    Item m;
-    const int row = it >> per_head_shift;
-    const int e = it - (row << per_head_shift);
-    m.which = row < p.q_heads ? 0 : row < p.q_heads + p.kv.heads ? 1 : 2;
-    m.head = m.which == 0 ? row : m.which == 1 ? row - p.q_heads : row - p.q_heads - p.kv.heads;
-    m.pair = m.which < 2 && e < (p.rot >> 3) ? 4 * e : -1;
-    m.o0 = HALF && m.pair >= 0 ? 4 * e : 8 * e;
-    m.o1 = HALF && m.pair >= 0 ? (p.rot >> 1) + 4 * e : 8 * e + 4;
-    return m;
-}
-
 template <int SRC, int DST, bool HALF, bool VEC>
 __global__ void __launch_bounds__(kThreads) lbv_rope_append_kernel(const __grid_constant__ RopeParams p)
 {
