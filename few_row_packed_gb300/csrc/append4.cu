@@ -2,7 +2,7 @@
 //
 // The rotation is that of rope_append.cu; a group x of 64 rotated elements is then held
 // as codes of 4 bits between its bounds:
-//     bias = round16(min x), scale = round16((max x - min x) / 15),
+//     bias = round16(min x), scale = round16((max x - min x) * (1 / 15)),
 //     code = round((x - bias) * (1 / scale)) in 0..15.
 // Queries are items of two groups of four elements, as in rope_append.cu.  Of keys and values
 // a thread has 8 neighbours, so a group of 64 is 8 lanes, whose minimum and maximum meet in three
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kThreads) lbv_rope_append4_kernel(const __grid
         odd = (__ballot_sync(0xffffffffu, odd) >> (lane & 24)) & 0xFFu;
         if (!in || page < 0)
             return;
-        uint16_t bias = from_f32<DST>(lo), scale = from_f32<DST>(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
+        uint16_t bias = from_f32<DST>(lo), scale = from_f32<DST>(__fmul_rn(__fsub_rn(hi, lo), 1.f / 15.f));
         float s = to_f32<DST>(scale);
         if (!(s >= 1.17549435e-38f))               // its reciprocal would not be finite
             s = 0.f, scale = 0;

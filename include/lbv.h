@@ -566,7 +566,7 @@ LBV_API lbv_status lbv_rope_destroy(lbv_rope* rope);
  * position, one past the block table, a page outside the cache) has its key
  * and value left out; its query is rotated all the same.
  * A cache of 4 bits gets, for each 64 elements x of a rotated key or a value (fp32):
- * bias = min x and scale = (max x - min x) / 15, each rounded to the cache's dtype, and the codes
+ * bias = min x and scale = (max x - min x) * (1 / 15), each rounded to the cache's dtype, and the codes
  * (x - bias) * (1 / scale), rounded to the nearest whole number in 0..15 (all 0 where the scale is 0 or
  * below 2^-126).  So that equal inputs give equal codes wherever the definition is followed,
  * every operation is rounded by itself there: the angle's fraction of a turn is cut to 2^-40 and

@@ -36,7 +36,7 @@ def quantise(x, round16):
     arithmetic; round16 rounds an fp32 number to the cache's dtype."""
     x = np.asarray(x, np.float32)
     f = np.float32
-    bias, scale = f(round16(x.min())), f(round16(f(x.max() - x.min()) / f(15)))
+    bias, scale = f(round16(x.min())), f(round16(f(x.max() - x.min()) * (f(1) / f(15))))
     if scale < f(2.0 ** -126):
         return np.zeros(64, np.int64), f(0), bias
     code = np.rint((x - bias) * (f(1) / scale))
