@@ -46,7 +46,7 @@ constexpr int kExtra = 3, kMinUnits = 2;
 constexpr int kKeyWarps = 4, kTeam = kKeyWarps * 32;
 // A reference that every score passes, negated: nothing has been seen yet.
 constexpr float kNone = 1e30f;
-constexpr int kItems = 8;                        // items that a team's warps may be apart: stages, and one
+constexpr int kItems = 16;                        // items that a team's warps may be apart: stages, and one
 
 // What a team needs to know of an item.
 struct alignas(16) Item {
@@ -55,7 +55,6 @@ struct alignas(16) Item {
     int key0, nb;          // its first key and its blocks in this share; 0 blocks: no more items
     int skip, jump;        // keys left out before block `jump` (behind the sinks)
     int c0, c1;            // shares that hold a part of it
-    __device__ int key_of(int j) const { return key0 + j * kBlock + (j >= jump ? skip : 0); }
 };
 static_assert(sizeof(Item) == 48, "ring entry");
 
@@ -69,7 +68,7 @@ struct Geo {
     static constexpr int REGS = NT == 1 ? 104 : 152, HELPER = NT == 1 ? 64 : 56;
     static constexpr int THREADS = TEAMS * kTeam + 128;
     static constexpr int STAGE = kBlock * 72 * (D / 64);
-    static constexpr int NST = D == 64 ? 6 : 4;
+    static constexpr int NST = D == 64 ? 8 : 4;
     static constexpr int SLOT = ROWS * (D + 3);             // floats of one partial result
     // a team's shared memory: the ring, the warps' results, queries of more than two tiles as
     // the lanes hold them
@@ -77,13 +76,14 @@ struct Geo {
     static constexpr int JROWS = NT == 3 ? 8 : ROWS;       // rows joined at a time
     static constexpr int QUERIES = JOIN + kKeyWarps * JROWS * D * 4;
     static constexpr int STATS = QUERIES + (NT == 3 ? NT * 32 * (D / 8) * 4 : 0);   // [4][ROWS] maxima, sums
-    static constexpr int ITEMS = STATS + 2 * kKeyWarps * ROWS * 4;
+    static constexpr int WORDS = STATS + 2 * kKeyWarps * ROWS * 4;  // uint64 [ROWS]: the rows' words of the tree
+    static constexpr int ITEMS = WORDS + 8 * ROWS;
     static constexpr int START = ITEMS;                     // where the share begins, before its first item
     static constexpr int BARS = ITEMS + kItems * 48;        // full, empty, items
     static constexpr int THERE = BARS + (2 * NST + kItems) * 8;     // a block's chunks that exist
     static constexpr int SIZE = (THERE + NST * 4 + 127) / 128 * 128;
     static constexpr int BYTES = TEAMS * SIZE;
-    static_assert(ITEMS % 16 == 0 && BARS % 8 == 0 && sizeof(Start) <= kItems * 48 && NST + 1 < kItems, "layout");
+    static_assert(ITEMS % 16 == 0 && BARS % 8 == 0 && sizeof(Start) <= kItems * 48 && NST + 1 < kItems && WORDS % 8 == 0, "layout");
     static_assert(BYTES <= 227 * 1024, "room");
 };
 
@@ -138,9 +138,9 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
     unsigned char* smem = smem_all + team * G::SIZE;
     const uint32_t sbase = smem_u32(smem);
     const int share = team * gridDim.x + blockIdx.x;         // the SMs first, then their teams
-    auto full = [&](int st) { return sbase + G::BARS + st * 8; };
-    auto empty = [&](int st) { return sbase + G::BARS + (G::NST + st) * 8; };
-    auto item_full = [&](int i) { return sbase + G::BARS + (2 * G::NST + i % kItems) * 8; };
+    auto full = [&](unsigned st) { return sbase + G::BARS + st * 8; };
+    auto empty = [&](unsigned st) { return sbase + G::BARS + (G::NST + st) * 8; };
+    auto item_full = [&](unsigned i) { return sbase + G::BARS + (2 * G::NST + i % kItems) * 8; };
     Item* items = reinterpret_cast<Item*>(smem + G::ITEMS);
 
     if (tid % kTeam == 0 && !helper) {
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
         const Start begin = *start;
         __syncwarp();                                        // the items take its place
         const int64_t page_bytes = kv4::page_bytes(p.kv);
-        int it = 0, n = 0;                                   // items published, blocks asked for
+        unsigned it = 0, n = 0;                              // items published, blocks asked for
         auto publish = [&](const Item& x) {
             if (lane == 0) {
                 items[it % kItems] = x;
@@ -192,22 +192,23 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
                 int next = page_of(w.b_first);
 #pragma unroll 1
                 for (int b = w.b_first; b < w.b_last; ++b) {
-                    const int st = n % G::NST, page = next;
+                    const unsigned st = n % G::NST;
+                    const int page = next;
                     next = page_of(b + 1);
                     // A stage is asked for again when it has been read, and its last copies have
                     // landed (readers that gave up free it all the same).
                     if (n >= G::NST) {
-                        const uint32_t parity = (uint32_t)((n / G::NST - 1) & 1);
+                        const uint32_t parity = (n / G::NST - 1) & 1;
                         ok = mbar_wait(empty(st), parity, p.wait_limit) &&
                              mbar_wait(full(st), parity, p.wait_limit);
                     }
-                    ok = __all_sync(0xffffffffu, ok && ((unsigned)n < p.first_copies || share > 0));
+                    ok = __all_sync(0xffffffffu, ok && (n < p.first_copies || share > 0));
                     if (!ok)                                 // no more copies, and no more items: places
                         break;                               // of those that are known may still be read
                     if (b == w.b_first) {
                         const bool whole = w.whole(), split = b < w.x.near;      // sinks, then a window
                         publish({w.q.q0, w.q.first, w.q.keys, w.x.row0, w.x.rows, w.head, w.key0(b),
-                                 w.b_last - b, split ? w.x.gap * kBlock : 0, w.x.near - b,
+                                 w.b_last - b, w.x.gap * kBlock, split ? w.x.near - b : -1,
                                  whole ? 0 : w.first_cta(), whole ? 0 : w.last_cta()});
                     }
                     ++n;
@@ -232,9 +233,8 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
         if (ok)
             publish(Item{});
         // the copies land before shared memory goes away, also after a wait that ran out
-        for (int i = 0; i < G::NST; ++i)
-            if (n - 1 - i >= 0 && !mbar_wait(full((n - 1 - i) % G::NST), (uint32_t)(((n - 1 - i) / G::NST) & 1),
-                                             p.wait_limit))
+        for (unsigned i = 1; i <= G::NST && i <= n; ++i)
+            if (!mbar_wait(full((n - i) % G::NST), ((n - i) / G::NST) & 1, p.wait_limit))
                 ok = false;
         if (!ok && lane == 0)
             atomicOr(p.status, 1u);
@@ -270,13 +270,14 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
     const float hidden = c < 0.f ? INFINITY : -INFINITY;
     float* joint = reinterpret_cast<float*>(smem + G::JOIN);
     float* stats = reinterpret_cast<float*>(smem + G::STATS);
-    int n = 0;
-    for (int it = 0;; ++it) {
+    uint64_t* words = reinterpret_cast<uint64_t*>(smem + G::WORDS);
+    unsigned n = 0;
+    for (unsigned it = 0;; ++it) {
         // one warp waits for the item, and all of them hear whether it came
         bool stop = false;
         if (warp == 0) {
             if (ok)
-                ok = mbar_wait(item_full(it), (uint32_t)((it / kItems) & 1), p.wait_limit);
+                ok = mbar_wait(item_full(it), (it / kItems) & 1, p.wait_limit);
             stop = !ok || items[it % kItems].nb == 0;
         }
         if (any_of_team(bar, stop))
@@ -318,7 +319,9 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
                         make_uint4(q[4 * e], q[4 * e + 1], q[4 * e + 2], q[4 * e + 3]);
             }
         }
-        if (NT == 3)
+        if (p.tree && tid % kTeam < item_rows)
+            words[tid % kTeam] = p.tree[w.q0 + token_of(p, w.row0 + tid % kTeam)];
+        if (NT == 3 || p.tree)
             named_bar_sync(bar, kTeam);
         float o[NT][D / 16][4];                                  // tile j: elements g D / 8 + 2 j, and the next
         float2 minus[NT], l[NT];                                 // references, negated, and sums of rows 2 t and 2 t + 1
@@ -336,11 +339,16 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
         const int open_lo =
             p.window > 0 ? w.first + token_of(p, w.row0 + item_rows - 1) - p.window + 1 : 0;
 
+        int k0 = w.key0 - kBlock;
+        const int jump = w.jump;
 #pragma unroll 1
         for (int j = 0; j < nb; ++j, ++n) {
-            const int st = n % G::NST, k0 = w.key_of(j);
-            if (ok)
-                ok = mbar_wait(full(st), (uint32_t)((n / G::NST) & 1), p.wait_limit);
+            const unsigned st = n % G::NST;
+            k0 += kBlock;
+            if (j == jump)
+                k0 += w.skip;
+            if (!mbar_try(full(st), (n / G::NST) & 1) && ok)
+                ok = mbar_wait(full(st), (n / G::NST) & 1, p.wait_limit);
             const uint32_t there = load4(sbase + G::THERE + st * 4);
             // whether a key of the block exists: slots past the context hold anything
             auto exists = [&](int key) { return ((there >> (key >> cs)) & 1) && k0 + key < w.keys; };
@@ -399,21 +407,24 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
             // ---- their probabilities ----
             const int key0 = k0 + warp * 16;
             if (key0 + 16 > open_hi || key0 < open_lo) {         // rare, so short code
-                Request q;
-                q.first = w.first, q.keys = w.keys;
-                uint32_t see = 0;
+                const int mine = key_at(g);
 #pragma unroll 1
-                for (int e = 0; e < 4 * NT; ++e) {
-                    const int r = (e >> 2) * 8 + 2 * t + (e & 1), tok = token_of(p, w.row0 + r);
-                    const uint64_t word = p.tree && r < item_rows ? p.tree[w.q0 + tok] : 0;
-                    if (r < item_rows && sees(p, q, q.first + tok, word, key0 + key_at(g) + ((e >> 1) & 1) * 8))
-                        see |= 1u << e;
+                for (int r = 0; r < ROWS; r += 8) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {                // rows r + 2 t and the next
+                        const int row = r + 2 * t + h;
+                        uint32_t see = 0;
+                        if (row < item_rows)
+                            see = seen32(p, w.first, w.keys, w.first + token_of(p, w.row0 + row),
+                                         p.tree ? words[row] : 0, key0) >> mine;
+#pragma unroll
+                        for (int i = 0; i < NT; ++i)
+                            if (8 * i == r) {
+                                s[i][h] = see & 1 ? s[i][h] : hidden;
+                                s[i][2 + h] = (see >> 8) & 1 ? s[i][2 + h] : hidden;
+                            }
+                    }
                 }
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        s[i][e] = (see >> (4 * i + e)) & 1 ? s[i][e] : hidden;
             }
             // exponents, for the references as they are
             float2 x[NT][2];

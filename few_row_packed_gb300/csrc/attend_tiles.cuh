@@ -87,11 +87,11 @@ struct Geo {
     static constexpr int SLOT = (D / 64) * HALF;            // one block's K or V; one Q tile
     static constexpr int Q = 0;
     static constexpr int RING = 2 * SLOT;
-    static constexpr int NSLOT = (D == 128 ? 5 : 10) - (KV4 ? 128 / D : 0);
+    static constexpr int NSLOT = (D == 128 ? 5 : 10) - (KV4 ? 2 * (128 / D) : 0);
     // 4 bits: a ring of a block's keys or values as they are held, codes and then scales
     static constexpr int HELD = RING + NSLOT * SLOT;
     static constexpr int CODES = kKeys * 32 * (D / 64), HSLOT = kKeys * 36 * (D / 64);
-    static constexpr int NHELD = KV4 ? (D == 128 ? 3 : 6) : 0;
+    static constexpr int NHELD = KV4 ? (D == 128 ? 6 : 12) : 0;
     static constexpr int BARS = HELD + NHELD * HSLOT;
     static constexpr int NBARS = 2 * NSLOT + 11 + 2 * kItems + 2 * NHELD;
     static constexpr int THERE = BARS + NBARS * 8;          // their chunks that exist
