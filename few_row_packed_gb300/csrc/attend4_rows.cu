@@ -41,8 +41,7 @@ namespace {
 // small batches less evenly: 64 requests of one token 101 us in place of 107, a window of
 // 2,048 over 32 requests 33 in place of 29, four tokens after 200,000 108 in place of 93.)
 constexpr int kBlock = 64;
-// Units of an item beside its blocks, and the least share of a team.
-constexpr int kExtra = 3, kMinUnits = 2;
+constexpr int kMinUnits = 2;                     // the least share of a team
 constexpr int kKeyWarps = 4, kTeam = kKeyWarps * 32;
 // A reference that every score passes, negated: nothing has been seen yet.
 constexpr float kNone = 1e30f;
@@ -62,18 +61,21 @@ static_assert(sizeof(Item) == 48, "ring entry");
 template <int D, int NT>
 struct Geo {
     static constexpr int ROWS = 8 * NT;
+    // (3 in place of 6: 32 trees 164 us, 158; 10: 162)
+    static constexpr int EXTRA = NT == 1 ? 3 : 6;           // units of an item beside its blocks
     // teams on an SM, and registers a thread after the split: 96 * 640 at launch = 104 * 512 +
     // 64 * 128, 128 * 512 = 152 * 384 + 56 * 128
     static constexpr int TEAMS = NT == 1 ? 4 : 3;
     static constexpr int REGS = NT == 1 ? 104 : 152, HELPER = NT == 1 ? 64 : 56;
     static constexpr int THREADS = TEAMS * kTeam + 128;
     static constexpr int STAGE = kBlock * 72 * (D / 64);
-    static constexpr int NST = D == 64 ? 8 : 4;
+    // (two stages, and four, take 4 to 7 % longer)
+    static constexpr int NST = D == 64 ? 6 : 3;
     static constexpr int SLOT = ROWS * (D + 3);             // floats of one partial result
     // a team's shared memory: the ring, the warps' results, queries of more than two tiles as
     // the lanes hold them
     static constexpr int JOIN = NST * STAGE;
-    static constexpr int JROWS = NT == 3 ? 8 : ROWS;       // rows joined at a time
+    static constexpr int JROWS = 8;                       // rows joined at a time
     static constexpr int QUERIES = JOIN + kKeyWarps * JROWS * D * 4;
     static constexpr int STATS = QUERIES + (NT == 3 ? NT * 32 * (D / 8) * 4 : 0);   // [4][ROWS] maxima, sums
     static constexpr int WORDS = STATS + 2 * kKeyWarps * ROWS * 4;  // uint64 [ROWS]: the rows' words of the tree
@@ -130,7 +132,7 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
 {
     using G = Geo<D, NT>;
     constexpr int ROWS = G::ROWS, PARTS = D / 64;
-    using S = Shape<ROWS, kBlock, kExtra>;
+    using S = Shape<ROWS, kBlock, G::EXTRA>;
     extern __shared__ __align__(1024) unsigned char smem_all[];
     const int tid = threadIdx.x, lane = tid & 31;
     const bool helper = tid >= G::TEAMS * kTeam;             // (its last warps may have no team)
@@ -472,15 +474,14 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
             // ---- and their values ----
             {
                 constexpr int W = D / 64;                        // words of 8 elements
-                uint32_t e[W][2][2][4];                          // pairs of keys, even and odd elements
+                uint32_t v[2][2][W], sc[2], bi[2];               // of two pairs of keys
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    uint32_t x[W], y[W];
                     if constexpr (W == 2) {
                         const uint2 a = load8(v_at0 + stage + h * eight), b = load8(v_at1 + stage + h * eight);
-                        x[0] = a.x, x[1] = a.y, y[0] = b.x, y[1] = b.y;
+                        v[h][0][0] = a.x, v[h][0][1] = a.y, v[h][1][0] = b.x, v[h][1][1] = b.y;
                     } else {
-                        x[0] = load4(v_at0 + stage + h * eight), y[0] = load4(v_at1 + stage + h * eight);
+                        v[h][0][0] = load4(v_at0 + stage + h * eight), v[h][1][0] = load4(v_at1 + stage + h * eight);
                     }
                     uint2 f = load8(v_pair + stage + h * eight4);
                     if (there != ~0u) {
@@ -488,22 +489,24 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
                         f.x = exists(key) ? f.x : 0u;
                         f.y = exists(key + 1) ? f.y : 0u;
                     }
-                    const uint32_t sc = __byte_perm(f.x, f.y, take_scales), bi = __byte_perm(f.x, f.y, take_biases);
-#pragma unroll
-                    for (int u = 0; u < W; ++u) {
-                        kv4::expand<DT>(__byte_perm(x[u], y[u], 0x5410), sc, bi, constants, e[u][h][0]);
-                        kv4::expand<DT>(__byte_perm(x[u], y[u], 0x7632), sc, bi, constants, e[u][h][1]);
-                    }
+                    sc[h] = __byte_perm(f.x, f.y, take_scales), bi[h] = __byte_perm(f.x, f.y, take_biases);
                 }
 #pragma unroll
-                for (int u = 0; u < W; ++u)
+                for (int u = 0; u < W; ++u) {
+                    uint32_t e[2][2][4];                         // even and odd elements
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        kv4::expand<DT>(__byte_perm(v[h][0][u], v[h][1][u], 0x5410), sc[h], bi[h], constants, e[h][0]);
+                        kv4::expand<DT>(__byte_perm(v[h][0][u], v[h][1][u], 0x7632), sc[h], bi[h], constants, e[h][1]);
+                    }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const uint32_t a[4] = {e[u][0][0][j], e[u][0][1][j], e[u][1][0][j], e[u][1][1][j]};
+                        const uint32_t a[4] = {e[0][0][j], e[0][1][j], e[1][0][j], e[1][1][j]};
 #pragma unroll
                         for (int i = 0; i < NT; ++i)
                             mma<DT>(o[i][u * 4 + j], a, pf[i][0], pf[i][1]);
                     }
+                }
             }
             __syncwarp();
             if (lane == 0)
