@@ -57,8 +57,8 @@ template <bool KV4>
 struct Roles {
     static constexpr int THREADS = KV4 ? 512 : 384;
     // registers a thread after the split: 168 * 384 at launch = 88 * 128 + 208 * 256, and
-    // 128 * 512 = (80 + 80) * 128 + 176 * 256
-    static constexpr int CONTROL = KV4 ? 80 : 88, STREAM = KV4 ? 176 : 208, EXPAND = 80;
+    // 128 * 512 = (80 + 48) * 128 + 192 * 256
+    static constexpr int CONTROL = KV4 ? 80 : 88, STREAM = KV4 ? 192 : 208, EXPAND = 48;
     // who fills a slot, and who reads an item (copies, MMAs, eight warps of the streams, and
     // those that expand)
     static constexpr int FILLERS = KV4 ? 4 : 1, READERS = KV4 ? 14 : 10;
@@ -87,11 +87,11 @@ struct Geo {
     static constexpr int SLOT = (D / 64) * HALF;            // one block's K or V; one Q tile
     static constexpr int Q = 0;
     static constexpr int RING = 2 * SLOT;
-    static constexpr int NSLOT = (D == 128 ? 5 : 10) - (KV4 ? 2 * (128 / D) : 0);
+    static constexpr int NSLOT = (D == 128 ? 5 : 10) - (KV4 ? 128 / D : 0);
     // 4 bits: a ring of a block's keys or values as they are held, codes and then scales
     static constexpr int HELD = RING + NSLOT * SLOT;
     static constexpr int CODES = kKeys * 32 * (D / 64), HSLOT = kKeys * 36 * (D / 64);
-    static constexpr int NHELD = KV4 ? (D == 128 ? 6 : 12) : 0;
+    static constexpr int NHELD = KV4 ? (D == 128 ? 3 : 6) : 0;
     static constexpr int BARS = HELD + NHELD * HSLOT;
     static constexpr int NBARS = 2 * NSLOT + 11 + 2 * kItems + 2 * NHELD;
     static constexpr int THERE = BARS + NBARS * 8;          // their chunks that exist
