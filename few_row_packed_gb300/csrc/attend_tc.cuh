@@ -45,21 +45,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t at, float (&d)[16])
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld4(uint32_t at, float (&d)[4])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];\n"
-                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-                 : "r"(at)
-                 : "memory");
-}
-
-__device__ __forceinline__ void tmem_st4(uint32_t at, const float (&d)[4])
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(at), "f"(d[0]), "f"(d[1]),
-                 "f"(d[2]), "f"(d[3])
-                 : "memory");
-}
-
 __device__ __forceinline__ void tmem_wait_ld()
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
@@ -111,34 +96,6 @@ __device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint
         : "memory");
 }
 
-// The same with A in tensor memory and B (like K) contiguous along the contracted dimension.
-__device__ __forceinline__ void mma4_tk(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add)
-{
-    asm volatile(
-        "{\n .reg .pred e, p;\n setp.ne.b32 p, %10, 0;\n elect.sync _|e, 0xffffffff;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %5, %9, p;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], %6, %9, 1;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], %7, %9, 1;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%4], %8, %9, 1;\n}\n" ::"r"(d), "r"(a),
-        "r"(a + 8), "r"(a + 16), "r"(a + 24), "l"(b), "l"(b + 2), "l"(b + 4), "l"(b + 6),
-        "r"(idesc), "r"(add)
-        : "memory");
-}
-
-// The same with both operands in shared memory with their rows along the contracted
-// dimension: 16 rows of each a step, of 128 bytes in A and of 32 in B.
-__device__ __forceinline__ void mma4_rr(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add)
-{
-    asm volatile(
-        "{\n .reg .pred e, p;\n setp.ne.b32 p, %10, 0;\n elect.sync _|e, 0xffffffff;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %5, %9, p;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %2, %6, %9, 1;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %3, %7, %9, 1;\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %4, %8, %9, 1;\n}\n" ::"r"(d), "l"(a), "l"(a + 128),
-        "l"(a + 256), "l"(a + 384), "l"(b), "l"(b + 32), "l"(b + 64), "l"(b + 96), "r"(idesc), "r"(add)
-        : "memory");
-}
-
 // Arrives on `bar` once every MMA the elected lane has issued is complete.
 __device__ __forceinline__ void commit(uint32_t bar)
 {
@@ -157,19 +114,11 @@ __device__ __forceinline__ uint64_t desc128(uint32_t addr, uint32_t lead)
            ((uint64_t)(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-// The same for rows of 32 bytes (16 elements) along the contracted dimension, swizzled
-// within 256 bytes: 8-row groups 256 bytes apart, 16-element column groups `lead` bytes.
-__device__ __forceinline__ uint64_t desc32(uint32_t addr, uint32_t lead)
-{
-    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lead >> 4) & 0x3FFFu) << 16) |
-           ((uint64_t)(256u >> 4) << 32) | (1ull << 46) | (6ull << 61);
-}
-
-// kind::f16, fp32 sums, M = 128; bits 15 and 16: A is M-major, B is N-major.
+// kind::f16, fp32 sums, M = 128; bit 16: B is N-major.
 template <int DT>
-__host__ __device__ constexpr uint32_t idesc(int n, bool b_n_major, bool a_m_major = false)
+__host__ __device__ constexpr uint32_t idesc(int n, bool b_n_major)
 {
-    return (1u << 4) | ((uint32_t)a_m_major << 15) | ((uint32_t)(DT == LBV_BF16) << 7) | ((uint32_t)(DT == LBV_BF16) << 10) |
+    return (1u << 4) | ((uint32_t)(DT == LBV_BF16) << 7) | ((uint32_t)(DT == LBV_BF16) << 10) |
            ((uint32_t)b_n_major << 16) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
