@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 import few_row_packed_gb300 as lbv
-from kv4_setup import DT, TINY, UNIT, Setup4, f64, round16, values
+from kv4_setup import DT, TINY, UNIT, Setup4, f64, round16, values, words16
 from oracle import kv4, step
 from test_gpu_step import LENGTHS, check_attend, lay_out, run_attend
 
@@ -249,6 +249,35 @@ def test_attend_scale(scale, heads):
     q = s.rows(heads, scale=3.0)
     out, lse, _ = run_attend(s, q, scale=scale)
     check_attend(Held(s), q, out, lse, scale=scale)
+
+
+@pytest.mark.parametrize("q_len, heads", [([2, 1], 2), ([4, 2], 12), ([40, 3], 12)])
+def test_attend_scores_of_any_size(q_len, heads):
+    """Constant keys of -2^(70 + e) against queries of 2^32 (64 exact products): every score is
+    below -10^30, and only the keys of the smallest visible e count, equally."""
+    s = Setup4(q_len, [190, 70], kv_heads=2, dim=64, dtype="bf16", page=16, seed=5)
+    held = s.data.view(torch.uint8).cpu().numpy()
+    e = np.random.default_rng(1).integers(0, 8, (s.pages, 16))
+    for slot in range(16):
+        for h in range(2):
+            _, at = kv4.offsets(16, 2, 64, h, slot, 0, 0)
+            pair = np.stack((words16(np.zeros(s.pages), "bf16"), words16(-2.0 ** (70 + e[:, slot]), "bf16")), -1)
+            held[:, at:at + 4] = pair.astype("<u2").view(np.uint8)
+    s.data.copy_(torch.from_numpy(held))
+    q = torch.full((s.tokens, heads, 64), 2.0 ** 32, dtype=torch.bfloat16, device="cuda")
+    out, lse, _ = run_attend(s, q, scale=1.0)
+    v = s.values()[1]
+    req, pos = step.positions(s.start, s.kv_len)
+    for t, (r, p) in enumerate(zip(req, pos)):
+        at = [(s.table[r, j // 16], j % 16) for j in range(p + 1)]
+        low = min(e[x] for x in at)
+        rows = np.stack([v[x] for x in at if e[x] == low])                    # [keys, kv heads, dim]
+        want = np.repeat(rows.mean(0), heads // 2, 0)
+        # probabilities of 1; sums and the division in fp32, rounded once
+        tol = UNIT["bf16"] * np.abs(want) + 2.0 ** -16 * np.abs(rows).max()
+        assert np.all(np.abs(f64(out)[t] - want) <= tol)
+        # the score, exact, times log2 e and back: three roundings of 2^-24 and two constants'
+        assert np.all(np.abs(f64(lse)[t] / -2.0 ** (108 + low) - 1) <= 2.0 ** -21)
 
 
 @pytest.mark.parametrize("dim, dtype, window, scale, heads", [
