@@ -16,8 +16,10 @@
 // definition gets the same codes.  (The angle's fraction of a turn is exact to 2^-40 before
 // that; its rounding to fp32 is off by up to 4e-7, a millionth of a step between codes.)
 //
-// Bound by memory: every element is read once, queries leave as 16 bits, keys and
-// values as 4.5.
+// Bound by memory: every element is read once, queries leave as 16 bits, keys and values as 4.5.
+// 8191 tokens of 48 + 8 + 8 heads of 128, fp32 to bf16: 72 us, 5.3 TB/s, 78 % of what a copy
+// reaches; the rest is cos and sin by radians and a key's partners, loaded again.  (With a thread
+// for both halves of a head's pairs, eight neighbours each: 126 us.)
 #include "kv4.cuh"
 #include "rope_rows.cuh"
 

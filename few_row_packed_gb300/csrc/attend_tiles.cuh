@@ -15,8 +15,8 @@
 //   * A row's reference maximum moves only when it grew by more than 8 (see
 //     attend_rows.cu); only then are its sums in tensor memory rescaled, by the
 //     row's own thread.
-//   * Over a cache of 4 bits four warps in place of the copy warp load the codes,
-//     expand them and store the slots' rows.
+//   * Over a cache of 4 bits the copies bring pieces of codes and scales, and four
+//     more warps expand them and store the slots' rows.
 //   * The blocks of the batch are divided evenly over one CTA per SM, as in
 //     attend_rows.cu; a causal tile counts those that it sees.  The parts of a
 //     divided item are added by a launch of their own (attend_join.cu).
@@ -29,6 +29,14 @@
 // their operations at the same rate 84.  With few blocks the start: 5 us to the first
 // scores and 5 more to fetch the block's code, some 20 KB; 8 tokens after 32,771 take
 // 36 us, their keys and values 20.
+//
+// Over a cache of 4 bits the four warps that expand: of 1,500 clocks a slot they spend 790 to
+// expand and store a thread's 128 elements, 75 in the fence before the MMAs read them, and the
+// rest waiting for codes and for places.  With two row tiles a block's products take nearly as long:
+// 2048 tokens at the end of 16,384 take 555 to 575 us, from the 16-bit cache 490.  With one they do
+// not: 32 requests of 8 tokens over 7,000 keys 148 us, from 16 bits 159.  Eight warps, keys and
+// values apart, leave the streams 168 registers or less, whose spills cost more than is won: 603
+// to 670 us and 157 to 163.
 #pragma once
 
 #include "attend_common.cuh"
@@ -57,7 +65,8 @@ template <bool KV4>
 struct Roles {
     static constexpr int THREADS = KV4 ? 512 : 384;
     // registers a thread after the split: 168 * 384 at launch = 88 * 128 + 208 * 256, and
-    // 128 * 512 = (80 + 48) * 128 + 192 * 256
+    // 128 * 512 = (80 + 48) * 128 + 192 * 256 (64 to expand and 184 for the streams: 1 to 4 %
+    // longer; 72 + 56: 2 %; 64 + 48 and 200: 3 to 5 %)
     static constexpr int CONTROL = KV4 ? 80 : 88, STREAM = KV4 ? 192 : 208, EXPAND = 48;
     // who fills a slot, and who reads an item (copies, MMAs, eight warps of the streams, and
     // those that expand)
@@ -88,7 +97,8 @@ struct Geo {
     static constexpr int Q = 0;
     static constexpr int RING = 2 * SLOT;
     static constexpr int NSLOT = (D == 128 ? 5 : 10) - (KV4 ? 128 / D : 0);
-    // 4 bits: a ring of a block's keys or values as they are held, codes and then scales
+    // 4 bits: a ring of a block's keys or values as they are held, codes and then scales (three
+    // of them beside four slots; six beside three slots take the same time within 3 %)
     static constexpr int HELD = RING + NSLOT * SLOT;
     static constexpr int CODES = kKeys * 32 * (D / 64), HSLOT = kKeys * 36 * (D / 64);
     static constexpr int NHELD = KV4 ? (D == 128 ? 3 : 6) : 0;
@@ -648,19 +658,24 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
                     }
                     float t[4][32];
                     if (!idle) {
-                        // masked scores are overwritten in place (rare, so short code)
+                        // masked scores are overwritten in place, 32 keys at a time: rare, so short
+                        // code (a prompt's chunk with a window of 1,024: 91 us; 16 at a time 92.6;
+                        // masked in registers 92.9, and 5 % more for a long context; leaving out
+                        // those 32 that every row sees 93)
                         if (k0 + kKeys > open_hi || k0 < open_lo) {
 #pragma unroll 1
-                            for (int e = 0; e < 8; ++e) {
-                                const uint32_t see = seen32(p, w.first, w.keys, pos, word, k0 + (e & ~1) * 16) >> (e & 1) * 16;
-                                float u[16];
-                                uint32_t r[16];
-                                tmem_ld16(s_at + e * 16, u);
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t see = seen32(p, w.first, w.keys, pos, word, k0 + e * 32);
+                                tmem_ld32(s_at + e * 32, t[0]);
                                 tmem_wait_ld();
 #pragma unroll
-                                for (int k = 0; k < 16; ++k)
-                                    r[k] = (see >> k) & 1u ? __float_as_uint(u[k]) : 0xFF800000u;
-                                tmem_st16(s_at + e * 16, r);
+                                for (int h = 0; h < 2; ++h) {
+                                    uint32_t r[16];
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k)
+                                        r[k] = (see >> (16 * h + k)) & 1u ? __float_as_uint(t[0][16 * h + k]) : 0xFF800000u;
+                                    tmem_st16(s_at + e * 32 + h * 16, r);
+                                }
                             }
                             tmem_wait_st();
                         }

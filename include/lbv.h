@@ -566,11 +566,13 @@ LBV_API lbv_status lbv_rope_destroy(lbv_rope* rope);
  * position, one past the block table, a page outside the cache) has its key
  * and value left out; its query is rotated all the same.
  * A cache of 4 bits gets, for each 64 elements x of a rotated key or a value (fp32):
- * bias = min x and scale = (max x - min x) * (1 / 15), each rounded to the cache's dtype, and the codes
- * (x - bias) * (1 / scale), rounded to the nearest whole number in 0..15 (all 0 where the scale is 0 or
- * below 2^-126).  So that equal inputs give equal codes wherever the definition is followed,
- * every operation is rounded by itself there: the angle's fraction of a turn is cut to 2^-40 and
- * taken to fp32 radians, whose cos and sin are fp32, and so are products and sums.  A group with a NaN or a magnitude above 2^15 (fp16) or 2^126 (bf16) reads as NaN.
+ * bias = min x and scale = (max x - min x) * (1 / 15), each rounded to the cache's
+ * dtype, and the codes (x - bias) * (1 / scale), rounded to the nearest whole number in
+ * 0..15 (all 0 where the scale is 0 or below 2^-126).  So that equal inputs give equal
+ * codes wherever the definition is followed, every operation is rounded by itself
+ * there: the angle's fraction of a turn is cut to 2^-40 and taken to fp32 radians, whose
+ * cos and sin are fp32, and so are products and sums.  A group with a NaN or a
+ * magnitude above 2^15 (fp16) or 2^126 (bf16) reads as NaN.
  * Errors: LBV_ERR_INVALID_ARG for null or misaligned pointers, sizes that do
  * not agree and dtypes that cannot be; LBV_ERR_UNSUPPORTED if rot_dim exceeds
  * the head.  The library allocates nothing.
@@ -606,7 +608,10 @@ LBV_API size_t lbv_attend_workspace_bytes(const lbv_kv_cache* cache, const lbv_b
  * by adds the rounded probabilities in the few-row kernel (up to 16 rows, new
  * tokens times query heads of a group, a request on average); in the
  * tensor-memory kernel (more rows) those of blocks where one key is half of a row's
- * sum so far, and the unrounded ones of the others.  So the same request may
+ * sum so far, and the unrounded ones of the others.  Over a cache of 4 bits the
+ * few-row kernel serves up to 24 rows and divides by the sum of the unrounded
+ * probabilities (an error of half a step of the type, where 4 bits hold a value to 2^-5
+ * of its group's range).  So the same request may
  * differ by the rounding of the probabilities between batches of either kind.
  * lse adds the unrounded ones in both.  Cache slots at or past
  * kv_len may hold anything; keys and values below it are taken to be finite.
@@ -675,7 +680,8 @@ LBV_API lbv_status lbv_kv_keep(const lbv_batch* batch, const lbv_kv_cache* cache
 
 /*
  * Copies page src[i] to page dst[i], keys and values of every slot, for i < count (dev
- * int32 arrays; at most the cache's pages): for requests that share pages and write to one of them, or to close up a cache.
+ * int32 arrays; at most the cache's pages): for requests that share pages and write to
+ * one of them, or to close up a cache.
  * A pair with a page outside the cache is left out.  No page is dst of one pair and
  * src or dst of another (the page would hold a mixture).  Errors:
  * LBV_ERR_INVALID_ARG.
