@@ -17,9 +17,13 @@
 // that; its rounding to fp32 is off by up to 4e-7, a millionth of a step between codes.)
 //
 // Bound by memory: every element is read once, queries leave as 16 bits, keys and values as 4.5.
-// 8191 tokens of 48 + 8 + 8 heads of 128, fp32 to bf16: 72 us, 5.3 TB/s, 78 % of what a copy
-// reaches; the rest is cos and sin by radians and a key's partners, loaded again.  (With a thread
-// for both halves of a head's pairs, eight neighbours each: 126 us.)
+// 8191 tokens of 48 + 8 + 8 heads of 128, fp32 to bf16: 64 us, 5.9 TB/s, 87 % of what a copy
+// reaches.  From bf16 56 us, 4.3 TB/s: there the instructions count, a third of them cos and sin by
+// radians and the codes.  (With a thread for both halves of a head's pairs, eight neighbours
+// each: 126 us from fp32.  With 256 threads a block, addresses and turns anew for every item and
+// elements turned to fp32 as they are loaded, which waits for each item's loads: 70 and 92.)
+#include <type_traits>
+
 #include "kv4.cuh"
 #include "rope_rows.cuh"
 
@@ -29,8 +33,9 @@ using namespace rope;
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kAhead = 4;             // items a thread keeps in flight
+constexpr int kThreads = 128;
+constexpr int kAhead = 4;             // items a thread keeps in flight (2: 17 %, 8: 4 % longer)
+constexpr int kBlocks = 8;            // blocks an SM has room for in registers (left to the compiler: 4 % longer)
 
 // cos and sin of pair j at position `at`, times the factor.
 __device__ __forceinline__ float2 turn32_of(const RopeParams& p, int j, int at)
@@ -51,8 +56,37 @@ __device__ __forceinline__ float dot(float a, float b, float c, float d)
     return __fadd_rn(__fmul_rn(a, b), __fmul_rn(c, d));
 }
 
+// Four elements as they are in memory: turned to fp32 where they are used, so that the loads of
+// all items are under way before one is waited for.
+template <int SRC>
+using Raw = std::conditional_t<SRC == LBV_F32, float4, uint2>;
+
+template <int SRC, bool VEC>
+__device__ __forceinline__ Raw<SRC> load_raw(const void* base, int64_t at)
+{
+    if constexpr (SRC == LBV_F32) {
+        const float* s = static_cast<const float*>(base) + at;
+        return VEC ? *reinterpret_cast<const float4*>(s) : make_float4(s[0], s[1], s[2], s[3]);
+    } else {
+        const uint16_t* s = static_cast<const uint16_t*>(base) + at;
+        return VEC ? *reinterpret_cast<const uint2*>(s)
+                   : make_uint2(s[0] | (uint32_t)s[1] << 16, s[2] | (uint32_t)s[3] << 16);
+    }
+}
+
+template <int SRC>
+__device__ __forceinline__ void unpack(const Raw<SRC>& r, float* x)
+{
+    if constexpr (SRC == LBV_F32) {
+        x[0] = r.x, x[1] = r.y, x[2] = r.z, x[3] = r.w;
+    } else {
+        x[0] = to_f32<SRC>((uint16_t)r.x), x[1] = to_f32<SRC>((uint16_t)(r.x >> 16));
+        x[2] = to_f32<SRC>((uint16_t)r.y), x[3] = to_f32<SRC>((uint16_t)(r.y >> 16));
+    }
+}
+
 template <int SRC, int DST, bool HALF, bool VEC>
-__global__ void __launch_bounds__(kThreads) lbv_rope_append4_kernel(const __grid_constant__ RopeParams p)
+__global__ void __launch_bounds__(kThreads, kBlocks) lbv_rope_append4_kernel(const __grid_constant__ RopeParams p)
 {
     __shared__ float2 turn[kMaxRot / 2];
     __shared__ int where[2];                       // request (-1: none), cache position
@@ -63,28 +97,26 @@ __global__ void __launch_bounds__(kThreads) lbv_rope_append4_kernel(const __grid
     const int total = keys + (2 * p.kv.heads << per_head_shift);
     const int step = kThreads * gridDim.y;
     const int first = blockIdx.y * kThreads + threadIdx.x;
+    // A thread's items are in one place of their heads: of a query, two groups of four; of a key
+    // or value, eight neighbours.
+    const int in_head = first & ((1 << per_head_shift) - 1), at = in_head * 8;
+    const Item m = item_of<HALF>(p, in_head, per_head_shift);
 
     after_previous();
-    float x0[kAhead][4], x1[kAhead][4];
-    // where eight neighbours of a key or value are: head (values after keys), first element
-    auto piece_of = [&](int it, int& which, int& head, int& at) {
-        const int e = it - keys, row = e >> per_head_shift;
+    Raw<SRC> x0[kAhead], x1[kAhead];
+    // the head of an item of keys or values, which come after the keys
+    auto row_of = [&](int it, int& which) {
+        const int row = (it - keys) >> per_head_shift;
         which = row >= p.kv.heads ? 2 : 1;
-        head = row - (which - 1) * p.kv.heads;
-        at = (e - (row << per_head_shift)) * 8;
+        return row - (which - 1) * p.kv.heads;
     };
-    auto fetch = [&](int it, float (&a)[4], float (&b)[4]) {
-        int which = 0, head, o0, o1;
-        if (it < keys) {
-            const Item m = item_of<HALF>(p, it, per_head_shift);
-            head = m.head, o0 = m.o0, o1 = m.o1;
-        } else {
-            piece_of(it, which, head, o0);
-            o1 = o0 + 4;
-        }
-        const int64_t at = tok * p.src_token[which] + head * p.src_head[which];
-        load4<SRC, VEC>(p.src[which], at + o0, a);
-        load4<SRC, VEC>(p.src[which], at + o1, b);
+    auto fetch = [&](int it, Raw<SRC>& a, Raw<SRC>& b) {
+        const bool query = it < keys;
+        int which = 0;
+        const int head = query ? it >> per_head_shift : row_of(it, which);
+        const int64_t from = tok * p.src_token[which] + head * p.src_head[which];
+        a = load_raw<SRC, VEC>(p.src[which], from + (query ? m.o0 : at));
+        b = load_raw<SRC, VEC>(p.src[which], from + (query ? m.o1 : at + 4));
     };
     auto is = [&](int it) { return it < queries || (it >= keys && it < total); };
 #pragma unroll
@@ -102,12 +134,18 @@ __global__ void __launch_bounds__(kThreads) lbv_rope_append4_kernel(const __grid
     const int slot = pos & ((1 << p.kv.page_shift) - 1);
     __syncthreads();
 
-    auto query = [&](int it, float (&a)[4], float (&b)[4]) {
-        const Item m = item_of<HALF>(p, it, per_head_shift);
+    float2 turns[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        turns[i] = turn[max(m.pair, 0) + i];
+    auto query = [&](int it, const Raw<SRC>& x0, const Raw<SRC>& x1) {
+        float a[4], b[4];
+        unpack<SRC>(x0, a);
+        unpack<SRC>(x1, b);
         if (m.pair >= 0) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float2 t = turn[m.pair + i];
+                const float2 t = turns[i];
                 float& x = HALF ? a[i] : i < 2 ? a[2 * i] : b[2 * i - 4];
                 float& y = HALF ? b[i] : i < 2 ? a[2 * i + 1] : b[2 * i - 3];
                 const float xn = cross(x, t.x, y, t.y);
@@ -115,16 +153,18 @@ __global__ void __launch_bounds__(kThreads) lbv_rope_append4_kernel(const __grid
                 x = xn;
             }
         }
-        uint16_t* d = p.q_out + tok * p.out_token + m.head * p.out_head;
+        uint16_t* d = p.q_out + tok * p.out_token + (it >> per_head_shift) * p.out_head;
         store4<DST, VEC>(d + m.o0, a);
         store4<DST, VEC>(d + m.o1, b);
     };
     // all lanes of a warp come here together; those past the last do nothing
-    auto held = [&](int it, float (&x0)[4], float (&x1)[4]) {
+    auto held = [&](int it, const Raw<SRC>& x0, const Raw<SRC>& x1) {
         const bool in = it < total;
-        int which, head, at;
-        piece_of(in ? it : keys, which, head, at);
-        float a[8] = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
+        int which;
+        const int head = row_of(in ? it : keys, which);
+        float a[8];
+        unpack<SRC>(x0, a);
+        unpack<SRC>(x1, a + 4);
         if (in && which == 1 && at < p.rot) {
             const int half = p.rot >> 1;           // a multiple of 4
 #pragma unroll
@@ -133,7 +173,8 @@ __global__ void __launch_bounds__(kThreads) lbv_rope_append4_kernel(const __grid
                 if constexpr (HALF) {
                     const bool low = o < half;
                     float b[4];
-                    load4<SRC, VEC>(p.src[1], tok * p.src_token[1] + head * p.src_head[1] + (low ? o + half : o - half), b);
+                    unpack<SRC>(load_raw<SRC, VEC>(p.src[1], tok * p.src_token[1] + head * p.src_head[1] +
+                                                                 (low ? o + half : o - half)), b);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float2 t = turn[(low ? o : o - half) + i];
@@ -188,7 +229,7 @@ __global__ void __launch_bounds__(kThreads) lbv_rope_append4_kernel(const __grid
         if ((at & 63) == 0)
             *reinterpret_cast<uint32_t*>(c + kv4::scale_at(planes, plane, to, cs)) = scale | ((uint32_t)bias << 16);
     };
-    auto finish = [&](int it, float (&a)[4], float (&b)[4]) {
+    auto finish = [&](int it, const Raw<SRC>& a, const Raw<SRC>& b) {
         if (it - lane >= keys)                     // a warp has either
             held(it, a, b);
         else if (it < queries)
