@@ -25,7 +25,7 @@
 // this kernel, as attend_rows.cu does for small batches, cost the block's loop registers.)
 //
 // What bounds it (48 query over 8 key/value heads of 128): 64 requests of one token over
-// 500 to 16,384 keys, 396 MB, take 94 us, 4.2 TB/s, 62 % of what a copy reaches; the 16-bit
+// 500 to 16,384 keys, 396 MB, take 93 us, 4.3 TB/s, 63 % of what a copy reaches; the 16-bit
 // cache's kernel takes 221.  Issue slots are 68 % busy with 71 million instructions, a third of
 // them codes', and the copies alone (no codes expanded) take 67 us.  More rows cost their products
 // and probabilities: 32 requests over 7,000 keys take 70 us with 6 rows each, 94 with 12, 121 with
@@ -81,12 +81,12 @@ struct Geo {
     // (two stages, and four, take 4 to 7 % longer)
     static constexpr int NST = D == 64 ? 6 : 3;
     static constexpr int SLOT = ROWS * (D + 3);             // floats of one partial result
-    // a team's shared memory: the ring, the warps' results, queries of more than two tiles as
-    // the lanes hold them
+    // a team's shared memory: the ring, the warps' results, the queries as the lanes want them (in
+    // registers: one tile's cost 1 %, two tiles' 6 %, by what they leave to the rest)
     static constexpr int JOIN = NST * STAGE;
     static constexpr int JROWS = 8;                       // rows joined at a time
     static constexpr int QUERIES = JOIN + kKeyWarps * JROWS * D * 4;
-    static constexpr int STATS = QUERIES + (NT == 3 ? NT * 32 * (D / 8) * 4 : 0);   // [4][ROWS] maxima, sums
+    static constexpr int STATS = QUERIES + NT * 32 * (D / 8) * 4;   // [4][ROWS] maxima, sums
     static constexpr int WORDS = STATS + 2 * kKeyWarps * ROWS * 4;  // uint64 [ROWS]: the rows' words of the tree
     static constexpr int ITEMS = WORDS + 8 * ROWS;
     static constexpr int START = ITEMS;                     // where the share begins, before its first item
@@ -279,6 +279,7 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
     // scores are c times the products; a scale of zero clears Q
     const float c = p.scale_log2 == 0.f ? 1.f : p.scale_log2;
     const float hidden = c < 0.f ? INFINITY : -INFINITY;
+    const uint32_t queries = sbase + G::QUERIES;
     float* joint = reinterpret_cast<float*>(smem + G::JOIN);
     float* stats = reinterpret_cast<float*>(smem + G::STATS);
     uint64_t* words = reinterpret_cast<uint64_t*>(smem + G::WORDS);
@@ -296,9 +297,8 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
         const Item& w = items[it % kItems];
         const int nb = w.nb, item_rows = w.rows;
         // The queries as the second operand: lane (g, t) has the t-th quarter of row g, a pair of
-        // elements a register.
-        constexpr int QR = D / 8, QT = NT == 3 ? 1 : NT;         // registers a tile; tiles kept in them
-        uint32_t qf[QT][QR];
+        // elements a word.  (Every warp writes all of them: the values are alike.)
+        constexpr int QR = D / 8;                                // words of a row of a tile
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             const int row = w.row0 + 8 * i + g;
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
             const int tok = token_of(p, row);
             const uint16_t* src = p.q + (int64_t)(w.q0 + (in ? tok : 0)) * p.q_token +
                                   (int64_t)(w.head * p.group + (in ? row - tok * p.group : 0)) * p.q_head + t * (D / 4);
-            uint32_t(&q)[QR] = qf[NT == 3 ? 0 : i];
+            uint32_t q[QR];
             if (!in) {
 #pragma unroll
                 for (int e = 0; e < QR; ++e)
@@ -322,18 +322,14 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
                 for (int e = 0; e < QR; ++e)
                     q[e] = (uint32_t)src[2 * e] | ((uint32_t)src[2 * e + 1] << 16);
             }
-            // (the same for every warp, and each writes it all: the values are alike)
-            if (NT == 3) {
 #pragma unroll
-                for (int e = 0; e < QR / 4; ++e)
-                    *reinterpret_cast<uint4*>(smem + G::QUERIES + ((i * (QR / 4) + e) * 32 + lane) * 16) =
-                        make_uint4(q[4 * e], q[4 * e + 1], q[4 * e + 2], q[4 * e + 3]);
-            }
+            for (int e = 0; e < QR / 4; ++e)
+                *reinterpret_cast<uint4*>(smem + G::QUERIES + ((i * (QR / 4) + e) * 32 + lane) * 16) =
+                    make_uint4(q[4 * e], q[4 * e + 1], q[4 * e + 2], q[4 * e + 3]);
         }
         if (p.tree && tid % kTeam < item_rows)
             words[tid % kTeam] = p.tree[w.q0 + token_of(p, w.row0 + tid % kTeam)];
-        if (NT == 3 || p.tree)
-            named_bar_sync(bar, kTeam);
+        named_bar_sync(bar, kTeam);
         float o[NT][D / 16][4];                                  // tile j: elements g D / 8 + 2 j, and the next
         float2 minus[NT], l[NT];                                 // references, negated, and sums of rows 2 t and 2 t + 1
 #pragma unroll
@@ -403,14 +399,8 @@ __global__ void __launch_bounds__(Geo<D, NT>::THREADS, 1)
                         const uint32_t a[4] = {e[0][2 * k], e[1][2 * k], e[0][2 * k + 1], e[1][2 * k + 1]};
 #pragma unroll
                         for (int i = 0; i < NT; ++i) {
-                            const int at = u * 4 + k * 2;
-                            if (NT == 3) {
-                                const uint2 q = load8(sbase + G::QUERIES +
-                                                      ((i * (QR / 4) + at / 4) * 32 + lane) * 16 + (at % 4) * 4);
-                                mma<DT>(s[i], a, q.x, q.y);
-                            } else {
-                                mma<DT>(s[i], a, qf[i][at], qf[i][at + 1]);
-                            }
+                            const uint2 q = load8(queries + ((i * (QR / 4) + u) * 32 + lane) * 16 + k * 8);
+                            mma<DT>(s[i], a, q.x, q.y);
                         }
                     }
                 }
