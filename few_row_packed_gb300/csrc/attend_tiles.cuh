@@ -15,8 +15,8 @@
 //   * A row's reference maximum moves only when it grew by more than 8 (see
 //     attend_rows.cu); only then are its sums in tensor memory rescaled, by the
 //     row's own thread.
-//   * Over a cache of 4 bits the copies bring pieces of codes and scales, and four
-//     more warps expand them and store the slots' rows.
+//   * Over a cache of 4 bits two warps copy pieces of codes and scales, and four more
+//     expand them and store the slots' rows.
 //   * The blocks of the batch are divided evenly over one CTA per SM, as in
 //     attend_rows.cu; a causal tile counts those that it sees.  The parts of a
 //     divided item are added by a launch of their own (attend_join.cu).
@@ -34,7 +34,7 @@
 // expand and store a thread's 128 elements, 75 in the fence before the MMAs read them, and the
 // rest waiting for codes and for places.  With two row tiles a block's products take nearly as long:
 // 2048 tokens at the end of 16,384 take 555 to 575 us, from the 16-bit cache 490.  With one they do
-// not: 32 requests of 8 tokens over 7,000 keys 148 us, from 16 bits 159.  Eight warps, keys and
+// not: 32 requests of 8 tokens over 7,000 keys 147 us, from 16 bits 159.  Eight warps, keys and
 // values apart, leave the streams 168 registers or less, whose spills cost more than is won: 603
 // to 670 us and 157 to 163.
 #pragma once
@@ -68,9 +68,9 @@ struct Roles {
     // 128 * 512 = (80 + 48) * 128 + 192 * 256 (64 to expand and 184 for the streams: 1 to 4 %
     // longer; 72 + 56: 2 %; 64 + 48 and 200: 3 to 5 %)
     static constexpr int CONTROL = KV4 ? 80 : 88, STREAM = KV4 ? 192 : 208, EXPAND = 48;
-    // who fills a slot, and who reads an item (copies, MMAs, eight warps of the streams, and
-    // those that expand)
-    static constexpr int FILLERS = KV4 ? 4 : 1, READERS = KV4 ? 14 : 10;
+    // who fills a slot, and who reads an item (copies, of 4 bits by two warps, MMAs, eight warps
+    // of the streams, and those that expand)
+    static constexpr int FILLERS = KV4 ? 4 : 1, READERS = KV4 ? 15 : 10;
 };
 
 constexpr int kItems = 4;                        // items the roles may be apart
@@ -259,13 +259,16 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(R::CONTROL));
-        if (KV4 && warp == 0) {
-            // ---- copies as the rows are held: K and V of each block in turn; lanes 2 i and
-            // 2 i + 1 have the codes and the scales of chunk i ----
+        if (KV4 && (warp == 0 || warp == 3)) {
+            // ---- copies as the rows are held: K of each block by one warp, V by the other; lanes
+            // 2 i and 2 i + 1 have the codes and the scales of chunk i.  (A lane's copy takes its
+            // warp some 40 clocks to issue: 32 requests of 8 tokens over 7,000 keys take 209 us with
+            // pages of 16 slots and one warp, 147 with two; heads of 64, pages of 64, 132 and 103.) ----
             const int cs = kv4::chunk_shift(p.kv), chunk0 = (lane >> 1) << cs;
             const int64_t page_bytes = kv4::page_bytes(p.kv);
             const uint32_t size = lane & 1 ? 4 * (D / 64) << cs : 32 * (D / 64) << cs;
-            int n = 0;                                               // copies so far
+            const int v = warp == 3;
+            int n = v;                                               // the next copy
             for (int it = 0;; ++it) {
                 const Item& w = item_at(it);
                 if (!ok || w.nb == 0)
@@ -278,14 +281,14 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
                                ? table[key >> p.kv.page_shift]
                                : -1;
                 };
-                int page = -1, next = page_of(0);
-                for (int i = 0; i < 2 * w.nb; ++i) {
-                    const int st = n % max(G::NHELD, 1), k0 = w.key_of(i >> 1);
-                    if ((i & 1) == 0) {
-                        page = next;
-                        next = page_of((i >> 1) + 1);
-                    }
-                    // read, and its last copy landed (see attend_rows.cu)
+                int next = page_of(0);
+                for (int b = 0; b < w.nb; ++b) {
+                    const int st = n % max(G::NHELD, 1), k0 = w.key_of(b), page = next;
+                    next = page_of(b + 1);
+                    // read, and its last copy landed (see attend_rows.cu).  In a ring of an odd length
+                    // that copy was the other warp's.  This warp's copy before had waited for the
+                    // reading of a later one than the place's last but one, so the parity cannot
+                    // mean that one.
                     if (n >= G::NHELD) {
                         wait(held_empty(st), (uint32_t)((n / max(G::NHELD, 1) - 1) & 1));
                         wait(held_full(st), (uint32_t)((n / max(G::NHELD, 1) - 1) & 1));
@@ -293,7 +296,7 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
                     ok = __all_sync(0xffffffffu, ok && ((unsigned)n < p.first_copies || blockIdx.x > 0));
                     if (!ok)
                         break;
-                    ++n;
+                    n += 2;
                     const bool go = page >= 0 && page < p.kv.pages;
                     const unsigned there = __ballot_sync(0xffffffffu, go);
                     if (lane == 0) {
@@ -307,7 +310,7 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
                     if (go) {
                         const int s = (k0 + chunk0) & ((1 << p.kv.page_shift) - 1);
                         bulk_copy(sbase + G::HELD + st * G::HSLOT + (lane & 1 ? G::CODES : 0) + (lane >> 1) * size,
-                                  base + page * page_bytes + (s >> cs) * (kv4::slot_bytes(D) << cs) + (i & 1) * size,
+                                  base + page * page_bytes + (s >> cs) * (kv4::slot_bytes(D) << cs) + v * size,
                                   size, held_full(st));
                     }
                 }
@@ -315,10 +318,11 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
                 if (lane == 0)
                     mbar_arrive(item_empty(it));
             }
-            // the copies land before shared memory goes away, also after a wait that ran out
-            for (int i = 0; i < G::NHELD; ++i)
-                if (n - 1 - i >= 0 && !mbar_wait(held_full((n - 1 - i) % max(G::NHELD, 1)),
-                                                 (uint32_t)(((n - 1 - i) / max(G::NHELD, 1)) & 1), p.wait_limit))
+            // the copies land before shared memory goes away, also after a wait that ran out: the
+            // ring's last, or then this warp's own
+            const int last = ok ? (n & ~1) - 1 : n - 2, step = ok ? 1 : 2;
+            for (int i = last; i >= 0 && i > last - G::NHELD; i -= step)
+                if (!mbar_wait(held_full(i % max(G::NHELD, 1)), (uint32_t)((i / max(G::NHELD, 1)) & 1), p.wait_limit))
                     ok = false;
         } else if (warp == 0) {
             // ---- copies: K and V of each block in turn ----
