@@ -220,3 +220,39 @@ def test_largest_page_and_single_head():
             # the probabilities and the output are rounded once each; scores are fp32 sums of dim terms
             e = (dim + 8) * 2.0 ** -24 * (q[:m, 0].double().abs() @ k[:, 0].double().abs().T).amax(-1) * dim ** -0.5 + 2.0 ** -20
             assert torch.all((out[:m, 0].double() - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2 * e[:, None]) * size)
+
+
+@pytest.mark.parametrize("dim, page, dtype", [(128, 8, "f16"), (128, 64, "bf16"), (64, 16, "f16")])
+def test_two_calls_at_once(dim, page, dtype):
+    """Few rows and many rows over one cache of 4 bits, on two streams with a workspace each,
+    again and again: the results are those of a call alone, to the bit."""
+    g = torch.Generator(device="cuda").manual_seed(page)
+    requests, longest, heads, kv_heads = 24, 2100, 12, 2
+    width = -(-longest // page)
+    cache = empty_cache(4, requests * width, page, kv_heads, dim, dtype)
+    table = torch.randperm(requests * width, generator=g, device="cuda").int().view(requests, width)
+    kv_len = torch.randint(300, longest + 1, (requests,), generator=g, device="cuda").int()
+    whole = lbv.Batch(torch.cat([kv_len.new_zeros(1), kv_len.cumsum(0).int()]), kv_len, table, int(kv_len.sum()))
+    rows = [torch.randn((whole.tokens, kv_heads, dim), generator=g, device="cuda") for _ in "kv"]
+    lbv.rope_append(lbv.Rope(lbv.rope_frequencies(dim)), whole, cache, None, *rows, None)
+    calls = []
+    for n in (1, 3, 9, 50):                             # 6, 18, 54 and 300 rows a request and key/value head
+        start = torch.arange(0, requests * n + 1, n, dtype=torch.int32, device="cuda")
+        batch = lbv.Batch(start, kv_len, table, requests * n)
+        q = torch.randn((requests * n, heads, dim), generator=g, device="cuda").to(DT[dtype])
+        ws = torch.zeros(lbv.attend_workspace_bytes(cache, batch, heads), dtype=torch.uint8, device="cuda")
+        want = torch.empty_like(q)
+        lbv.attend(cache, batch, q, want, dim ** -0.5, workspace=ws)
+        lbv.attend_status(ws)
+        calls.append((batch, q, ws, want))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    outs = [[torch.empty_like(c[1]) for _ in range(6)] for c in calls]
+    torch.cuda.synchronize()
+    for i in range(6):
+        for (batch, q, ws, _), st, out in zip(calls, streams, outs):
+            lbv.attend(cache, batch, q, out[i], dim ** -0.5, workspace=ws, stream=st)
+    torch.cuda.synchronize()
+    for (_, _, ws, want), out in zip(calls, outs):
+        lbv.attend_status(ws)
+        assert all(torch.equal(want, o) for o in out)
