@@ -33,7 +33,7 @@
 // Over a cache of 4 bits the four warps that expand: of 1,500 clocks a slot they spend 790 to
 // expand and store a thread's 128 elements, 75 in the fence before the MMAs read them, and the
 // rest waiting for codes and for places.  With two row tiles a block's products take nearly as long:
-// 2048 tokens at the end of 16,384 take 555 to 575 us, from the 16-bit cache 490.  With one they do
+// 2048 tokens at the end of 16,384 take 560 to 580 us, from the 16-bit cache 490.  With one they do
 // not: 32 requests of 8 tokens over 7,000 keys 147 us, from 16 bits 159.  Eight warps, keys and
 // values apart, leave the streams 168 registers or less, whose spills cost more than is won: 603
 // to 670 us and 157 to 163.
