@@ -26,11 +26,11 @@
 //
 // What bounds it (48 query over 8 key/value heads of 128): 64 requests of one token over
 // 500 to 16,384 keys, 396 MB, take 93 us, 4.3 TB/s, 63 % of what a copy reaches; the 16-bit
-// cache's kernel takes 221.  Issue slots are 68 % busy with 71 million instructions, a third of
-// them codes', and the copies alone (no codes expanded) take 67 us.  More rows cost their products
-// and probabilities: 32 requests over 7,000 keys take 70 us with 6 rows each, 94 with 12, 121 with
-// 24, where three teams an SM hide less of an instruction's latency.  A single request is its
-// launches, its start and its join: one token over 2,011 keys 10.5 us.
+// cache's kernel takes 221.  Issue slots are 68 % busy with 70 million instructions, half of them
+// codes', and their pipes near half; the copies alone (no codes expanded) take 67 us, three teams an SM
+// in place of four 94.  More rows cost their products and probabilities: 32 requests over 7,000
+// keys take 68 us with 6 rows each, 87 with 12, 120 with 24.  A single request is its launches, its
+// start and its join: one token over 2,011 keys 9.5 us.
 //
 // The divisor adds the probabilities before their rounding to 16 bits (off by 2^-9 of a
 // value for a row that one key dominates; the values themselves are held to 2^-5).
