@@ -27,8 +27,8 @@
 // What bounds it (48 query over 8 key/value heads of 128): 64 requests of one token over
 // 500 to 16,384 keys, 396 MB, take 93 us, 4.3 TB/s, 63 % of what a copy reaches; the 16-bit
 // cache's kernel takes 221.  Issue slots are 68 % busy with 70 million instructions, half of them
-// codes', and their pipes near half; the copies alone (no codes expanded) take 67 us, three teams an SM
-// in place of four 94.  More rows cost their products and probabilities: 32 requests over 7,000
+// codes', and their pipes near half; the copies alone (no codes expanded) take 67 us.
+// (Three teams an SM in place of four: 2 % longer.)  More rows cost their products and probabilities: 32 requests over 7,000
 // keys take 68 us with 6 rows each, 87 with 12, 120 with 24.  A single request is its launches, its
 // start and its join: one token over 2,011 keys 9.5 us.
 //

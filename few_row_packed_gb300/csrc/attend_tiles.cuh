@@ -33,8 +33,8 @@
 // Over a cache of 4 bits the four warps that expand: of 1,500 clocks a slot they spend 790 to
 // expand and store a thread's 128 elements, 75 in the fence before the MMAs read them, and the
 // rest waiting for codes and for places.  With two row tiles a block's products take nearly as long:
-// 2048 tokens at the end of 16,384 take 560 to 580 us, from the 16-bit cache 490.  With one they do
-// not: 32 requests of 8 tokens over 7,000 keys 147 us, from 16 bits 159.  Eight warps, keys and
+// 2048 tokens at the end of 16,384 take 555 to 575 us, from the 16-bit cache 490.  With one they do
+// not: 32 requests of 8 tokens over 7,000 keys 142 us, from 16 bits 159.  Eight warps, keys and
 // values apart, leave the streams 168 registers or less, whose spills cost more than is won: 603
 // to 670 us and 157 to 163.
 #pragma once
@@ -57,8 +57,12 @@ constexpr int kRows = 2 * kTile;                 // rows per item
 // 600 tokens, us: 16/3/4 141, these 139, 28/3/4 141, 24/4/4 143, 36/4/5 142; a prompt's
 // chunk is the same within 1 %.  The least share: 40 small batches take 4 % less with 8 or
 // 12 than with 24, 12 % less than with 48; 20 tokens over 3,943 keys 15.6 and 20.3 us.)
-constexpr int kExtra = 24, kNarrow = 3, kWide = 4, kMinUnits = 12;
-using Items = Shape<kRows, kKeys, kExtra, kNarrow, kWide, kTile>;
+// Over 4 bits a block takes as long to expand for one row tile as for two: 16/4/4 is 1 to 5 %
+// faster there than 24/3/4 (64 requests of 4 to 16 tokens 122 us and 128, the 16 above 167 and 170);
+// 12 and 24 are between.
+constexpr int kMinUnits = 12;
+template <bool KV4>
+using Items = Shape<kRows, kKeys, KV4 ? 16 : 24, KV4 ? 4 : 3, 4, kTile>;
 // Warps: copies and MMAs, then the two streams; over a cache of 4 bits four more, which expand what
 // the copies bring into the slots.
 template <bool KV4>
@@ -469,7 +473,7 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
         } else if (warp == 2) {
             // ---- the share's items ----
             Start& start = *reinterpret_cast<Start*>(smem + G::START);
-            find_start<Items>(p, lane, gridDim.x, kMinUnits, blockIdx.x, &start);
+            find_start<Items<KV4>>(p, lane, gridDim.x, kMinUnits, blockIdx.x, &start);
             __syncwarp();
             Item* out = reinterpret_cast<Item*>(smem + G::ITEMS);
             if ((int)blockIdx.x >= start.ctas) {             // fewer units than CTAs
@@ -478,7 +482,7 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
                     mbar_arrive(item_full(0));
                 }
             } else {
-                Walk<Items> w(p, start, blockIdx.x);
+                Walk<Items<KV4>> w(p, start, blockIdx.x);
                 int slot0 = 0;
                 for (int it = 0;; ++it) {
                     const bool more = w.next();

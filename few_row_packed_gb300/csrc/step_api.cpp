@@ -551,8 +551,8 @@ static lbv_status attend(const char* fn, const lbv_kv_cache* cache, const lbv_ba
     p.wait_limit = copies < 0 ? lbv::kAttendWaitLimit : lbv::kAttendTestLimit;
     p.first_copies = copies < 0 ? ~0u : (unsigned)copies;
     // Both kernels are right for every length.  Over 4 bits 32 requests of 7,000 keys take the few-row
-    // kernel 120 us with 24 rows each and 215 with 30, which are two of its tiles; the other 144 with
-    // 30 and 149 with 96.
+    // kernel 120 us with 24 rows each and 215 with 30, which are two of its tiles; the other 139 with
+    // 30 and 145 with 96.
     const int64_t rows = lbv::attend_average_rows(p);
     const auto launch = p.kv.packed ? (rows <= 24 ? lbv::launch_attend4_rows : lbv::launch_attend4_tiles)
                                     : (rows <= 16 ? lbv::launch_attend_rows : lbv::launch_attend_tiles);
