@@ -1,0 +1,77 @@
+"""GPU tests of attention at scores of any size, over caches of 16 and of 4 bits: the largest
+visible score has weight 1, also where an fp32 number's last bit is worth thousands."""
+import numpy as np
+import pytest
+
+import few_row_packed_gb300 as lbv
+from kv4_setup import DT, UNIT, Setup4, f64, words16
+from oracle import kv4, step
+from test_gpu_step import Setup, run_attend
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    lbv.build()
+
+
+def constant_keys(s, bits, level):
+    """Every element of a slot's key is level[page, slot]."""
+    if bits == 16:
+        s.k.copy_(torch.from_numpy(level)[..., None, None].expand(s.k.shape))
+        return f64(s.v)
+    held = s.data.cpu().numpy()
+    none = words16(np.zeros(s.pages), s.dtype)
+    for slot in range(s.page):
+        for h in range(s.heads):
+            for part in range(s.dim // 64):
+                _, at = kv4.offsets(s.page, s.heads, s.dim, h, slot, 0, part)
+                pair = np.stack((none, words16(level[:, slot], s.dtype)), -1)
+                held[:, at:at + 4] = pair.astype("<u2").view(np.uint8)
+    s.data.copy_(torch.from_numpy(held))
+    return s.values()[1]
+
+
+KINDS = [
+    (4, [2, 1], 2),             # few rows over 4 bits: a tile of 8 rows,
+    (4, [2, 2], 10),            # of 16,
+    (4, [4, 2], 12),            # and of 24
+]
+
+
+@pytest.mark.parametrize("bits, q_len, heads", KINDS)
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("power", [24, 28, 32, 36])
+@pytest.mark.parametrize("sign, scale", [(1, 0.3), (-1, 0.3), (1, -0.7)])
+def test_one_score_wins(bits, q_len, heads, dtype, power, sign, scale):
+    """Constant keys of (1 + r / 128) 2^a against constant queries of (1 + n / 128) 2^b: a score is 64
+    equal products of 16 bits, exact in fp32, and scores that differ do so by 2^-8 of them or
+    more: only the keys of the largest count, equally."""
+    make = Setup if bits == 16 else Setup4
+    s = make(q_len, [190, 300], kv_heads=2, dim=64, dtype=dtype, page=16, seed=power)
+    g = np.random.default_rng(power)
+    a, b = (power - 6) // 2, power - 6 - (power - 6) // 2
+    pages = s.cache.pages
+    level = ((128 + g.integers(0, 128, (pages, 16))) / 128 * 2.0 ** a).astype(np.float32)
+    v = constant_keys(s, bits, level)
+    query = sign * (128 + g.integers(0, 128, (s.tokens, heads))) / 128 * 2.0 ** b
+    q = torch.from_numpy(query)[..., None].expand(-1, -1, 64).to(DT[dtype]).cuda()
+    assert np.array_equal(f64(q)[..., 0], query)
+    out, lse, _ = run_attend(s, q, scale=scale)
+    got, got_lse, toward = f64(out), f64(lse), np.sign(sign * scale)
+    req, pos = step.positions(s.start, s.kv_len)
+    for t, (r, p) in enumerate(zip(req, pos)):
+        at = [(s.table[r, j // 16], j % 16) for j in range(p + 1)]
+        best = toward * max(toward * level[x] for x in at)
+        rows = np.stack([v[x] for x in at if level[x] == best])              # [keys, kv heads, dim]
+        want = np.repeat(rows.mean(0), heads // 2, 0)
+        # probabilities of 1; sums and the division in fp32, rounded once
+        tol = UNIT[dtype] * np.abs(want) + 2.0 ** -16 * np.abs(rows).max()
+        assert np.all(np.abs(got[t] - want) <= tol), (t, np.abs(got[t] - want).max())
+        # the score, exact, times the scale, log2 e and back: five roundings of 2^-24 at most
+        ref = 64 * query[t] * float(best) * float(np.float32(scale)) + np.log(len(rows))
+        assert np.all(np.abs(got_lse[t] / ref - 1) <= 2.0 ** -21)
