@@ -587,8 +587,8 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
         const uint32_t s_at = tmem + lanes + G::S0 + s * 128, o_at = tmem + lanes + G::O0;
         float2* stats = reinterpret_cast<float2*>(smem + G::STATS);
         int16_t* ratios = reinterpret_cast<int16_t*>(smem + G::RATIOS);
-        // scores are c times Q's: a negative scale negates Q, a zero one clears it
-        const float c = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
+        // scores are c0 times Q's: a negative scale negates Q, a zero one clears it
+        const float c0 = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
         int done = 0;                    // blocks of this stream so far
         int met = 0;                     // meetings of the two streams so far
         auto meet = [&] {
@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
             const bool dual = w.dual();
             const int nb = w.nb;
             const int item_row = dual ? s * kTile + trow : trow;
-            float m = -INFINITY;
+            float m = -INFINITY, c = c0;                             // c: what the row's scores are multiplied by
             // sums of the probabilities as they enter the product, and exact
             float2 l = make_float2(0.f, 0.f), x = make_float2(0.f, 0.f);
             int mine = 0;                                            // blocks of this item
@@ -721,11 +721,27 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
                             for (int k = 2; k < 32; k += 2)
                                 tops[e] = fmaxf(tops[e], fmaxf(t[e][k], t[e][k + 1]));
                         }
-                        const float top = c * fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                        const float most = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                        const float top = c * most;
                         const bool moved = top > m + 8.f;            // also from -inf
                         if (__any_sync(0xffffffffu, moved)) {
                             const float f = moved ? ex2(m - top) : 1.f;
-                            m = moved ? top : m;
+                            if (moved) {
+                                c = c0;
+                                m = c0 * most;
+                                // An exponent is c s - m, rounded once, so the largest score's is what was
+                                // rounded off m: up to 1/2 at 2^24, 8 at 2^28, beyond fp32's at 2^32.  From
+                                // 2^24 on c and m are made smaller by a power of two that leaves 2^23 of m.
+                                // Scores there are apart by the rest of a unit or more, and by 2^23 times
+                                // their relative difference: those that this brings nearer differ by
+                                // fewer units of their last place than their sums are off by.  (With scores
+                                // less the largest, times c, as two operations throughout, a prompt's chunk
+                                // over 4 bits takes 4.6 % longer; by this 1.7, which are spilled registers.)
+                                if (fabsf(m) >= 16777216.f) {
+                                    const float less = __uint_as_float((277u << 23) - (__float_as_uint(m) & 0x7F800000u));
+                                    m *= less, c *= less;
+                                }
+                            }
                             l.x *= f, l.y *= f, x.x *= f, x.y *= f;
                             if (mine > 0) {
                                 wait(o_done(s), (uint32_t)((done - 1) & 1));
@@ -743,7 +759,7 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
                             }
                             exps(0);
                         }
-                        heavy = 2.f * ex2(top - m) >= x.x + x.y;
+                        heavy = 2.f * ex2(c * most - m) >= x.x + x.y;
                         block = part;
                         tmem_st16(s_at, r);
                         exps(1);
@@ -804,6 +820,8 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
             }
             if (mine > 0)
                 wait(o_done(s), (uint32_t)((done - 1) & 1));
+            if (c != c0)                                 // a power of two
+                m *= c0 / c;
             float sum = l.x + l.y, exact = x.x + x.y;
             float f0 = 1.f, f1 = 0.f;                    // factors of this row in O_0 and O_1
             if (!dual) {
