@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, Geo<D>::CTAS)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         float& t = s[j][h * 2 + e];
-                        t *= p.scale_log2;
+                        t = __fmul_rn(t, p.scale_log2);          // rounded before it is compared
                         if (masked && !sees(p, w.q, pos[h], words[h], my0 + j * 8 + (lane & 3) * 2 + e))
                             t = -INFINITY;
                         top = fmaxf(top, t);
@@ -308,7 +308,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, Geo<D>::CTAS)
                 const float* t = tops + h * 8 + r0;
                 const float top = fmaxf(fmaxf(t[0], t[ROWS]), fmaxf(t[2 * ROWS], t[3 * ROWS]));
                 shrink[h] = 1.f;
-                if (top > m[h] + 8.f) {                          // also from -inf
+                // (also from -inf; a sum of m and 8 may round to the next number but one)
+                if (top - m[h] > 8.f) {
                     shrink[h] = ex2(m[h] - top);
                     m[h] = top;
                     moved = true;

@@ -81,3 +81,49 @@ def test_one_score_wins(bits, q_len, heads, dtype, power, sign, scale):
         # the score, exact, times the scale, log2 e and back: five roundings of 2^-24 at most
         ref = 64 * query[t] * float(best) * float(np.float32(scale)) + np.log(len(rows))
         assert np.all(np.abs(got_lse[t] / ref - 1) <= 2.0 ** -21)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("heads", [1, 12])
+def test_a_maximum_that_grows_by_one_unit(bits, dtype, heads):
+    """Scores of 2^27 + 16 and then 2^27 + 32, one unit of fp32's last place more: the first keys'
+    weight is 2^-16 of the others'.  (2^27 + 16 and 8 round to 2^27 + 32.)  200 requests over the
+    same pages, so that most are not divided."""
+    requests, page, dim, count = 200, 64, 128, 300
+    g = torch.Generator().manual_seed(3)
+    level = torch.where(torch.arange(5 * page) < 256, 4.0, 8.0).view(5, page, 1)
+    k = torch.empty((5, page, 1, dim))
+    k[..., :64], k[..., 64:] = 2.0 ** 14, level[..., None].expand(-1, -1, -1, 64)
+    v = torch.randn((5, page, 1, dim), generator=g)
+    if bits == 16:
+        k, v = k.to(DT[dtype]).cuda(), v.to(DT[dtype]).cuda()
+        cache, held = lbv.KVCache(k, v), f64(v)
+    else:
+        data = torch.zeros((5, kv4.page_bytes(page, 1, dim)), dtype=torch.uint8, device="cuda")
+        cache = lbv.KVCache4(data, page, 1, dim, DT[dtype])
+        whole = lbv.Batch(*(torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, 320], [320], [[0, 1, 2, 3, 4]])), 320)
+        still = lbv.Rope(np.zeros(8), lbv.ROPE_HALF)        # turns by nothing
+        lbv.rope_append(still, whole, cache, None, k.view(320, 1, dim).cuda(), v.view(320, 1, dim).cuda(), None)
+        back = [torch.empty((320, 1, dim), dtype=DT[dtype], device="cuda") for _ in "kv"]
+        lbv.kv_read(whole, cache, *back)
+        assert torch.equal(back[0].float().cpu(), k.view(320, 1, dim))
+        held = f64(back[1])
+    table = torch.arange(5, dtype=torch.int32).expand(requests, 5).contiguous().cuda()
+    batch = lbv.Batch(torch.arange(requests + 1, dtype=torch.int32, device="cuda"),
+                      torch.full((requests,), count, dtype=torch.int32, device="cuda"), table, requests)
+    q = torch.zeros((requests, heads, dim), dtype=DT[dtype], device="cuda")
+    q[..., 0], q[..., 64] = 2.0 ** 13, 4.0
+    out = torch.empty_like(q)
+    lse = torch.empty((requests, heads), device="cuda")
+    ws = torch.zeros(lbv.attend_workspace_bytes(cache, batch, heads), dtype=torch.uint8, device="cuda")
+    scale = float(np.float32(0.6931472))                    # times log2 e, in fp32: 1
+    assert np.float32(scale) * np.float32(1.44269504088896341) == 1
+    lbv.attend(cache, batch, q, out, scale, lse=lse, workspace=ws)
+    lbv.attend_status(ws)
+    p = 2.0 ** np.where(np.arange(count) < 256, -16.0, 0.0)
+    rows = held.reshape(-1, dim)[:count]
+    want, size = p @ rows / p.sum(), p @ np.abs(rows) / p.sum()
+    # the probabilities are powers of two; sums and the division in fp32, rounded once
+    assert np.all(np.abs(f64(out) - want) <= UNIT[dtype] * np.abs(want) + 2.0 ** -15 * size)
+    assert np.all(np.abs(f64(lse) / ((2.0 ** 27 + 32 + np.log2(p.sum())) * np.log(2)) - 1) <= 2.0 ** -21)
