@@ -553,7 +553,8 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
                 if (!ok)
                     break;
                 ++n;
-                if (lane == 0)                                       // every lane has read
+                __syncwarp();                                        // every lane has read
+                if (lane == 0)
                     mbar_arrive(held_empty(st));
 #pragma unroll
                 for (int part = 0; part < D / 64; ++part) {
