@@ -681,9 +681,9 @@ def kv_read(batch: Batch, cache: KVCache, k, v, stream=None):
 
 def kv_keep(batch: Batch, cache: KVCache, kept, left=None, stream=None):
     """Keeps the new tokens of each request whose bits are set in kept (int64
-    [requests]) and closes them up behind their context; left (int32 [requests],
-    apart from the batch's tensors, optional) = the contexts' new lengths.  See
-    lbv_kv_keep."""
+    [requests]; -1, all bits, keeps all of them, a prompt's too) and closes them up
+    behind their context; left (int32 [requests], apart from the batch's tensors,
+    optional) = the contexts' new lengths.  See lbv_kv_keep."""
     import torch
     device = _sizes(batch, cache)[2]
     if kept is None:

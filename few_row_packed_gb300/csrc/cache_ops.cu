@@ -118,10 +118,11 @@ __global__ void __launch_bounds__(kThreads)
     uint64_t word = n > 0 ? kept[r] : 0;
     if (n > 0 && n < kMost)
         word &= (1ull << n) - 1;
+    const bool all = word == ~0ull;                // also of more than a word names
     const int count = __popcll(word);
     if (left && head == 0 && tid == 0)
-        left[r] = first + count;
-    const int still = word == ~0ull ? kMost : __ffsll((long long)~word) - 1;    // the first of them stay where they are
+        left[r] = first + (all ? n : count);
+    const int still = all ? kMost : __ffsll((long long)~word) - 1;    // the first of them stay where they are
     const int moving = count - still;
     if (moving <= 0)
         return;
