@@ -546,7 +546,9 @@ class KVCache4(KVCache):
     """A caller's paged cache held in 4 bits, a scale and a bias for each 64 elements
     of a head (lbv_kv_cache4_create): data is a contiguous uint8 device tensor
     [pages, kv_cache4_page_bytes(page_size, heads, head_dim)], kept alive here; dtype
-    (fp16 or bf16) is the type of its values.  Stands wherever a KVCache does."""
+    (fp16 or bf16) is the type of its values.  Taken by every call that takes a KVCache.
+    Holds magnitudes up to 2^15 (fp16) or 2^126 (bf16): 64 elements with a larger one
+    or a NaN read as NaN (lbv_rope_append)."""
 
     def __init__(self, data, page_size: int, heads: int, head_dim: int, dtype):
         import torch

@@ -15,6 +15,8 @@
 // radians and every product and sum rounded by itself: a program that follows the
 // definition gets the same codes.  (The angle's fraction of a turn is exact to 2^-40 before
 // that; its rounding to fp32 is off by up to 4e-7, a millionth of a step between codes.)
+// Queries have no codes but the same turns, one table a token: 4e-7 of a query is 2^-21, where
+// its rounding to 16 bits takes 2^-11 or 2^-8.
 //
 // Bound by memory: every element is read once, queries leave as 16 bits, keys and values as 4.5.
 // 8191 tokens of 48 + 8 + 8 heads of 128, fp32 to bf16: 64 us, 5.9 TB/s, 87 % of what a copy

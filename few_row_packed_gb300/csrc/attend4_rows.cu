@@ -26,7 +26,7 @@
 //
 // What bounds it (48 query over 8 key/value heads of 128): 64 requests of one token over
 // 500 to 16,384 keys, 396 MB, take 93 us, 4.3 TB/s, 63 % of what a copy reaches; the 16-bit
-// cache's kernel takes 221.  Issue slots are 68 % busy with 70 million instructions, half of them
+// cache's kernel takes 215.  Issue slots are 69 % busy with 71 million instructions, half of them
 // codes', and their pipes near half; the copies alone (no codes expanded) take 67 us.
 // (Three teams an SM in place of four: 2 % longer.)  More rows cost their products and probabilities: 32 requests over 7,000
 // keys take 68 us with 6 rows each, 87 with 12, 120 with 24.  A single request is its launches, its
@@ -47,13 +47,18 @@ using namespace att;
 namespace {
 
 // Keys per block, 16 a warp.  (128, 32 a warp, save what a block costs beside its keys, and divide
-// small batches less evenly: 64 requests of one token 101 us in place of 107, a window of
-// 2,048 over 32 requests 33 in place of 29, four tokens after 200,000 108 in place of 93.)
+// small batches less evenly: in an earlier version of this kernel 64 requests of one token took 6 %
+// less, a window of 2,048 over 32 requests 14 % more, four tokens after 200,000 16 % more.)
 constexpr int kBlock = 64;
 constexpr int kMinUnits = 2;                     // the least share of a team
 constexpr int kKeyWarps = 4, kTeam = kKeyWarps * 32;
 // A reference that every score passes, negated: nothing has been seen yet.
 constexpr float kNone = 3.402823466e38f;
+// References from here on are worth a product that is rounded before they are taken from it: in a
+// fused multiply-add the largest score's exponent is what was rounded off the reference, up to
+// half a unit of its last place.  Below 2^12 that is 2^-13 or less, and 2^x rounds to 1 in 16 bits;
+// it is 1 at 2^25, 8 at 2^28 and more than fp32's exponents from 2^32 on.
+constexpr float kLarge = 4096.f;
 constexpr int kItems = 16;                        // items that a team's warps may be apart: stages, and one
 
 // What a team needs to know of an item.
@@ -70,7 +75,7 @@ static_assert(sizeof(Item) == 48, "ring entry");
 template <int D, int NT>
 struct Geo {
     static constexpr int ROWS = 8 * NT;
-    // (3 in place of 6: 32 trees 164 us, 158; 10: 162)
+    // (32 trees: 3 in place of 6 160 us, these 151, 10 156)
     static constexpr int EXTRA = NT == 1 ? 3 : 6;           // units of an item beside its blocks
     // teams on an SM, and registers a thread after the split: 96 * 640 at launch = 104 * 512 +
     // 64 * 128, 128 * 512 = 152 * 384 + 56 * 128
@@ -78,7 +83,7 @@ struct Geo {
     static constexpr int REGS = NT == 1 ? 104 : 152, HELPER = NT == 1 ? 64 : 56;
     static constexpr int THREADS = TEAMS * kTeam + 128;
     static constexpr int STAGE = kBlock * 72 * (D / 64);
-    // (two stages, and four, take 4 to 7 % longer)
+    // (two stages, and four, take 1 to 4 % longer)
     static constexpr int NST = D == 64 ? 6 : 3;
     static constexpr int SLOT = ROWS * (D + 3);             // floats of one partial result
     // a team's shared memory: the ring, the warps' results, the queries as the lanes want them (in

@@ -90,12 +90,6 @@ __device__ __forceinline__ void prefetch_l2(const void* p)
     asm volatile("prefetch.global.L2 [%0];\n" ::"l"(p) : "memory");
 }
 
-// References from here on are worth a product that is rounded before they are taken from it: in a
-// fused multiply-add the largest score's exponent is what was rounded off the reference, up to
-// half a unit of its last place.  Below 2^12 that is 2^-13 or less, and 2^x rounds to 1 in 16 bits;
-// it passes 1 at 2^25, 8 at 2^28 and fp32's exponents at 2^32.
-constexpr float kLarge = 4096.f;
-
 __device__ __forceinline__ float ex2(float x)
 {
     float y;

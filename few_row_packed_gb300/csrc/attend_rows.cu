@@ -24,14 +24,15 @@
 //     m16n8k16 with the rows as M), they agree on the rows' references, exchange
 //     their probabilities through shared memory, and each adds up a quarter of the
 //     head's elements over all 64 keys.  So no sums have to be joined at an item's
-//     end, and the accumulators take a quarter of the registers.  One tile of 16
-//     rows a read of the keys is what mma.sync sustains beside memory: it takes
-//     about 32 cycles an instruction and SM quarter, and tiles of 32 rows ran 1.4
-//     times slower than memory (310 us for 64 requests of one token, 220 with 16
-//     rows).  Larger tiles go to the tensor-memory kernel (attend_tiles.cu).
+//     end, and the accumulators take a quarter of the registers.  A tile is 16 rows:
+//     with 32, in an earlier version, 64 requests of one token took 310 us in place of
+//     220.  The tensor pipe's rate was not the cause (mma.sync takes 8 to 9 clocks an
+//     instruction and SM quarter by the counters, 18 % of the time with 16 rows); what
+//     was has not been measured.  Larger batches go to the tensor-memory kernel
+//     (attend_tiles.cu).
 //
 // 64 requests of one token over 500 to 16,384 keys, 48 query over 8 key/value heads of
-// 128: 216 to 220 us with the join, 6.4 to 6.5 TB/s, 94 to 96 % of what a copy reaches.  One request over
+// 128: 214 to 220 us with the join, 6.4 to 6.6 TB/s, 94 to 97 % of what a copy reaches.  One request over
 // 2,011 keys: 9.5 us, of round trips to memory.  32 requests of 1 to 8 tokens, 32 query
 // over 8 heads of 64, window 4096: 50 us, 61 %; a third of them has two row tiles, which
 // read their keys twice (60 us by the tensor-memory kernel).

@@ -23,17 +23,18 @@
 //
 // What bounds it (48 query over 8 key/value heads of 128, bf16): in long items the
 // hand-over of S and P, with the tensor cores 70 % busy: 2048 tokens at the end of 16,384
-// take 510 to 530 us, 1,460 to 1,520 TFLOP/s.  In short ones their ends, during which the
+// take 480 to 495 us, 1,560 to 1,600 TFLOP/s, in a graph of a few calls, and 520 in a long series,
+// whose clocks fall under the power limit.  In short ones their ends, during which the
 // tensor cores wait: code that runs once an item is fetched anew and takes some 25 clocks an
-// instruction, where the block's loop takes 9; 16 requests of 1 to 600 tokens take 139 us,
-// their operations at the same rate 84.  With few blocks the start: 5 us to the first
+// instruction, where the block's loop takes 9; 16 requests of 1 to 600 tokens take 135 us,
+// their operations at the same rate 77.  With few blocks the start: 5 us to the first
 // scores and 5 more to fetch the block's code, some 20 KB; 8 tokens after 32,771 take
 // 36 us, their keys and values 20.
 //
 // Over a cache of 4 bits the four warps that expand: of 1,500 clocks a slot they spend 790 to
 // expand and store a thread's 128 elements, 75 in the fence before the MMAs read them, and the
 // rest waiting for codes and for places.  With two row tiles a block's products take nearly as long:
-// 2048 tokens at the end of 16,384 take 555 to 575 us, from the 16-bit cache 490.  With one they do
+// 2048 tokens at the end of 16,384 take 560 to 565 us, 580 in a long series.  With one they do
 // not: 32 requests of 8 tokens over 7,000 keys 142 us, from 16 bits 159.  Eight warps, keys and
 // values apart, leave the streams 168 registers or less, whose spills cost more than is won: 603
 // to 670 us and 157 to 163.
@@ -54,7 +55,7 @@ constexpr int kTile = 128;                       // rows per stream
 constexpr int kRows = 2 * kTile;                 // rows per item
 // Units of an item: its queries and results, a block of one row tile, a block of two;
 // and the least share of a CTA.  A unit is 0.2 us of a long item.  (16 requests of 1 to
-// 600 tokens, us: 16/3/4 141, these 139, 28/3/4 141, 24/4/4 143, 36/4/5 142; a prompt's
+// 600 tokens: 16/3/4 and 28/3/4 take 1.5 % longer, 24/4/4 3, 36/4/5 2; a prompt's
 // chunk is the same within 1 %.  The least share: 40 small batches take 4 % less with 8 or
 // 12 than with 24, 12 % less than with 48; 20 tokens over 3,943 keys 15.6 and 20.3 us.)
 // Over 4 bits a block takes as long to expand for one row tile as for two: 16/4/4 is 1 to 5 %
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
     // After a wait that ran out, `ok` false, a thread waits for nothing more, goes on to its
     // item's end and leaves there with its warp.  Warps meet at bounded waits alone, so
     // that those it leaves behind run out too.  (The streams at a hardware barrier in place
-    // of `together`: 137 us for the 139 above, and no end if one of them left.)
+    // of `together`: 1.5 % less for the 16 requests above, and no end if one of them left.)
     auto wait = [&](uint32_t b, uint32_t parity) {
         if (ok)
             ok = mbar_wait(b, parity, p.wait_limit);
@@ -668,9 +669,9 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
                     float t[4][32];
                     if (!idle) {
                         // masked scores are overwritten in place, 32 keys at a time: rare, so short
-                        // code (a prompt's chunk with a window of 1,024: 91 us; 16 at a time 92.6;
-                        // masked in registers 92.9, and 5 % more for a long context; leaving out
-                        // those 32 that every row sees 93)
+                        // code (a prompt's chunk with a window of 1,024 takes 93 us; 16 at a time 2 %
+                        // longer; masked in registers 2 %, and 5 for a long context; leaving out
+                        // those 32 that every row sees 2 %)
                         if (k0 + kKeys > open_hi || k0 < open_lo) {
 #pragma unroll 1
                             for (int e = 0; e < 4; ++e) {

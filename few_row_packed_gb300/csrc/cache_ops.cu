@@ -2,8 +2,9 @@
 // back, closing up the accepted ones of a tree, copying pages.  All three move bytes and
 // are bound by memory, or with few bytes by a launch and round trips to memory:
 // 8191 tokens of 8 heads of 128 read from 4 bits take 9.2 us (43 MB, 4.6 TB/s; one token a block
-// 14.5), the accepted ones of 64 requests' trees 4.8 us (four round trips: counts, page, tokens,
-// stores), 256 pages of 262,144 bytes 21.9 us (134 MB, 6.1 TB/s, 90 % of what a copy reaches).
+// 14.5), the accepted ones of 64 requests' trees 3.2 us (four round trips: counts, page, tokens,
+// stores; 4.4 from Python), 256 pages of 262,144 bytes 22 us (134 MB, 6.1 TB/s, 90 % of what a copy
+// reaches).
 #include "kv4.cuh"
 #include "rope_rows.cuh"
 

@@ -572,7 +572,9 @@ LBV_API lbv_status lbv_rope_destroy(lbv_rope* rope);
  * codes wherever the definition is followed, every operation is rounded by itself
  * there: the angle's fraction of a turn is cut to 2^-40 and taken to fp32 radians, whose
  * cos and sin are fp32, and so are products and sums.  A group with a NaN or a
- * magnitude above 2^15 (fp16) or 2^126 (bf16) reads as NaN.
+ * magnitude above 2^15 (fp16, whose 16-bit cache holds up to 65504) or 2^126 (bf16)
+ * cannot be held and reads as NaN, all 64 of it: to lbv_attend it is a key or a value
+ * that is not finite.
  * Errors: LBV_ERR_INVALID_ARG for null or misaligned pointers, sizes that do
  * not agree and dtypes that cannot be; LBV_ERR_UNSUPPORTED if rot_dim exceeds
  * the head.  The library allocates nothing.
@@ -613,8 +615,12 @@ LBV_API size_t lbv_attend_workspace_bytes(const lbv_kv_cache* cache, const lbv_b
  * probabilities (an error of half a step of the type, where 4 bits hold a value to 2^-5
  * of its group's range).  So the same request may
  * differ by the rounding of the probabilities between batches of either kind.
- * lse adds the unrounded ones in both.  Cache slots at or past
- * kv_len may hold anything; keys and values below it are taken to be finite.
+ * lse adds the unrounded ones in both.  Scores are fp32 sums, of any size below
+ * 2^127 (times scale and log2 e): the largest weighs most however large it is, and from
+ * 2^24 on those that agree to fp32's rounding errors may share its weight.  Cache slots
+ * at or past kv_len may hold anything; keys and values below it are taken to be finite
+ * (one that is not makes NaN of rows that share a block with it, also of those that
+ * the mask hides it from).
  * Contexts are shorter than 2^30.  A mapped page outside the cache reads as zeros.
  *   workspace: dev, 256-byte aligned, lbv_attend_workspace_bytes(); zeroed once
  * by the caller, left ready for the next call by every call; calls that may
