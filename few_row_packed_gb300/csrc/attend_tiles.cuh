@@ -23,8 +23,8 @@
 //
 // What bounds it (48 query over 8 key/value heads of 128, bf16): in long items the
 // hand-over of S and P, with the tensor cores 70 % busy: 2048 tokens at the end of 16,384
-// take 480 to 495 us, 1,560 to 1,600 TFLOP/s, in a graph of a few calls, and 520 in a long series,
-// whose clocks fall under the power limit.  In short ones their ends, during which the
+// take 480 to 520 us, 1,490 to 1,600 TFLOP/s, by the clocks (a long series of calls meets the
+// power limit).  In short ones their ends, during which the
 // tensor cores wait: code that runs once an item is fetched anew and takes some 25 clocks an
 // instruction, where the block's loop takes 9; 16 requests of 1 to 600 tokens take 135 us,
 // their operations at the same rate 77.  With few blocks the start: 5 us to the first
@@ -34,7 +34,7 @@
 // Over a cache of 4 bits the four warps that expand: of 1,500 clocks a slot they spend 790 to
 // expand and store a thread's 128 elements, 75 in the fence before the MMAs read them, and the
 // rest waiting for codes and for places.  With two row tiles a block's products take nearly as long:
-// 2048 tokens at the end of 16,384 take 560 to 565 us, 580 in a long series.  With one they do
+// 2048 tokens at the end of 16,384 take 560 to 590 us.  With one they do
 // not: 32 requests of 8 tokens over 7,000 keys 142 us, from 16 bits 159.  Eight warps, keys and
 // values apart, leave the streams 168 registers or less, whose spills cost more than is won: 603
 // to 670 us and 157 to 163.
