@@ -34,7 +34,7 @@
 // Over a cache of 4 bits the four warps that expand: of 1,500 clocks a slot they spend 790 to
 // expand and store a thread's 128 elements, 75 in the fence before the MMAs read them, and the
 // rest waiting for codes and for places.  With two row tiles a block's products take nearly as long:
-// 2048 tokens at the end of 16,384 take 560 to 590 us.  With one they do
+// 2048 tokens at the end of 16,384 take 560 to 600 us.  With one they do
 // not: 32 requests of 8 tokens over 7,000 keys 142 us, from 16 bits 159.  Eight warps, keys and
 // values apart, leave the streams 168 registers or less, whose spills cost more than is won: 603
 // to 670 us and 157 to 163.
@@ -851,7 +851,7 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
             // dual: all columns of the row; else the stream's half of them
             const int e0 = dual ? 0 : s * (D / 64), e1 = dual ? D / 32 : (s + 1) * (D / 64);
             // (the quotient is rounded to 16 bits: an approximate reciprocal, off by 2^-23, will do)
-            const float f = sum > 0.f ? __fdividef(1.f, sum) : 0.f;
+            const float f = sum == 0.f ? 0.f : __fdividef(1.f, sum);     // (NaN stays)
 #pragma unroll 1
             for (int e = e0; e < e1; ++e) {
                 float o[32];
