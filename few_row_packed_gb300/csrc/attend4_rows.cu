@@ -57,7 +57,7 @@ constexpr float kNone = 3.402823466e38f;
 // References from here on are worth a product that is rounded before they are taken from it: in a
 // fused multiply-add the largest score's exponent is what was rounded off the reference, up to
 // half a unit of its last place.  Below 2^12 that is 2^-13 or less, and 2^x rounds to 1 in 16 bits;
-// it is 1 at 2^25, 8 at 2^28 and more than fp32's exponents from 2^32 on.
+// it is up to 1 below 2^25, 8 below 2^28 and more than fp32's exponents from 2^32 on.
 constexpr float kLarge = 4096.f;
 constexpr int kItems = 16;                        // items that a team's warps may be apart: stages, and one
 

@@ -732,7 +732,7 @@ __global__ void __launch_bounds__(Roles<KV4>::THREADS, 1)
                                 c = c0;
                                 m = c0 * most;
                                 // An exponent is c s - m, rounded once, so the largest score's is what was
-                                // rounded off m: up to 1/2 at 2^24, 8 at 2^28, beyond fp32's at 2^32.  From
+                                // rounded off m: up to 1/2 below 2^24, 8 below 2^28, fp32's limit at 2^32.  From
                                 // 2^24 on c and m are made smaller by a power of two that leaves 2^23 of m.
                                 // Scores there are apart by the rest of a unit or more, and by 2^23 times
                                 // their relative difference: those that this brings nearer differ by

@@ -42,8 +42,10 @@ KINDS = [
     (4, [4, 2], 12),            # and of 24
     (4, [20, 3], 12),           # many rows over 4 bits: one tile of 128,
     (4, [40, 30], 10),          # two,
-    (16, [20, 3], 12),          # and over 16 bits
+    (16, [20, 3], 12),          # over 16 bits,
     (16, [40, 30], 10),
+    (16, [2, 1], 2),            # and few rows there
+    (16, [2, 2], 14),
 ]
 
 
