@@ -677,8 +677,9 @@ LBV_API lbv_status lbv_kv_read(const lbv_batch* batch, const lbv_kv_cache* cache
  * left[r] (dev int32 [requests], or NULL) = kv_len - n + their number.  Bits at or
  * past n do not count; new tokens past the 64th are dropped, unless all 64 bits are set:
  * then all n new tokens stay, however many (a prompt in a batch beside drafts).  What the
- * slots from left[r] to kv_len hold afterwards does not matter.  Keys keep the rotary positions that they were
- * appended with.  A move from or to a slot that does not exist is left out.
+ * slots from left[r] to kv_len hold afterwards does not matter.  Keys keep the rotary
+ * positions that they were appended with.  A move from or to a slot that does not exist
+ * is left out.
  * The slots of the new tokens belong to one request each; left is apart from the batch's
  * arrays and from kept.  Errors: LBV_ERR_INVALID_ARG.
  */
